@@ -488,6 +488,138 @@ uint64_t nrnn_set_wait_limit_ns(uint64_t ns);
 int nrnn_probe_xu_rates(float *ex2_per_clk, float *rcp_per_clk, float *tanh_per_clk,
                         void *stream);
 
+/* Type of token ids and targets. */
+typedef enum { NRNN_I32 = 0, NRNN_I64 = 1 } nrnn_index_type;
+
+/*
+ * Embedding lookup: out_i = scale W[ids_i], a row of zeros where ids_i equals
+ * padding_id.  The buffers of this entry point and of the ones below need only
+ * their element's alignment (16-byte aligned rows are read faster), and d may
+ * be any width.
+ *
+ *   ids         device, n token ids of ids_type; an id outside [0, V) that is
+ *               not padding_id gives a row of NaN
+ *   W           device, (V, d) of dtype
+ *   n, V, d     sizes; n >= 0, V and d > 0; n and V below 2^31, d <= 2^24
+ *   padding_id  an id whose rows are zeros; a value outside [0, V) for none
+ *   out         device, (n, d) of dtype, not overlapping W
+ */
+int nrnn_embedding(const void *ids, int ids_type, const void *W, int dtype, int64_t n, int64_t V,
+                   int64_t d, int64_t padding_id, float scale, void *out, void *stream);
+
+/* Workspace bytes of nrnn_embedding_backward; 0 for invalid sizes. */
+size_t nrnn_embedding_backward_workspace_bytes(int64_t n, int64_t V, int64_t d);
+
+/*
+ * Gradient of the lookup: gW_v = scale sum of g_i over the i with ids_i = v,
+ * in fp32, rounded once; the sum's order is fixed by the ids alone, so the
+ * result does not change from run to run.  Padding and ids outside [0, V) take
+ * no part.
+ *
+ *   g           device, (n, d) of dtype: dL/dout
+ *   accumulate  0: gW is overwritten (zeros for ids that do not occur);
+ *               else added to (rows of ids that do not occur are not touched:
+ *               a weight shared with nrnn_vocab_loss_backward)
+ *   gW          device, (V, d) of dtype
+ *   workspace   device, 256-byte aligned, of at least
+ *               nrnn_embedding_backward_workspace_bytes(n, V, d)
+ */
+int nrnn_embedding_backward(const void *ids, int ids_type, const void *g, int dtype, int64_t n,
+                            int64_t V, int64_t d, int64_t padding_id, float scale, int accumulate,
+                            void *gW, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The norms before and after a block, with its gate and residual scale, in one
+ * pass over rows of d values:
+ *
+ *   y     = h rsqrt(mean(h^2) + eps) w_post silu(gate)
+ *   x_out = x + scale y
+ *   u     = x_out rsqrt(mean(x_out^2) + eps) w_pre
+ *
+ *   x, h, gate  device, (rows, d) of dtype: the residual stream, the block's
+ *               output and its gate's preactivation.  gate NULL: no gate.
+ *               h NULL (then gate NULL): u = norm(x) w_pre alone, the norm
+ *               before the first block
+ *   w_post, scale, w_pre   device, fp32 (d); NULL: ones
+ *   x_out       device, (rows, d) of dtype, may be x (unused if h is NULL)
+ *   u           device, (rows, d) of dtype; NULL (then h given): not wanted,
+ *               the norm after the last block
+ *   d           1 .. 8192, else NRNN_ERR_UNSUPPORTED;  eps >= 0
+ * u is computed from x_out before its rounding to dtype.
+ */
+int nrnn_block_norm_forward(const void *x, const void *h, const void *gate, const float *w_post,
+                            const float *scale, const float *w_pre, int dtype, int64_t rows,
+                            int64_t d, float eps, void *x_out, void *u, void *stream);
+
+/* Workspace bytes of nrnn_block_norm_backward; 0 for invalid sizes. */
+size_t nrnn_block_norm_backward_workspace_bytes(int64_t rows, int64_t d);
+
+/*
+ * Gradient of nrnn_block_norm_forward at the stored x_out (h NULL: x), h and
+ * gate.
+ *
+ *   g_x         device, (rows, d): dL/dx_out from the residual stream; NULL: zeros
+ *   g_u         device, (rows, d): dL/du; NULL: u took no part (then x_out and
+ *               w_pre are not read and gw_pre is zeros)
+ *   gx          device, (rows, d): dL/dx; may be g_x
+ *   rows        0: the weights' gradients are zeros
+ *   gh, g_gate  device, (rows, d): dL/dh and dL/dgate (unused where h or gate
+ *               is NULL); must not overlap the inputs
+ *   gw_post, g_scale, gw_pre   device, fp32 (d), overwritten; each may be NULL.
+ *               Sums over the rows in fp32, in an order fixed by the sizes
+ *   workspace   device, 256-byte aligned, of at least
+ *               nrnn_block_norm_backward_workspace_bytes(rows, d)
+ */
+int nrnn_block_norm_backward(const void *x_out, const void *h, const void *gate,
+                             const float *w_post, const float *scale, const float *w_pre,
+                             const void *g_x, const void *g_u, int dtype, int64_t rows, int64_t d,
+                             float eps, void *gx, void *gh, void *g_gate, float *gw_post,
+                             float *g_scale, float *gw_pre, void *workspace, size_t ws_bytes,
+                             void *stream);
+
+/*
+ * Workspace bytes of nrnn_vocab_loss_forward (backward = 0) or
+ * nrnn_vocab_loss_backward; 0 for invalid sizes.  No N x V array is kept: the
+ * backward holds one piece of the vocabulary at a time.
+ */
+size_t nrnn_vocab_loss_workspace_bytes(int64_t rows, int64_t d, int64_t V, int dtype, int backward);
+
+/*
+ * Softmax cross entropy over a vocabulary: with z_iv = logit_scale <x_i, W_v>,
+ * lse_i = log sum_v exp(z_iv) and loss_i = lse_i - z_i,targets_i.
+ *
+ *   x            device, (rows, d) of dtype;  W device, (V, d) of dtype
+ *   rows, d, V   rows >= 0, d and V > 0; rows and V at most 2^30, d at most 2^20
+ *   targets      device, rows ids of targets_type.  Rows whose target equals
+ *                ignore_index take no part: loss and lse are 0, and nothing
+ *                they hold is read.  Any other target outside [0, V) gives NaN
+ *   loss, lse    device, fp32 (rows)
+ *   workspace    device, 256-byte aligned, of at least
+ *                nrnn_vocab_loss_workspace_bytes(..., 0)
+ * fp32 inputs are multiplied with fp32 accuracy on the tensor cores.
+ */
+int nrnn_vocab_loss_forward(const void *x, const void *W, int dtype, int64_t rows, int64_t d,
+                            int64_t V, const void *targets, int targets_type, int64_t ignore_index,
+                            float logit_scale, float *loss, float *lse, void *workspace,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * Its gradient: with G_iv = g_loss_i logit_scale (exp(z_iv - lse_i) - [v =
+ * targets_i]), gx = G W and gW = G^T x, both overwritten.  bf16: G is rounded
+ * to bf16 before the two products.  Rows that take no part have a zero row in
+ * gx (NaN where the target is out of range) and add nothing to gW.
+ *
+ *   lse          device, fp32 (rows), as nrnn_vocab_loss_forward left it
+ *   g_loss       device, fp32 (rows): dL/dloss_i
+ *   gx, gW       device, (rows, d) and (V, d) of dtype
+ *   workspace    device, 256-byte aligned, of at least
+ *                nrnn_vocab_loss_workspace_bytes(..., 1)
+ */
+int nrnn_vocab_loss_backward(const void *x, const void *W, int dtype, int64_t rows, int64_t d,
+                             int64_t V, const void *targets, int targets_type, int64_t ignore_index,
+                             float logit_scale, const float *lse, const float *g_loss, void *gx,
+                             void *gW, void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

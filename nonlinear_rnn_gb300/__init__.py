@@ -40,5 +40,14 @@ from ._binding import (  # noqa: F401
     workspace_bytes,
     x_host_staging_bytes,
 )
+from ._language import (  # noqa: F401
+    BlockNormGrads,
+    block_norm,
+    block_norm_backward,
+    embedding,
+    embedding_backward,
+    vocab_loss,
+    vocab_loss_backward,
+)
 
 load()

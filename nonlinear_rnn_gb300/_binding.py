@@ -64,6 +64,18 @@ _SIGNATURES = {
                                     _vp, _vp, _vp, _sz, _i64, _vp], _int),
     "nrnn_newton_forward_noalloc": ([_vp, _int, _vp, _i64, _i64, _i64, _vp, _i64, _int, _f, _vp,
                                      _vp, _vp, _vp], _int),
+    "nrnn_embedding": ([_vp, _int, _vp, _int, _i64, _i64, _i64, _i64, _f, _vp, _vp], _int),
+    "nrnn_embedding_backward_workspace_bytes": ([_i64, _i64, _i64], _sz),
+    "nrnn_embedding_backward": ([_vp, _int, _vp, _int, _i64, _i64, _i64, _i64, _f, _int, _vp, _vp,
+                                 _sz, _vp], _int),
+    "nrnn_block_norm_forward": ([_vp] * 6 + [_int, _i64, _i64, _f, _vp, _vp, _vp], _int),
+    "nrnn_block_norm_backward_workspace_bytes": ([_i64, _i64], _sz),
+    "nrnn_block_norm_backward": ([_vp] * 8 + [_int, _i64, _i64, _f] + [_vp] * 7 + [_sz, _vp], _int),
+    "nrnn_vocab_loss_workspace_bytes": ([_i64, _i64, _i64, _int, _int], _sz),
+    "nrnn_vocab_loss_forward": ([_vp, _vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _f, _vp, _vp,
+                                 _vp, _sz, _vp], _int),
+    "nrnn_vocab_loss_backward": ([_vp, _vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _f, _vp, _vp,
+                                  _vp, _vp, _vp, _sz, _vp], _int),
 }
 EXPORTED = tuple(_SIGNATURES)
 

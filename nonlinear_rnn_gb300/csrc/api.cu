@@ -252,6 +252,26 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CU
 }  // namespace
 
 namespace nrnn {
+// 3-D map over a (planes, rows, inner) row-major bf16 array with a (box_inner x
+// box_rows x 1) box.
+bool make_map_planes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int64_t planes,
+                     uint32_t box_inner, uint32_t box_rows, bool swizzle128) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(planes)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner * 2),
+                             static_cast<cuuint64_t>(inner * 2 * rows)};
+    cuuint32_t box[3] = {box_inner, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r =
+        fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+           estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 size_t newton_error_offset(int K) { return layout(0, 0, 8, NRNN_F32, K, true).error_off; }
 }  // namespace nrnn
 

@@ -145,6 +145,12 @@ cudaError_t launch_pack_plan(const int32_t *cu, int S, int n_chunks, int4 *plan,
 
 size_t newton_smem_bytes(int dtype, bool fused);
 
+// 3-D TMA map over a (planes, rows, inner) row-major bf16 array, box
+// (box_inner x box_rows x 1), 128-byte swizzle (box_inner <= 64) or 64-byte
+// swizzle (box_inner <= 32); inner a multiple of 8, base 16-byte aligned
+bool make_map_planes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int64_t planes,
+                     uint32_t box_inner, uint32_t box_rows, bool swizzle128);
+
 // byte offset of the error word in a Newton forward's workspace
 size_t newton_error_offset(int K);
 

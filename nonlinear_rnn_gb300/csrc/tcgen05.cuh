@@ -18,6 +18,19 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr) {
     return d;
 }
 
+// MN-major tile with the 128-byte swizzle: the 64 M (or N) elements of one K
+// row are one 128-byte line, 8 K rows a core block; core blocks follow along K
+// every 1024 bytes (SBO) and along M/N every lbo bytes (LBO).
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3ffffu) >> 4);          // start address
+    d |= static_cast<uint64_t>(lbo >> 4) << 16;                        // LBO
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;                      // SBO
+    d |= static_cast<uint64_t>(1u) << 46;                              // version
+    d |= static_cast<uint64_t>(2u) << 61;                              // SWIZZLE_128B
+    return d;
+}
+
 // The same with the 64-byte swizzle: 8-row x 64-byte core blocks every 512
 // bytes (SBO), layout type 4 (SWIZZLE_64B).
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t smem_addr) {
@@ -77,6 +90,18 @@ __device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t adesc, uint64_t bd
             "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
             "l"(adesc), "l"(bdesc), "r"(IDESC), "r"(accumulate)
             : "memory");
+}
+
+// kind::f16 product with the instruction descriptor in a register (N chosen at
+// run time)
+__device__ __forceinline__ void mma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
@@ -140,6 +165,13 @@ template <bool TF32>
 constexpr uint32_t idesc_kmajor(int M, int N) {
     return (1u << 4) | ((TF32 ? 2u : 1u) << 7) | ((TF32 ? 2u : 1u) << 10) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// kind::f16 descriptor (bf16 A and B, fp32 D) without N, which the caller adds
+// as (N >> 3) << 17; mn_a, mn_b: the operand's tile is MN-major
+constexpr uint32_t idesc_bf16(int M, bool mn_a, bool mn_b) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (mn_a ? 1u << 15 : 0u) | (mn_b ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 }  // namespace nrnn
