@@ -9,24 +9,49 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import _device_tensor, _dtype_code, _raise, _stream, load
+from ._binding import BF16, F32, OK, _device_tensor, _raise, load
 
 I32, I64 = 0, 1
 
 
+# A decode step's calls take a few microseconds on the GPU, so this path is kept
+# short: the device is switched only if it has to be, and the stream is read
+# without making a Stream object (together 3 us a call).
+_INDEX_TYPES = {torch.int32: I32, torch.int64: I64}
+_STORAGE_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _run(what: str, fn, t: torch.Tensor, *args) -> None:
+    """fn(*args, stream) on t's device and that device's current stream."""
+    index = t.get_device()
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st != OK:
+        _raise(st, what)
+
+
 def _ids(t: torch.Tensor, what: str) -> tuple[torch.Tensor, int]:
     t = _device_tensor(t, what)
-    if t.dtype == torch.int64:
-        return t, I64
-    if t.dtype == torch.int32:
-        return t, I32
-    raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
+    kind = _INDEX_TYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
+    return t, kind
 
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+def _storage(t: torch.Tensor) -> int:
+    code = _STORAGE_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}; use float32 or bfloat16")
+    return code
+
+
+def _with(first: torch.Tensor, t: torch.Tensor, what: str) -> None:
+    if t.device != first.device:
+        raise ValueError(f"{what} must be on {first.device}, got {t.device}")
 
 
 def _at(t) -> int | None:
@@ -44,12 +69,8 @@ def _result(out, shape, like: torch.Tensor, what: str) -> torch.Tensor:
 
 def _space(workspace, nbytes: int, device) -> torch.Tensor:
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     return workspace
-
-
-def _on_device(t: torch.Tensor):
-    return torch.cuda.device(t.device)
 
 
 def embedding(ids: torch.Tensor, W: torch.Tensor, scale: float = 1.0,
@@ -61,14 +82,12 @@ def embedding(ids: torch.Tensor, W: torch.Tensor, scale: float = 1.0,
     W = _device_tensor(W, "W")
     if W.dim() != 2:
         raise ValueError("W must have shape (V, d)")
-    _same_device(ids, W=W)
+    _with(ids, W, "W")
     V, d = W.shape
+    code = _storage(W)
     rows = _result(out, (*ids.shape, d), W, "out")
-    with _on_device(W):
-        st = load().nrnn_embedding(ids.data_ptr(), ids_type, W.data_ptr(), _dtype_code(W),
-                                   ids.numel(), V, d, -1 if padding_idx is None else int(padding_idx),
-                                   float(scale), rows.data_ptr(), _stream(W.device))
-    _raise(st, "embedding")
+    _run("embedding", load().nrnn_embedding, W, ids.data_ptr(), ids_type, W.data_ptr(), code,
+         ids.numel(), V, d, -1 if padding_idx is None else padding_idx, scale, rows.data_ptr())
     return rows
 
 
@@ -82,23 +101,20 @@ def embedding_backward(ids: torch.Tensor, g: torch.Tensor, num_rows: int, scale:
     g = _device_tensor(g, "g")
     if g.dim() < 1 or tuple(g.shape[:-1]) != tuple(ids.shape):
         raise ValueError("g must have shape (*ids.shape, d)")
-    _same_device(ids, g=g)
+    _with(ids, g, "g")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     n, d, V = ids.numel(), g.shape[-1], int(num_rows)
-    code = _dtype_code(g)
+    code = _storage(g)
     lib = load()
     nbytes = lib.nrnn_embedding_backward_workspace_bytes(n, V, d)
     if nbytes == 0:
         raise ValueError("num_rows and the width of g must be positive (and fit the library's limits)")
     gW = _result(out, (V, d), g, "out")
     ws = _space(workspace, nbytes, g.device)
-    with _on_device(g):
-        st = lib.nrnn_embedding_backward(ids.data_ptr(), ids_type, g.data_ptr(), code, n, V, d,
-                                         -1 if padding_idx is None else int(padding_idx),
-                                         float(scale), int(bool(accumulate)), gW.data_ptr(),
-                                         ws.data_ptr(), nbytes, _stream(g.device))
-    _raise(st, "embedding_backward")
+    _run("embedding_backward", lib.nrnn_embedding_backward, g, ids.data_ptr(), ids_type, g.data_ptr(),
+         code, n, V, d, -1 if padding_idx is None else padding_idx, scale, accumulate,
+         gW.data_ptr(), ws.data_ptr(), nbytes)
     return gW
 
 
@@ -106,7 +122,7 @@ def _weight(t, d: int, x: torch.Tensor, what: str):
     if t is None:
         return None
     t = _device_tensor(t, what)
-    if tuple(t.shape) != (d,) or t.dtype != torch.float32 or t.device != x.device:
+    if t.dim() != 1 or t.shape[0] != d or t.dtype != torch.float32 or t.device != x.device:
         raise ValueError(f"{what} must be a float32 vector of {d} values on {x.device}")
     return t
 
@@ -139,16 +155,14 @@ def block_norm(x: torch.Tensor, h: torch.Tensor | None = None, gate: torch.Tenso
     if h is None and (gate is not None or not next_norm):
         raise ValueError("without h there is no gate, and u is the only result")
     h, gate = _like(h, x, "h"), _like(gate, x, "gate")
-    w_post, scale, w_pre = (_weight(w, d, x, n) for w, n in
-                            ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")))
-    x_out = x if h is None else _result(out, x.shape, x, "out")
+    w_post, scale = _weight(w_post, d, x, "w_post"), _weight(scale, d, x, "scale")
+    w_pre = _weight(w_pre, d, x, "w_pre")
+    code = _storage(x)
+    x_out = x if h is None else torch.empty_like(x) if out is None else _result(out, x.shape, x, "out")
     u = torch.empty_like(x) if next_norm else None
-    with _on_device(x):
-        st = load().nrnn_block_norm_forward(
-            x.data_ptr(), _at(h), _at(gate), _at(w_post), _at(scale), _at(w_pre), _dtype_code(x),
-            x.numel() // d if d else 0, d, float(eps), None if h is None else x_out.data_ptr(),
-            _at(u), _stream(x.device))
-    _raise(st, "block_norm")
+    _run("block_norm", load().nrnn_block_norm_forward, x, x.data_ptr(), _at(h), _at(gate), _at(w_post),
+         _at(scale), _at(w_pre), code, x.numel() // d if d else 0, d, eps,
+         None if h is None else x_out.data_ptr(), _at(u))
     return x_out, u
 
 
@@ -177,10 +191,11 @@ def block_norm_backward(x_out: torch.Tensor, h: torch.Tensor | None = None,
         raise ValueError("give g_x, g_u or both")
     if h is None and (gate is not None or g_u is None):
         raise ValueError("without h there is no gate, and u is the only result")
-    h, gate, g_x, g_u = (_like(t, x_out, n) for t, n in
-                         ((h, "h"), (gate, "gate"), (g_x, "g_x"), (g_u, "g_u")))
-    w_post, scale, w_pre = (_weight(w, d, x_out, n) for w, n in
-                            ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")))
+    h, gate = _like(h, x_out, "h"), _like(gate, x_out, "gate")
+    g_x, g_u = _like(g_x, x_out, "g_x"), _like(g_u, x_out, "g_u")
+    w_post, scale = _weight(w_post, d, x_out, "w_post"), _weight(scale, d, x_out, "scale")
+    w_pre = _weight(w_pre, d, x_out, "w_pre")
+    code = _storage(x_out)
     rows = x_out.numel() // d if d else 0
     lib = load()
     nbytes = lib.nrnn_block_norm_backward_workspace_bytes(rows, d)
@@ -193,12 +208,9 @@ def block_norm_backward(x_out: torch.Tensor, h: torch.Tensor | None = None,
     g_gate = None if gate is None else torch.empty_like(x_out)
     ws = _space(workspace, nbytes, dev)
     at = sums.data_ptr()
-    with _on_device(x_out):
-        st = lib.nrnn_block_norm_backward(
-            x_out.data_ptr(), _at(h), _at(gate), _at(w_post), _at(scale), _at(w_pre), _at(g_x),
-            _at(g_u), _dtype_code(x_out), rows, d, float(eps), gx.data_ptr(), _at(gh), _at(g_gate),
-            at, at + 4 * d, at + 8 * d, ws.data_ptr(), nbytes, _stream(dev))
-    _raise(st, "block_norm_backward")
+    _run("block_norm_backward", lib.nrnn_block_norm_backward, x_out, x_out.data_ptr(), _at(h),
+         _at(gate), _at(w_post), _at(scale), _at(w_pre), _at(g_x), _at(g_u), code, rows, d, eps,
+         gx.data_ptr(), _at(gh), _at(g_gate), at, at + 4 * d, at + 8 * d, ws.data_ptr(), nbytes)
     return BlockNormGrads(gx, gh, g_gate, None if h is None else sums[0],
                           None if h is None else sums[1], None if g_u is None else sums[2])
 
@@ -210,10 +222,11 @@ def _vocab_args(x, W, targets):
         raise ValueError("x must have shape (..., d) and W (V, d)")
     if x.dtype != W.dtype:
         raise TypeError("x and W must share a dtype")
-    if tuple(targets.shape) != tuple(x.shape[:-1]):
+    if targets.shape != x.shape[:-1]:
         raise ValueError("targets must have shape x.shape[:-1]")
-    _same_device(x, W=W, targets=targets)
-    return x, W, targets, kind
+    _with(x, W, "W")
+    _with(x, targets, "targets")
+    return x, W, targets, kind, _storage(x)
 
 
 def vocab_loss(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0,
@@ -224,20 +237,17 @@ def vocab_loss(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, logit_sc
     normaliser, which vocab_loss_backward takes.  Rows whose target is
     ignore_index take no part (0 in both); any other target outside [0, V)
     gives NaN (nothing synchronises to raise)."""
-    x, W, targets, kind = _vocab_args(x, W, targets)
+    x, W, targets, kind, code = _vocab_args(x, W, targets)
     V, d = W.shape
-    rows, code = targets.numel(), _dtype_code(x)
+    rows = targets.numel()
     lib = load()
     nbytes = lib.nrnn_vocab_loss_workspace_bytes(rows, d, V, code, 0)
     out = torch.empty((2, *targets.shape), dtype=torch.float32, device=x.device)
     loss, lse = out[0], out[1]
     ws = _space(workspace, nbytes, x.device)
-    with _on_device(x):
-        st = lib.nrnn_vocab_loss_forward(x.data_ptr(), W.data_ptr(), code, rows, d, V,
-                                         targets.data_ptr(), kind, int(ignore_index),
-                                         float(logit_scale), loss.data_ptr(), lse.data_ptr(),
-                                         ws.data_ptr(), nbytes, _stream(x.device))
-    _raise(st, "vocab_loss")
+    _run("vocab_loss", lib.nrnn_vocab_loss_forward, x, x.data_ptr(), W.data_ptr(), code, rows, d, V,
+         targets.data_ptr(), kind, ignore_index, logit_scale, loss.data_ptr(), lse.data_ptr(),
+         ws.data_ptr(), nbytes)
     return loss, lse
 
 
@@ -248,24 +258,20 @@ def vocab_loss_backward(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
     and g_loss = dL/dloss, float32 (...) (for a mean over the kept rows: one
     over their number).  The logits are computed again, a piece of the
     vocabulary at a time."""
-    x, W, targets, kind = _vocab_args(x, W, targets)
+    x, W, targets, kind, code = _vocab_args(x, W, targets)
     V, d = W.shape
-    rows, code = targets.numel(), _dtype_code(x)
+    rows = targets.numel()
     both = []
     for t, what in ((lse, "lse"), (g_loss, "g_loss")):
         t = _device_tensor(t, what)
-        if tuple(t.shape) != tuple(targets.shape) or t.dtype != torch.float32 or t.device != x.device:
+        if t.shape != targets.shape or t.dtype != torch.float32 or t.device != x.device:
             raise ValueError(f"{what} must be float32 of shape {tuple(targets.shape)} on {x.device}")
         both.append(t)
     lib = load()
     nbytes = lib.nrnn_vocab_loss_workspace_bytes(rows, d, V, code, 1)
     gx, gW = torch.empty_like(x), torch.empty_like(W)
     ws = _space(workspace, nbytes, x.device)
-    with _on_device(x):
-        st = lib.nrnn_vocab_loss_backward(x.data_ptr(), W.data_ptr(), code, rows, d, V,
-                                          targets.data_ptr(), kind, int(ignore_index),
-                                          float(logit_scale), both[0].data_ptr(),
-                                          both[1].data_ptr(), gx.data_ptr(), gW.data_ptr(),
-                                          ws.data_ptr(), nbytes, _stream(x.device))
-    _raise(st, "vocab_loss_backward")
+    _run("vocab_loss_backward", lib.nrnn_vocab_loss_backward, x, x.data_ptr(), W.data_ptr(), code, rows,
+         d, V, targets.data_ptr(), kind, ignore_index, logit_scale, both[0].data_ptr(),
+         both[1].data_ptr(), gx.data_ptr(), gW.data_ptr(), ws.data_ptr(), nbytes)
     return gx, gW

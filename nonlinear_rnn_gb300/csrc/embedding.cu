@@ -11,17 +11,22 @@
 // radix sort, and the sums follow the sorted order in fixed groups of 32.
 #include <initializer_list>
 
-#include <cooperative_groups.h>
-
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
 #include "nrnn_internal.h"
 #include "rows.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace nrnn {
 namespace {
+
+// programmatic dependent launch: the next kernel of the call may be scheduled now;
+// wait until the one before has completed
+__device__ __forceinline__ void dependents_may_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_prerequisites() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // A warp works on 32 VEC consecutive columns (a slab) of a row.
 constexpr int GROUP_ROWS = 4;      // rows of one warp of the lookup
@@ -71,138 +76,362 @@ __global__ void __launch_bounds__(EMBED_THREADS)
 }
 
 // -------------------------------------------------------------------- the sort
-// Stable least-significant-digit radix sort of (id, position) by one cluster of
-// CTAs, all passes in one launch: the digit counts are exchanged through
-// distributed shared memory between two cluster barriers, where separate
-// launches would cost several microseconds each.  Every warp owns a contiguous
-// range of the input, so ranks follow (CTA, warp, step, lane) = input order.
+// Stable least-significant-digit radix sort of (id, position), up to 9 bits a
+// pass.  Each pass is two launches over at most SORT_CTAS contiguous parts of the
+// input: k_sort_count leaves the parts' digit counts, and k_sort_place adds up
+// the counts before its own part (all parts' for lower digits, earlier parts'
+// for equal ones), ranks its pairs and writes them.  Ranks follow (part, round,
+// warp, step, lane) = input order.  Up to SORT_TILE ids are sorted by one CTA in
+// one launch.  A tile's pairs are put in order in shared memory first, so that a
+// digit's run leaves as whole lines.  (All passes in one cluster of 16 CTAs took
+// 56 us for 262144 ids, bound by those SMs, and no less for few.)
 // Ids that take no part (padding, out of range) get the key V and sort last.
-constexpr int SORT_CTAS = 8;
-constexpr int SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
+//
+// The launches' further CTAs clear gW meanwhile, a share each.
+constexpr int SORT_CTAS = 152;
+constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_MAX_BITS = 9, SORT_DIGITS = 1 << SORT_MAX_BITS;
-constexpr size_t SORT_SMEM = sizeof(uint32_t) * SORT_DIGITS * (SORT_WARPS + 2);
+constexpr int SORT_STEPS = 4;                              // pairs of a thread in a tile
+constexpr int SORT_TILE = SORT_STEPS * SORT_THREADS;
+constexpr int CLEAR_CTAS = 304;
 
-struct SortBuffers {
-    uint32_t *key[2], *pos[2];   // the sorted pairs end in [1]
-    uint8_t *present;            // V flags: the id occurs (null: not wanted)
-    uint32_t *spanning;          // count of the list of segments that span chunks
+struct SortArgs {
+    const void *ids;
+    uint32_t n, V;
+    int64_t pad;
+    const uint32_t *kin, *pin;   // the pass's pairs; null: the ids themselves
+    uint32_t *kout, *pout;
+    uint32_t *count;             // [ctas][SORT_DIGITS]
+    uint32_t *spanning;          // count of the list of long segments
+    int ctas, rounds;            // parts, and tiles of a part
+    int shift, bits;
+    uint4 *clear;                // this launch's share of gW
+    int64_t clear16;
+    unsigned char *ends[2];      // the bytes of gW before and after its 16-byte pieces
+    int end_bytes[2];
 };
 
-template <typename Id>
-__global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS)
-    k_sort_ids(const void *ids, uint32_t n, uint32_t V, int64_t pad, SortBuffers b, int passes,
-               int bits) {
-    extern __shared__ uint32_t sort_smem[];
-    uint32_t *cnt = sort_smem;                              // [SORT_WARPS][SORT_DIGITS]
-    uint32_t *total = cnt + SORT_WARPS * SORT_DIGITS;       // [SORT_DIGITS] this CTA's counts
-    uint32_t *base = total + SORT_DIGITS;                   // [SORT_DIGITS] first place of a digit
-    __shared__ uint32_t warp_sum[SORT_DIGITS / 32];
-    cg::cluster_group cluster = cg::this_cluster();
-    const uint32_t r = cluster.block_rank();
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    const uint32_t mask = (1u << bits) - 1u;
-    // steps of 32 pairs per warp
-    const uint32_t steps = (n + SORT_CTAS * SORT_THREADS - 1) / (SORT_CTAS * SORT_THREADS);
-    const uint64_t w0 = (static_cast<uint64_t>(r) * SORT_WARPS + w) * steps * 32;
+struct SortShared {
+    uint32_t cnt[SORT_WARPS][SORT_DIGITS];
+    uint32_t start[SORT_DIGITS];     // first place of a digit in the tile
+    uint32_t base[SORT_DIGITS];      // and in the output
+    uint32_t sums[2][4][SORT_DIGITS];
+    uint32_t key[SORT_TILE], pos[SORT_TILE];
+    uint32_t warp_sum[SORT_WARPS];
+};
 
-    if (b.present != nullptr)
-        for (uint32_t i = r * SORT_THREADS + tid; i < V; i += SORT_CTAS * SORT_THREADS)
-            b.present[i] = 0;
-    if (r == 0 && tid == 0) *b.spanning = 0;
-
-    for (int p = 0; p < passes; ++p) {
-        const int shift = p * bits;
-        // the last pass writes [1]
-        const int to = (passes - 1 - p) & 1 ? 0 : 1;
-        const uint32_t *kin = b.key[to ^ 1], *pin = b.pos[to ^ 1];
-        uint32_t *kout = b.key[to], *pout = b.pos[to];
-        auto key_at = [&](uint64_t i) -> uint32_t {
-            if (i >= n) return 0xffffffffu;
-            if (p > 0) return __ldcg(kin + i);
-            const int64_t id = id_at<Id>(ids, i);
-            return id >= 0 && id < V && id != pad ? static_cast<uint32_t>(id) : V;
-        };
-        uint32_t *mine = cnt + w * SORT_DIGITS;
-        for (int i = tid; i < SORT_WARPS * SORT_DIGITS; i += SORT_THREADS) cnt[i] = 0;
-        __syncthreads();
-        for (uint32_t s = 0; s < steps; ++s) {
-            const uint64_t i = w0 + static_cast<uint64_t>(s) * 32 + lane;
-            const uint32_t k = key_at(i);
-            const uint32_t digit = i < n ? (k >> shift) & mask : 0xffffffffu;
-            const unsigned peers = __match_any_sync(FULL_MASK, digit);
-            if (i < n && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
-            __syncwarp();
-        }
-        __syncthreads();
-        if (tid < SORT_DIGITS) {
-            uint32_t run = 0;
-#pragma unroll 8
-            for (int v = 0; v < SORT_WARPS; ++v) {
-                const uint32_t c = cnt[v * SORT_DIGITS + tid];
-                cnt[v * SORT_DIGITS + tid] = run;
-                run += c;
-            }
-            total[tid] = run;
-        }
-        cluster.sync();
-        uint32_t before = 0, all = 0;
-        if (tid < SORT_DIGITS) {
-            for (uint32_t c = 0; c < SORT_CTAS; ++c) {
-                const uint32_t t = *cluster.map_shared_rank(total + tid, c);
-                before += c < r ? t : 0;
-                all += t;
-            }
-        }
-        // exclusive scan of `all` over the digits (the first 16 warps)
-        uint32_t incl = all;
+// lanes that hold the same digit (out-of-range lanes share one above the digits):
+// one ballot per bit, independent of one another, which is faster than match.any
+// on digits that mostly differ
+__device__ __forceinline__ unsigned same_digit(uint32_t digit) {
+    unsigned peers = FULL_MASK;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t t = __shfl_up_sync(FULL_MASK, incl, o);
-            if (lane >= o) incl += t;
-        }
-        if (tid < SORT_DIGITS && lane == 31) warp_sum[w] = incl;
-        __syncthreads();
-        if (tid < SORT_DIGITS) {
-            uint32_t lower = 0;
-            for (int v = 0; v < w; ++v) lower += warp_sum[v];
-            base[tid] = lower + incl - all + before;
-        }
-        __syncthreads();
-        for (int i = tid; i < SORT_WARPS * SORT_DIGITS; i += SORT_THREADS)
-            cnt[i] += base[i & (SORT_DIGITS - 1)];
-        __syncthreads();
-        for (uint32_t s = 0; s < steps; ++s) {
-            const uint64_t i = w0 + static_cast<uint64_t>(s) * 32 + lane;
-            const uint32_t k = key_at(i);
-            const uint32_t digit = i < n ? (k >> shift) & mask : 0xffffffffu;
-            const unsigned peers = __match_any_sync(FULL_MASK, digit);
-            const uint32_t first = i < n ? mine[digit] : 0;
-            __syncwarp();
-            if (i < n) {
-                const uint32_t at = first + __popc(peers & ((1u << lane) - 1u));
-                kout[at] = k;
-                pout[at] = p > 0 ? __ldcg(pin + i) : static_cast<uint32_t>(i);
-                if (lane == __ffs(peers) - 1) mine[digit] = first + __popc(peers);
-            }
-            __syncwarp();
-        }
-        cluster.sync();   // this pass's pairs are visible; `total` is free again
+    for (int i = 0; i <= SORT_MAX_BITS; ++i) {
+        const bool one = (digit >> i) & 1u;
+        const unsigned vote = __ballot_sync(FULL_MASK, one);
+        peers &= one ? vote : ~vote;
     }
-    if (b.present != nullptr) {
-        const uint32_t *keys = b.key[1];
-        for (uint64_t i = r * SORT_THREADS + tid; i < n; i += SORT_CTAS * SORT_THREADS) {
-            const uint32_t k = __ldcg(keys + i);
-            if (k < V && (i == 0 || __ldcg(keys + i - 1) != k)) b.present[k] = 1;
+    return peers;
+}
+
+template <typename Id>
+__device__ __forceinline__ void sort_load(const SortArgs &a, uint64_t i0, uint32_t (&k)[SORT_STEPS]) {
+#pragma unroll
+    for (int j = 0; j < SORT_STEPS; ++j) {
+        const uint64_t i = i0 + j * 32;
+        k[j] = a.V;
+        if (i >= a.n) continue;
+        if (a.kin != nullptr) {
+            k[j] = a.kin[i];
+        } else {
+            const int64_t id = id_at<Id>(a.ids, i);
+            if (id >= 0 && id < a.V && id != a.pad) k[j] = static_cast<uint32_t>(id);
         }
     }
 }
 
+// counts the warp's digits; rank: a pair's rank among its warp's equal digits
+__device__ __forceinline__ void sort_rank(uint32_t *mine, const uint32_t (&k)[SORT_STEPS], uint64_t i0,
+                                          uint64_t n, int shift, uint32_t mask,
+                                          uint32_t (&rank)[SORT_STEPS]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < SORT_STEPS; ++j) {
+        const bool in = i0 + j * 32 < n;
+        const uint32_t digit = in ? (k[j] >> shift) & mask : SORT_DIGITS;
+        const unsigned peers = same_digit(digit);
+        const uint32_t before = in ? mine[digit] : 0;
+        __syncwarp();
+        rank[j] = before + __popc(peers & ((1u << lane) - 1u));
+        if (in && lane == __ffs(peers) - 1) mine[digit] = before + __popc(peers);
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void sort_zero(SortShared &s) {
+    uint4 *p = reinterpret_cast<uint4 *>(s.cnt);
+#pragma unroll
+    for (int i = 0; i < SORT_WARPS * SORT_DIGITS / 4 / SORT_THREADS; ++i)
+        p[i * SORT_THREADS + threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// the warps' counts of this thread's digit become counts before each warp; returns their sum
+__device__ __forceinline__ uint32_t sort_scan_warps(SortShared &s) {
+    uint32_t c[SORT_WARPS], run = 0;
+#pragma unroll
+    for (int v = 0; v < SORT_WARPS; ++v) c[v] = s.cnt[v][threadIdx.x];
+#pragma unroll
+    for (int v = 0; v < SORT_WARPS; ++v) {
+        s.cnt[v][threadIdx.x] = run;
+        run += c[v];
+    }
+    return run;
+}
+
+// exclusive scan of v over the digits (one per thread)
+__device__ __forceinline__ uint32_t sort_scan_digits(SortShared &s, uint32_t v) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(FULL_MASK, incl, o);
+        if (lane >= o) incl += t;
+    }
+    __syncthreads();   // warp_sum is free
+    if (lane == 31) s.warp_sum[w] = incl;
+    __syncthreads();
+    uint32_t lower = 0;
+#pragma unroll
+    for (int v2 = 0; v2 < SORT_WARPS; ++v2) lower += v2 < w ? s.warp_sum[v2] : 0;
+    return lower + incl - v;
+}
+static_assert(SORT_THREADS == SORT_DIGITS, "one digit per thread");
+
+__device__ __forceinline__ void clear_share(const SortArgs &a, int cta) {
+    const int64_t step = static_cast<int64_t>(CLEAR_CTAS) * SORT_THREADS;
+    for (int64_t i = static_cast<int64_t>(cta) * SORT_THREADS + threadIdx.x; i < a.clear16; i += step)
+        a.clear[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (cta == 0)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (static_cast<int>(threadIdx.x) < a.end_bytes[q]) a.ends[q][threadIdx.x] = 0;
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(SORT_THREADS) k_sort_count(const SortArgs a) {
+    extern __shared__ __align__(16) unsigned char sort_smem[];
+    SortShared &s = *reinterpret_cast<SortShared *>(sort_smem);
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (static_cast<int>(blockIdx.x) >= a.ctas) return clear_share(a, blockIdx.x - a.ctas);
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t k[SORT_STEPS], rank[SORT_STEPS];
+    const uint64_t part = static_cast<uint64_t>(blockIdx.x) * a.rounds * SORT_TILE;
+    sort_zero(s);
+    __syncthreads();
+    for (int r = 0; r < a.rounds; ++r) {
+        const uint64_t i0 = part + r * static_cast<uint64_t>(SORT_TILE) + w * (32 * SORT_STEPS) + lane;
+        sort_load<Id>(a, i0, k);
+        sort_rank(s.cnt[w], k, i0, a.n, a.shift, (1u << a.bits) - 1u, rank);
+    }
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (int v = 0; v < SORT_WARPS; ++v) all += s.cnt[v][threadIdx.x];
+    a.count[blockIdx.x * SORT_DIGITS + threadIdx.x] = all;
+}
+
+// ranks a tile's pairs and writes them from s.base on
+__device__ __forceinline__ void sort_place(SortShared &s, const SortArgs &a, uint64_t tile,
+                                           uint64_t i0, const uint32_t (&k)[SORT_STEPS]) {
+    const int w = threadIdx.x >> 5;
+    const uint32_t mask = (1u << a.bits) - 1u;
+    uint32_t p[SORT_STEPS], rank[SORT_STEPS];
+#pragma unroll
+    for (int j = 0; j < SORT_STEPS; ++j) {
+        const uint64_t i = i0 + j * 32;
+        p[j] = a.kin != nullptr && i < a.n ? a.pin[i] : static_cast<uint32_t>(i);
+    }
+    sort_rank(s.cnt[w], k, i0, a.n, a.shift, mask, rank);
+    __syncthreads();
+    const uint32_t own = sort_scan_warps(s);
+    const uint32_t start = sort_scan_digits(s, own);
+    s.start[threadIdx.x] = start;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < SORT_STEPS; ++j) {
+        if (i0 + j * 32 >= a.n) continue;
+        const uint32_t digit = (k[j] >> a.shift) & mask;
+        const uint32_t at = s.start[digit] + s.cnt[w][digit] + rank[j];
+        s.key[at] = k[j];
+        s.pos[at] = p[j];
+    }
+    __syncthreads();
+    const uint32_t have = tile >= a.n ? 0 : a.n - tile < SORT_TILE ? static_cast<uint32_t>(a.n - tile) : SORT_TILE;
+#pragma unroll
+    for (int j = 0; j < SORT_STEPS; ++j) {
+        const uint32_t i = j * SORT_THREADS + threadIdx.x;
+        if (i >= have) continue;
+        const uint32_t key = s.key[i], digit = (key >> a.shift) & mask;
+        const uint32_t at = s.base[digit] + i - s.start[digit];
+        a.kout[at] = key;
+        a.pout[at] = s.pos[i];
+    }
+    __syncthreads();
+    s.base[threadIdx.x] += own;   // the next tile's
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(SORT_THREADS) k_sort_place(const SortArgs a) {
+    extern __shared__ __align__(16) unsigned char sort_smem[];
+    SortShared &s = *reinterpret_cast<SortShared *>(sort_smem);
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (static_cast<int>(blockIdx.x) >= a.ctas) return clear_share(a, blockIdx.x - a.ctas);
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+    if (blockIdx.x == 0 && t == 0) *a.spanning = 0;
+    // digit counts: 128 threads a part (four digits each), four parts at a time
+    uint4 before = make_uint4(0u, 0u, 0u, 0u), all = before;
+    const uint4 *count = reinterpret_cast<const uint4 *>(a.count) + (t & 127);
+#pragma unroll 8
+    for (int c = t >> 7; c < a.ctas; c += 4) {
+        const uint4 v = count[c * (SORT_DIGITS / 4)];
+        all.x += v.x; all.y += v.y; all.z += v.z; all.w += v.w;
+        if (c < static_cast<int>(blockIdx.x)) {
+            before.x += v.x; before.y += v.y; before.z += v.z; before.w += v.w;
+        }
+    }
+    reinterpret_cast<uint4 *>(s.sums[0][t >> 7])[t & 127] = before;
+    reinterpret_cast<uint4 *>(s.sums[1][t >> 7])[t & 127] = all;
+    __syncthreads();
+    uint32_t lower = 0, total = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        lower += s.sums[0][q][t];
+        total += s.sums[1][q][t];
+    }
+    s.base[t] = sort_scan_digits(s, total) + lower;
+    const uint64_t part = static_cast<uint64_t>(blockIdx.x) * a.rounds * SORT_TILE;
+    for (int r = 0; r < a.rounds; ++r) {
+        const uint64_t tile = part + r * static_cast<uint64_t>(SORT_TILE);
+        const uint64_t i0 = tile + w * (32 * SORT_STEPS) + lane;
+        uint32_t k[SORT_STEPS];
+        sort_load<Id>(a, i0, k);
+        sort_zero(s);
+        __syncthreads();
+        sort_place(s, a, tile, i0, k);
+    }
+}
+
+// at most SORT_TILE ids: every pass in shared memory
+template <typename Id>
+__global__ void __launch_bounds__(SORT_THREADS) k_sort_one(SortArgs a, int passes) {
+    extern __shared__ __align__(16) unsigned char sort_smem[];
+    SortShared &s = *reinterpret_cast<SortShared *>(sort_smem);
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (blockIdx.x > 0) return clear_share(a, blockIdx.x - 1);
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+    const uint32_t mask = (1u << a.bits) - 1u;
+    if (t == 0) *a.spanning = 0;
+    const uint64_t i0 = w * (32 * SORT_STEPS) + lane;
+    uint32_t k[SORT_STEPS], p[SORT_STEPS], rank[SORT_STEPS];
+    sort_load<Id>(a, i0, k);
+#pragma unroll
+    for (int j = 0; j < SORT_STEPS; ++j) p[j] = static_cast<uint32_t>(i0) + j * 32;
+    for (int q = 0; q < passes; ++q) {
+        const int shift = q * a.bits;
+        sort_zero(s);
+        __syncthreads();
+        sort_rank(s.cnt[w], k, i0, a.n, shift, mask, rank);
+        __syncthreads();
+        const uint32_t start = sort_scan_digits(s, sort_scan_warps(s));
+        s.start[t] = start;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < SORT_STEPS; ++j) {
+            if (i0 + j * 32 >= a.n) continue;
+            const uint32_t digit = (k[j] >> shift) & mask;
+            const uint32_t at = s.start[digit] + s.cnt[w][digit] + rank[j];
+            s.key[at] = k[j];
+            s.pos[at] = p[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < SORT_STEPS; ++j) {
+            if (i0 + j * 32 >= a.n) continue;
+            k[j] = s.key[i0 + j * 32];
+            p[j] = s.pos[i0 + j * 32];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < SORT_STEPS; ++j) {
+        if (i0 + j * 32 >= a.n) continue;
+        a.kout[i0 + j * 32] = k[j];
+        a.pout[i0 + j * 32] = p[j];
+    }
+}
+
+template <typename Id>
+cudaError_t sort_ids(SortArgs a, uint32_t *const (&key)[2], uint32_t *const (&pos)[2], int passes,
+                     unsigned char *clear, int64_t clear16, bool clears, cudaStream_t stream) {
+    static std::atomic<unsigned long long> configured{0};
+    constexpr int smem = sizeof(SortShared);
+    cudaError_t e = once_per_device(configured, [](int) {
+        cudaError_t r = cudaFuncSetAttribute(k_sort_count<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(k_sort_place<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(k_sort_one<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return r;
+    });
+    if (e != cudaSuccess) return e;
+    const int more = clears ? CLEAR_CTAS : 0;
+    if (a.n <= SORT_TILE) {
+        a.kout = key[1];
+        a.pout = pos[1];
+        a.clear = reinterpret_cast<uint4 *>(clear);
+        a.clear16 = clear16;
+        k_sort_one<Id><<<1 + more, SORT_THREADS, smem, stream>>>(a, passes);
+        return cudaGetLastError();
+    }
+    const int64_t tiles = (static_cast<int64_t>(a.n) + SORT_TILE - 1) / SORT_TILE;
+    a.rounds = static_cast<int>((tiles + SORT_CTAS - 1) / SORT_CTAS);
+    a.ctas = static_cast<int>((tiles + a.rounds - 1) / a.rounds);
+    const int64_t share = (clear16 + 2 * passes - 1) / (2 * passes);
+    int64_t cleared = 0;
+    for (int q = 0; q < passes; ++q) {
+        a.shift = q * a.bits;
+        const int to = (passes - 1 - q) & 1 ? 0 : 1;   // the last pass writes [1]
+        a.kin = q == 0 ? nullptr : key[to ^ 1];
+        a.pin = pos[to ^ 1];
+        a.kout = key[to];
+        a.pout = pos[to];
+        for (int half = 0; half < 2; ++half) {
+            a.clear = reinterpret_cast<uint4 *>(clear) + cleared;
+            a.clear16 = clear16 - cleared < share ? clear16 - cleared : share;
+            cleared += a.clear16;
+            if (q == 0 && half == 0) {
+                k_sort_count<Id><<<a.ctas + more, SORT_THREADS, smem, stream>>>(a);
+                e = cudaGetLastError();
+            } else {
+                e = launch_dependent(half == 0 ? k_sort_count<Id> : k_sort_place<Id>,
+                                     a.ctas + more, SORT_THREADS, smem, stream, a);
+            }
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
+}
+
 // ---------------------------------------------------------------- the gradient
 // A warp sums one slab of a chunk of 32 consecutive sorted pairs, eight rows of
-// loads in flight.  A segment (the pairs of one id) inside the chunk is written
-// at once; one that crosses a chunk's edge leaves fp32 partial sums: slot 0 of a
-// chunk for the segment that came in from the left, slot 1 for one that begins
-// here and goes on.  Those are joined in order by k_embed_join.
+// loads in flight.  It writes the segments (the pairs of one id) that begin in
+// its chunk, going on into the next chunk for one that crosses the edge.  Only a
+// long segment, one that fills at least one whole chunk, is cut at the chunks'
+// edges: each chunk leaves its part of the sum in fp32 (slot 0: the segment came
+// in from the left, slot 1: it begins here), and k_embed_join adds the parts in
+// order.  With ids as frequent as words, only some hundred ids are that long.
 constexpr int CHUNK = 32;
 
 template <typename T, int VEC>
@@ -219,81 +448,122 @@ __device__ __forceinline__ void write_row(T *p, float (&acc)[VEC], float scale, 
     store_f32<T, VEC>(p, o);
 }
 
+// Rows on their way: each lane copies its own VEC columns to its own place in
+// shared memory (cp.async) and reads them back itself, so a warp keeps 16 rows
+// in flight in no registers and needs no barrier.  (Eight rows in registers: 126
+// registers, 16 warps an SM, 2.8 TB/s on 262144 x 1024 bf16.)
+constexpr int BATCH = 8;             // rows of one commit group
+constexpr int RING = 2 * BATCH;
+
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src) {
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src),
+                     "n"(BYTES >= 4 ? BYTES : 4)
+                     : "memory");
+}
+
 template <typename T, int VEC>
 __global__ void __launch_bounds__(EMBED_THREADS)
     k_embed_grad(const uint32_t *__restrict__ key, const uint32_t *__restrict__ pos,
-                 const uint8_t *__restrict__ present, const T *__restrict__ g, T *__restrict__ gW,
-                 float *__restrict__ part, uint32_t *__restrict__ spanning, uint32_t n, uint32_t V,
-                 int64_t d, int slabs, int64_t chunk_items, int64_t items, float scale,
-                 bool accumulate) {
+                 const T *__restrict__ g, T *__restrict__ gW, float *__restrict__ part,
+                 uint32_t *__restrict__ spanning, uint32_t n, uint32_t V, int64_t d, int slabs,
+                 int64_t items, float scale, bool accumulate) {
+    using P = Pack<T, VEC>;
+    extern __shared__ __align__(16) unsigned char grad_smem[];
     const int lane = threadIdx.x & 31;
-    int64_t item = blockIdx.x * static_cast<int64_t>(EMBED_THREADS / 32) + (threadIdx.x >> 5);
+    P *ring = reinterpret_cast<P *>(grad_smem) + (threadIdx.x >> 5) * RING * 32 + lane;   // [RING][32]
+    const int64_t item = blockIdx.x * static_cast<int64_t>(EMBED_THREADS / 32) + (threadIdx.x >> 5);
+    dependents_may_launch();
+    wait_for_prerequisites();
     if (item >= items) return;
-    const bool zero = item >= chunk_items;
-    if (zero) item -= chunk_items;
     const int64_t c = static_cast<int64_t>(item % slabs) * (32 * VEC) + lane * VEC;
     const bool in = c < d;
-    if (zero) {   // rows of ids that do not occur
-        const int64_t v0 = item / slabs * 32;
-        const bool absent = v0 + lane < V && present[v0 + lane] == 0;
-        unsigned todo = __ballot_sync(FULL_MASK, absent);
-        const float none[VEC] = {};
-        while (todo != 0) {
-            const int j = __ffs(todo) - 1;
-            todo &= todo - 1;
-            if (in) store_f32<T, VEC>(gW + (v0 + j) * d + c, none);
-        }
-        return;
-    }
     const uint32_t chunk = static_cast<uint32_t>(item / slabs);
     const uint64_t i0 = static_cast<uint64_t>(chunk) * CHUNK;
-    const uint32_t k_lane = i0 + lane < n ? key[i0 + lane] : V;
-    const uint32_t p_lane = i0 + lane < n ? pos[i0 + lane] : 0;
-    const uint32_t k_prev = i0 > 0 ? key[i0 - 1] : 0xffffffffu;
-    const uint32_t k_next = i0 + CHUNK < n ? key[i0 + CHUNK] : V;
-    const int m = __popc(__ballot_sync(FULL_MASK, k_lane < V));   // valid pairs come first
+    // this chunk's pairs and the next one's; V marks pairs that take no part
+    uint32_t k_lane = i0 + lane < n ? key[i0 + lane] : V;
+    uint32_t p_lane = i0 + lane < n ? pos[i0 + lane] : 0;
+    const uint32_t k_more = i0 + CHUNK + lane < n ? key[i0 + CHUNK + lane] : V;
+    const uint32_t p_more = i0 + CHUNK + lane < n ? pos[i0 + CHUNK + lane] : 0;
+    const uint32_t k_prev = i0 > 0 ? key[i0 - 1] : 0xffffffffu;       // last and first pair
+    const uint32_t k_prev0 = i0 > 0 ? key[i0 - CHUNK] : 0xffffffffu;  // of the chunk before
+    const uint32_t first = __shfl_sync(FULL_MASK, k_lane, 0), last = __shfl_sync(FULL_MASK, k_lane, 31);
+    const uint32_t more0 = __shfl_sync(FULL_MASK, k_more, 0), more31 = __shfl_sync(FULL_MASK, k_more, 31);
+    const int valid = __popc(__ballot_sync(FULL_MASK, k_lane < V));   // valid pairs come first
+    if (valid == 0) return;
+    const bool whole = first == last;
+    // the segment that came in from the left: its part is ours only if it is long
+    const bool came_in = first == k_prev;
+    const bool head_long = came_in && (whole || k_prev0 == first);
+    // the segment that goes on to the right
+    const bool goes_on = last < V && more0 == last;
+    const bool tail_long = goes_on && (whole || more31 == last);
+    int j_first = 0;
+    if (came_in && !head_long) j_first = __popc(__ballot_sync(FULL_MASK, k_lane == first));
+    // pairs of the next chunk that end our last segment
+    const int extra = goes_on && !tail_long ? __popc(__ballot_sync(FULL_MASK, k_more == last)) : 0;
+    const int m = valid + extra;   // extra > 0 only if valid == 32
+    if (j_first >= m) return;
     float acc[VEC] = {};
-    uint32_t cur = __shfl_sync(FULL_MASK, k_lane, 0);
-    bool began = cur != k_prev;   // the current segment begins in this chunk
-    auto flush = [&](bool ended) {
-        if (began && ended) {
+    uint32_t cur = __shfl_sync(FULL_MASK, k_lane, j_first & 31);
+    bool in_part = head_long;   // the current segment came in from the left
+    auto flush = [&](bool out_part) {
+        if (!in_part && !out_part) {
             if (in) write_row<T, VEC>(gW + static_cast<int64_t>(cur) * d + c, acc, scale, accumulate);
         } else {
-            float *to = part + (static_cast<int64_t>(chunk) * 2 + (began ? 1 : 0)) * d + c;
+            float *to = part + (static_cast<int64_t>(chunk) * 2 + (in_part ? 0 : 1)) * d + c;
             if (in) store_f32<float, VEC>(to, acc);
-            if (began && c == 0) spanning[1 + atomicAdd(spanning, 1u)] = chunk;
+            if (!in_part && c == 0) spanning[1 + atomicAdd(spanning, 1u)] = chunk;
         }
     };
-    constexpr int AHEAD = 8;
-    for (int j0 = 0; j0 < m; j0 += AHEAD) {
-        float v[AHEAD][VEC];
+    // starts the copies of rows j0 .. j0 + 7
+    auto issue = [&](int j0) {
+        P direct[BATCH];
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const uint32_t at = __shfl_sync(FULL_MASK, p_lane, (j0 + a) & 31);
-            if (in && j0 + a < m) load_f32<T, VEC>(g + static_cast<int64_t>(at) * d + c, v[a]);
+        for (int a = 0; a < BATCH; ++a) {
+            const int j = j0 + a;
+            const uint32_t at0 = __shfl_sync(FULL_MASK, p_lane, j & 31), at1 = __shfl_sync(FULL_MASK, p_more, j & 31);
+            const T *src = g + static_cast<int64_t>(j < CHUNK ? at0 : at1) * d + c;
+            if (!in || j >= m) continue;
+            if (sizeof(P) >= 4) copy_async<sizeof(P)>(ring + j % RING * 32, src);
+            else direct[a] = *reinterpret_cast<const P *>(src);
         }
+        if (sizeof(P) >= 4) {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            if (j0 + a >= m) break;
-            const uint32_t k = __shfl_sync(FULL_MASK, k_lane, (j0 + a) & 31);
+            for (int a = 0; a < BATCH; ++a)
+                if (in && j0 + a < m) ring[(j0 + a) % RING * 32] = direct[a];
+        }
+    };
+    issue(j_first);
+    for (int j0 = j_first; j0 < m; j0 += BATCH) {
+        issue(j0 + BATCH);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const int j1 = j0 + BATCH < m ? j0 + BATCH : m;
+        for (int j = j0; j < j1; ++j) {
+            const uint32_t k0 = __shfl_sync(FULL_MASK, k_lane, j & 31);
+            const uint32_t k = j < CHUNK ? k0 : last;
             if (k != cur) {
-                flush(true);
+                flush(false);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
                 cur = k;
-                began = true;
+                in_part = false;
             }
+            const P v = ring[j % RING * 32];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] += v[a][e];
+            for (int e = 0; e < VEC; ++e) acc[e] += to_f32(v.v[e]);
         }
     }
-    if (m > 0) flush(k_next != cur);
+    flush(tail_long && cur == last);
 }
 
-// Joins the partial sums of the segments that span chunks: a CTA per (segment,
-// slab); its warps take every JOIN_WARPS-th chunk and the warps' sums are added
+// Joins the parts of the long segments: a CTA per (segment, slab); its warps take every JOIN_WARPS-th chunk and the warps' sums are added
 // in order.
-constexpr int JOIN_WARPS = 16;
+constexpr int JOIN_WARPS = 8, JOIN_CTAS = 152 * 8;
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
@@ -301,22 +571,22 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
                  const uint32_t *__restrict__ spanning, T *__restrict__ gW, uint32_t n, int64_t d,
                  int slabs, float scale, bool accumulate) {
     __shared__ float sum[JOIN_WARPS][32][VEC + 1];
+    wait_for_prerequisites();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t items = static_cast<int64_t>(spanning[0]) * slabs;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const uint32_t c0 = spanning[1 + item / slabs];
         const int64_t c = static_cast<int64_t>(item % slabs) * (32 * VEC) + lane * VEC;
         const uint32_t k = key[static_cast<uint64_t>(c0) * CHUNK + CHUNK - 1];
-        // first pair after the segment
-        uint64_t lo = static_cast<uint64_t>(c0 + 1) * CHUNK, hi = n;
-        while (lo < hi) {
-            const uint64_t mid = (lo + hi) / 2;
-            if (key[mid] == k) lo = mid + 1; else hi = mid;
+        // its last chunk: the chunks after c0 that begin with k, counted by all threads
+        uint32_t c1 = c0;
+        for (int got = JOIN_WARPS * 32; got == JOIN_WARPS * 32; c1 += got) {
+            const uint64_t i = (static_cast<uint64_t>(c1) + 1 + threadIdx.x) * CHUNK;
+            got = __syncthreads_count(i < n && key[i] == k);
         }
-        const uint32_t c1 = static_cast<uint32_t>((lo - 1) / CHUNK);   // its last chunk
         float acc[VEC] = {};
         if (c < d) {
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t q = c0 + w; q <= c1; q += JOIN_WARPS) {
                 float v[VEC];
                 load_f32<float, VEC>(part + (static_cast<int64_t>(q) * 2 + (q == c0 ? 1 : 0)) * d + c, v);
@@ -339,10 +609,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
 
 // ---------------------------------------------------------------- host side
 struct GradLayout {
-    size_t key[2], pos[2], present, spanning, part, total;
+    size_t key[2], pos[2], count, spanning, part, total;
 };
 
-GradLayout grad_layout(int64_t n, int64_t V, int64_t d) {
+GradLayout grad_layout(int64_t n, int64_t d) {
     GradLayout l{};
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -355,7 +625,7 @@ GradLayout grad_layout(int64_t n, int64_t V, int64_t d) {
         l.key[i] = take(sizeof(uint32_t) * n);
         l.pos[i] = take(sizeof(uint32_t) * n);
     }
-    l.present = take(V);
+    l.count = take(sizeof(uint32_t) * SORT_CTAS * SORT_DIGITS);
     l.spanning = take(sizeof(uint32_t) * (1 + chunks));
     l.part = take(sizeof(float) * chunks * 2 * d);
     l.total = at;
@@ -386,24 +656,26 @@ cudaError_t lookup(const void *ids, int ids_type, const void *W, void *out, int6
 }
 
 template <typename T, int VEC>
-cudaError_t gradient(const void *g, void *gW, const SortBuffers &b, float *part, int64_t n,
-                     int64_t V, int64_t d, float scale, bool accumulate, cudaStream_t stream) {
+cudaError_t gradient(const void *g, void *gW, const SortArgs &a, float *part, int64_t n, int64_t d,
+                     float scale, bool accumulate, cudaStream_t stream) {
+    constexpr int smem = EMBED_THREADS * RING * static_cast<int>(sizeof(Pack<T, VEC>));
+    static std::atomic<unsigned long long> configured{0};
+    cudaError_t e = once_per_device(configured, [](int) {
+        return cudaFuncSetAttribute(k_embed_grad<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
     const int slabs = static_cast<int>((d + 32 * VEC - 1) / (32 * VEC));
-    const int64_t chunk_items = (n + CHUNK - 1) / CHUNK * slabs;
-    const int64_t items = chunk_items + (accumulate ? 0 : (V + 31) / 32 * slabs);
+    const int64_t items = (n + CHUNK - 1) / CHUNK * slabs;
     const int64_t blocks = (items + EMBED_THREADS / 32 - 1) / (EMBED_THREADS / 32);
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    k_embed_grad<T, VEC><<<static_cast<unsigned>(blocks), EMBED_THREADS, 0, stream>>>(
-        b.key[1], b.pos[1], b.present, static_cast<const T *>(g), static_cast<T *>(gW), part,
-        b.spanning, static_cast<uint32_t>(n), static_cast<uint32_t>(V), d, slabs, chunk_items,
-        items, scale, accumulate);
-    cudaError_t e = cudaGetLastError();
+    e = launch_dependent(k_embed_grad<T, VEC>, static_cast<unsigned>(blocks), EMBED_THREADS, smem, stream,
+                         a.kin, a.pin, static_cast<const T *>(g), static_cast<T *>(gW), part,
+                         a.spanning, a.n, a.V, d, slabs, items, scale, accumulate);
     if (e != cudaSuccess || n <= CHUNK) return e;
     const int64_t most = (n / CHUNK) * slabs;
-    k_embed_join<T, VEC><<<static_cast<unsigned>(most < 608 ? most : 608), JOIN_WARPS * 32, 0, stream>>>(
-        b.key[1], part, b.spanning, static_cast<T *>(gW), static_cast<uint32_t>(n), d, slabs,
-        scale, accumulate);
-    return cudaGetLastError();
+    return launch_dependent(k_embed_join<T, VEC>, static_cast<unsigned>(most < JOIN_CTAS ? most : JOIN_CTAS),
+                            JOIN_WARPS * 32, 0, stream, a.kin, part, a.spanning,
+                            static_cast<T *>(gW), a.n, d, slabs, scale, accumulate);
 }
 
 }  // namespace
@@ -431,7 +703,7 @@ int nrnn_embedding(const void *ids, int ids_type, const void *W, int dtype, int6
 
 size_t nrnn_embedding_backward_workspace_bytes(int64_t n, int64_t V, int64_t d) {
     if (n < 0 || V <= 0 || d <= 0 || n > INT32_MAX || V >= INT32_MAX || d > (1 << 24)) return 0;
-    return grad_layout(n, V, d).total;
+    return grad_layout(n, d).total;
 }
 
 int nrnn_embedding_backward(const void *ids, int ids_type, const void *g, int dtype, int64_t n,
@@ -443,7 +715,7 @@ int nrnn_embedding_backward(const void *ids, int ids_type, const void *g, int dt
     if (gW == nullptr || (n > 0 && g == nullptr)) return NRNN_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(gW)) % elem != 0)
         return NRNN_ERR_INVALID_ARG;
-    const GradLayout l = grad_layout(n, V, d);
+    const GradLayout l = grad_layout(n, d);
     if (workspace == nullptr || ws_bytes < l.total || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
         return NRNN_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -453,38 +725,41 @@ int nrnn_embedding_backward(const void *ids, int ids_type, const void *g, int dt
                    ? NRNN_OK : NRNN_ERR_CUDA;
     }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    SortBuffers b;
-    for (int i = 0; i < 2; ++i) {
-        b.key[i] = reinterpret_cast<uint32_t *>(ws + l.key[i]);
-        b.pos[i] = reinterpret_cast<uint32_t *>(ws + l.pos[i]);
-    }
-    b.present = accumulate ? nullptr : ws + l.present;
-    b.spanning = reinterpret_cast<uint32_t *>(ws + l.spanning);
+    SortArgs a{};
+    a.ids = ids;
+    a.n = static_cast<uint32_t>(n);
+    a.V = static_cast<uint32_t>(V);
+    a.pad = padding_id;
+    uint32_t *const key[2] = {reinterpret_cast<uint32_t *>(ws + l.key[0]),
+                              reinterpret_cast<uint32_t *>(ws + l.key[1])};
+    uint32_t *const pos[2] = {reinterpret_cast<uint32_t *>(ws + l.pos[0]),
+                              reinterpret_cast<uint32_t *>(ws + l.pos[1])};
+    a.count = reinterpret_cast<uint32_t *>(ws + l.count);
+    a.spanning = reinterpret_cast<uint32_t *>(ws + l.spanning);
     int key_bits = 1;
     while ((static_cast<int64_t>(1) << key_bits) <= V) ++key_bits;   // keys 0 .. V
     const int passes = (key_bits + SORT_MAX_BITS - 1) / SORT_MAX_BITS;
-    const int bits = (key_bits + passes - 1) / passes;
-    auto sort = ids_type == NRNN_I64 ? k_sort_ids<int64_t> : k_sort_ids<int32_t>;
-    static std::atomic<unsigned long long> configured{0};
-    cudaError_t e = once_per_device(configured, [](int) {
-        cudaError_t r = cudaFuncSetAttribute(k_sort_ids<int64_t>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(SORT_SMEM));
-        if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(k_sort_ids<int32_t>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(SORT_SMEM));
-        return r;
-    });
+    a.bits = (key_bits + passes - 1) / passes;
+    // the sort's launches clear gW, in whole 16-byte pieces but for its ends
+    const size_t gw_bytes = static_cast<size_t>(V) * d * elem;
+    unsigned char *to = static_cast<unsigned char *>(gW);
+    size_t head = (16 - reinterpret_cast<uintptr_t>(gW) % 16) % 16;
+    if (head > gw_bytes) head = gw_bytes;
+    const int64_t clear16 = accumulate ? 0 : static_cast<int64_t>((gw_bytes - head) / 16);
+    if (!accumulate) {
+        a.end_bytes[0] = static_cast<int>(head);
+        a.end_bytes[1] = static_cast<int>((gw_bytes - head) % 16);
+        a.ends[0] = to;
+        a.ends[1] = to + gw_bytes - a.end_bytes[1];
+    }
+    cudaError_t e = ids_type == NRNN_I64 ? sort_ids<int64_t>(a, key, pos, passes, to + head, clear16, accumulate == 0, s)
+                                         : sort_ids<int32_t>(a, key, pos, passes, to + head, clear16, accumulate == 0, s);
     if (e != cudaSuccess) return NRNN_ERR_CUDA;
-    sort<<<SORT_CTAS, SORT_THREADS, SORT_SMEM, s>>>(ids, static_cast<uint32_t>(n),
-                                                    static_cast<uint32_t>(V), padding_id, b, passes,
-                                                    bits);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return NRNN_ERR_CUDA;
+    a.kin = key[1];   // the sorted pairs
+    a.pin = pos[1];
     const int vec = vec_of(elem, d, 32, {g, gW});
-    e = NRNN_BY_WIDTH(dtype, vec, gradient, g, gW, b, reinterpret_cast<float *>(ws + l.part), n, V,
-                      d, scale, accumulate != 0, s);
+    e = NRNN_BY_WIDTH(dtype, vec, gradient, g, gW, a, reinterpret_cast<float *>(ws + l.part), n, d,
+                      scale, accumulate != 0, s);
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
