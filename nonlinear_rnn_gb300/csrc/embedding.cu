@@ -11,10 +11,14 @@
 // radix sort, and the sums follow the sorted order in fixed groups of 32.
 #include <initializer_list>
 
+#include <cooperative_groups.h>
+
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
 #include "nrnn_internal.h"
 #include "rows.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace nrnn {
 namespace {
@@ -30,7 +34,7 @@ __device__ __forceinline__ void wait_for_prerequisites() {
 
 // A warp works on 32 VEC consecutive columns (a slab) of a row.
 constexpr int GROUP_ROWS = 4;      // rows of one warp of the lookup
-constexpr int EMBED_THREADS = 256;
+constexpr int EMBED_THREADS = 128;
 
 template <typename Id> __device__ __forceinline__ int64_t id_at(const void *ids, int64_t i) {
     return static_cast<int64_t>(static_cast<const Id *>(ids)[i]);
@@ -81,10 +85,9 @@ __global__ void __launch_bounds__(EMBED_THREADS)
 // input: k_sort_count leaves the parts' digit counts, and k_sort_place adds up
 // the counts before its own part (all parts' for lower digits, earlier parts'
 // for equal ones), ranks its pairs and writes them.  Ranks follow (part, round,
-// warp, step, lane) = input order.  Up to SORT_TILE ids are sorted by one CTA in
-// one launch.  A tile's pairs are put in order in shared memory first, so that a
+// warp, step, lane) = input order.  A tile's pairs are put in order in shared memory first, so that a
 // digit's run leaves as whole lines.  (All passes in one cluster of 16 CTAs took
-// 56 us for 262144 ids, bound by those SMs, and no less for few.)
+// 56 us for 262144 ids, bound by those SMs; up to 32768 ids it is faster.)
 // Ids that take no part (padding, out of range) get the key V and sort last.
 //
 // The launches' further CTAs clear gW meanwhile, a share each.
@@ -102,7 +105,7 @@ struct SortArgs {
     const uint32_t *kin, *pin;   // the pass's pairs; null: the ids themselves
     uint32_t *kout, *pout;
     uint32_t *count;             // [ctas][SORT_DIGITS]
-    uint32_t *spanning;          // count of the list of long segments
+    uint32_t *spanning;          // the list of long segments: count, then {chunk, id}
     int ctas, rounds;            // parts, and tiles of a part
     int shift, bits;
     uint4 *clear;                // this launch's share of gW
@@ -206,6 +209,7 @@ __device__ __forceinline__ uint32_t sort_scan_digits(SortShared &s, uint32_t v) 
     return lower + incl - v;
 }
 static_assert(SORT_THREADS == SORT_DIGITS, "one digit per thread");
+static_assert(CLEAR_CTAS % 16 == 0, "whole clusters of the clearing CTAs");
 
 __device__ __forceinline__ void clear_share(const SortArgs &a, int cta) {
     const int64_t step = static_cast<int64_t>(CLEAR_CTAS) * SORT_THREADS;
@@ -323,18 +327,31 @@ __global__ void __launch_bounds__(SORT_THREADS) k_sort_place(const SortArgs a) {
     }
 }
 
-// at most SORT_TILE ids: every pass in shared memory
+// Up to SORT_CLUSTER tiles: one cluster with a tile per CTA does every pass in
+// one launch.  A pass's counts and pairs are exchanged through distributed shared
+// memory; only the sorted pairs go to global memory.  (30001 ids: two launches a
+// pass took 23 us.)
+constexpr int SORT_CLUSTER = 16;   // above the portable 8: allowed by attribute
+
+struct ClusterSortShared {
+    SortShared s;
+    uint32_t key[2][SORT_TILE], pos[2][SORT_TILE];
+    uint32_t total[SORT_DIGITS];
+};
+
 template <typename Id>
-__global__ void __launch_bounds__(SORT_THREADS) k_sort_one(SortArgs a, int passes) {
+__global__ void __launch_bounds__(SORT_THREADS) k_sort_cluster(SortArgs a, int passes) {
     extern __shared__ __align__(16) unsigned char sort_smem[];
-    SortShared &s = *reinterpret_cast<SortShared *>(sort_smem);
-    dependents_may_launch();
-    wait_for_prerequisites();
-    if (blockIdx.x > 0) return clear_share(a, blockIdx.x - 1);
+    ClusterSortShared &c = *reinterpret_cast<ClusterSortShared *>(sort_smem);
+    SortShared &s = c.s;
+    if (static_cast<int>(blockIdx.x) >= a.ctas) return clear_share(a, blockIdx.x - a.ctas);
+    cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t r = cluster.block_rank();
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     const uint32_t mask = (1u << a.bits) - 1u;
-    if (t == 0) *a.spanning = 0;
-    const uint64_t i0 = w * (32 * SORT_STEPS) + lane;
+    if (r == 0 && t == 0) *a.spanning = 0;
+    const uint32_t slot = w * (32 * SORT_STEPS) + lane;          // + 32 j: this thread's pairs
+    const uint64_t i0 = static_cast<uint64_t>(r) * SORT_TILE + slot;
     uint32_t k[SORT_STEPS], p[SORT_STEPS], rank[SORT_STEPS];
     sort_load<Id>(a, i0, k);
 #pragma unroll
@@ -345,23 +362,31 @@ __global__ void __launch_bounds__(SORT_THREADS) k_sort_one(SortArgs a, int passe
         __syncthreads();
         sort_rank(s.cnt[w], k, i0, a.n, shift, mask, rank);
         __syncthreads();
-        const uint32_t start = sort_scan_digits(s, sort_scan_warps(s));
-        s.start[t] = start;
+        c.total[t] = sort_scan_warps(s);
+        cluster.sync();
+        uint32_t before = 0, all = 0;
+        for (int o = 0; o < a.ctas; ++o) {
+            const uint32_t v = *cluster.map_shared_rank(c.total + t, o);
+            before += o < static_cast<int>(r) ? v : 0;
+            all += v;
+        }
+        const uint32_t base = sort_scan_digits(s, all) + before;
+        s.base[t] = base;
         __syncthreads();
+        uint32_t *to_key = c.key[q & 1], *to_pos = c.pos[q & 1];
 #pragma unroll
         for (int j = 0; j < SORT_STEPS; ++j) {
             if (i0 + j * 32 >= a.n) continue;
             const uint32_t digit = (k[j] >> shift) & mask;
-            const uint32_t at = s.start[digit] + s.cnt[w][digit] + rank[j];
-            s.key[at] = k[j];
-            s.pos[at] = p[j];
+            const uint32_t at = s.base[digit] + s.cnt[w][digit] + rank[j];
+            *cluster.map_shared_rank(to_key + at % SORT_TILE, at / SORT_TILE) = k[j];
+            *cluster.map_shared_rank(to_pos + at % SORT_TILE, at / SORT_TILE) = p[j];
         }
-        __syncthreads();
+        cluster.sync();   // the pairs have arrived; `total` is free again
 #pragma unroll
         for (int j = 0; j < SORT_STEPS; ++j) {
-            if (i0 + j * 32 >= a.n) continue;
-            k[j] = s.key[i0 + j * 32];
-            p[j] = s.pos[i0 + j * 32];
+            k[j] = to_key[slot + j * 32];
+            p[j] = to_pos[slot + j * 32];
         }
     }
 #pragma unroll
@@ -382,20 +407,35 @@ cudaError_t sort_ids(SortArgs a, uint32_t *const (&key)[2], uint32_t *const (&po
         if (r == cudaSuccess)
             r = cudaFuncSetAttribute(k_sort_place<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(k_sort_one<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            r = cudaFuncSetAttribute(k_sort_cluster<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     sizeof(ClusterSortShared));
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(k_sort_cluster<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return r;
     });
     if (e != cudaSuccess) return e;
     const int more = clears ? CLEAR_CTAS : 0;
-    if (a.n <= SORT_TILE) {
+    const int64_t tiles = (static_cast<int64_t>(a.n) + SORT_TILE - 1) / SORT_TILE;
+    if (tiles <= SORT_CLUSTER) {
+        a.ctas = 1;
+        while (a.ctas < tiles) a.ctas *= 2;   // divides the clearing CTAs
         a.kout = key[1];
         a.pout = pos[1];
         a.clear = reinterpret_cast<uint4 *>(clear);
         a.clear16 = clear16;
-        k_sort_one<Id><<<1 + more, SORT_THREADS, smem, stream>>>(a, passes);
-        return cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(a.ctas + more));
+        cfg.blockDim = dim3(SORT_THREADS);
+        cfg.dynamicSmemBytes = sizeof(ClusterSortShared);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(a.ctas);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, k_sort_cluster<Id>, a, passes);
     }
-    const int64_t tiles = (static_cast<int64_t>(a.n) + SORT_TILE - 1) / SORT_TILE;
     a.rounds = static_cast<int>((tiles + SORT_CTAS - 1) / SORT_CTAS);
     a.ctas = static_cast<int>((tiles + a.rounds - 1) / a.rounds);
     const int64_t share = (clear16 + 2 * passes - 1) / (2 * passes);
@@ -425,14 +465,17 @@ cudaError_t sort_ids(SortArgs a, uint32_t *const (&key)[2], uint32_t *const (&po
 }
 
 // ---------------------------------------------------------------- the gradient
-// A warp sums one slab of a chunk of 32 consecutive sorted pairs, eight rows of
-// loads in flight.  It writes the segments (the pairs of one id) that begin in
-// its chunk, going on into the next chunk for one that crosses the edge.  Only a
-// long segment, one that fills at least one whole chunk, is cut at the chunks'
-// edges: each chunk leaves its part of the sum in fp32 (slot 0: the segment came
-// in from the left, slot 1: it begins here), and k_embed_join adds the parts in
-// order.  With ids as frequent as words, only some hundred ids are that long.
-constexpr int CHUNK = 32;
+// A warp sums one slab of a chunk of consecutive sorted pairs.  It writes the
+// segments (the pairs of one id) that begin in its chunk, going on into the next
+// chunk for one that crosses the edge.  Only a long segment, one that fills at
+// least one whole chunk, is cut at the chunks' edges: each chunk leaves its part
+// of the sum in fp32 (slot 0: the segment came in from the left, slot 1: it
+// begins here), and k_embed_join adds the parts in order.  With ids as frequent
+// as words, only some hundred ids are that long.  Chunks have 32 pairs, or (where
+// those are more than the SMs hold warps for) up to MAX_CHUNK, which leaves fewer
+// parts: at 262144 pairs of 1024 columns joining took 46 us at 32.
+constexpr int MIN_CHUNK = 32, MAX_CHUNK = 64;
+constexpr int64_t FEW_WARPS = 10000;
 
 template <typename T, int VEC>
 __device__ __forceinline__ void write_row(T *p, float (&acc)[VEC], float scale, bool accumulate) {
@@ -468,7 +511,7 @@ template <typename T, int VEC>
 __global__ void __launch_bounds__(EMBED_THREADS)
     k_embed_grad(const uint32_t *__restrict__ key, const uint32_t *__restrict__ pos,
                  const T *__restrict__ g, T *__restrict__ gW, float *__restrict__ part,
-                 uint32_t *__restrict__ spanning, uint32_t n, uint32_t V, int64_t d, int slabs,
+                 uint32_t *__restrict__ spanning, uint32_t n, uint32_t V, int64_t d, int L, int slabs,
                  int64_t items, float scale, bool accumulate) {
     using P = Pack<T, VEC>;
     extern __shared__ __align__(16) unsigned char grad_smem[];
@@ -481,33 +524,52 @@ __global__ void __launch_bounds__(EMBED_THREADS)
     const int64_t c = static_cast<int64_t>(item % slabs) * (32 * VEC) + lane * VEC;
     const bool in = c < d;
     const uint32_t chunk = static_cast<uint32_t>(item / slabs);
-    const uint64_t i0 = static_cast<uint64_t>(chunk) * CHUNK;
-    // this chunk's pairs and the next one's; V marks pairs that take no part
-    uint32_t k_lane = i0 + lane < n ? key[i0 + lane] : V;
-    uint32_t p_lane = i0 + lane < n ? pos[i0 + lane] : 0;
-    const uint32_t k_more = i0 + CHUNK + lane < n ? key[i0 + CHUNK + lane] : V;
-    const uint32_t p_more = i0 + CHUNK + lane < n ? pos[i0 + CHUNK + lane] : 0;
-    const uint32_t k_prev = i0 > 0 ? key[i0 - 1] : 0xffffffffu;       // last and first pair
-    const uint32_t k_prev0 = i0 > 0 ? key[i0 - CHUNK] : 0xffffffffu;  // of the chunk before
-    const uint32_t first = __shfl_sync(FULL_MASK, k_lane, 0), last = __shfl_sync(FULL_MASK, k_lane, 31);
-    const uint32_t more0 = __shfl_sync(FULL_MASK, k_more, 0), more31 = __shfl_sync(FULL_MASK, k_more, 31);
-    const int valid = __popc(__ballot_sync(FULL_MASK, k_lane < V));   // valid pairs come first
-    if (valid == 0) return;
+    const uint64_t i0 = static_cast<uint64_t>(chunk) * L, i1 = i0 + L;
+    auto key_at = [&](uint64_t i) { return i < n ? key[i] : V; };   // V: takes no part
+    const uint32_t first = key_at(i0), last = key_at(i1 - 1);
+    const uint32_t next0 = key_at(i1), next1 = key_at(i1 + L - 1);  // ends of the next chunk
+    const uint32_t prev0 = i0 > 0 ? key[i0 - L] : 0xffffffffu;       // and of the one before
+    const uint32_t prev1 = i0 > 0 ? key[i0 - 1] : 0xffffffffu;
+    if (first >= V) return;
     const bool whole = first == last;
     // the segment that came in from the left: its part is ours only if it is long
-    const bool came_in = first == k_prev;
-    const bool head_long = came_in && (whole || k_prev0 == first);
+    const bool came_in = first == prev1;
+    const bool head_long = came_in && (whole || prev0 == first);
+    const bool skip = came_in && !head_long;
     // the segment that goes on to the right
-    const bool goes_on = last < V && more0 == last;
-    const bool tail_long = goes_on && (whole || more31 == last);
-    int j_first = 0;
-    if (came_in && !head_long) j_first = __popc(__ballot_sync(FULL_MASK, k_lane == first));
-    // pairs of the next chunk that end our last segment
-    const int extra = goes_on && !tail_long ? __popc(__ballot_sync(FULL_MASK, k_more == last)) : 0;
-    const int m = valid + extra;   // extra > 0 only if valid == 32
-    if (j_first >= m) return;
+    const bool goes_on = last < V && next0 == last;
+    const bool tail_long = goes_on && (whole || next1 == last);
+    const int blocks = L / 32 * (goes_on && !tail_long ? 2 : 1);
+    // 32 pairs at a time; taken: those of this warp (consecutive ones), starts:
+    // the first ones of their segments
+    struct Block { uint32_t k, p; unsigned taken, starts; };
+    auto fetch = [&](int b, uint32_t k_before) {
+        Block r{V, 0, 0, 0};
+        if (b >= blocks) return r;
+        const uint64_t i = i0 + b * 32 + lane;
+        r.k = key_at(i);
+        r.p = i < n ? pos[i] : 0;
+        const bool take = r.k < V && (i < i1 ? !(skip && r.k == first) : r.k == last);
+        uint32_t before = __shfl_up_sync(FULL_MASK, r.k, 1);
+        if (lane == 0) before = k_before;
+        r.taken = __ballot_sync(FULL_MASK, take);
+        r.starts = __ballot_sync(FULL_MASK, take && r.k != before);
+        return r;
+    };
+    int b = 0;
+    Block now = fetch(0, V);
+    while (now.taken == 0 && ++b < L / 32) now = fetch(b, V);   // skipped pairs
+    if (now.taken == 0) return;
+    const int j_first = __ffs(now.taken) - 1;
+    now.starts &= ~(1u << j_first);
+    Block next = fetch(b + 1, __shfl_sync(FULL_MASK, now.k, 31));
+    auto rows_of = [&] {   // rows from `now` on, across the edge to `next`
+        const int end = 32 - __clz(now.taken);
+        return end == 32 ? 32 + __popc(next.taken) : end;
+    };
+    int m = rows_of();
     float acc[VEC] = {};
-    uint32_t cur = __shfl_sync(FULL_MASK, k_lane, j_first & 31);
+    uint32_t cur = __shfl_sync(FULL_MASK, now.k, j_first);
     bool in_part = head_long;   // the current segment came in from the left
     auto flush = [&](bool out_part) {
         if (!in_part && !out_part) {
@@ -515,7 +577,7 @@ __global__ void __launch_bounds__(EMBED_THREADS)
         } else {
             float *to = part + (static_cast<int64_t>(chunk) * 2 + (in_part ? 0 : 1)) * d + c;
             if (in) store_f32<float, VEC>(to, acc);
-            if (!in_part && c == 0) spanning[1 + atomicAdd(spanning, 1u)] = chunk;
+            if (!in_part && c == 0) reinterpret_cast<uint2 *>(spanning)[1 + atomicAdd(spanning, 1u)] = make_uint2(chunk, cur);
         }
     };
     // starts the copies of rows j0 .. j0 + 7
@@ -524,8 +586,8 @@ __global__ void __launch_bounds__(EMBED_THREADS)
 #pragma unroll
         for (int a = 0; a < BATCH; ++a) {
             const int j = j0 + a;
-            const uint32_t at0 = __shfl_sync(FULL_MASK, p_lane, j & 31), at1 = __shfl_sync(FULL_MASK, p_more, j & 31);
-            const T *src = g + static_cast<int64_t>(j < CHUNK ? at0 : at1) * d + c;
+            const uint32_t at0 = __shfl_sync(FULL_MASK, now.p, j & 31), at1 = __shfl_sync(FULL_MASK, next.p, j & 31);
+            const T *src = g + static_cast<int64_t>(j < 32 ? at0 : at1) * d + c;
             if (!in || j >= m) continue;
             if (sizeof(P) >= 4) copy_async<sizeof(P)>(ring + j % RING * 32, src);
             else direct[a] = *reinterpret_cast<const P *>(src);
@@ -539,23 +601,29 @@ __global__ void __launch_bounds__(EMBED_THREADS)
         }
     };
     issue(j_first);
-    for (int j0 = j_first; j0 < m; j0 += BATCH) {
+    for (int j0 = j_first; j0 < m;) {
         issue(j0 + BATCH);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         const int j1 = j0 + BATCH < m ? j0 + BATCH : m;
+#pragma unroll 4
         for (int j = j0; j < j1; ++j) {
-            const uint32_t k0 = __shfl_sync(FULL_MASK, k_lane, j & 31);
-            const uint32_t k = j < CHUNK ? k0 : last;
-            if (k != cur) {
+            if ((j < 32 ? now.starts >> j : next.starts >> (j - 32)) & 1u) {
                 flush(false);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-                cur = k;
+                cur = __shfl_sync(FULL_MASK, j < 32 ? now.k : next.k, j & 31);
                 in_part = false;
             }
             const P v = ring[j % RING * 32];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) acc[e] += to_f32(v.v[e]);
+        }
+        j0 += BATCH;
+        if (j0 >= 32 && m > 32) {   // on to the next block; 32 is a multiple of the ring
+            j0 -= 32;
+            now = next;
+            next = fetch(++b + 1, __shfl_sync(FULL_MASK, now.k, 31));
+            m = rows_of();
         }
     }
     flush(tail_long && cur == last);
@@ -563,25 +631,25 @@ __global__ void __launch_bounds__(EMBED_THREADS)
 
 // Joins the parts of the long segments: a CTA per (segment, slab); its warps take every JOIN_WARPS-th chunk and the warps' sums are added
 // in order.
-constexpr int JOIN_WARPS = 8, JOIN_CTAS = 152 * 8;
+constexpr int JOIN_WARPS = 16, JOIN_CTAS = 152 * 4;
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
     k_embed_join(const uint32_t *__restrict__ key, const float *__restrict__ part,
                  const uint32_t *__restrict__ spanning, T *__restrict__ gW, uint32_t n, int64_t d,
-                 int slabs, float scale, bool accumulate) {
+                 int L, int slabs, float scale, bool accumulate) {
     __shared__ float sum[JOIN_WARPS][32][VEC + 1];
     wait_for_prerequisites();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t items = static_cast<int64_t>(spanning[0]) * slabs;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const uint32_t c0 = spanning[1 + item / slabs];
+        const uint2 entry = reinterpret_cast<const uint2 *>(spanning)[1 + item / slabs];
+        const uint32_t c0 = entry.x, k = entry.y;
         const int64_t c = static_cast<int64_t>(item % slabs) * (32 * VEC) + lane * VEC;
-        const uint32_t k = key[static_cast<uint64_t>(c0) * CHUNK + CHUNK - 1];
         // its last chunk: the chunks after c0 that begin with k, counted by all threads
         uint32_t c1 = c0;
         for (int got = JOIN_WARPS * 32; got == JOIN_WARPS * 32; c1 += got) {
-            const uint64_t i = (static_cast<uint64_t>(c1) + 1 + threadIdx.x) * CHUNK;
+            const uint64_t i = (static_cast<uint64_t>(c1) + 1 + threadIdx.x) * L;
             got = __syncthreads_count(i < n && key[i] == k);
         }
         float acc[VEC] = {};
@@ -620,13 +688,13 @@ GradLayout grad_layout(int64_t n, int64_t d) {
         at += (bytes + 255) / 256 * 256;
         return o;
     };
-    const int64_t chunks = (n + CHUNK - 1) / CHUNK;
+    const int64_t chunks = (n + MIN_CHUNK - 1) / MIN_CHUNK;
     for (int i = 0; i < 2; ++i) {
         l.key[i] = take(sizeof(uint32_t) * n);
         l.pos[i] = take(sizeof(uint32_t) * n);
     }
     l.count = take(sizeof(uint32_t) * SORT_CTAS * SORT_DIGITS);
-    l.spanning = take(sizeof(uint32_t) * (1 + chunks));
+    l.spanning = take(2 * sizeof(uint32_t) * (1 + chunks));
     l.part = take(sizeof(float) * chunks * 2 * d);
     l.total = at;
     return l;
@@ -665,17 +733,19 @@ cudaError_t gradient(const void *g, void *gW, const SortArgs &a, float *part, in
     });
     if (e != cudaSuccess) return e;
     const int slabs = static_cast<int>((d + 32 * VEC - 1) / (32 * VEC));
-    const int64_t items = (n + CHUNK - 1) / CHUNK * slabs;
+    int L = MIN_CHUNK;
+    while (L < MAX_CHUNK && (n + L - 1) / L * slabs > FEW_WARPS) L *= 2;
+    const int64_t items = (n + L - 1) / L * slabs;
     const int64_t blocks = (items + EMBED_THREADS / 32 - 1) / (EMBED_THREADS / 32);
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     e = launch_dependent(k_embed_grad<T, VEC>, static_cast<unsigned>(blocks), EMBED_THREADS, smem, stream,
                          a.kin, a.pin, static_cast<const T *>(g), static_cast<T *>(gW), part,
-                         a.spanning, a.n, a.V, d, slabs, items, scale, accumulate);
-    if (e != cudaSuccess || n <= CHUNK) return e;
-    const int64_t most = (n / CHUNK) * slabs;
+                         a.spanning, a.n, a.V, d, L, slabs, items, scale, accumulate);
+    if (e != cudaSuccess || n <= L) return e;
+    const int64_t most = n / L * slabs;
     return launch_dependent(k_embed_join<T, VEC>, static_cast<unsigned>(most < JOIN_CTAS ? most : JOIN_CTAS),
                             JOIN_WARPS * 32, 0, stream, a.kin, part, a.spanning,
-                            static_cast<T *>(gW), a.n, d, slabs, scale, accumulate);
+                            static_cast<T *>(gW), a.n, d, L, slabs, scale, accumulate);
 }
 
 }  // namespace
