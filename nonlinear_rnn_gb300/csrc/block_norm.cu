@@ -12,7 +12,9 @@
 //   t    = gx' + r (a - x^ <a x^>),  a = gu w_pre       = dL/dx, and dL/d(scale y)
 //   gh   = q (b - h^ <b h^>),        b = t scale silu(gate) w_post
 //   ggate = t scale h^ w_post silu'(gate)
-//   gw_pre = sum gu x^,  gscale = sum t y,  gw_post = sum t scale silu(gate) h^
+//   gw_pre = sum gu x^,  gscale = w_post s,  gw_post = scale s,  s = sum t silu(gate) h^
+//
+// scale and w_post only ever act as their product, so the kernels hold that.
 //
 // Neither direction has a product to speak of: both are bound by HBM, 5 row
 // passes forward (x, h, gate in; x', u out) and 8 backward (x', h, gate, gx',
@@ -30,15 +32,14 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int MAX_D = 8192;   // a row in the registers of one CTA
 
-__device__ __forceinline__ float sigmoid(float v) {
-    return __fdividef(1.f, 1.f + ex2_approx(-v * LOG2E));
+// sigmoid of both lanes
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    const float2 t = mul2(v, make_float2(-LOG2E, -LOG2E));
+    const float2 d = add2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-template <int TPR> __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
-    return v;
-}
 
 struct NormArgs {
     const void *x, *h, *gate;            // x: x' in the backward
@@ -46,124 +47,179 @@ struct NormArgs {
     const void *g_x, *g_u;               // backward: null = zeros
     void *out_x, *out_u;                 // forward: x', u
     void *gx, *gh, *g_gate;
-    float *part;                         // backward: [CTAs][3][d] sums of the weights' gradients
+    float *part;                         // backward: [CTAs][2][d] sums s and gw_pre
     int64_t rows;
     int d;
     float eps;
+    int team_shift;                      // rows of up to a warp: log2 of the threads a row
     bool norm_u;                         // u is wanted (forward), w_pre's branch exists (backward)
 };
 
-// E columns of a row per thread, as E / VEC vectors TPR vectors apart
-template <typename T, int VEC, int E>
-__device__ __forceinline__ void load_row(const void *base, int64_t row, int d, int c0, int step,
-                                         float (&f)[E]) {
-    const T *p = static_cast<const T *>(base) + row * d;
-#pragma unroll
-    for (int i = 0; i < E / VEC; ++i) {
-        const int c = c0 + i * step;
-        float v[VEC] = {};
-        if (c < d) load_f32<T, VEC>(p + c, v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f[i * VEC + e] = v[e];
-    }
-}
-template <typename T, int VEC, int E>
-__device__ __forceinline__ void store_row(void *base, int64_t row, int d, int c0, int step,
-                                          const float (&f)[E]) {
-    T *p = static_cast<T *>(base) + row * d;
-#pragma unroll
-    for (int i = 0; i < E / VEC; ++i) {
-        const int c = c0 + i * step;
-        float v[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = f[i * VEC + e];
-        if (c < d) store_f32<T, VEC>(p + c, v);
-    }
-}
-// the threads' E columns of a (d) fp32 vector; null = ones
-template <int VEC, int E>
-__device__ __forceinline__ void load_weight(const float *w, int d, int c0, int step, float (&f)[E]) {
-#pragma unroll
-    for (int i = 0; i < E / VEC; ++i) {
-        const int c = c0 + i * step;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f[i * VEC + e] = w == nullptr ? 1.f : c < d ? __ldg(w + c + e) : 0.f;
-    }
-}
+// How a row lies in registers, for both directions.  TPR threads (a team) hold a
+// row, as PIECES pieces of 16 bytes a thread, TPR pieces apart.  A team takes
+// every teams-th row; the number of teams is a multiple of 8, so all rows of a
+// team begin at the same place within a 16-byte piece even where d is odd: piece 0
+// holds that many columns of the row before (`shift`), and the row's two end pieces
+// are masked, and written by elements.  So a thread's columns are the same in
+// all its rows, and the sums of the weights' gradients stay in its registers.
+// EDGE: d is not a multiple of VEC, so a row has ends.  VEC = 1 (a piece is two
+// elements): tensors that do not share an alignment.  (Odd rows read by elements
+// took 446 us for the backward of 65537 x 515 bf16.)  The arithmetic is on pairs:
+// one issue slot for two fp32 operations, since with bf16 storage the issue rate
+// is nearer than the memory's.
+template <typename T, int VEC_, int PIECES_, bool EDGE_> struct Layout {
+    using Type = T;
+    static constexpr int VEC = VEC_, PIECES = PIECES_;
+    static constexpr bool EDGE = EDGE_;
+    static constexpr int N = VEC * PIECES, PAIRS = N / 2;   // columns of a thread
+};
 
-// ------------------------------------------------------------------- forward
-// TPR threads a row (a power of two up to a warp), or a whole CTA (TPR = 256)
-// for rows of more than 32 E columns.
-constexpr int FWD_THREADS = 256;
+template <typename L> struct Row {
+    using T = typename L::Type;
+    using P = Pack<T, L::VEC>;
+    int c0[L::PIECES];   // first column of each piece (negative in a shifted row's first)
+    bool whole[L::PIECES];
+    int d;
+    int64_t total;       // elements of the array
 
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *smem) {
-    if (TPR <= 32) return lanes_sum<TPR>(v);
-    v = lanes_sum<32>(v);
-    if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
+    __device__ __forceinline__ Row(int t, int tpr, int d_, int shift, int64_t rows) : d(d_), total(rows * d_) {
 #pragma unroll
-    for (int w = 0; w < TPR / 32; ++w) s += smem[w];
-    return s;
-}
-
-template <typename T, int VEC, int E, int TPR>
-__global__ void __launch_bounds__(FWD_THREADS) k_norm_forward(const NormArgs a) {
-    __shared__ float red[2][FWD_THREADS / 32];
-    const int t = threadIdx.x % TPR;
-    const int64_t row = blockIdx.x * static_cast<int64_t>(FWD_THREADS / TPR) + threadIdx.x / TPR;
-    const bool live = row < a.rows;
-    const int64_t at = live ? row : a.rows - 1;   // threads past the end repeat the last row unstored
-    const int c0 = t * VEC, step = TPR * VEC;
-    float x[E], v[E], w[E];
-    load_row<T, VEC>(a.x, at, a.d, c0, step, x);
-    if (a.h != nullptr) {
-        load_row<T, VEC>(a.h, at, a.d, c0, step, v);
-        float gate[E];
-        if (a.gate != nullptr) load_row<T, VEC>(a.gate, at, a.d, c0, step, gate);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(v[e], v[e], ss);
-        const float q = rsqrtf(row_sum<TPR>(ss, red[0]) / a.d + a.eps);
-        load_weight<VEC>(a.w_post, a.d, c0, step, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= q * w[e];
-        if (a.gate != nullptr) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= gate[e] * sigmoid(gate[e]);
+        for (int i = 0; i < L::PIECES; ++i) {
+            c0[i] = (t + i * tpr) * L::VEC - shift;
+            whole[i] = L::EDGE ? c0[i] >= 0 && c0[i] + L::VEC <= d : c0[i] < d;
         }
-        load_weight<VEC>(a.scale, a.d, c0, step, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(w[e], v[e], x[e]);
-        if (live) store_row<T, VEC>(a.out_x, row, a.d, c0, step, x);
     }
-    if (!a.norm_u) return;
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < E / VEC; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            if (c0 + i * step < a.d) ss = fmaf(x[i * VEC + e], x[i * VEC + e], ss);
-    const float r = rsqrtf(row_sum<TPR>(ss, red[1]) / a.d + a.eps);
-    load_weight<VEC>(a.w_pre, a.d, c0, step, w);
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] *= r * w[e];
-    if (live) store_row<T, VEC>(a.out_u, row, a.d, c0, step, x);
-}
+    // raw pieces, so that a load can be in flight long before its use
+    struct Raw { P v[L::PIECES]; };
 
-// ------------------------------------------------------------------ backward
-// Persistent CTAs; blockDim.x <= TPR threads a row, or (TPR = 32) a warp a row
-// and BWD_WARPS rows a CTA.  Each thread keeps its E columns of the
-// weights and of their gradients in registers over all its rows.
-constexpr int BWD_E = 8, BWD_WARPS = 4;
+    __device__ __forceinline__ void fetch(const void *base, int64_t at, Raw &o) const {
+        const T *p = static_cast<const T *>(base) + at;
+#pragma unroll
+        for (int i = 0; i < L::PIECES; ++i) {
+            // an end piece is read whole too (a merge of its elements would wait for
+            // them here), unless it passes the end of the array
+            if (L::EDGE ? c0[i] < d && at + c0[i] + L::VEC <= total : whole[i]) {
+                o.v[i] = *reinterpret_cast<const P *>(p + c0[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < L::VEC; ++e) {
+                    const int c = c0[i] + e;
+                    o.v[i].v[e] = from_f32<T>(0.f);
+                    if (L::EDGE && c >= 0 && c < d) o.v[i].v[e] = p[c];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *base, int64_t at, const float2 (&f)[L::PAIRS]) const {
+        T *p = static_cast<T *>(base) + at;
+#pragma unroll
+        for (int i = 0; i < L::PIECES; ++i) {
+            P o;
+            narrow(f, i, o);
+            if (whole[i]) {
+                *reinterpret_cast<P *>(p + c0[i]) = o;
+            } else if (L::EDGE) {
+#pragma unroll
+                for (int e = 0; e < L::VEC; ++e) {
+                    const int c = c0[i] + e;
+                    if (c >= 0 && c < d) p[c] = o.v[e];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void widen(const Raw &o, float2 (&f)[L::PAIRS]) const {
+        if constexpr (sizeof(T) == 2 && L::VEC > 1) {
+#pragma unroll
+            for (int i = 0; i < L::PAIRS; ++i) {   // a bf16 is the upper half of its fp32
+                const uint32_t w = reinterpret_cast<const uint32_t *>(o.v)[i];
+                f[i] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < L::PAIRS; ++i)
+                f[i] = make_float2(to_f32(o.v[2 * i / L::VEC].v[2 * i % L::VEC]),
+                                   to_f32(o.v[(2 * i + 1) / L::VEC].v[(2 * i + 1) % L::VEC]));
+        }
+        if (!L::EDGE) return;
+#pragma unroll
+        for (int i = 0; i < L::PIECES; ++i) {
+            if (whole[i]) continue;   // an end piece: the neighbouring rows' columns are zeros
+#pragma unroll
+            for (int e = 0; e < L::VEC; ++e) {
+                const int c = c0[i] + e, j = i * L::VEC + e;
+                if (c < 0 || c >= d) (j % 2 == 0 ? f[j / 2].x : f[j / 2].y) = 0.f;
+            }
+        }
+    }
+    static __device__ __forceinline__ void narrow(const float2 (&f)[L::PAIRS], int i, P &o) {
+        if constexpr (sizeof(T) == 2 && L::VEC > 1) {
+#pragma unroll
+            for (int e = 0; e < L::VEC / 2; ++e) {
+                const float2 v = f[i * (L::VEC / 2) + e];
+                reinterpret_cast<__nv_bfloat162 *>(&o)[e] = __floats2bfloat162_rn(v.x, v.y);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < L::VEC; ++e) {
+                const int j = i * L::VEC + e;
+                o.v[e] = from_f32<T>(j % 2 == 0 ? f[j / 2].x : f[j / 2].y);
+            }
+        }
+    }
+    // zero outside the row
+    __device__ __forceinline__ float column(const float *a, const float *b, int j) const {
+        const int c = c0[j / L::VEC] + j % L::VEC;
+        if (c < 0 || c >= d) return 0.f;
+        return (a == nullptr ? 1.f : __ldg(a + c)) * (b == nullptr ? 1.f : __ldg(b + c));
+    }
+};
 
-// sums of N values over a row's threads; buf: [2][N][32], used in turn
+// This thread's columns of scale w_post and of w_pre (null: ones; zeros outside the
+// row) wait in shared memory, in an order that only this thread reads: in
+// registers they would cost what keeps the next row's loads in flight.
+template <typename L, int THREADS> struct Weights {
+    float4 *mine;
+    static constexpr int QUADS = L::N / 4;
+    static constexpr size_t BYTES = sizeof(float) * 2 * L::N * THREADS;
+
+    __device__ __forceinline__ Weights(float4 *smem, const Row<L> &r, const NormArgs &a)
+        : mine(smem + threadIdx.x) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int q = 0; q < QUADS; ++q) {
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f[e] = w == 0 ? r.column(a.w_post, a.scale, 4 * q + e) : r.column(a.w_pre, nullptr, 4 * q + e);
+                mine[(w * QUADS + q) * THREADS] = make_float4(f[0], f[1], f[2], f[3]);
+            }
+    }
+    // volatile: not to be kept in registers across the loop after all
+    __device__ __forceinline__ void load(int w, float2 (&f)[L::PAIRS]) const {
+#pragma unroll
+        for (int q = 0; q < QUADS; ++q)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(f[2 * q].x), "=f"(f[2 * q].y), "=f"(f[2 * q + 1].x), "=f"(f[2 * q + 1].y)
+                         : "r"(smem_u32(mine + (w * QUADS + q) * THREADS)));
+    }
+};
+enum { W_OUT = 0, W_PRE = 1 };
+
+// N sums over a team.  A team of more than a warp is a CTA: buf is [N][32], and
+// the caller alternates between two of them, so one barrier a call is enough.
 template <int TPR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float *buf) {
+__device__ __forceinline__ void team_sums(float (&v)[N], float *buf, int tpr) {
+    if (TPR <= 32) {
+        for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lanes_sum<32>(v[i]);
-    if (TPR == 32) return;
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], o);
+        return;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(FULL_MASK, v[i], o);
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -172,100 +228,211 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float *buf) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float s = 0.f;
-        for (int w = 0; w < warps; ++w) s += buf[i * 32 + w];
+        if (TPR <= 128) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) s += w < warps ? buf[i * 32 + w] : 0.f;
+        } else {
+            for (int w = 0; w < warps; ++w) s += buf[i * 32 + w];
+        }
         v[i] = s;
     }
 }
 
-template <typename T, int VEC, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? BWD_WARPS * 32 : TPR) k_norm_backward(const NormArgs a) {
-    constexpr int E = BWD_E;
-    __shared__ float red[2][4 * 32];   // three sums, then one; two rows in turn
-    extern __shared__ float join[];    // TPR = 32: [3][d]
-    const int tpr = TPR == 32 ? 32 : blockDim.x;
-    const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-    const int c0 = t * VEC, step = tpr * VEC;
-    const float inv_d = 1.f / a.d;
-    float w_post[E], scale[E], w_pre[E];
-    load_weight<VEC>(a.w_post, a.d, c0, step, w_post);
-    load_weight<VEC>(a.scale, a.d, c0, step, scale);
-    load_weight<VEC>(a.w_pre, a.d, c0, step, w_pre);
-    float s_post[E] = {}, s_scale[E] = {}, s_pre[E] = {};
-    int turn = 0;
-    for (int64_t row = blockIdx.x * static_cast<int64_t>(groups) + group; row < a.rows;
-         row += static_cast<int64_t>(gridDim.x) * groups, turn ^= 1) {
-        float x[E] = {}, h[E] = {}, gate[E], gx[E] = {}, gu[E] = {};
-        if (a.norm_u) {
-            load_row<T, VEC>(a.x, row, a.d, c0, step, x);
-            load_row<T, VEC>(a.g_u, row, a.d, c0, step, gu);
-        }
-        if (a.g_x != nullptr) load_row<T, VEC>(a.g_x, row, a.d, c0, step, gx);
-        if (a.h != nullptr) load_row<T, VEC>(a.h, row, a.d, c0, step, h);
-        if (a.gate != nullptr) load_row<T, VEC>(a.gate, row, a.d, c0, step, gate);
-        float m[3] = {};
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            m[0] = fmaf(x[e], x[e], m[0]);
-            m[1] = fmaf(gu[e] * w_pre[e], x[e], m[1]);
-            m[2] = fmaf(h[e], h[e], m[2]);
-        }
-        row_sums<TPR, 3>(m, red[turn]);
-        const float r = rsqrtf(m[0] * inv_d + a.eps), q = rsqrtf(m[2] * inv_d + a.eps);
-        const float mean_ax = m[1] * inv_d * r;   // <a x^>
-        if (a.norm_u) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float xn = x[e] * r;
-                s_pre[e] = fmaf(gu[e], xn, s_pre[e]);
-                gx[e] = fmaf(r, fmaf(-xn, mean_ax, gu[e] * w_pre[e]), gx[e]);   // t
-            }
-        }
-        store_row<T, VEC>(a.gx, row, a.d, c0, step, gx);
-        if (a.h == nullptr) continue;
-        float k[1] = {};
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float hn = h[e] * q;
-            float of = 1.f, slope = 0.f;
-            if (a.gate != nullptr) {
-                const float s = sigmoid(gate[e]);
-                of = gate[e] * s;
-                slope = s * fmaf(gate[e], 1.f - s, 1.f);
-            }
-            const float n = hn * w_post[e], gy = gx[e] * scale[e];
-            s_scale[e] = fmaf(gx[e], n * of, s_scale[e]);
-            s_post[e] = fmaf(gy * of, hn, s_post[e]);
-            gate[e] = gy * n * slope;      // dL/dgate
-            gx[e] = gy * of * w_post[e];   // b
-            h[e] = hn;
-            k[0] = fmaf(gx[e], hn, k[0]);
-        }
-        if (a.gate != nullptr) store_row<T, VEC>(a.g_gate, row, a.d, c0, step, gate);
-        row_sums<TPR, 1>(k, red[turn] + 3 * 32);
-        const float mean_bh = k[0] * inv_d;
-#pragma unroll
-        for (int e = 0; e < E; ++e) gx[e] = q * fmaf(-h[e], mean_bh, gx[e]);
-        store_row<T, VEC>(a.gh, row, a.d, c0, step, gx);
+// TPR = 32: up to a warp a row (a power of two, 1 << shift) and several rows a CTA;
+// else up to TPR threads, a CTA
+template <int TPR> struct Teams {
+    static constexpr int THREADS = TPR <= 32 ? 128 : TPR;
+    int t, tpr, in_cta, per_cta, team, teams;
+    __device__ __forceinline__ Teams(int shift) {
+        tpr = TPR <= 32 ? 1 << shift : blockDim.x;
+        per_cta = TPR <= 32 ? THREADS >> shift : 1;
+        in_cta = TPR <= 32 ? threadIdx.x >> shift : 0;
+        t = TPR <= 32 ? threadIdx.x & (tpr - 1) : threadIdx.x;
+        team = blockIdx.x * per_cta + in_cta;
+        teams = gridDim.x * per_cta;
     }
-    // this CTA's sums: warps of a CTA in order (TPR = 32), then to the workspace
-    float *part = a.part + blockIdx.x * static_cast<int64_t>(3) * a.d;
-    for (int g = 0; g < groups; ++g) {
-        if (TPR == 32) __syncthreads();
-        if (g != group) continue;
-        float *to = TPR == 32 && g < groups - 1 ? join : part;
+};
+
+// resident threads an SM that the kernels' registers leave room for
+constexpr int FWD_THREADS_PER_SM = 640, BWD_THREADS_PER_SM = 512;
+constexpr int resident(int threads, int per_sm) { return per_sm / threads > 0 ? per_sm / threads : 1; }
+
+// ------------------------------------------------------------------- forward
+template <typename L, int TPR>
+__global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THREADS, FWD_THREADS_PER_SM))
+    k_norm_forward(const NormArgs a) {
+    extern __shared__ float4 norm_smem[];
+    __shared__ float red[2][2 * 32];
+    const Teams<TPR> g(a.team_shift);
+    const Row<L> r(g.t, g.tpr, a.d, static_cast<int>(static_cast<int64_t>(g.team) * a.d % L::VEC), a.rows);
+    const float inv_d = 1.f / a.d;
+    const Weights<L, Teams<TPR>::THREADS> weights(norm_smem, r, a);
+    typename Row<L>::Raw rx, rh, rg;
+    auto fetch_row = [&](int64_t row) {
+        if (row >= a.rows) return;
+        const int64_t at = row * a.d;
+        r.fetch(a.x, at, rx);
+        if (a.h != nullptr) r.fetch(a.h, at, rh);
+        if (a.gate != nullptr) r.fetch(a.gate, at, rg);
+    };
+    // teams that share a warp run the same number of rounds
+    const int64_t rounds = (a.rows + g.teams - 1) / g.teams;
+    int64_t row = g.team;
+    fetch_row(row);
+    for (int64_t i = 0; i < rounds; ++i, row += g.teams) {
+        float2 x[L::PAIRS], w[L::PAIRS];
+        r.widen(rx, x);
+        const int64_t at = row * a.d;
+        if (a.h != nullptr) {
+            float2 v[L::PAIRS], ss = both(0.f);
+            r.widen(rh, v);
 #pragma unroll
-        for (int i = 0; i < E / VEC; ++i)
+            for (int e = 0; e < L::PAIRS; ++e) ss = fma2(v[e], v[e], ss);
+            if (a.gate != nullptr) {
+                float2 gate[L::PAIRS];
+                r.widen(rg, gate);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int c = c0 + i * step + e, o = i * VEC + e;
-                if (c >= a.d) continue;
-                float v[3] = {s_post[o], s_scale[o], s_pre[o]};
-#pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    if (TPR == 32 && g > 0) v[q] += join[q * a.d + c];
-                    to[q * a.d + c] = v[q];
-                }
+                for (int e = 0; e < L::PAIRS; ++e)
+                    v[e] = mul2(v[e], mul2(gate[e], sigmoid2(gate[e])));
             }
+            fetch_row(row + g.teams);   // in flight over this row's sums
+            float sum[1] = {ss.x + ss.y};
+            team_sums<TPR, 1>(sum, red[i & 1], g.tpr);
+            const float2 q = both(rsqrtf(sum[0] * inv_d + a.eps));
+            weights.load(W_OUT, w);
+#pragma unroll
+            for (int e = 0; e < L::PAIRS; ++e) x[e] = fma2(mul2(v[e], q), w[e], x[e]);
+            if (row < a.rows) r.store(a.out_x, at, x);
+        } else {
+            fetch_row(row + g.teams);
+        }
+        if (!a.norm_u) continue;
+        float2 ss = both(0.f);
+#pragma unroll
+        for (int e = 0; e < L::PAIRS; ++e) ss = fma2(x[e], x[e], ss);
+        float sum[1] = {ss.x + ss.y};
+        team_sums<TPR, 1>(sum, red[i & 1] + 32, g.tpr);
+        const float2 s = both(rsqrtf(sum[0] * inv_d + a.eps));
+        weights.load(W_PRE, w);
+#pragma unroll
+        for (int e = 0; e < L::PAIRS; ++e) x[e] = mul2(mul2(x[e], s), w[e]);
+        if (row < a.rows) r.store(a.out_u, at, x);
+    }
+}
+
+// ------------------------------------------------------------------ backward
+template <typename L, int TPR>
+__global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THREADS, BWD_THREADS_PER_SM))
+    k_norm_backward(const NormArgs a) {
+    __shared__ float red[2][4 * 32];   // three sums, then one; two rows in turn
+    extern __shared__ float4 norm_smem[];
+    const Teams<TPR> g(a.team_shift);
+    const Row<L> r(g.t, g.tpr, a.d, static_cast<int>(static_cast<int64_t>(g.team) * a.d % L::VEC), a.rows);
+    const float inv_d = 1.f / a.d;
+    const Weights<L, Teams<TPR>::THREADS> weights(norm_smem, r, a);
+    float2 s_out[L::PAIRS] = {}, s_pre[L::PAIRS] = {};
+    typename Row<L>::Raw rx, rh, rg, rgx, rgu;
+    auto fetch_row = [&](int64_t row) {
+        if (row >= a.rows) return;
+        const int64_t at = row * a.d;
+        if (a.norm_u) {
+            r.fetch(a.x, at, rx);
+            r.fetch(a.g_u, at, rgu);
+        }
+        if (a.g_x != nullptr) r.fetch(a.g_x, at, rgx);
+        if (a.h != nullptr) r.fetch(a.h, at, rh);
+        if (a.gate != nullptr) r.fetch(a.gate, at, rg);
+    };
+    const int64_t rounds = (a.rows + g.teams - 1) / g.teams;
+    int64_t row = g.team;
+    fetch_row(row);
+    for (int64_t i = 0; i < rounds; ++i, row += g.teams) {
+        const bool live = row < a.rows;   // a team past the end adds nothing
+        float2 x[L::PAIRS] = {}, h[L::PAIRS] = {}, gate[L::PAIRS] = {}, gx[L::PAIRS] = {}, gu[L::PAIRS] = {};
+        if (live) {
+            if (a.norm_u) {
+                r.widen(rx, x);
+                r.widen(rgu, gu);
+            }
+            if (a.g_x != nullptr) r.widen(rgx, gx);
+            if (a.h != nullptr) r.widen(rh, h);
+            if (a.gate != nullptr) r.widen(rg, gate);
+        }
+        fetch_row(row + g.teams);
+        const int64_t at = row * a.d;
+        float2 m0 = both(0.f), m1 = m0, m2 = m0, w[L::PAIRS];
+        weights.load(W_PRE, w);
+#pragma unroll
+        for (int e = 0; e < L::PAIRS; ++e) {
+            m0 = fma2(x[e], x[e], m0);
+            w[e] = mul2(gu[e], w[e]);   // a
+            m1 = fma2(w[e], x[e], m1);
+            m2 = fma2(h[e], h[e], m2);
+        }
+        float m[3] = {m0.x + m0.y, m1.x + m1.y, m2.x + m2.y};
+        team_sums<TPR, 3>(m, red[i & 1], g.tpr);
+        if (a.norm_u && live) {
+            const float s = rsqrtf(m[0] * inv_d + a.eps);
+            const float2 s2 = both(s), mean_ax = both(-m[1] * inv_d * s);   // -<a x^>
+#pragma unroll
+            for (int e = 0; e < L::PAIRS; ++e) {
+                const float2 xn = mul2(x[e], s2);
+                s_pre[e] = fma2(gu[e], xn, s_pre[e]);
+                gx[e] = fma2(s2, fma2(xn, mean_ax, w[e]), gx[e]);   // t
+            }
+        }
+        if (live) r.store(a.gx, at, gx);
+        if (a.h == nullptr) continue;
+        const float q = rsqrtf(m[2] * inv_d + a.eps);
+        float2 k2 = both(0.f);
+        if (live) {
+            weights.load(W_OUT, w);
+#pragma unroll
+            for (int e = 0; e < L::PAIRS; ++e) {
+                h[e] = mul2(h[e], both(q));                     // h^
+                const float2 c = mul2(gx[e], w[e]);             // t scale w_post
+                if (a.gate != nullptr) {
+                    const float2 sg = sigmoid2(gate[e]);
+                    const float2 of = mul2(gate[e], sg);        // silu
+                    // silu' = sg (1 + gate (1 - sg)) = sg + of - of sg
+                    const float2 slope = fma2(of, make_float2(-sg.x, -sg.y), add2(sg, of));
+                    gate[e] = mul2(mul2(c, h[e]), slope);
+                    s_out[e] = fma2(mul2(gx[e], of), h[e], s_out[e]);
+                    gx[e] = mul2(c, of);                        // b
+                } else {
+                    s_out[e] = fma2(gx[e], h[e], s_out[e]);
+                    gx[e] = c;
+                }
+                k2 = fma2(gx[e], h[e], k2);
+            }
+            if (a.gate != nullptr) r.store(a.g_gate, at, gate);
+        }
+        float k[1] = {k2.x + k2.y};
+        team_sums<TPR, 1>(k, red[i & 1] + 3 * 32, g.tpr);
+        const float2 mean_bh = both(-k[0] * inv_d), q2 = both(q);
+#pragma unroll
+        for (int e = 0; e < L::PAIRS; ++e) gx[e] = mul2(q2, fma2(h[e], mean_bh, gx[e]));
+        if (live) r.store(a.gh, at, gx);
+    }
+    // this CTA's sums: its teams in order, then to the workspace
+    float *part = a.part + blockIdx.x * static_cast<int64_t>(2) * a.d;
+    float *join = reinterpret_cast<float *>(norm_smem);   // [2][d], where the weights were
+    for (int o = 0; o < g.per_cta; ++o) {
+        if (TPR <= 32) __syncthreads();
+        if (g.in_cta != o) continue;
+        float *to = o < g.per_cta - 1 ? join : part;
+#pragma unroll
+        for (int j = 0; j < L::N; ++j) {
+            const int c = r.c0[j / L::VEC] + j % L::VEC;
+            if (c < 0 || c >= a.d) continue;
+            float v[2] = {j % 2 == 0 ? s_out[j / 2].x : s_out[j / 2].y,
+                          j % 2 == 0 ? s_pre[j / 2].x : s_pre[j / 2].y};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (TPR <= 32 && o > 0) v[q] += join[q * a.d + c];
+                to[q * a.d + c] = v[q];
+            }
+        }
     }
 }
 
@@ -274,65 +441,101 @@ __global__ void __launch_bounds__(TPR == 32 ? BWD_WARPS * 32 : TPR) k_norm_backw
 constexpr int JOIN_WARPS = 16;
 
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
-    k_norm_join(const float *__restrict__ part, int n_part, int d, float *gw_post, float *g_scale,
-                float *gw_pre) {
+    k_norm_join(const float *__restrict__ part, int n_part, int d, const float *w_post,
+                const float *scale, float *gw_post, float *g_scale, float *gw_pre) {
     __shared__ float sum[JOIN_WARPS][32];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x * 32 + lane;   // column of [3][d]
+    const int c = blockIdx.x * 32 + lane;   // column of [2][d]
     float s = 0.f;
-    if (c < 3 * d) {
-#pragma unroll 4
-        for (int p = w; p < n_part; p += JOIN_WARPS) s += part[static_cast<int64_t>(p) * 3 * d + c];
+    if (c < 2 * d) {
+#pragma unroll 8
+        for (int p = w; p < n_part; p += JOIN_WARPS) s += part[static_cast<int64_t>(p) * 2 * d + c];
     }
     sum[w][lane] = s;
     __syncthreads();
-    if (w > 0 || c >= 3 * d) return;
+    if (w > 0 || c >= 2 * d) return;
 #pragma unroll
     for (int q = 1; q < JOIN_WARPS; ++q) s += sum[q][lane];
-    float *to = c < d ? gw_post : c < 2 * d ? g_scale : gw_pre;
-    if (to != nullptr) to[c % d] = s;
+    if (c < d) {
+        if (gw_post != nullptr) gw_post[c] = scale == nullptr ? s : s * scale[c];
+        if (g_scale != nullptr) g_scale[c] = w_post == nullptr ? s : s * w_post[c];
+    } else if (gw_pre != nullptr) {
+        gw_pre[c - d] = s;
+    }
 }
 
 // ---------------------------------------------------------------- host side
 bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-template <typename T, int VEC, int E, int TPR>
-cudaError_t forward_as(const NormArgs &a, cudaStream_t s) {
-    const int64_t blocks = (a.rows + FWD_THREADS / TPR - 1) / (FWD_THREADS / TPR);
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    k_norm_forward<T, VEC, E, TPR><<<static_cast<unsigned>(blocks), FWD_THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+// Threads a row: the fewest that hold it in n columns each, a power of two up to
+// a warp, whole warps beyond.
+int team_size(int d, int vec, int n) {
+    const int columns = d % vec == 0 ? d : d + vec - 1;   // a shifted row takes more
+    const int need = (columns + n - 1) / n;
+    if (need > 32) return (need + 31) / 32 * 32;
+    int t = 1;
+    while (t < need) t *= 2;
+    return t;
 }
-
-// the fewest threads a row that hold it in at most 32 columns each
-template <typename T, int VEC> cudaError_t forward_for(const NormArgs &a, cudaStream_t s) {
-    constexpr int E = 32;
-    if (a.d <= 8 * 8) return forward_as<T, VEC, 8, 8>(a, s);
-    if (a.d <= 8 * E) return forward_as<T, VEC, E, 8>(a, s);
-    if (a.d <= 16 * E) return forward_as<T, VEC, E, 16>(a, s);
-    if (a.d <= 32 * E) return forward_as<T, VEC, E, 32>(a, s);
-    return forward_as<T, VEC, E, 256>(a, s);
-}
-
-// 608 = 152 SMs x 4: the CTAs of a backward launch for long inputs
-constexpr int BWD_CTAS = 608;
-
-int backward_ctas(int64_t rows, int d) {
-    const int64_t per = d <= 32 * BWD_E ? BWD_WARPS : 1;
+// CTAs: enough teams for every row once, at most the resident ones; a multiple of
+// 8 teams
+int cta_count(int64_t rows, int tpr, int threads_per_sm) {
+    const int64_t per = tpr <= 32 ? 128 / tpr : 1;
+    const int threads = tpr <= 32 ? 128 : tpr;
+    int64_t most = 152 * resident(threads, threads_per_sm);
     const int64_t want = (rows + per - 1) / per;
-    return static_cast<int>(want < BWD_CTAS ? want : BWD_CTAS);
+    most = want < most ? want : most;
+    return static_cast<int>(per >= 8 ? most : (most * per + 7) / 8 * 8 / per);
 }
 
-template <typename T, int VEC> cudaError_t backward_for(const NormArgs &a, int ctas, cudaStream_t s) {
-    if (a.d <= 32 * BWD_E) {
-        k_norm_backward<T, VEC, 32><<<ctas, BWD_WARPS * 32, sizeof(float) * 3 * a.d, s>>>(a);
-    } else {
-        const int threads = ((a.d + BWD_E - 1) / BWD_E + 31) / 32 * 32;
-        if (threads <= 128) k_norm_backward<T, VEC, 128><<<ctas, threads, 0, s>>>(a);
-        else k_norm_backward<T, VEC, 1024><<<ctas, threads, 0, s>>>(a);
+template <typename L, int TPR, typename K>
+cudaError_t launch_norm(K kernel, NormArgs a, int ctas, int tpr, cudaStream_t s) {
+    constexpr size_t smem = Weights<L, Teams<TPR>::THREADS>::BYTES;
+    if (smem > 40 * 1024) {   // 48 KB with the static part need no attribute
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
     }
+    while (TPR <= 32 && (1 << a.team_shift) < tpr) ++a.team_shift;
+    kernel<<<ctas, TPR <= 32 ? Teams<TPR>::THREADS : tpr, smem, s>>>(a);
     return cudaGetLastError();
 }
+
+// 16 columns a thread forward (two pieces of bf16, four of fp32 would be too many
+// registers: two), 8 backward
+template <typename T, int VEC> constexpr int fwd_pieces() { return VEC == 1 ? 8 : 2; }
+template <typename T, int VEC> constexpr int bwd_pieces() { return 8 / VEC; }
+
+template <typename T, int VEC, bool EDGE> cudaError_t forward_for(const NormArgs &a, cudaStream_t s) {
+    using L = Layout<T, VEC, fwd_pieces<T, VEC>(), EDGE>;
+    const int tpr = team_size(a.d, VEC, L::N), ctas = cta_count(a.rows, tpr, FWD_THREADS_PER_SM);
+    if (tpr <= 32) return launch_norm<L, 32>(k_norm_forward<L, 32>, a, ctas, tpr, s);
+    if (tpr <= 128) return launch_norm<L, 128>(k_norm_forward<L, 128>, a, ctas, tpr, s);
+    if (tpr <= 512) return launch_norm<L, 512>(k_norm_forward<L, 512>, a, ctas, tpr, s);
+    return launch_norm<L, 1024>(k_norm_forward<L, 1024>, a, ctas, tpr, s);
+}
+
+template <typename T, int VEC, bool EDGE>
+cudaError_t backward_for(const NormArgs &a, int ctas, cudaStream_t s) {
+    using L = Layout<T, VEC, bwd_pieces<T, VEC>(), EDGE>;
+    const int tpr = team_size(a.d, VEC, L::N);
+    if (tpr <= 32) return launch_norm<L, 32>(k_norm_backward<L, 32>, a, ctas, tpr, s);
+    if (tpr <= 128) return launch_norm<L, 128>(k_norm_backward<L, 128>, a, ctas, tpr, s);
+    if (tpr <= 512) return launch_norm<L, 512>(k_norm_backward<L, 512>, a, ctas, tpr, s);
+    return launch_norm<L, 1024>(k_norm_backward<L, 1024>, a, ctas, tpr, s);
+}
+
+// calls f<T, VEC, EDGE>(args...) for the storage type, the access width and d
+#define NRNN_BY_ROW(dtype, vec, d, f, ...)                                            \
+    ((dtype) == NRNN_BF16 ? ((vec) == 1          ? f<__nv_bfloat16, 1, false>(__VA_ARGS__) \
+                             : (d) % (vec) == 0  ? f<__nv_bfloat16, 8, false>(__VA_ARGS__) \
+                                                 : f<__nv_bfloat16, 8, true>(__VA_ARGS__)) \
+                          : ((vec) == 1          ? f<float, 1, false>(__VA_ARGS__)         \
+                             : (d) % (vec) == 0  ? f<float, 4, false>(__VA_ARGS__)         \
+                                                 : f<float, 4, true>(__VA_ARGS__)))
+
+// CTAs of a backward launch: the most that any access width takes
+int backward_ctas(int64_t rows, int d, int vec) { return cta_count(rows, team_size(d, vec, 8), BWD_THREADS_PER_SM); }
 
 int check_norm(int dtype, int64_t rows, int64_t d, float eps) {
     if (dtype != NRNN_F32 && dtype != NRNN_BF16) return NRNN_ERR_INVALID_ARG;
@@ -341,10 +544,11 @@ int check_norm(int dtype, int64_t rows, int64_t d, float eps) {
     return NRNN_OK;
 }
 
-// widest access of 16 bytes, or one element
+// 16-byte pieces where every tensor begins on a 16-byte boundary, else one element
+// (a row of 8192 odd columns would take more than a CTA's threads with pieces)
 int width_for(int elem, int64_t d, std::initializer_list<const void *> ptrs) {
     const int vec = 16 / elem;
-    if (d % vec != 0) return 1;
+    if (team_size(static_cast<int>(d), vec, 8) > 1024) return 1;
     for (const void *p : ptrs)
         if (!aligned_to(p, 16)) return 1;
     return vec;
@@ -375,18 +579,20 @@ int nrnn_block_norm_forward(const void *x, const void *h, const void *gate, cons
     a.rows = rows; a.d = static_cast<int>(d); a.eps = eps;
     a.norm_u = u != nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool wide = width_for(elem, d, {x, h, gate, x_out, u}) > 1;
-    cudaError_t e;
-    if (dtype == NRNN_BF16)
-        e = wide ? forward_for<__nv_bfloat16, 8>(a, s) : forward_for<__nv_bfloat16, 1>(a, s);
-    else
-        e = wide ? forward_for<float, 4>(a, s) : forward_for<float, 1>(a, s);
+    const int vec = width_for(elem, d, {x, h, gate, x_out, u});
+    const cudaError_t e = NRNN_BY_ROW(dtype, vec, d, forward_for, a, s);
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 size_t nrnn_block_norm_backward_workspace_bytes(int64_t rows, int64_t d) {
     if (rows < 0 || d <= 0 || d > MAX_D) return 0;
-    const size_t bytes = sizeof(float) * 3 * d * (rows > 0 ? backward_ctas(rows, static_cast<int>(d)) : 1);
+    int ctas = 1;
+    if (rows > 0)
+        for (int vec : {1, 4, 8}) {
+            const int n = backward_ctas(rows, static_cast<int>(d), vec);
+            ctas = n > ctas ? n : ctas;
+        }
+    const size_t bytes = sizeof(float) * 2 * d * ctas;
     return (bytes + 255) / 256 * 256;
 }
 
@@ -421,18 +627,16 @@ int nrnn_block_norm_backward(const void *x_out, const void *h, const void *gate,
     a.part = static_cast<float *>(workspace);
     a.rows = rows; a.d = static_cast<int>(d); a.eps = eps;
     a.norm_u = g_u != nullptr;
-    const int ctas = rows > 0 ? backward_ctas(rows, a.d) : 0;
+    int ctas = 0;
     cudaError_t e = cudaSuccess;
     if (rows > 0) {
-        const bool wide = width_for(elem, d, {x_out, h, gate, g_x, g_u, gx, gh, g_gate}) > 1;
-        if (dtype == NRNN_BF16)
-            e = wide ? backward_for<__nv_bfloat16, 8>(a, ctas, s) : backward_for<__nv_bfloat16, 1>(a, ctas, s);
-        else
-            e = wide ? backward_for<float, 4>(a, ctas, s) : backward_for<float, 1>(a, ctas, s);
+        const int vec = width_for(elem, d, {x_out, h, gate, g_x, g_u, gx, gh, g_gate});
+        ctas = backward_ctas(rows, a.d, vec);
+        e = NRNN_BY_ROW(dtype, vec, d, backward_for, a, ctas, s);
     }
     if (e == cudaSuccess) {
-        k_norm_join<<<(3 * a.d + 31) / 32, JOIN_WARPS * 32, 0, s>>>(a.part, ctas, a.d, gw_post, g_scale,
-                                                                   gw_pre);
+        k_norm_join<<<(2 * a.d + 31) / 32, JOIN_WARPS * 32, 0, s>>>(a.part, ctas, a.d, w_post, scale,
+                                                                   gw_post, g_scale, gw_pre);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
