@@ -74,11 +74,18 @@ template <typename T, int VEC_, int PIECES_, bool EDGE_> struct Layout {
     static constexpr int N = VEC * PIECES, PAIRS = N / 2;   // columns of a thread
 };
 
+// bytes < 16: the rest is zeros
+__device__ __forceinline__ void copy_async_16(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
 template <typename L> struct Row {
     using T = typename L::Type;
     using P = Pack<T, L::VEC>;
     int c0[L::PIECES];   // first column of each piece (negative in a shifted row's first)
     bool whole[L::PIECES];
+    uint32_t mask[L::EDGE ? L::PIECES * 4 : 1];   // bits of the pieces' words inside the row
     int d;
     int64_t total;       // elements of the array
 
@@ -87,26 +94,37 @@ template <typename L> struct Row {
         for (int i = 0; i < L::PIECES; ++i) {
             c0[i] = (t + i * tpr) * L::VEC - shift;
             whole[i] = L::EDGE ? c0[i] >= 0 && c0[i] + L::VEC <= d : c0[i] < d;
+            if (L::EDGE) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    constexpr int PER = 4 / sizeof(T);
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                        const int c = c0[i] + w * PER + e;
+                        if (c >= 0 && c < d) m |= PER == 1 ? 0xffffffffu : 0xffffu << (16 * e);
+                    }
+                    mask[(i * 4 + w) % (L::EDGE ? L::PIECES * 4 : 1)] = m;
+                }
+            }
         }
     }
-    // raw pieces, so that a load can be in flight long before its use
-    struct Raw { P v[L::PIECES]; };
-
-    __device__ __forceinline__ void fetch(const void *base, int64_t at, Raw &o) const {
+    // starts the copy of this thread's pieces to shared memory, THREADS pieces apart
+    template <int THREADS>
+    __device__ __forceinline__ void fetch(const void *base, int64_t at, P *to) const {
         const T *p = static_cast<const T *>(base) + at;
 #pragma unroll
         for (int i = 0; i < L::PIECES; ++i) {
-            // an end piece is read whole too (a merge of its elements would wait for
-            // them here), unless it passes the end of the array
-            if (L::EDGE ? c0[i] < d && at + c0[i] + L::VEC <= total : whole[i]) {
-                o.v[i] = *reinterpret_cast<const P *>(p + c0[i]);
+            P *dst = to + i * THREADS;
+            if (c0[i] >= d) continue;
+            if (L::EDGE) {
+                // an end piece is copied whole too, but for what lies past the array
+                const int64_t left = (total - at - c0[i]) * static_cast<int64_t>(sizeof(T));
+                copy_async_16(dst, p + c0[i], left < 16 ? static_cast<int>(left) : 16);
+            } else if (sizeof(P) == 16) {
+                copy_async_16(dst, p + c0[i], 16);
             } else {
-#pragma unroll
-                for (int e = 0; e < L::VEC; ++e) {
-                    const int c = c0[i] + e;
-                    o.v[i].v[e] = from_f32<T>(0.f);
-                    if (L::EDGE && c >= 0 && c < d) o.v[i].v[e] = p[c];
-                }
+                *dst = *reinterpret_cast<const P *>(p + c0[i]);
             }
         }
     }
@@ -118,36 +136,44 @@ template <typename L> struct Row {
             narrow(f, i, o);
             if (whole[i]) {
                 *reinterpret_cast<P *>(p + c0[i]) = o;
-            } else if (L::EDGE) {
+            } else if (L::EDGE) {   // by words, and the one that holds the row's end by elements
 #pragma unroll
-                for (int e = 0; e < L::VEC; ++e) {
-                    const int c = c0[i] + e;
-                    if (c >= 0 && c < d) p[c] = o.v[e];
+                for (int w = 0; w < 4; ++w) {
+                    constexpr int PER = 4 / sizeof(T);
+                    const uint32_t m = mask[(i * 4 + w) % (L::EDGE ? L::PIECES * 4 : 1)];
+                    T *to = p + c0[i] + w * PER;
+                    if (m == 0xffffffffu) *reinterpret_cast<uint32_t *>(to) = reinterpret_cast<const uint32_t *>(&o)[w];
+                    else if (PER == 2 && m == 0xffffu) to[0] = o.v[(w * PER) % L::VEC];
+                    else if (PER == 2 && m == 0xffff0000u) to[1] = o.v[(w * PER + 1) % L::VEC];
                 }
             }
         }
     }
-    __device__ __forceinline__ void widen(const Raw &o, float2 (&f)[L::PAIRS]) const {
-        if constexpr (sizeof(T) == 2 && L::VEC > 1) {
-#pragma unroll
-            for (int i = 0; i < L::PAIRS; ++i) {   // a bf16 is the upper half of its fp32
-                const uint32_t w = reinterpret_cast<const uint32_t *>(o.v)[i];
-                f[i] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < L::PAIRS; ++i)
-                f[i] = make_float2(to_f32(o.v[2 * i / L::VEC].v[2 * i % L::VEC]),
-                                   to_f32(o.v[(2 * i + 1) / L::VEC].v[(2 * i + 1) % L::VEC]));
-        }
-        if (!L::EDGE) return;
+    // the pieces as fp32, zeros outside the row
+    template <int THREADS>
+    __device__ __forceinline__ void widen(const P *from, float2 (&f)[L::PAIRS]) const {
 #pragma unroll
         for (int i = 0; i < L::PIECES; ++i) {
-            if (whole[i]) continue;   // an end piece: the neighbouring rows' columns are zeros
+            P v{};
+            if (L::EDGE || whole[i]) v = from[i * THREADS];
+            if (L::EDGE) {   // not the neighbouring rows' columns
 #pragma unroll
-            for (int e = 0; e < L::VEC; ++e) {
-                const int c = c0[i] + e, j = i * L::VEC + e;
-                if (c < 0 || c >= d) (j % 2 == 0 ? f[j / 2].x : f[j / 2].y) = 0.f;
+                for (int w = 0; w < 4; ++w)
+                    reinterpret_cast<uint32_t *>(&v)[w % (sizeof(P) / 4 > 0 ? sizeof(P) / 4 : 1)] &=
+                        mask[(i * 4 + w) % (L::EDGE ? L::PIECES * 4 : 1)];
+            }
+            if constexpr (sizeof(T) == 2 && L::VEC > 1) {
+#pragma unroll
+                for (int e = 0; e < L::VEC / 2; ++e) {   // a bf16 is the upper half of its fp32
+                    const uint32_t w = reinterpret_cast<const uint32_t *>(&v)[e];
+                    f[i * (L::VEC / 2) + e] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < L::VEC; ++e) {
+                    const int j = i * L::VEC + e;
+                    (j % 2 == 0 ? f[j / 2].x : f[j / 2].y) = to_f32(v.v[e]);
+                }
             }
         }
     }
@@ -171,6 +197,21 @@ template <typename L> struct Row {
         const int c = c0[j / L::VEC] + j % L::VEC;
         if (c < 0 || c >= d) return 0.f;
         return (a == nullptr ? 1.f : __ldg(a + c)) * (b == nullptr ? 1.f : __ldg(b + c));
+    }
+};
+
+// TPR = 32: up to a warp a row (a power of two, 1 << shift) and several rows a CTA;
+// else up to TPR threads, a CTA
+template <int TPR> struct Teams {
+    static constexpr int THREADS = TPR <= 32 ? 128 : TPR;
+    int t, tpr, in_cta, per_cta, team, teams;
+    __device__ __forceinline__ Teams(int shift) {
+        tpr = TPR <= 32 ? 1 << shift : blockDim.x;
+        per_cta = TPR <= 32 ? THREADS >> shift : 1;
+        in_cta = TPR <= 32 ? threadIdx.x >> shift : 0;
+        t = TPR <= 32 ? threadIdx.x & (tpr - 1) : threadIdx.x;
+        team = blockIdx.x * per_cta + in_cta;
+        teams = gridDim.x * per_cta;
     }
 };
 
@@ -206,6 +247,30 @@ template <typename L, int THREADS> struct Weights {
 };
 enum { W_OUT = 0, W_PRE = 1 };
 
+// Rows on their way: each thread copies its own pieces to its own places in shared
+// memory (cp.async) and reads them back itself, so the next row's loads are in
+// flight over this row's sums without registers or barriers.  (Loads to registers
+// a row ahead were waited for at once: 327 us for the backward of 65536 x 1024
+// bf16, and 237 us without looking ahead.)
+template <typename L, int THREADS, int TENSORS, int DEPTH> struct Stage {
+    using P = typename Row<L>::P;
+    P *mine;
+    static constexpr size_t BYTES = sizeof(P) * L::PIECES * TENSORS * DEPTH * THREADS;
+    __device__ __forceinline__ explicit Stage(void *smem) : mine(static_cast<P *>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ P *at(int turn, int tensor) const {
+        return mine + (turn * TENSORS + tensor) * (L::PIECES * THREADS);
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait_row() {   // the oldest row has arrived
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    }
+};
+// rows in flight: wide rows leave room for one
+constexpr int depth_for(int tpr) { return tpr > 512 ? 1 : 2; }
+template <typename L, int TPR, int TENSORS> constexpr size_t smem_for() {
+    return Weights<L, Teams<TPR>::THREADS>::BYTES + Stage<L, Teams<TPR>::THREADS, TENSORS, depth_for(TPR)>::BYTES;
+}
+
 // N sums over a team.  A team of more than a warp is a CTA: buf is [N][32], and
 // the caller alternates between two of them, so one barrier a call is enough.
 template <int TPR, int N>
@@ -238,23 +303,9 @@ __device__ __forceinline__ void team_sums(float (&v)[N], float *buf, int tpr) {
     }
 }
 
-// TPR = 32: up to a warp a row (a power of two, 1 << shift) and several rows a CTA;
-// else up to TPR threads, a CTA
-template <int TPR> struct Teams {
-    static constexpr int THREADS = TPR <= 32 ? 128 : TPR;
-    int t, tpr, in_cta, per_cta, team, teams;
-    __device__ __forceinline__ Teams(int shift) {
-        tpr = TPR <= 32 ? 1 << shift : blockDim.x;
-        per_cta = TPR <= 32 ? THREADS >> shift : 1;
-        in_cta = TPR <= 32 ? threadIdx.x >> shift : 0;
-        t = TPR <= 32 ? threadIdx.x & (tpr - 1) : threadIdx.x;
-        team = blockIdx.x * per_cta + in_cta;
-        teams = gridDim.x * per_cta;
-    }
-};
-
-// resident threads an SM that the kernels' registers leave room for
-constexpr int FWD_THREADS_PER_SM = 640, BWD_THREADS_PER_SM = 512;
+// resident threads an SM that the kernels' registers and shared memory leave room for
+constexpr int FWD_THREADS_PER_SM = 640;
+constexpr int bwd_threads_per_sm(int vec) { return vec == 8 ? 640 : 512; }   // fp32 rows stage twice the bytes
 constexpr int resident(int threads, int per_sm) { return per_sm / threads > 0 ? per_sm / threads : 1; }
 
 // ------------------------------------------------------------------- forward
@@ -267,35 +318,41 @@ __global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THRE
     const Row<L> r(g.t, g.tpr, a.d, static_cast<int>(static_cast<int64_t>(g.team) * a.d % L::VEC), a.rows);
     const float inv_d = 1.f / a.d;
     const Weights<L, Teams<TPR>::THREADS> weights(norm_smem, r, a);
-    typename Row<L>::Raw rx, rh, rg;
-    auto fetch_row = [&](int64_t row) {
-        if (row >= a.rows) return;
-        const int64_t at = row * a.d;
-        r.fetch(a.x, at, rx);
-        if (a.h != nullptr) r.fetch(a.h, at, rh);
-        if (a.gate != nullptr) r.fetch(a.gate, at, rg);
+    constexpr int THREADS = Teams<TPR>::THREADS, DEPTH = depth_for(TPR);
+    const Stage<L, THREADS, 3, DEPTH> stage(reinterpret_cast<unsigned char *>(norm_smem) +
+                                            Weights<L, THREADS>::BYTES);
+    auto fetch_row = [&](int64_t row, int turn) {
+        if (row < a.rows) {
+            const int64_t at = row * a.d;
+            r.template fetch<THREADS>(a.x, at, stage.at(turn, 0));
+            if (a.h != nullptr) r.template fetch<THREADS>(a.h, at, stage.at(turn, 1));
+            if (a.gate != nullptr) r.template fetch<THREADS>(a.gate, at, stage.at(turn, 2));
+        }
+        stage.commit();
     };
     // teams that share a warp run the same number of rounds
     const int64_t rounds = (a.rows + g.teams - 1) / g.teams;
     int64_t row = g.team;
-    fetch_row(row);
+    if (DEPTH > 1) fetch_row(row, 0);
     for (int64_t i = 0; i < rounds; ++i, row += g.teams) {
+        const int turn = DEPTH > 1 ? i & 1 : 0;
+        fetch_row(DEPTH > 1 ? row + g.teams : row, DEPTH > 1 ? turn ^ 1 : 0);
+        stage.wait_row();
         float2 x[L::PAIRS], w[L::PAIRS];
-        r.widen(rx, x);
+        r.template widen<THREADS>(stage.at(turn, 0), x);
         const int64_t at = row * a.d;
         if (a.h != nullptr) {
             float2 v[L::PAIRS], ss = both(0.f);
-            r.widen(rh, v);
+            r.template widen<THREADS>(stage.at(turn, 1), v);
 #pragma unroll
             for (int e = 0; e < L::PAIRS; ++e) ss = fma2(v[e], v[e], ss);
             if (a.gate != nullptr) {
                 float2 gate[L::PAIRS];
-                r.widen(rg, gate);
+                r.template widen<THREADS>(stage.at(turn, 2), gate);
 #pragma unroll
                 for (int e = 0; e < L::PAIRS; ++e)
                     v[e] = mul2(v[e], mul2(gate[e], sigmoid2(gate[e])));
             }
-            fetch_row(row + g.teams);   // in flight over this row's sums
             float sum[1] = {ss.x + ss.y};
             team_sums<TPR, 1>(sum, red[i & 1], g.tpr);
             const float2 q = both(rsqrtf(sum[0] * inv_d + a.eps));
@@ -303,8 +360,6 @@ __global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THRE
 #pragma unroll
             for (int e = 0; e < L::PAIRS; ++e) x[e] = fma2(mul2(v[e], q), w[e], x[e]);
             if (row < a.rows) r.store(a.out_x, at, x);
-        } else {
-            fetch_row(row + g.teams);
         }
         if (!a.norm_u) continue;
         float2 ss = both(0.f);
@@ -322,43 +377,49 @@ __global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THRE
 
 // ------------------------------------------------------------------ backward
 template <typename L, int TPR>
-__global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THREADS, BWD_THREADS_PER_SM))
+__global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THREADS, bwd_threads_per_sm(L::VEC)))
     k_norm_backward(const NormArgs a) {
     __shared__ float red[2][4 * 32];   // three sums, then one; two rows in turn
     extern __shared__ float4 norm_smem[];
     const Teams<TPR> g(a.team_shift);
+    dependents_may_launch();
     const Row<L> r(g.t, g.tpr, a.d, static_cast<int>(static_cast<int64_t>(g.team) * a.d % L::VEC), a.rows);
     const float inv_d = 1.f / a.d;
     const Weights<L, Teams<TPR>::THREADS> weights(norm_smem, r, a);
     float2 s_out[L::PAIRS] = {}, s_pre[L::PAIRS] = {};
-    typename Row<L>::Raw rx, rh, rg, rgx, rgu;
-    auto fetch_row = [&](int64_t row) {
-        if (row >= a.rows) return;
-        const int64_t at = row * a.d;
-        if (a.norm_u) {
-            r.fetch(a.x, at, rx);
-            r.fetch(a.g_u, at, rgu);
+    constexpr int THREADS = Teams<TPR>::THREADS, DEPTH = depth_for(TPR);
+    const Stage<L, THREADS, 5, DEPTH> stage(reinterpret_cast<unsigned char *>(norm_smem) +
+                                            Weights<L, THREADS>::BYTES);
+    auto fetch_row = [&](int64_t row, int turn) {
+        if (row < a.rows) {
+            const int64_t at = row * a.d;
+            if (a.norm_u) {
+                r.template fetch<THREADS>(a.x, at, stage.at(turn, 0));
+                r.template fetch<THREADS>(a.g_u, at, stage.at(turn, 1));
+            }
+            if (a.g_x != nullptr) r.template fetch<THREADS>(a.g_x, at, stage.at(turn, 2));
+            if (a.h != nullptr) r.template fetch<THREADS>(a.h, at, stage.at(turn, 3));
+            if (a.gate != nullptr) r.template fetch<THREADS>(a.gate, at, stage.at(turn, 4));
         }
-        if (a.g_x != nullptr) r.fetch(a.g_x, at, rgx);
-        if (a.h != nullptr) r.fetch(a.h, at, rh);
-        if (a.gate != nullptr) r.fetch(a.gate, at, rg);
+        stage.commit();
     };
     const int64_t rounds = (a.rows + g.teams - 1) / g.teams;
     int64_t row = g.team;
-    fetch_row(row);
+    if (DEPTH > 1) fetch_row(row, 0);
     for (int64_t i = 0; i < rounds; ++i, row += g.teams) {
+        const int turn = DEPTH > 1 ? i & 1 : 0;
+        fetch_row(DEPTH > 1 ? row + g.teams : row, DEPTH > 1 ? turn ^ 1 : 0);
+        stage.wait_row();
         const bool live = row < a.rows;   // a team past the end adds nothing
-        float2 x[L::PAIRS] = {}, h[L::PAIRS] = {}, gate[L::PAIRS] = {}, gx[L::PAIRS] = {}, gu[L::PAIRS] = {};
+        float2 x[L::PAIRS] = {}, h[L::PAIRS] = {}, gx[L::PAIRS] = {}, gu[L::PAIRS] = {};
         if (live) {
             if (a.norm_u) {
-                r.widen(rx, x);
-                r.widen(rgu, gu);
+                r.template widen<THREADS>(stage.at(turn, 0), x);
+                r.template widen<THREADS>(stage.at(turn, 1), gu);
             }
-            if (a.g_x != nullptr) r.widen(rgx, gx);
-            if (a.h != nullptr) r.widen(rh, h);
-            if (a.gate != nullptr) r.widen(rg, gate);
+            if (a.g_x != nullptr) r.template widen<THREADS>(stage.at(turn, 2), gx);
+            if (a.h != nullptr) r.template widen<THREADS>(stage.at(turn, 3), h);
         }
-        fetch_row(row + g.teams);
         const int64_t at = row * a.d;
         float2 m0 = both(0.f), m1 = m0, m2 = m0, w[L::PAIRS];
         weights.load(W_PRE, w);
@@ -387,6 +448,8 @@ __global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THRE
         float2 k2 = both(0.f);
         if (live) {
             weights.load(W_OUT, w);
+            float2 gate[L::PAIRS] = {};
+            if (a.gate != nullptr) r.template widen<THREADS>(stage.at(turn, 4), gate);
 #pragma unroll
             for (int e = 0; e < L::PAIRS; ++e) {
                 h[e] = mul2(h[e], both(q));                     // h^
@@ -444,6 +507,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
     k_norm_join(const float *__restrict__ part, int n_part, int d, const float *w_post,
                 const float *scale, float *gw_post, float *g_scale, float *gw_pre) {
     __shared__ float sum[JOIN_WARPS][32];
+    wait_for_prerequisites();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;   // column of [2][d]
     float s = 0.f;
@@ -467,11 +531,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
 // ---------------------------------------------------------------- host side
 bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Threads a row: the fewest that hold it in n columns each, a power of two up to
+// Threads a row: the fewest that hold it in `pieces` each, a power of two up to
 // a warp, whole warps beyond.
-int team_size(int d, int vec, int n) {
-    const int columns = d % vec == 0 ? d : d + vec - 1;   // a shifted row takes more
-    const int need = (columns + n - 1) / n;
+int team_size(int d, int vec, int pieces) {
+    int common = vec;   // the largest power of two that divides both
+    while (d % common != 0) common /= 2;
+    const int have = (d + vec - common + vec - 1) / vec;   // pieces of the most shifted row
+    const int need = (have + pieces - 1) / pieces;
     if (need > 32) return (need + 31) / 32 * 32;
     int t = 1;
     while (t < need) t *= 2;
@@ -488,9 +554,9 @@ int cta_count(int64_t rows, int tpr, int threads_per_sm) {
     return static_cast<int>(per >= 8 ? most : (most * per + 7) / 8 * 8 / per);
 }
 
-template <typename L, int TPR, typename K>
+template <typename L, int TPR, int TENSORS, typename K>
 cudaError_t launch_norm(K kernel, NormArgs a, int ctas, int tpr, cudaStream_t s) {
-    constexpr size_t smem = Weights<L, Teams<TPR>::THREADS>::BYTES;
+    constexpr size_t smem = smem_for<L, TPR, TENSORS>();
     if (smem > 40 * 1024) {   // 48 KB with the static part need no attribute
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
@@ -501,28 +567,37 @@ cudaError_t launch_norm(K kernel, NormArgs a, int ctas, int tpr, cudaStream_t s)
     return cudaGetLastError();
 }
 
-// 16 columns a thread forward (two pieces of bf16, four of fp32 would be too many
-// registers: two), 8 backward
-template <typename T, int VEC> constexpr int fwd_pieces() { return VEC == 1 ? 8 : 2; }
+// Pieces a thread: two forward, 8 columns backward (its sums take the registers of
+// the others).  A bf16 row that two pieces a thread would leave half empty takes
+// one forward (65537 x 515: 66 pieces in 3 warps instead of 128 in 2).
 template <typename T, int VEC> constexpr int bwd_pieces() { return 8 / VEC; }
 
+template <typename T, int VEC, bool EDGE, int PIECES>
+cudaError_t forward_as(const NormArgs &a, cudaStream_t s) {
+    using L = Layout<T, VEC, PIECES, EDGE>;
+    const int tpr = team_size(a.d, VEC, PIECES), ctas = cta_count(a.rows, tpr, FWD_THREADS_PER_SM);
+    if (tpr <= 32) return launch_norm<L, 32, 3>(k_norm_forward<L, 32>, a, ctas, tpr, s);
+    if (tpr <= 128) return launch_norm<L, 128, 3>(k_norm_forward<L, 128>, a, ctas, tpr, s);
+    if (tpr <= 512) return launch_norm<L, 512, 3>(k_norm_forward<L, 512>, a, ctas, tpr, s);
+    return launch_norm<L, 1024, 3>(k_norm_forward<L, 1024>, a, ctas, tpr, s);
+}
+
 template <typename T, int VEC, bool EDGE> cudaError_t forward_for(const NormArgs &a, cudaStream_t s) {
-    using L = Layout<T, VEC, fwd_pieces<T, VEC>(), EDGE>;
-    const int tpr = team_size(a.d, VEC, L::N), ctas = cta_count(a.rows, tpr, FWD_THREADS_PER_SM);
-    if (tpr <= 32) return launch_norm<L, 32>(k_norm_forward<L, 32>, a, ctas, tpr, s);
-    if (tpr <= 128) return launch_norm<L, 128>(k_norm_forward<L, 128>, a, ctas, tpr, s);
-    if (tpr <= 512) return launch_norm<L, 512>(k_norm_forward<L, 512>, a, ctas, tpr, s);
-    return launch_norm<L, 1024>(k_norm_forward<L, 1024>, a, ctas, tpr, s);
+    if constexpr (VEC == 1) return forward_as<T, 1, false, 8>(a, s);
+    else if constexpr (VEC == 8) {
+        if (team_size(a.d, VEC, 1) < 2 * team_size(a.d, VEC, 2)) return forward_as<T, VEC, EDGE, 1>(a, s);
+    }
+    if constexpr (VEC > 1) return forward_as<T, VEC, EDGE, 2>(a, s);
 }
 
 template <typename T, int VEC, bool EDGE>
 cudaError_t backward_for(const NormArgs &a, int ctas, cudaStream_t s) {
     using L = Layout<T, VEC, bwd_pieces<T, VEC>(), EDGE>;
-    const int tpr = team_size(a.d, VEC, L::N);
-    if (tpr <= 32) return launch_norm<L, 32>(k_norm_backward<L, 32>, a, ctas, tpr, s);
-    if (tpr <= 128) return launch_norm<L, 128>(k_norm_backward<L, 128>, a, ctas, tpr, s);
-    if (tpr <= 512) return launch_norm<L, 512>(k_norm_backward<L, 512>, a, ctas, tpr, s);
-    return launch_norm<L, 1024>(k_norm_backward<L, 1024>, a, ctas, tpr, s);
+    const int tpr = team_size(a.d, VEC, L::PIECES);
+    if (tpr <= 32) return launch_norm<L, 32, 5>(k_norm_backward<L, 32>, a, ctas, tpr, s);
+    if (tpr <= 128) return launch_norm<L, 128, 5>(k_norm_backward<L, 128>, a, ctas, tpr, s);
+    if (tpr <= 512) return launch_norm<L, 512, 5>(k_norm_backward<L, 512>, a, ctas, tpr, s);
+    return launch_norm<L, 1024, 5>(k_norm_backward<L, 1024>, a, ctas, tpr, s);
 }
 
 // calls f<T, VEC, EDGE>(args...) for the storage type, the access width and d
@@ -535,7 +610,7 @@ cudaError_t backward_for(const NormArgs &a, int ctas, cudaStream_t s) {
                                                  : f<float, 4, true>(__VA_ARGS__)))
 
 // CTAs of a backward launch: the most that any access width takes
-int backward_ctas(int64_t rows, int d, int vec) { return cta_count(rows, team_size(d, vec, 8), BWD_THREADS_PER_SM); }
+int backward_ctas(int64_t rows, int d, int vec) { return cta_count(rows, team_size(d, vec, 8 / vec), bwd_threads_per_sm(vec)); }
 
 int check_norm(int dtype, int64_t rows, int64_t d, float eps) {
     if (dtype != NRNN_F32 && dtype != NRNN_BF16) return NRNN_ERR_INVALID_ARG;
@@ -548,7 +623,7 @@ int check_norm(int dtype, int64_t rows, int64_t d, float eps) {
 // (a row of 8192 odd columns would take more than a CTA's threads with pieces)
 int width_for(int elem, int64_t d, std::initializer_list<const void *> ptrs) {
     const int vec = 16 / elem;
-    if (team_size(static_cast<int>(d), vec, 8) > 1024) return 1;
+    if (team_size(static_cast<int>(d), vec, 8 / vec) > 1024) return 1;
     for (const void *p : ptrs)
         if (!aligned_to(p, 16)) return 1;
     return vec;
@@ -635,9 +710,8 @@ int nrnn_block_norm_backward(const void *x_out, const void *h, const void *gate,
         e = NRNN_BY_ROW(dtype, vec, d, backward_for, a, ctas, s);
     }
     if (e == cudaSuccess) {
-        k_norm_join<<<(2 * a.d + 31) / 32, JOIN_WARPS * 32, 0, s>>>(a.part, ctas, a.d, w_post, scale,
-                                                                   gw_post, g_scale, gw_pre);
-        e = cudaGetLastError();
+        e = launch_dependent(k_norm_join, (2 * a.d + 31) / 32, JOIN_WARPS * 32, 0, s, a.part, ctas, a.d,
+                             w_post, scale, gw_post, g_scale, gw_pre);
     }
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }

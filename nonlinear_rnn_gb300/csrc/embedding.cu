@@ -23,15 +23,6 @@ namespace cg = cooperative_groups;
 namespace nrnn {
 namespace {
 
-// programmatic dependent launch: the next kernel of the call may be scheduled now;
-// wait until the one before has completed
-__device__ __forceinline__ void dependents_may_launch() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_prerequisites() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // A warp works on 32 VEC consecutive columns (a slab) of a row.
 constexpr int GROUP_ROWS = 4;      // rows of one warp of the lookup
 constexpr int EMBED_THREADS = 128;

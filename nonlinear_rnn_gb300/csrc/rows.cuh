@@ -7,6 +7,15 @@
 
 namespace nrnn {
 
+// programmatic dependent launch: the next kernel of the call may be scheduled now;
+// wait until the one before has completed
+__device__ __forceinline__ void dependents_may_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_prerequisites() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // VEC consecutive elements of a row as one load or store
 template <typename T, int VEC> struct __align__(sizeof(T) * VEC) Pack { T v[VEC]; };
 
