@@ -19,6 +19,14 @@
 //   GW   G^T x   rows of gW of this piece
 // The piece of G is all that is ever kept of the N x V matrix.
 //
+// GX and GW have few output tiles and long inner dimensions.  Whole waves of tiles
+// go one to a CTA, which walk the inner dimension side by side and share what they
+// read in L2; the tiles that do not fill a wave are cut by inner slices, an equal
+// run of the (tile, slice) sequence to every CTA.  A tile that is cut leaves fp32
+// parts in the workspace, which k_join_parts adds in order.  (Whole tiles only: gx
+// of 16384 x 1024 was 512 tiles on 152 SMs, 84% of them busy on average.  All tiles
+// by slices: the CTAs read G at different places, and slower.)
+//
 // Rows whose target is ignored take no part: the kept rows are numbered on the
 // device and gathered (k_kept_rows, k_gather_rows), and the kernel reads their
 // number there, so ignored rows cost nothing and whatever they hold (infinities,
@@ -54,12 +62,11 @@ enum Form { LSE, DL, GX, GW };
 
 constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
 constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int EPI_WARPS = 4;
+constexpr int EPI_WARPS = 8;   // two per 32 TMEM lanes: one alone on its scheduler waits on its own results
 constexpr int GEMM_THREADS = 128 + EPI_WARPS * 32;
 constexpr int BOX = 32;                                   // rows and columns of a stored block of G
 constexpr int BOX_BYTES = BOX * BOX * 2;
 constexpr size_t GEMM_SMEM = STAGES * STAGE_BYTES + EPI_WARPS * 2 * BOX_BYTES + 1024;
-constexpr int SPLIT_BN = 128;      // fp32: columns of a tile (its sums are held in registers)
 constexpr int SPLIT_CHUNK = 8;     // fp32: 64-wide slices per accumulator
 constexpr int SEGMENTS = 6;        // fp32: plane products, smallest first
 __device__ constexpr int PLANE_A[SEGMENTS] = {2, 1, 0, 1, 0, 0};
@@ -74,17 +81,16 @@ struct GemmArgs {
     int col0;                 // LSE, DL: first vocabulary row; GX: B's first inner row;
                               // GW: first row of gW
     int group;                // LSE: column tiles a unit takes one after another
-    int splits;               // GX: splits of the inner dimension
+    float *parts;             // GX, GW: [CTAs][2][BM][bn] sums of cut tiles
     float scale;              // logit scale c
     const int2 *row;          // per kept row {its row in x, its target}
     const float2 *grad;       // DL: per kept row {lse log2(e), gl c}
-    float2 *part;             // LSE: [rows][groups] {maximum, sum} in base 2
+    float2 *part;             // LSE: [rows][groups][2] {maximum, sum} in base 2
     float *z_target;          // LSE: base-2 logit of the target
     void *out;                // GX, GW: the gradient in the storage type
-    float *acc;               // GX: [splits][rows][acc_pitch] sums over pieces (null: store out)
-    int64_t acc_plane;
+    float *acc;               // GX: [rows][acc_pitch] sums over the pieces (null: one piece)
     int acc_pitch;
-    bool acc_add;             // GX: add to acc
+    bool acc_in, acc_out;     // GX: add acc; store to acc instead of out
     int d;                    // width of gx and gW rows
 };
 
@@ -121,50 +127,92 @@ template <typename T> __device__ __forceinline__ void store_cols(T *p, const flo
     }
 }
 
-// A unit is what a CTA takes at a time: a tile, or (LSE) `group` tiles beside
-// one another.  Every role walks the same sequence of tiles and chunks.
+// A unit is what a CTA takes at a time: a tile; `group` tiles beside one another
+// (LSE); or a tile's slices k0 .. k1 (GX, GW).  Every role walks the same sequence.
+struct Unit { int m0, n0, tiles, k0, k1, group, slot; };   // slot: -1 = a whole tile
+
 template <int FORM> struct Walk {
-    int tiles_m, tiles_n, n_units, kb;   // kb: 64-wide slices of the inner dimension
-    __device__ Walk(const GemmArgs &a) {
+    int tiles_m, tiles_n, n_units, kb, u;   // kb: 64-wide slices of the inner dimension
+    int whole;                              // GX, GW: tiles that are not cut
+    int64_t pos, end;                       // this CTA's run of (tile - whole, slice)
+
+    __device__ explicit Walk(const GemmArgs &a, int ctas) {
         const int kept = *a.kept;
         const int M = a.M < 0 ? kept : a.M, K = a.K < 0 ? kept : a.K;
         tiles_m = (M + BM - 1) / BM;
         tiles_n = (a.n_cols + a.bn - 1) / a.bn;
         kb = (K + BK - 1) / BK;
-        n_units = FORM == LSE  ? tiles_m * ((tiles_n + a.group - 1) / a.group)
-                  : FORM == GX ? tiles_m * tiles_n * a.splits
-                               : tiles_m * tiles_n;
+        n_units = tiles_m * (FORM == LSE ? (tiles_n + a.group - 1) / a.group : tiles_n);
+        whole = kb == 0 ? n_units : n_units / ctas * ctas;   // nothing to sum: zeros, tile by tile
+        u = blockIdx.x;
+        run(blockIdx.x, ctas, pos, end);
+    }
+    // the run of CTA b
+    __device__ void run(int b, int ctas, int64_t &from, int64_t &to) const {
+        const int64_t all = static_cast<int64_t>(n_units - whole) * kb;
+        from = all * b / ctas;
+        to = all * (b + 1) / ctas;
+    }
+    __device__ __forceinline__ bool next(const GemmArgs &a, Unit &t) {
+        t.k0 = 0; t.k1 = kb; t.tiles = 1; t.group = 0; t.slot = -1;
+        if (FORM == LSE || FORM == DL) {
+            if (u >= n_units) return false;
+            // rows fastest: the CTAs working at one time share a tile of W
+            t.m0 = u % tiles_m * BM;
+            t.group = u / tiles_m;
+            t.n0 = t.group;
+            if (FORM == LSE) {
+                t.n0 *= a.group;
+                t.tiles = tiles_n - t.n0 < a.group ? tiles_n - t.n0 : a.group;
+            }
+            t.n0 *= a.bn;
+            u += gridDim.x;
+            return true;
+        }
+        int tile = u;
+        if (u < whole) {
+            u += gridDim.x;
+        } else {
+            if (pos >= end) return false;
+            tile = whole + static_cast<int>(pos / kb);
+            t.k0 = static_cast<int>(pos % kb);
+            if (end - pos < kb - t.k0) t.k1 = t.k0 + static_cast<int>(end - pos);
+            pos += t.k1 - t.k0;
+            if (t.k0 > 0) t.slot = 0;
+            else if (t.k1 < kb) t.slot = 1;
+        }
+        // columns fastest: the CTAs working at one time share G's tiles
+        t.n0 = tile % tiles_n * a.bn;
+        t.m0 = tile / tiles_n * BM;
+        return true;
     }
 };
-struct Unit { int m0, n0, tiles, k0, k1, split; };
 
-template <int FORM>
-__device__ __forceinline__ Unit unit_at(const Walk<FORM> &w, const GemmArgs &a, int u) {
-    Unit t;
-    t.k0 = 0; t.k1 = w.kb; t.tiles = 1; t.split = 0;
-    if (FORM == LSE || FORM == DL) {
-        // rows fastest: the CTAs working at one time share a tile of W
-        t.m0 = u % w.tiles_m * BM;
-        const int g = u / w.tiles_m;
-        if (FORM == LSE) {
-            t.n0 = g * a.group;
-            t.tiles = w.tiles_n - t.n0 < a.group ? w.tiles_n - t.n0 : a.group;
-            t.n0 *= a.bn;
-        } else {
-            t.n0 = g * a.bn;
+// 32 (or fewer: n) columns from c of row m of the GX or GW product to their place
+template <int FORM, typename T>
+__device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m, int c, float (&v)[32], int n) {
+    int64_t row;
+    if (FORM == GX) {
+        if (m >= kept) return;
+        if (a.acc_in || a.acc_out) {
+            float *to = a.acc + static_cast<int64_t>(m) * a.acc_pitch + c;
+            if (a.acc_in) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (e < n) v[e] += to[e];
+            }
+            if (a.acc_out) {
+                store_cols<float>(to, v, n, n % 4 == 0);
+                return;
+            }
         }
+        row = a.row[m].x;
     } else {
-        // columns fastest: they share G's tile
-        t.n0 = u % w.tiles_n * a.bn;
-        u /= w.tiles_n;
-        t.m0 = u % w.tiles_m * BM;
-        if (FORM == GX) {
-            t.split = u / w.tiles_m;
-            t.k0 = static_cast<int>(static_cast<int64_t>(w.kb) * t.split / a.splits);
-            t.k1 = static_cast<int>(static_cast<int64_t>(w.kb) * (t.split + 1) / a.splits);
-        }
+        if (m >= a.M) return;
+        row = static_cast<int64_t>(a.col0) + m;
     }
-    return t;
+    const bool wide = a.d % (16 / sizeof(T)) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+    store_cols<T>(static_cast<T *>(a.out) + row * a.d + c, v, n, wide);
 }
 
 // T: storage type of the inputs (float: split products)
@@ -211,7 +259,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
-    const Walk<FORM> w(a);
+    dependents_may_launch();
+    wait_for_prerequisites();
+    Walk<FORM> w(a, gridDim.x);
+    Unit t;
     constexpr int PASSES = SPLIT ? SEGMENTS : 1;
 
     if (warp == 0 && lane == 0) {
@@ -220,8 +271,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const uint32_t bytes = A_BYTES + (MN_B ? boxes_b * 64 * BK * 2 : a.bn * BK * 2);
         int it = 0;
         bool go = true;
-        for (int u = blockIdx.x; go && u < w.n_units; u += gridDim.x) {
-            const Unit t = unit_at<FORM>(w, a, u);
+        while (go && w.next(a, t)) {
             for (int j = 0; go && j < t.tiles; ++j) {
                 const int n0 = t.n0 + j * a.bn;
                 for (int c0 = t.k0; go && c0 < t.k1;) {
@@ -263,8 +313,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const uint32_t idesc = idesc_bf16(BM, MN_A, MN_B) | static_cast<uint32_t>(a.bn >> 3) << 17;
         int it = 0, phase = 0;
         bool go = true;
-        for (int u = blockIdx.x; go && u < w.n_units; u += gridDim.x) {
-            const Unit t = unit_at<FORM>(w, a, u);
+        while (go && w.next(a, t)) {
             for (int j = 0; go && j < t.tiles; ++j) {
                 for (int c0 = t.k0; go && c0 < t.k1; ++phase) {
                     const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
@@ -301,14 +350,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         }
     } else if (warp >= 4) {
         // --------------------------------------------------------------- epilogue
-        const int quarter = warp & 3;
+        // warps 4..7 take the even 32-column pieces of their lanes, 8..11 the odd ones
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int kept = *a.kept;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        unsigned char *stage_out = smem + STAGES * STAGE_BYTES + quarter * 2 * BOX_BYTES;
+        unsigned char *stage_out = smem + STAGES * STAGE_BYTES + (warp - 4) * 2 * BOX_BYTES;
+        const float scale2 = a.scale * LOG2E;
+        constexpr float NEG_INF = -INFINITY;
+        const float nan = __int_as_float(0x7fffffff);
         int nblk = 0, phase = 0;
         bool ok = true;   // false once a wait gave up: NaN from there on
-        for (int u = blockIdx.x; u < w.n_units; u += gridDim.x) {
-            const Unit t = unit_at<FORM>(w, a, u);
+        while (w.next(a, t)) {
             const int m = t.m0 + quarter * 32 + lane;   // this thread's row of the product
             // LSE, DL: the row's constants
             int target = -1;
@@ -321,42 +373,56 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     gl = g.y;
                 }
             }
-            const float scale2 = a.scale * LOG2E;
-            float mx = __int_as_float(0xff800000), sum = 0.f;   // LSE: running maximum and sum
+            float mx = NEG_INF;              // LSE: running maximum and sums (two lanes of pairs)
+            float2 sum = make_float2(0.f, 0.f);
 
             // 32 columns c .. c + 31 of the tile at n0, as fp32
             auto take = [&](int n0, int c, float (&v)[32]) {
-                const int left = a.n_cols - n0 - c;   // valid columns
+                const int left = min(a.n_cols - n0, a.bn) - c;   // valid columns
+                if (left <= 0 && FORM != DL) return;
                 if (FORM == LSE) {
-                    if (left <= 0) return;
-                    float cm = __int_as_float(0xff800000);
+                    float2 *p = reinterpret_cast<float2 *>(v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        v[e] = e < left ? v[e] * scale2 : __int_as_float(0xff800000);
-                        cm = fmaxf(cm, v[e]);
-                    }
-                    const float up = fmaxf(mx, cm);
-                    const float ref = up == __int_as_float(0xff800000) ? 0.f : up;
-                    float s = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) s += ex2_approx(v[e] - ref);
-                    sum = fmaf(sum, ex2_approx(mx - ref), s);
-                    mx = up;
+                    for (int e = 0; e < 16; ++e) p[e] = mul2(p[e], make_float2(scale2, scale2));
                     const int at = target - n0 - c;
-                    if (at >= 0 && at < 32) {
+                    if (at >= 0 && at < min(left, 32)) {
                         float z = 0.f;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) z = e == at ? v[e] : z;
                         a.z_target[m] = z;
                     }
-                } else if (FORM == DL) {
-                    const int at = target - n0 - c;
+                    if (left < 32)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float p = ex2_approx(fmaf(v[e], scale2, -lse2));
-                        v[e] = m < kept && e < left ? gl * (e == at ? p - 1.f : p) : 0.f;
-                        if (!ok) v[e] = __int_as_float(0x7fffffff);
+                        for (int e = 0; e < 32; ++e) v[e] = e < left ? v[e] : NEG_INF;
+                    float up = mx;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) up = fmaxf(up, v[e]);
+                    const float ref = up == NEG_INF ? 0.f : up;
+                    const float keep = ex2_approx(mx - ref);
+                    sum = mul2(sum, make_float2(keep, keep));
+                    mx = up;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = add2(p[e], make_float2(-ref, -ref));
+                        sum = add2(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                     }
+                } else if (FORM == DL) {
+                    float2 *p = reinterpret_cast<float2 *>(v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = fma2(p[e], make_float2(scale2, scale2), make_float2(-lse2, -lse2));
+                        p[e] = mul2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(gl, gl));
+                    }
+                    const int at = target - n0 - c;
+                    if (at >= 0 && at < 32)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = e == at ? v[e] - gl : v[e];
+                    if (left < 32 || m >= kept)   // zeros outside, whatever the exponential gave
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = e < left && m < kept ? v[e] : 0.f;
+                    if (!ok)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = nan;
 #pragma unroll
                     for (int pl = 0; pl < (SPLIT ? 3 : 1); ++pl) {
                         unsigned char *blk = stage_out + (nblk & 1) * BOX_BYTES;
@@ -389,31 +455,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 } else {
                     if (!ok)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __int_as_float(0x7fffffff);
-                    const int n = min(left, a.bn - c);
-                    if (n <= 0) return;
-                    if (FORM == GX && a.acc != nullptr) {
-                        if (m >= kept) return;
-                        float *to = a.acc + t.split * a.acc_plane + static_cast<int64_t>(m) * a.acc_pitch + n0 + c;
-                        if (a.acc_add) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (e < n) v[e] += to[e];
-                        }
-                        store_cols<float>(to, v, n, n % 4 == 0);
+                        for (int e = 0; e < 32; ++e) v[e] = nan;
+                    const int n = min(left, 32);
+                    if (t.slot < 0) {
+                        store_product<FORM, T>(a, kept, m, n0 + c, v, n);
                     } else {
-                        int64_t row;
-                        if (FORM == GX) {
-                            if (m >= kept) return;
-                            row = a.row[m].x;
-                        } else {
-                            if (m >= a.M) return;
-                            row = static_cast<int64_t>(a.col0) + m;
-                        }
-                        T *to = static_cast<T *>(a.out) + row * a.d + n0 + c;
-                        const bool wide = a.d % (16 / sizeof(T)) == 0 &&
-                                          (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
-                        store_cols<T>(to, v, n, wide);
+                        float *to = a.parts + ((static_cast<int64_t>(blockIdx.x) * 2 + t.slot) * BM + quarter * 32 + lane) * a.bn + c;
+                        store_cols<float>(to, v, n, n % 4 == 0);
                     }
                 }
             };
@@ -421,40 +469,40 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             for (int j = 0; j < t.tiles; ++j) {
                 const int n0 = t.n0 + j * a.bn;
                 if (SPLIT) {
-                    float acc[SPLIT_BN];
+                    constexpr int PIECES = BN / 64;   // 32-column pieces of this warp
+                    float acc[PIECES][32];
 #pragma unroll
-                    for (int e = 0; e < SPLIT_BN; ++e) acc[e] = 0.f;
+                    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) acc[i][e] = 0.f;
                     for (int c0 = t.k0; c0 < t.k1; c0 += SPLIT_CHUNK, ++phase) {
                         const int buf = phase & 1;
                         ok &= wait_or_abort(&accf_bar[buf], (phase >> 1) & 1, &s_abort);
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-                        for (int c = 0; c < SPLIT_BN; c += 32) {
+                        for (int i = 0; i < PIECES; ++i) {
+                            const int c = (2 * i + half) * 32;
                             if (c < a.bn) {
                                 uint32_t v[32];
                                 tmem_ld_cols<32>(tmem + lane_base + buf * BN + c, v);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) acc[c + e] += __uint_as_float(v[e]);
+                                for (int e = 0; e < 32; ++e) acc[i][e] += __uint_as_float(v[e]);
                             }
                         }
                         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                         mbar_arrive(&acce_bar[buf]);
                     }
 #pragma unroll
-                    for (int c = 0; c < SPLIT_BN; c += 32) {
-                        if (c < a.bn) {
-                            float v[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = acc[c + e];
-                            take(n0, c, v);
-                        }
+                    for (int i = 0; i < PIECES; ++i) {
+                        const int c = (2 * i + half) * 32;
+                        if (c < a.bn) take(n0, c, acc[i]);
                     }
                 } else if (t.k0 < t.k1) {
                     const int buf = phase & 1;
                     ok &= wait_or_abort(&accf_bar[buf], (phase >> 1) & 1, &s_abort);
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-                    for (int c = 0; c < a.bn; c += 32) {
+                    for (int c = half * 32; c < a.bn; c += 64) {
                         uint32_t r[32];
                         tmem_ld_cols<32>(tmem + lane_base + buf * BN + c, r);
                         float v[32];
@@ -467,16 +515,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     ++phase;
                 } else {   // nothing to sum: zeros (no kept rows)
 #pragma unroll 1
-                    for (int c = 0; c < a.bn; c += 32) {
+                    for (int c = half * 32; c < a.bn; c += 64) {
                         float v[32] = {};
                         take(n0, c, v);
                     }
                 }
             }
             if (FORM == LSE && m < kept) {
-                if (!ok) sum = __int_as_float(0x7fffffff);
                 const int groups = (w.tiles_n + a.group - 1) / a.group;
-                a.part[static_cast<int64_t>(m) * groups + u / w.tiles_m] = make_float2(mx, sum);
+                a.part[(static_cast<int64_t>(m) * groups + t.group) * 2 + half] =
+                    make_float2(mx, ok ? sum.x + sum.y : nan);
             }
         }
         if (FORM == DL && lane == 0) bulk_wait_all();   // the stores are done before the CTA exits
@@ -492,44 +540,144 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     }
 }
 
+// Adds the parts of the tiles that the GX or GW launch of `ctas` CTAs cut, in the
+// order of their slices.  blockIdx.x: a cut tile.  A warp takes a row, 8 columns a
+// lane; with SPLIT_PARTS (few tiles in many parts) the CTA's warps take a share of
+// one row's parts each, and the shares are added in order.
+constexpr int JOIN_WARPS = 8;
+
+template <int FORM, typename T, bool SPLIT_PARTS>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a, int ctas) {
+    __shared__ float share[SPLIT_PARTS ? JOIN_WARPS : 1][BN];
+    dependents_may_launch();
+    wait_for_prerequisites();
+    const Walk<FORM> w(a, ctas);
+    const int tile = w.whole + blockIdx.x;
+    if (tile >= w.n_units) return;
+    const int kept = *a.kept, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = SPLIT_PARTS ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
+    const int m = tile / w.tiles_n * BM + row, n0 = tile % w.tiles_n * a.bn;
+    if (m >= (FORM == GX ? kept : a.M)) return;
+    // the runs that hold slices of this tile: b0 .. b1
+    const int64_t all = static_cast<int64_t>(w.n_units - w.whole) * w.kb;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * w.kb, stop = first + w.kb;
+    auto run_of = [&](int64_t slice) {   // the run that holds a slice
+        int b = static_cast<int>(slice * ctas / all);
+        int64_t from, to;
+        for (w.run(b, ctas, from, to); slice < from; w.run(--b, ctas, from, to)) {}
+        for (; slice >= to; w.run(++b, ctas, from, to)) {}
+        return b;
+    };
+    const int b0 = run_of(first), b1 = run_of(stop - 1);
+    if (b0 == b1) return;   // one run has it whole
+    const bool dense = all >= ctas;   // no run is empty
+    const int c = lane * 8;
+    float v[8] = {};
+    if (c < a.bn) {
+        const int64_t step = static_cast<int64_t>(2) * BM * a.bn;
+        const float *p = a.parts + b0 * step + static_cast<int64_t>(row) * a.bn + c;
+        const int q0 = SPLIT_PARTS ? warp : 0, dq = SPLIT_PARTS ? JOIN_WARPS : 1;
+#pragma unroll 4
+        for (int q = q0; q <= b1 - b0; q += dq) {
+            if (!dense) {
+                int64_t f, t;
+                w.run(b0 + q, ctas, f, t);
+                if (f == t) continue;
+            }
+            // the first run's part begins with the tile: slot 1
+            float x[8];
+            load_f32<float, 8>(p + q * step + (q == 0 ? static_cast<int64_t>(BM) * a.bn : 0), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += x[e];
+        }
+    }
+    if (SPLIT_PARTS) {
+        if (c < a.bn)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) share[warp][c + e] = v[e];
+        __syncthreads();
+        if (warp > 0 || c >= a.bn) return;
+        for (int q = 1; q < JOIN_WARPS; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += share[q][c + e];
+    }
+    const int n = min(min(a.bn, a.n_cols - n0) - c, 8);
+    if (n <= 0) return;
+    const int col = n0 + c;
+    int64_t at;
+    if (FORM == GX) {
+        float *acc = a.acc + static_cast<int64_t>(m) * a.acc_pitch + col;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (a.acc_in && e < n) v[e] += acc[e];
+        if (a.acc_out) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) acc[e] = v[e];
+            return;
+        }
+        at = static_cast<int64_t>(a.row[m].x) * a.d + col;
+    } else {
+        at = (static_cast<int64_t>(a.col0) + m) * a.d + col;
+    }
+    T *to = static_cast<T *>(a.out) + at;
+    if (a.d % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 16 / sizeof(T)) {
+            float o[16 / sizeof(T)];
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) o[i] = v[e + i];
+            store_f32<T, 16 / sizeof(T)>(to + e, o);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) to[e] = from_f32<T>(v[e]);
+    }
+}
+
 // ------------------------------------------------------------------ the rows
 // Numbers the rows whose target takes part, in order: row[m] = {row, target}.
-// One CTA; each round takes 1024 x ROUND targets.
-constexpr int KEPT_THREADS = 1024, ROUND = 4;
+// One CTA; each round takes 1024 x ROUND targets, 32 x ROUND consecutive ones a warp.
+constexpr int KEPT_THREADS = 1024, ROUND = 16;
 
 template <typename Id>
 __global__ void __launch_bounds__(KEPT_THREADS)
     k_kept_rows(const void *targets, int n, int64_t V, int64_t ignore, int2 *row, int *kept) {
     __shared__ int warp_sum[KEPT_THREADS / 32];
+    dependents_may_launch();
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     int base = 0;
     for (int64_t r0 = 0; r0 < n; r0 += KEPT_THREADS * ROUND) {
         int64_t id[ROUND];
+        unsigned vote[ROUND];
         int mine = 0;
-        const int64_t i0 = r0 + static_cast<int64_t>(t) * ROUND;
-#pragma unroll
-        for (int e = 0; e < ROUND; ++e) {
-            id[e] = i0 + e < n ? static_cast<int64_t>(static_cast<const Id *>(targets)[i0 + e]) : -1;
-            if (i0 + e >= n || id[e] == ignore || id[e] < 0 || id[e] >= V) id[e] = -1;
-            mine += id[e] >= 0;
-        }
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(FULL_MASK, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) warp_sum[w] = incl;
-        __syncthreads();
-        int lower = 0, all = 0;
-        for (int v = 0; v < KEPT_THREADS / 32; ++v) {
-            lower += v < w ? warp_sum[v] : 0;
-            all += warp_sum[v];
-        }
-        int at = base + lower + incl - mine;
+        const int64_t i0 = r0 + w * (32 * ROUND) + lane;
 #pragma unroll
         for (int e = 0; e < ROUND; ++e)
-            if (id[e] >= 0) row[at++] = make_int2(static_cast<int>(i0 + e), static_cast<int>(id[e]));
+            id[e] = i0 + e * 32 < n ? static_cast<int64_t>(static_cast<const Id *>(targets)[i0 + e * 32]) : -1;
+#pragma unroll
+        for (int e = 0; e < ROUND; ++e) {
+            vote[e] = __ballot_sync(FULL_MASK, i0 + e * 32 < n && id[e] != ignore && id[e] >= 0 && id[e] < V);
+            mine += __popc(vote[e]);
+        }
+        if (lane == 0) warp_sum[w] = mine;
+        __syncthreads();
+        int all = warp_sum[lane];
+        int at = lane < w ? all : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            all += __shfl_xor_sync(FULL_MASK, all, o);
+            at += __shfl_xor_sync(FULL_MASK, at, o);
+        }
+        at += base;
+#pragma unroll
+        for (int e = 0; e < ROUND; ++e) {
+            if (vote[e] >> lane & 1u)
+                row[at + __popc(vote[e] & ((1u << lane) - 1u))] =
+                    make_int2(static_cast<int>(i0) + e * 32, static_cast<int>(id[e]));
+            at += __popc(vote[e]);
+        }
         base += all;
         __syncthreads();
     }
@@ -556,33 +704,54 @@ struct GatherArgs {
     int n;
 };
 
+// One row of `pitch` values (a multiple of 8) as bf16 planes, by the lanes of a warp;
+// src null: zeros.  16 bytes out at a time; wide: 16 bytes in as well.
 template <typename T>
 __device__ __forceinline__ void copy_row(const T *src, __nv_bfloat16 *dst, int64_t plane, int d,
-                                         int pitch, int lane) {
-    for (int c = lane * 2; c < pitch; c += 64) {
-        float v0 = src != nullptr && c < d ? to_f32(src[c]) : 0.f;
-        float v1 = src != nullptr && c + 1 < d ? to_f32(src[c + 1]) : 0.f;
+                                         int pitch, int lane, bool wide) {
+#pragma unroll 4
+    for (int c = lane * 8; c < pitch; c += 256) {
+        float v[8];
+        if (src != nullptr && wide) {
+#pragma unroll
+            for (int q = 0; q < 8; q += 16 / sizeof(T)) {
+                float x[16 / sizeof(T)];
+                load_f32<T, 16 / sizeof(T)>(src + c + q, x);
+#pragma unroll
+                for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) v[q + e] = x[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = src != nullptr && c + e < d ? to_f32(src[c + e]) : 0.f;
+        }
 #pragma unroll
         for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-            *reinterpret_cast<__nv_bfloat162 *>(dst + p * plane + c) = h;
-            v0 -= __low2float(h);
-            v1 -= __high2float(h);
+            store_f32<__nv_bfloat16, 8>(dst + p * plane + c, v);
+            if (sizeof(T) == 4)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
         }
     }
+}
+// rows of src can be read 16 bytes at a time
+template <typename T> __device__ __forceinline__ bool wide_rows(const void *src, int d) {
+    return d % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
 }
 
 template <typename T, typename Id>
 __global__ void __launch_bounds__(256) k_gather_rows(const GatherArgs a) {
+    dependents_may_launch();
+    wait_for_prerequisites();
     const int lane = threadIdx.x & 31;
     const int kept = *a.kept;
+    const bool wide = wide_rows<T>(a.x, a.d);
     const int padded = (kept + BM - 1) / BM * BM;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t m = blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows_pad; m += warps) {
         if (m < padded) {
             const int src = m < kept ? a.row[m].x : -1;
             copy_row<T>(src >= 0 ? static_cast<const T *>(a.x) + static_cast<int64_t>(src) * a.d : nullptr,
-                        a.out + m * a.pitch, a.rows_pad * a.pitch, a.d, a.pitch, lane);
+                        a.out + m * a.pitch, a.rows_pad * a.pitch, a.d, a.pitch, lane, wide);
             if (a.grad != nullptr && m < kept && lane == 0)
                 a.grad[m] = make_float2(a.lse[src] * LOG2E, a.gl[src] * a.scale);
         }
@@ -600,9 +769,12 @@ __global__ void __launch_bounds__(256) k_gather_rows(const GatherArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_planes(const T *W, __nv_bfloat16 *out, int64_t V, int d, int pitch) {
+    dependents_may_launch();
+    wait_for_prerequisites();   // the planes' memory may still be read by the call before
+    const bool wide = wide_rows<T>(W, d);
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t v = blockIdx.x * 8 + (threadIdx.x >> 5); v < V; v += warps)
-        copy_row<T>(W + v * d, out + v * pitch, V * pitch, d, pitch, threadIdx.x & 31);
+        copy_row<T>(W + v * d, out + v * pitch, V * pitch, d, pitch, threadIdx.x & 31, wide);
 }
 
 // Joins the row's partial maxima and sums; a warp per row.  Rows that take no
@@ -612,6 +784,7 @@ __global__ void __launch_bounds__(256)
     k_loss_join(const float2 *__restrict__ part, int groups, const float *__restrict__ z_target,
                 const int2 *__restrict__ row, const int *__restrict__ kept, const void *targets, int n,
                 int64_t V, int64_t ignore, float *__restrict__ loss, float *__restrict__ lse) {
+    wait_for_prerequisites();
     const int lane = threadIdx.x & 31;
     const int64_t m = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (m >= n) return;
@@ -648,39 +821,39 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// gx rows from the sums over pieces and splits
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_gx_join(const float *__restrict__ acc, int splits, int64_t plane, int pitch,
-              const int2 *__restrict__ row, const int *__restrict__ kept, T *__restrict__ gx, int d) {
-    const int lane = threadIdx.x & 31;
-    const int64_t m = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (m >= *kept) return;
-    T *to = gx + static_cast<int64_t>(row[m].x) * d;
-    for (int c = lane; c < d; c += 32) {
-        float s = 0.f;
-        for (int q = 0; q < splits; ++q) s += acc[q * plane + m * pitch + c];
-        to[c] = from_f32<T>(s);
-    }
-}
-
 // ---------------------------------------------------------------- host side
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The sizes a call works with, the same for the workspace query and the call.
 struct Plan {
-    int planes, pitch, d_bn, tile_v;
+    int planes, pitch, d_bn, fwd_bn;
     int64_t rows_pad;
     bool copy_w;
     int64_t piece;        // backward: vocabulary rows of a piece
-    int pieces, splits, group, groups;
-    bool acc;
-    size_t kept, row, x, w, part, z, grad, dl, accs, total;
+    int pieces, group, groups;
+    size_t kept, row, x, w, part, z, grad, dl, parts, acc, total;
 };
 
 // bytes the piece of G may take
 constexpr int64_t PIECE_BYTES = 1ll << 30;
+
+// Columns of the forward's tiles.  With enough tiles the widest; with few row tiles
+// the width that leaves the busiest CTA the fewest columns (50021 columns on 152
+// CTAs: two tiles of 256 where three of 112 are 336 columns, 22 us against 19).
+int forward_columns(int64_t tiles_m, int64_t V) {
+    if (tiles_m * ceil_div(V, BN) >= 8 * SMS) return BN;
+    int best = BN;
+    int64_t least = INT64_MAX;
+    for (int bn = BN; bn >= 64; bn -= 16) {
+        const int64_t load = ceil_div(tiles_m * ceil_div(V, bn), SMS) * bn;
+        if (load < least) {
+            least = load;
+            best = bn;
+        }
+    }
+    return best;
+}
 
 Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool backward) {
     Plan p{};
@@ -689,12 +862,11 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
     p.pitch = static_cast<int>((d + 7) / 8 * 8);
     p.rows_pad = ceil_div(n, BM) * BM;
     p.copy_w = split || d % 8 != 0 || !w_aligned;
-    const int most = split ? SPLIT_BN : BN;
     // columns of gx and gW in equal tiles
-    p.d_bn = static_cast<int>(ceil_div(ceil_div(d, ceil_div(d, most)), 16) * 16);
+    p.d_bn = static_cast<int>(ceil_div(ceil_div(d, ceil_div(d, BN)), 16) * 16);
     const int64_t tiles_m = ceil_div(n, BM);
-    p.tile_v = most;
-    const int64_t tiles_v = ceil_div(V, p.tile_v);
+    p.fwd_bn = forward_columns(tiles_m, V);
+    const int64_t tiles_v = ceil_div(V, p.fwd_bn);
     // about eight units per CTA
     p.group = static_cast<int>(tiles_m * tiles_v / (SMS * 8));
     p.group = p.group < 1 ? 1 : p.group > 16 ? 16 : p.group;
@@ -710,7 +882,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
     p.x = take(sizeof(__nv_bfloat16) * p.planes * p.rows_pad * p.pitch);
     p.w = take(p.copy_w ? sizeof(__nv_bfloat16) * p.planes * V * p.pitch : 0);
     if (!backward) {
-        p.part = take(sizeof(float2) * n * p.groups);
+        p.part = take(sizeof(float2) * 2 * n * p.groups);
         p.z = take(sizeof(float) * n);
     } else {
         p.grad = take(sizeof(float2) * n);
@@ -719,14 +891,9 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
         p.piece = p.piece < 2048 ? 2048 : p.piece;
         p.piece = p.piece > all ? all : p.piece;
         p.pieces = static_cast<int>(ceil_div(V, p.piece));
-        // split gx's long inner dimension when its tiles do not fill the SMs
-        const int64_t tiles = tiles_m * ceil_div(d, p.d_bn);
-        p.splits = static_cast<int>(tiles >= SMS * 2 ? 1 : ceil_div(SMS * 2, tiles));
-        const int64_t most_splits = p.piece / 512 > 0 ? p.piece / 512 : 1;
-        p.splits = static_cast<int>(p.splits < most_splits ? p.splits : most_splits);
-        p.acc = p.pieces > 1 || p.splits > 1;
         p.dl = take(sizeof(__nv_bfloat16) * p.planes * p.rows_pad * p.piece);
-        p.accs = take(p.acc ? sizeof(float) * p.splits * p.rows_pad * p.pitch : 0);
+        p.parts = take(sizeof(float) * 2 * SMS * BM * p.d_bn);
+        p.acc = take(p.pieces > 1 ? sizeof(float) * p.rows_pad * p.pitch : 0);
     }
     p.total = at;
     return p;
@@ -734,27 +901,35 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
 
 template <int FORM, typename T>
 cudaError_t gemm(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut,
-                 const GemmArgs &a, int64_t most_units, cudaStream_t s) {
+                 const GemmArgs &a, int64_t most_units, int64_t tiles, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
-    static int sms_of[64];
-    cudaError_t e = once_per_device(configured, [](int dev) {
-        cudaError_t r = cudaFuncSetAttribute(k_vocab_gemm<FORM, T>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(GEMM_SMEM));
-        int n = 0;
-        if (r == cudaSuccess) r = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (r == cudaSuccess && dev < 64) sms_of[dev] = n;
-        return r;
+    cudaError_t e = once_per_device(configured, [](int) {
+        return cudaFuncSetAttribute(k_vocab_gemm<FORM, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(GEMM_SMEM));
     });
     if (e != cudaSuccess) return e;
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64) return cudaErrorInvalidDevice;
     if (most_units > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const int64_t grid = most_units < sms_of[dev] ? most_units : sms_of[dev];
-    k_vocab_gemm<FORM, T><<<static_cast<unsigned>(grid), GEMM_THREADS, GEMM_SMEM, s>>>(tmA, tmB, tmOut, a);
-    return cudaGetLastError();
+    const unsigned grid = static_cast<unsigned>(most_units < SMS ? most_units : SMS);
+    e = launch_dependent(k_vocab_gemm<FORM, T>, grid, GEMM_THREADS, GEMM_SMEM, s, tmA, tmB, tmOut, a);
+    if constexpr (FORM == GX || FORM == GW) {
+        if (e == cudaSuccess && grid > 1) {
+            // tiles that may be cut: those left over by whole waves of any number of kept rows
+            const int64_t cut = tiles < grid ? tiles : grid - 1;
+            const bool few = cut * 8 <= grid;   // eight parts each and more
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(cut), few ? BM : BM / JOIN_WARPS);
+            cfg.blockDim = dim3(JOIN_WARPS * 32);
+            cfg.stream = s;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, few ? k_join_parts<FORM, T, true> : k_join_parts<FORM, T, false>, a,
+                                   static_cast<int>(grid));
+        }
+    }
+    return e;
 }
 
 struct Call {
@@ -782,16 +957,19 @@ cudaError_t lay_out(const Call &c, const Plan &p, const float *lse, const float 
     g.grad = lse != nullptr ? reinterpret_cast<float2 *>(c.ws + p.grad) : nullptr;
     g.gx = gx; g.targets = c.targets; g.V = c.V; g.ignore = c.ignore; g.n = static_cast<int>(c.n);
     const int64_t blocks = p.rows_pad / 8;
-    k_gather_rows<T, Id><<<static_cast<unsigned>(blocks < 4864 ? blocks : 4864), 256, 0, c.stream>>>(g);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess)
+        e = launch_dependent(k_gather_rows<T, Id>, static_cast<unsigned>(blocks < 4864 ? blocks : 4864), 256,
+                             0, c.stream, g);
     *w_out = c.W;
-    if (p.copy_w) {
+    if (e == cudaSuccess && p.copy_w) {
         __nv_bfloat16 *w = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.w);
         const int64_t b = ceil_div(c.V, 8);
-        k_planes<T><<<static_cast<unsigned>(b < 4864 ? b : 4864), 256, 0, c.stream>>>(
-            static_cast<const T *>(c.W), w, c.V, static_cast<int>(c.d), p.pitch);
+        e = launch_dependent(k_planes<T>, static_cast<unsigned>(b < 4864 ? b : 4864), 256, 0, c.stream,
+                             static_cast<const T *>(c.W), w, c.V, static_cast<int>(c.d), p.pitch);
         *w_out = w;
     }
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T, typename Id>
@@ -801,23 +979,23 @@ int forward(const Call &c, float *loss, float *lse) {
     if (lay_out<T, Id>(c, p, nullptr, nullptr, nullptr, &w) != cudaSuccess) return NRNN_ERR_CUDA;
     CUtensorMap tmA, tmB;
     if (!make_map_planes(&tmA, c.ws + p.x, p.pitch, p.rows_pad, p.planes, BK, BM, true) ||
-        !make_map_planes(&tmB, w, p.pitch, c.V, p.planes, BK, p.tile_v, true))
+        !make_map_planes(&tmB, w, p.pitch, c.V, p.planes, BK, p.fwd_bn, true))
         return NRNN_ERR_CUDA;
     GemmArgs a{};
     a.kept = reinterpret_cast<int *>(c.ws + p.kept);
     a.M = -1; a.K = static_cast<int>(c.d);
-    a.bn = p.tile_v; a.n_cols = static_cast<int>(c.V);
+    a.bn = p.fwd_bn; a.n_cols = static_cast<int>(c.V);
     a.group = p.group;
     a.scale = c.scale;
     a.row = reinterpret_cast<int2 *>(c.ws + p.row);
     a.part = reinterpret_cast<float2 *>(c.ws + p.part);
     a.z_target = reinterpret_cast<float *>(c.ws + p.z);
-    if (gemm<LSE, T>(tmA, tmB, tmA, a, ceil_div(c.n, BM) * p.groups, c.stream) != cudaSuccess)
+    if (gemm<LSE, T>(tmA, tmB, tmA, a, ceil_div(c.n, BM) * p.groups, 0, c.stream) != cudaSuccess)
         return NRNN_ERR_CUDA;
-    k_loss_join<Id><<<static_cast<unsigned>(ceil_div(c.n, 8)), 256, 0, c.stream>>>(
-        a.part, p.groups, a.z_target, a.row, a.kept, c.targets, static_cast<int>(c.n), c.V, c.ignore,
-        loss, lse);
-    return cudaGetLastError() == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    return launch_dependent(k_loss_join<Id>, static_cast<unsigned>(ceil_div(c.n, 8)), 256, 0, c.stream, a.part,
+                            2 * p.groups, a.z_target, a.row, a.kept, c.targets, static_cast<int>(c.n), c.V,
+                            c.ignore, loss, lse) == cudaSuccess
+               ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 template <typename T, typename Id>
@@ -827,7 +1005,7 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
     if (lay_out<T, Id>(c, p, lse, gl, gx, &w) != cudaSuccess) return NRNN_ERR_CUDA;
     unsigned char *x = c.ws + p.x, *dl = c.ws + p.dl;
     CUtensorMap xk, wk, gk, wn, gn, xn, gs;   // K-major x, W, G; MN-major W, G, x; G's stores
-    const int tile_v = p.tile_v;
+    constexpr int tile_v = BN;
     if (!make_map_planes(&xk, x, p.pitch, p.rows_pad, p.planes, BK, BM, true) ||
         !make_map_planes(&wk, w, p.pitch, c.V, p.planes, BK, tile_v, true) ||
         !make_map_planes(&gk, dl, p.piece, p.rows_pad, p.planes, BK, BM, true) ||
@@ -842,8 +1020,8 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
     a.row = reinterpret_cast<int2 *>(c.ws + p.row);
     a.grad = reinterpret_cast<float2 *>(c.ws + p.grad);
     a.d = static_cast<int>(c.d);
-    a.splits = p.splits;
-    a.acc_plane = p.rows_pad * p.pitch;
+    a.parts = reinterpret_cast<float *>(c.ws + p.parts);
+    a.acc = reinterpret_cast<float *>(c.ws + p.acc);
     a.acc_pitch = p.pitch;
     const int64_t tiles_m = ceil_div(c.n, BM), tiles_d = ceil_div(c.d, p.d_bn);
     for (int i = 0; i < p.pieces; ++i) {
@@ -852,28 +1030,24 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
         a.col0 = static_cast<int>(v0);
         a.M = -1; a.K = static_cast<int>(c.d);
         a.bn = tile_v; a.n_cols = cols;
-        if (gemm<DL, T>(xk, wk, gs, a, tiles_m * ceil_div(cols, tile_v), c.stream) != cudaSuccess)
+        if (gemm<DL, T>(xk, wk, gs, a, tiles_m * ceil_div(cols, tile_v), 0, c.stream) != cudaSuccess)
             return NRNN_ERR_CUDA;
         a.bn = p.d_bn; a.n_cols = a.d;
         a.K = cols;
         a.out = gx;
-        a.acc = p.acc ? reinterpret_cast<float *>(c.ws + p.accs) : nullptr;
-        a.acc_add = i > 0;
-        if (gemm<GX, T>(gk, wn, gs, a, tiles_m * tiles_d * p.splits, c.stream) != cudaSuccess)
+        a.acc_in = i > 0;
+        a.acc_out = i + 1 < p.pieces;
+        if (gemm<GX, T>(gk, wn, gs, a, tiles_m * tiles_d * ceil_div(cols, BK),
+                        tiles_m * tiles_d, c.stream) != cudaSuccess)
             return NRNN_ERR_CUDA;
         a.M = cols; a.K = -1;
         a.out = gW;
-        a.acc = nullptr;
-        if (gemm<GW, T>(gn, xn, gs, a, ceil_div(cols, BM) * tiles_d, c.stream) != cudaSuccess)
+        if (gemm<GW, T>(gn, xn, gs, a, ceil_div(cols, BM) * tiles_d * ceil_div(c.n, BK),
+                        ceil_div(cols, BM) * tiles_d, c.stream) != cudaSuccess)
             return NRNN_ERR_CUDA;
     }
-    if (p.acc)
-        k_gx_join<T><<<static_cast<unsigned>(ceil_div(c.n, 8)), 256, 0, c.stream>>>(
-            reinterpret_cast<float *>(c.ws + p.accs), p.splits, a.acc_plane, p.pitch, a.row, a.kept,
-            static_cast<T *>(gx), a.d);
-    return cudaGetLastError() == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    return NRNN_OK;
 }
-
 int check_vocab(const Call &c) {
     if (c.dtype != NRNN_F32 && c.dtype != NRNN_BF16) return NRNN_ERR_INVALID_ARG;
     if (c.targets_type != NRNN_I32 && c.targets_type != NRNN_I64) return NRNN_ERR_INVALID_ARG;
