@@ -265,47 +265,47 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     Unit t;
     constexpr int PASSES = SPLIT ? SEGMENTS : 1;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
-        const int boxes_b = (a.bn + 63) / 64;
+        // Lane i starts the i-th copy of a stage: one box of a K-major operand, 64
+        // columns of an MN-major one.  (One lane after another took longer than the
+        // products of a stage: gW of 16384 x 65536 x 1024 ran at 1.4 PFLOP/s.)
+        constexpr int BOXES_A = MN_A ? BM / 64 : 1;
+        const int boxes_b = MN_B ? (a.bn + 63) / 64 : 1;
         const uint32_t bytes = A_BYTES + (MN_B ? boxes_b * 64 * BK * 2 : a.bn * BK * 2);
+        const bool is_a = lane < BOXES_A, copies = lane < BOXES_A + boxes_b;
+        const int box = is_a ? lane : lane - BOXES_A;
+        const bool mn = is_a ? MN_A : MN_B;
+        const uint32_t offset = (is_a ? 0 : A_BYTES) + box * (64 * BK * 2);
         int it = 0;
         bool go = true;
         while (go && w.next(a, t)) {
             for (int j = 0; go && j < t.tiles; ++j) {
-                const int n0 = t.n0 + j * a.bn;
+                // this lane's coordinate along M or N
+                const int at = is_a ? t.m0 + box * 64
+                                    : (MN_B ? 0 : a.col0) + t.n0 + j * a.bn + box * 64;
                 for (int c0 = t.k0; go && c0 < t.k1;) {
                     const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
                     for (int p = 0; go && p < PASSES; ++p) {
-                        const int pa = SPLIT ? PLANE_A[p] : 0, pb = SPLIT ? PLANE_B[p] : 0;
+                        const int plane = SPLIT ? (is_a ? PLANE_A[p] : PLANE_B[p]) : 0;
                         for (int k = c0; k < c1; ++k, ++it) {
                             const int s = it % STAGES;
                             if (it >= STAGES)
-                                go = wait_or_abort(&empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort);
+                                go = __all_sync(FULL_MASK, wait_or_abort(&empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort));
                             if (!go) break;
-                            unsigned char *sa = smem + s * STAGE_BYTES, *sb = sa + A_BYTES;
-                            mbar_arrive_expect_tx(&full_bar[s], bytes);
-                            if (MN_A) {
-                                for (int b = 0; b < BM / 64; ++b)
-                                    tma_load_3d(sa + b * (64 * BK * 2), &tmA, &full_bar[s], t.m0 + b * 64,
-                                                k * BK, pa);
-                            } else {
-                                tma_load_3d(sa, &tmA, &full_bar[s], k * BK, t.m0, pa);
-                            }
-                            if (MN_B) {
-                                for (int b = 0; b < boxes_b; ++b)
-                                    tma_load_3d(sb + b * (64 * BK * 2), &tmB, &full_bar[s], n0 + b * 64,
-                                                (FORM == GX ? a.col0 : 0) + k * BK, pb);
-                            } else {
-                                tma_load_3d(sb, &tmB, &full_bar[s], k * BK, a.col0 + n0, pb);
-                            }
+                            if (lane == 0) mbar_arrive_expect_tx(&full_bar[s], bytes);
+                            __syncwarp();
+                            const int along_k = k * BK + (FORM == GX && !is_a ? a.col0 : 0);
+                            if (copies)
+                                tma_load_3d(smem + s * STAGE_BYTES + offset, is_a ? &tmA : &tmB, &full_bar[s],
+                                            mn ? at : along_k, mn ? along_k : at, plane);
                         }
                     }
                     c0 = c1;
                 }
             }
         }
-        if (!go)   // see the copies in flight through
+        if (!go && lane == 0)   // see the copies in flight through
             for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
                 mbar_wait_bounded(&full_bar[i % STAGES], (i / STAGES) & 1, WAIT_NS, &g_vocab_error);
     } else if (warp == 1 && lane == 0) {
