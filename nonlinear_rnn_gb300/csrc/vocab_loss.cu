@@ -7,10 +7,12 @@
 // 2 N V d operations forward, 6 N V d backward (the logits are computed again):
 // bound by the tensor cores, except for few rows, where reading W bounds it.
 //
-// All three products run on one persistent tcgen05 kernel (k_vocab_gemm): one
-// CTA per SM, 128 x (up to 256) tiles, TMA into a ring of 128-byte-swizzled
-// stages, one thread issuing tcgen05.mma into one of two TMEM accumulators
-// while the epilogue warps drain the other.  Its forms differ in the operands'
+// All three products run on one persistent tcgen05 kernel (k_vocab_gemm): a pair
+// of CTAs on two SMs (cta_group::2) per 256 x (up to 256) tile, TMA into a ring of
+// 128-byte-swizzled stages, one thread issuing tcgen05.mma into one of two TMEM
+// accumulators while the epilogue warps drain the other.  A pair reads half of
+// what two single tiles read: with one CTA per 128 x 256 tile the L2 could not
+// feed the tensor cores (77% active, 96 bytes a cycle and SM asked for).  Its forms differ in the operands'
 // orientation (the transposed ones are read MN-major from where they lie: no
 // transposed copy is made) and in the epilogue:
 //   LSE  x W^T   running maximum and sum of each row over the unit's vocabulary
@@ -20,9 +22,9 @@
 // The piece of G is all that is ever kept of the N x V matrix.
 //
 // GX and GW have few output tiles and long inner dimensions.  Whole waves of tiles
-// go one to a CTA, which walk the inner dimension side by side and share what they
+// go one to a pair, which walk the inner dimension side by side and share what they
 // read in L2; the tiles that do not fill a wave are cut by inner slices, an equal
-// run of the (tile, slice) sequence to every CTA.  A tile that is cut leaves fp32
+// run of the (tile, slice) sequence to every pair.  A tile that is cut leaves fp32
 // parts in the workspace, which k_join_parts adds in order.  (Whole tiles only: gx
 // of 16384 x 1024 was 512 tiles on 152 SMs, 84% of them busy on average.  All tiles
 // by slices: the CTAs read G at different places, and slower.)
@@ -54,14 +56,15 @@ namespace {
 
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr int SMS = 152;   // work is divided for this many persistent CTAs
+constexpr int PAIRS = 76;   // of 152 SMs: the work is divided for this many
 
 __device__ uint32_t g_vocab_error;
 
 enum Form { LSE, DL, GX, GW };
 
-constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int BM = 256, BN = 256, BK = 64, STAGES = 6;   // of a pair
+constexpr int HALF_M = BM / 2;                             // rows of A and D in one CTA
+constexpr int A_BYTES = HALF_M * BK * 2, B_BYTES = BN / 2 * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int EPI_WARPS = 8;   // two per 32 TMEM lanes: one alone on its scheduler waits on its own results
 constexpr int GEMM_THREADS = 128 + EPI_WARPS * 32;
 constexpr int BOX = 32;                                   // rows and columns of a stored block of G
@@ -76,12 +79,12 @@ struct GemmArgs {
     const int *kept;          // device: number of kept rows
     int M;                    // rows of the product on the host's side: -1 = kept
     int K;                    // inner size: -1 = kept
-    int bn;                   // columns of a tile: a multiple of 16, at most BN
+    int bn;                   // columns of a tile: a multiple of 32, at most BN
     int n_cols;               // columns of the product (LSE, DL: of this piece)
     int col0;                 // LSE, DL: first vocabulary row; GX: B's first inner row;
                               // GW: first row of gW
     int group;                // LSE: column tiles a unit takes one after another
-    float *parts;             // GX, GW: [CTAs][2][BM][bn] sums of cut tiles
+    float *parts;             // GX, GW: [pairs][2][BM][bn] sums of cut tiles
     float scale;              // logit scale c
     const int2 *row;          // per kept row {its row in x, its target}
     const float2 *grad;       // DL: per kept row {lse log2(e), gl c}
@@ -127,37 +130,38 @@ template <typename T> __device__ __forceinline__ void store_cols(T *p, const flo
     }
 }
 
-// A unit is what a CTA takes at a time: a tile; `group` tiles beside one another
+// A unit is what a pair takes at a time: a tile; `group` tiles beside one another
 // (LSE); or a tile's slices k0 .. k1 (GX, GW).  Every role walks the same sequence.
 struct Unit { int m0, n0, tiles, k0, k1, group, slot; };   // slot: -1 = a whole tile
 
 template <int FORM> struct Walk {
     int tiles_m, tiles_n, n_units, kb, u;   // kb: 64-wide slices of the inner dimension
     int whole;                              // GX, GW: tiles that are not cut
-    int64_t pos, end;                       // this CTA's run of (tile - whole, slice)
+    int64_t pos, end;                       // this pair's run of (tile - whole, slice)
+    int pairs;
 
-    __device__ explicit Walk(const GemmArgs &a, int ctas) {
+    __device__ Walk(const GemmArgs &a, int pair, int pairs_) : pairs(pairs_) {
         const int kept = *a.kept;
         const int M = a.M < 0 ? kept : a.M, K = a.K < 0 ? kept : a.K;
         tiles_m = (M + BM - 1) / BM;
         tiles_n = (a.n_cols + a.bn - 1) / a.bn;
         kb = (K + BK - 1) / BK;
         n_units = tiles_m * (FORM == LSE ? (tiles_n + a.group - 1) / a.group : tiles_n);
-        whole = kb == 0 ? n_units : n_units / ctas * ctas;   // nothing to sum: zeros, tile by tile
-        u = blockIdx.x;
-        run(blockIdx.x, ctas, pos, end);
+        whole = kb == 0 ? n_units : n_units / pairs * pairs;   // nothing to sum: zeros, tile by tile
+        u = pair;
+        run(pair, pos, end);
     }
-    // the run of CTA b
-    __device__ void run(int b, int ctas, int64_t &from, int64_t &to) const {
+    // the run of pair b
+    __device__ void run(int b, int64_t &from, int64_t &to) const {
         const int64_t all = static_cast<int64_t>(n_units - whole) * kb;
-        from = all * b / ctas;
-        to = all * (b + 1) / ctas;
+        from = all * b / pairs;
+        to = all * (b + 1) / pairs;
     }
     __device__ __forceinline__ bool next(const GemmArgs &a, Unit &t) {
         t.k0 = 0; t.k1 = kb; t.tiles = 1; t.group = 0; t.slot = -1;
         if (FORM == LSE || FORM == DL) {
             if (u >= n_units) return false;
-            // rows fastest: the CTAs working at one time share a tile of W
+            // rows fastest: the pairs working at one time share a tile of W
             t.m0 = u % tiles_m * BM;
             t.group = u / tiles_m;
             t.n0 = t.group;
@@ -166,12 +170,12 @@ template <int FORM> struct Walk {
                 t.tiles = tiles_n - t.n0 < a.group ? tiles_n - t.n0 : a.group;
             }
             t.n0 *= a.bn;
-            u += gridDim.x;
+            u += pairs;
             return true;
         }
         int tile = u;
         if (u < whole) {
-            u += gridDim.x;
+            u += pairs;
         } else {
             if (pos >= end) return false;
             tile = whole + static_cast<int>(pos / kb);
@@ -181,7 +185,7 @@ template <int FORM> struct Walk {
             if (t.k0 > 0) t.slot = 0;
             else if (t.k1 < kb) t.slot = 1;
         }
-        // columns fastest: the CTAs working at one time share G's tiles
+        // columns fastest: the pairs working at one time share G's tiles
         t.n0 = tile % tiles_n * a.bn;
         t.m0 = tile / tiles_n * BM;
         return true;
@@ -217,7 +221,7 @@ __device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m
 
 // T: storage type of the inputs (float: split products)
 template <int FORM, typename T>
-__global__ void __launch_bounds__(GEMM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     k_vocab_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmOut, const GemmArgs a) {
     constexpr bool SPLIT = sizeof(T) == 4;
@@ -232,14 +236,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __shared__ volatile uint32_t s_abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full_bar[s], 1);
+            mbar_init(&full_bar[s], 1);   // rank 0's: both CTAs' copies
             mbar_init(&empty_bar[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf_bar[b], 1);
-            mbar_init(&acce_bar[b], EPI_WARPS * 32);
+            mbar_init(&acce_bar[b], 2 * EPI_WARPS);   // rank 0's: both epilogues
         }
         mbar_init(&drain_bar, 1);
         s_abort = 0;
@@ -249,19 +254,21 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         if (FORM == DL) prefetch_tensormap(&tmOut);
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&s_tmem)),
                      "r"(TMEM_COLS)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    cluster_sync_all();   // both CTAs' barriers are there
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = s_tmem;
     dependents_may_launch();
     wait_for_prerequisites();
-    Walk<FORM> w(a, gridDim.x);
+    const int pair = blockIdx.x >> 1;
+    Walk<FORM> w(a, pair, gridDim.x >> 1);
     Unit t;
     constexpr int PASSES = SPLIT ? SEGMENTS : 1;
 
@@ -270,9 +277,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         // Lane i starts the i-th copy of a stage: one box of a K-major operand, 64
         // columns of an MN-major one.  (One lane after another took longer than the
         // products of a stage: gW of 16384 x 65536 x 1024 ran at 1.4 PFLOP/s.)
-        constexpr int BOXES_A = MN_A ? BM / 64 : 1;
-        const int boxes_b = MN_B ? (a.bn + 63) / 64 : 1;
-        const uint32_t bytes = A_BYTES + (MN_B ? boxes_b * 64 * BK * 2 : a.bn * BK * 2);
+        constexpr int BOXES_A = MN_A ? HALF_M / 64 : 1;
+        const int half_n = a.bn / 2;
+        const int boxes_b = MN_B ? (half_n + 63) / 64 : 1;
+        const uint32_t bytes = A_BYTES + (MN_B ? boxes_b * 64 : half_n) * BK * 2;
         const bool is_a = lane < BOXES_A, copies = lane < BOXES_A + boxes_b;
         const int box = is_a ? lane : lane - BOXES_A;
         const bool mn = is_a ? MN_A : MN_B;
@@ -282,8 +290,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         while (go && w.next(a, t)) {
             for (int j = 0; go && j < t.tiles; ++j) {
                 // this lane's coordinate along M or N
-                const int at = is_a ? t.m0 + box * 64
-                                    : (MN_B ? 0 : a.col0) + t.n0 + j * a.bn + box * 64;
+                const int at = is_a ? t.m0 + static_cast<int>(rank) * HALF_M + box * 64
+                                    : (MN_B ? 0 : a.col0) + t.n0 + j * a.bn +
+                                          static_cast<int>(rank) * half_n + box * 64;
                 for (int c0 = t.k0; go && c0 < t.k1;) {
                     const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
                     for (int p = 0; go && p < PASSES; ++p) {
@@ -293,22 +302,23 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                             if (it >= STAGES)
                                 go = __all_sync(FULL_MASK, wait_or_abort(&empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort));
                             if (!go) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&full_bar[s], bytes);
+                            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * bytes);
                             __syncwarp();
                             const int along_k = k * BK + (FORM == GX && !is_a ? a.col0 : 0);
                             if (copies)
-                                tma_load_3d(smem + s * STAGE_BYTES + offset, is_a ? &tmA : &tmB, &full_bar[s],
-                                            mn ? at : along_k, mn ? along_k : at, plane);
+                                tma_load_3d_pair(smem + s * STAGE_BYTES + offset, is_a ? &tmA : &tmB,
+                                                 cluster_addr(&full_bar[s], 0), mn ? at : along_k,
+                                                 mn ? along_k : at, plane);
                         }
                     }
                     c0 = c1;
                 }
             }
         }
-        if (!go && lane == 0)   // see the copies in flight through
+        if (!go && lane == 0 && rank == 0)   // see the copies in flight through
             for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
                 mbar_wait_bounded(&full_bar[i % STAGES], (i / STAGES) & 1, WAIT_NS, &g_vocab_error);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc = idesc_bf16(BM, MN_A, MN_B) | static_cast<uint32_t>(a.bn >> 3) << 17;
         int it = 0, phase = 0;
@@ -335,22 +345,22 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                                                      : sw128_desc(sa + kk * 32);
                             const uint64_t db = MN_B ? sw128_mn_desc(sb + kk * 2048, 64 * BK * 2)
                                                      : sw128_desc(sb + kk * 32);
-                            mma_f16(d, da, db, idesc, i > 0 || kk > 0 ? 1u : 0u);
+                            mma_f16_pair(d, da, db, idesc, i > 0 || kk > 0 ? 1u : 0u);
                         }
-                        mma_commit(&empty_bar[s]);
+                        mma_commit_pair(&empty_bar[s]);
                     }
-                    if (go) mma_commit(&accf_bar[buf]);
+                    if (go) mma_commit_pair(&accf_bar[buf]);
                     c0 = c1;
                 }
             }
         }
         if (!go) {   // see the products in flight through
-            mma_commit(&drain_bar);
+            mma_commit_pair(&drain_bar);
             mbar_wait_bounded(&drain_bar, 0, WAIT_NS, &g_vocab_error);
         }
     } else if (warp >= 4) {
         // --------------------------------------------------------------- epilogue
-        // warps 4..7 take the even 32-column pieces of their lanes, 8..11 the odd ones
+        // warps 4..7 take the even 32-column pieces of their 32 rows, 8..11 the odd ones
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int kept = *a.kept;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
@@ -360,8 +370,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const float nan = __int_as_float(0x7fffffff);
         int nblk = 0, phase = 0;
         bool ok = true;   // false once a wait gave up: NaN from there on
+        auto release = [&](int buf) {   // this warp has read the accumulator
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&acce_bar[buf], 0));
+        };
         while (w.next(a, t)) {
-            const int m = t.m0 + quarter * 32 + lane;   // this thread's row of the product
+            const int in_tile = static_cast<int>(rank) * HALF_M + quarter * 32;   // the warp's first row
+            const int m = t.m0 + in_tile + lane;   // this thread's row of the product
             // LSE, DL: the row's constants
             int target = -1;
             float lse2 = 0.f, gl = 0.f;
@@ -447,7 +463,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_3d(&tmOut, blk, n0 + c, t.m0 + quarter * 32, pl);
+                            tma_store_3d(&tmOut, blk, n0 + c, t.m0 + in_tile, pl);
                             bulk_commit();
                         }
                         ++nblk;
@@ -460,7 +476,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     if (t.slot < 0) {
                         store_product<FORM, T>(a, kept, m, n0 + c, v, n);
                     } else {
-                        float *to = a.parts + ((static_cast<int64_t>(blockIdx.x) * 2 + t.slot) * BM + quarter * 32 + lane) * a.bn + c;
+                        float *to = a.parts + ((static_cast<int64_t>(pair) * 2 + t.slot) * BM + in_tile + lane) * a.bn + c;
                         store_cols<float>(to, v, n, n % 4 == 0);
                     }
                 }
@@ -489,8 +505,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                                 for (int e = 0; e < 32; ++e) acc[i][e] += __uint_as_float(v[e]);
                             }
                         }
-                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                        mbar_arrive(&acce_bar[buf]);
+                        release(buf);
                     }
 #pragma unroll
                     for (int i = 0; i < PIECES; ++i) {
@@ -510,8 +525,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                         for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
                         take(n0, c, v);
                     }
-                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                    mbar_arrive(&acce_bar[buf]);
+                    release(buf);
                     ++phase;
                 } else {   // nothing to sum: zeros (no kept rows)
 #pragma unroll 1
@@ -532,26 +546,27 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
+    cluster_sync_all();   // neither CTA leaves while the other may still reach into it
     if (warp == 2) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(TMEM_COLS)
                      : "memory");
     }
 }
 
-// Adds the parts of the tiles that the GX or GW launch of `ctas` CTAs cut, in the
+// Adds the parts of the tiles that the GX or GW launch of `pairs` pairs cut, in the
 // order of their slices.  blockIdx.x: a cut tile.  A warp takes a row, 8 columns a
 // lane; with SPLIT_PARTS (few tiles in many parts) the CTA's warps take a share of
 // one row's parts each, and the shares are added in order.
 constexpr int JOIN_WARPS = 8;
 
 template <int FORM, typename T, bool SPLIT_PARTS>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a, int ctas) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a, int pairs) {
     __shared__ float share[SPLIT_PARTS ? JOIN_WARPS : 1][BN];
     dependents_may_launch();
     wait_for_prerequisites();
-    const Walk<FORM> w(a, ctas);
+    const Walk<FORM> w(a, 0, pairs);
     const int tile = w.whole + blockIdx.x;
     if (tile >= w.n_units) return;
     const int kept = *a.kept, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -562,15 +577,15 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a
     const int64_t all = static_cast<int64_t>(w.n_units - w.whole) * w.kb;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * w.kb, stop = first + w.kb;
     auto run_of = [&](int64_t slice) {   // the run that holds a slice
-        int b = static_cast<int>(slice * ctas / all);
+        int b = static_cast<int>(slice * pairs / all);
         int64_t from, to;
-        for (w.run(b, ctas, from, to); slice < from; w.run(--b, ctas, from, to)) {}
-        for (; slice >= to; w.run(++b, ctas, from, to)) {}
+        for (w.run(b, from, to); slice < from; w.run(--b, from, to)) {}
+        for (; slice >= to; w.run(++b, from, to)) {}
         return b;
     };
     const int b0 = run_of(first), b1 = run_of(stop - 1);
     if (b0 == b1) return;   // one run has it whole
-    const bool dense = all >= ctas;   // no run is empty
+    const bool dense = all >= pairs;   // no run is empty
     const int c = lane * 8;
     float v[8] = {};
     if (c < a.bn) {
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a
         for (int q = q0; q <= b1 - b0; q += dq) {
             if (!dense) {
                 int64_t f, t;
-                w.run(b0 + q, ctas, f, t);
+                w.run(b0 + q, f, t);
                 if (f == t) continue;
             }
             // the first run's part begins with the tile: slot 1
@@ -685,7 +700,7 @@ __global__ void __launch_bounds__(KEPT_THREADS)
 }
 
 // Copies the kept rows of x to (planes, rows_pad, pitch) bf16, zeros after them
-// up to a multiple of 128 rows and beyond column d; with lse given, the rows'
+// up to a multiple of 256 rows and beyond column d; with lse given, the rows'
 // constants of the DL form.  Then, with gx given, clears the rows of gx that
 // take no part (a target out of range gives NaN).
 struct GatherArgs {
@@ -839,14 +854,14 @@ struct Plan {
 constexpr int64_t PIECE_BYTES = 1ll << 30;
 
 // Columns of the forward's tiles.  With enough tiles the widest; with few row tiles
-// the width that leaves the busiest CTA the fewest columns (50021 columns on 152
-// CTAs: two tiles of 256 where three of 112 are 336 columns, 22 us against 19).
+// the width that leaves the busiest pair the fewest columns (50021 columns on 76
+// pairs: three tiles of 256 where eleven of 64 are 704 columns).
 int forward_columns(int64_t tiles_m, int64_t V) {
-    if (tiles_m * ceil_div(V, BN) >= 8 * SMS) return BN;
+    if (tiles_m * ceil_div(V, BN) >= 8 * PAIRS) return BN;
     int best = BN;
     int64_t least = INT64_MAX;
-    for (int bn = BN; bn >= 64; bn -= 16) {
-        const int64_t load = ceil_div(tiles_m * ceil_div(V, bn), SMS) * bn;
+    for (int bn = BN; bn >= 64; bn -= 32) {
+        const int64_t load = ceil_div(tiles_m * ceil_div(V, bn), PAIRS) * bn;
         if (load < least) {
             least = load;
             best = bn;
@@ -863,12 +878,12 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
     p.rows_pad = ceil_div(n, BM) * BM;
     p.copy_w = split || d % 8 != 0 || !w_aligned;
     // columns of gx and gW in equal tiles
-    p.d_bn = static_cast<int>(ceil_div(ceil_div(d, ceil_div(d, BN)), 16) * 16);
+    p.d_bn = static_cast<int>(ceil_div(ceil_div(d, ceil_div(d, BN)), 32) * 32);
     const int64_t tiles_m = ceil_div(n, BM);
     p.fwd_bn = forward_columns(tiles_m, V);
     const int64_t tiles_v = ceil_div(V, p.fwd_bn);
-    // about eight units per CTA
-    p.group = static_cast<int>(tiles_m * tiles_v / (SMS * 8));
+    // about eight units per pair
+    p.group = static_cast<int>(tiles_m * tiles_v / (PAIRS * 8));
     p.group = p.group < 1 ? 1 : p.group > 16 ? 16 : p.group;
     p.groups = static_cast<int>(ceil_div(tiles_v, p.group));
     size_t at = 0;
@@ -892,7 +907,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
         p.piece = p.piece > all ? all : p.piece;
         p.pieces = static_cast<int>(ceil_div(V, p.piece));
         p.dl = take(sizeof(__nv_bfloat16) * p.planes * p.rows_pad * p.piece);
-        p.parts = take(sizeof(float) * 2 * SMS * BM * p.d_bn);
+        p.parts = take(sizeof(float) * 2 * PAIRS * BM * p.d_bn);
         p.acc = take(p.pieces > 1 ? sizeof(float) * p.rows_pad * p.pitch : 0);
     }
     p.total = at;
@@ -909,13 +924,13 @@ cudaError_t gemm(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorM
     });
     if (e != cudaSuccess) return e;
     if (most_units > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const unsigned grid = static_cast<unsigned>(most_units < SMS ? most_units : SMS);
-    e = launch_dependent(k_vocab_gemm<FORM, T>, grid, GEMM_THREADS, GEMM_SMEM, s, tmA, tmB, tmOut, a);
+    const unsigned pairs = static_cast<unsigned>(most_units < PAIRS ? most_units : PAIRS);
+    e = launch_dependent(k_vocab_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, GEMM_SMEM, s, tmA, tmB, tmOut, a);
     if constexpr (FORM == GX || FORM == GW) {
-        if (e == cudaSuccess && grid > 1) {
+        if (e == cudaSuccess && pairs > 1) {
             // tiles that may be cut: those left over by whole waves of any number of kept rows
-            const int64_t cut = tiles < grid ? tiles : grid - 1;
-            const bool few = cut * 8 <= grid;   // eight parts each and more
+            const int64_t cut = tiles < pairs ? tiles : pairs - 1;
+            const bool few = cut * 8 <= pairs;   // eight parts each and more
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(cut), few ? BM : BM / JOIN_WARPS);
             cfg.blockDim = dim3(JOIN_WARPS * 32);
@@ -926,7 +941,7 @@ cudaError_t gemm(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorM
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             e = cudaLaunchKernelEx(&cfg, few ? k_join_parts<FORM, T, true> : k_join_parts<FORM, T, false>, a,
-                                   static_cast<int>(grid));
+                                   static_cast<int>(pairs));
         }
     }
     return e;
@@ -978,8 +993,8 @@ int forward(const Call &c, float *loss, float *lse) {
     const void *w;
     if (lay_out<T, Id>(c, p, nullptr, nullptr, nullptr, &w) != cudaSuccess) return NRNN_ERR_CUDA;
     CUtensorMap tmA, tmB;
-    if (!make_map_planes(&tmA, c.ws + p.x, p.pitch, p.rows_pad, p.planes, BK, BM, true) ||
-        !make_map_planes(&tmB, w, p.pitch, c.V, p.planes, BK, p.fwd_bn, true))
+    if (!make_map_planes(&tmA, c.ws + p.x, p.pitch, p.rows_pad, p.planes, BK, HALF_M, true) ||
+        !make_map_planes(&tmB, w, p.pitch, c.V, p.planes, BK, p.fwd_bn / 2, true))
         return NRNN_ERR_CUDA;
     GemmArgs a{};
     a.kept = reinterpret_cast<int *>(c.ws + p.kept);
@@ -1006,9 +1021,9 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
     unsigned char *x = c.ws + p.x, *dl = c.ws + p.dl;
     CUtensorMap xk, wk, gk, wn, gn, xn, gs;   // K-major x, W, G; MN-major W, G, x; G's stores
     constexpr int tile_v = BN;
-    if (!make_map_planes(&xk, x, p.pitch, p.rows_pad, p.planes, BK, BM, true) ||
-        !make_map_planes(&wk, w, p.pitch, c.V, p.planes, BK, tile_v, true) ||
-        !make_map_planes(&gk, dl, p.piece, p.rows_pad, p.planes, BK, BM, true) ||
+    if (!make_map_planes(&xk, x, p.pitch, p.rows_pad, p.planes, BK, HALF_M, true) ||
+        !make_map_planes(&wk, w, p.pitch, c.V, p.planes, BK, tile_v / 2, true) ||
+        !make_map_planes(&gk, dl, p.piece, p.rows_pad, p.planes, BK, HALF_M, true) ||
         !make_map_planes(&wn, w, p.pitch, c.V, p.planes, 64, BK, true) ||
         !make_map_planes(&gn, dl, p.piece, p.rows_pad, p.planes, 64, BK, true) ||
         !make_map_planes(&xn, x, p.pitch, p.rows_pad, p.planes, 64, BK, true) ||
