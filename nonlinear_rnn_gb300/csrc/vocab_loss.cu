@@ -23,8 +23,9 @@
 //
 // GX and GW have few output tiles and long inner dimensions.  Whole waves of tiles
 // go one to a pair, which walk the inner dimension side by side and share what they
-// read in L2; the tiles that do not fill a wave are cut by inner slices, an equal
-// run of the (tile, slice) sequence to every pair.  A tile that is cut leaves fp32
+// read in L2, the column tiles of one row tile to a team of pairs beside one
+// another; the tiles that do not fill a wave are cut by inner slices, an equal run
+// of the (row tile, slice) sequence to every team.  A tile that is cut leaves fp32
 // parts in the workspace, which k_join_parts adds in order.  (Whole tiles only: gx
 // of 16384 x 1024 was 512 tiles on 152 SMs, 84% of them busy on average.  All tiles
 // by slices: the CTAs read G at different places, and slower.)
@@ -62,14 +63,18 @@ __device__ uint32_t g_vocab_error;
 
 enum Form { LSE, DL, GX, GW };
 
+// GX, GW: the column tiles of a row tile go to as many pairs beside one another, up
+// to this many
+constexpr int MOST_SIDE = 8;
+
 constexpr int BM = 256, BN = 256, BK = 64, STAGES = 6;   // of a pair
 constexpr int HALF_M = BM / 2;                             // rows of A and D in one CTA
 constexpr int A_BYTES = HALF_M * BK * 2, B_BYTES = BN / 2 * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int EPI_WARPS = 8;   // two per 32 TMEM lanes: one alone on its scheduler waits on its own results
 constexpr int GEMM_THREADS = 128 + EPI_WARPS * 32;
-constexpr int BOX = 32;                                   // rows and columns of a stored block of G
-constexpr int BOX_BYTES = BOX * BOX * 2;
-constexpr size_t GEMM_SMEM = STAGES * STAGE_BYTES + EPI_WARPS * 2 * BOX_BYTES + 1024;
+constexpr int PIECE = 64;                                  // columns that an epilogue warp takes at a time
+constexpr int BOX_ROWS = 32, BOX_BYTES = BOX_ROWS * PIECE * 2;   // a stored block of G
+constexpr size_t GEMM_SMEM = STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + 1024;
 constexpr int SPLIT_CHUNK = 8;     // fp32: 64-wide slices per accumulator
 constexpr int SEGMENTS = 6;        // fp32: plane products, smallest first
 __device__ constexpr int PLANE_A[SEGMENTS] = {2, 1, 0, 1, 0, 0};
@@ -113,11 +118,11 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     return true;
 }
 
-template <typename T> __device__ __forceinline__ void store_cols(T *p, const float (&v)[32], int n, bool wide) {
+template <typename T> __device__ __forceinline__ void store_cols(T *p, const float (&v)[PIECE], int n, bool wide) {
     constexpr int VEC = 16 / sizeof(T);
     if (wide) {
 #pragma unroll
-        for (int c = 0; c < 32; c += VEC) {
+        for (int c = 0; c < PIECE; c += VEC) {
             float o[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) o[e] = v[c + e];
@@ -125,7 +130,7 @@ template <typename T> __device__ __forceinline__ void store_cols(T *p, const flo
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
+        for (int c = 0; c < PIECE; ++c)
             if (c < n) p[c] = from_f32<T>(v[c]);
     }
 }
@@ -137,8 +142,8 @@ struct Unit { int m0, n0, tiles, k0, k1, group, slot; };   // slot: -1 = a whole
 template <int FORM> struct Walk {
     int tiles_m, tiles_n, n_units, kb, u;   // kb: 64-wide slices of the inner dimension
     int whole;                              // GX, GW: tiles that are not cut
-    int64_t pos, end;                       // this pair's run of (tile - whole, slice)
-    int pairs;
+    int64_t pos, end;                       // this team's run of (row tile - whole, slice)
+    int pairs, side, side_at, teams;
 
     __device__ Walk(const GemmArgs &a, int pair, int pairs_) : pairs(pairs_) {
         const int kept = *a.kept;
@@ -147,15 +152,27 @@ template <int FORM> struct Walk {
         tiles_n = (a.n_cols + a.bn - 1) / a.bn;
         kb = (K + BK - 1) / BK;
         n_units = tiles_m * (FORM == LSE ? (tiles_n + a.group - 1) / a.group : tiles_n);
-        whole = kb == 0 ? n_units : n_units / pairs * pairs;   // nothing to sum: zeros, tile by tile
         u = pair;
-        run(pair, pos, end);
+        if (FORM == LSE || FORM == DL) return;
+        // teams of pairs with the column tiles of one row tile side by side
+        side = tiles_n <= MOST_SIDE && tiles_n <= pairs ? tiles_n : 1;
+        teams = pairs / side;
+        side_at = pair % side;
+        n_units /= side;
+        whole = kb == 0 ? n_units : n_units / teams * teams;   // nothing to sum: zeros, tile by tile
+        u = pair / side;
+        if (u < teams) {
+            run(u, pos, end);
+        } else {   // a pair left over
+            u = n_units;
+            pos = end = 0;
+        }
     }
-    // the run of pair b
+    // the run of team b
     __device__ void run(int b, int64_t &from, int64_t &to) const {
         const int64_t all = static_cast<int64_t>(n_units - whole) * kb;
-        from = all * b / pairs;
-        to = all * (b + 1) / pairs;
+        from = all * b / teams;
+        to = all * (b + 1) / teams;
     }
     __device__ __forceinline__ bool next(const GemmArgs &a, Unit &t) {
         t.k0 = 0; t.k1 = kb; t.tiles = 1; t.group = 0; t.slot = -1;
@@ -175,7 +192,7 @@ template <int FORM> struct Walk {
         }
         int tile = u;
         if (u < whole) {
-            u += pairs;
+            u += teams;
         } else {
             if (pos >= end) return false;
             tile = whole + static_cast<int>(pos / kb);
@@ -185,16 +202,15 @@ template <int FORM> struct Walk {
             if (t.k0 > 0) t.slot = 0;
             else if (t.k1 < kb) t.slot = 1;
         }
-        // columns fastest: the pairs working at one time share G's tiles
-        t.n0 = tile % tiles_n * a.bn;
-        t.m0 = tile / tiles_n * BM;
+        t.n0 = (side > 1 ? side_at : tile % tiles_n) * a.bn;
+        t.m0 = (side > 1 ? tile : tile / tiles_n) * BM;
         return true;
     }
 };
 
-// 32 (or fewer: n) columns from c of row m of the GX or GW product to their place
+// PIECE (or fewer: n) columns from c of row m of the GX or GW product to their place
 template <int FORM, typename T>
-__device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m, int c, float (&v)[32], int n) {
+__device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m, int c, float (&v)[PIECE], int n) {
     int64_t row;
     if (FORM == GX) {
         if (m >= kept) return;
@@ -202,7 +218,7 @@ __device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m
             float *to = a.acc + static_cast<int64_t>(m) * a.acc_pitch + c;
             if (a.acc_in) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < PIECE; ++e)
                     if (e < n) v[e] += to[e];
             }
             if (a.acc_out) {
@@ -360,15 +376,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         }
     } else if (warp >= 4) {
         // --------------------------------------------------------------- epilogue
-        // warps 4..7 take the even 32-column pieces of their 32 rows, 8..11 the odd ones
+        // warps 4..7 take the even pieces of their 32 rows, 8..11 the odd ones
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const int kept = *a.kept;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        unsigned char *stage_out = smem + STAGES * STAGE_BYTES + (warp - 4) * 2 * BOX_BYTES;
+        unsigned char *stage_out = smem + STAGES * STAGE_BYTES + (warp - 4) * BOX_BYTES;
         const float scale2 = a.scale * LOG2E;
         constexpr float NEG_INF = -INFINITY;
         const float nan = __int_as_float(0x7fffffff);
-        int nblk = 0, phase = 0;
+        int phase = 0;
         bool ok = true;   // false once a wait gave up: NaN from there on
         auto release = [&](int buf) {   // this warp has read the accumulator
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -389,63 +405,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     gl = g.y;
                 }
             }
-            float mx = NEG_INF;              // LSE: running maximum and sums (two lanes of pairs)
-            float2 sum = make_float2(0.f, 0.f);
+            // LSE: running maximum and sums.  Four chains each: one alone waits for
+            // every step's result.
+            float mx = NEG_INF;
+            float2 sum[2] = {};
 
-            // 32 columns c .. c + 31 of the tile at n0, as fp32
-            auto take = [&](int n0, int c, float (&v)[32]) {
+            // columns c .. c + PIECE - 1 of the tile at n0, as fp32
+            auto take = [&](int n0, int c, float (&v)[PIECE]) {
+                float2 *p = reinterpret_cast<float2 *>(v);
                 const int left = min(a.n_cols - n0, a.bn) - c;   // valid columns
                 if (left <= 0 && FORM != DL) return;
                 if (FORM == LSE) {
-                    float2 *p = reinterpret_cast<float2 *>(v);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) p[e] = mul2(p[e], make_float2(scale2, scale2));
+                    for (int e = 0; e < PIECE / 2; ++e) p[e] = mul2(p[e], make_float2(scale2, scale2));
                     const int at = target - n0 - c;
-                    if (at >= 0 && at < min(left, 32)) {
+                    if (at >= 0 && at < min(left, PIECE)) {
                         float z = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) z = e == at ? v[e] : z;
+                        for (int e = 0; e < PIECE; ++e) z = e == at ? v[e] : z;
                         a.z_target[m] = z;
                     }
-                    if (left < 32)
+                    if (left < PIECE)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = e < left ? v[e] : NEG_INF;
-                    float up = mx;
+                        for (int e = 0; e < PIECE; ++e) v[e] = e < left ? v[e] : NEG_INF;
+                    float up[4] = {mx, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) up = fmaxf(up, v[e]);
-                    const float ref = up == NEG_INF ? 0.f : up;
+                    for (int e = 0; e < PIECE; ++e) up[e % 4] = fmaxf(up[e % 4], v[e]);
+                    const float most = fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3]));
+                    const float ref = most == NEG_INF ? 0.f : most;
                     const float keep = ex2_approx(mx - ref);
-                    sum = mul2(sum, make_float2(keep, keep));
-                    mx = up;
+                    mx = most;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int q = 0; q < 2; ++q) sum[q] = mul2(sum[q], make_float2(keep, keep));
+#pragma unroll
+                    for (int e = 0; e < PIECE / 2; ++e) {
                         const float2 x = add2(p[e], make_float2(-ref, -ref));
-                        sum = add2(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                        sum[e % 2] = add2(sum[e % 2], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                     }
                 } else if (FORM == DL) {
-                    float2 *p = reinterpret_cast<float2 *>(v);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < PIECE / 2; ++e) {
                         const float2 x = fma2(p[e], make_float2(scale2, scale2), make_float2(-lse2, -lse2));
                         p[e] = mul2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(gl, gl));
                     }
                     const int at = target - n0 - c;
-                    if (at >= 0 && at < 32)
+                    if (at >= 0 && at < PIECE)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = e == at ? v[e] - gl : v[e];
-                    if (left < 32 || m >= kept)   // zeros outside, whatever the exponential gave
+                        for (int e = 0; e < PIECE; ++e) v[e] = e == at ? v[e] - gl : v[e];
+                    if (left < PIECE || m >= kept)   // zeros outside, whatever the exponential gave
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = e < left && m < kept ? v[e] : 0.f;
+                        for (int e = 0; e < PIECE; ++e) v[e] = e < left && m < kept ? v[e] : 0.f;
                     if (!ok)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = nan;
+                        for (int e = 0; e < PIECE; ++e) v[e] = nan;
 #pragma unroll
                     for (int pl = 0; pl < (SPLIT ? 3 : 1); ++pl) {
-                        unsigned char *blk = stage_out + (nblk & 1) * BOX_BYTES;
-                        if (lane == 0) bulk_wait_read<1>();   // this block's previous store has read it
+                        if (lane == 0) bulk_wait_read<0>();   // the store before has read the block
                         __syncwarp();
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < PIECE / 8; ++q) {
                             uint4 pk;
                             uint32_t *o = reinterpret_cast<uint32_t *>(&pk);
 #pragma unroll
@@ -458,21 +476,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                                     hi -= __high2float(h2);
                                 }
                             }
-                            *reinterpret_cast<uint4 *>(blk + lane * 64 + 16 * (q ^ ((lane >> 1) & 3))) = pk;
+                            // 128-byte swizzle: 16-byte piece q of row r lies at q ^ (r & 7)
+                            *reinterpret_cast<uint4 *>(stage_out + lane * 128 + 16 * (q ^ (lane & 7))) = pk;
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_3d(&tmOut, blk, n0 + c, t.m0 + in_tile, pl);
+                            tma_store_3d(&tmOut, stage_out, n0 + c, t.m0 + in_tile, pl);
                             bulk_commit();
                         }
-                        ++nblk;
                     }
                 } else {
                     if (!ok)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = nan;
-                    const int n = min(left, 32);
+                        for (int e = 0; e < PIECE; ++e) v[e] = nan;
+                    const int n = min(left, PIECE);
                     if (t.slot < 0) {
                         store_product<FORM, T>(a, kept, m, n0 + c, v, n);
                     } else {
@@ -485,31 +503,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             for (int j = 0; j < t.tiles; ++j) {
                 const int n0 = t.n0 + j * a.bn;
                 if (SPLIT) {
-                    constexpr int PIECES = BN / 64;   // 32-column pieces of this warp
-                    float acc[PIECES][32];
+                    constexpr int PIECES = BN / PIECE / 2;   // of this warp
+                    float acc[PIECES][PIECE];
 #pragma unroll
                     for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) acc[i][e] = 0.f;
+                        for (int e = 0; e < PIECE; ++e) acc[i][e] = 0.f;
                     for (int c0 = t.k0; c0 < t.k1; c0 += SPLIT_CHUNK, ++phase) {
                         const int buf = phase & 1;
                         ok &= wait_or_abort(&accf_bar[buf], (phase >> 1) & 1, &s_abort);
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-                        for (int i = 0; i < PIECES; ++i) {
-                            const int c = (2 * i + half) * 32;
-                            if (c < a.bn) {
-                                uint32_t v[32];
-                                tmem_ld_cols<32>(tmem + lane_base + buf * BN + c, v);
+                        for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) acc[i][e] += __uint_as_float(v[e]);
+                            for (int h = 0; h < PIECE; h += 32) {
+                                const int c = (2 * i + half) * PIECE + h;
+                                if (c < a.bn) {
+                                    uint32_t v[32];
+                                    tmem_ld_cols<32>(tmem + lane_base + buf * BN + c, v);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) acc[i][h + e] += __uint_as_float(v[e]);
+                                }
                             }
-                        }
                         release(buf);
                     }
 #pragma unroll
                     for (int i = 0; i < PIECES; ++i) {
-                        const int c = (2 * i + half) * 32;
+                        const int c = (2 * i + half) * PIECE;
                         if (c < a.bn) take(n0, c, acc[i]);
                     }
                 } else if (t.k0 < t.k1) {
@@ -517,20 +537,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     ok &= wait_or_abort(&accf_bar[buf], (phase >> 1) & 1, &s_abort);
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-                    for (int c = half * 32; c < a.bn; c += 64) {
-                        uint32_t r[32];
-                        tmem_ld_cols<32>(tmem + lane_base + buf * BN + c, r);
-                        float v[32];
+                    for (int c = half * PIECE; c < a.bn; c += 2 * PIECE) {
+                        uint32_t r[PIECE];
+                        tmem_ld_cols<PIECE>(tmem + lane_base + buf * BN + c, r);
+                        float v[PIECE];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+                        for (int e = 0; e < PIECE; ++e) v[e] = __uint_as_float(r[e]);
+                        if (c + 2 * PIECE >= a.bn) release(buf);   // the last piece is in registers
                         take(n0, c, v);
                     }
-                    release(buf);
+                    if (half * PIECE >= a.bn) release(buf);
                     ++phase;
                 } else {   // nothing to sum: zeros (no kept rows)
 #pragma unroll 1
-                    for (int c = half * 32; c < a.bn; c += 64) {
-                        float v[32] = {};
+                    for (int c = half * PIECE; c < a.bn; c += 2 * PIECE) {
+                        float v[PIECE] = {};
                         take(n0, c, v);
                     }
                 }
@@ -538,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             if (FORM == LSE && m < kept) {
                 const int groups = (w.tiles_n + a.group - 1) / a.group;
                 a.part[(static_cast<int64_t>(m) * groups + t.group) * 2 + half] =
-                    make_float2(mx, ok ? sum.x + sum.y : nan);
+                    make_float2(mx, ok ? (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) : nan);
             }
         }
         if (FORM == DL && lane == 0) bulk_wait_all();   // the stores are done before the CTA exits
@@ -567,17 +588,19 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a
     dependents_may_launch();
     wait_for_prerequisites();
     const Walk<FORM> w(a, 0, pairs);
-    const int tile = w.whole + blockIdx.x;
+    const int cut = blockIdx.x / w.side, tile = w.whole + cut;   // among the row tiles of a team
     if (tile >= w.n_units) return;
+    const int side_at = blockIdx.x % w.side;
     const int kept = *a.kept, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = SPLIT_PARTS ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
-    const int m = tile / w.tiles_n * BM + row, n0 = tile % w.tiles_n * a.bn;
+    const int m = (w.side > 1 ? tile : tile / w.tiles_n) * BM + row;
+    const int n0 = (w.side > 1 ? side_at : tile % w.tiles_n) * a.bn;
     if (m >= (FORM == GX ? kept : a.M)) return;
     // the runs that hold slices of this tile: b0 .. b1
     const int64_t all = static_cast<int64_t>(w.n_units - w.whole) * w.kb;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * w.kb, stop = first + w.kb;
+    const int64_t first = static_cast<int64_t>(cut) * w.kb, stop = first + w.kb;
     auto run_of = [&](int64_t slice) {   // the run that holds a slice
-        int b = static_cast<int>(slice * pairs / all);
+        int b = static_cast<int>(slice * w.teams / all);
         int64_t from, to;
         for (w.run(b, from, to); slice < from; w.run(--b, from, to)) {}
         for (; slice >= to; w.run(++b, from, to)) {}
@@ -585,12 +608,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a
     };
     const int b0 = run_of(first), b1 = run_of(stop - 1);
     if (b0 == b1) return;   // one run has it whole
-    const bool dense = all >= pairs;   // no run is empty
+    const bool dense = all >= w.teams;   // no run is empty
     const int c = lane * 8;
     float v[8] = {};
     if (c < a.bn) {
-        const int64_t step = static_cast<int64_t>(2) * BM * a.bn;
-        const float *p = a.parts + b0 * step + static_cast<int64_t>(row) * a.bn + c;
+        const int64_t step = static_cast<int64_t>(2) * BM * a.bn * w.side;   // to the next team's
+        const float *p = a.parts + b0 * step + (static_cast<int64_t>(side_at) * 2 * BM + row) * a.bn + c;
         const int q0 = SPLIT_PARTS ? warp : 0, dq = SPLIT_PARTS ? JOIN_WARPS : 1;
 #pragma unroll 4
         for (int q = q0; q <= b1 - b0; q += dq) {
@@ -929,7 +952,7 @@ cudaError_t gemm(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorM
     if constexpr (FORM == GX || FORM == GW) {
         if (e == cudaSuccess && pairs > 1) {
             // tiles that may be cut: those left over by whole waves of any number of kept rows
-            const int64_t cut = tiles < pairs ? tiles : pairs - 1;
+            const int64_t cut = tiles < pairs ? tiles : pairs;
             const bool few = cut * 8 <= pairs;   // eight parts each and more
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(cut), few ? BM : BM / JOIN_WARPS);
@@ -1027,7 +1050,7 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
         !make_map_planes(&wn, w, p.pitch, c.V, p.planes, 64, BK, true) ||
         !make_map_planes(&gn, dl, p.piece, p.rows_pad, p.planes, 64, BK, true) ||
         !make_map_planes(&xn, x, p.pitch, p.rows_pad, p.planes, 64, BK, true) ||
-        !make_map_planes(&gs, dl, p.piece, p.rows_pad, p.planes, BOX, BOX, false))
+        !make_map_planes(&gs, dl, p.piece, p.rows_pad, p.planes, PIECE, BOX_ROWS, true))
         return NRNN_ERR_CUDA;
     GemmArgs a{};
     a.kept = reinterpret_cast<int *>(c.ws + p.kept);
