@@ -876,15 +876,16 @@ struct Plan {
 // bytes the piece of G may take
 constexpr int64_t PIECE_BYTES = 1ll << 30;
 
-// Columns of the forward's tiles.  With enough tiles the widest; with few row tiles
-// the width that leaves the busiest pair the fewest columns (50021 columns on 76
-// pairs: three tiles of 256 where eleven of 64 are 704 columns).
+// Columns of the forward's tiles.  With enough tiles the widest; with few, the width
+// that leaves the busiest pair the least to do: a tile costs its columns and, for
+// the rows of x that it reads again, about 64 more (4 rows over 50021 x 1024: three
+// tiles of 224 a pair instead of three of 256).
 int forward_columns(int64_t tiles_m, int64_t V) {
     if (tiles_m * ceil_div(V, BN) >= 8 * PAIRS) return BN;
     int best = BN;
     int64_t least = INT64_MAX;
     for (int bn = BN; bn >= 64; bn -= 32) {
-        const int64_t load = ceil_div(tiles_m * ceil_div(V, bn), PAIRS) * bn;
+        const int64_t load = ceil_div(tiles_m * ceil_div(V, bn), PAIRS) * (bn + 64);
         if (load < least) {
             least = load;
             best = bn;
