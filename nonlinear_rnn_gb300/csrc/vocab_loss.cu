@@ -675,18 +675,18 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a
 }
 
 // ------------------------------------------------------------------ the rows
-// Numbers the rows whose target takes part, in order: row[m] = {row, target}.
-// One CTA; each round takes 1024 x ROUND targets, 32 x ROUND consecutive ones a warp.
-constexpr int KEPT_THREADS = 1024, ROUND = 16;
+// Numbers the rows whose target takes part, in order: row[m] = {row, target}, by one
+// CTA; each round takes THREADS x ROUND targets, 32 x ROUND consecutive ones a warp.
+// Returns their number.
+constexpr int KEPT_THREADS = 1024, GATHER_THREADS = 256, ROUND = 16;
 
-template <typename Id>
-__global__ void __launch_bounds__(KEPT_THREADS)
-    k_kept_rows(const void *targets, int n, int64_t V, int64_t ignore, int2 *row, int *kept) {
-    __shared__ int warp_sum[KEPT_THREADS / 32];
-    dependents_may_launch();
+template <int THREADS, typename Id>
+__device__ __forceinline__ int number_rows(const void *targets, int n, int64_t V, int64_t ignore, int2 *row) {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ int warp_sum[WARPS];
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     int base = 0;
-    for (int64_t r0 = 0; r0 < n; r0 += KEPT_THREADS * ROUND) {
+    for (int64_t r0 = 0; r0 < n; r0 += THREADS * ROUND) {
         int64_t id[ROUND];
         unsigned vote[ROUND];
         int mine = 0;
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(KEPT_THREADS)
         }
         if (lane == 0) warp_sum[w] = mine;
         __syncthreads();
-        int all = warp_sum[lane];
+        int all = lane < WARPS ? warp_sum[lane] : 0;
         int at = lane < w ? all : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -719,17 +719,29 @@ __global__ void __launch_bounds__(KEPT_THREADS)
         base += all;
         __syncthreads();
     }
-    if (t == 0) *kept = base;
+    return base;
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(KEPT_THREADS)
+    k_kept_rows(const void *targets, int n, int64_t V, int64_t ignore, int2 *row, int *kept) {
+    dependents_may_launch();
+    const int all = number_rows<KEPT_THREADS, Id>(targets, n, V, ignore, row);
+    if (threadIdx.x == 0) *kept = all;
 }
 
 // Copies the kept rows of x to (planes, rows_pad, pitch) bf16, zeros after them
 // up to a multiple of 256 rows and beyond column d; with lse given, the rows'
 // constants of the DL form.  Then, with gx given, clears the rows of gx that
-// take no part (a target out of range gives NaN).
+// take no part (a target out of range gives NaN).  FEW: every CTA numbers the rows
+// for itself (the first one for the kernels that follow too), which is sooner done
+// than a launch before this one.
+constexpr int FEW_ROWS = GATHER_THREADS * ROUND;
+
 struct GatherArgs {
     const void *x;
-    const int2 *row;
-    const int *kept;
+    int2 *row;
+    int *kept;
     __nv_bfloat16 *out;
     int64_t rows_pad;
     int d, pitch;
@@ -776,18 +788,30 @@ template <typename T> __device__ __forceinline__ bool wide_rows(const void *src,
     return d % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
 }
 
-template <typename T, typename Id>
-__global__ void __launch_bounds__(256) k_gather_rows(const GatherArgs a) {
+template <typename T, typename Id, bool FEW>
+__global__ void __launch_bounds__(GATHER_THREADS) k_gather_rows(const GatherArgs a) {
+    __shared__ int2 few_rows[FEW ? FEW_ROWS : 1];
     dependents_may_launch();
     wait_for_prerequisites();
     const int lane = threadIdx.x & 31;
-    const int kept = *a.kept;
+    const int2 *rows = a.row;
+    int kept;
+    if (FEW) {
+        kept = number_rows<GATHER_THREADS, Id>(a.targets, a.n, a.V, a.ignore, few_rows);
+        rows = few_rows;
+        if (blockIdx.x == 0) {
+            for (int i = threadIdx.x; i < kept; i += GATHER_THREADS) a.row[i] = few_rows[i];
+            if (threadIdx.x == 0) *a.kept = kept;
+        }
+    } else {
+        kept = *a.kept;
+    }
     const bool wide = wide_rows<T>(a.x, a.d);
     const int padded = (kept + BM - 1) / BM * BM;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t m = blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows_pad; m += warps) {
         if (m < padded) {
-            const int src = m < kept ? a.row[m].x : -1;
+            const int src = m < kept ? rows[m].x : -1;
             copy_row<T>(src >= 0 ? static_cast<const T *>(a.x) + static_cast<int64_t>(src) * a.d : nullptr,
                         a.out + m * a.pitch, a.rows_pad * a.pitch, a.d, a.pitch, lane, wide);
             if (a.grad != nullptr && m < kept && lane == 0)
@@ -986,8 +1010,6 @@ cudaError_t lay_out(const Call &c, const Plan &p, const float *lse, const float 
                     const void **w_out) {
     int *kept = reinterpret_cast<int *>(c.ws + p.kept);
     int2 *row = reinterpret_cast<int2 *>(c.ws + p.row);
-    k_kept_rows<Id><<<1, KEPT_THREADS, 0, c.stream>>>(c.targets, static_cast<int>(c.n), c.V, c.ignore,
-                                                      row, kept);
     GatherArgs g{};
     g.x = c.x; g.row = row; g.kept = kept;
     g.out = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.x);
@@ -995,11 +1017,18 @@ cudaError_t lay_out(const Call &c, const Plan &p, const float *lse, const float 
     g.lse = lse; g.gl = gl; g.scale = c.scale;
     g.grad = lse != nullptr ? reinterpret_cast<float2 *>(c.ws + p.grad) : nullptr;
     g.gx = gx; g.targets = c.targets; g.V = c.V; g.ignore = c.ignore; g.n = static_cast<int>(c.n);
-    const int64_t blocks = p.rows_pad / 8;
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess)
-        e = launch_dependent(k_gather_rows<T, Id>, static_cast<unsigned>(blocks < 4864 ? blocks : 4864), 256,
-                             0, c.stream, g);
+    const int64_t want = p.rows_pad / (GATHER_THREADS / 32);
+    const unsigned blocks = static_cast<unsigned>(want < 4864 ? want : 4864);
+    cudaError_t e;
+    if (c.n <= FEW_ROWS) {
+        k_gather_rows<T, Id, true><<<blocks, GATHER_THREADS, 0, c.stream>>>(g);
+        e = cudaGetLastError();
+    } else {
+        k_kept_rows<Id><<<1, KEPT_THREADS, 0, c.stream>>>(c.targets, static_cast<int>(c.n), c.V, c.ignore, row, kept);
+        e = cudaGetLastError();
+        if (e == cudaSuccess)
+            e = launch_dependent(k_gather_rows<T, Id, false>, blocks, GATHER_THREADS, 0, c.stream, g);
+    }
     *w_out = c.W;
     if (e == cudaSuccess && p.copy_w) {
         __nv_bfloat16 *w = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.w);
