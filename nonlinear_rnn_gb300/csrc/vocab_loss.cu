@@ -839,6 +839,103 @@ __global__ void __launch_bounds__(256)
         copy_row<T>(W + v * d, out + v * pitch, V * pitch, d, pitch, threadIdx.x & 31, wide);
 }
 
+// ------------------------------------------------------------ few rows, fp32
+// lse of at most FEW_MOST fp32 rows on the fp32 cores: writing W's planes and reading
+// them back would be four times the bytes that W has (33 rows over 47579 x 552: 126
+// us).  A warp takes FEW_V rows of W at a time, 128 bytes a lane apart, against every
+// row of x from shared memory, so a value of x that is read serves FEW_V products.
+// Bound by reading W up to about 16 rows.
+constexpr int FEW_MOST = 16, FEW_WARPS = 8;
+constexpr int few_v(int n) { return n > 4 ? 4 : 8; }   // rows of W of a warp: what the registers allow
+constexpr int FEW_X_BYTES = 160 * 1024;   // of the rows of x in shared memory
+
+template <int N, int VEC, typename Id>
+__global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
+    k_few_rows(const float *__restrict__ x, const float *__restrict__ W, const void *targets, int n,
+               int d, int64_t V, int64_t ignore, float scale2, float2 *part, float *z_target, int2 *row,
+               int *kept) {
+    extern __shared__ __align__(16) float few_x[];   // [N][pitch], zeros past n and d
+    __shared__ int2 rows[FEW_MOST];
+    constexpr float NEG_INF = -INFINITY;
+    constexpr int FEW_V = few_v(N);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pitch = (d + 32 * VEC - 1) / (32 * VEC) * (32 * VEC);
+    dependents_may_launch();
+    const int live = number_rows<FEW_WARPS * 32, Id>(targets, n, V, ignore, rows);
+    if (blockIdx.x == 0) {
+        if (static_cast<int>(threadIdx.x) < live) row[threadIdx.x] = rows[threadIdx.x];
+        if (threadIdx.x == 0) *kept = live;
+    }
+    for (int i = threadIdx.x; i < N * pitch; i += FEW_WARPS * 32) {
+        const int r = i / pitch, c = i - r * pitch;
+        few_x[i] = r < live && c < d ? x[static_cast<int64_t>(rows[r].x) * d + c] : 0.f;
+    }
+    __syncthreads();
+    // lane r < N: the reference and sum of row r over this warp's rows of W
+    float ref = NEG_INF, sum = 0.f;
+    const int my_target = lane < live ? rows[lane].y : -1;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * FEW_WARPS * FEW_V;
+    for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * FEW_WARPS + warp) * FEW_V; v0 < V; v0 += step) {
+        float acc[FEW_V][N];
+#pragma unroll
+        for (int q = 0; q < FEW_V; ++q)
+#pragma unroll
+            for (int r = 0; r < N; ++r) acc[q][r] = 0.f;
+#pragma unroll 2
+        for (int c = lane * VEC; c < pitch; c += 32 * VEC) {
+            float w[FEW_V][VEC];
+#pragma unroll
+            for (int q = 0; q < FEW_V; ++q) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) w[q][e] = 0.f;
+                if (c < d && v0 + q < V) load_f32<float, VEC>(W + (v0 + q) * d + c, w[q]);
+            }
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+                float xv[VEC];
+                load_f32<float, VEC>(few_x + r * pitch + c, xv);
+#pragma unroll
+                for (int q = 0; q < FEW_V; ++q)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[q][r] = fmaf(w[q][e], xv[e], acc[q][r]);
+            }
+        }
+        // the lanes' sums: halves are exchanged and added, until lane l has the sums of
+        // row r = l / (32 / N) (all its lanes the same)
+#pragma unroll
+        for (int q = 0; q < FEW_V; ++q) {
+            float z[N];
+#pragma unroll
+            for (int r = 0; r < N; ++r) z[r] = acc[q][r];
+#pragma unroll
+            for (int o = 16, have = N; o > 0; o >>= 1) {
+                if (have > 1) {
+                    have /= 2;
+                    const bool upper = lane & o;
+#pragma unroll
+                    for (int r = 0; r < N / 2; ++r) {
+                        if (r >= have) break;
+                        const float give = upper ? z[r] : z[r + have], keep = upper ? z[r + have] : z[r];
+                        z[r] = keep + __shfl_xor_sync(FULL_MASK, give, o);
+                    }
+                } else {
+                    z[0] += __shfl_xor_sync(FULL_MASK, z[0], o);
+                }
+            }
+            // row r's value to lane r
+            const float mine = __shfl_sync(FULL_MASK, z[0], (lane % N) * (32 / N)) * scale2;
+            if (lane < N && v0 + q < V) {
+                if (my_target == v0 + q) z_target[lane] = mine;
+                const float most = fmaxf(ref, mine);
+                const float at = most == NEG_INF ? 0.f : most;
+                sum = sum * ex2_approx(ref - at) + ex2_approx(mine - at);
+                ref = most;
+            }
+        }
+    }
+    if (lane < live) part[static_cast<int64_t>(lane) * (gridDim.x * FEW_WARPS) + blockIdx.x * FEW_WARPS + warp] = make_float2(ref, sum);
+}
+
 // Joins the row's partial maxima and sums; a warp per row.  Rows that take no
 // part: zeros (a target out of range: NaN).
 template <typename Id>
@@ -897,6 +994,9 @@ struct Plan {
     size_t kept, row, x, w, part, z, grad, dl, parts, acc, total;
 };
 
+constexpr int FEW_CTAS = 4 * PAIRS;
+int few_size(int64_t n) { return n <= 1 ? 1 : n <= 4 ? 4 : FEW_MOST; }   // rows it is built for
+
 // bytes the piece of G may take
 constexpr int64_t PIECE_BYTES = 1ll << 30;
 
@@ -945,7 +1045,8 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
     p.x = take(sizeof(__nv_bfloat16) * p.planes * p.rows_pad * p.pitch);
     p.w = take(p.copy_w ? sizeof(__nv_bfloat16) * p.planes * V * p.pitch : 0);
     if (!backward) {
-        p.part = take(sizeof(float2) * 2 * n * p.groups);
+        const int64_t parts = 2 * p.groups > FEW_CTAS * FEW_WARPS || n > FEW_MOST ? 2 * p.groups : FEW_CTAS * FEW_WARPS;
+        p.part = take(sizeof(float2) * n * parts);
         p.z = take(sizeof(float) * n);
     } else {
         p.grad = take(sizeof(float2) * n);
@@ -1040,9 +1141,57 @@ cudaError_t lay_out(const Call &c, const Plan &p, const float *lse, const float 
     return e;
 }
 
+// loss and lse from `parts` partial sums a row
+template <typename Id> int join_loss(const Call &c, const Plan &p, int parts, float *loss, float *lse) {
+    return launch_dependent(k_loss_join<Id>, static_cast<unsigned>(ceil_div(c.n, 8)), 256, 0, c.stream,
+                            reinterpret_cast<const float2 *>(c.ws + p.part), parts,
+                            reinterpret_cast<const float *>(c.ws + p.z),
+                            reinterpret_cast<const int2 *>(c.ws + p.row),
+                            reinterpret_cast<const int *>(c.ws + p.kept), c.targets,
+                            static_cast<int>(c.n), c.V, c.ignore, loss, lse) == cudaSuccess
+               ? NRNN_OK : NRNN_ERR_CUDA;
+}
+
+// fp32 rows that the few-rows form takes: few, and fit in shared memory
+bool few_rows(int64_t n, int64_t d, int dtype) {
+    return dtype == NRNN_F32 && n <= FEW_MOST && few_size(n) * (d + 127) * 4 <= FEW_X_BYTES;
+}
+
+template <int N, int VEC, typename Id>
+cudaError_t launch_few(const Call &c, const Plan &p) {
+    constexpr int most = FEW_X_BYTES;
+    static std::atomic<unsigned long long> configured{0};
+    cudaError_t e = once_per_device(configured, [](int) {
+        return cudaFuncSetAttribute(k_few_rows<N, VEC, Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    });
+    if (e != cudaSuccess) return e;
+    const size_t smem = sizeof(float) * N * (ceil_div(c.d, 32 * VEC) * 32 * VEC);
+    k_few_rows<N, VEC, Id><<<FEW_CTAS, FEW_WARPS * 32, smem, c.stream>>>(
+        static_cast<const float *>(c.x), static_cast<const float *>(c.W), c.targets, static_cast<int>(c.n),
+        static_cast<int>(c.d), c.V, c.ignore, c.scale * LOG2E, reinterpret_cast<float2 *>(c.ws + p.part),
+        reinterpret_cast<float *>(c.ws + p.z), reinterpret_cast<int2 *>(c.ws + p.row),
+        reinterpret_cast<int *>(c.ws + p.kept));
+    return cudaGetLastError();
+}
+
+template <typename Id> cudaError_t launch_few(const Call &c, const Plan &p) {
+    const bool wide = c.d % 4 == 0 && (reinterpret_cast<uintptr_t>(c.W) & 15) == 0;
+    switch (few_size(c.n)) {
+        case 1: return wide ? launch_few<1, 4, Id>(c, p) : launch_few<1, 1, Id>(c, p);
+        case 4: return wide ? launch_few<4, 4, Id>(c, p) : launch_few<4, 1, Id>(c, p);
+        default: return wide ? launch_few<16, 4, Id>(c, p) : launch_few<16, 1, Id>(c, p);
+    }
+}
+
 template <typename T, typename Id>
 int forward(const Call &c, float *loss, float *lse) {
     const Plan p = plan_for(c.n, c.d, c.V, c.dtype, reinterpret_cast<uintptr_t>(c.W) % 16 == 0, false);
+    if constexpr (sizeof(T) == 4) {
+        if (few_rows(c.n, c.d, c.dtype)) {
+            if (launch_few<Id>(c, p) != cudaSuccess) return NRNN_ERR_CUDA;
+            return join_loss<Id>(c, p, FEW_CTAS * FEW_WARPS, loss, lse);
+        }
+    }
     const void *w;
     if (lay_out<T, Id>(c, p, nullptr, nullptr, nullptr, &w) != cudaSuccess) return NRNN_ERR_CUDA;
     CUtensorMap tmA, tmB;
@@ -1060,10 +1209,7 @@ int forward(const Call &c, float *loss, float *lse) {
     a.z_target = reinterpret_cast<float *>(c.ws + p.z);
     if (gemm<LSE, T>(tmA, tmB, tmA, a, ceil_div(c.n, BM) * p.groups, 0, c.stream) != cudaSuccess)
         return NRNN_ERR_CUDA;
-    return launch_dependent(k_loss_join<Id>, static_cast<unsigned>(ceil_div(c.n, 8)), 256, 0, c.stream, a.part,
-                            2 * p.groups, a.z_target, a.row, a.kept, c.targets, static_cast<int>(c.n), c.V,
-                            c.ignore, loss, lse) == cudaSuccess
-               ? NRNN_OK : NRNN_ERR_CUDA;
+    return join_loss<Id>(c, p, 2 * p.groups, loss, lse);
 }
 
 template <typename T, typename Id>

@@ -319,11 +319,30 @@ def loss64(x, W, target, gl, c):
 @pytest.mark.parametrize("n,V,d", LOSS)
 @pytest.mark.parametrize("ignored,c", [(0.0, 1.0), (0.3, 0.6)])
 def test_vocab_loss(n, V, d, t, ignored, c):
+    check_vocab_loss(n, V, d, t, ignored, c)
+
+
+# few rows (4, 16 and 17: the edges of the fp32 few-rows form), rows too wide for it,
+# more column tiles than pairs work side by side, a gradient cut into many parts,
+# far fewer kept rows than rows, a vocabulary below one tile
+MORE = [(4, 900, 96, 0.0), (16, 900, 515, 0.0), (16, 700, 1024, 0.4), (17, 900, 96, 0.0), (16, 300, 2600, 0.0),
+        (200, 600, 2600, 0.1), (100, 50021, 512, 0.0), (3000, 2500, 320, 0.98), (5000, 40, 128, 0.5),
+        (260, 20000, 1000, 0.0)]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("n,V,d,ignored", MORE)
+def test_vocab_loss_more_shapes(n, V, d, ignored, t):
+    check_vocab_loss(n, V, d, t, ignored, 0.8)
+
+
+def check_vocab_loss(n, V, d, t, ignored, c):
     g, x, W, target, gl = loss_inputs(n, V, d, t, ignored, 9)
     idt = torch.int32 if n % 2 else torch.int64
     loss, lse = nr.vocab_loss(x, W, target.to(idt), logit_scale=c)
     kept, X, lse_ref, loss_ref, G, zmag = loss64(x, W, target, gl, c)
-    # logits: up to 64 accumulation steps of 2 u; then sums of positive terms
+    # logits: up to d / 16 accumulation steps of 2 u (d <= 2600: 2^-15.6, here with
+    # errors that do not all lie one way 2^-17); then sums of positive terms
     tz = 2.0 ** -17 * zmag + 2.0 ** -20 * (1 + lse_ref.abs())
     check(lse, lse_ref, tz, "lse")
     check(loss, loss_ref, 2 * tz, "loss")
