@@ -21,6 +21,11 @@
 // gu in; gx, gh, ggate out).  A row is read once and stays in registers; the
 // statistics are recomputed in the backward from the row it reads anyway
 // instead of being stored.  All arithmetic and all sums are fp32.
+//
+// Measured: forward of 262144 x 1024 bf16 417 us (6.4 TB/s, 0.96 of a plain copy),
+// backward of 65536 x 1024 bf16 188 us (5.7 TB/s), of 32768 x 256 fp32 57 us with
+// the join (4.7 TB/s), of 65537 x 515 bf16 without a gate 164 us (2.5 TB/s: 66 pieces
+// on 96 threads, and the rows' ends).
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
 #include "nrnn_internal.h"

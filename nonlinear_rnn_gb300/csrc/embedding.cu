@@ -8,7 +8,12 @@
 //
 // The gradient must not depend on the order in which threads run, so it uses no
 // floating-point atomics: the (id, position) pairs are put in order by a stable
-// radix sort, and the sums follow the sorted order in fixed groups of 32.
+// radix sort, and the sums follow the sorted order in fixed groups.
+//
+// Measured: the lookup of 262144 fp32 rows of 512 takes 103 us (6.0 TB/s of the
+// distinct rows and the output).  The gradient of 262144 bf16 rows of 1024 with ids
+// as frequent as words, V = 65536, takes 167 us: sorting 40 us, beside which gW is
+// cleared, sums 107 us (5.6 TB/s), joining 17 us (a chain of dependent reads).
 #include <initializer_list>
 
 #include <cooperative_groups.h>
@@ -32,7 +37,8 @@ template <typename Id> __device__ __forceinline__ int64_t id_at(const void *ids,
 }
 
 // ------------------------------------------------------------------ the lookup
-// A warp copies one slab of GROUP_ROWS rows, all loads before the first store.
+// A warp copies one slab of GROUP_ROWS rows, all loads before the first store: with
+// one row a warp the loads in flight would not cover the memory's latency.
 // An id outside [0, V) that is not the padding id gives a row of NaN.
 template <typename T, int VEC, typename Id>
 __global__ void __launch_bounds__(EMBED_THREADS)
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(SORT_THREADS) k_sort_place(const SortArgs a) {
 // Up to SORT_CLUSTER tiles: one cluster with a tile per CTA does every pass in
 // one launch.  A pass's counts and pairs are exchanged through distributed shared
 // memory; only the sorted pairs go to global memory.  (30001 ids: two launches a
-// pass took 23 us.)
+// pass took 23 us; here 13.)
 constexpr int SORT_CLUSTER = 16;   // above the portable 8: allowed by attribute
 
 struct ClusterSortShared {
@@ -356,10 +362,14 @@ __global__ void __launch_bounds__(SORT_THREADS) k_sort_cluster(SortArgs a, int p
         c.total[t] = sort_scan_warps(s);
         cluster.sync();
         uint32_t before = 0, all = 0;
-        for (int o = 0; o < a.ctas; ++o) {
-            const uint32_t v = *cluster.map_shared_rank(c.total + t, o);
-            before += o < static_cast<int>(r) ? v : 0;
-            all += v;
+        uint32_t theirs[SORT_CLUSTER];   // all remote reads in flight together
+#pragma unroll
+        for (int o = 0; o < SORT_CLUSTER; ++o)
+            theirs[o] = o < a.ctas ? *cluster.map_shared_rank(c.total + t, o) : 0;
+#pragma unroll
+        for (int o = 0; o < SORT_CLUSTER; ++o) {
+            before += o < static_cast<int>(r) ? theirs[o] : 0;
+            all += theirs[o];
         }
         const uint32_t base = sort_scan_digits(s, all) + before;
         s.base[t] = base;

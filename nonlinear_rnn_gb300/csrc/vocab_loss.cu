@@ -35,12 +35,20 @@
 // number there, so ignored rows cost nothing and whatever they hold (infinities,
 // NaN) reaches no output.
 //
-// fp32 inputs are written as three bf16 planes, v = hi + mid + lo exactly up to
-// 2^-24, and a product is the six plane products down to 2^-16 relative:
+// fp32 inputs are written as three bf16 planes, v = hi + mid + lo up to 2^-24, and a
+// product is the six plane products above 2^-24 relative, smallest first:
 // (lo,hi) (mid,mid) (hi,lo) (mid,hi) (hi,mid) (hi,hi).  The tensor cores'
 // accumulation rounds coarser than fp32 addition does, so an accumulator takes
 // at most 512 elements of the inner dimension before the epilogue adds it to
 // fp32 registers.
+//
+// Measured: 16384 rows over 65536 x 1024 bf16 with gradient 5.2 to 5.6 ms (1.57 to
+// 1.68 PFLOP/s; cuBLAS runs at 1.75 when kept up: the power limit holds the clocks at
+// 1.7 GHz); 4096 over 32768 x 512 bf16 0.43 ms (1.2 PFLOP/s: a tile's 8 slices hide
+// less of its epilogue), 3001 over 10007 x 250 fp32 0.29 ms, 4 rows over 50021 x 1024
+// bf16, forward only, 35 us (W once in 23 us).  Without its epilogue the forward's
+// main loop takes 0.96 of the time at d = 1024, 0.94 at 512 and 0.55 at 64, where the
+// exponentials bind.
 //
 // Every wait is bounded.  One that gives up sets g_vocab_error and the CTA's
 // abort flag, which ends the other roles' waits too: the producer and the issuer

@@ -47,3 +47,26 @@ def test_training_lowers_the_loss():
     assert all(math.isfinite(v) for v in losses)
     assert losses[0] > 0.9 * math.log(300)
     assert sum(losses[-5:]) / 5 < 0.6 * losses[0]
+
+
+def test_readme_usage_of_the_language_operators():
+    """The README's second example at a small size."""
+    import nonlinear_rnn_gb300 as nr
+    d, V = 64, 200
+    W_x = (torch.randn(3 * d, d, device="cuda") / d ** 0.5).to(torch.bfloat16)
+    params = torch.rand(6, d) * 2 - 1
+    E = torch.randn(V, d, device="cuda", dtype=torch.bfloat16) / d ** 0.5
+    tokens = torch.randint(0, V, (2, 48), device="cuda")
+    targets = tokens.roll(-1, 1)
+    x0 = nr.embedding(tokens, E, scale=8.0)
+    _, u = nr.block_norm(x0)
+    H, _ = nr.newton_forward(nr.input_projection(u, W_x), params, check=False)
+    x1, v = nr.block_norm(x0, h=H)
+    loss, lse = nr.vocab_loss(v, E, targets)
+    gv, gE = nr.vocab_loss_backward(v, E, targets, lse, torch.full_like(loss, 1 / loss.numel()))
+    g = nr.block_norm_backward(x1, h=H, g_u=gv)
+    before = gE.clone()
+    nr.embedding_backward(tokens, g.gx, V, scale=8.0, out=gE, accumulate=True)
+    assert loss.shape == (2, 48) and gv.shape == v.shape and gE.shape == E.shape
+    assert all(bool(t.isfinite().all()) for t in (loss, gv, gE, g.gx, g.gh))
+    assert not torch.equal(before, gE)
