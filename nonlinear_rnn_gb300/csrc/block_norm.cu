@@ -310,7 +310,10 @@ __device__ __forceinline__ void team_sums(float (&v)[N], float *buf, int tpr) {
 
 // resident threads an SM that the kernels' registers and shared memory leave room for
 constexpr int FWD_THREADS_PER_SM = 640;
-constexpr int bwd_threads_per_sm(int vec) { return vec == 8 ? 640 : 512; }   // fp32 rows stage twice the bytes
+// backward: by a thread's columns; fp32 rows (vec = 4) stage twice the bytes
+constexpr int bwd_threads_per_sm(int vec, int columns) {
+    return columns > 8 ? 384 : vec == 8 ? 640 : 512;
+}
 constexpr int resident(int threads, int per_sm) { return per_sm / threads > 0 ? per_sm / threads : 1; }
 
 // ------------------------------------------------------------------- forward
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THRE
 
 // ------------------------------------------------------------------ backward
 template <typename L, int TPR>
-__global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THREADS, bwd_threads_per_sm(L::VEC)))
+__global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THREADS, bwd_threads_per_sm(L::VEC, L::N)))
     k_norm_backward(const NormArgs a) {
     __shared__ float red[2][4 * 32];   // three sums, then one; two rows in turn
     extern __shared__ float4 norm_smem[];
@@ -572,11 +575,8 @@ cudaError_t launch_norm(K kernel, NormArgs a, int ctas, int tpr, cudaStream_t s)
     return cudaGetLastError();
 }
 
-// Pieces a thread: two forward, 8 columns backward (its sums take the registers of
-// the others).  A bf16 row that two pieces a thread would leave half empty takes
+// Pieces a thread forward: two.  A bf16 row that two pieces a thread would leave half empty takes
 // one forward (65537 x 515: 66 pieces in 3 warps instead of 128 in 2).
-template <typename T, int VEC> constexpr int bwd_pieces() { return 8 / VEC; }
-
 template <typename T, int VEC, bool EDGE, int PIECES>
 cudaError_t forward_as(const NormArgs &a, cudaStream_t s) {
     using L = Layout<T, VEC, PIECES, EDGE>;
@@ -595,10 +595,25 @@ template <typename T, int VEC, bool EDGE> cudaError_t forward_for(const NormArgs
     if constexpr (VEC > 1) return forward_as<T, VEC, EDGE, 2>(a, s);
 }
 
+// Backward: 8 columns a thread; a bf16 row of 33 to 64 pieces takes a warp with two
+// pieces a thread instead of two warps, without barriers and with the work that does
+// not grow with the columns done once (65536 x 512 127 -> 104 us; with three pieces
+// the registers leave too few warps: 65537 x 515 201 -> 232 us).
+struct BwdShape { int pieces, tpr; };
+BwdShape bwd_shape(int d, int vec) {
+    if (vec == 8 && team_size(d, vec, 1) > 32 && team_size(d, vec, 2) <= 32) return {2, team_size(d, vec, 2)};
+    return {8 / vec, team_size(d, vec, 8 / vec)};
+}
+
 template <typename T, int VEC, bool EDGE>
 cudaError_t backward_for(const NormArgs &a, int ctas, cudaStream_t s) {
-    using L = Layout<T, VEC, bwd_pieces<T, VEC>(), EDGE>;
-    const int tpr = team_size(a.d, VEC, L::PIECES);
+    const BwdShape shape = bwd_shape(a.d, VEC);
+    const int tpr = shape.tpr;
+    if constexpr (VEC == 8) {
+        using L2 = Layout<T, VEC, 2, EDGE>;
+        if (shape.pieces == 2) return launch_norm<L2, 32, 5>(k_norm_backward<L2, 32>, a, ctas, tpr, s);
+    }
+    using L = Layout<T, VEC, 8 / VEC, EDGE>;
     if (tpr <= 32) return launch_norm<L, 32, 5>(k_norm_backward<L, 32>, a, ctas, tpr, s);
     if (tpr <= 128) return launch_norm<L, 128, 5>(k_norm_backward<L, 128>, a, ctas, tpr, s);
     if (tpr <= 512) return launch_norm<L, 512, 5>(k_norm_backward<L, 512>, a, ctas, tpr, s);
@@ -614,8 +629,11 @@ cudaError_t backward_for(const NormArgs &a, int ctas, cudaStream_t s) {
                              : (d) % (vec) == 0  ? f<float, 4, false>(__VA_ARGS__)         \
                                                  : f<float, 4, true>(__VA_ARGS__)))
 
-// CTAs of a backward launch: the most that any access width takes
-int backward_ctas(int64_t rows, int d, int vec) { return cta_count(rows, team_size(d, vec, 8 / vec), bwd_threads_per_sm(vec)); }
+// CTAs of a backward launch
+int backward_ctas(int64_t rows, int d, int vec) {
+    const BwdShape shape = bwd_shape(d, vec);
+    return cta_count(rows, shape.tpr, bwd_threads_per_sm(vec, shape.pieces * vec));
+}
 
 int check_norm(int dtype, int64_t rows, int64_t d, float eps) {
     if (dtype != NRNN_F32 && dtype != NRNN_BF16) return NRNN_ERR_INVALID_ARG;

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(SORT_THREADS) k_sort_place(const SortArgs a) {
 // Up to SORT_CLUSTER tiles: one cluster with a tile per CTA does every pass in
 // one launch.  A pass's counts and pairs are exchanged through distributed shared
 // memory; only the sorted pairs go to global memory.  (30001 ids: two launches a
-// pass took 23 us; here 13.)
+// pass took 23 us; here 15.)
 constexpr int SORT_CLUSTER = 16;   // above the portable 8: allowed by attribute
 
 struct ClusterSortShared {
