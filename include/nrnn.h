@@ -30,8 +30,9 @@
  *   - params: device, fp32, shape (6, d_h): rows a_z, a_r, a_c, b_z, b_r, b_c.
  *   - stream: a cudaStream_t (NULL = legacy default stream).  Calls are
  *     asynchronous on that stream unless stated otherwise.  The Newton
- *     kernels are launched with programmatic stream serialization and signal
- *     their dependents early: a kernel the caller launches after them with
+ *     kernels and those of the language-model operators are launched with
+ *     programmatic stream serialization and signal their dependents early: a
+ *     kernel the caller launches after them with
  *     that launch attribute must execute griddepcontrol.wait (as programmatic
  *     dependent launch requires) before it reads their outputs.  Ordinary
  *     launches, copies and events after a call are ordered as usual.

@@ -22,9 +22,9 @@
 // statistics are recomputed in the backward from the row it reads anyway
 // instead of being stored.  All arithmetic and all sums are fp32.
 //
-// Measured: forward of 262144 x 1024 bf16 417 us (6.4 TB/s, 0.96 of a plain copy),
-// backward of 65536 x 1024 bf16 188 us (5.7 TB/s), of 32768 x 256 fp32 57 us with
-// the join (4.7 TB/s), of 65537 x 515 bf16 without a gate 164 us (2.5 TB/s: 66 pieces
+// Measured: forward of 262144 x 1024 bf16 415 us (6.5 TB/s, 0.97 of a plain copy),
+// backward of 65536 x 1024 bf16 188 us (5.7 TB/s), of 32768 x 256 fp32 55 us with
+// the join (4.9 TB/s), of 65537 x 515 bf16 without a gate 161 us (2.5 TB/s: 66 pieces
 // on 96 threads, and the rows' ends).
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THRE
     k_norm_forward(const NormArgs a) {
     extern __shared__ float4 norm_smem[];
     __shared__ float red[2][2 * 32];
+    wait_for_prerequisites();
     const Teams<TPR> g(a.team_shift);
     const Row<L> r(g.t, g.tpr, a.d, static_cast<int>(static_cast<int64_t>(g.team) * a.d % L::VEC), a.rows);
     const float inv_d = 1.f / a.d;
@@ -391,6 +392,7 @@ __global__ void __launch_bounds__(Teams<TPR>::THREADS, resident(Teams<TPR>::THRE
     extern __shared__ float4 norm_smem[];
     const Teams<TPR> g(a.team_shift);
     dependents_may_launch();
+    wait_for_prerequisites();
     const Row<L> r(g.t, g.tpr, a.d, static_cast<int>(static_cast<int64_t>(g.team) * a.d % L::VEC), a.rows);
     const float inv_d = 1.f / a.d;
     const Weights<L, Teams<TPR>::THREADS> weights(norm_smem, r, a);
@@ -571,8 +573,7 @@ cudaError_t launch_norm(K kernel, NormArgs a, int ctas, int tpr, cudaStream_t s)
         if (e != cudaSuccess) return e;
     }
     while (TPR <= 32 && (1 << a.team_shift) < tpr) ++a.team_shift;
-    kernel<<<ctas, TPR <= 32 ? Teams<TPR>::THREADS : tpr, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, ctas, TPR <= 32 ? Teams<TPR>::THREADS : tpr, smem, s, a);
 }
 
 // Pieces a thread forward: two.  A bf16 row that two pieces a thread would leave half empty takes

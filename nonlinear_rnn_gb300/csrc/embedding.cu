@@ -10,9 +10,9 @@
 // floating-point atomics: the (id, position) pairs are put in order by a stable
 // radix sort, and the sums follow the sorted order in fixed groups.
 //
-// Measured: the lookup of 262144 fp32 rows of 512 takes 103 us (6.0 TB/s of the
+// Measured: the lookup of 262144 fp32 rows of 512 takes 101 us (6.1 TB/s of the
 // distinct rows and the output).  The gradient of 262144 bf16 rows of 1024 with ids
-// as frequent as words, V = 65536, takes 167 us: sorting 40 us, beside which gW is
+// as frequent as words, V = 65536, takes 166 us: sorting 40 us, beside which gW is
 // cleared, sums 107 us (5.6 TB/s), joining 17 us (a chain of dependent reads).
 #include <initializer_list>
 
@@ -44,6 +44,7 @@ template <typename T, int VEC, typename Id>
 __global__ void __launch_bounds__(EMBED_THREADS)
     k_embedding(const void *__restrict__ ids, const T *__restrict__ W, T *__restrict__ out,
                 int64_t n, int64_t V, int64_t d, int slabs, int64_t pad, float scale) {
+    wait_for_prerequisites();
     const int lane = threadIdx.x & 31;
     const int64_t item =
         blockIdx.x * static_cast<int64_t>(EMBED_THREADS / 32) + (threadIdx.x >> 5);
@@ -341,6 +342,8 @@ __global__ void __launch_bounds__(SORT_THREADS) k_sort_cluster(SortArgs a, int p
     extern __shared__ __align__(16) unsigned char sort_smem[];
     ClusterSortShared &c = *reinterpret_cast<ClusterSortShared *>(sort_smem);
     SortShared &s = c.s;
+    dependents_may_launch();
+    wait_for_prerequisites();
     if (static_cast<int>(blockIdx.x) >= a.ctas) return clear_share(a, blockIdx.x - a.ctas);
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t r = cluster.block_rank();
@@ -429,12 +432,14 @@ cudaError_t sort_ids(SortArgs a, uint32_t *const (&key)[2], uint32_t *const (&po
         cfg.blockDim = dim3(SORT_THREADS);
         cfg.dynamicSmemBytes = sizeof(ClusterSortShared);
         cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = static_cast<unsigned>(a.ctas);
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         return cudaLaunchKernelEx(&cfg, k_sort_cluster<Id>, a, passes);
     }
     a.rounds = static_cast<int>((tiles + SORT_CTAS - 1) / SORT_CTAS);
@@ -452,13 +457,8 @@ cudaError_t sort_ids(SortArgs a, uint32_t *const (&key)[2], uint32_t *const (&po
             a.clear = reinterpret_cast<uint4 *>(clear) + cleared;
             a.clear16 = clear16 - cleared < share ? clear16 - cleared : share;
             cleared += a.clear16;
-            if (q == 0 && half == 0) {
-                k_sort_count<Id><<<a.ctas + more, SORT_THREADS, smem, stream>>>(a);
-                e = cudaGetLastError();
-            } else {
-                e = launch_dependent(half == 0 ? k_sort_count<Id> : k_sort_place<Id>,
-                                     a.ctas + more, SORT_THREADS, smem, stream, a);
-            }
+            e = launch_dependent(half == 0 ? k_sort_count<Id> : k_sort_place<Id>,
+                                 a.ctas + more, SORT_THREADS, smem, stream, a);
             if (e != cudaSuccess) return e;
         }
     }
@@ -718,10 +718,9 @@ cudaError_t lookup(const void *ids, int ids_type, const void *W, void *out, int6
     const int64_t items = (n + GROUP_ROWS - 1) / GROUP_ROWS * slabs;
     const int64_t blocks = (items + EMBED_THREADS / 32 - 1) / (EMBED_THREADS / 32);
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    auto kernel = ids_type == NRNN_I64 ? k_embedding<T, VEC, int64_t> : k_embedding<T, VEC, int32_t>;
-    kernel<<<static_cast<unsigned>(blocks), EMBED_THREADS, 0, stream>>>(
-        ids, static_cast<const T *>(W), static_cast<T *>(out), n, V, d, slabs, pad, scale);
-    return cudaGetLastError();
+    return launch_dependent(ids_type == NRNN_I64 ? k_embedding<T, VEC, int64_t> : k_embedding<T, VEC, int32_t>,
+                            static_cast<unsigned>(blocks), EMBED_THREADS, 0, stream, ids,
+                            static_cast<const T *>(W), static_cast<T *>(out), n, V, d, slabs, pad, scale);
 }
 
 template <typename T, int VEC>

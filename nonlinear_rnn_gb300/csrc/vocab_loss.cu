@@ -42,11 +42,11 @@
 // at most 512 elements of the inner dimension before the epilogue adds it to
 // fp32 registers.
 //
-// Measured: 16384 rows over 65536 x 1024 bf16 with gradient 5.2 to 5.6 ms (1.57 to
+// Measured: 16384 rows over 65536 x 1024 bf16 with gradient 5.2 to 5.6 ms (1.56 to
 // 1.68 PFLOP/s; cuBLAS runs at 1.75 when kept up: the power limit holds the clocks at
-// 1.7 GHz); 4096 over 32768 x 512 bf16 0.43 ms (1.2 PFLOP/s: a tile's 8 slices hide
-// less of its epilogue), 3001 over 10007 x 250 fp32 0.29 ms, 4 rows over 50021 x 1024
-// bf16, forward only, 35 us (W once in 23 us).  Without its epilogue the forward's
+// 1.7 GHz); 4096 over 32768 x 512 bf16 0.42 ms (1.2 PFLOP/s: a tile's 8 slices hide
+// less of its epilogue), 3001 over 10007 x 250 fp32 0.285 ms, 4 rows over 50021 x 1024
+// bf16, forward only, 30 us (W once in 20 to 23 us).  Without its epilogue the forward's
 // main loop takes 0.96 of the time at d = 1024, 0.94 at 512 and 0.55 at 64, where the
 // exponentials bind.
 //
@@ -739,6 +739,7 @@ template <typename Id>
 __global__ void __launch_bounds__(KEPT_THREADS)
     k_kept_rows(const void *targets, int n, int64_t V, int64_t ignore, int2 *row, int *kept) {
     dependents_may_launch();
+    wait_for_prerequisites();
     const int all = number_rows<KEPT_THREADS, Id>(targets, n, V, ignore, row);
     if (threadIdx.x == 0) *kept = all;
 }
@@ -874,6 +875,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pitch = (d + 32 * VEC - 1) / (32 * VEC) * (32 * VEC);
     dependents_may_launch();
+    wait_for_prerequisites();
     const int live = number_rows<FEW_WARPS * 32, Id>(targets, n, V, ignore, rows);
     if (blockIdx.x == 0) {
         if (static_cast<int>(threadIdx.x) < live) row[threadIdx.x] = rows[threadIdx.x];
@@ -1142,8 +1144,8 @@ cudaError_t lay_out(const Call &c, const Plan &p, const float *lse, const float 
     if (c.n <= FEW_ROWS) {
         e = launch_dependent(k_gather_rows<T, Id, true>, blocks, GATHER_THREADS, 0, c.stream, g);
     } else {
-        k_kept_rows<Id><<<1, KEPT_THREADS, 0, c.stream>>>(c.targets, static_cast<int>(c.n), c.V, c.ignore, row, kept);
-        e = cudaGetLastError();
+        e = launch_dependent(k_kept_rows<Id>, 1, KEPT_THREADS, 0, c.stream, c.targets, static_cast<int>(c.n), c.V,
+                             c.ignore, row, kept);
         if (e == cudaSuccess)
             e = launch_dependent(k_gather_rows<T, Id, false>, blocks, GATHER_THREADS, 0, c.stream, g);
     }
@@ -1183,12 +1185,11 @@ cudaError_t launch_few(const Call &c, const Plan &p) {
     });
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(float) * N * (ceil_div(c.d, 32 * VEC) * 32 * VEC);
-    k_few_rows<N, VEC, Id><<<FEW_CTAS, FEW_WARPS * 32, smem, c.stream>>>(
-        static_cast<const float *>(c.x), static_cast<const float *>(c.W), c.targets, static_cast<int>(c.n),
-        static_cast<int>(c.d), c.V, c.ignore, c.scale * LOG2E, reinterpret_cast<float2 *>(c.ws + p.part),
-        reinterpret_cast<float *>(c.ws + p.z), reinterpret_cast<int2 *>(c.ws + p.row),
-        reinterpret_cast<int *>(c.ws + p.kept));
-    return cudaGetLastError();
+    return launch_dependent(k_few_rows<N, VEC, Id>, FEW_CTAS, FEW_WARPS * 32, smem, c.stream,
+                            static_cast<const float *>(c.x), static_cast<const float *>(c.W), c.targets,
+                            static_cast<int>(c.n), static_cast<int>(c.d), c.V, c.ignore, c.scale * LOG2E,
+                            reinterpret_cast<float2 *>(c.ws + p.part), reinterpret_cast<float *>(c.ws + p.z),
+                            reinterpret_cast<int2 *>(c.ws + p.row), reinterpret_cast<int *>(c.ws + p.kept));
 }
 
 template <typename Id> cudaError_t launch_few(const Call &c, const Plan &p) {
