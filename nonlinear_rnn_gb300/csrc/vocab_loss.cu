@@ -10,14 +10,14 @@
 // All three products run on one persistent tcgen05 kernel (k_vocab_gemm): a pair
 // of CTAs on two SMs (cta_group::2) per 256 x (up to 256) tile, TMA into a ring of
 // 128-byte-swizzled stages, one thread issuing tcgen05.mma into one of two TMEM
-// accumulators while the epilogue warps drain the other.  A pair reads half of
-// what two single tiles read: with one CTA per 128 x 256 tile the L2 could not
-// feed the tensor cores (77% active, 96 bytes a cycle and SM asked for).  Its forms differ in the operands'
-// orientation (the transposed ones are read MN-major from where they lie: no
-// transposed copy is made) and in the epilogue:
+// accumulators while the epilogue warps drain the other.  Each CTA of a pair stages
+// half of B for both: the same tensor activity as one CTA per 128 x 256 tile (77% at
+// 1.9 GHz), but 5% faster where the power limit sets the clock.  The kernel's forms
+// differ in the operands' orientation (the transposed ones are read MN-major from
+// where they lie: no transposed copy is made) and in the epilogue:
 //   LSE  x W^T   running maximum and sum of each row over the unit's vocabulary
 //   DL   x W^T   G of one piece of the vocabulary, to the workspace
-//   GX   G W     gx, or its share of this piece / this split of the piece
+//   GX   G W     gx, or this piece's share of it
 //   GW   G^T x   rows of gW of this piece
 // The piece of G is all that is ever kept of the N x V matrix.
 //
@@ -37,10 +37,10 @@
 //
 // fp32 inputs are written as three bf16 planes, v = hi + mid + lo up to 2^-24, and a
 // product is the six plane products above 2^-24 relative, smallest first:
-// (lo,hi) (mid,mid) (hi,lo) (mid,hi) (hi,mid) (hi,hi).  The tensor cores'
-// accumulation rounds coarser than fp32 addition does, so an accumulator takes
-// at most 512 elements of the inner dimension before the epilogue adds it to
-// fp32 registers.
+// (lo,hi) (mid,mid) (hi,lo) (mid,hi) (hi,mid) (hi,hi).  The tensor cores add less
+// exactly than fp32 rounding does (bf16 logits of 1024 products: lse 3e-7 off, fp32
+// products 4e-8), so an accumulator takes at most 512 elements of the inner
+// dimension before the epilogue adds it to fp32 registers.
 //
 // Measured: 16384 rows over 65536 x 1024 bf16 with gradient 5.2 to 5.6 ms (1.56 to
 // 1.68 PFLOP/s; cuBLAS runs at 1.75 when kept up: the power limit holds the clocks at
@@ -106,7 +106,7 @@ struct GemmArgs {
     float2 *part;             // LSE: [rows][groups][2] {maximum, sum} in base 2
     float *z_target;          // LSE: base-2 logit of the target
     void *out;                // GX, GW: the gradient in the storage type
-    float *acc;               // GX: [rows][acc_pitch] sums over the pieces (null: one piece)
+    float *acc;               // GX: [rows][acc_pitch] sums over the pieces, if there are several
     int acc_pitch;
     bool acc_in, acc_out;     // GX: add acc; store to acc instead of out
     int d;                    // width of gx and gW rows
@@ -1096,7 +1096,7 @@ cudaError_t gemm(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorM
     const unsigned pairs = static_cast<unsigned>(most_units < PAIRS ? most_units : PAIRS);
     e = launch_dependent(k_vocab_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, GEMM_SMEM, s, tmA, tmB, tmOut, a);
     if constexpr (FORM == GX || FORM == GW) {
-        if (e == cudaSuccess && pairs > 1) {
+        if (e == cudaSuccess && pairs > 1 && most_units > tiles) {   // tiles of several slices
             // tiles that may be cut: those left over by whole waves of any number of kept rows
             const int64_t cut = tiles < pairs ? tiles : pairs;
             const bool few = cut * 8 <= pairs;   // eight parts each and more
