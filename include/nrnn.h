@@ -597,7 +597,8 @@ size_t nrnn_vocab_loss_workspace_bytes(int64_t rows, int64_t d, int64_t V, int d
  *   loss, lse    device, fp32 (rows)
  *   workspace    device, 256-byte aligned, of at least
  *                nrnn_vocab_loss_workspace_bytes(..., 0)
- * fp32 inputs are multiplied with fp32 accuracy on the tensor cores.
+ * fp32 inputs are multiplied with fp32 accuracy on the tensor cores; an infinity
+ * in fp32 W or in a row that takes part may count as NaN.
  */
 int nrnn_vocab_loss_forward(const void *x, const void *W, int dtype, int64_t rows, int64_t d,
                             int64_t V, const void *targets, int targets_type, int64_t ignore_index,

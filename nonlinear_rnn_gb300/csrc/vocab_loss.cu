@@ -37,7 +37,8 @@
 //
 // fp32 inputs are written as three bf16 planes, v = hi + mid + lo up to 2^-24, and a
 // product is the six plane products above 2^-24 relative, smallest first:
-// (lo,hi) (mid,mid) (hi,lo) (mid,hi) (hi,mid) (hi,hi).  The tensor cores add less
+// (lo,hi) (mid,mid) (hi,lo) (mid,hi) (hi,mid) (hi,hi).  (An infinity leaves
+// no number, so in W or in a kept row it counts as NaN.)  The tensor cores add less
 // exactly than fp32 rounding does (bf16 logits of 1024 products: lse 3e-7 off, fp32
 // products 4e-8), so an accumulator takes at most 512 elements of the inner
 // dimension before the epilogue adds it to fp32 registers.
@@ -776,6 +777,13 @@ struct GatherArgs {
     int n;
 };
 
+// The first plane of v: the nearest bf16, or the one below in magnitude where that is
+// an infinity but v (the lowest value, as a mask) is not, so that v less it is a number.
+__device__ __forceinline__ float plane_of(float v) {
+    const float h = __bfloat162float(__float2bfloat16_rn(v));
+    return isinf(h) ? __bfloat162float(__float2bfloat16_rz(v)) : h;
+}
+
 // One row of `pitch` values (a multiple of 8) as bf16 planes, by the lanes of a warp;
 // src null: zeros.  16 bytes out at a time; wide: 16 bytes in as well.
 template <typename T>
@@ -798,10 +806,13 @@ __device__ __forceinline__ void copy_row(const T *src, __nv_bfloat16 *dst, int64
         }
 #pragma unroll
         for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
-            store_f32<__nv_bfloat16, 8>(dst + p * plane + c, v);
-            if (sizeof(T) == 4)
+            float h[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
+            for (int e = 0; e < 8; ++e) {
+                h[e] = sizeof(T) == 4 ? plane_of(v[e]) : v[e];
+                v[e] -= h[e];
+            }
+            store_f32<__nv_bfloat16, 8>(dst + p * plane + c, h);
         }
     }
 }

@@ -413,6 +413,33 @@ def test_vocab_loss_large_logits():
     check(loss, torch.full_like(loss_ref, math.log(3000)), 1e-5)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("n", [4, 40])
+def test_vocab_loss_lowest_value(n, t):
+    """A vocabulary row that the type's lowest value masks takes no probability."""
+    g, x, W, target, gl = loss_inputs(n, 500, 96, t, 0.0, 14)
+    target.clamp_min_(1)
+    x[:, 0] = 0.5
+    x[1, 1] = torch.finfo(t).max
+    W[:, 1] = 0
+    W[0] = 0
+    W[0, 0] = torch.finfo(t).min
+    loss, lse = nr.vocab_loss(x, W, target)
+    x2 = x.clone()
+    x2[1, 1] = 0
+    kept, X, lse_ref, loss_ref, G, zmag = loss64(x2, W[1:], target - 1, gl, 1.0)
+    tz = 2.0 ** -17 * zmag + 2.0 ** -20 * (1 + lse_ref.abs())
+    check(lse, lse_ref, tz, "lse")
+    check(loss, loss_ref, 2 * tz, "loss")
+    gx, gW = nr.vocab_loss_backward(x2, W, target, lse, gl)
+    part = 2.0 ** -8 if t == torch.bfloat16 else 2.0 ** -16
+    more = gl.abs().to(F64)[:, None] * 2 * tz[:, None] + part * G.abs()
+    gx_ref, gW_ref, rt = G @ W[1:].to(F64), G.T @ X, round_tol(t)
+    check(gx, gx_ref, more @ W[1:].to(F64).abs() + rt * gx_ref.abs(), "gx")
+    check(gW[1:], gW_ref, more.T @ X.abs() + rt * gW_ref.abs(), "gW")
+    assert bool((gW[0] == 0).all())
+
+
 def test_vocab_loss_strides_and_alignment():
     g, x, W, target, gl = loss_inputs(60, 700, 64, torch.bfloat16, 0.2, 12)
     flat = torch.empty(700 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(700, 64).copy_(W)
