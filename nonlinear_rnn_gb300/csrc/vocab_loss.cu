@@ -46,7 +46,7 @@
 // Measured: 16384 rows over 65536 x 1024 bf16 with gradient 5.2 to 5.6 ms (1.56 to
 // 1.68 PFLOP/s; cuBLAS runs at 1.75 when kept up: the power limit holds the clocks at
 // 1.7 GHz); 4096 over 32768 x 512 bf16 0.42 ms (1.2 PFLOP/s: a tile's 8 slices hide
-// less of its epilogue), 3001 over 10007 x 250 fp32 0.285 ms, 4 rows over 50021 x 1024
+// less of its epilogue), 3001 over 10007 x 250 fp32 0.289 ms, 4 rows over 50021 x 1024
 // bf16, forward only, 30 us (W once in 20 to 23 us).  Without its epilogue the forward's
 // main loop takes 0.96 of the time at d = 1024, 0.94 at 512 and 0.55 at 64, where the
 // exponentials bind.
