@@ -152,6 +152,23 @@ def _device_tensor(t: torch.Tensor, what: str) -> torch.Tensor:
     return t.contiguous()   # strided views are copied (shapes_layout: one extra copy)
 
 
+def _space(given, nbytes: int, device, what: str = "workspace") -> torch.Tensor:
+    """The caller's buffer if it holds nbytes, else a new one.  Kernels write to its
+    address, so it has to be one block of memory of the device they run on."""
+    if given is not None:
+        if not isinstance(given, torch.Tensor) or not given.is_cuda or not given.is_contiguous() \
+                or given.device.index != _index(device):
+            raise ValueError(f"{what} must be a contiguous tensor on {device}")
+        if given.numel() * given.element_size() >= nbytes:
+            return given
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _index(device) -> int:
+    device = torch.device(device)
+    return torch.cuda.current_device() if device.index is None else device.index
+
+
 def params_tensor(params, d_h: int, device) -> torch.Tensor:
     """(6, d_h) fp32 device tensor from a dict (a_z, a_r, a_c, b_z, b_r, b_c) or array."""
     if isinstance(params, dict):
@@ -247,8 +264,7 @@ def newton_forward(preact: torch.Tensor, params, cu_seqlens=None, K: int = 3,
               else lib.nrnn_newton_workspace_bytes(B, T, d_h, code, int(K), ALGOS[algo]))
     if nbytes == 0:
         raise ValueError("invalid shape, K or algo")
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    workspace = _space(workspace, nbytes, dev)
     host = ctypes.c_float(0.0) if check else None
     if H_init is not None:
         H_init = _device_tensor(H_init, "H_init")
@@ -259,7 +275,7 @@ def newton_forward(preact: torch.Tensor, params, cu_seqlens=None, K: int = 3,
                                           _ptr(H_init), int(K), float(residual_fail),
                                           ALGOS[algo], _ptr(H), _ptr(rho),
                                           ctypes.byref(host) if host is not None else None,
-                                          _ptr(workspace), workspace.numel(), _stream(dev))
+                                          _ptr(workspace), workspace.nbytes, _stream(dev))
     _raise(st, "newton_forward", H=H, residual=(host.value if host is not None else None))
     return H, rho
 
@@ -308,13 +324,12 @@ def newton_forward_host(preact: torch.Tensor, params, cu_seqlens=None, K: int = 
                                                 int(tokens_per_block))
     if nbytes == 0:
         raise ValueError("invalid shape or K")
-    if staging is None or staging.numel() < nbytes:
-        staging = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    staging = _space(staging, nbytes, dev, "staging")
     rho = ctypes.c_float(0.0)
     with torch.cuda.device(dev):
         st = lib.nrnn_newton_forward_host(_ptr(preact), code, _ptr(prm), B, T, d_h, cu_ptr, S,
                                           int(K), float(residual_fail), _ptr(H),
-                                          ctypes.byref(rho), _ptr(staging), staging.numel(),
+                                          ctypes.byref(rho), _ptr(staging), staging.nbytes,
                                           int(tokens_per_block), _stream(dev))
     if st == -5 and not check:
         return H, float(rho.value)
@@ -372,13 +387,12 @@ def newton_forward_x_host(x: torch.Tensor, W_x: torch.Tensor, params, cu_seqlens
                                                   int(tokens_per_block))
     if nbytes == 0:
         raise ValueError("invalid shape or K")
-    if staging is None or staging.numel() < nbytes:
-        staging = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    staging = _space(staging, nbytes, dev, "staging")
     rho = ctypes.c_float(0.0)
     with torch.cuda.device(dev):
         st = lib.nrnn_newton_forward_x_host(_ptr(x), _ptr(W_x), code, _ptr(prm), B, T, d_in, d_h,
                                             cu_ptr, S, int(K), float(residual_fail), _ptr(H),
-                                            ctypes.byref(rho), _ptr(staging), staging.numel(),
+                                            ctypes.byref(rho), _ptr(staging), staging.nbytes,
                                             int(tokens_per_block), _stream(dev))
     if st == -5 and not check:
         return H, float(rho.value)
@@ -407,14 +421,13 @@ def newton_forward_x(x: torch.Tensor, W_x: torch.Tensor, params, cu_seqlens=None
     H = out if out is not None else torch.empty((B, T, d_h), dtype=x.dtype, device=dev)
     rho = torch.empty((), dtype=torch.float32, device=dev)
     nbytes = lib.nrnn_newton_workspace_bytes(B, T, d_h, code, int(K), ALGOS["fused"])
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    workspace = _space(workspace, max(nbytes, 256), dev)
     host = ctypes.c_float(0.0) if check else None
     with torch.cuda.device(dev):
         st = lib.nrnn_newton_forward_x(_ptr(x), _ptr(W_x), code, _ptr(prm), B, T, d_in, d_h,
                                        _ptr(cu), S, int(K), float(residual_fail), _ptr(H),
                                        _ptr(rho), ctypes.byref(host) if host is not None else None,
-                                       _ptr(workspace), workspace.numel(), _stream(dev))
+                                       _ptr(workspace), workspace.nbytes, _stream(dev))
     _raise(st, "newton_forward_x", H=H, residual=(host.value if host is not None else None))
     return H, rho
 
@@ -442,12 +455,11 @@ def newton_backward(preact: torch.Tensor, params, H: torch.Tensor, gH: torch.Ten
     gprm = torch.empty((6, d_h), dtype=torch.float32, device=dev)
     nbytes = (lib.nrnn_newton_workspace_bytes_pack(T, d_h, code, 1, ALGOS["fused"], S) if S > 0
               else lib.nrnn_newton_workspace_bytes(B, T, d_h, code, 1, ALGOS["fused"]))
-    ws = workspace if workspace is not None else torch.empty(max(nbytes, 256), dtype=torch.uint8,
-                                                             device=dev)
+    ws = _space(workspace, 0 if workspace is not None else max(nbytes, 256), dev)
     with torch.cuda.device(dev):
         st = lib.nrnn_newton_backward(_ptr(preact), code, _ptr(prm), B, T, d_h, _ptr(cu), S,
                                       _ptr(H), _ptr(gH), _ptr(gP), _ptr(gprm), _ptr(ws),
-                                      ws.numel(), _stream(dev))
+                                      ws.nbytes, _stream(dev))
     _raise(st, "newton_backward")
     return gP, gprm
 
@@ -578,8 +590,8 @@ def input_projection(x: torch.Tensor, W_x: torch.Tensor, out: torch.Tensor | Non
     P = out if out is not None else torch.empty((*x.shape[:-1], n_out), dtype=x.dtype, device=x.device)
     code = _dtype_code(x)
     nbytes = lib.nrnn_input_projection_workspace_bytes(code, d_in, n_out // 3)
-    if nbytes > 0 and (workspace is None or workspace.numel() < nbytes):
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    if nbytes > 0:
+        workspace = _space(workspace, nbytes, x.device)
     with torch.cuda.device(x.device):
         st = lib.nrnn_input_projection(_ptr(x), _ptr(W_x), code, rows, d_in, n_out // 3, _ptr(P),
                                        _ptr(workspace) if nbytes > 0 else None, int(nbytes),

@@ -9,7 +9,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import BF16, F32, OK, _device_tensor, _raise, load
+from ._binding import BF16, F32, OK, _device_tensor, _raise, _space, load
 
 I32, I64 = 0, 1
 
@@ -65,12 +65,6 @@ def _result(out, shape, like: torch.Tensor, what: str) -> torch.Tensor:
             or not out.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor of {like.dtype} on {like.device}")
     return out
-
-
-def _space(workspace, nbytes: int, device) -> torch.Tensor:
-    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace
 
 
 def embedding(ids: torch.Tensor, W: torch.Tensor, scale: float = 1.0,
