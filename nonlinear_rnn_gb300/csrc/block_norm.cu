@@ -540,6 +540,11 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
 
 // ---------------------------------------------------------------- host side
 bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool all_aligned_to(size_t a, std::initializer_list<const void *> ptrs) {
+    for (const void *p : ptrs)
+        if (!aligned_to(p, a)) return false;
+    return true;
+}
 
 // Threads a row: the fewest that hold it in `pieces` each, a power of two up to
 // a warp, whole warps beyond.
@@ -669,8 +674,9 @@ int nrnn_block_norm_forward(const void *x, const void *h, const void *gate, cons
     if (h == nullptr && (gate != nullptr || u == nullptr)) return NRNN_ERR_INVALID_ARG;
     if (x == nullptr || (h != nullptr && x_out == nullptr)) return NRNN_ERR_INVALID_ARG;
     const int elem = dtype == NRNN_BF16 ? 2 : 4;
-    for (const void *p : {x, h, gate, static_cast<const void *>(x_out), static_cast<const void *>(u)})
-        if (!aligned_to(p, elem)) return NRNN_ERR_INVALID_ARG;
+    if (!all_aligned_to(elem, {x, h, gate, x_out, u}) ||
+        !all_aligned_to(sizeof(float), {w_post, scale, w_pre}))
+        return NRNN_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = x; a.h = h; a.gate = gate;
     a.w_post = w_post; a.scale = scale; a.w_pre = w_pre;
@@ -711,9 +717,9 @@ int nrnn_block_norm_backward(const void *x_out, const void *h, const void *gate,
             return NRNN_ERR_INVALID_ARG;
     }
     const int elem = dtype == NRNN_BF16 ? 2 : 4;
-    for (const void *p : {x_out, h, gate, g_x, g_u, static_cast<const void *>(gx),
-                          static_cast<const void *>(gh), static_cast<const void *>(g_gate)})
-        if (!aligned_to(p, elem)) return NRNN_ERR_INVALID_ARG;
+    if (!all_aligned_to(elem, {x_out, h, gate, g_x, g_u, gx, gh, g_gate}) ||
+        !all_aligned_to(sizeof(float), {w_post, scale, w_pre, gw_post, g_scale, gw_pre}))
+        return NRNN_ERR_INVALID_ARG;
     if (workspace == nullptr || !aligned_to(workspace, 256) ||
         ws_bytes < nrnn_block_norm_backward_workspace_bytes(rows, d))
         return NRNN_ERR_WORKSPACE;

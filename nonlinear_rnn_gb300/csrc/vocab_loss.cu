@@ -1344,7 +1344,9 @@ int nrnn_vocab_loss_forward(const void *x, const void *W, int dtype, int64_t row
     const int st = check_vocab(c);
     if (st != NRNN_OK) return st;
     if (rows == 0) return NRNN_OK;
-    if (loss == nullptr || lse == nullptr) return NRNN_ERR_INVALID_ARG;
+    if (loss == nullptr || lse == nullptr ||
+        (reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(lse)) % sizeof(float) != 0)
+        return NRNN_ERR_INVALID_ARG;
     if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
         ws_bytes < plan_for(rows, d, V, dtype, reinterpret_cast<uintptr_t>(W) % 16 == 0, false).total)
         return NRNN_ERR_WORKSPACE;
@@ -1365,7 +1367,8 @@ int nrnn_vocab_loss_backward(const void *x, const void *W, int dtype, int64_t ro
     const size_t elem = dtype == NRNN_BF16 ? 2 : 4;
     if (gW == nullptr || (rows > 0 && (lse == nullptr || g_loss == nullptr || gx == nullptr)))
         return NRNN_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(gx) | reinterpret_cast<uintptr_t>(gW)) % elem != 0)
+    if ((reinterpret_cast<uintptr_t>(gx) | reinterpret_cast<uintptr_t>(gW)) % elem != 0 ||
+        (reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(g_loss)) % sizeof(float) != 0)
         return NRNN_ERR_INVALID_ARG;
     if (rows == 0)
         return cudaMemsetAsync(gW, 0, elem * V * d, c.stream) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
