@@ -148,6 +148,15 @@ template <typename T> __device__ __forceinline__ void store_cols(T *p, const flo
     }
 }
 
+// Two values as bf16, the nearest; or the type's largest where that is an infinity,
+// so that a finite value less its first plane is a number.  (An infinity less the
+// largest stays one, and its third plane is NaN.)
+__device__ __forceinline__ __nv_bfloat162 finite_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return *reinterpret_cast<__nv_bfloat162 *>(&r);
+}
+
 // A unit is what a pair takes at a time: a tile; `group` tiles beside one another
 // (LSE); or a tile's slices k0 .. k1 (GX, GW).  Every role walks the same sequence.
 struct Unit { int m0, n0, tiles, k0, k1, group, slot; };   // slot: -1 = a whole tile
@@ -438,7 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float &lo = v[q * 8 + 2 * e], &hi = v[q * 8 + 2 * e + 1];
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(lo, hi);
+                        const __nv_bfloat162 h2 =
+                            SPLIT && plane == 0 ? finite_bf16x2(lo, hi) : __floats2bfloat162_rn(lo, hi);
                         o[e] = *reinterpret_cast<const uint32_t *>(&h2);
                         if (SPLIT) {
                             lo -= __low2float(h2);
