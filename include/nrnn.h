@@ -465,8 +465,11 @@ int nrnn_debug_pack_plan(const int32_t *cu_seqlens, int64_t num_segments, int64_
                          void *plan, void *stream);
 
 /*
- * Upper limit, in nanoseconds, of every bounded device wait that later calls
- * launch (default 2e9 = 2 s).  Process-wide; returns the previous value.
+ * Upper limit, in nanoseconds, of the bounded device waits of the Newton
+ * forward and backward and of the vocabulary loss that later calls launch
+ * (default 2e9 = 2 s).  The tensor-core waits of nrnn_input_projection and
+ * nrnn_decode_step_x always give up after 2 s.  Process-wide; returns the
+ * previous value.
  */
 uint64_t nrnn_set_wait_limit_ns(uint64_t ns);
 
@@ -596,7 +599,10 @@ size_t nrnn_vocab_loss_workspace_bytes(int64_t rows, int64_t d, int64_t V, int d
  *                they hold is read.  Any other target outside [0, V) gives NaN
  *   loss, lse    device, fp32 (rows)
  *   workspace    device, 256-byte aligned, of at least
- *                nrnn_vocab_loss_workspace_bytes(..., 0)
+ *                nrnn_vocab_loss_workspace_bytes(..., 0).  Its second 32-bit word
+ *                is 0 once the work is done, or not if a device wait gave up
+ *                (nrnn_set_wait_limit_ns): then outputs are NaN where they
+ *                depended on it.  So too in the backward
  * fp32 inputs are multiplied with fp32 accuracy on the tensor cores; an infinity
  * in fp32 W or in a row that takes part may count as NaN.
  */

@@ -272,6 +272,8 @@ bool make_map_planes(CUtensorMap *m, const void *base, int64_t inner, int64_t ro
     return r == CUDA_SUCCESS;
 }
 
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+
 size_t newton_error_offset(int K) { return layout(0, 0, 8, NRNN_F32, K, true).error_off; }
 }  // namespace nrnn
 

@@ -154,6 +154,9 @@ bool make_map_planes(CUtensorMap *m, const void *base, int64_t inner, int64_t ro
 // byte offset of the error word in a Newton forward's workspace
 size_t newton_error_offset(int K);
 
+// the process-wide limit of bounded device waits
+uint64_t wait_limit_ns();
+
 // Which look-back form launch_newton takes for these arguments (B, n_ut,
 // plan are read): 0 plain, 1 early reads.
 int newton_lookback_form(int dtype, bool fused, const NewtonArgs &a, bool plan = false);

@@ -51,10 +51,11 @@
 // main loop takes 0.96 of the time at d = 1024, 0.94 at 512 and 0.55 at 64, where the
 // exponentials bind.
 //
-// Every wait is bounded.  One that gives up sets g_vocab_error and the CTA's
-// abort flag, which ends the other roles' waits too: the producer and the issuer
-// stop (and see their copies and products in flight through), and the epilogue
-// writes NaN from there on.
+// Every wait is bounded.  One that gives up sets the call's error word (the
+// workspace's second) and the abort flag of both CTAs of the pair, which ends the
+// other roles' waits too: the producers and the issuer stop, and the epilogues hand
+// back no accumulator and write NaN from there on.  Neither CTA leaves before the
+// copies and products that both have in flight are done (settle).
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
 #include "nrnn_internal.h"
@@ -64,11 +65,9 @@
 namespace nrnn {
 namespace {
 
-constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr uint64_t SETTLE_NS = 2000000000ull;   // for what is in flight after a wait gave up
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int PAIRS = 76;   // of 152 SMs: the work is divided for this many
-
-__device__ uint32_t g_vocab_error;
 
 enum Form { LSE, DL, GX, GW };
 
@@ -91,6 +90,8 @@ __device__ constexpr int PLANE_B[SEGMENTS] = {0, 1, 2, 0, 1, 0};
 
 struct GemmArgs {
     const int *kept;          // device: number of kept rows
+    uint32_t *error;          // device: set by a wait that gave up
+    uint64_t wait_ns;         // limit of a wait
     int M;                    // rows of the product on the host's side: -1 = kept
     int K;                    // inner size: -1 = kept
     int bn;                   // columns of a tile: a multiple of 32, at most BN
@@ -115,20 +116,41 @@ struct GemmArgs {
                               // rows over 50021 x 1024 bf16 with gradient: 139 -> 121 us)
 };
 
-// mbar_wait_bounded that also ends when another role of the CTA gave up
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
+// mbar_wait_bounded that also ends when another role of the pair gave up, and tells
+// both CTAs when it does
+__device__ __forceinline__ bool wait_or_abort(const GemmArgs &a, uint64_t *bar, uint32_t parity,
+                                              volatile uint32_t *abort) {
     if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t hint = static_cast<uint32_t>(a.wait_ns < 1000000u ? a.wait_ns : 1000000u);
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (*abort != 0) return false;
-        if (mbar_try_wait_hint(bar, parity, 1000000u)) return true;
-        if (globaltimer_ns() - t0 > WAIT_NS) {
-            *abort = 1;
-            atomicOr(&g_vocab_error, 2u);
+        if (mbar_try_wait_hint(bar, parity, hint)) return true;
+        if (globaltimer_ns() - t0 > a.wait_ns) {
+            for (uint32_t r = 0; r < 2; ++r)
+                cluster_store(cluster_addr(const_cast<const uint32_t *>(abort), r), 1u);
+            atomicOr(a.error, 2u);
             return false;
         }
     }
-    return true;
+}
+
+// After a wait gave up, and both CTAs' roles have ended: sees through what is in flight.
+// issued: stages that each CTA's producer started the copies of.  One that is ahead of
+// the other (by at most the ring, whose stages are handed back to both at once) has
+// copies that the stage's barrier, rank 0's, cannot complete on: it is brought to wait
+// for that CTA's bytes alone.  By the issuing thread of rank 0.
+__device__ __forceinline__ void settle(const GemmArgs &a, const volatile int *issued, uint64_t *full_bar,
+                                       uint64_t *drain_bar, uint32_t bytes_1) {
+    mma_commit_pair(drain_bar);
+    mbar_wait_bounded(drain_bar, 0, SETTLE_NS, a.error);
+    const int n0 = issued[0], n1 = issued[1], both = n0 < n1 ? n0 : n1, most = n0 < n1 ? n1 : n0;
+    for (int i = both > STAGES ? both - STAGES : 0; i < most; ++i) {
+        uint64_t *bar = &full_bar[i % STAGES];
+        if (i >= both && n0 > n1) mbar_complete_tx(bar, bytes_1);              // was to come from rank 1
+        else if (i >= both) mbar_arrive_expect_tx(bar, bytes_1);               // rank 0 never got there
+        mbar_wait_bounded(bar, (i / STAGES) & 1, SETTLE_NS, a.error);
+    }
 }
 
 template <typename T> __device__ __forceinline__ void store_cols(T *p, const float (&v)[PIECE], int n, bool wide) {
@@ -257,6 +279,17 @@ __device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m
     store_cols<T>(static_cast<T *>(a.out) + row * a.d + c, v, n, wide);
 }
 
+// rows of x below one CTA's: rank 1 reads none
+template <int FORM> __device__ __forceinline__ bool few_rows_of_a(const GemmArgs &a) {
+    return (FORM == LSE || FORM == DL) && a.a_rows < HALF_M;
+}
+// bytes of a stage's copies in the CTA of a rank: one box of a K-major operand, 64
+// columns each of an MN-major one
+template <int FORM> __device__ __forceinline__ uint32_t stage_bytes(const GemmArgs &a, int rank) {
+    const int half_n = a.bn / 2, b_rows = FORM == GX || FORM == GW ? (half_n + 63) / 64 * 64 : half_n;
+    return (!few_rows_of_a<FORM>(a) ? A_BYTES : rank == 0 ? a.a_rows * BK * 2 : 0) + b_rows * BK * 2;
+}
+
 // T: storage type of the inputs (float: split products)
 template <int FORM, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
@@ -271,7 +304,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], accf_bar[2], acce_bar[2],
         drain_bar;
     __shared__ uint32_t s_tmem;
-    __shared__ volatile uint32_t s_abort;
+    __shared__ volatile uint32_t s_abort;     // a role of either CTA gave up
+    __shared__ volatile int s_issued[2];      // rank 0's: stages that each producer went through
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -309,18 +343,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     Walk<FORM> w(a, pair, gridDim.x >> 1);
     Unit t;
     constexpr int PASSES = SPLIT ? SEGMENTS : 1;
-
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
-        // Lane i starts the i-th copy of a stage: one box of a K-major operand, 64
-        // columns of an MN-major one.  (One lane after another took longer than the
-        // products of a stage: gW of 16384 x 65536 x 1024 ran at 1.4 PFLOP/s.)
+        // Lane i starts the i-th copy of a stage.  (One lane after another took longer than
+        // the products of a stage: gW of 16384 x 65536 x 1024 ran at 1.4 PFLOP/s.)
         constexpr int BOXES_A = MN_A ? HALF_M / 64 : 1;
         const int half_n = a.bn / 2;
         const int boxes_b = MN_B ? (half_n + 63) / 64 : 1;
-        const bool few = !MN_A && FORM != GX && a.a_rows < HALF_M;
-        const uint32_t bytes = (few ? a.a_rows * BK * 2 : 2 * A_BYTES) +
-                               2 * (MN_B ? boxes_b * 64 : half_n) * BK * 2;   // of both CTAs
+        const bool few = few_rows_of_a<FORM>(a);
+        const uint32_t bytes = stage_bytes<FORM>(a, 0) + stage_bytes<FORM>(a, 1);
         const bool is_a = lane < BOXES_A;
         const bool copies = is_a ? rank == 0 || !few : lane < BOXES_A + boxes_b;
         const int box = is_a ? lane : lane - BOXES_A;
@@ -341,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                         for (int k = c0; k < c1; ++k, ++it) {
                             const int s = it % STAGES;
                             if (it >= STAGES)
-                                go = __all_sync(FULL_MASK, wait_or_abort(&empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort));
+                                go = __all_sync(FULL_MASK, wait_or_abort(a, &empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort));
                             if (!go) break;
                             if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full_bar[s], bytes);
                             __syncwarp();
@@ -356,9 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 }
             }
         }
-        if (!go && lane == 0 && rank == 0)   // see the copies in flight through
-            for (int i = it > STAGES ? it - STAGES : 0; i < it; ++i)
-                mbar_wait_bounded(&full_bar[i % STAGES], (i / STAGES) & 1, WAIT_NS, &g_vocab_error);
+        if (lane == 0) cluster_store(cluster_addr(const_cast<const int *>(&s_issued[rank]), 0), static_cast<uint32_t>(it));
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc = idesc_bf16(BM, MN_A, MN_B) | static_cast<uint32_t>(a.bn >> 3) << 17;
@@ -369,13 +398,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 for (int c0 = t.k0; go && c0 < t.k1; ++phase) {
                     const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
                     const int buf = phase & 1;
-                    if (phase >= 2) go = wait_or_abort(&acce_bar[buf], ((phase >> 1) - 1) & 1, &s_abort);
+                    if (phase >= 2) go = wait_or_abort(a, &acce_bar[buf], ((phase >> 1) - 1) & 1, &s_abort);
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t d = tmem + buf * BN;
                     const int its = (c1 - c0) * PASSES;
                     for (int i = 0; go && i < its; ++i, ++it) {
                         const int s = it % STAGES;
-                        go = wait_or_abort(&full_bar[s], (it / STAGES) & 1, &s_abort);
+                        go = wait_or_abort(a, &full_bar[s], (it / STAGES) & 1, &s_abort);
                         if (!go) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BYTES;
@@ -395,10 +424,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 }
             }
         }
-        if (!go) {   // see the products in flight through
-            mma_commit_pair(&drain_bar);
-            mbar_wait_bounded(&drain_bar, 0, WAIT_NS, &g_vocab_error);
-        }
     } else if (warp >= 4) {
         // --------------------------------------------------------------- epilogue
         // warps 4..7 take the even pieces of their 32 rows, 8..11 the odd ones
@@ -414,7 +439,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         auto release = [&](int buf) {   // this warp has read the accumulator
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&acce_bar[buf], 0));
+            if (lane == 0 && ok) mbar_arrive_cluster(cluster_addr(&acce_bar[buf], 0));
+        };
+        auto accumulator = [&](int buf, uint32_t parity) {   // the same outcome for the whole warp
+            ok &= wait_or_abort(a, &accf_bar[buf], parity, &s_abort);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         };
         while (w.next(a, t)) {
             const int in_tile = static_cast<int>(rank) * HALF_M + quarter * 32;   // the warp's first row
@@ -543,8 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                         for (int e = 0; e < PIECE; ++e) acc[i][e] = 0.f;
                     for (int c0 = t.k0; c0 < t.k1; c0 += SPLIT_CHUNK, ++phase) {
                         const int buf = phase & 1;
-                        ok &= wait_or_abort(&accf_bar[buf], (phase >> 1) & 1, &s_abort);
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        accumulator(buf, (phase >> 1) & 1);
 #pragma unroll
                         for (int i = 0; i < PIECES; ++i)
 #pragma unroll
@@ -566,8 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     }
                 } else if (t.k0 < t.k1) {
                     const int buf = phase & 1;
-                    ok &= wait_or_abort(&accf_bar[buf], (phase >> 1) & 1, &s_abort);
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    accumulator(buf, (phase >> 1) & 1);
 #pragma unroll 1
                     for (int c = half * PIECE; c < a.bn; c += 2 * PIECE) {
                         uint32_t r[PIECE];
@@ -600,6 +627,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     cluster_sync_all();   // neither CTA leaves while the other may still reach into it
+    if (s_abort != 0) {   // the same in both
+        if (warp == 1 && lane == 0) {
+            if (rank == 0) settle(a, s_issued, full_bar, &drain_bar, stage_bytes<FORM>(a, 1));
+            else mbar_wait_bounded(&drain_bar, 0, SETTLE_NS, a.error);
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
     if (warp == 2) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -756,11 +791,11 @@ __device__ __forceinline__ int number_rows(const void *targets, int n, int64_t V
 
 template <typename Id>
 __global__ void __launch_bounds__(KEPT_THREADS)
-    k_kept_rows(const void *targets, int n, int64_t V, int64_t ignore, int2 *row, int *kept) {
+    k_kept_rows(const void *targets, int n, int64_t V, int64_t ignore, int2 *row, int *kept) {   // kept: {number, error}
     dependents_may_launch();
     wait_for_prerequisites();
     const int all = number_rows<KEPT_THREADS, Id>(targets, n, V, ignore, row);
-    if (threadIdx.x == 0) *kept = all;
+    if (threadIdx.x == 0) kept[0] = all, kept[1] = 0;
 }
 
 // Copies the kept rows of x to (planes, rows_pad, pitch) bf16, zeros after them
@@ -844,7 +879,7 @@ __global__ void __launch_bounds__(GATHER_THREADS) k_gather_rows(const GatherArgs
         rows = few_rows;
         if (blockIdx.x == 0) {
             for (int i = threadIdx.x; i < kept; i += GATHER_THREADS) a.row[i] = few_rows[i];
-            if (threadIdx.x == 0) *a.kept = kept;
+            if (threadIdx.x == 0) a.kept[0] = kept, a.kept[1] = 0;
         }
     } else {
         kept = *a.kept;
@@ -908,7 +943,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
     const int live = number_rows<FEW_WARPS * 32, Id>(targets, n, V, ignore, rows);
     if (blockIdx.x == 0) {
         if (static_cast<int>(threadIdx.x) < live) row[threadIdx.x] = rows[threadIdx.x];
-        if (threadIdx.x == 0) *kept = live;
+        if (threadIdx.x == 0) kept[0] = live, kept[1] = 0;
     }
     for (int i = threadIdx.x; i < N * pitch; i += FEW_WARPS * 32) {
         const int r = i / pitch, c = i - r * pitch;
@@ -1089,7 +1124,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
         at += up256(bytes);
         return o;
     };
-    p.kept = take(sizeof(int));
+    p.kept = take(2 * sizeof(int));   // first of all: the error word is the workspace's second
     p.row = take(sizeof(int2) * n);
     p.x = take(sizeof(__nv_bfloat16) * p.planes * p.rows_pad * p.pitch);
     p.w = take(p.copy_w ? sizeof(__nv_bfloat16) * p.planes * V * p.pitch : 0);
@@ -1247,6 +1282,8 @@ int forward(const Call &c, float *loss, float *lse) {
         return NRNN_ERR_CUDA;
     GemmArgs a{};
     a.kept = reinterpret_cast<int *>(c.ws + p.kept);
+    a.error = reinterpret_cast<uint32_t *>(c.ws + p.kept) + 1;
+    a.wait_ns = wait_limit_ns();
     a.M = -1; a.K = static_cast<int>(c.d);
     a.bn = p.fwd_bn; a.n_cols = static_cast<int>(c.V);
     a.group = p.group;
@@ -1285,6 +1322,8 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
     GemmArgs a{};
     a.blocks_out = blocks_out;
     a.kept = reinterpret_cast<int *>(c.ws + p.kept);
+    a.error = reinterpret_cast<uint32_t *>(c.ws + p.kept) + 1;
+    a.wait_ns = wait_limit_ns();
     a.scale = c.scale;
     a.a_rows = rows_of_x(c.n);
     a.row = reinterpret_cast<int2 *>(c.ws + p.row);
