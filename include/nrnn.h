@@ -516,8 +516,8 @@ size_t nrnn_embedding_backward_workspace_bytes(int64_t n, int64_t V, int64_t d);
 
 /*
  * Gradient of the lookup: gW_v = scale sum of g_i over the i with ids_i = v,
- * in fp32, rounded once; the sum's order is fixed by the ids alone, so the
- * result does not change from run to run.  Padding and ids outside [0, V) take
+ * in fp32, rounded once; the sum's order is fixed by the ids, d and dtype alone,
+ * so the result does not change from run to run.  Padding and ids outside [0, V) take
  * no part.
  *
  *   g           device, (n, d) of dtype: dL/dout
@@ -570,7 +570,8 @@ size_t nrnn_block_norm_backward_workspace_bytes(int64_t rows, int64_t d);
  *   gh, g_gate  device, (rows, d): dL/dh and dL/dgate (unused where h or gate
  *               is NULL); must not overlap the inputs
  *   gw_post, g_scale, gw_pre   device, fp32 (d), overwritten; each may be NULL.
- *               Sums over the rows in fp32, in an order fixed by the sizes
+ *               Sums over the rows in fp32, in an order fixed by the sizes, dtype
+ *               and whether all buffers are 16-byte aligned
  *   workspace   device, 256-byte aligned, of at least
  *               nrnn_block_norm_backward_workspace_bytes(rows, d)
  */

@@ -733,8 +733,11 @@ cudaError_t gradient(const void *g, void *gW, const SortArgs &a, float *part, in
     });
     if (e != cudaSuccess) return e;
     const int slabs = static_cast<int>((d + 32 * VEC - 1) / (32 * VEC));
+    // the chunks set the order of the sums: by the warps of aligned rows, whatever these are
+    const int vec = vec_of(sizeof(T), d, 32, {});
+    const int64_t full_slabs = (d + 32 * vec - 1) / (32 * vec);
     int L = MIN_CHUNK;
-    while (L < MAX_CHUNK && (n + L - 1) / L * slabs > FEW_WARPS) L *= 2;
+    while (L < MAX_CHUNK && (n + L - 1) / L * full_slabs > FEW_WARPS) L *= 2;
     const int64_t items = (n + L - 1) / L * slabs;
     const int64_t blocks = (items + EMBED_THREADS / 32 - 1) / (EMBED_THREADS / 32);
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
