@@ -141,7 +141,7 @@ def block_norm(x: torch.Tensor, h: torch.Tensor | None = None, gate: torch.Tenso
     with norm(v) = v / sqrt(mean(v^2) + eps) over the last axis.  x, h, gate
     (..., d); w_post, scale, w_pre float32 (d), None = ones; gate None: no gate.
     Returns (x_out, u).  h None: the norm before the first block, x_out is x.
-    next_norm=False: the last block, u is None.  out: x_out's tensor, may be x."""
+    next_norm=False: the last block, u is None.  out (with h): x_out's tensor, may be x."""
     x = _device_tensor(x, "x")
     if x.dim() < 1:
         raise ValueError("x must have shape (..., d)")
@@ -151,6 +151,8 @@ def block_norm(x: torch.Tensor, h: torch.Tensor | None = None, gate: torch.Tenso
     h, gate = _like(h, x, "h"), _like(gate, x, "gate")
     w_post, scale = _weight(w_post, d, x, "w_post"), _weight(scale, d, x, "scale")
     w_pre = _weight(w_pre, d, x, "w_pre")
+    if h is None and out is not None and out is not x:
+        raise ValueError("without h x_out is x: there is nothing for out")
     code = _storage(x)
     x_out = x if h is None else torch.empty_like(x) if out is None else _result(out, x.shape, x, "out")
     u = torch.empty_like(x) if next_norm else None
