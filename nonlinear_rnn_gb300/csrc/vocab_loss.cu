@@ -927,11 +927,22 @@ constexpr int FEW_MOST = 16, FEW_WARPS = 8;
 constexpr int few_v(int n) { return n > 4 ? 4 : 8; }   // rows of W of a warp: what the registers allow
 constexpr int FEW_X_BYTES = 160 * 1024;   // of the rows of x in shared memory
 
-template <int N, int VEC, typename Id>
+// GRAD: G of one piece of the vocabulary, as planes, from the same logits: were they
+// taken on the tensor cores, which add them up less exactly, the probabilities would
+// not add up to one with this lse (gradients of 16 rows of logits of 60 were 2e-5 off).
+struct FewGrad {
+    const float2 *grad;       // per kept row {lse log2(e), gl c}
+    __nv_bfloat16 *dl;        // [planes][..][pitch]
+    int64_t plane;
+    int pitch, col0, cols;
+};
+constexpr int FEW_G_ROWS = BK;   // rows of G that the products read as inner elements
+
+template <int N, int VEC, typename Id, bool GRAD>
 __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
     k_few_rows(const float *__restrict__ x, const float *__restrict__ W, const void *targets, int n,
                int d, int64_t V, int64_t ignore, float scale2, float2 *part, float *z_target, int2 *row,
-               int *kept) {
+               int *kept, const FewGrad grad) {
     extern __shared__ __align__(16) float few_x[];   // [N][pitch], zeros past n and d
     __shared__ int2 rows[FEW_MOST];
     constexpr float NEG_INF = -INFINITY;
@@ -940,10 +951,25 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
     const int pitch = (d + 32 * VEC - 1) / (32 * VEC) * (32 * VEC);
     dependents_may_launch();
     wait_for_prerequisites();
-    const int live = number_rows<FEW_WARPS * 32, Id>(targets, n, V, ignore, rows);
-    if (blockIdx.x == 0) {
-        if (static_cast<int>(threadIdx.x) < live) row[threadIdx.x] = rows[threadIdx.x];
-        if (threadIdx.x == 0) kept[0] = live, kept[1] = 0;
+    int live;
+    if (GRAD) {   // numbered by the gathering kernel
+        live = *kept;
+        if (static_cast<int>(threadIdx.x) < live) rows[threadIdx.x] = row[threadIdx.x];
+        // zeros in the rows that the products read besides
+        const int pieces = (grad.cols + BK - 1) / BK * (BK / 8);   // of 16 bytes, a row
+        for (int i = blockIdx.x * (FEW_WARPS * 32) + threadIdx.x; i < 3 * (FEW_G_ROWS - live) * pieces;
+             i += gridDim.x * (FEW_WARPS * 32)) {
+            const int r = i / pieces, c = i - r * pieces, pl = r / (FEW_G_ROWS - live);
+            const int64_t at = pl * grad.plane + static_cast<int64_t>(live + r - pl * (FEW_G_ROWS - live)) * grad.pitch;
+            *reinterpret_cast<uint4 *>(grad.dl + at + c * 8) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncthreads();
+    } else {
+        live = number_rows<FEW_WARPS * 32, Id>(targets, n, V, ignore, rows);
+        if (blockIdx.x == 0) {
+            if (static_cast<int>(threadIdx.x) < live) row[threadIdx.x] = rows[threadIdx.x];
+            if (threadIdx.x == 0) kept[0] = live, kept[1] = 0;
+        }
     }
     for (int i = threadIdx.x; i < N * pitch; i += FEW_WARPS * 32) {
         const int r = i / pitch, c = i - r * pitch;
@@ -953,8 +979,12 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
     // lane r < N: the reference and sum of row r over this warp's rows of W
     float ref = NEG_INF, sum = 0.f;
     const int my_target = lane < live ? rows[lane].y : -1;
+    const float2 mine_grad = GRAD && lane < live ? grad.grad[lane] : make_float2(0.f, 0.f);
     const int64_t step = static_cast<int64_t>(gridDim.x) * FEW_WARPS * FEW_V;
-    for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * FEW_WARPS + warp) * FEW_V; v0 < V; v0 += step) {
+    const int64_t v_begin = GRAD ? grad.col0 : 0, v_end = GRAD ? v_begin + grad.cols : V;
+    const int64_t v_stop = GRAD ? v_begin + (grad.cols + BK - 1) / BK * BK : V;   // zeros from v_end on
+    for (int64_t v0 = v_begin + (static_cast<int64_t>(blockIdx.x) * FEW_WARPS + warp) * FEW_V; v0 < v_stop; v0 += step) {
+        float G[FEW_V];
         float acc[FEW_V][N];
 #pragma unroll
         for (int q = 0; q < FEW_V; ++q)
@@ -967,7 +997,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
             for (int q = 0; q < FEW_V; ++q) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) w[q][e] = 0.f;
-                if (c < d && v0 + q < V) load_f32<float, VEC>(W + (v0 + q) * d + c, w[q]);
+                if (c < d && v0 + q < v_end) load_f32<float, VEC>(W + (v0 + q) * d + c, w[q]);
             }
 #pragma unroll
             for (int r = 0; r < N; ++r) {
@@ -1003,7 +1033,10 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
             }
             // row r's value to lane r
             const float mine = __shfl_sync(FULL_MASK, z[0], (lane % N) * (32 / N)) * scale2;
-            if (lane < N && v0 + q < V) {
+            if (GRAD) {
+                const float p = ex2_approx(mine - mine_grad.x) * mine_grad.y;
+                G[q] = v0 + q >= v_end ? 0.f : my_target == v0 + q ? p - mine_grad.y : p;
+            } else if (lane < N && v0 + q < V) {
                 if (my_target == v0 + q) z_target[lane] = mine;
                 const float most = fmaxf(ref, mine);
                 const float at = most == NEG_INF ? 0.f : most;
@@ -1011,7 +1044,25 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
                 ref = most;
             }
         }
+        if (GRAD && lane < live) {
+            __nv_bfloat16 *to = grad.dl + static_cast<int64_t>(lane) * grad.pitch + (v0 - v_begin);
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl) {
+                Pack<__nv_bfloat16, FEW_V> o;
+#pragma unroll
+                for (int q = 0; q < FEW_V; q += 2) {
+                    const __nv_bfloat162 h =
+                        pl == 0 ? finite_bf16x2(G[q], G[q + 1]) : __floats2bfloat162_rn(G[q], G[q + 1]);
+                    o.v[q] = __low2bfloat16(h);
+                    o.v[q + 1] = __high2bfloat16(h);
+                    G[q] -= __low2float(h);
+                    G[q + 1] -= __high2float(h);
+                }
+                *reinterpret_cast<Pack<__nv_bfloat16, FEW_V> *>(to + pl * grad.plane) = o;
+            }
+        }
     }
+    if (GRAD) return;
     if (lane < live) part[static_cast<int64_t>(lane) * (gridDim.x * FEW_WARPS) + blockIdx.x * FEW_WARPS + warp] = make_float2(ref, sum);
 }
 
@@ -1240,28 +1291,28 @@ bool few_rows(int64_t n, int64_t d, int dtype) {
     return dtype == NRNN_F32 && n <= FEW_MOST && few_size(n) * (d + 127) * 4 <= FEW_X_BYTES;
 }
 
-template <int N, int VEC, typename Id>
-cudaError_t launch_few(const Call &c, const Plan &p) {
+template <int N, int VEC, typename Id, bool GRAD>
+cudaError_t launch_few(const Call &c, const Plan &p, const FewGrad &grad) {
     constexpr int most = FEW_X_BYTES;
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_few_rows<N, VEC, Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        return cudaFuncSetAttribute(k_few_rows<N, VEC, Id, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     });
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(float) * N * (ceil_div(c.d, 32 * VEC) * 32 * VEC);
-    return launch_dependent(k_few_rows<N, VEC, Id>, FEW_CTAS, FEW_WARPS * 32, smem, c.stream,
+    return launch_dependent(k_few_rows<N, VEC, Id, GRAD>, FEW_CTAS, FEW_WARPS * 32, smem, c.stream,
                             static_cast<const float *>(c.x), static_cast<const float *>(c.W), c.targets,
                             static_cast<int>(c.n), static_cast<int>(c.d), c.V, c.ignore, c.scale * LOG2E,
                             reinterpret_cast<float2 *>(c.ws + p.part), reinterpret_cast<float *>(c.ws + p.z),
-                            reinterpret_cast<int2 *>(c.ws + p.row), reinterpret_cast<int *>(c.ws + p.kept));
+                            reinterpret_cast<int2 *>(c.ws + p.row), reinterpret_cast<int *>(c.ws + p.kept), grad);
 }
 
-template <typename Id> cudaError_t launch_few(const Call &c, const Plan &p) {
+template <typename Id, bool GRAD> cudaError_t launch_few(const Call &c, const Plan &p, const FewGrad &grad = {}) {
     const bool wide = c.d % 4 == 0 && (reinterpret_cast<uintptr_t>(c.W) & 15) == 0;
     switch (few_size(c.n)) {
-        case 1: return wide ? launch_few<1, 4, Id>(c, p) : launch_few<1, 1, Id>(c, p);
-        case 4: return wide ? launch_few<4, 4, Id>(c, p) : launch_few<4, 1, Id>(c, p);
-        default: return wide ? launch_few<16, 4, Id>(c, p) : launch_few<16, 1, Id>(c, p);
+        case 1: return wide ? launch_few<1, 4, Id, GRAD>(c, p, grad) : launch_few<1, 1, Id, GRAD>(c, p, grad);
+        case 4: return wide ? launch_few<4, 4, Id, GRAD>(c, p, grad) : launch_few<4, 1, Id, GRAD>(c, p, grad);
+        default: return wide ? launch_few<16, 4, Id, GRAD>(c, p, grad) : launch_few<16, 1, Id, GRAD>(c, p, grad);
     }
 }
 
@@ -1270,7 +1321,7 @@ int forward(const Call &c, float *loss, float *lse) {
     const Plan p = plan_for(c.n, c.d, c.V, c.dtype, reinterpret_cast<uintptr_t>(c.W) % 16 == 0, false);
     if constexpr (sizeof(T) == 4) {
         if (few_rows(c.n, c.d, c.dtype)) {
-            if (launch_few<Id>(c, p) != cudaSuccess) return NRNN_ERR_CUDA;
+            if (launch_few<Id, false>(c, p) != cudaSuccess) return NRNN_ERR_CUDA;
             return join_loss<Id>(c, p, FEW_CTAS * FEW_WARPS, loss, lse);
         }
     }
@@ -1339,8 +1390,15 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
         a.col0 = static_cast<int>(v0);
         a.M = -1; a.K = static_cast<int>(c.d);
         a.bn = tile_v; a.n_cols = cols;
-        if (gemm<DL, T>(xk, wk, gs, a, tiles_m * ceil_div(cols, tile_v), 0, c.stream) != cudaSuccess)
-            return NRNN_ERR_CUDA;
+        cudaError_t e;
+        if (few_rows(c.n, c.d, c.dtype)) {   // the form that the forward takes its logits in
+            const FewGrad few{a.grad, reinterpret_cast<__nv_bfloat16 *>(dl), p.rows_pad * p.piece,
+                              static_cast<int>(p.piece), a.col0, cols};
+            e = launch_few<int32_t, true>(c, p, few);   // (reads no ids)
+        } else {
+            e = gemm<DL, T>(xk, wk, gs, a, tiles_m * ceil_div(cols, tile_v), 0, c.stream);
+        }
+        if (e != cudaSuccess) return NRNN_ERR_CUDA;
         a.bn = p.d_bn; a.n_cols = a.d;
         a.K = cols;
         a.out = gx;
