@@ -7,6 +7,7 @@ import of this module fails."""
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from dataclasses import dataclass, field
@@ -164,6 +165,17 @@ def _space(given, nbytes: int, device, what: str = "workspace") -> torch.Tensor:
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _out(given, shape, dtype, device) -> torch.Tensor:
+    """The caller's result tensor, or a new one.  As _space: its address is written to
+    (a tensor of another shape with as many elements will do)."""
+    if given is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(given, torch.Tensor) or not given.is_cuda or not given.is_contiguous() \
+            or given.device.index != _index(device) or given.dtype != dtype or given.numel() != math.prod(shape):
+        raise ValueError(f"out must be a contiguous {tuple(shape)} tensor of {dtype} on {device}")
+    return given
+
+
 def _index(device) -> int:
     device = torch.device(device)
     return torch.cuda.current_device() if device.index is None else device.index
@@ -256,7 +268,7 @@ def newton_forward(preact: torch.Tensor, params, cu_seqlens=None, K: int = 3,
     dev = preact.device
     prm = params_tensor(params, d_h, dev)
     cu, S = _cu_device(cu_seqlens, B, T, dev)
-    H = out if out is not None else torch.empty((B, T, d_h), dtype=preact.dtype, device=dev)
+    H = _out(out, (B, T, d_h), preact.dtype, dev)
     if tuple(H.shape) != (B, T, d_h) or H.dtype != preact.dtype or not H.is_contiguous():
         raise ValueError("out has the wrong shape, dtype or layout")
     rho = torch.empty((), dtype=torch.float32, device=dev)
@@ -418,7 +430,7 @@ def newton_forward_x(x: torch.Tensor, W_x: torch.Tensor, params, cu_seqlens=None
     dev = x.device
     prm = params_tensor(params, d_h, dev)
     cu, S = _cu_device(cu_seqlens, B, T, dev)
-    H = out if out is not None else torch.empty((B, T, d_h), dtype=x.dtype, device=dev)
+    H = _out(out, (B, T, d_h), x.dtype, dev)
     rho = torch.empty((), dtype=torch.float32, device=dev)
     nbytes = lib.nrnn_newton_workspace_bytes(B, T, d_h, code, int(K), ALGOS["fused"])
     workspace = _space(workspace, max(nbytes, 256), dev)
@@ -473,7 +485,7 @@ def picard(preact: torch.Tensor, params, sweeps: int, cu_seqlens=None,
     dev = preact.device
     prm = params_tensor(params, d_h, dev)
     cu, S = _cu_device(cu_seqlens, B, T, dev)
-    G = out if out is not None else torch.empty((B, T, d_h), dtype=preact.dtype, device=dev)
+    G = _out(out, (B, T, d_h), preact.dtype, dev)
     tmp = torch.empty_like(G) if sweeps >= 2 else None
     with torch.cuda.device(dev):
         st = lib.nrnn_picard(_ptr(preact), _dtype_code(preact), _ptr(prm), B, T, d_h, _ptr(cu), S,
@@ -493,7 +505,7 @@ def sequential_forward(preact: torch.Tensor, params, cu_seqlens=None,
     dev = preact.device
     prm = params_tensor(params, d_h, dev)
     cu, S = _cu_device(cu_seqlens, B, T, dev)
-    H = out if out is not None else torch.empty((B, T, d_h), dtype=preact.dtype, device=dev)
+    H = _out(out, (B, T, d_h), preact.dtype, dev)
     with torch.cuda.device(dev):
         st = lib.nrnn_sequential_forward(_ptr(preact), _dtype_code(preact), _ptr(prm), B, T, d_h,
                                          _ptr(cu), S, _ptr(H), _stream(dev))
@@ -526,7 +538,7 @@ def decode_step(params, h: torch.Tensor | None = None, preact: torch.Tensor | No
         h = _device_tensor(h, "h")
         if tuple(h.shape) != (slots, d_h) or h.dtype != src.dtype:
             raise ValueError("h must be (slots, d_h) in the input dtype")
-    H = out if out is not None else torch.empty((slots, d_h), dtype=src.dtype, device=dev)
+    H = _out(out, (slots, d_h), src.dtype, dev)
     with torch.cuda.device(dev):
         if preact is not None:
             st = lib.nrnn_decode_step(_ptr(src), _dtype_code(src), _ptr(prm), slots, d_h, _ptr(h),
@@ -587,7 +599,7 @@ def input_projection(x: torch.Tensor, W_x: torch.Tensor, out: torch.Tensor | Non
     if W_x.shape[1] != d_in or n_out % 3:
         raise ValueError("W_x must have shape (3 d_h, d_in)")
     rows = x.numel() // d_in
-    P = out if out is not None else torch.empty((*x.shape[:-1], n_out), dtype=x.dtype, device=x.device)
+    P = _out(out, (*x.shape[:-1], n_out), x.dtype, x.device)
     code = _dtype_code(x)
     nbytes = lib.nrnn_input_projection_workspace_bytes(code, d_in, n_out // 3)
     if nbytes > 0:

@@ -50,3 +50,35 @@ def test_calls_refuse_buffers_that_are_not_theirs():
         call(torch.empty(room, dtype=torch.uint8, device="cuda"))
         call(None)
     torch.cuda.synchronize()
+
+
+def test_a_host_result_tensor_is_refused():
+    with pytest.raises(ValueError):
+        _binding._out(torch.empty(2, 3), (2, 3), torch.float32, torch.device("cuda:0"))
+
+
+@pytest.mark.gpu
+def test_calls_refuse_result_tensors_that_are_not_theirs():
+    t = dict(device="cuda")
+    P, prm = torch.zeros(1, 70, 96, **t), torch.ones(6, 32)
+    x, W = torch.ones(5, 16, **t), torch.ones(48, 16, **t)
+    xb, Wb = torch.ones(1, 70, 32, dtype=torch.bfloat16, **t), torch.ones(96, 32, dtype=torch.bfloat16, **t)
+    f32, b16 = torch.float32, torch.bfloat16
+    cases = {
+        "newton_forward": (lambda o: nr.newton_forward(P, prm, check=False, out=o), (1, 70, 32), f32),
+        "newton_forward_x": (lambda o: nr.newton_forward_x(xb, Wb, prm, check=False, out=o), (1, 70, 32), b16),
+        "picard": (lambda o: nr.picard(P, prm, 2, out=o), (1, 70, 32), f32),
+        "sequential_forward": (lambda o: nr.sequential_forward(P, prm, out=o), (1, 70, 32), f32),
+        "decode_step": (lambda o: nr.decode_step(prm, preact=P[0, :5], out=o), (5, 32), f32),
+        "input_projection": (lambda o: nr.input_projection(x, W, out=o), (5, 48), f32),
+    }
+    for name, (call, shape, dtype) in cases.items():
+        numel = torch.Size(shape).numel()
+        for bad in (torch.empty(shape, dtype=dtype), torch.empty(1, dtype=dtype, **t).expand(shape),
+                    torch.empty(numel - 1, dtype=dtype, **t), torch.empty(shape, dtype=torch.float16, **t),
+                    torch.empty(2 * numel, dtype=dtype, **t)[::2].view(shape)):
+            with pytest.raises(ValueError):
+                call(bad)
+                pytest.fail(name)
+        call(torch.empty(shape, dtype=dtype, **t))
+    torch.cuda.synchronize()
