@@ -104,7 +104,9 @@ struct GemmArgs {
     float *parts;             // GX, GW: [pairs][2][BM][bn] sums of cut tiles
     float scale;              // logit scale c
     const int2 *row;          // per kept row {its row in x, its target}
-    const float2 *grad;       // DL: per kept row {lse log2(e), gl c}
+    const float2 *grad;       // DL: per kept row {lse log2(e), gl c / back}
+    const float *back;        // GX, GW of bf16: what G was divided by
+    int g_planes;             // bf16: planes of G, 1 or 2
     float2 *part;             // LSE: [rows][groups][2] {maximum, sum} in base 2
     float *z_target;          // LSE: base-2 logit of the target
     void *out;                // GX, GW: the gradient in the storage type
@@ -168,6 +170,12 @@ template <typename T> __device__ __forceinline__ void store_cols(T *p, const flo
         for (int c = 0; c < PIECE; ++c)
             if (c < n) p[c] = from_f32<T>(v[c]);
     }
+}
+
+__device__ __forceinline__ void times(float (&v)[PIECE], float f) {
+    float2 *p = reinterpret_cast<float2 *>(v);
+#pragma unroll
+    for (int e = 0; e < PIECE / 2; ++e) p[e] = mul2(p[e], make_float2(f, f));
 }
 
 // Two values as bf16, the nearest; or the type's largest where that is an infinity,
@@ -254,7 +262,8 @@ template <int FORM> struct Walk {
 
 // PIECE (or fewer: n) columns from c of row m of the GX or GW product to their place
 template <int FORM, typename T>
-__device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m, int c, float (&v)[PIECE], int n) {
+__device__ __forceinline__ void store_product(const GemmArgs &a, int kept, float back, int m, int c, float (&v)[PIECE],
+                                              int n) {
     int64_t row;
     if (FORM == GX) {
         if (m >= kept) return;
@@ -275,6 +284,7 @@ __device__ __forceinline__ void store_product(const GemmArgs &a, int kept, int m
         if (m >= a.M) return;
         row = static_cast<int64_t>(a.col0) + m;
     }
+    if (sizeof(T) == 2) times(v, back);
     const bool wide = a.d % (16 / sizeof(T)) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
     store_cols<T>(static_cast<T *>(a.out) + row * a.d + c, v, n, wide);
 }
@@ -355,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         const bool is_a = lane < BOXES_A;
         const bool copies = is_a ? rank == 0 || !few : lane < BOXES_A + boxes_b;
         const int box = is_a ? lane : lane - BOXES_A;
+        const int twice = !SPLIT && (FORM == GX || FORM == GW) ? a.g_planes : 1;   // G's planes, smaller first
         const bool mn = is_a ? MN_A : MN_B;
         const uint32_t offset = (is_a ? 0 : A_BYTES) + box * (64 * BK * 2);
         int it = 0;
@@ -368,8 +379,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 for (int c0 = t.k0; go && c0 < t.k1;) {
                     const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
                     for (int p = 0; go && p < PASSES; ++p) {
-                        const int plane = SPLIT ? (is_a ? PLANE_A[p] : PLANE_B[p]) : 0;
-                        for (int k = c0; k < c1; ++k, ++it) {
+                        int plane = SPLIT ? (is_a ? PLANE_A[p] : PLANE_B[p]) : 0;
+                        for (int i = 0; i < (c1 - c0) * twice; ++i, ++it) {
+                            int k = c0 + i;
+                            if (!SPLIT && twice == 2) {
+                                k = c0 + (i >> 1);
+                                plane = is_a ? 1 - (i & 1) : 0;
+                            }
                             const int s = it % STAGES;
                             if (it >= STAGES)
                                 go = __all_sync(FULL_MASK, wait_or_abort(a, &empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort));
@@ -401,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     if (phase >= 2) go = wait_or_abort(a, &acce_bar[buf], ((phase >> 1) - 1) & 1, &s_abort);
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t d = tmem + buf * BN;
-                    const int its = (c1 - c0) * PASSES;
+                    const int its = (c1 - c0) * PASSES * (!SPLIT && (FORM == GX || FORM == GW) ? a.g_planes : 1);
                     for (int i = 0; go && i < its; ++i, ++it) {
                         const int s = it % STAGES;
                         go = wait_or_abort(a, &full_bar[s], (it / STAGES) & 1, &s_abort);
@@ -434,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         const float scale2 = a.scale * LOG2E;
         constexpr float NEG_INF = -INFINITY;
         const float nan = __int_as_float(0x7fffffff);
+        const float back = !SPLIT && (FORM == GX || FORM == GW) ? *a.back : 1.f;
         int phase = 0;
         bool ok = true;   // false once a wait gave up: NaN from there on
         auto release = [&](int buf) {   // this warp has read the accumulator
@@ -441,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             __syncwarp();
             if (lane == 0 && ok) mbar_arrive_cluster(cluster_addr(&acce_bar[buf], 0));
         };
-        auto accumulator = [&](int buf, uint32_t parity) {   // the same outcome for the whole warp
+        auto accumulator = [&](int buf, uint32_t parity) {
             ok &= wait_or_abort(a, &accf_bar[buf], parity, &s_abort);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         };
@@ -465,8 +482,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             float2 sum[2] = {};
 
             // the warp's 32 x PIECE block, rounded to bf16, to column x and row y of tmOut;
-            // v keeps what rounding leaves (fp32: the next plane)
-            auto store_block = [&](float (&v)[PIECE], int x, int y, int plane) {
+            // with more planes than one, v keeps what rounding leaves for the next
+            auto store_block = [&](float (&v)[PIECE], int x, int y, int plane, auto planes) {
+                constexpr bool MORE = decltype(planes)::value > 1;
                 if (lane == 0) bulk_wait_read<0>();   // the store before has read the block
                 __syncwarp();
 #pragma unroll
@@ -477,9 +495,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     for (int e = 0; e < 4; ++e) {
                         float &lo = v[q * 8 + 2 * e], &hi = v[q * 8 + 2 * e + 1];
                         const __nv_bfloat162 h2 =
-                            SPLIT && plane == 0 ? finite_bf16x2(lo, hi) : __floats2bfloat162_rn(lo, hi);
+                            MORE && plane == 0 ? finite_bf16x2(lo, hi) : __floats2bfloat162_rn(lo, hi);
                         o[e] = *reinterpret_cast<const uint32_t *>(&h2);
-                        if (SPLIT) {
+                        if (MORE) {
                             lo -= __low2float(h2);
                             hi -= __high2float(h2);
                         }
@@ -543,17 +561,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     if (!ok)
 #pragma unroll
                         for (int e = 0; e < PIECE; ++e) v[e] = nan;
+                    using std::integral_constant;
+                    const int x = n0 + c, y = t.m0 + in_tile;
+                    if (SPLIT) {
 #pragma unroll
-                    for (int pl = 0; pl < (SPLIT ? 3 : 1); ++pl) store_block(v, n0 + c, t.m0 + in_tile, pl);
+                        for (int pl = 0; pl < 3; ++pl) store_block(v, x, y, pl, integral_constant<int, 3>{});
+                    } else if (a.g_planes == 2) {
+#pragma unroll
+                        for (int pl = 0; pl < 2; ++pl) store_block(v, x, y, pl, integral_constant<int, 2>{});
+                    } else {
+                        store_block(v, x, y, 0, integral_constant<int, 1>{});
+                    }
                 } else {
                     if (!ok)
 #pragma unroll
                         for (int e = 0; e < PIECE; ++e) v[e] = nan;
                     const int n = min(left, PIECE);
                     if (FORM == GW && !SPLIT && a.blocks_out && t.slot < 0) {
-                        if (t.m0 + in_tile < a.M) store_block(v, n0 + c, a.col0 + t.m0 + in_tile, 0);
+                        times(v, back);
+                        if (t.m0 + in_tile < a.M)
+                            store_block(v, n0 + c, a.col0 + t.m0 + in_tile, 0, std::integral_constant<int, 1>{});
                     } else if (t.slot < 0) {
-                        store_product<FORM, T>(a, kept, m, n0 + c, v, n);
+                        store_product<FORM, T>(a, kept, back, m, n0 + c, v, n);
                     } else {
                         float *to = a.parts + ((static_cast<int64_t>(pair) * 2 + t.slot) * BM + in_tile + lane) * a.bn + c;
                         store_cols<float>(to, v, n, n % 4 == 0);
@@ -725,6 +754,11 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a
     } else {
         at = (static_cast<int64_t>(a.col0) + m) * a.d + col;
     }
+    if (sizeof(T) == 2) {
+        const float back = *a.back;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= back;
+    }
     T *to = static_cast<T *>(a.out) + at;
     if (a.d % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
 #pragma unroll
@@ -816,6 +850,7 @@ struct GatherArgs {
     const float *lse, *gl;
     float scale;
     float2 *grad;
+    float *back;              // bf16: see mantissa_of
     void *gx;
     const void *targets;
     int64_t V, ignore;
@@ -827,6 +862,17 @@ struct GatherArgs {
 __device__ __forceinline__ float plane_of(float v) {
     const float h = __bfloat162float(__float2bfloat16_rn(v));
     return isinf(h) ? __bfloat162float(__float2bfloat16_rz(v)) : h;
+}
+
+// The mantissa, in [1, 2), of a finite value that is not zero or subnormal; else 1.
+// A bf16 G is divided by the mantissa of the first kept row's dL/dloss c, and its two
+// products are multiplied by it at their end.  Where all rows have the same dL/dloss
+// (a mean), their largest entries are then 1 - p times a power of two.  With the
+// mantissa, entries of rows of small p would all be close to one value and be rounded
+// alike: for 15 rows gx was off by 2.05 times what rounding it costs, now 1.28.
+__device__ __forceinline__ float mantissa_of(float v) {
+    const uint32_t bits = __float_as_uint(v), exponent = bits >> 23 & 0xffu;
+    return exponent == 0 || exponent == 255 ? 1.f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
 }
 
 // One row of `pitch` values (a multiple of 8) as bf16 planes, by the lanes of a warp;
@@ -885,6 +931,11 @@ __global__ void __launch_bounds__(GATHER_THREADS) k_gather_rows(const GatherArgs
         kept = *a.kept;
     }
     const bool wide = wide_rows<T>(a.x, a.d);
+    float back = 1.f;
+    if (sizeof(T) == 2 && a.grad != nullptr) {
+        if (kept > 0) back = mantissa_of(a.gl[rows[0].x] * a.scale);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.back = back;
+    }
     const int padded = (kept + BM - 1) / BM * BM;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t m = blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows_pad; m += warps) {
@@ -893,7 +944,7 @@ __global__ void __launch_bounds__(GATHER_THREADS) k_gather_rows(const GatherArgs
             copy_row<T>(src >= 0 ? static_cast<const T *>(a.x) + static_cast<int64_t>(src) * a.d : nullptr,
                         a.out + m * a.pitch, a.rows_pad * a.pitch, a.d, a.pitch, lane, wide);
             if (a.grad != nullptr && m < kept && lane == 0)
-                a.grad[m] = make_float2(a.lse[src] * LOG2E, a.gl[src] * a.scale);
+                a.grad[m] = make_float2(a.lse[src] * LOG2E, a.gl[src] * a.scale / back);
         }
         if (a.gx != nullptr && m < a.n) {
             const int64_t id = static_cast<int64_t>(static_cast<const Id *>(a.targets)[m]);
@@ -1121,7 +1172,7 @@ int rows_of_x(int64_t n) { return n < HALF_M ? static_cast<int>(ceil_div(n, 8) *
 
 // The sizes a call works with, the same for the workspace query and the call.
 struct Plan {
-    int planes, pitch, d_bn, fwd_bn;
+    int planes, g_planes, pitch, d_bn, fwd_bn;
     int64_t rows_pad;
     bool copy_w;
     int64_t piece;        // backward: vocabulary rows of a piece
@@ -1134,6 +1185,12 @@ int few_size(int64_t n) { return n <= 1 ? 1 : n <= 4 ? 4 : FEW_MOST; }   // rows
 
 // bytes the piece of G may take
 constexpr int64_t PIECE_BYTES = 1ll << 30;
+
+// Rows up to which a bf16 G is kept as two planes, to 2^-16: the roundings of so few
+// rows' largest entries need not average out (4 rows: gx off by up to 1.54 times what
+// rounding it costs, 1.00 with two planes).  It takes another 256-row product of each
+// slice of W where reading W bounds the call; above, that would be paid in full.
+constexpr int TWO_PLANES_MOST = 64;
 
 // Columns of the forward's tiles.  With enough tiles the widest; with few, the width
 // that leaves the busiest pair the least to do: a tile costs its columns and, for
@@ -1157,6 +1214,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
     Plan p{};
     const bool split = dtype == NRNN_F32;
     p.planes = split ? 3 : 1;
+    p.g_planes = split ? 3 : n <= TWO_PLANES_MOST ? 2 : 1;
     p.pitch = static_cast<int>((d + 7) / 8 * 8);
     p.rows_pad = ceil_div(n, BM) * BM;
     p.copy_w = split || d % 8 != 0 || !w_aligned;
@@ -1175,7 +1233,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
         at += up256(bytes);
         return o;
     };
-    p.kept = take(2 * sizeof(int));   // first of all: the error word is the workspace's second
+    p.kept = take(3 * sizeof(int));   // {number, error, back}; first of all: the header names the error's place
     p.row = take(sizeof(int2) * n);
     p.x = take(sizeof(__nv_bfloat16) * p.planes * p.rows_pad * p.pitch);
     p.w = take(p.copy_w ? sizeof(__nv_bfloat16) * p.planes * V * p.pitch : 0);
@@ -1186,11 +1244,11 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
     } else {
         p.grad = take(sizeof(float2) * n);
         const int64_t all = ceil_div(V, BN) * BN;
-        p.piece = PIECE_BYTES / (2 * p.planes * p.rows_pad) / BN * BN;
+        p.piece = PIECE_BYTES / (2 * p.g_planes * p.rows_pad) / BN * BN;
         p.piece = p.piece < 2048 ? 2048 : p.piece;
         p.piece = p.piece > all ? all : p.piece;
         p.pieces = static_cast<int>(ceil_div(V, p.piece));
-        p.dl = take(sizeof(__nv_bfloat16) * p.planes * p.rows_pad * p.piece);
+        p.dl = take(sizeof(__nv_bfloat16) * p.g_planes * p.rows_pad * p.piece);
         p.parts = take(sizeof(float) * 2 * PAIRS * BM * p.d_bn);
         p.acc = take(p.pieces > 1 ? sizeof(float) * p.rows_pad * p.pitch : 0);
     }
@@ -1252,6 +1310,7 @@ cudaError_t lay_out(const Call &c, const Plan &p, const float *lse, const float 
     g.rows_pad = p.rows_pad; g.d = static_cast<int>(c.d); g.pitch = p.pitch;
     g.lse = lse; g.gl = gl; g.scale = c.scale;
     g.grad = lse != nullptr ? reinterpret_cast<float2 *>(c.ws + p.grad) : nullptr;
+    g.back = reinterpret_cast<float *>(kept + 2);
     g.gx = gx; g.targets = c.targets; g.V = c.V; g.ignore = c.ignore; g.n = static_cast<int>(c.n);
     const int64_t want = p.rows_pad / (GATHER_THREADS / 32);
     const unsigned blocks = static_cast<unsigned>(want < 4864 ? want : 4864);
@@ -1358,11 +1417,11 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
     constexpr int tile_v = BN;
     if (!make_map_planes(&xk, x, p.pitch, p.rows_pad, p.planes, BK, rows_of_x(c.n), true) ||
         !make_map_planes(&wk, w, p.pitch, c.V, p.planes, BK, tile_v / 2, true) ||
-        !make_map_planes(&gk, dl, p.piece, p.rows_pad, p.planes, BK, HALF_M, true) ||
+        !make_map_planes(&gk, dl, p.piece, p.rows_pad, p.g_planes, BK, HALF_M, true) ||
         !make_map_planes(&wn, w, p.pitch, c.V, p.planes, 64, BK, true) ||
-        !make_map_planes(&gn, dl, p.piece, p.rows_pad, p.planes, 64, BK, true) ||
+        !make_map_planes(&gn, dl, p.piece, p.rows_pad, p.g_planes, 64, BK, true) ||
         !make_map_planes(&xn, x, p.pitch, p.rows_pad, p.planes, 64, BK, true) ||
-        !make_map_planes(&gs, dl, p.piece, p.rows_pad, p.planes, PIECE, BOX_ROWS, true))
+        !make_map_planes(&gs, dl, p.piece, p.rows_pad, p.g_planes, PIECE, BOX_ROWS, true))
         return NRNN_ERR_CUDA;
     // blocks of 64 columns: the tiles have to be whole blocks, so that none reaches into
     // the next tile's columns (past gW's ends TMA writes nothing)
@@ -1379,6 +1438,8 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
     a.a_rows = rows_of_x(c.n);
     a.row = reinterpret_cast<int2 *>(c.ws + p.row);
     a.grad = reinterpret_cast<float2 *>(c.ws + p.grad);
+    a.back = reinterpret_cast<float *>(c.ws + p.kept) + 2;
+    a.g_planes = p.g_planes;
     a.d = static_cast<int>(c.d);
     a.parts = reinterpret_cast<float *>(c.ws + p.parts);
     a.acc = reinterpret_cast<float *>(c.ws + p.acc);
