@@ -39,9 +39,11 @@
 // product is the six plane products above 2^-24 relative, smallest first:
 // (lo,hi) (mid,mid) (hi,lo) (mid,hi) (hi,mid) (hi,hi).  (An infinity leaves
 // no number, so in W or in a kept row it counts as NaN.)  The tensor cores add less
-// exactly than fp32 rounding does (bf16 logits of 1024 products: lse 3e-7 off, fp32
-// products 4e-8), so an accumulator takes at most 512 elements of the inner
-// dimension before the epilogue adds it to fp32 registers.
+// exactly than fp32 rounding does: every step of 16 drops what lies below the running
+// sum's last bit (bf16 logits of 1024 products: lse 3e-7 off, fp32 products 4e-8).  So
+// an accumulator takes at most 256 elements of the inner dimension before the epilogue
+// adds it to fp32 registers.  (3001 rows over 10007 x 250: 512 elements gx 8.0e-7 off,
+// 256 4.5e-7 in the same time, 128 2.7e-7 in 2% more; fp32 products 7.6e-7.)
 //
 // Measured: 16384 rows over 65536 x 1024 bf16 with gradient 5.2 to 5.6 ms (1.56 to
 // 1.68 PFLOP/s; cuBLAS runs at 1.75 when kept up: the power limit holds the clocks at
@@ -83,7 +85,7 @@ constexpr int GEMM_THREADS = 128 + EPI_WARPS * 32;
 constexpr int PIECE = 64;                                  // columns that an epilogue warp takes at a time
 constexpr int BOX_ROWS = 32, BOX_BYTES = BOX_ROWS * PIECE * 2;   // a stored block of G
 constexpr size_t GEMM_SMEM = STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + 1024;
-constexpr int SPLIT_CHUNK = 8;     // fp32: 64-wide slices per accumulator
+constexpr int SPLIT_CHUNK = 4;     // fp32: 64-wide slices per accumulator
 constexpr int SEGMENTS = 6;        // fp32: plane products, smallest first
 __device__ constexpr int PLANE_A[SEGMENTS] = {2, 1, 0, 1, 0, 0};
 __device__ constexpr int PLANE_B[SEGMENTS] = {0, 1, 2, 0, 1, 0};
