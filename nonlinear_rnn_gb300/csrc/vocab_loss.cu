@@ -106,11 +106,11 @@ struct GemmArgs {
     float *parts;             // GX, GW: [pairs][2][BM][bn] sums of cut tiles
     float scale;              // logit scale c
     const int2 *row;          // per kept row {its row in x, its target}
-    const float2 *grad;       // DL: per kept row {lse log2(e), gl c / back}
+    const float4 *grad;       // DL: per kept row, see row_grad
     const float *back;        // GX, GW of bf16: what G was divided by
     int g_planes;             // bf16: planes of G, 1 or 2
     float2 *part;             // LSE: [rows][groups][2] {maximum, sum} in base 2
-    float *z_target;          // LSE: base-2 logit of the target
+    float *z_target;          // LSE: the target's product <x, W_t>
     void *out;                // GX, GW: the gradient in the storage type
     float *acc;               // GX: [rows][acc_pitch] sums over the pieces, if there are several
     int acc_pitch;
@@ -469,13 +469,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             const int m = t.m0 + in_tile + lane;   // this thread's row of the product
             // LSE, DL: the row's constants
             int target = -1;
-            float lse2 = 0.f, gl = 0.f;
+            float lse2 = 0.f, gl = 0.f, gl_p = 0.f;
             if ((FORM == LSE || FORM == DL) && m < kept) {
                 target = a.row[m].y - a.col0;
                 if (FORM == DL) {
-                    const float2 g = a.grad[m];
+                    const float4 g = a.grad[m];
                     lse2 = g.x;
                     gl = g.y;
+                    gl_p = g.z;
                 }
             }
             // LSE: running maximum and sums.  Four chains each: one alone waits for
@@ -521,8 +522,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 const int left = min(a.n_cols - n0, a.bn) - c;   // valid columns
                 if (left <= 0 && FORM != DL) return;
                 if (FORM == LSE) {
-#pragma unroll
-                    for (int e = 0; e < PIECE / 2; ++e) p[e] = mul2(p[e], make_float2(scale2, scale2));
+                    // Sums of 2^(z scale2 - ref), the product not rounded by itself (as in DL, whose
+                    // probabilities would not add up to one with this lse else: by 3e-6 at a logit
+                    // of 48).  The reference is the largest scaled logit, rounded, or near it.
                     const int at = target - n0 - c;
                     if (at >= 0 && at < min(left, PIECE)) {
                         float z = 0.f;
@@ -530,28 +532,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                         for (int e = 0; e < PIECE; ++e) z = e == at ? v[e] : z;
                         a.z_target[m] = z;
                     }
+                    if (scale2 < 0.f)
+#pragma unroll
+                        for (int e = 0; e < PIECE; ++e) v[e] = -v[e];
+                    const float s2 = fabsf(scale2);
                     if (left < PIECE)
 #pragma unroll
                         for (int e = 0; e < PIECE; ++e) v[e] = e < left ? v[e] : NEG_INF;
-                    float up[4] = {mx, NEG_INF, NEG_INF, NEG_INF};
+                    float up[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
                     for (int e = 0; e < PIECE; ++e) up[e % 4] = fmaxf(up[e % 4], v[e]);
-                    const float most = fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3]));
+                    const float most = fmaxf(mx, fmaxf(fmaxf(up[0], up[1]), fmaxf(up[2], up[3])) * s2);
                     const float ref = most == NEG_INF ? 0.f : most;
                     const float keep = ex2_approx(mx - ref);
                     mx = most;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) sum[q] = mul2(sum[q], make_float2(keep, keep));
+                    if (left < PIECE) {   // what is outside adds nothing (also at a scale of zero)
 #pragma unroll
-                    for (int e = 0; e < PIECE / 2; ++e) {
-                        const float2 x = add2(p[e], make_float2(-ref, -ref));
-                        sum[e % 2] = add2(sum[e % 2], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                        for (int e = 0; e < PIECE; ++e) {
+                            const float x = e < left ? ex2_approx(fmaf(v[e], s2, -ref)) : 0.f;
+                            (e % 2 == 0 ? sum[e / 2 % 2].x : sum[e / 2 % 2].y) += x;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < PIECE / 2; ++e) {
+                            const float2 x = fma2(p[e], make_float2(s2, s2), make_float2(-ref, -ref));
+                            sum[e % 2] = add2(sum[e % 2], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                        }
                     }
                 } else if (FORM == DL) {
 #pragma unroll
                     for (int e = 0; e < PIECE / 2; ++e) {
                         const float2 x = fma2(p[e], make_float2(scale2, scale2), make_float2(-lse2, -lse2));
-                        p[e] = mul2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(gl, gl));
+                        p[e] = mul2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(gl_p, gl_p));
                     }
                     const int at = target - n0 - c;
                     if (at >= 0 && at < PIECE)
@@ -851,7 +865,7 @@ struct GatherArgs {
     int d, pitch;
     const float *lse, *gl;
     float scale;
-    float2 *grad;
+    float4 *grad;
     float *back;              // bf16: see mantissa_of
     void *gx;
     const void *targets;
@@ -875,6 +889,15 @@ __device__ __forceinline__ float plane_of(float v) {
 __device__ __forceinline__ float mantissa_of(float v) {
     const uint32_t bits = __float_as_uint(v), exponent = bits >> 23 & 0xffu;
     return exponent == 0 || exponent == 255 ? 1.f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+}
+
+// A kept row's constants of the DL form: {l = lse log2(e), g, g 2^(l - lse log2(e))} with
+// g = gl c / back.  What rounding l leaves out is put into the factor of p, whose sum
+// would be off by it (1e-6 at an lse of 20).
+__device__ __forceinline__ float4 row_grad(float lse, float g) {
+    constexpr float LOG2E_LOW = 1.92596303e-8f;   // log2(e) less LOG2E
+    const float l = lse * LOG2E, low = fmaf(lse, LOG2E, -l) + lse * LOG2E_LOW;
+    return make_float4(l, g, isfinite(low) ? fmaf(-low * LN2, g, g) : g, 0.f);
 }
 
 // One row of `pitch` values (a multiple of 8) as bf16 planes, by the lanes of a warp;
@@ -946,7 +969,7 @@ __global__ void __launch_bounds__(GATHER_THREADS) k_gather_rows(const GatherArgs
             copy_row<T>(src >= 0 ? static_cast<const T *>(a.x) + static_cast<int64_t>(src) * a.d : nullptr,
                         a.out + m * a.pitch, a.rows_pad * a.pitch, a.d, a.pitch, lane, wide);
             if (a.grad != nullptr && m < kept && lane == 0)
-                a.grad[m] = make_float2(a.lse[src] * LOG2E, a.gl[src] * a.scale / back);
+                a.grad[m] = row_grad(a.lse[src], a.gl[src] * a.scale / back);
         }
         if (a.gx != nullptr && m < a.n) {
             const int64_t id = static_cast<int64_t>(static_cast<const Id *>(a.targets)[m]);
@@ -984,7 +1007,7 @@ constexpr int FEW_X_BYTES = 160 * 1024;   // of the rows of x in shared memory
 // taken on the tensor cores, which add them up less exactly, the probabilities would
 // not add up to one with this lse (gradients of 16 rows of logits of 60 were 2e-5 off).
 struct FewGrad {
-    const float2 *grad;       // per kept row {lse log2(e), gl c}
+    const float4 *grad;       // per kept row, see row_grad
     __nv_bfloat16 *dl;        // [planes][..][pitch]
     int64_t plane;
     int pitch, col0, cols;
@@ -1032,7 +1055,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
     // lane r < N: the reference and sum of row r over this warp's rows of W
     float ref = NEG_INF, sum = 0.f;
     const int my_target = lane < live ? rows[lane].y : -1;
-    const float2 mine_grad = GRAD && lane < live ? grad.grad[lane] : make_float2(0.f, 0.f);
+    const float4 mine_grad = GRAD && lane < live ? grad.grad[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
     const int64_t step = static_cast<int64_t>(gridDim.x) * FEW_WARPS * FEW_V;
     const int64_t v_begin = GRAD ? grad.col0 : 0, v_end = GRAD ? v_begin + grad.cols : V;
     const int64_t v_stop = GRAD ? v_begin + (grad.cols + BK - 1) / BK * BK : V;   // zeros from v_end on
@@ -1085,15 +1108,15 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, N > 4 ? 1 : 2)
                 }
             }
             // row r's value to lane r
-            const float mine = __shfl_sync(FULL_MASK, z[0], (lane % N) * (32 / N)) * scale2;
+            const float mine = __shfl_sync(FULL_MASK, z[0], (lane % N) * (32 / N));
             if (GRAD) {
-                const float p = ex2_approx(mine - mine_grad.x) * mine_grad.y;
+                const float p = ex2_approx(fmaf(mine, scale2, -mine_grad.x)) * mine_grad.z;
                 G[q] = v0 + q >= v_end ? 0.f : my_target == v0 + q ? p - mine_grad.y : p;
             } else if (lane < N && v0 + q < V) {
                 if (my_target == v0 + q) z_target[lane] = mine;
-                const float most = fmaxf(ref, mine);
+                const float most = fmaxf(ref, mine * scale2);
                 const float at = most == NEG_INF ? 0.f : most;
-                sum = sum * ex2_approx(ref - at) + ex2_approx(mine - at);
+                sum = sum * ex2_approx(ref - at) + ex2_approx(fmaf(mine, scale2, -at));
                 ref = most;
             }
         }
@@ -1125,7 +1148,7 @@ template <typename Id>
 __global__ void __launch_bounds__(256)
     k_loss_join(const float2 *__restrict__ part, int groups, const float *__restrict__ z_target,
                 const int2 *__restrict__ row, const int *__restrict__ kept, const void *targets, int n,
-                int64_t V, int64_t ignore, float *__restrict__ loss, float *__restrict__ lse) {
+                int64_t V, int64_t ignore, float scale2, float *__restrict__ loss, float *__restrict__ lse) {
     wait_for_prerequisites();
     const int lane = threadIdx.x & 31;
     const int64_t m = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -1148,11 +1171,11 @@ __global__ void __launch_bounds__(256)
             s = s * ex2_approx(mx - ref) + os * ex2_approx(om - ref);
             mx = up;
         }
-        if (lane == 0) {
-            const float l2 = mx + log2f(s);
+        if (lane == 0) {   // one rounding of lse at its own size: the backward's p takes it all
+            const float ln_s = logf(s);
             const int i = row[m].x;
-            lse[i] = l2 * LN2;
-            loss[i] = (l2 - z_target[m]) * LN2;
+            lse[i] = fmaf(mx, LN2, ln_s);
+            loss[i] = fmaf(fmaf(-z_target[m], scale2, mx), LN2, ln_s);
         }
     }
     const int64_t id = static_cast<int64_t>(static_cast<const Id *>(targets)[m]);
@@ -1244,7 +1267,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t V, int dtype, bool w_aligned, bool b
         p.part = take(sizeof(float2) * n * parts);
         p.z = take(sizeof(float) * n);
     } else {
-        p.grad = take(sizeof(float2) * n);
+        p.grad = take(sizeof(float4) * n);
         const int64_t all = ceil_div(V, BN) * BN;
         p.piece = PIECE_BYTES / (2 * p.g_planes * p.rows_pad) / BN * BN;
         p.piece = p.piece < 2048 ? 2048 : p.piece;
@@ -1311,7 +1334,7 @@ cudaError_t lay_out(const Call &c, const Plan &p, const float *lse, const float 
     g.out = reinterpret_cast<__nv_bfloat16 *>(c.ws + p.x);
     g.rows_pad = p.rows_pad; g.d = static_cast<int>(c.d); g.pitch = p.pitch;
     g.lse = lse; g.gl = gl; g.scale = c.scale;
-    g.grad = lse != nullptr ? reinterpret_cast<float2 *>(c.ws + p.grad) : nullptr;
+    g.grad = lse != nullptr ? reinterpret_cast<float4 *>(c.ws + p.grad) : nullptr;
     g.back = reinterpret_cast<float *>(kept + 2);
     g.gx = gx; g.targets = c.targets; g.V = c.V; g.ignore = c.ignore; g.n = static_cast<int>(c.n);
     const int64_t want = p.rows_pad / (GATHER_THREADS / 32);
@@ -1343,7 +1366,7 @@ template <typename Id> int join_loss(const Call &c, const Plan &p, int parts, fl
                             reinterpret_cast<const float *>(c.ws + p.z),
                             reinterpret_cast<const int2 *>(c.ws + p.row),
                             reinterpret_cast<const int *>(c.ws + p.kept), c.targets,
-                            static_cast<int>(c.n), c.V, c.ignore, loss, lse) == cudaSuccess
+                            static_cast<int>(c.n), c.V, c.ignore, c.scale * LOG2E, loss, lse) == cudaSuccess
                ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
@@ -1439,7 +1462,7 @@ int backward(const Call &c, const float *lse, const float *gl, void *gx, void *g
     a.scale = c.scale;
     a.a_rows = rows_of_x(c.n);
     a.row = reinterpret_cast<int2 *>(c.ws + p.row);
-    a.grad = reinterpret_cast<float2 *>(c.ws + p.grad);
+    a.grad = reinterpret_cast<float4 *>(c.ws + p.grad);
     a.back = reinterpret_cast<float *>(c.ws + p.kept) + 2;
     a.g_planes = p.g_planes;
     a.d = static_cast<int>(c.d);
