@@ -549,7 +549,9 @@ int nrnn_embedding_backward(const void *ids, int ids_type, const void *g, int dt
  *   u           device, (rows, d) of dtype; NULL (then h given): not wanted,
  *               the norm after the last block
  *   d           1 .. 8192, else NRNN_ERR_UNSUPPORTED;  eps >= 0
- * u is computed from x_out before its rounding to dtype.
+ * u is computed from x_out before its rounding to dtype.  h silu(gate) is formed
+ * before it is divided by h's root mean square: finite inputs whose product (or
+ * whose squares' sum) passes fp32's largest value give infinities or NaN.
  */
 int nrnn_block_norm_forward(const void *x, const void *h, const void *gate, const float *w_post,
                             const float *scale, const float *w_pre, int dtype, int64_t rows,
@@ -584,8 +586,11 @@ int nrnn_block_norm_backward(const void *x_out, const void *h, const void *gate,
 
 /*
  * Workspace bytes of nrnn_vocab_loss_forward (backward = 0) or
- * nrnn_vocab_loss_backward; 0 for invalid sizes.  No N x V array is kept: the
- * backward holds one piece of the vocabulary at a time.
+ * nrnn_vocab_loss_backward; 0 for invalid sizes.  The forward stores no logits.
+ * The backward holds their gradient G as bf16 planes (one for bf16 inputs, two of
+ * them up to 64 rows, three for fp32), rows rounded up to 256, for as many
+ * vocabulary entries at a time as fit in 1 GiB (2048 at least): all of rows x V
+ * where that fits.  fp32 inputs need three bf16 planes of x and W besides.
  */
 size_t nrnn_vocab_loss_workspace_bytes(int64_t rows, int64_t d, int64_t V, int dtype, int backward);
 
@@ -604,8 +609,11 @@ size_t nrnn_vocab_loss_workspace_bytes(int64_t rows, int64_t d, int64_t V, int d
  *                is 0 once the work is done, or not if a device wait gave up
  *                (nrnn_set_wait_limit_ns): then outputs are NaN where they
  *                depended on it.  So too in the backward
- * fp32 inputs are multiplied with fp32 accuracy on the tensor cores; an infinity
- * in fp32 W or in a row that takes part may count as NaN.
+ * fp32 inputs are multiplied with fp32 accuracy on the tensor cores, values below
+ * about 2^-110 less exactly (the lower of their three planes are subnormal); an
+ * infinity in fp32 W or in a row that takes part may count as NaN.  bf16: products
+ * are exact and summed in the tensor cores' fp32, which is less exact than fp32
+ * rounding by an amount that grows with d (lse 3e-7 relative at 512, 1e-5 at 16384).
  */
 int nrnn_vocab_loss_forward(const void *x, const void *W, int dtype, int64_t rows, int64_t d,
                             int64_t V, const void *targets, int targets_type, int64_t ignore_index,
@@ -614,9 +622,10 @@ int nrnn_vocab_loss_forward(const void *x, const void *W, int dtype, int64_t row
 
 /*
  * Its gradient: with G_iv = g_loss_i logit_scale (exp(z_iv - lse_i) - [v =
- * targets_i]), gx = G W and gW = G^T x, both overwritten.  bf16: G is rounded
- * to bf16 before the two products.  Rows that take no part have a zero row in
- * gx (NaN where the target is out of range) and add nothing to gW.
+ * targets_i]), gx = G W and gW = G^T x, both overwritten.  bf16 and more than 64
+ * rows: G is rounded to bf16 before the two products.  Rows that take no part
+ * have a zero row in gx (NaN where the target is out of range) and add nothing
+ * to gW.
  *
  *   lse          device, fp32 (rows), as nrnn_vocab_loss_forward left it
  *   g_loss       device, fp32 (rows): dL/dloss_i

@@ -228,7 +228,7 @@ def _vocab_args(x, W, targets):
 def vocab_loss(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, logit_scale: float = 1.0,
                ignore_index: int = -100, workspace: torch.Tensor | None = None):
     """Softmax cross entropy over the vocabulary with logits logit_scale * x W^T,
-    which are never stored: x (..., d), W (V, d), targets (...) int32/int64.
+    which are not stored: x (..., d), W (V, d), targets (...) int32/int64.
     Returns (loss, lse), float32 (...): the loss of each row and the log of its
     normaliser, which vocab_loss_backward takes.  Rows whose target is
     ignore_index take no part (0 in both); any other target outside [0, V)
@@ -252,8 +252,8 @@ def vocab_loss_backward(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
                         workspace: torch.Tensor | None = None):
     """(dL/dx, dL/dW) of vocab_loss() in x's dtype, from lse as it returned it
     and g_loss = dL/dloss, float32 (...) (for a mean over the kept rows: one
-    over their number).  The logits are computed again, a piece of the
-    vocabulary at a time."""
+    over their number).  The logits are computed again, as much of the
+    vocabulary at a time as 1 GiB of their gradient holds."""
     x, W, targets, kind, code = _vocab_args(x, W, targets)
     V, d = W.shape
     rows = targets.numel()

@@ -16,6 +16,10 @@
 //
 // scale and w_post only ever act as their product, so the kernels hold that.
 //
+// (h silu(gate) is formed before the division by h's norm: preactivations and states
+// whose product passes fp32's largest value, of about 1e19 each, overflow where the
+// order above would not.)
+//
 // Neither direction has a product to speak of: both are bound by HBM, 5 row
 // passes forward (x, h, gate in; x', u out) and 8 backward (x', h, gate, gx',
 // gu in; gx, gh, ggate out).  A row is read once and stays in registers; the

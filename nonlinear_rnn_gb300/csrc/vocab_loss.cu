@@ -1,5 +1,5 @@
-// Softmax cross entropy over a vocabulary, in pieces of the vocabulary, without
-// keeping the logits, and its gradient.
+// Softmax cross entropy over a vocabulary without keeping the logits, and its
+// gradient in pieces of the vocabulary.
 //
 //   z_iv = c <x_i, W_v>,  lse_i = log sum_v exp z_iv,  loss_i = lse_i - z_i,t(i)
 //   G_iv = gl_i c (exp(z_iv - lse_i) - [v = t(i)]),  gx = G W,  gW = G^T x
@@ -19,7 +19,8 @@
 //   DL   x W^T   G of one piece of the vocabulary, to the workspace
 //   GX   G W     gx, or this piece's share of it
 //   GW   G^T x   rows of gW of this piece
-// The piece of G is all that is ever kept of the N x V matrix.
+// G of a piece, up to 1 GiB, is all that is ever kept of an N x V matrix (all of it where
+// it fits).
 //
 // GX and GW have few output tiles and long inner dimensions.  Whole waves of tiles
 // go one to a pair, which walk the inner dimension side by side and share what they
@@ -35,7 +36,13 @@
 // number there, so ignored rows cost nothing and whatever they hold (infinities,
 // NaN) reaches no output.
 //
-// fp32 inputs are written as three bf16 planes, v = hi + mid + lo up to 2^-24, and a
+// For bf16 inputs G is rounded to bf16: both operands of a product have to be of one
+// type, fp16 has not the range, and a second plane of G would be two more products in
+// eight.  The results are rounded to bf16 too and are off by that alone nearly as much
+// (1.04 to 1.2 times it, 1.45 at most; see mantissa_of and TWO_PLANES_MOST).
+//
+// fp32 inputs are written as three bf16 planes, v = hi + mid + lo up to 2^-24 (values
+// below 2^-110 less exactly: their lower planes are subnormal), and a
 // product is the six plane products above 2^-24 relative, smallest first:
 // (lo,hi) (mid,mid) (hi,lo) (mid,hi) (hi,mid) (hi,hi).  (An infinity leaves
 // no number, so in W or in a kept row it counts as NaN.)  The tensor cores add less
@@ -48,8 +55,8 @@
 // Measured: 16384 rows over 65536 x 1024 bf16 with gradient 5.2 to 5.6 ms (1.56 to
 // 1.68 PFLOP/s; cuBLAS runs at 1.75 when kept up: the power limit holds the clocks at
 // 1.7 GHz); 4096 over 32768 x 512 bf16 0.42 ms (1.2 PFLOP/s: a tile's 8 slices hide
-// less of its epilogue), 3001 over 10007 x 250 fp32 0.289 ms, 4 rows over 50021 x 1024
-// bf16, forward only, 30 us (W once in 20 to 23 us).  Without its epilogue the forward's
+// less of its epilogue), 3001 over 10007 x 250 fp32 0.292 ms, 4 rows over 50021 x 1024
+// bf16, forward only, 31 to 35 us (W once in 20 to 23 us).  Without its epilogue the forward's
 // main loop takes 0.96 of the time at d = 1024, 0.94 at 512 and 0.55 at 64, where the
 // exponentials bind.
 //
@@ -523,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 if (left <= 0 && FORM != DL) return;
                 if (FORM == LSE) {
                     // Sums of 2^(z scale2 - ref), the product not rounded by itself (as in DL, whose
-                    // probabilities would not add up to one with this lse else: by 3e-6 at a logit
+                    // probabilities would not add up to one with this lse else, by 2.6e-6 at logits
                     // of 48).  The reference is the largest scaled logit, rounded, or near it.
                     const int at = target - n0 - c;
                     if (at >= 0 && at < min(left, PIECE)) {
@@ -892,8 +899,8 @@ __device__ __forceinline__ float mantissa_of(float v) {
 }
 
 // A kept row's constants of the DL form: {l = lse log2(e), g, g 2^(l - lse log2(e))} with
-// g = gl c / back.  What rounding l leaves out is put into the factor of p, whose sum
-// would be off by it (1e-6 at an lse of 20).
+// g = gl c / back.  What rounding l leaves out (2^-18 at an lse of 48) is put into the
+// factor of p, which would be off by it.
 __device__ __forceinline__ float4 row_grad(float lse, float g) {
     constexpr float LOG2E_LOW = 1.92596303e-8f;   // log2(e) less LOG2E
     const float l = lse * LOG2E, low = fmaf(lse, LOG2E, -l) + lse * LOG2E_LOW;
@@ -998,7 +1005,9 @@ __global__ void __launch_bounds__(256)
 // them back would be four times the bytes that W has (33 rows over 47579 x 552: 126
 // us).  A warp takes FEW_V rows of W at a time, 128 bytes a lane apart, against every
 // row of x from shared memory, so a value of x that is read serves FEW_V products.
-// Bound by reading W up to about 16 rows.
+// One row over 50021 x 1024 reads W at 0.70 of HBM (44 us), four at 0.58 (53); 5 to 16
+// rows are built as 16 on one CTA of eight warps an SM, which covers too little of the
+// latencies: 102 to 125 us.
 constexpr int FEW_MOST = 16, FEW_WARPS = 8;
 constexpr int few_v(int n) { return n > 4 ? 4 : 8; }   // rows of W of a warp: what the registers allow
 constexpr int FEW_X_BYTES = 160 * 1024;   // of the rows of x in shared memory
@@ -1006,6 +1015,7 @@ constexpr int FEW_X_BYTES = 160 * 1024;   // of the rows of x in shared memory
 // GRAD: G of one piece of the vocabulary, as planes, from the same logits: were they
 // taken on the tensor cores, which add them up less exactly, the probabilities would
 // not add up to one with this lse (gradients of 16 rows of logits of 60 were 2e-5 off).
+// With gradient, 50021 x 1024: 4 rows 485 -> 420 us by it, 16 rows 543 -> 542.
 struct FewGrad {
     const float4 *grad;       // per kept row, see row_grad
     __nv_bfloat16 *dl;        // [planes][..][pitch]
@@ -1208,13 +1218,17 @@ struct Plan {
 constexpr int FEW_CTAS = 4 * PAIRS;
 int few_size(int64_t n) { return n <= 1 ? 1 : n <= 4 ? 4 : FEW_MOST; }   // rows it is built for
 
-// bytes the piece of G may take
+// Bytes the piece of G may take.  More would be faster where it binds, as gx's sums
+// pass through memory less often, but the caller pays for it: 262144 rows over 65536 x
+// 1024 bf16 with gradient take 122 ms with 1 GiB (32 pieces of 2048), 107 with 2, 97
+// with 4.  At least 2048 columns, 32 slices of gx's products.
 constexpr int64_t PIECE_BYTES = 1ll << 30;
 
 // Rows up to which a bf16 G is kept as two planes, to 2^-16: the roundings of so few
 // rows' largest entries need not average out (4 rows: gx off by up to 1.54 times what
-// rounding it costs, 1.00 with two planes).  It takes another 256-row product of each
-// slice of W where reading W bounds the call; above, that would be paid in full.
+// rounding it costs, 1.00 with two planes).  That is another product of the same
+// slices: 64 rows over 50021 x 512 with gradient 87 -> 99 us, 4 over 50021 x 1024 123 ->
+// 141.  200 rows over 50021 x 1024 would go from 160 to 188 for 1.2 -> 1.00.
 constexpr int TWO_PLANES_MOST = 64;
 
 // Columns of the forward's tiles.  With enough tiles the widest; with few, the width
