@@ -37,8 +37,8 @@
 // NaN) reaches no output.
 //
 // For bf16 inputs G is rounded to bf16: both operands of a product have to be of one
-// type, fp16 has not the range, and a second plane of G would be two more products in
-// eight.  The results are rounded to bf16 too and are off by that alone nearly as much
+// type, fp16 has not the range, and a second plane of G would make six products of the
+// four (forward included).  The results are rounded to bf16 too and are off by that alone nearly as much
 // (1.04 to 1.2 times it, 1.45 at most; see mantissa_of and TWO_PLANES_MOST).
 //
 // fp32 inputs are written as three bf16 planes, v = hi + mid + lo up to 2^-24 (values
@@ -56,7 +56,7 @@
 // 1.68 PFLOP/s; cuBLAS runs at 1.75 when kept up: the power limit holds the clocks at
 // 1.7 GHz); 4096 over 32768 x 512 bf16 0.42 ms (1.2 PFLOP/s: a tile's 8 slices hide
 // less of its epilogue), 3001 over 10007 x 250 fp32 0.292 ms, 4 rows over 50021 x 1024
-// bf16, forward only, 31 to 35 us (W once in 20 to 23 us).  Without its epilogue the forward's
+// bf16, forward only, 31 to 37 us (W once in 20 to 23 us).  Without its epilogue the forward's
 // main loop takes 0.96 of the time at d = 1024, 0.94 at 512 and 0.55 at 64, where the
 // exponentials bind.
 //
@@ -892,7 +892,8 @@ __device__ __forceinline__ float plane_of(float v) {
 // products are multiplied by it at their end.  Where all rows have the same dL/dloss
 // (a mean), their largest entries are then 1 - p times a power of two.  With the
 // mantissa, entries of rows of small p would all be close to one value and be rounded
-// alike: for 15 rows gx was off by 2.05 times what rounding it costs, now 1.28.
+// alike: gx of 15 rows, G as one plane, is off by up to 2.05 times what rounding it
+// costs with the mantissa and by 1.28 times without; of 1500 rows 1.47 and 1.14.
 __device__ __forceinline__ float mantissa_of(float v) {
     const uint32_t bits = __float_as_uint(v), exponent = bits >> 23 & 0xffu;
     return exponent == 0 || exponent == 255 ? 1.f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
