@@ -522,7 +522,8 @@ size_t nrnn_embedding_backward_workspace_bytes(int64_t n, int64_t V, int64_t d);
  *
  *   g           device, (n, d) of dtype: dL/dout
  *   accumulate  0: gW is overwritten (zeros for ids that do not occur);
- *               else added to (rows of ids that do not occur are not touched:
+ *               else added to and rounded to dtype once more (rows of ids that do
+ *               not occur are not touched:
  *               a weight shared with nrnn_vocab_loss_backward)
  *   gW          device, (V, d) of dtype
  *   workspace   device, 256-byte aligned, of at least
