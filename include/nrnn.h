@@ -639,6 +639,124 @@ int nrnn_vocab_loss_backward(const void *x, const void *W, int dtype, int64_t ro
                              float logit_scale, const float *lse, const float *g_loss, void *gx,
                              void *gW, void *workspace, size_t ws_bytes, void *stream);
 
+/*
+ * Workspace bytes of nrnn_linear_recurrence_forward (backward = 0) or
+ * nrnn_linear_recurrence_backward; num_segments 0: no pack.  0 for invalid sizes.
+ */
+size_t nrnn_linear_recurrence_workspace_bytes(int64_t B, int64_t T, int64_t d_h, int dtype,
+                                              int64_t num_segments, int backward);
+
+/*
+ * Gated linear recurrence: the linear sibling of the diagonal GRU, whose gates do
+ * not depend on the state, so that one scan over time computes it.
+ *
+ *   r = sig(P_a + b_a),  a = exp(-rate r),  i = sig(P_i + b_i),  s = sqrt(1 - a^2)
+ *   h_t = a_t h_{t-1} + s_t i_t v_t
+ *
+ *   preact      device, (B, T, 3 d_h) of dtype, blocks [a | i | v]: what
+ *               nrnn_input_projection gives for W_x of these blocks
+ *   params      device, fp32 (3, d_h): rows rate (>= 0; else NaN), b_a, b_i
+ *   cu_seqlens  as for nrnn_newton_forward; every segment starts from its own state
+ *   state       device, fp32 (B, d_h), or (num_segments, d_h) for a pack: the states
+ *               before the first step; NULL: zeros
+ *   H           device, (B, T, d_h) of dtype
+ *   last        device, fp32 of state's shape: the states after the last step,
+ *               unrounded (an empty sequence's are its first); may be state; NULL:
+ *               not wanted
+ *   workspace   device, 256-byte aligned, of at least
+ *               nrnn_linear_recurrence_workspace_bytes(..., 0)
+ * States are fp32 throughout; no result depends on the order in which threads run.
+ * A sigmoid is bounded below by 2^-63.
+ */
+int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *params, int64_t B,
+                                   int64_t T, int64_t d_h, const int32_t *cu_seqlens,
+                                   int64_t num_segments, const float *state, void *H, float *last,
+                                   void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Its gradient at the stored H (for bf16: as rounded).
+ *
+ *   gH          device, (B, T, d_h) of dtype: dL/dH
+ *   g_last      device, fp32 of state's shape: dL/dlast; NULL: zeros
+ *   gP          device, (B, T, 3 d_h) of dtype: dL/dpreact
+ *   gparams     device, fp32 (3, d_h), overwritten; sums in a fixed order
+ *   g_state     device, fp32 of state's shape: dL/dstate; NULL: not wanted
+ *   workspace   device, 256-byte aligned, of at least
+ *               nrnn_linear_recurrence_workspace_bytes(..., 1)
+ * Where s is zero (a rate of zero) its infinite derivative is left out.
+ */
+int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *params, int64_t B,
+                                    int64_t T, int64_t d_h, const int32_t *cu_seqlens,
+                                    int64_t num_segments, const float *state, const void *H,
+                                    const void *gH, const float *g_last, void *gP, float *gparams,
+                                    float *g_state, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One step per slot: h = state_out = the recurrence's next state.
+ *
+ *   preact      device, (slots, 3 d_h) of dtype
+ *   state       device, fp32 (slots, d_h); NULL: zeros
+ *   h           device, (slots, d_h) of dtype: the new state, rounded
+ *   state_out   device, fp32 (slots, d_h): the new state; may be state
+ */
+int nrnn_linear_recurrence_step(const void *preact, int dtype, const float *params, int64_t slots,
+                                int64_t d_h, const float *state, void *h, float *state_out,
+                                void *stream);
+
+/*
+ * Bytes of what nrnn_gated_mlp_forward keeps for the gradient, and workspace bytes of
+ * the forward (backward = 0) or backward; 0 for invalid sizes.
+ */
+size_t nrnn_gated_mlp_kept_bytes(int64_t rows, int64_t f, int dtype);
+size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dtype, int backward);
+
+/*
+ * Gated feed-forward block: a = x Wg^T, b = x Wu^T, y = (silu(a) b) W_out^T.
+ *
+ *   x           device, (rows, d) of dtype
+ *   W_in        device, (2 f, d) of dtype: the rows of Wg, then those of Wu
+ *   W_out       device, (d, f) of dtype
+ *   rows, d, f  rows >= 0, d and f > 0; rows at most 2^30, d and f at most 2^20
+ *   y           device, (rows, d) of dtype
+ *   kept        device, 256-byte aligned, nrnn_gated_mlp_kept_bytes: what the
+ *               gradient takes (its layout is the library's); NULL: not wanted
+ *   workspace   device, 256-byte aligned, nrnn_gated_mlp_workspace_bytes(..., 0)
+ * The buffers of the tensors need only their element's alignment.
+ */
+int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, int dtype,
+                           int64_t rows, int64_t d, int64_t f, void *y, void *kept,
+                           void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Its gradient, from what the forward kept for the same x and weights:
+ * g = dL/dy (rows, d); gx (rows, d), gW_in (2 f, d) and gW_out (d, f) are overwritten.
+ */
+int nrnn_gated_mlp_backward(const void *x, const void *W_in, const void *W_out, const void *kept,
+                            const void *g, int dtype, int64_t rows, int64_t d, int64_t f, void *gx,
+                            void *gW_in, void *gW_out, void *workspace, size_t ws_bytes,
+                            void *stream);
+
+/*
+ * Dropout whose mask is made again from a counter wherever it is needed:
+ *
+ *   out_e = residual_e + (word(e) >= round(p 2^32) ? x_e / (1 - p) : 0)
+ *
+ * word(e) is the (e mod 4)-th word of the Philox 4x32 generator of ten rounds with
+ * counter {e / 4 low, e / 4 high, offset low, offset high} (32 bits each) and key
+ * {seed low, seed high}, so the gradient with respect to x is the same call on the
+ * gradient without residual.  What is dropped adds zero whatever x holds.
+ *
+ *   x, residual, out   device, n elements of dtype; residual NULL: zeros; out may be
+ *                      x or residual, but not overlap them otherwise
+ *   n           0 .. 2^48;  p in [0, 1]
+ *   seed_device device, one 64-bit word that is read instead of seed when the kernel
+ *               runs (a captured call then draws another mask once it changes); NULL:
+ *               seed
+ */
+int nrnn_dropout(const void *x, int dtype, int64_t n, double p, uint64_t seed,
+                 const uint64_t *seed_device, uint64_t offset, const void *residual, void *out,
+                 void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,6 +40,16 @@ from ._binding import (  # noqa: F401
     workspace_bytes,
     x_host_staging_bytes,
 )
+from ._block import (  # noqa: F401
+    RECURRENCE_ORDER,
+    LinearRecurrenceGrads,
+    dropout,
+    gated_mlp,
+    gated_mlp_backward,
+    linear_recurrence,
+    linear_recurrence_backward,
+    linear_recurrence_step,
+)
 from ._language import (  # noqa: F401
     BlockNormGrads,
     block_norm,

@@ -77,6 +77,17 @@ _SIGNATURES = {
                                  _vp, _sz, _vp], _int),
     "nrnn_vocab_loss_backward": ([_vp, _vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _f, _vp, _vp,
                                   _vp, _vp, _vp, _sz, _vp], _int),
+    "nrnn_linear_recurrence_workspace_bytes": ([_i64, _i64, _i64, _int, _i64, _int], _sz),
+    "nrnn_linear_recurrence_forward": ([_vp, _int, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                                        _vp, _sz, _vp], _int),
+    "nrnn_linear_recurrence_backward": ([_vp, _int, _vp, _i64, _i64, _i64, _vp, _i64] + [_vp] * 8 +
+                                        [_sz, _vp], _int),
+    "nrnn_linear_recurrence_step": ([_vp, _int, _vp, _i64, _i64, _vp, _vp, _vp, _vp], _int),
+    "nrnn_gated_mlp_kept_bytes": ([_i64, _i64, _int], _sz),
+    "nrnn_gated_mlp_workspace_bytes": ([_i64, _i64, _i64, _int, _int], _sz),
+    "nrnn_gated_mlp_forward": ([_vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _int),
+    "nrnn_gated_mlp_backward": ([_vp] * 5 + [_int, _i64, _i64, _i64] + [_vp] * 4 + [_sz, _vp], _int),
+    "nrnn_dropout": ([_vp, _int, _i64, _c.c_double, _u64, _vp, _u64, _vp, _vp, _vp], _int),
 }
 EXPORTED = tuple(_SIGNATURES)
 

@@ -16,7 +16,8 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libnrnn.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cu", "newton.cu", "picard.cu", "sequential.cu", "projection_tc.cu", "decode.cu", "backward.cu", "noalloc.cu", "probe.cu", "host_pipeline.cu", "pack_plan.cu",
-           "embedding.cu", "block_norm.cu", "vocab_loss.cu"]
+           "embedding.cu", "block_norm.cu", "vocab_loss.cu",
+           "linear_recurrence.cu", "gated_mlp.cu", "dropout.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
