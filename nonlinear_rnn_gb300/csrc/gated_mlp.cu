@@ -4,146 +4,935 @@
 //   gm = g Wo, ga = gm b silu'(a), gb = gm silu(a)
 //   gx = [ga gb] W_in, gW_in = [ga gb]^T x, gW_out = g^T m
 //
-// 6 n d f operations forward and 12 n d f backward.
+// 6 n d f operations forward and 12 n d f backward: bound by the tensor cores, except
+// for few rows, where reading the weights bounds it.
+//
+// All products run on one persistent tcgen05 kernel (k_mlp_gemm) of CTA pairs
+// (cta_group::2), as the vocabulary loss's: 256 x (up to 256) tiles, TMA into a ring of
+// 128-byte-swizzled stages, one thread issuing the products into one of two TMEM
+// accumulators while eight epilogue warps drain the other.  Transposed operands are read
+// MN-major from where they lie.  The forms:
+//   UP   x W_in^T    A pair's two CTAs stage one half each of a tile's columns: one the
+//                    rows of Wg, the other the same rows of Wu.  The accumulator then
+//                    holds a and b of the same 128 units beside one another, and the
+//                    epilogue forms m without either having been stored.  With the
+//                    gradient to come a and b are kept, in the storage type.
+//   DOWN m W_out^T
+//   DH   g W_out     gm, from which the epilogue forms ga and gb by the kept a and b
+//   GX   [ga gb] W_in          the inner dimension runs over ga, then gb
+//   GWI  [ga gb]^T x           rows of gW_in, Wg's tiles, then Wu's
+//   GWO  g^T m
+//
+// UP and DH have many tiles; the others may have few and long inner dimensions.  For
+// them whole waves of tiles go one to a pair and the rest is cut by inner slices, an
+// equal run of the (tile, slice) sequence to every team of pairs; parts of a cut tile go
+// to the workspace in fp32 and k_join_parts adds them in order.
+//
+// For bf16, m (formed from unrounded a and b) is rounded before the second product, and
+// a, b, ga and gb where they are stored: an operand of the tensor cores is bf16, and a
+// second plane of each would double every product.  y and gW_out are 1.41 times as far
+// off as rounding the exact result once, gx and gW_in 1.8 times.
+//
+// fp32 operands are split into three bf16 planes, v = hi + mid + lo up to 2^-24, and a
+// product is the six plane products above 2^-24 relative, smallest first.  An
+// accumulator takes at most 256 elements of the inner dimension before the epilogue adds
+// it to fp32 registers, as the tensor cores add less exactly than fp32 rounding does.
+// (An infinity leaves no number: in fp32 operands it counts as NaN.)
+//
+// Every wait is bounded.  One that gives up sets the call's error word (the workspace's
+// first) and the abort flag of both CTAs of the pair, which ends the other roles' waits
+// too; the epilogues write NaN from there on, and neither CTA leaves before what both
+// have in flight is done (settle).
 #include "../../include/nrnn.h"
 #include "nrnn_internal.h"
-#include "rows.cuh"
+#include "pair.cuh"
 
 namespace nrnn {
 namespace {
 
-constexpr int TILE = 64, DEEP = 16;
+constexpr int PAIRS = 76;   // of 152 SMs
+constexpr int MOST_SIDE = 8;
 
-struct Product {
-    const void *A, *B;
-    int64_t a_row, a_k, b_row, b_k;   // strides of a row and of an inner element
-    int64_t M, N, K;
-    void *out;
-    int64_t pitch;
-    bool add;
+enum Form { UP, DOWN, DH, GX, GWI, GWO };
+
+constexpr int BM = 256, BN = 256, BK = 64;                 // of a pair
+constexpr int HALF_M = BM / 2;                             // rows of A and D in one CTA
+constexpr int A_BYTES = HALF_M * BK * 2, B_BYTES = BN / 2 * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int GEMM_THREADS = 128 + EPI_WARPS * 32;
+constexpr int PIECE = 64;                                  // columns that an epilogue warp takes at a time
+constexpr int BOX_ROWS = 32, BOX_BYTES = BOX_ROWS * PIECE * 2;
+constexpr int SPLIT_CHUNK = 4;     // fp32: 64-wide slices per accumulator
+constexpr int SEGMENTS = 6;        // fp32: plane products, smallest first
+__device__ constexpr int PLANE_A[SEGMENTS] = {2, 1, 0, 1, 0, 0};
+__device__ constexpr int PLANE_B[SEGMENTS] = {0, 1, 2, 0, 1, 0};
+
+// staged blocks of an epilogue warp, and the stages that they leave room for
+template <int FORM, typename T> constexpr int blocks_of() { return sizeof(T) == 4 ? 1 : FORM == UP ? 3 : FORM == DH ? 2 : 1; }
+template <int FORM, typename T> constexpr int stages_of() { return blocks_of<FORM, T>() == 3 ? 4 : blocks_of<FORM, T>() == 2 ? 5 : 6; }
+template <int FORM, typename T> constexpr size_t gemm_smem() {
+    return stages_of<FORM, T>() * STAGE_BYTES + EPI_WARPS * blocks_of<FORM, T>() * BOX_BYTES + 1024;
+}
+
+struct GemmArgs {
+    uint32_t *error;          // device: set by a wait that gave up
+    uint64_t wait_ns;         // limit of a wait
+    int M, N;                 // rows (GWI: of one half) and columns of the product
+    int tiles_m, tiles_n;     // row tiles (GWI: of both halves) and column tiles
+    int kb, kb_half;          // 64-wide inner slices; GX: of one half
+    int m_half;               // GWI: row tiles of a half
+    int bn;                   // columns of a tile: a multiple of 64, at most BN (UP: of both halves)
+    int whole, units;         // DOWN, GX, GWI, GWO: row tiles of a team that are not cut, and all
+    int side, teams;          // pairs of a team (its column tiles beside one another), teams
+    float *parts;             // [pairs][2][BM][bn] sums of cut tiles
+    void *out;                // the result in the storage type, rows of N
+    bool blocks_out;          // bf16: tmOut is over the result, whose blocks leave by TMA
+    bool keep;                // UP: a and b are stored
+    float *ab;                // fp32: a and b, [2][M][pitch]
+    int pitch;
 };
 
-// out(m, n) = sum_k A(m, k) B(n, k), fp32 sums; 64 x 64 tiles, 4 x 4 a thread
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) k_product(const Product p) {
-    __shared__ float a[DEEP][TILE + 1], b[DEEP][TILE + 1];
-    const T *A = static_cast<const T *>(p.A), *B = static_cast<const T *>(p.B);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TILE;
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.y) * TILE; m0 < p.M; m0 += static_cast<int64_t>(gridDim.y) * TILE) {
-        float c[4][4] = {};
-        for (int64_t k0 = 0; k0 < p.K; k0 += DEEP) {
-            for (int i = threadIdx.x; i < TILE * DEEP; i += 256) {
-                const bool along_k = p.a_k == 1;
-                const int r = along_k ? i / DEEP : i % TILE, k = along_k ? i % DEEP : i / TILE;
-                a[k][r] = m0 + r < p.M && k0 + k < p.K ? to_f32(A[(m0 + r) * p.a_row + (k0 + k) * p.a_k]) : 0.f;
-            }
-            for (int i = threadIdx.x; i < TILE * DEEP; i += 256) {
-                const bool along_k = p.b_k == 1;
-                const int r = along_k ? i / DEEP : i % TILE, k = along_k ? i % DEEP : i / TILE;
-                b[k][r] = n0 + r < p.N && k0 + k < p.K ? to_f32(B[(n0 + r) * p.b_row + (k0 + k) * p.b_k]) : 0.f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < DEEP; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) c[i][j] = fmaf(a[k][ty * 4 + i], b[k][tx + 16 * j], c[i][j]);
-            __syncthreads();
+// A unit is what a pair takes at a time: a tile, or a tile's slices k0 .. k1
+struct Unit { int tm, tn, k0, k1, slot; };   // slot: -1 = a whole tile
+
+template <int FORM> constexpr bool CUTS = FORM != UP && FORM != DH;
+
+template <int FORM> struct Walk {
+    int u, pairs, side_at;
+    int64_t pos, end;
+
+    __device__ Walk(const GemmArgs &a, int pair, int pairs_) : u(pair), pairs(pairs_), side_at(0), pos(0), end(0) {
+        if (!CUTS<FORM>) return;
+        side_at = pair % a.side;
+        u = pair / a.side;
+        if (u < a.teams) run(a, u, pos, end);
+        else u = a.units;   // a pair left over
+    }
+    // the run of team b
+    __device__ static void run(const GemmArgs &a, int b, int64_t &from, int64_t &to) {
+        const int64_t all = static_cast<int64_t>(a.units - a.whole) * a.kb;
+        from = all * b / a.teams;
+        to = all * (b + 1) / a.teams;
+    }
+    __device__ __forceinline__ bool next(const GemmArgs &a, Unit &t) {
+        t.k0 = 0; t.k1 = a.kb; t.slot = -1;
+        if (!CUTS<FORM>) {
+            if (u >= a.units) return false;
+            // rows fastest: the pairs working at one time share a tile of the weights
+            t.tm = u % a.tiles_m;
+            t.tn = u / a.tiles_m;
+            u += pairs;
+            return true;
         }
+        int tile = u;
+        if (u < a.whole) {
+            u += a.teams;
+        } else {
+            if (pos >= end) return false;
+            tile = a.whole + static_cast<int>(pos / a.kb);
+            t.k0 = static_cast<int>(pos % a.kb);
+            if (end - pos < a.kb - t.k0) t.k1 = t.k0 + static_cast<int>(end - pos);
+            pos += t.k1 - t.k0;
+            if (t.k0 > 0) t.slot = 0;
+            else if (t.k1 < a.kb) t.slot = 1;
+        }
+        t.tn = a.side > 1 ? side_at : tile % a.tiles_n;
+        t.tm = a.side > 1 ? tile : tile / a.tiles_n;
+        return true;
+    }
+};
+
+template <typename T> __device__ __forceinline__ void store_cols(T *p, const float (&v)[PIECE], int n, bool wide) {
+    constexpr int VEC = 16 / sizeof(T);
+    if (wide) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < PIECE; c += VEC) {
+            float o[VEC];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty * 4 + i, n = n0 + tx + 16 * j;
-                if (m < p.M && n < p.N) {
-                    O *o = static_cast<O *>(p.out) + m * p.pitch + n;
-                    *o = from_f32<O>(p.add ? to_f32(*o) + c[i][j] : c[i][j]);
-                }
-            }
+            for (int e = 0; e < VEC; ++e) o[e] = v[c + e];
+            if (c < n) store_f32<T, VEC>(p + c, o);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < PIECE; ++c)
+            if (c < n) p[c] = from_f32<T>(v[c]);
     }
 }
 
 __device__ __forceinline__ float sigmoid_of(float x) { return rcp_approx(1.f + ex2_approx(-LOG2E * x)); }
 
-// a, b as kept for the gradient, m from them unrounded
-template <typename T>
-__global__ void __launch_bounds__(256) k_gate(const float *a, const float *b, T *ka, T *kb, T *m, int64_t n) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const float x = a[i];
-        ka[i] = from_f32<T>(x);
-        kb[i] = from_f32<T>(b[i]);
-        m[i] = from_f32<T>(x * sigmoid_of(x) * b[i]);
+// ga and gb in place of a and b
+__device__ __forceinline__ void gate_back(float gm, float &a, float &b) {
+    const float s = sigmoid_of(a), gs = gm * s;
+    const float ga = gs * b * fmaf(a, 1.f - s, 1.f);
+    b = gs * a;
+    a = ga;
+}
+
+template <int FORM> __device__ constexpr bool mn_a() { return FORM == GWI || FORM == GWO; }
+template <int FORM> __device__ constexpr bool mn_b() { return FORM != UP && FORM != DOWN; }
+
+// bytes of a stage's copies in one CTA: one box of a K-major operand, 64 columns each of
+// an MN-major one
+template <int FORM> __device__ __forceinline__ uint32_t stage_bytes(const GemmArgs &a) {
+    const int half_n = a.bn / 2, b_rows = mn_b<FORM>() ? (half_n + 63) / 64 * 64 : half_n;
+    return A_BYTES + b_rows * BK * 2;
+}
+
+// T: storage type of the inputs (float: split products)
+template <int FORM, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
+    k_mlp_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmAB, const GemmArgs a) {
+    constexpr bool SPLIT = sizeof(T) == 4;
+    constexpr bool MN_A = mn_a<FORM>(), MN_B = mn_b<FORM>();
+    constexpr int STAGES = stages_of<FORM, T>(), BLOCKS = blocks_of<FORM, T>();
+    constexpr uint32_t TMEM_COLS = 512;   // two accumulators
+    extern __shared__ unsigned char dsmem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], accf_bar[2], acce_bar[2],
+        drain_bar, ab_bar[EPI_WARPS];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile uint32_t s_abort;     // a role of either CTA gave up
+    __shared__ volatile int s_issued[2];      // rank 0's: stages that each producer went through
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);   // rank 0's: both CTAs' copies
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf_bar[b], 1);
+            mbar_init(&acce_bar[b], 2 * EPI_WARPS);   // rank 0's: both epilogues
+        }
+        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(&ab_bar[w], 1);
+        mbar_init(&drain_bar, 1);
+        s_abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmOut);
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&s_tmem)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync_all();   // both CTAs' barriers are there
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = s_tmem;
+    dependents_may_launch();
+    wait_for_prerequisites();
+    const int pair = blockIdx.x >> 1;
+    Walk<FORM> w(a, pair, gridDim.x >> 1);
+    Unit t;
+    constexpr int PASSES = SPLIT ? SEGMENTS : 1;
+    const int half_n = a.bn / 2;
+    if (warp == 0) {
+        // ---------------------------------------------------------- TMA producer
+        // Lane i starts the i-th copy of a stage.
+        constexpr int BOXES_A = MN_A ? HALF_M / 64 : 1;
+        const int boxes_b = MN_B ? (half_n + 63) / 64 : 1;
+        const uint32_t bytes = 2 * stage_bytes<FORM>(a);
+        const bool is_a = lane < BOXES_A, copies = lane < BOXES_A + boxes_b;
+        const int box = is_a ? lane : lane - BOXES_A;
+        const bool mn = is_a ? MN_A : MN_B;
+        const uint32_t offset = (is_a ? 0 : A_BYTES) + box * (64 * BK * 2);
+        int it = 0;
+        bool go = true;
+        while (go && w.next(a, t)) {
+            // this lane's coordinate along M or N, and the half of an operand that has two
+            int at, half = 0;
+            if (is_a) {
+                const int tm = FORM == GWI && t.tm >= a.m_half ? t.tm - a.m_half : t.tm;
+                half = FORM == GWI && t.tm >= a.m_half;
+                at = tm * BM + static_cast<int>(rank) * HALF_M + box * 64;
+            } else if (FORM == UP) {
+                at = t.tn * half_n;
+                half = static_cast<int>(rank);
+            } else {
+                at = t.tn * a.bn + static_cast<int>(rank) * half_n + box * 64;
+            }
+            // operands of two halves: plane p of half h is 2 p + h
+            constexpr bool TWO_A = FORM == GX || FORM == GWI, TWO_B = FORM == UP || FORM == GX;
+            const bool two = is_a ? TWO_A : TWO_B;
+            for (int c0 = t.k0; go && c0 < t.k1;) {
+                const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
+                for (int p = 0; go && p < PASSES; ++p) {
+                    const int plane = SPLIT ? (is_a ? PLANE_A[p] : PLANE_B[p]) : 0;
+                    for (int k = c0; k < c1; ++k, ++it) {
+                        const int s = it % STAGES;
+                        if (it >= STAGES)
+                            go = __all_sync(FULL_MASK, wait_or_abort(a, &empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort));
+                        if (!go) break;
+                        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full_bar[s], bytes);
+                        __syncwarp();
+                        const bool second = FORM == GX && k >= a.kb_half;
+                        const int along_k = (second ? k - a.kb_half : k) * BK;
+                        const int z = two ? 2 * plane + (FORM == GX ? (second ? 1 : 0) : half) : plane;
+                        if (copies)
+                            tma_load_3d_pair(smem + s * STAGE_BYTES + offset, is_a ? &tmA : &tmB,
+                                             cluster_addr(&full_bar[s], 0), mn ? at : along_k, mn ? along_k : at, z);
+                    }
+                }
+                c0 = c1;
+            }
+        }
+        if (lane == 0) cluster_store(cluster_addr(const_cast<const int *>(&s_issued[rank]), 0), static_cast<uint32_t>(it));
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc = idesc_bf16(BM, MN_A, MN_B) | static_cast<uint32_t>(a.bn >> 3) << 17;
+        int it = 0, phase = 0;
+        bool go = true;
+        while (go && w.next(a, t)) {
+            for (int c0 = t.k0; go && c0 < t.k1; ++phase) {
+                const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
+                const int buf = phase & 1;
+                if (phase >= 2) go = wait_or_abort(a, &acce_bar[buf], ((phase >> 1) - 1) & 1, &s_abort);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t d = tmem + buf * BN;
+                const int its = (c1 - c0) * PASSES;
+                for (int i = 0; go && i < its; ++i, ++it) {
+                    const int s = it % STAGES;
+                    go = wait_or_abort(a, &full_bar[s], (it / STAGES) & 1, &s_abort);
+                    if (!go) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        // 16 elements of K: 32 bytes of a K-major row, or 16 128-byte lines
+                        const uint64_t da = MN_A ? sw128_mn_desc(sa + kk * 2048, 64 * BK * 2) : sw128_desc(sa + kk * 32);
+                        const uint64_t db = MN_B ? sw128_mn_desc(sb + kk * 2048, 64 * BK * 2) : sw128_desc(sb + kk * 32);
+                        mma_f16_pair(d, da, db, idesc, i > 0 || kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_pair(&empty_bar[s]);
+                }
+                if (go) mma_commit_pair(&accf_bar[buf]);
+                c0 = c1;
+            }
+        }
+    } else if (warp >= 4) {
+        // --------------------------------------------------------------- epilogue
+        // warps 4..7 take the even pieces of their 32 rows, 8..11 the odd ones
+        const int quarter = warp & 3, odd = (warp - 4) >> 2;
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        unsigned char *stage_out = smem + STAGES * STAGE_BYTES + (warp - 4) * BLOCKS * BOX_BYTES;
+        const float nan = __int_as_float(0x7fffffff);
+        int phase = 0;
+        uint32_t ab_phase = 0;
+        bool ok = true;   // false once a wait gave up: NaN from there on
+        auto release = [&](int buf) {   // this warp has read the accumulator
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive_cluster(cluster_addr(&acce_bar[buf], 0));
+        };
+        auto accumulator = [&](int buf, uint32_t parity) {
+            ok &= wait_or_abort(a, &accf_bar[buf], parity, &s_abort);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        };
+        // block i of this warp: 16-byte piece q of this thread's row, 128-byte swizzle
+        auto place = [&](int i, int q) {
+            return reinterpret_cast<uint4 *>(stage_out + i * BOX_BYTES + lane * 128 + 16 * (q ^ (lane & 7)));
+        };
+        auto blocks_free = [&]() {   // the stores before have read the blocks
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+        };
+        auto to_bf16 = [](const float *v) {
+            uint4 pk;
+            uint32_t *o = reinterpret_cast<uint32_t *>(&pk);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                o[e] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            return pk;
+        };
+        // the three planes of a piece, v is used up, to column x, row y, planes z, z + dz, z + 2 dz
+        auto store_planes = [&](float (&v)[PIECE], int x, int y, int z, int dz) {
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl) {
+                blocks_free();
+#pragma unroll
+                for (int q = 0; q < PIECE / 8; ++q) {
+                    uint4 pk;
+                    uint32_t *o = reinterpret_cast<uint32_t *>(&pk);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float &lo = v[q * 8 + 2 * e], &hi = v[q * 8 + 2 * e + 1];
+                        const __nv_bfloat162 h2 = pl == 0 ? finite_bf16x2(lo, hi) : __floats2bfloat162_rn(lo, hi);
+                        o[e] = *reinterpret_cast<const uint32_t *>(&h2);
+                        lo -= __low2float(h2);
+                        hi -= __high2float(h2);
+                    }
+                    *place(0, q) = pk;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && y < a.M) {
+                    tma_store_3d(&tmOut, stage_out, x, y, z + pl * dz);
+                    bulk_commit();
+                }
+            }
+        };
+        while (w.next(a, t)) {
+            const int in_tile = static_cast<int>(rank) * HALF_M + quarter * 32;   // the warp's first row
+            const bool second = FORM == GWI && t.tm >= a.m_half;
+            const int y0 = (second ? t.tm - a.m_half : t.tm) * BM + in_tile;      // in its half
+            const int m = y0 + lane;                                              // this thread's row
+            auto read32 = [&](int buf, int col, float (&v)[32]) {
+                uint32_t r[32];
+                tmem_ld_cols<32>(tmem + lane_base + buf * BN + col, r);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = ok ? __uint_as_float(r[e]) : nan;
+            };
+            // a piece of a plain product's tile
+            auto take = [&](int c, float (&v)[PIECE]) {
+                const int left = min(a.N - t.tn * a.bn, a.bn) - c, n = min(left, PIECE);
+                if (left <= 0) return;
+                if (t.slot >= 0) {
+                    float *to = a.parts + ((static_cast<int64_t>(pair) * 2 + t.slot) * BM + in_tile + lane) * a.bn + c;
+                    store_cols<float>(to, v, PIECE, true);
+                } else if (!SPLIT && a.blocks_out) {
+                    blocks_free();
+#pragma unroll
+                    for (int q = 0; q < PIECE / 8; ++q) *place(0, q) = to_bf16(v + 8 * q);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && y0 < a.M) {
+                        tma_store_3d(&tmOut, stage_out, t.tn * a.bn + c, y0, second ? 1 : 0);
+                        bulk_commit();
+                    }
+                } else if (m < a.M) {
+                    const int64_t row = (second ? a.M : 0) + static_cast<int64_t>(m);
+                    const bool wide = a.N % (16 / static_cast<int>(sizeof(T))) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+                    store_cols<T>(static_cast<T *>(a.out) + row * a.N + t.tn * a.bn + c, v, n, wide);
+                }
+            };
+            if constexpr (SPLIT) {
+                // UP: a piece of a and the same one of b; DH: one piece; else two pieces
+                constexpr int PIECES = FORM == DH ? 1 : 2;
+                float acc[PIECES][PIECE];
+                auto column = [&](int i) { return FORM == UP ? i * half_n + odd * PIECE : (2 * i + odd) * PIECE; };
+                const bool mine = FORM != UP || odd * PIECE < half_n;
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                    for (int e = 0; e < PIECE; ++e) acc[i][e] = 0.f;
+                for (int c0 = t.k0; c0 < t.k1; c0 += SPLIT_CHUNK, ++phase) {
+                    const int buf = phase & 1;
+                    accumulator(buf, (phase >> 1) & 1);
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                        for (int h = 0; h < PIECE; h += 32)
+                            if (mine && column(i) + h < a.bn) {
+                                float v[32];
+                                read32(buf, column(i) + h, v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) acc[i][h + e] += v[e];
+                            }
+                    release(buf);
+                }
+                if constexpr (FORM == UP) {
+                    const int x = t.tn * half_n + odd * PIECE, left = a.N - x;
+                    if (mine && left > 0) {
+                        if (a.keep && m < a.M) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                store_cols<float>(a.ab + (static_cast<int64_t>(i) * a.M + m) * a.pitch + x, acc[i],
+                                                  min(a.pitch - x, PIECE), true);
+                        }
+#pragma unroll
+                        for (int e = 0; e < PIECE; ++e) acc[0][e] = acc[0][e] * sigmoid_of(acc[0][e]) * acc[1][e];
+                        store_planes(acc[0], x, y0, 0, 1);
+                    }
+                } else if constexpr (FORM == DH) {
+                    const int x = t.tn * a.bn + odd * PIECE, left = a.N - x;
+                    if (odd * PIECE < a.bn && left > 0) {
+                        float gb[PIECE];
+                        const float *pa = a.ab + static_cast<int64_t>(m) * a.pitch + x, *pb = pa + static_cast<int64_t>(a.M) * a.pitch;
+#pragma unroll
+                        for (int q = 0; q < PIECE; q += 4) {
+                            float va[4] = {}, vb[4] = {};
+                            if (m < a.M && q < left) {   // (the pitch is a multiple of 8: whole fours)
+                                load_f32<float, 4>(pa + q, va);
+                                load_f32<float, 4>(pb + q, vb);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                gate_back(acc[0][q + e], va[e], vb[e]);
+                                acc[0][q + e] = va[e];
+                                gb[q + e] = vb[e];
+                            }
+                        }
+                        store_planes(acc[0], x, y0, 0, 2);
+                        store_planes(gb, x, y0, 1, 2);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i)
+                        if (column(i) < a.bn) take(column(i), acc[i]);
+                }
+            } else if (FORM == UP) {
+                const int buf = phase & 1, x = t.tn * half_n + odd * PIECE;
+                accumulator(buf, (phase >> 1) & 1);
+                ++phase;
+                if (odd * PIECE >= half_n || x >= a.N) {
+                    release(buf);
+                    continue;
+                }
+                blocks_free();
+#pragma unroll
+                for (int h = 0; h < PIECE; h += 32) {
+                    float va[32], vb[32];
+                    read32(buf, odd * PIECE + h, va);
+                    read32(buf, half_n + odd * PIECE + h, vb);
+                    if (h + 32 == PIECE) release(buf);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (a.keep) {
+                            *place(0, h / 8 + q) = to_bf16(va + 8 * q);
+                            *place(1, h / 8 + q) = to_bf16(vb + 8 * q);
+                        }
+#pragma unroll
+                        for (int e = 8 * q; e < 8 * q + 8; ++e) va[e] = va[e] * sigmoid_of(va[e]) * vb[e];
+                        *place(BLOCKS - 1, h / 8 + q) = to_bf16(va + 8 * q);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && y0 < a.M) {
+                    if (a.keep) {
+                        tma_store_3d(&tmAB, stage_out, x, y0, 0);
+                        tma_store_3d(&tmAB, stage_out + BOX_BYTES, x, y0, 1);
+                    }
+                    tma_store_3d(&tmOut, stage_out + (BLOCKS - 1) * BOX_BYTES, x, y0, 0);
+                    bulk_commit();
+                }
+            } else if (FORM == DH) {
+                const int buf = phase & 1;
+#pragma unroll 1
+                for (int c = odd * PIECE; c < a.bn; c += 2 * PIECE) {
+                    const int x = t.tn * a.bn + c;
+                    const bool inside = x < a.N && y0 < a.M;
+                    // a and b of the piece, while the products are under way
+                    if (inside) {
+                        blocks_free();
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&ab_bar[warp - 4], 2 * BOX_BYTES);
+                            tma_load_3d(stage_out, &tmAB, &ab_bar[warp - 4], x, y0, 0);
+                            tma_load_3d(stage_out + BOX_BYTES, &tmAB, &ab_bar[warp - 4], x, y0, 1);
+                        }
+                    }
+                    if (c < 2 * PIECE) accumulator(buf, (phase >> 1) & 1);
+                    if (inside) {
+                        // (no other role waits for these copies: they are seen through whatever happens)
+                        ok &= mbar_wait_bounded(&ab_bar[warp - 4], ab_phase, SETTLE_NS, a.error);
+                        ab_phase ^= 1;
+#pragma unroll
+                        for (int h = 0; h < PIECE; h += 32) {
+                            float g[32];
+                            read32(buf, c + h, g);
+                            if (h + 32 == PIECE && c + 2 * PIECE >= a.bn) release(buf);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const Pack<__nv_bfloat16, 8> pa = *reinterpret_cast<const Pack<__nv_bfloat16, 8> *>(place(0, h / 8 + q));
+                                const Pack<__nv_bfloat16, 8> pb = *reinterpret_cast<const Pack<__nv_bfloat16, 8> *>(place(1, h / 8 + q));
+                                float va[8], vb[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    va[e] = to_f32(pa.v[e]);
+                                    vb[e] = to_f32(pb.v[e]);
+                                    gate_back(g[8 * q + e], va[e], vb[e]);
+                                }
+                                *place(0, h / 8 + q) = to_bf16(va);
+                                *place(1, h / 8 + q) = to_bf16(vb);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&tmOut, stage_out, x, y0, 0);
+                            tma_store_3d(&tmOut, stage_out + BOX_BYTES, x, y0, 1);
+                            bulk_commit();
+                        }
+                    } else if (c + 2 * PIECE >= a.bn) {
+                        release(buf);
+                    }
+                }
+                if (odd * PIECE >= a.bn) {
+                    accumulator(buf, (phase >> 1) & 1);
+                    release(buf);
+                }
+                ++phase;
+            } else {
+                const int buf = phase & 1;
+                accumulator(buf, (phase >> 1) & 1);
+#pragma unroll 1
+                for (int c = odd * PIECE; c < a.bn; c += 2 * PIECE) {
+                    float v[PIECE];
+                    {
+                        uint32_t r[PIECE];
+                        tmem_ld_cols<PIECE>(tmem + lane_base + buf * BN + c, r);
+#pragma unroll
+                        for (int e = 0; e < PIECE; ++e) v[e] = ok ? __uint_as_float(r[e]) : nan;
+                    }
+                    if (c + 2 * PIECE >= a.bn) release(buf);   // the last piece is in registers
+                    take(c, v);
+                }
+                if (odd * PIECE >= a.bn) release(buf);
+                ++phase;
+            }
+        }
+        if (lane == 0) bulk_wait_all();   // the stores are done before the CTA exits
+    }
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync_all();   // neither CTA leaves while the other may still reach into it
+    if (s_abort != 0) {   // the same in both
+        if (warp == 1 && lane == 0) {
+            if (rank == 0) settle<STAGES>(a, s_issued, full_bar, &drain_bar, stage_bytes<FORM>(a));
+            else mbar_wait_bounded(&drain_bar, 0, SETTLE_NS, a.error);
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(TMEM_COLS)
+                     : "memory");
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_gate_back(const T *a, const T *b, const float *gm, T *ga, T *gb, int64_t n) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const float x = to_f32(a[i]), s = sigmoid_of(x), g = gm[i];
-        ga[i] = from_f32<T>(g * to_f32(b[i]) * s * fmaf(x, 1.f - s, 1.f));
-        gb[i] = from_f32<T>(g * x * s);
+// Adds the parts of the tiles that a launch of `pairs` pairs cut, in the order of their
+// slices.  blockIdx.x: a cut tile.  A warp takes a row, 8 columns a lane; with
+// SPLIT_PARTS (few tiles in many parts) the CTA's warps take a share of one row's parts
+// each, and the shares are added in order.
+constexpr int JOIN_WARPS = 8;
+
+template <int FORM, typename T, bool SPLIT_PARTS>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a) {
+    __shared__ float share[SPLIT_PARTS ? JOIN_WARPS : 1][BN];
+    dependents_may_launch();
+    wait_for_prerequisites();
+    const int cut = blockIdx.x / a.side, tile = a.whole + cut;
+    if (tile >= a.units) return;
+    const int side_at = blockIdx.x % a.side, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = SPLIT_PARTS ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
+    const int tm = a.side > 1 ? tile : tile / a.tiles_n, tn = a.side > 1 ? side_at : tile % a.tiles_n;
+    const bool second = FORM == GWI && tm >= a.m_half;
+    const int m = (second ? tm - a.m_half : tm) * BM + row;
+    if (m >= a.M) return;
+    // the runs that hold slices of this tile: b0 .. b1
+    const int64_t all = static_cast<int64_t>(a.units - a.whole) * a.kb;
+    const int64_t first = static_cast<int64_t>(cut) * a.kb, stop = first + a.kb;
+    auto run_of = [&](int64_t slice) {   // the run that holds a slice
+        int b = static_cast<int>(slice * a.teams / all);
+        int64_t from, to;
+        for (Walk<FORM>::run(a, b, from, to); slice < from; Walk<FORM>::run(a, --b, from, to)) {}
+        for (; slice >= to; Walk<FORM>::run(a, ++b, from, to)) {}
+        return b;
+    };
+    const int b0 = run_of(first), b1 = run_of(stop - 1);
+    if (b0 == b1) return;   // one run has it whole
+    const bool dense = all >= a.teams;   // no run is empty
+    const int c = lane * 8;
+    float v[8] = {};
+    if (c < a.bn) {
+        const int64_t step = static_cast<int64_t>(2) * BM * a.bn * a.side;   // to the next team's
+        const float *p = a.parts + b0 * step + (static_cast<int64_t>(side_at) * 2 * BM + row) * a.bn + c;
+        const int q0 = SPLIT_PARTS ? warp : 0, dq = SPLIT_PARTS ? JOIN_WARPS : 1;
+#pragma unroll 4
+        for (int q = q0; q <= b1 - b0; q += dq) {
+            if (!dense) {
+                int64_t f, to;
+                Walk<FORM>::run(a, b0 + q, f, to);
+                if (f == to) continue;
+            }
+            // the first run's part begins with the tile: slot 1
+            float x[8];
+            load_f32<float, 8>(p + q * step + (q == 0 ? static_cast<int64_t>(BM) * a.bn : 0), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += x[e];
+        }
+    }
+    if (SPLIT_PARTS) {
+        if (c < a.bn)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) share[warp][c + e] = v[e];
+        __syncthreads();
+        if (warp > 0 || c >= a.bn) return;
+        for (int q = 1; q < JOIN_WARPS; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += share[q][c + e];
+    }
+    const int n = min(min(a.bn, a.N - tn * a.bn) - c, 8);
+    if (n <= 0) return;
+    T *to = static_cast<T *>(a.out) + ((second ? a.M : 0) + static_cast<int64_t>(m)) * a.N + tn * a.bn + c;
+    if (a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 16 / sizeof(T)) {
+            float o[16 / sizeof(T)];
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) o[i] = v[e + i];
+            store_f32<T, 16 / sizeof(T)>(to + e, o);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) to[e] = from_f32<T>(v[e]);
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(256) k_round(const float *in, T *out, int64_t n) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
-        out[i] = from_f32<T>(in[i]);
+// rows of src as (planes, rows, pitch) bf16, zeros beyond column d
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_planes(const T *src, __nv_bfloat16 *out, int64_t rows, int d, int pitch) {
+    dependents_may_launch();
+    wait_for_prerequisites();
+    const bool wide = wide_rows<T>(src, d);
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps)
+        copy_row<T>(src + r * d, out + r * pitch, rows * pitch, d, pitch, threadIdx.x & 31, wide);
 }
 
+// ---------------------------------------------------------------- host side
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Call {
     const void *x, *W_in, *W_out;
     int dtype;
     int64_t n, d, f;
+    unsigned char *ws;
     cudaStream_t stream;
 };
 
-template <typename T, typename O>
-cudaError_t product(const Call &c, const void *A, int64_t a_row, int64_t a_k, const void *B, int64_t b_row, int64_t b_k,
-                    int64_t M, int64_t N, int64_t K, O *out, int64_t pitch, bool add = false) {
-    if (M == 0 || N == 0) return cudaSuccess;
-    const Product p{A, B, a_row, a_k, b_row, b_k, M, N, K, out, pitch, add};
-    const int64_t rows = (M + TILE - 1) / TILE;
-    k_product<T, O><<<dim3(static_cast<unsigned>((N + TILE - 1) / TILE), static_cast<unsigned>(rows < 65535 ? rows : 65535)), 256, 0, c.stream>>>(p);
-    return cudaGetLastError();
+// What the gradient takes: a and b [2][n][pf] in the storage type, m [planes][n][pf] bf16.
+// (Not rounded up, so that its size tells one number of rows from another.)
+struct Kept { size_t m, total; int64_t pf; };
+Kept kept_layout(int64_t n, int64_t f, int dtype) {
+    Kept k{};
+    k.pf = ceil_div(f, 8) * 8;
+    const size_t es = dtype == NRNN_BF16 ? 2 : 4, planes = dtype == NRNN_BF16 ? 1 : 3;
+    k.m = up256(2 * es * n * k.pf);
+    k.total = k.m + 2 * planes * n * k.pf + 16;
+    return k;
 }
 
-// ws: 2 n f fp32, then (nothing to keep) 3 n f of T
-template <typename T> int forward(const Call &c, T *y, T *kept, float *ws) {
-    const int64_t nf = c.n * c.f;
-    if (kept == nullptr) kept = reinterpret_cast<T *>(ws + 2 * nf);
-    T *m = kept + 2 * nf;
-    const T *W = static_cast<const T *>(c.W_in);
-    cudaError_t e = product<T>(c, c.x, c.d, 1, W, c.d, 1, c.n, c.f, c.d, ws, c.f);
-    if (e == cudaSuccess) e = product<T>(c, c.x, c.d, 1, W + c.f * c.d, c.d, 1, c.n, c.f, c.d, ws + nf, c.f);
-    if (e != cudaSuccess) return NRNN_ERR_CUDA;
-    k_gate<T><<<1024, 256, 0, c.stream>>>(ws, ws + nf, kept, kept + nf, m, nf);
-    e = product<T>(c, m, c.f, 1, c.W_out, c.f, 1, c.n, c.d, c.f, y, c.d);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+// The workspace.  An operand of bf16 whose rows are 16-byte aligned is used where it
+// lies, every other one is copied to bf16 planes of aligned rows.
+struct Plan {
+    int planes;
+    int64_t pd, pf;
+    size_t x, w_in, w_out, g, kept, gab, parts, total;
+};
+constexpr size_t NO_COPY = ~static_cast<size_t>(0);
+
+bool used_in_place(const void *p, int64_t row, int dtype) {
+    return dtype == NRNN_BF16 && row % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// ws: n f fp32 of gm, 2 n f of T, n d fp32 of gx
+// columns of a tile of a plain product: equal tiles of whole 64-column blocks
+int tile_columns(int64_t N) { return static_cast<int>(ceil_div(ceil_div(N, ceil_div(N, BN)), 64) * 64); }
+
+Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in_lies, bool w_out_lies, bool g_lies,
+              bool keep, bool backward) {
+    Plan p{};
+    p.planes = dtype == NRNN_F32 ? 3 : 1;
+    p.pd = ceil_div(d, 8) * 8;
+    p.pf = ceil_div(f, 8) * 8;
+    size_t at = 256;   // the error word
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up256(bytes);
+        return o;
+    };
+    p.x = x_lies ? NO_COPY : take(2 * p.planes * n * p.pd);
+    p.w_in = w_in_lies ? NO_COPY : take(2 * p.planes * 2 * f * p.pd);
+    p.w_out = w_out_lies ? NO_COPY : take(2 * p.planes * d * p.pf);
+    p.kept = keep || backward ? NO_COPY : take(kept_layout(n, f, dtype).total);
+    p.g = !backward || g_lies ? NO_COPY : take(2 * p.planes * n * p.pd);
+    p.gab = backward ? take(2 * p.planes * 2 * n * p.pf) : NO_COPY;
+    const int64_t widest = tile_columns(d) > tile_columns(f) ? tile_columns(d) : tile_columns(f);
+    p.parts = take(sizeof(float) * 2 * PAIRS * BM * widest);
+    p.total = at;
+    return p;
+}
+
+// an operand as bf16 planes: where it lies, or its copy
 template <typename T>
-int backward(const Call &c, const T *kept, const void *g, T *gx, T *gW_in, T *gW_out, float *ws) {
-    const int64_t nf = c.n * c.f;
-    const T *a = kept, *b = a + nf, *m = b + nf;
-    float *gm = ws, *sum = gm + nf;
-    T *ga = reinterpret_cast<T *>(sum + c.n * c.d), *gb = ga + nf;
-    const T *W = static_cast<const T *>(c.W_in);
-    cudaError_t e = product<T>(c, g, c.d, 1, c.W_out, 1, c.f, c.n, c.f, c.d, gm, c.f);
-    if (e != cudaSuccess) return NRNN_ERR_CUDA;
-    k_gate_back<T><<<1024, 256, 0, c.stream>>>(a, b, gm, ga, gb, nf);
-    e = product<T>(c, ga, c.f, 1, W, 1, c.d, c.n, c.d, c.f, sum, c.d);
-    if (e == cudaSuccess) e = product<T>(c, gb, c.f, 1, W + c.f * c.d, 1, c.d, c.n, c.d, c.f, sum, c.d, true);
-    if (e == cudaSuccess) e = product<T>(c, ga, 1, c.f, c.x, 1, c.d, c.f, c.d, c.n, gW_in, c.d);
-    if (e == cudaSuccess) e = product<T>(c, gb, 1, c.f, c.x, 1, c.d, c.f, c.d, c.n, gW_in + c.f * c.d, c.d);
-    if (e == cudaSuccess) e = product<T>(c, g, 1, c.d, m, 1, c.f, c.d, c.f, c.n, gW_out, c.f);
-    if (e != cudaSuccess) return NRNN_ERR_CUDA;
-    k_round<T><<<1024, 256, 0, c.stream>>>(sum, gx, c.n * c.d);
-    return cudaGetLastError() == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+cudaError_t operand(const Call &c, const void *src, size_t copy, int64_t rows, int64_t d, int64_t pitch, const void **out) {
+    *out = src;
+    if (copy == NO_COPY) return cudaSuccess;
+    __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(c.ws + copy);
+    *out = to;
+    const int64_t b = ceil_div(rows, 8);
+    return launch_dependent(k_planes<T>, static_cast<unsigned>(b < 4864 ? b : 4864), 256, 0, c.stream,
+                            static_cast<const T *>(src), to, rows, static_cast<int>(d), static_cast<int>(pitch));
+}
+
+template <int FORM, typename T>
+cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut,
+                 const CUtensorMap &tmAB, GemmArgs a) {
+    static std::atomic<unsigned long long> configured{0};
+    constexpr size_t smem = gemm_smem<FORM, T>();
+    cudaError_t e = once_per_device(configured, [](int) {
+        return cudaFuncSetAttribute(k_mlp_gemm<FORM, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+    const int64_t most = CUTS<FORM> ? tiles * a.kb : tiles;
+    if (most > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const int pairs = static_cast<int>(most < PAIRS ? most : PAIRS);
+    a.side = 1;
+    a.teams = pairs;
+    a.units = a.whole = static_cast<int>(tiles);
+    if (CUTS<FORM>) {
+        // teams of pairs with the column tiles of one row tile side by side
+        a.side = a.tiles_n <= MOST_SIDE && a.tiles_n <= pairs ? a.tiles_n : 1;
+        a.teams = pairs / a.side;
+        a.units = static_cast<int>(tiles / a.side);
+        a.whole = a.units / a.teams * a.teams;
+    }
+    e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, tmAB, a);
+    const int64_t cut = static_cast<int64_t>(a.units - a.whole) * a.side;
+    if (e == cudaSuccess && cut > 0) {
+        const bool few = cut * 8 <= pairs;   // eight parts each and more
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cut), few ? BM : BM / JOIN_WARPS);
+        cfg.blockDim = dim3(JOIN_WARPS * 32);
+        cfg.stream = c.stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, few ? k_join_parts<FORM, T, true> : k_join_parts<FORM, T, false>, a);
+    }
+    return e;
+}
+
+// a map over bf16 (planes, rows, inner) whose rows are pitch elements apart
+bool map(CUtensorMap *m, const void *base, int64_t inner, int64_t pitch, int64_t rows, int64_t planes, int box_inner, int box_rows) {
+    return make_map_pitched(m, base, inner, pitch, rows, planes, box_inner, box_rows);
+}
+
+GemmArgs args_of(const Call &c, int64_t M, int64_t N, int64_t K, int bn) {
+    GemmArgs a{};
+    a.error = reinterpret_cast<uint32_t *>(c.ws);
+    a.wait_ns = wait_limit_ns();
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.bn = bn;
+    a.tiles_m = static_cast<int>(ceil_div(M, BM));
+    a.tiles_n = static_cast<int>(ceil_div(N, bn));
+    a.kb = static_cast<int>(ceil_div(K, BK));
+    return a;
+}
+
+template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned char *kept, bool keep) {
+    const Kept kl = kept_layout(c.n, c.f, c.dtype);
+    unsigned char *m = kept + kl.m;
+    const void *x, *w_in, *w_out;
+    if (cudaMemsetAsync(c.ws, 0, sizeof(uint32_t), c.stream) != cudaSuccess ||
+        operand<T>(c, c.x, p.x, c.n, c.d, p.pd, &x) != cudaSuccess ||
+        operand<T>(c, c.W_in, p.w_in, 2 * c.f, c.d, p.pd, &w_in) != cudaSuccess ||
+        operand<T>(c, c.W_out, p.w_out, c.d, c.f, p.pf, &w_out) != cudaSuccess)
+        return NRNN_ERR_CUDA;
+    CUtensorMap ta, tb, to, tab;
+    // UP: equal tiles of the units, in whole 64-unit blocks
+    const int units = static_cast<int>(ceil_div(ceil_div(c.f, ceil_div(c.f, BN / 2)), 64) * 64);
+    if (!map(&ta, x, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, BK, units) ||
+        !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS) || (p.planes == 1 && !map(&tab, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
+        return NRNN_ERR_CUDA;
+    if (p.planes != 1) tab = to;
+    GemmArgs a = args_of(c, c.n, c.f, c.d, 2 * units);
+    a.tiles_n = static_cast<int>(ceil_div(c.f, units));
+    a.keep = keep;
+    a.ab = reinterpret_cast<float *>(kept);
+    a.pitch = static_cast<int>(p.pf);
+    if (gemm<UP, T>(c, ta, tb, to, tab, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    const int bn = tile_columns(c.d);
+    a = args_of(c, c.n, c.d, c.f, bn);
+    a.parts = reinterpret_cast<float *>(c.ws + p.parts);
+    a.out = y;
+    a.blocks_out = used_in_place(y, c.d, c.dtype);
+    if (!map(&ta, m, c.f, p.pf, c.n, p.planes, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, BK, bn / 2) ||
+        (a.blocks_out && !map(&to, y, c.d, c.d, c.n, 1, PIECE, BOX_ROWS)))
+        return NRNN_ERR_CUDA;
+    return gemm<DOWN, T>(c, ta, tb, to, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+}
+
+template <typename T>
+int backward(const Call &c, const Plan &p, const unsigned char *kept, const void *g_, T *gx, T *gW_in, T *gW_out) {
+    const Kept kl = kept_layout(c.n, c.f, c.dtype);
+    const unsigned char *m = kept + kl.m;
+    unsigned char *gab = c.ws + p.gab;
+    const void *x, *w_in, *w_out, *g;
+    if (cudaMemsetAsync(c.ws, 0, sizeof(uint32_t), c.stream) != cudaSuccess ||
+        operand<T>(c, c.x, p.x, c.n, c.d, p.pd, &x) != cudaSuccess ||
+        operand<T>(c, c.W_in, p.w_in, 2 * c.f, c.d, p.pd, &w_in) != cudaSuccess ||
+        operand<T>(c, c.W_out, p.w_out, c.d, c.f, p.pf, &w_out) != cudaSuccess ||
+        operand<T>(c, g_, p.g, c.n, c.d, p.pd, &g) != cudaSuccess)
+        return NRNN_ERR_CUDA;
+    CUtensorMap ta, tb, to, tab;
+    float *parts = reinterpret_cast<float *>(c.ws + p.parts);
+    // ga and gb.  fp32: one piece of an epilogue warp holds ga and gb, so tiles of 128
+    int bn = tile_columns(c.f);
+    if (p.planes != 1 && bn > 2 * PIECE) bn = 2 * PIECE;
+    GemmArgs a = args_of(c, c.n, c.f, c.d, bn);
+    a.ab = const_cast<float *>(reinterpret_cast<const float *>(kept));
+    a.pitch = static_cast<int>(p.pf);
+    if (!map(&ta, g, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, 64, BK) ||
+        !map(&to, gab, c.f, p.pf, c.n, 2 * p.planes, PIECE, BOX_ROWS) ||
+        (p.planes == 1 && !map(&tab, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
+        return NRNN_ERR_CUDA;
+    if (p.planes != 1) tab = to;
+    if (gemm<DH, T>(c, ta, tb, to, tab, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    // gx
+    bn = tile_columns(c.d);
+    a = args_of(c, c.n, c.d, c.f, bn);
+    a.kb_half = a.kb;
+    a.kb *= 2;
+    a.parts = parts;
+    a.out = gx;
+    a.blocks_out = used_in_place(gx, c.d, c.dtype);
+    if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, 64, BK) ||
+        (a.blocks_out && !map(&to, gx, c.d, c.d, c.n, 1, PIECE, BOX_ROWS)))
+        return NRNN_ERR_CUDA;
+    if (gemm<GX, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    // gW_in
+    a = args_of(c, c.f, c.d, c.n, bn);
+    a.m_half = a.tiles_m;
+    a.tiles_m *= 2;
+    a.parts = parts;
+    a.out = gW_in;
+    a.blocks_out = used_in_place(gW_in, c.d, c.dtype);
+    if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.planes, 64, BK) || !map(&tb, x, c.d, p.pd, c.n, p.planes, 64, BK) ||
+        (a.blocks_out && !map(&to, gW_in, c.d, c.d, c.f, 2, PIECE, BOX_ROWS)))
+        return NRNN_ERR_CUDA;
+    if (gemm<GWI, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    // gW_out
+    bn = tile_columns(c.f);
+    a = args_of(c, c.d, c.f, c.n, bn);
+    a.parts = parts;
+    a.out = gW_out;
+    a.blocks_out = used_in_place(gW_out, c.f, c.dtype);
+    if (!map(&ta, g, c.d, p.pd, c.n, p.planes, 64, BK) || !map(&tb, m, c.f, p.pf, c.n, p.planes, 64, BK) ||
+        (a.blocks_out && !map(&to, gW_out, c.f, c.f, c.d, 1, PIECE, BOX_ROWS)))
+        return NRNN_ERR_CUDA;
+    return gemm<GWO, T>(c, ta, tb, to, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 bool sizes_fit(int64_t n, int64_t d, int64_t f) { return n <= (1 << 30) && d <= (1 << 20) && f <= (1 << 20); }
@@ -172,34 +961,35 @@ extern "C" {
 
 size_t nrnn_gated_mlp_kept_bytes(int64_t rows, int64_t f, int dtype) {
     if (rows < 0 || f <= 0 || !sizes_fit(rows, 1, f) || (dtype != NRNN_F32 && dtype != NRNN_BF16)) return 0;
-    return up256(3 * (dtype == NRNN_BF16 ? 2 : 4) * rows * f + 1);
+    return kept_layout(rows, f, dtype).total;
 }
 
 size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dtype, int backward) {
     if (d <= 0 || !sizes_fit(0, d, 1) || nrnn_gated_mlp_kept_bytes(rows, f, dtype) == 0) return 0;
-    const size_t elem = dtype == NRNN_BF16 ? 2 : 4;
-    return up256(rows * f * (backward ? 4 + 2 * elem : 8 + 3 * elem) + (backward ? 4 * rows * d : 0) + 1);
+    return plan_for(rows, d, f, dtype, false, false, false, false, false, backward != 0).total;
 }
 
 int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, int dtype, int64_t rows, int64_t d,
                            int64_t f, void *y, void *kept, void *workspace, size_t ws_bytes, void *stream) {
-    const Call c{x, W_in, W_out, dtype, rows, d, f, static_cast<cudaStream_t>(stream)};
+    const Call c{x, W_in, W_out, dtype, rows, d, f, static_cast<unsigned char *>(workspace), static_cast<cudaStream_t>(stream)};
     const int st = check(c);
     if (st != NRNN_OK) return st;
     if (rows == 0) return NRNN_OK;
     const uintptr_t elem = dtype == NRNN_BF16 ? 2 : 4;
     if (y == nullptr || reinterpret_cast<uintptr_t>(y) % elem != 0 || reinterpret_cast<uintptr_t>(kept) % 256 != 0)
         return NRNN_ERR_INVALID_ARG;
-    if (!usable(workspace, ws_bytes, nrnn_gated_mlp_workspace_bytes(rows, d, f, dtype, 0))) return NRNN_ERR_WORKSPACE;
-    float *ws = static_cast<float *>(workspace);
-    return dtype == NRNN_BF16 ? forward(c, static_cast<__nv_bfloat16 *>(y), static_cast<__nv_bfloat16 *>(kept), ws)
-                              : forward(c, static_cast<float *>(y), static_cast<float *>(kept), ws);
+    const Plan p = plan_for(rows, d, f, dtype, used_in_place(x, d, dtype), used_in_place(W_in, d, dtype),
+                            used_in_place(W_out, f, dtype), false, kept != nullptr, false);
+    if (!usable(workspace, ws_bytes, p.total)) return NRNN_ERR_WORKSPACE;
+    unsigned char *k = kept != nullptr ? static_cast<unsigned char *>(kept) : c.ws + p.kept;
+    return dtype == NRNN_BF16 ? forward(c, p, static_cast<__nv_bfloat16 *>(y), k, kept != nullptr)
+                              : forward(c, p, static_cast<float *>(y), k, kept != nullptr);
 }
 
 int nrnn_gated_mlp_backward(const void *x, const void *W_in, const void *W_out, const void *kept, const void *g,
                             int dtype, int64_t rows, int64_t d, int64_t f, void *gx, void *gW_in, void *gW_out,
                             void *workspace, size_t ws_bytes, void *stream) {
-    const Call c{x, W_in, W_out, dtype, rows, d, f, static_cast<cudaStream_t>(stream)};
+    const Call c{x, W_in, W_out, dtype, rows, d, f, static_cast<unsigned char *>(workspace), static_cast<cudaStream_t>(stream)};
     const int st = check(c);
     if (st != NRNN_OK) return st;
     const uintptr_t elem = dtype == NRNN_BF16 ? 2 : 4;
@@ -212,13 +1002,14 @@ int nrnn_gated_mlp_backward(const void *x, const void *W_in, const void *W_out, 
         return cudaMemsetAsync(gW_in, 0, elem * 2 * f * d, c.stream) == cudaSuccess &&
                        cudaMemsetAsync(gW_out, 0, elem * f * d, c.stream) == cudaSuccess
                    ? NRNN_OK : NRNN_ERR_CUDA;
-    if (!usable(workspace, ws_bytes, nrnn_gated_mlp_workspace_bytes(rows, d, f, dtype, 1))) return NRNN_ERR_WORKSPACE;
+    const Plan p = plan_for(rows, d, f, dtype, used_in_place(x, d, dtype), used_in_place(W_in, d, dtype),
+                            used_in_place(W_out, f, dtype), used_in_place(g, d, dtype), true, true);
+    if (!usable(workspace, ws_bytes, p.total)) return NRNN_ERR_WORKSPACE;
+    const unsigned char *k = static_cast<const unsigned char *>(kept);
     return dtype == NRNN_BF16
-               ? backward<__nv_bfloat16>(c, static_cast<const __nv_bfloat16 *>(kept), g, static_cast<__nv_bfloat16 *>(gx),
-                                         static_cast<__nv_bfloat16 *>(gW_in), static_cast<__nv_bfloat16 *>(gW_out),
-                                         static_cast<float *>(workspace))
-               : backward<float>(c, static_cast<const float *>(kept), g, static_cast<float *>(gx), static_cast<float *>(gW_in),
-                                 static_cast<float *>(gW_out), static_cast<float *>(workspace));
+               ? backward(c, p, k, g, static_cast<__nv_bfloat16 *>(gx), static_cast<__nv_bfloat16 *>(gW_in),
+                          static_cast<__nv_bfloat16 *>(gW_out))
+               : backward(c, p, k, g, static_cast<float *>(gx), static_cast<float *>(gW_in), static_cast<float *>(gW_out));
 }
 
 }  // extern "C"

@@ -151,6 +151,11 @@ size_t newton_smem_bytes(int dtype, bool fused);
 bool make_map_planes(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int64_t planes,
                      uint32_t box_inner, uint32_t box_rows, bool swizzle128);
 
+// the same with the 128-byte swizzle over rows that are pitch elements apart (a multiple
+// of 8); inner may be any width
+bool make_map_pitched(CUtensorMap *m, const void *base, int64_t inner, int64_t pitch, int64_t rows,
+                      int64_t planes, uint32_t box_inner, uint32_t box_rows);
+
 // byte offset of the error word in a Newton forward's workspace
 size_t newton_error_offset(int K);
 

@@ -68,13 +68,12 @@
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
 #include "nrnn_internal.h"
+#include "pair.cuh"
 #include "rows.cuh"
-#include "tcgen05.cuh"
 
 namespace nrnn {
 namespace {
 
-constexpr uint64_t SETTLE_NS = 2000000000ull;   // for what is in flight after a wait gave up
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int PAIRS = 76;   // of 152 SMs: the work is divided for this many
 
@@ -127,43 +126,6 @@ struct GemmArgs {
                               // rows over 50021 x 1024 bf16 with gradient: 139 -> 121 us)
 };
 
-// mbar_wait_bounded that also ends when another role of the pair gave up, and tells
-// both CTAs when it does
-__device__ __forceinline__ bool wait_or_abort(const GemmArgs &a, uint64_t *bar, uint32_t parity,
-                                              volatile uint32_t *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint32_t hint = static_cast<uint32_t>(a.wait_ns < 1000000u ? a.wait_ns : 1000000u);
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (*abort != 0) return false;
-        if (mbar_try_wait_hint(bar, parity, hint)) return true;
-        if (globaltimer_ns() - t0 > a.wait_ns) {
-            for (uint32_t r = 0; r < 2; ++r)
-                cluster_store(cluster_addr(const_cast<const uint32_t *>(abort), r), 1u);
-            atomicOr(a.error, 2u);
-            return false;
-        }
-    }
-}
-
-// After a wait gave up, and both CTAs' roles have ended: sees through what is in flight.
-// issued: stages that each CTA's producer started the copies of.  One that is ahead of
-// the other (by at most the ring, whose stages are handed back to both at once) has
-// copies that the stage's barrier, rank 0's, cannot complete on: it is brought to wait
-// for that CTA's bytes alone.  By the issuing thread of rank 0.
-__device__ __forceinline__ void settle(const GemmArgs &a, const volatile int *issued, uint64_t *full_bar,
-                                       uint64_t *drain_bar, uint32_t bytes_1) {
-    mma_commit_pair(drain_bar);
-    mbar_wait_bounded(drain_bar, 0, SETTLE_NS, a.error);
-    const int n0 = issued[0], n1 = issued[1], both = n0 < n1 ? n0 : n1, most = n0 < n1 ? n1 : n0;
-    for (int i = both > STAGES ? both - STAGES : 0; i < most; ++i) {
-        uint64_t *bar = &full_bar[i % STAGES];
-        if (i >= both && n0 > n1) mbar_complete_tx(bar, bytes_1);              // was to come from rank 1
-        else if (i >= both) mbar_arrive_expect_tx(bar, bytes_1);               // rank 0 never got there
-        mbar_wait_bounded(bar, (i / STAGES) & 1, SETTLE_NS, a.error);
-    }
-}
-
 template <typename T> __device__ __forceinline__ void store_cols(T *p, const float (&v)[PIECE], int n, bool wide) {
     constexpr int VEC = 16 / sizeof(T);
     if (wide) {
@@ -185,15 +147,6 @@ __device__ __forceinline__ void times(float (&v)[PIECE], float f) {
     float2 *p = reinterpret_cast<float2 *>(v);
 #pragma unroll
     for (int e = 0; e < PIECE / 2; ++e) p[e] = mul2(p[e], make_float2(f, f));
-}
-
-// Two values as bf16, the nearest; or the type's largest where that is an infinity,
-// so that a finite value less its first plane is a number.  (An infinity less the
-// largest stays one, and its third plane is NaN.)
-__device__ __forceinline__ __nv_bfloat162 finite_bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return *reinterpret_cast<__nv_bfloat162 *>(&r);
 }
 
 // A unit is what a pair takes at a time: a tile; `group` tiles beside one another
@@ -681,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     cluster_sync_all();   // neither CTA leaves while the other may still reach into it
     if (s_abort != 0) {   // the same in both
         if (warp == 1 && lane == 0) {
-            if (rank == 0) settle(a, s_issued, full_bar, &drain_bar, stage_bytes<FORM>(a, 1));
+            if (rank == 0) settle<STAGES>(a, s_issued, full_bar, &drain_bar, stage_bytes<FORM>(a, 1));
             else mbar_wait_bounded(&drain_bar, 0, SETTLE_NS, a.error);
         }
         __syncwarp();
@@ -880,13 +833,6 @@ struct GatherArgs {
     int n;
 };
 
-// The first plane of v: the nearest bf16, or the one below in magnitude where that is
-// an infinity but v (the lowest value, as a mask) is not, so that v less it is a number.
-__device__ __forceinline__ float plane_of(float v) {
-    const float h = __bfloat162float(__float2bfloat16_rn(v));
-    return isinf(h) ? __bfloat162float(__float2bfloat16_rz(v)) : h;
-}
-
 // The mantissa, in [1, 2), of a finite value that is not zero or subnormal; else 1.
 // A bf16 G is divided by the mantissa of the first kept row's dL/dloss c, and its two
 // products are multiplied by it at their end.  Where all rows have the same dL/dloss
@@ -906,43 +852,6 @@ __device__ __forceinline__ float4 row_grad(float lse, float g) {
     constexpr float LOG2E_LOW = 1.92596303e-8f;   // log2(e) less LOG2E
     const float l = lse * LOG2E, low = fmaf(lse, LOG2E, -l) + lse * LOG2E_LOW;
     return make_float4(l, g, isfinite(low) ? fmaf(-low * LN2, g, g) : g, 0.f);
-}
-
-// One row of `pitch` values (a multiple of 8) as bf16 planes, by the lanes of a warp;
-// src null: zeros.  16 bytes out at a time; wide: 16 bytes in as well.
-template <typename T>
-__device__ __forceinline__ void copy_row(const T *src, __nv_bfloat16 *dst, int64_t plane, int d,
-                                         int pitch, int lane, bool wide) {
-#pragma unroll 4
-    for (int c = lane * 8; c < pitch; c += 256) {
-        float v[8];
-        if (src != nullptr && wide) {
-#pragma unroll
-            for (int q = 0; q < 8; q += 16 / sizeof(T)) {
-                float x[16 / sizeof(T)];
-                load_f32<T, 16 / sizeof(T)>(src + c + q, x);
-#pragma unroll
-                for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) v[q + e] = x[e];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = src != nullptr && c + e < d ? to_f32(src[c + e]) : 0.f;
-        }
-#pragma unroll
-        for (int p = 0; p < (sizeof(T) == 4 ? 3 : 1); ++p) {
-            float h[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[e] = sizeof(T) == 4 ? plane_of(v[e]) : v[e];
-                v[e] -= h[e];
-            }
-            store_f32<__nv_bfloat16, 8>(dst + p * plane + c, h);
-        }
-    }
-}
-// rows of src can be read 16 bytes at a time
-template <typename T> __device__ __forceinline__ bool wide_rows(const void *src, int d) {
-    return d % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
 }
 
 template <typename T, typename Id, bool FEW>
