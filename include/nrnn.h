@@ -466,7 +466,8 @@ int nrnn_debug_pack_plan(const int32_t *cu_seqlens, int64_t num_segments, int64_
 
 /*
  * Upper limit, in nanoseconds, of the bounded device waits of the Newton
- * forward and backward and of the vocabulary loss that later calls launch
+ * forward and backward, of the vocabulary loss, of the linear recurrence and of the
+ * gated feed-forward block that later calls launch
  * (default 2e9 = 2 s).  The tensor-core waits of nrnn_input_projection and
  * nrnn_decode_step_x always give up after 2 s.  Process-wide; returns the
  * previous value.
@@ -661,11 +662,13 @@ size_t nrnn_linear_recurrence_workspace_bytes(int64_t B, int64_t T, int64_t d_h,
  *               before the first step; NULL: zeros
  *   H           device, (B, T, d_h) of dtype
  *   last        device, fp32 of state's shape: the states after the last step,
- *               unrounded (an empty sequence's are its first); may be state; NULL:
- *               not wanted
+ *               unrounded (an empty sequence's are its first); NULL: not wanted
  *   workspace   device, 256-byte aligned, of at least
- *               nrnn_linear_recurrence_workspace_bytes(..., 0)
- * States are fp32 throughout; no result depends on the order in which threads run.
+ *               nrnn_linear_recurrence_workspace_bytes(..., 0).  Its second 32-bit
+ *               word is 0 once the work is done, or not if a device wait gave up
+ *               (nrnn_set_wait_limit_ns): then outputs are NaN where they depended
+ *               on it.  So too in the backward
+ * The outputs must not overlap one another or the inputs.  States are fp32 throughout; no result depends on the order in which threads run.
  * A sigmoid is bounded below by 2^-63.
  */
 int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *params, int64_t B,
@@ -720,7 +723,10 @@ size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dt
  *   y           device, (rows, d) of dtype
  *   kept        device, 256-byte aligned, nrnn_gated_mlp_kept_bytes: what the
  *               gradient takes (its layout is the library's); NULL: not wanted
- *   workspace   device, 256-byte aligned, nrnn_gated_mlp_workspace_bytes(..., 0)
+ *   workspace   device, 256-byte aligned, nrnn_gated_mlp_workspace_bytes(..., 0).  Its
+ *               first 32-bit word is 0 once the work is done, or not if a device wait
+ *               gave up (nrnn_set_wait_limit_ns): then outputs are NaN where they
+ *               depended on it.  So too in the backward
  * The buffers of the tensors need only their element's alignment.
  */
 int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, int dtype,

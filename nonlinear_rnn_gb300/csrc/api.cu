@@ -145,7 +145,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 3-D map over a (B, T, width) row-major array with a (TILE_U x NEWTON_L x 1) box.
-bool make_map(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_t T, int64_t B) {
+bool make_map(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_t T, int64_t B,
+              uint32_t units = TILE_U, uint32_t steps = NEWTON_L) {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
     const size_t es = elem_size(dtype);
@@ -153,7 +154,7 @@ bool make_map(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_
                           static_cast<cuuint64_t>(B)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(width * es),
                              static_cast<cuuint64_t>(width * es * T)};
-    cuuint32_t box[3] = {TILE_U, NEWTON_L, 1};
+    cuuint32_t box[3] = {units, steps, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(m, dtype == NRNN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
@@ -166,7 +167,8 @@ bool make_map(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_
 // 4-D map over a (B, T, 3 d_h) preactivation-shaped array seen as (d_h, gate,
 // T, B), box (TILE_U x 1 x NEWTON_L x 1): one gate block of a tile, clipped at
 // d_h so that a partial unit tile never reaches into the next gate's columns.
-bool make_map_gates(CUtensorMap *m, const void *base, int dtype, int64_t d_h, int64_t T, int64_t B) {
+bool make_map_gates(CUtensorMap *m, const void *base, int dtype, int64_t d_h, int64_t T, int64_t B,
+                    uint32_t units = TILE_U, uint32_t steps = NEWTON_L) {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
     const size_t es = elem_size(dtype);
@@ -174,7 +176,7 @@ bool make_map_gates(CUtensorMap *m, const void *base, int dtype, int64_t d_h, in
                           static_cast<cuuint64_t>(B)};
     cuuint64_t strides[3] = {static_cast<cuuint64_t>(d_h * es), static_cast<cuuint64_t>(3 * d_h * es),
                              static_cast<cuuint64_t>(3 * d_h * es * T)};
-    cuuint32_t box[4] = {TILE_U, 1, NEWTON_L, 1};
+    cuuint32_t box[4] = {units, 1, steps, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = fn(m, dtype == NRNN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
@@ -280,6 +282,15 @@ bool make_map_planes(CUtensorMap *m, const void *base, int64_t inner, int64_t ro
 bool make_map_pitched(CUtensorMap *m, const void *base, int64_t inner, int64_t pitch, int64_t rows,
                       int64_t planes, uint32_t box_inner, uint32_t box_rows) {
     return map_planes(m, base, inner, pitch, rows, planes, box_inner, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool make_map_steps(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_t T, int64_t B,
+                    uint32_t units, uint32_t steps) {
+    return make_map(m, base, dtype, width, T, B, units, steps);
+}
+bool make_map_gate_steps(CUtensorMap *m, const void *base, int dtype, int64_t d, int64_t T, int64_t B,
+                         uint32_t units, uint32_t steps) {
+    return make_map_gates(m, base, dtype, d, T, B, units, steps);
 }
 
 uint64_t wait_limit_ns() { return g_wait_ns.load(); }

@@ -11,26 +11,92 @@
 //   gP_a = -w rate r (1 - r),  g_rate = -sum w r,  g_b_a = sum gP_a
 //   gP_i = G s v i (1 - i),    g_b_i = sum gP_i,   gP_v = G s i
 //
-// r and i are bounded below by 2^-63 (the exponential is clamped, so that 1 - r is
-// exact to rounding on both sides); where s is zero all the same (a rate of zero)
-// the term with a^2 / s is left out, which is its limit as r vanishes.
+// r and i are bounded below by 2^-63 (the exponential is clamped, so that two sigmoids
+// share a reciprocal and 1 - r is exact to rounding on both sides); where s is zero all
+// the same (a rate of zero) the term with a^2 / s is left out, which is its limit as r
+// vanishes.
+//
+// One pass over the data in each direction, bound by HBM: 4 values a unit and step
+// forward, 8 backward.  A tile is 64 units (two a lane, on packed f32x2 arithmetic) and
+// SEG steps a warp; TMA brings it to shared memory and takes the result from there.
+// CTAs are persistent: they take tiles from a counter, every column's next chunk after
+// all columns' chunks before it (backward: from the end of time), and start the copies
+// of the next tile while they work on one.  A thread composes the maps h -> A h + B of
+// its steps, the warps' maps meet in shared memory, and the carry into the chunk comes
+// from a look-back whose grouping is fixed: chunks form groups of `group`; a chunk
+// publishes its map, folds the maps of its group's chunks before it, in order, and
+// starts them from the state at the end of the group before, which that group's last
+// chunk publishes.  So no result depends on timing, and a chain has one hop a group.
+//
+// A sequence's first state (backward: the gradient of its last) cuts the scan: the map
+// of a step that begins a pack's segment is marked by the sign of its A (a decay is
+// never negative), and what a marked map is applied to is not looked at, NaN or not.
+//
+// A wait that gives up (the limit of nrnn_set_wait_limit_ns) sets the workspace's second
+// word, which ends the other waits too, and gives NaN in what depended on it.
+#include <type_traits>
+
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
 #include "nrnn_internal.h"
+#include "rows.cuh"
+#include "tcgen05.cuh"
 
 namespace nrnn {
 namespace {
 
-struct Gates {
-    float a, s;        // decay, sqrt(1 - a^2)
-    float r, omr;      // r, 1 - r
-    float i, omi;
+constexpr int UNITS = 64, NW = 4, THREADS = NW * 32;
+constexpr uint64_t SETTLE_NS = 2000000000ull;   // for copies in flight after a wait gave up
+
+template <typename TS> constexpr int seg_of() { return sizeof(TS) == 2 ? 16 : 8; }       // steps a warp
+template <typename TS> constexpr int steps_of() { return NW * seg_of<TS>(); }            // steps a tile
+template <typename TS> constexpr int plane_of() { return steps_of<TS>() * UNITS; }       // elements of a tile's block
+
+struct RecArgs {
+    const void *H;                    // backward: (B, T, d)
+    const float *params, *state;      // (3, d); (rows, d) or null
+    const int32_t *cu;                // pack: (rows + 1) offsets
+    int rows;                         // sequences: B or segments
+    int T, d;
+    int n_ut, n_cols, n_chunks;       // unit tiles; B n_ut; chunks of time
+    int group;                        // chunks of a look-back group
+    int64_t n_tiles;
+    float *last;                      // forward: (rows, d) or null
+    const float *g_last;              // backward: (rows, d) or null
+    float *g_state;                   // backward: (rows, d) or null
+    float *part;                      // backward: [n_cols][n_chunks][3][UNITS] sums of a tile
+    unsigned long long *slots;        // [n_cols][n_chunks][UNITS] maps of chunks
+    unsigned long long *ends;         // [n_cols][groups][UNITS] states after a group
+    uint32_t *ticket;
+    uint32_t *error;
+    uint64_t wait_ns;
 };
 
-__device__ __forceinline__ void sigmoid_both(float x, float &s, float &oms) {
-    const float e = ex2_approx(min_nan(-LOG2E * x, EXP2_CLAMP));
-    s = rcp_approx(1.0f + e);
-    oms = e * s;
+// ---------------------------------------------------------------- the gates
+struct UnitWeights {   // of a lane's two units
+    float2 rate, fall2, nb_a, nb_i;   // rate; -rate log2 e; -b log2 e
+};
+
+__device__ __forceinline__ float2 two_of(const float *p, bool ok) {
+    return ok ? *reinterpret_cast<const float2 *>(p) : make_float2(0.f, 0.f);
+}
+__device__ __forceinline__ UnitWeights weights_of(const float *params, int d, int u, bool ok) {
+    UnitWeights w;
+    w.rate = two_of(params + u, ok);
+    w.fall2 = mul2(w.rate, splat2(-LOG2E));
+    w.nb_a = mul2(two_of(params + d + u, ok), splat2(-LOG2E));
+    w.nb_i = mul2(two_of(params + 2 * d + u, ok), splat2(-LOG2E));
+    return w;
+}
+
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
+    const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ void store2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
 
 __device__ __forceinline__ float sqrt_approx(float x) {
@@ -38,133 +104,579 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-// 1 - e^-y: below 1/4 by its series to y^6 / 720, where the difference would lose bits
-__device__ __forceinline__ float one_less_exp(float y, float e) {
-    const float p = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 720, 1.f / 120), -1.f / 24), 1.f / 6), -0.5f), 1.f);
-    return y < 0.25f ? p : 1.f - e;
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__device__ __forceinline__ Gates gates_of(float pa, float pi, float rate, float b_a, float b_i) {
-    Gates g;
-    sigmoid_both(pa + b_a, g.r, g.omr);
-    sigmoid_both(pi + b_i, g.i, g.omi);
-    const float fall = rate * g.r;
-    g.a = ex2_approx(-LOG2E * fall);
-    g.s = sqrt_approx(one_less_exp(2.f * fall, g.a * g.a));
-    return g;
+// 1 - a^2 with a = exp(-fall): for small y = 2 fall, where the difference would lose
+// bits, by the series of 1 - e^-y.  TERMS 5: below 1/4, to y^6 / 5040 (5e-8); 3: below
+// 1/16, to y^4 / 120 (1.3e-7), and 2^-19 by the difference at that border.
+template <int TERMS> __device__ __forceinline__ float2 one_less_square(float2 a, float2 y) {
+    float2 p;
+    if (TERMS == 5) {
+        p = fma2(y, splat2(-1.f / 720), splat2(1.f / 120));
+        p = fma2(y, p, splat2(-1.f / 24));
+    } else {
+        p = splat2(-1.f / 24);
+    }
+    p = fma2(y, p, splat2(1.f / 6));
+    p = fma2(y, p, splat2(-0.5f));
+    p = fma2(y, p, splat2(1.f));
+    p = mul2(y, p);
+    const float2 q = fma2(mul2(a, splat2(-1.f)), a, splat2(1.f));
+    constexpr float LIMIT = TERMS == 5 ? 0.25f : 0.0625f;
+    return make_float2(y.x < LIMIT ? p.x : q.x, y.y < LIMIT ? p.y : q.y);
 }
 
-constexpr int SEQ_THREADS = 128;
+// e^-x in exponent-2 units, clamped: 1 / (1 + e) = sig, e / (1 + e) = 1 - sig
+__device__ __forceinline__ float2 falling(float2 p, float2 nb) {
+    return ex2_2(clamp2(fma2(p, splat2(-LOG2E), nb)));
+}
 
-struct RecArgs {
-    const void *P, *H, *gH;
-    const float *params, *state;      // state (rows, d) or null
-    const int32_t *cu;
-    int rows;                         // sequences: B or segments
-    int64_t T;
-    int d;
-    void *H_out;
-    float *last;                      // (rows, d) or null
-    const float *g_last;
-    void *gP;
-    float *g_state, *gparams;
-    float *part;                      // (rows, 3, d) sums of the parameters' gradients
+template <int TERMS>
+__device__ __forceinline__ void forward_gates(float2 pa, float2 pi, float2 v, const UnitWeights &w, float2 &a, float2 &u) {
+    const float2 one = splat2(1.f);
+    const float2 da = add2(falling(pa, w.nb_a), one), di = add2(falling(pi, w.nb_i), one);
+    const float2 inv = rcp_2(mul2(da, di));
+    const float2 r = mul2(inv, di), i = mul2(inv, da);
+    a = ex2_2(mul2(w.fall2, r));
+    const float2 q = one_less_square<TERMS>(a, mul2(add2(w.rate, w.rate), r));
+    u = mul2(mul2(make_float2(sqrt_approx(q.x), sqrt_approx(q.y)), i), v);
+}
+
+__device__ __forceinline__ float2 decay_of(float2 pa, const UnitWeights &w) {
+    return ex2_2(mul2(w.fall2, rcp_2(add2(falling(pa, w.nb_a), splat2(1.f)))));
+}
+
+// ------------------------------------------------------ maps h -> A h + B of two units
+struct Map2 { float2 A, B; };
+
+__device__ __forceinline__ bool marked(float A) { return __float_as_int(A) < 0; }
+template <bool CUTS> __device__ __forceinline__ float apply(float A, float B, float h) {
+    const float y = fmaf(A, h, B);
+    return CUTS && marked(A) ? B : y;
+}
+template <bool CUTS> __device__ __forceinline__ float2 apply(const Map2 &m, float2 h) {
+    if (!CUTS) return fma2(m.A, h, m.B);
+    return make_float2(apply<true>(m.A.x, m.B.x, h.x), apply<true>(m.A.y, m.B.y, h.y));
+}
+__device__ __forceinline__ float both(float A1, float A2) {   // the product, marked if either is
+    return __uint_as_float(__float_as_uint(A1 * A2) | ((__float_as_uint(A1) | __float_as_uint(A2)) & 0x80000000u));
+}
+// m1, then m2
+template <bool CUTS> __device__ __forceinline__ Map2 then(const Map2 &m1, const Map2 &m2) {
+    Map2 m;
+    m.B = apply<CUTS>(m2, m1.B);
+    m.A = CUTS ? make_float2(both(m1.A.x, m2.A.x), both(m1.A.y, m2.A.y)) : mul2(m1.A, m2.A);
+    return m;
+}
+
+// a lane's two slots; the pair of either is its own ready flag (see publish)
+__device__ __forceinline__ void publish2(unsigned long long *slot, const Map2 &m) {
+    unsigned long long v0 = pack_pair(m.A.x, m.B.x), v1 = pack_pair(m.A.y, m.B.y);
+    if (v0 == SLOT_EMPTY) v0 = pack_pair(0.f, -0.f);
+    if (v1 == SLOT_EMPTY) v1 = pack_pair(0.f, -0.f);
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(slot), "l"(v0), "l"(v1) : "memory");
+}
+__device__ __forceinline__ ulonglong2 peek2(const unsigned long long *slot) {
+    ulonglong2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "l"(slot) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool there(const ulonglong2 &v) { return v.x != SLOT_EMPTY && v.y != SLOT_EMPTY; }
+__device__ __forceinline__ Map2 map_of(const ulonglong2 &v) {
+    return Map2{make_float2(pair_A(v.x), pair_A(v.y)), make_float2(pair_b(v.x), pair_b(v.y))};
+}
+// waits for a slot; false (and NaN) if it gave up or another wait of the call did
+__device__ __forceinline__ Map2 await2(const unsigned long long *slot, ulonglong2 v, const RecArgs &a) {
+    if (!there(v)) {
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            v = peek2(slot);
+            if (there(v)) break;
+            __nanosleep(32);
+            const bool late = globaltimer_ns() - t0 > a.wait_ns;
+            if (late) atomicOr(a.error, 1u);
+            if (late || *static_cast<volatile uint32_t *>(a.error) != 0) {
+                const float nan = __int_as_float(0x7fffffff);
+                return Map2{splat2(nan), splat2(nan)};
+            }
+        }
+    }
+    return map_of(v);
+}
+
+// What a CTA shares while it works on a tile
+struct Shared {
+    float2 aggA[NW][32], aggB[NW][32];     // maps of the warps' steps, in the scan's order
+    float2 preA[NW][32], preB[NW][32];     // maps of runs of the group's chunks before
+    float2 end[32];                        // state after the group before
+    uint64_t bar[2];
+    int64_t tile[2];
 };
 
-__device__ __forceinline__ void span_of(const RecArgs &a, int row, int64_t &t0, int64_t &t1) {
-    if (a.cu == nullptr) {
-        t0 = row * a.T;
-        t1 = t0 + a.T;
-        return;
+// The carry into this warp's steps.  q: the chunk in the scan's order (backward: from the
+// end of time); m: the map of this warp's steps; place: the warp in the scan's order;
+// first: the state that the first group starts from.  Called by all threads; two barriers.
+template <bool CUTS>
+__device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int col, int q, int place, int lane, const Map2 &m,
+                                             float2 first, bool ok) {
+    s.aggA[place][lane] = m.A;
+    s.aggB[place][lane] = m.B;
+    const int before = q % a.group, g = q / a.group, groups = (a.n_chunks + a.group - 1) / a.group;
+    unsigned long long *slot = a.slots + (static_cast<int64_t>(col) * a.n_chunks + q) * UNITS + 2 * lane;
+    unsigned long long *end = a.ends + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
+    __syncthreads();
+    auto warps_map = [&](int w) { return Map2{s.aggA[w][lane], s.aggB[w][lane]}; };
+    Map2 all{};
+    if (place == 0) {
+        all = warps_map(0);
+#pragma unroll
+        for (int w = 1; w < NW; ++w) all = then<CUTS>(all, warps_map(w));
+        if (q + 1 < a.n_chunks && before + 1 < a.group) publish2(slot, all);
     }
-    t0 = min(max(static_cast<int64_t>(__ldg(a.cu + row)), static_cast<int64_t>(0)), a.T);
-    t1 = min(max(static_cast<int64_t>(__ldg(a.cu + row + 1)), t0), a.T);
+    // a run of the group's chunks before this one: 0 .. before - 1
+    const int k0 = before * place / NW, k1 = before * (place + 1) / NW;
+    if (place == NW - 1) {   // and the state after the group before
+        float2 h = first;
+        if (g > 0) h = await2(end - UNITS, peek2(end - UNITS), a).B;
+        s.end[lane] = h;
+    }
+    Map2 run{splat2(1.f), splat2(0.f)};
+    for (int k = k0; k < k1; k += 4) {
+        ulonglong2 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (k + j < k1) v[j] = peek2(slot - static_cast<int64_t>(before - k - j) * UNITS);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (k + j < k1) {
+                const Map2 x = await2(slot - static_cast<int64_t>(before - k - j) * UNITS, v[j], a);
+                run = k + j == k0 ? x : then<CUTS>(run, x);
+            }
+    }
+    s.preA[place][lane] = run.A;
+    s.preB[place][lane] = run.B;
+    __syncthreads();
+    float2 h = s.end[lane];
+    if (before > 0)
+#pragma unroll
+        for (int w = 0; w < NW; ++w) h = apply<CUTS>(Map2{s.preA[w][lane], s.preB[w][lane]}, h);
+    if (!ok) h = splat2(__int_as_float(0x7fffffff));
+    if (place == 0 && before + 1 == a.group && q + 1 < a.n_chunks) publish2(end, Map2{splat2(0.f), apply<CUTS>(all, h)});
+    for (int w = 0; w < place; ++w) h = apply<CUTS>(warps_map(w), h);
+    return h;
 }
 
-template <typename TS>
-__global__ void __launch_bounds__(SEQ_THREADS) k_forward(const RecArgs a) {
-    const int u = blockIdx.x * SEQ_THREADS + threadIdx.x;
-    if (u >= a.d) return;
-    const float rate = a.params[u], b_a = a.params[a.d + u], b_i = a.params[2 * a.d + u];
-    for (int row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        int64_t t0, t1;
-        span_of(a, row, t0, t1);
-        const int64_t at = static_cast<int64_t>(row) * a.d + u;
-        float h = a.state != nullptr ? a.state[at] : 0.f;
-        for (int64_t t = t0; t < t1; ++t) {
-            const TS *p = static_cast<const TS *>(a.P) + t * 3 * a.d + u;
-            const Gates g = gates_of(to_f32(p[0]), to_f32(p[a.d]), rate, b_a, b_i);
-            h = fmaf(g.a, h, g.s * g.i * to_f32(p[2 * a.d]));
-            static_cast<TS *>(a.H_out)[t * a.d + u] = from_f32<TS>(h);
+// A pack's segments at a warp's SEG steps from t0: lane r < SEG has the segment of step
+// t0 + r, and whether the step is its first or its last (bit r of the masks).
+template <int SEG>
+__device__ __forceinline__ int segments_at(const RecArgs &a, int t0, int lane, uint32_t &heads, uint32_t &tails) {
+    const int t = t0 + lane;
+    int seg = 0;
+    bool head = false, tail = false;
+    if (lane < SEG && t < a.T) {
+        int lo = 0, hi = a.rows;   // the last seg with cu[seg] <= t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(a.cu + mid) <= t) lo = mid;
+            else hi = mid;
         }
-        if (a.last != nullptr) a.last[at] = h;
+        seg = lo;
+        head = __ldg(a.cu + seg) == t;
+        tail = __ldg(a.cu + seg + 1) == t + 1;
     }
+    heads = __ballot_sync(FULL_MASK, head);
+    tails = __ballot_sync(FULL_MASK, tail);
+    return seg;
 }
 
-template <typename TS>
-__global__ void __launch_bounds__(SEQ_THREADS) k_backward(const RecArgs a) {
-    const int u = blockIdx.x * SEQ_THREADS + threadIdx.x;
-    if (u >= a.d) return;
-    const float rate = a.params[u], b_a = a.params[a.d + u], b_i = a.params[2 * a.d + u];
-    for (int row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        int64_t t0, t1;
-        span_of(a, row, t0, t1);
-        const int64_t at = static_cast<int64_t>(row) * a.d + u;
-        float nu = a.g_last != nullptr ? a.g_last[at] : 0.f;
-        float g_rate = 0.f, g_ba = 0.f, g_bi = 0.f;
-        for (int64_t t = t1 - 1; t >= t0; --t) {
-            const TS *p = static_cast<const TS *>(a.P) + t * 3 * a.d + u;
-            const Gates g = gates_of(to_f32(p[0]), to_f32(p[a.d]), rate, b_a, b_i);
-            const float v = to_f32(p[2 * a.d]);
-            const float before = t > t0 ? to_f32(static_cast<const TS *>(a.H)[(t - 1) * a.d + u])
-                                        : a.state != nullptr ? a.state[at] : 0.f;
-            const float G = to_f32(static_cast<const TS *>(a.gH)[t * a.d + u]) + nu;
-            nu = g.a * G;
-            const float over = g.s > 0.f ? g.a * rcp_approx(g.s) : 0.f;
-            const float w = nu * (before - over * g.i * v);
-            const float wr = w * g.r;
-            const float ga = -rate * wr * g.omr, gv = G * g.s * g.i, gi = gv * v * g.omi;
-            TS *o = static_cast<TS *>(a.gP) + t * 3 * a.d + u;
-            o[0] = from_f32<TS>(ga);
-            o[a.d] = from_f32<TS>(gi);
-            o[2 * a.d] = from_f32<TS>(gv);
-            g_rate -= wr;
-            g_ba += ga;
-            g_bi += gi;
+// bounded wait for a tile's copies; after one that gave up the copies are seen through
+__device__ __forceinline__ bool tile_is_there(uint64_t *bar, uint32_t parity, const RecArgs &a) {
+    if (mbar_wait_bounded(bar, parity, a.wait_ns, a.error)) return true;
+    mbar_wait_bounded(bar, parity, SETTLE_NS, a.error);
+    return false;
+}
+
+struct Place { int col, b, u0, q, t0; };
+template <typename TS, bool REVERSE> __device__ __forceinline__ Place place_of(const RecArgs &a, int64_t tile) {
+    Place p;
+    p.q = static_cast<int>(tile / a.n_cols);
+    p.col = static_cast<int>(tile - static_cast<int64_t>(p.q) * a.n_cols);
+    p.b = p.col / a.n_ut;
+    p.u0 = (p.col - p.b * a.n_ut) * UNITS;
+    p.t0 = (REVERSE ? a.n_chunks - 1 - p.q : p.q) * steps_of<TS>();
+    return p;
+}
+
+// ---------------------------------------------------------------- forward
+constexpr int FORWARD_CTAS = 4;   // an SM
+
+template <typename TS, bool PACK>
+__global__ void __launch_bounds__(THREADS, FORWARD_CTAS)
+    k_forward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const RecArgs a) {
+    constexpr int SEG = seg_of<TS>(), L = steps_of<TS>(), PLANE = plane_of<TS>(), TERMS = sizeof(TS) == 2 ? 3 : 5;
+    extern __shared__ __align__(128) unsigned char dsmem[];   // two tiles
+    __shared__ Shared s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    TS *const tiles = reinterpret_cast<TS *>(dsmem);
+    auto start = [&](int64_t tile, int buf) {   // the copies of a tile
+        const Place p = place_of<TS, false>(a, tile);
+        mbar_arrive_expect_tx(&s.bar[buf], 3u * PLANE * sizeof(TS));
+#pragma unroll
+        for (int g = 0; g < 3; ++g)
+            tma_load_3d(tiles + (buf * 3 + g) * PLANE, &tmP, &s.bar[buf], g * a.d + p.u0, p.t0, p.b);
+    };
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (tid == 0) {
+        mbar_init(&s.bar[0], 1);
+        mbar_init(&s.bar[1], 1);
+        fence_mbar_init();
+        s.tile[0] = atomicAdd(a.ticket, 1u);
+        if (s.tile[0] < a.n_tiles) start(s.tile[0], 0);
+    }
+    __syncthreads();
+    for (int it = 0;; ++it) {
+        const int buf = it & 1;
+        const int64_t tile = s.tile[buf];
+        if (tile >= a.n_tiles) break;
+        const Place p = place_of<TS, false>(a, tile);
+        const int u = p.u0 + 2 * lane, r0 = warp * SEG;
+        const bool uok = u < a.d;
+        const UnitWeights w = weights_of(a.params, a.d, u, uok);
+        TS *const mine = tiles + buf * 3 * PLANE + r0 * UNITS + 2 * lane;
+        uint32_t heads = 0, tails = 0;
+        int seg = p.b;
+        if (PACK) seg = segments_at<SEG>(a, p.t0 + r0, lane, heads, tails);
+        else if (a.T - 1 - p.t0 - r0 >= 0 && a.T - 1 - p.t0 - r0 < SEG) tails = 1u << (a.T - 1 - p.t0 - r0);
+        float2 first = splat2(0.f);   // what the first group starts from
+        if (!PACK && p.q < a.group && a.state != nullptr) first = two_of(a.state + static_cast<int64_t>(p.b) * a.d + u, uok);
+        // state before a segment's first step
+        auto state_at = [&](int r) {
+            const int sg = __shfl_sync(FULL_MASK, seg, r);
+            return two_of(a.state + static_cast<int64_t>(sg) * a.d + u, uok && a.state != nullptr);
+        };
+        int64_t next = 0;
+        if (tid == 0) next = atomicAdd(a.ticket, 1u);
+        const bool ok = tile_is_there(&s.bar[buf], (it >> 1) & 1, a);
+        float2 da[SEG], du[SEG];
+        Map2 m{splat2(1.f), splat2(0.f)};
+        auto compose = [&](auto special) {
+#pragma unroll
+            for (int i = 0; i < SEG; ++i) {
+                forward_gates<TERMS>(load2(mine + i * UNITS), load2(mine + PLANE + i * UNITS), load2(mine + 2 * PLANE + i * UNITS),
+                                     w, da[i], du[i]);
+                if (decltype(special)::value && (heads >> i & 1u)) {
+                    m.B = fma2(da[i], state_at(i), du[i]);
+                    m.A = splat2(-0.f);
+                } else {
+                    m.B = fma2(da[i], m.B, du[i]);
+                    m.A = mul2(da[i], m.A);
+                }
+            }
+        };
+        if (PACK && heads != 0) compose(std::true_type{});
+        else compose(std::false_type{});
+        if (tid == 0) {
+            s.tile[buf ^ 1] = next;
+            if (next < a.n_tiles) {
+                bulk_wait_read<0>();   // the other tile's result has left it
+                start(next, buf ^ 1);
+            }
         }
-        if (a.g_state != nullptr) a.g_state[at] = nu;
-        float *part = a.part + static_cast<int64_t>(row) * 3 * a.d + u;
-        part[0] = g_rate;
-        part[a.d] = g_ba;
-        part[2 * a.d] = g_bi;
+        float2 h = carry_into<PACK>(a, s, p.col, p.q, warp, lane, m, first, ok);
+        auto write = [&](auto special) {
+#pragma unroll
+            for (int i = 0; i < SEG; ++i) {
+                if (decltype(special)::value && PACK && (heads >> i & 1u)) h = state_at(i);
+                h = fma2(da[i], h, du[i]);
+                store2(mine + i * UNITS, h);
+                if (decltype(special)::value && (tails >> i & 1u) && a.last != nullptr) {
+                    const int sg = PACK ? __shfl_sync(FULL_MASK, seg, i) : p.b;
+                    if (uok) *reinterpret_cast<float2 *>(a.last + static_cast<int64_t>(sg) * a.d + u) = h;
+                }
+            }
+        };
+        if ((heads | tails) != 0) write(std::true_type{});
+        else write(std::false_type{});
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            tma_store_3d(&tmH, tiles + buf * 3 * PLANE, p.u0, p.t0, p.b);
+            bulk_commit();
+        }
+    }
+    if (tid == 0) bulk_wait_read<0>();   // the tiles outlive the stores' reads
+}
+
+// ---------------------------------------------------------------- backward
+constexpr int BACKWARD_CTAS = 4;   // an SM
+
+// shared -> global store of a block of dL/dP through the 4-D map (d, block, T, B)
+__device__ __forceinline__ void store_block(const CUtensorMap *map, const void *src, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+template <typename TS, bool PACK>
+__global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
+    k_backward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH,
+               const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmGP, const RecArgs a) {
+    constexpr int SEG = seg_of<TS>(), L = steps_of<TS>(), PLANE = plane_of<TS>(), TERMS = sizeof(TS) == 2 ? 3 : 5;
+    extern __shared__ __align__(128) unsigned char dsmem[];   // one tile: P, H, gH
+    __shared__ Shared s;
+    __shared__ float2 sums[3][NW][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    TS *const Ps = reinterpret_cast<TS *>(dsmem), *const Hs = Ps + 3 * PLANE, *const Gs = Hs + PLANE;
+    auto start = [&](int64_t tile) {
+        const Place p = place_of<TS, true>(a, tile);
+        mbar_arrive_expect_tx(&s.bar[0], 5u * PLANE * sizeof(TS));
+#pragma unroll
+        for (int g = 0; g < 3; ++g) tma_load_3d(Ps + g * PLANE, &tmP, &s.bar[0], g * a.d + p.u0, p.t0, p.b);
+        tma_load_3d(Hs, &tmH, &s.bar[0], p.u0, p.t0, p.b);
+        tma_load_3d(Gs, &tmG, &s.bar[0], p.u0, p.t0, p.b);
+    };
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (tid == 0) {
+        mbar_init(&s.bar[0], 1);
+        fence_mbar_init();
+        s.tile[0] = atomicAdd(a.ticket, 1u);
+        if (s.tile[0] < a.n_tiles) start(s.tile[0]);
+    }
+    __syncthreads();
+    for (int it = 0;; ++it) {
+        const int64_t tile = s.tile[it & 1];
+        if (tile >= a.n_tiles) break;
+        const Place p = place_of<TS, true>(a, tile);
+        const int u = p.u0 + 2 * lane, r0 = warp * SEG;
+        const bool uok = u < a.d;
+        const UnitWeights w = weights_of(a.params, a.d, u, uok);
+        TS *const mine = Ps + r0 * UNITS + 2 * lane;
+        const TS *const h_mine = Hs + r0 * UNITS + 2 * lane, *const g_mine = Gs + r0 * UNITS + 2 * lane;
+        uint32_t heads = 0, tails = 0;
+        int seg = p.b;
+        if (PACK) {
+            seg = segments_at<SEG>(a, p.t0 + r0, lane, heads, tails);
+        } else {
+            const int end = a.T - 1 - p.t0 - r0;
+            if (end >= 0 && end < SEG) tails = 1u << end;
+            if (p.t0 + r0 == 0) heads = 1u;
+        }
+        auto row_of = [&](int r) { return static_cast<int64_t>(PACK ? __shfl_sync(FULL_MASK, seg, r) : p.b) * a.d + u; };
+        float2 before0 = splat2(0.f);   // H at the step before this warp's first
+        if (warp == 0 && p.t0 > 0 && uok)
+            before0 = load2(static_cast<const TS *>(a.H) + (static_cast<int64_t>(p.b) * a.T + p.t0 - 1) * a.d + u);
+        int64_t next = 0;
+        if (tid == 0) next = atomicAdd(a.ticket, 1u);
+        const bool ok = tile_is_there(&s.bar[0], it & 1, a);
+        if (warp > 0) before0 = load2(h_mine - UNITS);
+        // nu_{t+1} -> nu_t = a_t (gH_t + nu_{t+1}), the last step first; a sequence's last
+        // step starts from the gradient of its last state
+        float2 da[SEG];
+        Map2 m{splat2(1.f), splat2(0.f)};
+        auto compose = [&](auto special) {
+#pragma unroll
+            for (int i = SEG - 1; i >= 0; --i) {
+                da[i] = decay_of(load2(mine + i * UNITS), w);
+                if (decltype(special)::value && (tails >> i & 1u)) {
+                    const float2 g = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
+                    m.B = g;
+                    m.A = splat2(-0.f);
+                }
+                m.B = mul2(da[i], add2(load2(g_mine + i * UNITS), m.B));
+                m.A = mul2(da[i], m.A);
+            }
+        };
+        if (tails != 0) compose(std::true_type{});
+        else compose(std::false_type{});
+        float2 nu = carry_into<PACK>(a, s, p.col, p.q, NW - 1 - warp, lane, m, splat2(0.f), ok);
+        float2 g_rate = splat2(0.f), g_ba = splat2(0.f), g_bi = splat2(0.f);
+        auto write = [&](auto special) {
+#pragma unroll
+            for (int i = SEG - 1; i >= 0; --i) {
+                constexpr bool SPECIAL = decltype(special)::value;
+                if (SPECIAL && (tails >> i & 1u)) nu = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
+                const float2 one = splat2(1.f);
+                const float2 ea = falling(load2(mine + i * UNITS), w.nb_a), ei = falling(load2(mine + PLANE + i * UNITS), w.nb_i);
+                const float2 v = load2(mine + 2 * PLANE + i * UNITS);
+                const float2 xa = add2(ea, one), xi = add2(ei, one);
+                const float2 inv = rcp_2(mul2(xa, xi));
+                const float2 r = mul2(inv, xi), gi = mul2(inv, xa);
+                const float2 q = one_less_square<TERMS>(da[i], mul2(add2(w.rate, w.rate), r));
+                const float2 rs = make_float2(q.x > 0.f ? rsqrt_approx(q.x) : 0.f, q.y > 0.f ? rsqrt_approx(q.y) : 0.f);
+                const float2 sq = mul2(q, rs), over = mul2(da[i], rs);
+                float2 before = i > 0 ? load2(h_mine + (i - 1) * UNITS) : before0;
+                if (SPECIAL && (heads >> i & 1u)) before = two_of(a.state + row_of(i), uok && a.state != nullptr);
+                const float2 G = add2(load2(g_mine + i * UNITS), nu);
+                nu = mul2(da[i], G);
+                if (SPECIAL && (heads >> i & 1u) && a.g_state != nullptr) {
+                    const int64_t at = row_of(i);
+                    if (uok) *reinterpret_cast<float2 *>(a.g_state + at) = nu;
+                }
+                const float2 iv = mul2(gi, v);
+                // -w r; w = nu (before - over i v)
+                const float2 wr = mul2(mul2(nu, r), fma2(over, iv, mul2(before, splat2(-1.f))));
+                const float2 ga = mul2(mul2(wr, w.rate), mul2(ea, r));      // 1 - r = ea r
+                const float2 Gs_ = mul2(G, sq);
+                const float2 gv = mul2(Gs_, gi), gp = mul2(mul2(Gs_, iv), mul2(ei, gi));
+                g_rate = add2(g_rate, wr);
+                g_ba = add2(g_ba, ga);
+                g_bi = add2(g_bi, gp);
+                store2(mine + i * UNITS, ga);
+                store2(mine + PLANE + i * UNITS, gp);
+                store2(mine + 2 * PLANE + i * UNITS, gv);
+            }
+        };
+        if ((heads | tails) != 0) write(std::true_type{});
+        else write(std::false_type{});
+        sums[0][warp][lane] = g_rate;
+        sums[1][warp][lane] = g_ba;
+        sums[2][warp][lane] = g_bi;
+        if (tid == 0) s.tile[(it + 1) & 1] = next;
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+#pragma unroll
+            for (int g = 0; g < 3; ++g) store_block(&tmGP, Ps + g * PLANE, p.u0, g, p.t0, p.b);
+            bulk_commit();
+            bulk_wait_read<0>();
+            if (next < a.n_tiles) start(next);
+        }
+        if (warp < 3) {
+            float2 t = sums[warp][0][lane];
+#pragma unroll
+            for (int k = 1; k < NW; ++k) t = add2(t, sums[warp][k][lane]);
+            float *to = a.part + ((static_cast<int64_t>(p.col) * a.n_chunks + p.q) * 3 + warp) * UNITS + 2 * lane;
+            *reinterpret_cast<float2 *>(to) = t;
+        }
+        // (the next tile's two barriers lie between these reads and its sums)
     }
 }
 
-// sums of the parameters' gradients over the rows, in order
-__global__ void __launch_bounds__(128) k_join(const float *part, int rows, int n, float *out) {
-    const int j = blockIdx.x * 128 + threadIdx.x;
-    if (j >= n) return;
-    float s = 0.f;
-    for (int r = 0; r < rows; ++r) s += part[static_cast<int64_t>(r) * n + j];
-    out[j] = s;
+// Sums of the parameters' gradients over rows and chunks, in order: a CTA takes a unit
+// tile and one of JOIN_SLICES shares of (row, chunk); the CTA that ends last, by a
+// counter, adds the shares.
+constexpr int JOIN_SLICES = 32, JOIN_THREADS = 3 * UNITS;
+
+__global__ void __launch_bounds__(JOIN_THREADS)
+    k_join(const float *part, int rows, int n_ut, int n_chunks, int d, float *share, uint32_t *count, float *gparams) {
+    __shared__ bool is_last;
+    dependents_may_launch();
+    wait_for_prerequisites();
+    const int ut = blockIdx.x, slice = blockIdx.y, j = threadIdx.x;
+    const int64_t all = static_cast<int64_t>(rows) * n_chunks;
+    const int64_t k0 = all * slice / JOIN_SLICES, k1 = all * (slice + 1) / JOIN_SLICES;
+    auto at = [&](int64_t k) {
+        const int64_t b = k / n_chunks, q = k - b * n_chunks;
+        return part[((b * n_ut + ut) * n_chunks + q) * JOIN_THREADS + j];
+    };
+    float t[4] = {};
+    int64_t k = k0;
+    for (; k + 4 <= k1; k += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] += at(k + e);
+    for (; k < k1; ++k) t[0] += at(k);
+    share[(static_cast<int64_t>(ut) * JOIN_SLICES + slice) * JOIN_THREADS + j] = (t[0] + t[1]) + (t[2] + t[3]);
+    __threadfence();
+    __syncthreads();
+    if (j == 0) is_last = atomicAdd(count + ut, 1u) == JOIN_SLICES - 1;
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    float sum = 0.f;
+#pragma unroll 8
+    for (int e = 0; e < JOIN_SLICES; ++e)
+        sum += __ldcg(share + (static_cast<int64_t>(ut) * JOIN_SLICES + e) * JOIN_THREADS + j);
+    const int u = ut * UNITS + j % UNITS;
+    if (u < d) gparams[static_cast<int64_t>(j / UNITS) * d + u] = sum;
 }
 
+// Clears a call's counters and slots.  Sequences without a step hand their state (or its
+// gradient) on; with no steps at all the parameters' gradients are zeros.
+__global__ void __launch_bounds__(256)
+    k_prepare(uint4 *clear, int64_t n16, const int32_t *cu, int rows, int T, int d, const float *in, float *out, float *zeros) {
+    dependents_may_launch();
+    wait_for_prerequisites();
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t i = i0; i < n16; i += step) clear[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (out != nullptr && (cu != nullptr || T == 0))
+        for (int64_t i = i0; i < static_cast<int64_t>(rows) * d; i += step) {
+            const int64_t row = i / d;
+            if (cu == nullptr || __ldg(cu + row) >= __ldg(cu + row + 1)) out[i] = in != nullptr ? in[i] : 0.f;
+        }
+    if (zeros != nullptr)
+        for (int64_t i = i0; i < 3 * static_cast<int64_t>(d); i += step) zeros[i] = 0.f;
+}
+
+// ---------------------------------------------------------------- one step
 template <typename TS>
 __global__ void __launch_bounds__(256)
-    k_step(const TS *P, const float *params, const float *state, int64_t n, int d, TS *h_out, float *last) {
+    k_step(const TS *P, const float *params, const float *state, int64_t pairs, int d, TS *h_out, float *last) {
+    dependents_may_launch();
+    wait_for_prerequisites();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= n) return;
-    const int64_t slot = i / d;
-    const int u = static_cast<int>(i - slot * d);
+    if (i >= pairs) return;
+    const int64_t slot = i / (d / 2);
+    const int u = 2 * static_cast<int>(i - slot * (d / 2));
     const TS *p = P + slot * 3 * d + u;
-    const Gates g = gates_of(to_f32(p[0]), to_f32(p[d]), params[u], params[d + u], params[2 * d + u]);
-    const float h = fmaf(g.a, state != nullptr ? state[i] : 0.f, g.s * g.i * to_f32(p[2 * d]));
-    h_out[i] = from_f32<TS>(h);
-    last[i] = h;
+    const float2 pa = load2(p), pi = load2(p + d), v = load2(p + 2 * d);
+    const float2 before = two_of(state + slot * d + u, state != nullptr);
+    float2 a, x;
+    forward_gates<5>(pa, pi, v, weights_of(params, d, u, true), a, x);
+    const float2 h = fma2(a, before, x);
+    store2(h_out + slot * d + u, h);
+    *reinterpret_cast<float2 *>(last + slot * d + u) = h;
 }
 
+// ---------------------------------------------------------------- host side
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+struct Layout {
+    int64_t n_ut, n_cols, n_chunks, groups, group, n_tiles;
+    int64_t slots, ends, cleared, part, share, total;
+};
+
+// Chunks of a look-back group.  A chain has a hop a group, about 1.5 us, and a chunk
+// reads half a group's maps on average: many columns have few chunks of each under way
+// and short chains, and take small groups.
+int64_t group_of(int64_t n_cols, int64_t n_chunks) {
+    (void)n_chunks;
+    return n_cols >= 64 ? 8 : 32;
+}
+
+Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, bool backward) {
+    Layout y{};
+    const int64_t steps = dtype == NRNN_BF16 ? steps_of<__nv_bfloat16>() : steps_of<float>();
+    y.n_ut = ceil_div(d, UNITS);
+    y.n_cols = B * y.n_ut;
+    y.n_chunks = ceil_div(T, steps);
+    y.group = group_of(y.n_cols, y.n_chunks);
+    y.groups = ceil_div(y.n_chunks, y.group);
+    y.n_tiles = y.n_cols * y.n_chunks;
+    int64_t at = 256 + up256(4 * y.n_ut);   // ticket, error; the join's counters
+    y.slots = at;
+    at += 8 * UNITS * y.n_tiles;
+    y.ends = at;
+    at += 8 * UNITS * y.n_cols * y.groups;
+    y.cleared = at;
+    y.part = at;
+    if (backward) {
+        at += up256(4 * 3 * UNITS * y.n_tiles);
+        y.share = at;
+        at += up256(4 * 3 * UNITS * JOIN_SLICES * y.n_ut);
+    }
+    y.total = at;
+    return y;
+}
 
 int check(const void *P, int dtype, const float *params, int64_t B, int64_t T, int64_t d,
           const int32_t *cu, int64_t S) {
@@ -172,7 +684,8 @@ int check(const void *P, int dtype, const float *params, int64_t B, int64_t T, i
     if (B < 0 || T < 0 || d <= 0 || S < 0) return NRNN_ERR_INVALID_ARG;
     if (B > INT32_MAX || T > INT32_MAX || d > (1 << 24) || S > INT32_MAX - 1 || d % 8 != 0)
         return NRNN_ERR_UNSUPPORTED;
-    if (B > 0 && T > (INT64_MAX >> 8) / (B * d)) return NRNN_ERR_UNSUPPORTED;
+    // tiles are counted in 32 bits
+    if (B > 0 && T > 0 && ceil_div(T, 32) > INT32_MAX / (B * ceil_div(d, UNITS))) return NRNN_ERR_UNSUPPORTED;
     if (cu != nullptr && (B != 1 || S < 1)) return NRNN_ERR_CU_SEQLENS;
     if (params == nullptr || !aligned16(params)) return NRNN_ERR_INVALID_ARG;
     if (B * T > 0 && (P == nullptr || !aligned16(P))) return NRNN_ERR_INVALID_ARG;
@@ -180,9 +693,79 @@ int check(const void *P, int dtype, const float *params, int64_t B, int64_t T, i
 }
 
 bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
-    if (a == nullptr || b == nullptr) return false;
+    if (a == nullptr || b == nullptr || a_bytes == 0 || b_bytes == 0) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + b_bytes && y < x + a_bytes;
+}
+
+bool usable(const void *ws, size_t have, int64_t need) {
+    return ws != nullptr && reinterpret_cast<uintptr_t>(ws) % 256 == 0 && have >= static_cast<size_t>(need);
+}
+
+RecArgs args_of(const Layout &y, const float *params, const float *state, const int32_t *cu, int64_t rows, int64_t T,
+                int64_t d, unsigned char *ws) {
+    RecArgs a{};
+    a.params = params; a.state = state; a.cu = cu;
+    a.rows = static_cast<int>(rows); a.T = static_cast<int>(T); a.d = static_cast<int>(d);
+    a.n_ut = static_cast<int>(y.n_ut); a.n_cols = static_cast<int>(y.n_cols); a.n_chunks = static_cast<int>(y.n_chunks);
+    a.group = static_cast<int>(y.group);
+    a.n_tiles = y.n_tiles;
+    a.ticket = reinterpret_cast<uint32_t *>(ws);
+    a.error = a.ticket + 1;
+    a.slots = reinterpret_cast<unsigned long long *>(ws + y.slots);
+    a.ends = reinterpret_cast<unsigned long long *>(ws + y.ends);
+    a.part = reinterpret_cast<float *>(ws + y.part);
+    a.wait_ns = wait_limit_ns();
+    return a;
+}
+
+cudaError_t prepare(const Layout &y, const RecArgs &a, unsigned char *ws, const float *in, float *out, float *zeros,
+                    cudaStream_t s) {
+    const int64_t n16 = y.n_tiles > 0 ? y.cleared / 16 : 0;
+    const int64_t most = n16 > static_cast<int64_t>(a.rows) * a.d ? n16 : static_cast<int64_t>(a.rows) * a.d;
+    const int64_t b = ceil_div(most, 256);
+    return launch_dependent(k_prepare, static_cast<unsigned>(b < 1 ? 1 : b < 1216 ? b : 1216), 256, 0, s,
+                            reinterpret_cast<uint4 *>(ws), n16, a.cu, a.rows, a.T, a.d, in, out, zeros);
+}
+
+unsigned ctas_for(int64_t tiles, int per_sm) {
+    const int64_t most = 152ll * per_sm;
+    return static_cast<unsigned>(tiles < most ? tiles : most);
+}
+
+// 3-D map over (B, T, width) with a box of one tile's block
+template <typename TS> bool map_tile(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_t T, int64_t B) {
+    return make_map_steps(m, base, dtype, width, T, B, UNITS, steps_of<TS>());
+}
+
+template <typename TS, bool PACK>
+cudaError_t launch_forward(const Layout &y, const RecArgs &a, int dtype, const void *P, void *H, int64_t B, cudaStream_t s) {
+    static std::atomic<unsigned long long> configured{0};
+    constexpr size_t smem = 2ull * 3 * plane_of<TS>() * sizeof(TS);
+    cudaError_t e = once_per_device(configured, [](int) {
+        return cudaFuncSetAttribute(k_forward<TS, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    });
+    if (e != cudaSuccess) return e;
+    CUtensorMap tmP, tmH;
+    if (!map_tile<TS>(&tmP, P, dtype, 3 * a.d, a.T, B) || !map_tile<TS>(&tmH, H, dtype, a.d, a.T, B)) return cudaErrorUnknown;
+    return launch_dependent(k_forward<TS, PACK>, ctas_for(y.n_tiles, FORWARD_CTAS), THREADS, smem, s, tmP, tmH, a);
+}
+
+template <typename TS, bool PACK>
+cudaError_t launch_backward(const Layout &y, const RecArgs &a, int dtype, const void *P, const void *H, const void *gH,
+                            void *gP, int64_t B, cudaStream_t s) {
+    static std::atomic<unsigned long long> configured{0};
+    constexpr size_t smem = 5ull * plane_of<TS>() * sizeof(TS);
+    cudaError_t e = once_per_device(configured, [](int) {
+        return cudaFuncSetAttribute(k_backward<TS, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    });
+    if (e != cudaSuccess) return e;
+    CUtensorMap tmP, tmH, tmG, tmGP;
+    if (!map_tile<TS>(&tmP, P, dtype, 3 * a.d, a.T, B) || !map_tile<TS>(&tmH, H, dtype, a.d, a.T, B) ||
+        !map_tile<TS>(&tmG, gH, dtype, a.d, a.T, B) ||
+        !make_map_gate_steps(&tmGP, gP, dtype, a.d, a.T, B, UNITS, steps_of<TS>()))
+        return cudaErrorUnknown;
+    return launch_dependent(k_backward<TS, PACK>, ctas_for(y.n_tiles, BACKWARD_CTAS), THREADS, smem, s, tmP, tmH, tmG, tmGP, a);
 }
 
 }  // namespace
@@ -194,11 +777,10 @@ extern "C" {
 
 size_t nrnn_linear_recurrence_workspace_bytes(int64_t B, int64_t T, int64_t d_h, int dtype,
                                               int64_t num_segments, int backward) {
-    if (B < 0 || T < 0 || d_h <= 0 || d_h > (1 << 24) || num_segments < 0 ||
-        (dtype != NRNN_F32 && dtype != NRNN_BF16))
+    if (num_segments < 0 || (dtype != NRNN_F32 && dtype != NRNN_BF16) || B < 0 || T < 0 || d_h <= 0 || B > INT32_MAX ||
+        T > INT32_MAX || d_h > (1 << 24) || (B > 0 && T > 0 && ceil_div(T, 32) > INT32_MAX / (B * ceil_div(d_h, UNITS))))
         return 0;
-    const int64_t rows = num_segments > 0 ? num_segments : B;
-    return 256 + (backward ? sizeof(float) * 3 * d_h * rows : 0);
+    return static_cast<size_t>(layout_of(B, T, d_h, dtype, backward != 0).total);
 }
 
 int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *params, int64_t B,
@@ -211,21 +793,25 @@ int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *p
     const int64_t rows = cu_seqlens != nullptr ? num_segments : B;
     if ((n > 0 && (H == nullptr || !aligned16(H))) || !aligned16(state) || !aligned16(last) ||
         overlap(preact, 3 * n * es, H, n * es) || overlap(state, rows * d_h * 4, H, n * es) ||
-        (state != last && overlap(state, rows * d_h * 4, last, rows * d_h * 4)))
+        overlap(state, rows * d_h * 4, last, rows * d_h * 4) || overlap(preact, 3 * n * es, last, rows * d_h * 4) ||
+        overlap(H, n * es, last, rows * d_h * 4))
         return NRNN_ERR_INVALID_ARG;
-    if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
-        ws_bytes < nrnn_linear_recurrence_workspace_bytes(B, T, d_h, dtype, cu_seqlens ? num_segments : 0, 0))
-        return NRNN_ERR_WORKSPACE;
+    const Layout y = layout_of(B, T, d_h, dtype, false);
+    if (!usable(workspace, ws_bytes, y.total)) return NRNN_ERR_WORKSPACE;
     if (rows == 0) return NRNN_OK;
-    RecArgs a{};
-    a.P = preact; a.params = params; a.state = state; a.cu = cu_seqlens;
-    a.rows = static_cast<int>(rows); a.T = T; a.d = static_cast<int>(d_h);
-    a.H_out = H; a.last = last;
-    const dim3 grid(static_cast<unsigned>((d_h + SEQ_THREADS - 1) / SEQ_THREADS), static_cast<unsigned>(rows < 65535 ? rows : 65535));
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == NRNN_BF16) k_forward<__nv_bfloat16><<<grid, SEQ_THREADS, 0, s>>>(a);
-    else k_forward<float><<<grid, SEQ_THREADS, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    RecArgs a = args_of(y, params, state, cu_seqlens, rows, T, d_h, ws);
+    a.last = last;
+    cudaError_t e = prepare(y, a, ws, state, last, nullptr, s);
+    if (e == cudaSuccess && n > 0) {
+        const bool pack = cu_seqlens != nullptr;
+        e = dtype == NRNN_BF16 ? (pack ? launch_forward<__nv_bfloat16, true>(y, a, dtype, preact, H, B, s)
+                                       : launch_forward<__nv_bfloat16, false>(y, a, dtype, preact, H, B, s))
+                               : (pack ? launch_forward<float, true>(y, a, dtype, preact, H, B, s)
+                                       : launch_forward<float, false>(y, a, dtype, preact, H, B, s));
+    }
+    return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *params, int64_t B,
@@ -236,29 +822,43 @@ int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *
     const int st = check(preact, dtype, params, B, T, d_h, cu_seqlens, num_segments);
     if (st != NRNN_OK) return st;
     const int64_t es = dtype == NRNN_BF16 ? 2 : 4, n = B * T * d_h;
-    const int64_t rows = cu_seqlens != nullptr ? num_segments : B;
+    const int64_t rows = cu_seqlens != nullptr ? num_segments : B, sb = rows * d_h * 4;
     if (gparams == nullptr || !aligned16(gparams) || !aligned16(state) || !aligned16(g_last) || !aligned16(g_state) ||
         (n > 0 && (H == nullptr || gH == nullptr || gP == nullptr || !aligned16(H) || !aligned16(gH) || !aligned16(gP))) ||
         overlap(preact, 3 * n * es, gP, 3 * n * es) || overlap(H, n * es, gP, 3 * n * es) ||
-        overlap(gH, n * es, gP, 3 * n * es))
+        overlap(gH, n * es, gP, 3 * n * es) || overlap(state, sb, g_state, sb) || overlap(g_last, sb, g_state, sb) ||
+        overlap(gP, 3 * n * es, g_state, sb))
         return NRNN_ERR_INVALID_ARG;
-    if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
-        ws_bytes < nrnn_linear_recurrence_workspace_bytes(B, T, d_h, dtype, cu_seqlens ? num_segments : 0, 1))
-        return NRNN_ERR_WORKSPACE;
+    const Layout y = layout_of(B, T, d_h, dtype, true);
+    if (!usable(workspace, ws_bytes, y.total)) return NRNN_ERR_WORKSPACE;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    RecArgs a{};
-    a.P = preact; a.params = params; a.state = state; a.cu = cu_seqlens;
-    a.rows = static_cast<int>(rows); a.T = T; a.d = static_cast<int>(d_h);
-    a.H = H; a.gH = gH; a.g_last = g_last; a.gP = gP; a.g_state = g_state;
-    a.part = static_cast<float *>(workspace);
-    if (rows > 0) {
-        const dim3 grid(static_cast<unsigned>((d_h + SEQ_THREADS - 1) / SEQ_THREADS), static_cast<unsigned>(rows < 65535 ? rows : 65535));
-        if (dtype == NRNN_BF16) k_backward<__nv_bfloat16><<<grid, SEQ_THREADS, 0, s>>>(a);
-        else k_backward<float><<<grid, SEQ_THREADS, 0, s>>>(a);
+    RecArgs a = args_of(y, params, state, cu_seqlens, rows, T, d_h, ws);
+    a.H = H;
+    a.g_last = g_last;
+    a.g_state = g_state;
+    cudaError_t e = prepare(y, a, ws, g_last, g_state, n > 0 ? nullptr : gparams, s);
+    if (e == cudaSuccess && n > 0) {
+        const bool pack = cu_seqlens != nullptr;
+        e = dtype == NRNN_BF16 ? (pack ? launch_backward<__nv_bfloat16, true>(y, a, dtype, preact, H, gH, gP, B, s)
+                                       : launch_backward<__nv_bfloat16, false>(y, a, dtype, preact, H, gH, gP, B, s))
+                               : (pack ? launch_backward<float, true>(y, a, dtype, preact, H, gH, gP, B, s)
+                                       : launch_backward<float, false>(y, a, dtype, preact, H, gH, gP, B, s));
+        if (e == cudaSuccess) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(y.n_ut), JOIN_SLICES);
+            cfg.blockDim = dim3(JOIN_THREADS);
+            cfg.stream = s;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, k_join, static_cast<const float *>(a.part), static_cast<int>(B), a.n_ut, a.n_chunks,
+                                   a.d, reinterpret_cast<float *>(ws + y.share), reinterpret_cast<uint32_t *>(ws + 256), gparams);
+        }
     }
-    const int m = static_cast<int>(3 * d_h);
-    k_join<<<(m + 127) / 128, 128, 0, s>>>(a.part, a.rows, m, gparams);
-    return cudaGetLastError() == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 int nrnn_linear_recurrence_step(const void *preact, int dtype, const float *params, int64_t slots,
@@ -274,15 +874,16 @@ int nrnn_linear_recurrence_step(const void *preact, int dtype, const float *para
         (state != state_out && overlap(state, 4 * n, state_out, 4 * n)))
         return NRNN_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t blocks = (n + 255) / 256;
+    const int64_t pairs = n / 2, blocks = ceil_div(pairs, 256);
     if (blocks > INT32_MAX) return NRNN_ERR_UNSUPPORTED;
-    if (dtype == NRNN_BF16)
-        k_step<<<static_cast<unsigned>(blocks), 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(preact), params, state, n,
-                                                             static_cast<int>(d_h), static_cast<__nv_bfloat16 *>(h), state_out);
-    else
-        k_step<<<static_cast<unsigned>(blocks), 256, 0, s>>>(static_cast<const float *>(preact), params, state, n,
-                                                             static_cast<int>(d_h), static_cast<float *>(h), state_out);
-    return cudaGetLastError() == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    const cudaError_t e =
+        dtype == NRNN_BF16
+            ? launch_dependent(k_step<__nv_bfloat16>, static_cast<unsigned>(blocks), 256, 0, s,
+                               static_cast<const __nv_bfloat16 *>(preact), params, state, pairs, static_cast<int>(d_h),
+                               static_cast<__nv_bfloat16 *>(h), state_out)
+            : launch_dependent(k_step<float>, static_cast<unsigned>(blocks), 256, 0, s, static_cast<const float *>(preact), params,
+                               state, pairs, static_cast<int>(d_h), static_cast<float *>(h), state_out);
+    return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -156,6 +156,13 @@ bool make_map_planes(CUtensorMap *m, const void *base, int64_t inner, int64_t ro
 bool make_map_pitched(CUtensorMap *m, const void *base, int64_t inner, int64_t pitch, int64_t rows,
                       int64_t planes, uint32_t box_inner, uint32_t box_rows);
 
+// 3-D map over a (B, T, width) row-major array with a (units x steps x 1) box, no swizzle
+bool make_map_steps(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_t T, int64_t B,
+                    uint32_t units, uint32_t steps);
+// 4-D map over a (B, T, 3 d) array seen as (d, block, T, B), box (units x 1 x steps x 1)
+bool make_map_gate_steps(CUtensorMap *m, const void *base, int dtype, int64_t d, int64_t T, int64_t B,
+                         uint32_t units, uint32_t steps);
+
 // byte offset of the error word in a Newton forward's workspace
 size_t newton_error_offset(int K);
 
