@@ -23,10 +23,11 @@
 // all columns' chunks before it (backward: from the end of time), and start the copies
 // of the next tile while they work on one.  A thread composes the maps h -> A h + B of
 // its steps, the warps' maps meet in shared memory, and the carry into the chunk comes
-// from a look-back whose grouping is fixed: chunks form groups of `group`; a chunk
-// publishes its map, folds the maps of its group's chunks before it, in order, and
-// starts them from the state at the end of the group before, which that group's last
-// chunk publishes.  So no result depends on timing, and a chain has one hop a group.
+// from a look-back whose grouping is fixed: chunks form groups of `group`, groups form
+// spans of `span`.  A chunk publishes its map, and a group's last chunk that of the group.
+// A chunk folds, in order, the maps of its span's groups and of its group's chunks before
+// it, and starts them from the state at the end of the span before, which that span's
+// last chunk publishes.  So no result depends on timing, and a chain has one hop a span.
 //
 // A sequence's first state (backward: the gradient of its last) cuts the scan: the map
 // of a step that begins a pack's segment is marked by the sign of its A (a decay is
@@ -59,14 +60,15 @@ struct RecArgs {
     int rows;                         // sequences: B or segments
     int T, d;
     int n_ut, n_cols, n_chunks;       // unit tiles; B n_ut; chunks of time
-    int group;                        // chunks of a look-back group
+    int group, span;                  // look-back: chunks of a group, groups of a span
     int64_t n_tiles;
     float *last;                      // forward: (rows, d) or null
     const float *g_last;              // backward: (rows, d) or null
     float *g_state;                   // backward: (rows, d) or null
     float *part;                      // backward: [n_cols][n_chunks][3][UNITS] sums of a tile
     unsigned long long *slots;        // [n_cols][n_chunks][UNITS] maps of chunks
-    unsigned long long *ends;         // [n_cols][groups][UNITS] states after a group
+    unsigned long long *maps;         // [n_cols][groups][UNITS] maps of groups
+    unsigned long long *ends;         // [n_cols][spans][UNITS] states after a span
     uint32_t *ticket;
     uint32_t *error;
     uint64_t wait_ns;
@@ -211,23 +213,27 @@ __device__ __forceinline__ Map2 await2(const unsigned long long *slot, ulonglong
 // What a CTA shares while it works on a tile
 struct Shared {
     float2 aggA[NW][32], aggB[NW][32];     // maps of the warps' steps, in the scan's order
-    float2 preA[NW][32], preB[NW][32];     // maps of runs of the group's chunks before
-    float2 end[32];                        // state after the group before
+    float2 preA[NW][32], preB[NW][32];     // maps of runs of groups (0, 1) and chunks (2, 3) before
+    float2 end[32];                        // state after the span before
     uint64_t bar[2];
     int64_t tile[2];
 };
 
 // The carry into this warp's steps.  q: the chunk in the scan's order (backward: from the
 // end of time); m: the map of this warp's steps; place: the warp in the scan's order;
-// first: the state that the first group starts from.  Called by all threads; two barriers.
+// first: the state that the first span starts from.  Called by all threads; two barriers.
 template <bool CUTS>
 __device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int col, int q, int place, int lane, const Map2 &m,
                                              float2 first, bool ok) {
+    const float2 nan = splat2(__int_as_float(0x7fffffff));
     s.aggA[place][lane] = m.A;
-    s.aggB[place][lane] = m.B;
-    const int before = q % a.group, g = q / a.group, groups = (a.n_chunks + a.group - 1) / a.group;
+    s.aggB[place][lane] = ok ? m.B : nan;   // (a tile whose copies gave up)
+    const int g = q / a.group, before = q - g * a.group, sp = g / a.span, gi = g - sp * a.span;
+    const int groups = (a.n_chunks + a.group - 1) / a.group, spans = (groups + a.span - 1) / a.span;
     unsigned long long *slot = a.slots + (static_cast<int64_t>(col) * a.n_chunks + q) * UNITS + 2 * lane;
-    unsigned long long *end = a.ends + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
+    unsigned long long *map = a.maps + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
+    unsigned long long *end = a.ends + (static_cast<int64_t>(col) * spans + sp) * UNITS + 2 * lane;
+    const bool closes = before + 1 == a.group, closes_span = closes && gi + 1 == a.span;
     __syncthreads();
     auto warps_map = [&](int w) { return Map2{s.aggA[w][lane], s.aggB[w][lane]}; };
     Map2 all{};
@@ -235,37 +241,47 @@ __device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int co
         all = warps_map(0);
 #pragma unroll
         for (int w = 1; w < NW; ++w) all = then<CUTS>(all, warps_map(w));
-        if (q + 1 < a.n_chunks && before + 1 < a.group) publish2(slot, all);
+        if (!closes) publish2(slot, all);
     }
-    // a run of the group's chunks before this one: 0 .. before - 1
-    const int k0 = before * place / NW, k1 = before * (place + 1) / NW;
-    if (place == NW - 1) {   // and the state after the group before
-        float2 h = first;
-        if (g > 0) h = await2(end - UNITS, peek2(end - UNITS), a).B;
-        s.end[lane] = h;
-    }
+    // maps before: the first two warps take halves of the span's groups, the others of
+    // the group's chunks
+    const unsigned long long *const list = place < 2 ? map - static_cast<int64_t>(gi) * UNITS : slot - static_cast<int64_t>(before) * UNITS;
+    const int n = place < 2 ? gi : before, k0 = n * (place & 1) / 2, k1 = n * ((place & 1) + 1) / 2;
     Map2 run{splat2(1.f), splat2(0.f)};
     for (int k = k0; k < k1; k += 4) {
         ulonglong2 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (k + j < k1) v[j] = peek2(slot - static_cast<int64_t>(before - k - j) * UNITS);
+            if (k + j < k1) v[j] = peek2(list + static_cast<int64_t>(k + j) * UNITS);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (k + j < k1) {
-                const Map2 x = await2(slot - static_cast<int64_t>(before - k - j) * UNITS, v[j], a);
+                const Map2 x = await2(list + static_cast<int64_t>(k + j) * UNITS, v[j], a);
                 run = k + j == k0 ? x : then<CUTS>(run, x);
             }
     }
     s.preA[place][lane] = run.A;
     s.preB[place][lane] = run.B;
+    if (closes && gi + 1 < a.span) {   // the group's map waits for nothing but its chunks'
+        __syncwarp();
+        if (place != 1) asm volatile("bar.sync 1, 96;" ::: "memory");   // three of the warps
+        if (place == 0) {
+            Map2 whole = then<CUTS>(Map2{s.preA[2][lane], s.preB[2][lane]}, Map2{s.preA[3][lane], s.preB[3][lane]});
+            publish2(map, then<CUTS>(whole, all));
+        }
+    }
+    if (place == 1) {
+        float2 h = first;
+        if (sp > 0) h = await2(end - UNITS, peek2(end - UNITS), a).B;
+        s.end[lane] = h;
+    }
     __syncthreads();
     float2 h = s.end[lane];
-    if (before > 0)
+    if (gi + before > 0)
 #pragma unroll
         for (int w = 0; w < NW; ++w) h = apply<CUTS>(Map2{s.preA[w][lane], s.preB[w][lane]}, h);
-    if (!ok) h = splat2(__int_as_float(0x7fffffff));
-    if (place == 0 && before + 1 == a.group && q + 1 < a.n_chunks) publish2(end, Map2{splat2(0.f), apply<CUTS>(all, h)});
+    if (!ok) h = nan;
+    if (place == 0 && closes_span) publish2(end, Map2{splat2(0.f), apply<CUTS>(all, h)});
     for (int w = 0; w < place; ++w) h = apply<CUTS>(warps_map(w), h);
     return h;
 }
@@ -352,8 +368,8 @@ __global__ void __launch_bounds__(THREADS, FORWARD_CTAS)
         int seg = p.b;
         if (PACK) seg = segments_at<SEG>(a, p.t0 + r0, lane, heads, tails);
         else if (a.T - 1 - p.t0 - r0 >= 0 && a.T - 1 - p.t0 - r0 < SEG) tails = 1u << (a.T - 1 - p.t0 - r0);
-        float2 first = splat2(0.f);   // what the first group starts from
-        if (!PACK && p.q < a.group && a.state != nullptr) first = two_of(a.state + static_cast<int64_t>(p.b) * a.d + u, uok);
+        float2 first = splat2(0.f);   // what the first span starts from
+        if (!PACK && p.q < a.group * a.span && a.state != nullptr) first = two_of(a.state + static_cast<int64_t>(p.b) * a.d + u, uok);
         // state before a segment's first step
         auto state_at = [&](int r) {
             const int sg = __shfl_sync(FULL_MASK, seg, r);
@@ -641,16 +657,16 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-    int64_t n_ut, n_cols, n_chunks, groups, group, n_tiles;
-    int64_t slots, ends, cleared, part, share, total;
+    int64_t n_ut, n_cols, n_chunks, group, span, n_tiles;
+    int64_t slots, maps, ends, cleared, part, share, total;
 };
 
-// Chunks of a look-back group.  A chain has a hop a group, about 1.5 us, and a chunk
-// reads half a group's maps on average: many columns have few chunks of each under way
-// and short chains, and take small groups.
-int64_t group_of(int64_t n_cols, int64_t n_chunks) {
-    (void)n_chunks;
-    return n_cols >= 64 ? 8 : 32;
+// Chunks of a look-back group and groups of a span.  A chain has a hop a span, 2 to 3 us,
+// and a chunk reads half a group's and half a span's maps on average.  Many columns have
+// few chunks of each under way and short chains: small groups, spans of one.
+void grouping(int64_t n_cols, int64_t &group, int64_t &span) {
+    group = n_cols >= 64 ? 8 : 16;
+    span = n_cols >= 64 ? 1 : 16;
 }
 
 Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, bool backward) {
@@ -659,14 +675,16 @@ Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, bool backward) {
     y.n_ut = ceil_div(d, UNITS);
     y.n_cols = B * y.n_ut;
     y.n_chunks = ceil_div(T, steps);
-    y.group = group_of(y.n_cols, y.n_chunks);
-    y.groups = ceil_div(y.n_chunks, y.group);
+    grouping(y.n_cols, y.group, y.span);
+    const int64_t groups = ceil_div(y.n_chunks, y.group);
     y.n_tiles = y.n_cols * y.n_chunks;
     int64_t at = 256 + up256(4 * y.n_ut);   // ticket, error; the join's counters
     y.slots = at;
     at += 8 * UNITS * y.n_tiles;
+    y.maps = at;
+    at += y.span > 1 ? 8 * UNITS * y.n_cols * groups : 0;
     y.ends = at;
-    at += 8 * UNITS * y.n_cols * y.groups;
+    at += 8 * UNITS * y.n_cols * ceil_div(groups, y.span);
     y.cleared = at;
     y.part = at;
     if (backward) {
@@ -709,10 +727,12 @@ RecArgs args_of(const Layout &y, const float *params, const float *state, const 
     a.rows = static_cast<int>(rows); a.T = static_cast<int>(T); a.d = static_cast<int>(d);
     a.n_ut = static_cast<int>(y.n_ut); a.n_cols = static_cast<int>(y.n_cols); a.n_chunks = static_cast<int>(y.n_chunks);
     a.group = static_cast<int>(y.group);
+    a.span = static_cast<int>(y.span);
     a.n_tiles = y.n_tiles;
     a.ticket = reinterpret_cast<uint32_t *>(ws);
     a.error = a.ticket + 1;
     a.slots = reinterpret_cast<unsigned long long *>(ws + y.slots);
+    a.maps = reinterpret_cast<unsigned long long *>(ws + y.maps);
     a.ends = reinterpret_cast<unsigned long long *>(ws + y.ends);
     a.part = reinterpret_cast<float *>(ws + y.part);
     a.wait_ns = wait_limit_ns();
