@@ -49,9 +49,16 @@ namespace {
 constexpr int UNITS = 64, NW = 4, THREADS = NW * 32;
 constexpr uint64_t SETTLE_NS = 2000000000ull;   // for copies in flight after a wait gave up
 
-template <typename TS> constexpr int seg_of() { return sizeof(TS) == 2 ? 16 : 8; }       // steps a warp
-template <typename TS> constexpr int steps_of() { return NW * seg_of<TS>(); }            // steps a tile
-template <typename TS> constexpr int plane_of() { return steps_of<TS>() * UNITS; }       // elements of a tile's block
+// A kernel's form.  WIDE: many columns, so few chunks of one are under way at a time:
+// tickets and copies run a tile ahead, and every warp reads the few maps before by
+// itself.  Else chunks of a column wait for many others: tickets are taken late, and the
+// warps share the maps before.
+template <typename TS, bool WIDE> struct Shape {
+    static constexpr int SEG = sizeof(TS) == 2 ? 16 : 8;      // steps a warp
+    static constexpr int L = NW * SEG, PLANE = L * UNITS;     // steps and elements of a tile's block
+    static constexpr int FORWARD_CTAS = WIDE || sizeof(TS) == 2 ? 4 : 5, BACKWARD_CTAS = 4;   // an SM
+    static constexpr int FORWARD_TILES = WIDE ? 2 : 1;        // in shared memory
+};
 
 struct RecArgs {
     const void *H;                    // backward: (B, T, d)
@@ -61,7 +68,7 @@ struct RecArgs {
     int T, d;
     int n_ut, n_cols, n_chunks;       // unit tiles; B n_ut; chunks of time
     int group, span;                  // look-back: chunks of a group, groups of a span
-    int64_t n_tiles;
+    uint32_t n_tiles;
     float *last;                      // forward: (rows, d) or null
     const float *g_last;              // backward: (rows, d) or null
     float *g_state;                   // backward: (rows, d) or null
@@ -76,7 +83,7 @@ struct RecArgs {
 
 // ---------------------------------------------------------------- the gates
 struct UnitWeights {   // of a lane's two units
-    float2 rate, fall2, nb_a, nb_i;   // rate; -rate log2 e; -b log2 e
+    float2 fall2, nb_a, nb_i;   // -rate log2 e; -b log2 e
 };
 
 __device__ __forceinline__ float2 two_of(const float *p, bool ok) {
@@ -84,8 +91,7 @@ __device__ __forceinline__ float2 two_of(const float *p, bool ok) {
 }
 __device__ __forceinline__ UnitWeights weights_of(const float *params, int d, int u, bool ok) {
     UnitWeights w;
-    w.rate = two_of(params + u, ok);
-    w.fall2 = mul2(w.rate, splat2(-LOG2E));
+    w.fall2 = mul2(two_of(params + u, ok), splat2(-LOG2E));
     w.nb_a = mul2(two_of(params + d + u, ok), splat2(-LOG2E));
     w.nb_i = mul2(two_of(params + 2 * d + u, ok), splat2(-LOG2E));
     return w;
@@ -112,24 +118,21 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
     return y;
 }
 
-// 1 - a^2 with a = exp(-fall): for small y = 2 fall, where the difference would lose
-// bits, by the series of 1 - e^-y.  TERMS 5: below 1/4, to y^6 / 5040 (5e-8); 3: below
-// 1/16, to y^4 / 120 (1.3e-7), and 2^-19 by the difference at that border.
-template <int TERMS> __device__ __forceinline__ float2 one_less_square(float2 a, float2 y) {
-    float2 p;
-    if (TERMS == 5) {
-        p = fma2(y, splat2(-1.f / 720), splat2(1.f / 120));
-        p = fma2(y, p, splat2(-1.f / 24));
-    } else {
-        p = splat2(-1.f / 24);
-    }
-    p = fma2(y, p, splat2(1.f / 6));
-    p = fma2(y, p, splat2(-0.5f));
-    p = fma2(y, p, splat2(1.f));
-    p = mul2(y, p);
-    const float2 q = fma2(mul2(a, splat2(-1.f)), a, splat2(1.f));
-    constexpr float LIMIT = TERMS == 5 ? 0.25f : 0.0625f;
-    return make_float2(y.x < LIMIT ? p.x : q.x, y.y < LIMIT ? p.y : q.y);
+// a^2 - 1 with a = 2^z, z <= 0: for z near zero, where the difference would lose bits, by
+// the series of 2^2z - 1, y = -2 z ln 2.  TERMS 5: below y = 1/4, to y^6 / 720 (5e-8 of
+// it); 3: below 1/16, to y^4 / 24 (1.3e-7), and 2^-19 by the difference at that border.
+template <int TERMS> __device__ __forceinline__ float2 square_less_one(float2 a, float2 z) {
+    constexpr float C1 = 1.3862943611f, C2 = 0.9609060278f, C3 = 0.4440274099f, C4 = 0.1538881736f, C5 = 0.0426668398f,
+                    C6 = 0.0098579527f;   // (2 ln 2)^k / k!
+    float2 p = TERMS == 5 ? fma2(z, splat2(C6), splat2(C5)) : splat2(C4);
+    if (TERMS == 5) p = fma2(z, p, splat2(C4));
+    p = fma2(z, p, splat2(C3));
+    p = fma2(z, p, splat2(C2));
+    p = fma2(z, p, splat2(C1));
+    p = mul2(z, p);
+    const float2 q = fma2(a, a, splat2(-1.f));
+    constexpr float LIMIT = (TERMS == 5 ? -0.25f : -0.0625f) / 1.3862943611f;
+    return make_float2(z.x > LIMIT ? p.x : q.x, z.y > LIMIT ? p.y : q.y);
 }
 
 // e^-x in exponent-2 units, clamped: 1 / (1 + e) = sig, e / (1 + e) = 1 - sig
@@ -143,9 +146,10 @@ __device__ __forceinline__ void forward_gates(float2 pa, float2 pi, float2 v, co
     const float2 da = add2(falling(pa, w.nb_a), one), di = add2(falling(pi, w.nb_i), one);
     const float2 inv = rcp_2(mul2(da, di));
     const float2 r = mul2(inv, di), i = mul2(inv, da);
-    a = ex2_2(mul2(w.fall2, r));
-    const float2 q = one_less_square<TERMS>(a, mul2(add2(w.rate, w.rate), r));
-    u = mul2(mul2(make_float2(sqrt_approx(q.x), sqrt_approx(q.y)), i), v);
+    const float2 z = mul2(w.fall2, r);
+    a = ex2_2(z);
+    const float2 q = square_less_one<TERMS>(a, z);
+    u = mul2(mul2(make_float2(sqrt_approx(-q.x), sqrt_approx(-q.y)), i), v);
 }
 
 __device__ __forceinline__ float2 decay_of(float2 pa, const UnitWeights &w) {
@@ -212,76 +216,106 @@ __device__ __forceinline__ Map2 await2(const unsigned long long *slot, ulonglong
 
 // What a CTA shares while it works on a tile
 struct Shared {
-    float2 aggA[NW][32], aggB[NW][32];     // maps of the warps' steps, in the scan's order
-    float2 preA[NW][32], preB[NW][32];     // maps of runs of groups (0, 1) and chunks (2, 3) before
-    float2 end[32];                        // state after the span before
+    float2 aggA[2][NW][32], aggB[2][NW][32];   // maps of the warps' steps, in the scan's order
+    float2 preA[NW][32], preB[NW][32];         // maps of runs of groups (0, 1) and chunks (2, 3) before
+    float2 end[32];                            // state after the span before
     uint64_t bar[2];
-    int64_t tile[2];
+    uint32_t tile[2];
 };
 
-// The carry into this warp's steps.  q: the chunk in the scan's order (backward: from the
-// end of time); m: the map of this warp's steps; place: the warp in the scan's order;
-// first: the state that the first span starts from.  Called by all threads; two barriers.
-template <bool CUTS>
-__device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int col, int q, int place, int lane, const Map2 &m,
-                                             float2 first, bool ok) {
+constexpr int WIDE_GROUP = 4;   // chunks of a group where columns are many (spans of one group)
+
+// The carry into this warp's steps.  it: the CTA's count of tiles; q: the chunk in the
+// scan's order (backward: from the end of time); m: the map of this warp's steps; place:
+// the warp in the scan's order; first: the state that the first span starts from; ok:
+// the tile's copies came.  Called by all threads; between() runs after the (first) barrier.
+template <bool WIDE, bool CUTS, typename Fn>
+__device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int it, int col, int q, int place, int lane,
+                                             const Map2 &m, float2 first, bool ok, Fn &&between) {
     const float2 nan = splat2(__int_as_float(0x7fffffff));
-    s.aggA[place][lane] = m.A;
-    s.aggB[place][lane] = ok ? m.B : nan;   // (a tile whose copies gave up)
-    const int g = q / a.group, before = q - g * a.group, sp = g / a.span, gi = g - sp * a.span;
-    const int groups = (a.n_chunks + a.group - 1) / a.group, spans = (groups + a.span - 1) / a.span;
-    unsigned long long *slot = a.slots + (static_cast<int64_t>(col) * a.n_chunks + q) * UNITS + 2 * lane;
-    unsigned long long *map = a.maps + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
-    unsigned long long *end = a.ends + (static_cast<int64_t>(col) * spans + sp) * UNITS + 2 * lane;
-    const bool closes = before + 1 == a.group, closes_span = closes && gi + 1 == a.span;
-    __syncthreads();
-    auto warps_map = [&](int w) { return Map2{s.aggA[w][lane], s.aggB[w][lane]}; };
-    Map2 all{};
-    if (place == 0) {
-        all = warps_map(0);
+    float2 (&aggA)[NW][32] = s.aggA[it & 1], (&aggB)[NW][32] = s.aggB[it & 1];
+    aggA[place][lane] = m.A;
+    aggB[place][lane] = ok ? m.B : nan;   // (a tile whose copies gave up)
+    auto warps_map = [&](int w) { return Map2{aggA[w][lane], aggB[w][lane]}; };
+    auto whole_tile = [&]() {
+        Map2 all = warps_map(0);
 #pragma unroll
         for (int w = 1; w < NW; ++w) all = then<CUTS>(all, warps_map(w));
-        if (!closes) publish2(slot, all);
-    }
-    // maps before: the first two warps take halves of the span's groups, the others of
-    // the group's chunks
-    const unsigned long long *const list = place < 2 ? map - static_cast<int64_t>(gi) * UNITS : slot - static_cast<int64_t>(before) * UNITS;
-    const int n = place < 2 ? gi : before, k0 = n * (place & 1) / 2, k1 = n * ((place & 1) + 1) / 2;
-    Map2 run{splat2(1.f), splat2(0.f)};
-    for (int k = k0; k < k1; k += 4) {
-        ulonglong2 v[4];
+        return all;
+    };
+    unsigned long long *const slot = a.slots + (static_cast<int64_t>(col) * a.n_chunks + q) * UNITS + 2 * lane;
+    float2 h = first;
+    if constexpr (WIDE) {
+        const int g = q / WIDE_GROUP, before = q % WIDE_GROUP, groups = (a.n_chunks + WIDE_GROUP - 1) / WIDE_GROUP;
+        const bool closes = before + 1 == WIDE_GROUP && q + 1 < a.n_chunks;
+        unsigned long long *const end = a.ends + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
+        ulonglong2 v[WIDE_GROUP - 1], e = make_ulonglong2(SLOT_EMPTY, SLOT_EMPTY);
+        if (g > 0) e = peek2(end - UNITS);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (k + j < k1) v[j] = peek2(list + static_cast<int64_t>(k + j) * UNITS);
+        for (int k = 1; k < WIDE_GROUP; ++k)   // chunk q - k
+            if (k <= before) v[k - 1] = peek2(slot - k * UNITS);
+        __syncthreads();
+        between();
+        if (place == 0 && !closes) publish2(slot, whole_tile());
+        if (g > 0) h = await2(end - UNITS, e, a).B;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (k + j < k1) {
-                const Map2 x = await2(list + static_cast<int64_t>(k + j) * UNITS, v[j], a);
-                run = k + j == k0 ? x : then<CUTS>(run, x);
-            }
-    }
-    s.preA[place][lane] = run.A;
-    s.preB[place][lane] = run.B;
-    if (closes && gi + 1 < a.span) {   // the group's map waits for nothing but its chunks'
-        __syncwarp();
-        if (place != 1) asm volatile("bar.sync 1, 96;" ::: "memory");   // three of the warps
+        for (int k = WIDE_GROUP - 1; k > 0; --k)
+            if (k <= before) h = apply<CUTS>(await2(slot - k * UNITS, v[k - 1], a), h);
+        if (!ok) h = nan;
+        if (place == 0 && closes) publish2(end, Map2{splat2(0.f), apply<CUTS>(whole_tile(), h)});
+    } else {
+        const int g = q / a.group, before = q - g * a.group, sp = g / a.span, gi = g - sp * a.span;
+        const int groups = (a.n_chunks + a.group - 1) / a.group, spans = (groups + a.span - 1) / a.span;
+        unsigned long long *const map = a.maps + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
+        unsigned long long *const end = a.ends + (static_cast<int64_t>(col) * spans + sp) * UNITS + 2 * lane;
+        const bool closes = before + 1 == a.group, closes_span = closes && gi + 1 == a.span;
+        __syncthreads();
+        Map2 all{};
         if (place == 0) {
-            Map2 whole = then<CUTS>(Map2{s.preA[2][lane], s.preB[2][lane]}, Map2{s.preA[3][lane], s.preB[3][lane]});
-            publish2(map, then<CUTS>(whole, all));
+            all = whole_tile();
+            if (!closes) publish2(slot, all);
         }
-    }
-    if (place == 1) {
-        float2 h = first;
-        if (sp > 0) h = await2(end - UNITS, peek2(end - UNITS), a).B;
-        s.end[lane] = h;
-    }
-    __syncthreads();
-    float2 h = s.end[lane];
-    if (gi + before > 0)
+        // maps before: the first two warps take halves of the span's groups, the others
+        // of the group's chunks
+        const unsigned long long *const list =
+            place < 2 ? map - static_cast<int64_t>(gi) * UNITS : slot - static_cast<int64_t>(before) * UNITS;
+        const int n = place < 2 ? gi : before, k0 = n * (place & 1) / 2, k1 = n * ((place & 1) + 1) / 2;
+        Map2 run{splat2(1.f), splat2(0.f)};
+        for (int k = k0; k < k1; k += 4) {
+            ulonglong2 v[4];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) h = apply<CUTS>(Map2{s.preA[w][lane], s.preB[w][lane]}, h);
-    if (!ok) h = nan;
-    if (place == 0 && closes_span) publish2(end, Map2{splat2(0.f), apply<CUTS>(all, h)});
+            for (int j = 0; j < 4; ++j)
+                if (k + j < k1) v[j] = peek2(list + static_cast<int64_t>(k + j) * UNITS);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k + j < k1) {
+                    const Map2 x = await2(list + static_cast<int64_t>(k + j) * UNITS, v[j], a);
+                    run = k + j == k0 ? x : then<CUTS>(run, x);
+                }
+        }
+        s.preA[place][lane] = run.A;
+        s.preB[place][lane] = run.B;
+        if (closes && gi + 1 < a.span) {   // the group's map waits for nothing but its chunks'
+            __syncwarp();
+            if (place != 1) asm volatile("bar.sync 1, 96;" ::: "memory");   // three of the warps
+            if (place == 0) {
+                const Map2 chunks = then<CUTS>(Map2{s.preA[2][lane], s.preB[2][lane]}, Map2{s.preA[3][lane], s.preB[3][lane]});
+                publish2(map, then<CUTS>(chunks, all));
+            }
+        }
+        if (place == 1) {
+            if (sp > 0) h = await2(end - UNITS, peek2(end - UNITS), a).B;
+            s.end[lane] = h;
+        }
+        __syncthreads();
+        between();
+        h = s.end[lane];
+        if (gi + before > 0)
+#pragma unroll
+            for (int w = 0; w < NW; ++w) h = apply<CUTS>(Map2{s.preA[w][lane], s.preB[w][lane]}, h);
+        if (!ok) h = nan;
+        if (place == 0 && closes_span) publish2(end, Map2{splat2(0.f), apply<CUTS>(all, h)});
+    }
     for (int w = 0; w < place; ++w) h = apply<CUTS>(warps_map(w), h);
     return h;
 }
@@ -317,29 +351,28 @@ __device__ __forceinline__ bool tile_is_there(uint64_t *bar, uint32_t parity, co
 }
 
 struct Place { int col, b, u0, q, t0; };
-template <typename TS, bool REVERSE> __device__ __forceinline__ Place place_of(const RecArgs &a, int64_t tile) {
+template <int L, bool REVERSE> __device__ __forceinline__ Place place_of(const RecArgs &a, uint32_t tile) {
     Place p;
-    p.q = static_cast<int>(tile / a.n_cols);
-    p.col = static_cast<int>(tile - static_cast<int64_t>(p.q) * a.n_cols);
+    p.q = static_cast<int>(tile / static_cast<uint32_t>(a.n_cols));
+    p.col = static_cast<int>(tile) - p.q * a.n_cols;
     p.b = p.col / a.n_ut;
     p.u0 = (p.col - p.b * a.n_ut) * UNITS;
-    p.t0 = (REVERSE ? a.n_chunks - 1 - p.q : p.q) * steps_of<TS>();
+    p.t0 = (REVERSE ? a.n_chunks - 1 - p.q : p.q) * L;
     return p;
 }
 
 // ---------------------------------------------------------------- forward
-constexpr int FORWARD_CTAS = 4;   // an SM
-
-template <typename TS, bool PACK>
-__global__ void __launch_bounds__(THREADS, FORWARD_CTAS)
+template <typename TS, bool WIDE, bool PACK>
+__global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
     k_forward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const RecArgs a) {
-    constexpr int SEG = seg_of<TS>(), L = steps_of<TS>(), PLANE = plane_of<TS>(), TERMS = sizeof(TS) == 2 ? 3 : 5;
-    extern __shared__ __align__(128) unsigned char dsmem[];   // two tiles
+    using Form = Shape<TS, WIDE>;
+    constexpr int SEG = Form::SEG, PLANE = Form::PLANE, TERMS = sizeof(TS) == 2 ? 3 : 5;
+    extern __shared__ __align__(128) unsigned char dsmem[];   // FORWARD_TILES tiles
     __shared__ Shared s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     TS *const tiles = reinterpret_cast<TS *>(dsmem);
-    auto start = [&](int64_t tile, int buf) {   // the copies of a tile
-        const Place p = place_of<TS, false>(a, tile);
+    auto start = [&](uint32_t tile, int buf) {   // the copies of a tile
+        const Place p = place_of<Form::L, false>(a, tile);
         mbar_arrive_expect_tx(&s.bar[buf], 3u * PLANE * sizeof(TS));
 #pragma unroll
         for (int g = 0; g < 3; ++g)
@@ -356,10 +389,10 @@ __global__ void __launch_bounds__(THREADS, FORWARD_CTAS)
     }
     __syncthreads();
     for (int it = 0;; ++it) {
-        const int buf = it & 1;
-        const int64_t tile = s.tile[buf];
+        const int buf = WIDE ? it & 1 : 0;
+        const uint32_t tile = s.tile[it & 1];
         if (tile >= a.n_tiles) break;
-        const Place p = place_of<TS, false>(a, tile);
+        const Place p = place_of<Form::L, false>(a, tile);
         const int u = p.u0 + 2 * lane, r0 = warp * SEG;
         const bool uok = u < a.d;
         const UnitWeights w = weights_of(a.params, a.d, u, uok);
@@ -369,15 +402,16 @@ __global__ void __launch_bounds__(THREADS, FORWARD_CTAS)
         if (PACK) seg = segments_at<SEG>(a, p.t0 + r0, lane, heads, tails);
         else if (a.T - 1 - p.t0 - r0 >= 0 && a.T - 1 - p.t0 - r0 < SEG) tails = 1u << (a.T - 1 - p.t0 - r0);
         float2 first = splat2(0.f);   // what the first span starts from
-        if (!PACK && p.q < a.group * a.span && a.state != nullptr) first = two_of(a.state + static_cast<int64_t>(p.b) * a.d + u, uok);
+        if (!PACK && p.q < a.group * a.span && a.state != nullptr)
+            first = two_of(a.state + static_cast<int64_t>(p.b) * a.d + u, uok);
         // state before a segment's first step
         auto state_at = [&](int r) {
             const int sg = __shfl_sync(FULL_MASK, seg, r);
             return two_of(a.state + static_cast<int64_t>(sg) * a.d + u, uok && a.state != nullptr);
         };
-        int64_t next = 0;
-        if (tid == 0) next = atomicAdd(a.ticket, 1u);
-        const bool ok = tile_is_there(&s.bar[buf], (it >> 1) & 1, a);
+        uint32_t next = 0;
+        if (WIDE && tid == 0) next = atomicAdd(a.ticket, 1u);
+        const bool ok = tile_is_there(&s.bar[buf], (WIDE ? it >> 1 : it) & 1, a);
         float2 da[SEG], du[SEG];
         Map2 m{splat2(1.f), splat2(0.f)};
         auto compose = [&](auto special) {
@@ -396,14 +430,14 @@ __global__ void __launch_bounds__(THREADS, FORWARD_CTAS)
         };
         if (PACK && heads != 0) compose(std::true_type{});
         else compose(std::false_type{});
-        if (tid == 0) {
-            s.tile[buf ^ 1] = next;
-            if (next < a.n_tiles) {
-                bulk_wait_read<0>();   // the other tile's result has left it
-                start(next, buf ^ 1);
+        if (WIDE && tid == 0) s.tile[(it + 1) & 1] = next;
+        if (WIDE && lane == 0) bulk_wait_read<0>();   // this warp's result has left the tile before
+        float2 h = carry_into<WIDE, PACK>(a, s, it, p.col, p.q, warp, lane, m, first, ok, [&]() {
+            if (tid == 0) {
+                if (!WIDE) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
+                else if (next < a.n_tiles) start(next, buf ^ 1);
             }
-        }
-        float2 h = carry_into<PACK>(a, s, p.col, p.q, warp, lane, m, first, ok);
+        });
         auto write = [&](auto special) {
 #pragma unroll
             for (int i = 0; i < SEG; ++i) {
@@ -419,18 +453,21 @@ __global__ void __launch_bounds__(THREADS, FORWARD_CTAS)
         if ((heads | tails) != 0) write(std::true_type{});
         else write(std::false_type{});
         fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            tma_store_3d(&tmH, tiles + buf * 3 * PLANE, p.u0, p.t0, p.b);
+        __syncwarp();
+        if (lane == 0 && p.t0 + r0 < a.T) {
+            tma_store_3d(&tmH, mine, p.u0, p.t0 + r0, p.b);
             bulk_commit();
         }
+        if (!WIDE) {   // (else s.tile was written before this tile's barrier, and the shared maps alternate)
+            if (lane == 0) bulk_wait_read<0>();
+            __syncthreads();
+            if (tid == 0 && next < a.n_tiles) start(next, 0);
+        }
     }
-    if (tid == 0) bulk_wait_read<0>();   // the tiles outlive the stores' reads
+    if (lane == 0) bulk_wait_read<0>();   // the tiles outlive the stores' reads
 }
 
 // ---------------------------------------------------------------- backward
-constexpr int BACKWARD_CTAS = 4;   // an SM
-
 // shared -> global store of a block of dL/dP through the 4-D map (d, block, T, B)
 __device__ __forceinline__ void store_block(const CUtensorMap *map, const void *src, int x, int y, int z, int w) {
     asm volatile(
@@ -440,18 +477,19 @@ __device__ __forceinline__ void store_block(const CUtensorMap *map, const void *
         : "memory");
 }
 
-template <typename TS, bool PACK>
-__global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
+template <typename TS, bool WIDE, bool PACK>
+__global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
     k_backward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH,
                const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmGP, const RecArgs a) {
-    constexpr int SEG = seg_of<TS>(), L = steps_of<TS>(), PLANE = plane_of<TS>(), TERMS = sizeof(TS) == 2 ? 3 : 5;
+    using Form = Shape<TS, WIDE>;
+    constexpr int SEG = Form::SEG, PLANE = Form::PLANE, TERMS = sizeof(TS) == 2 ? 3 : 5;
     extern __shared__ __align__(128) unsigned char dsmem[];   // one tile: P, H, gH
     __shared__ Shared s;
     __shared__ float2 sums[3][NW][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     TS *const Ps = reinterpret_cast<TS *>(dsmem), *const Hs = Ps + 3 * PLANE, *const Gs = Hs + PLANE;
-    auto start = [&](int64_t tile) {
-        const Place p = place_of<TS, true>(a, tile);
+    auto start = [&](uint32_t tile) {
+        const Place p = place_of<Form::L, true>(a, tile);
         mbar_arrive_expect_tx(&s.bar[0], 5u * PLANE * sizeof(TS));
 #pragma unroll
         for (int g = 0; g < 3; ++g) tma_load_3d(Ps + g * PLANE, &tmP, &s.bar[0], g * a.d + p.u0, p.t0, p.b);
@@ -468,9 +506,9 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
     }
     __syncthreads();
     for (int it = 0;; ++it) {
-        const int64_t tile = s.tile[it & 1];
+        const uint32_t tile = s.tile[it & 1];
         if (tile >= a.n_tiles) break;
-        const Place p = place_of<TS, true>(a, tile);
+        const Place p = place_of<Form::L, true>(a, tile);
         const int u = p.u0 + 2 * lane, r0 = warp * SEG;
         const bool uok = u < a.d;
         const UnitWeights w = weights_of(a.params, a.d, u, uok);
@@ -489,8 +527,6 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
         float2 before0 = splat2(0.f);   // H at the step before this warp's first
         if (warp == 0 && p.t0 > 0 && uok)
             before0 = load2(static_cast<const TS *>(a.H) + (static_cast<int64_t>(p.b) * a.T + p.t0 - 1) * a.d + u);
-        int64_t next = 0;
-        if (tid == 0) next = atomicAdd(a.ticket, 1u);
         const bool ok = tile_is_there(&s.bar[0], it & 1, a);
         if (warp > 0) before0 = load2(h_mine - UNITS);
         // nu_{t+1} -> nu_t = a_t (gH_t + nu_{t+1}), the last step first; a sequence's last
@@ -502,8 +538,7 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
             for (int i = SEG - 1; i >= 0; --i) {
                 da[i] = decay_of(load2(mine + i * UNITS), w);
                 if (decltype(special)::value && (tails >> i & 1u)) {
-                    const float2 g = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
-                    m.B = g;
+                    m.B = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
                     m.A = splat2(-0.f);
                 }
                 m.B = mul2(da[i], add2(load2(g_mine + i * UNITS), m.B));
@@ -512,8 +547,14 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
         };
         if (tails != 0) compose(std::true_type{});
         else compose(std::false_type{});
-        float2 nu = carry_into<PACK>(a, s, p.col, p.q, NW - 1 - warp, lane, m, splat2(0.f), ok);
-        float2 g_rate = splat2(0.f), g_ba = splat2(0.f), g_bi = splat2(0.f);
+        uint32_t next = 0;
+        float2 nu = carry_into<WIDE, PACK>(a, s, it, p.col, p.q, NW - 1 - warp, lane, m, splat2(0.f), ok, [&]() {
+            if (tid == 0) {
+                next = atomicAdd(a.ticket, 1u);
+                s.tile[(it + 1) & 1] = next;
+            }
+        });
+        float2 g_wr = splat2(0.f), g_ba = splat2(0.f), g_bi = splat2(0.f);
         auto write = [&](auto special) {
 #pragma unroll
             for (int i = SEG - 1; i >= 0; --i) {
@@ -525,9 +566,10 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
                 const float2 xa = add2(ea, one), xi = add2(ei, one);
                 const float2 inv = rcp_2(mul2(xa, xi));
                 const float2 r = mul2(inv, xi), gi = mul2(inv, xa);
-                const float2 q = one_less_square<TERMS>(da[i], mul2(add2(w.rate, w.rate), r));
-                const float2 rs = make_float2(q.x > 0.f ? rsqrt_approx(q.x) : 0.f, q.y > 0.f ? rsqrt_approx(q.y) : 0.f);
-                const float2 sq = mul2(q, rs), over = mul2(da[i], rs);
+                const float2 z = mul2(w.fall2, r);                       // log2 of the decay
+                const float2 q = square_less_one<TERMS>(da[i], z);
+                const float2 rs = make_float2(q.x < 0.f ? rsqrt_approx(-q.x) : 0.f, q.y < 0.f ? rsqrt_approx(-q.y) : 0.f);
+                const float2 msq = mul2(q, rs), over = mul2(da[i], rs);   // -s, a / s
                 float2 before = i > 0 ? load2(h_mine + (i - 1) * UNITS) : before0;
                 if (SPECIAL && (heads >> i & 1u)) before = two_of(a.state + row_of(i), uok && a.state != nullptr);
                 const float2 G = add2(load2(g_mine + i * UNITS), nu);
@@ -536,13 +578,13 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
                     const int64_t at = row_of(i);
                     if (uok) *reinterpret_cast<float2 *>(a.g_state + at) = nu;
                 }
-                const float2 iv = mul2(gi, v);
-                // -w r; w = nu (before - over i v)
-                const float2 wr = mul2(mul2(nu, r), fma2(over, iv, mul2(before, splat2(-1.f))));
-                const float2 ga = mul2(mul2(wr, w.rate), mul2(ea, r));      // 1 - r = ea r
-                const float2 Gs_ = mul2(G, sq);
-                const float2 gv = mul2(Gs_, gi), gp = mul2(mul2(Gs_, iv), mul2(ei, gi));
-                g_rate = add2(g_rate, wr);
+                const float2 ngi = mul2(gi, splat2(-1.f)), miv = mul2(ngi, v);
+                // w r with w = nu (before - over i v); then gP_a = -rate w r (1 - r), 1 - r = ea r
+                const float2 wr = mul2(mul2(nu, r), fma2(over, miv, before));
+                const float2 ga = mul2(wr, mul2(mul2(z, splat2(0.6931471806f)), ea));   // -rate r = z ln 2
+                const float2 mGs = mul2(G, msq);
+                const float2 gv = mul2(mGs, ngi), gp = mul2(mul2(mGs, miv), mul2(ei, gi));
+                g_wr = add2(g_wr, wr);
                 g_ba = add2(g_ba, ga);
                 g_bi = add2(g_bi, gp);
                 store2(mine + i * UNITS, ga);
@@ -552,19 +594,19 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
         };
         if ((heads | tails) != 0) write(std::true_type{});
         else write(std::false_type{});
-        sums[0][warp][lane] = g_rate;
+        sums[0][warp][lane] = mul2(g_wr, splat2(-1.f));
         sums[1][warp][lane] = g_ba;
         sums[2][warp][lane] = g_bi;
-        if (tid == 0) s.tile[(it + 1) & 1] = next;
         fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
+        __syncwarp();
+        if (lane == 0 && p.t0 + r0 < a.T) {
 #pragma unroll
-            for (int g = 0; g < 3; ++g) store_block(&tmGP, Ps + g * PLANE, p.u0, g, p.t0, p.b);
+            for (int g = 0; g < 3; ++g) store_block(&tmGP, Ps + g * PLANE + r0 * UNITS, p.u0, g, p.t0 + r0, p.b);
             bulk_commit();
             bulk_wait_read<0>();
-            if (next < a.n_tiles) start(next);
         }
+        __syncthreads();
+        if (tid == 0 && next < a.n_tiles) start(next);
         if (warp < 3) {
             float2 t = sums[warp][0][lane];
 #pragma unroll
@@ -572,7 +614,7 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_CTAS)
             float *to = a.part + ((static_cast<int64_t>(p.col) * a.n_chunks + p.q) * 3 + warp) * UNITS + 2 * lane;
             *reinterpret_cast<float2 *>(to) = t;
         }
-        // (the next tile's two barriers lie between these reads and its sums)
+        // (the next tile's first barrier lies between these reads and its sums)
     }
 }
 
@@ -657,25 +699,26 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
+    bool wide;
     int64_t n_ut, n_cols, n_chunks, group, span, n_tiles;
     int64_t slots, maps, ends, cleared, part, share, total;
 };
 
-// Chunks of a look-back group and groups of a span.  A chain has a hop a span, 2 to 3 us,
-// and a chunk reads half a group's and half a span's maps on average.  Many columns have
-// few chunks of each under way and short chains: small groups, spans of one.
-void grouping(int64_t n_cols, int64_t &group, int64_t &span) {
-    group = n_cols >= 64 ? 8 : 16;
-    span = n_cols >= 64 ? 1 : 16;
-}
+// Columns from which a call takes the WIDE form.
+constexpr int64_t WIDE_COLUMNS = 64;
 
 Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, bool backward) {
     Layout y{};
-    const int64_t steps = dtype == NRNN_BF16 ? steps_of<__nv_bfloat16>() : steps_of<float>();
     y.n_ut = ceil_div(d, UNITS);
     y.n_cols = B * y.n_ut;
+    y.wide = y.n_cols >= WIDE_COLUMNS;
+    const int64_t steps = dtype == NRNN_BF16 ? (y.wide ? Shape<__nv_bfloat16, true>::L : Shape<__nv_bfloat16, false>::L)
+                                             : (y.wide ? Shape<float, true>::L : Shape<float, false>::L);
     y.n_chunks = ceil_div(T, steps);
-    grouping(y.n_cols, y.group, y.span);
+    // a chain has a hop a span (else, 2 to 3 us), and a chunk reads half a group's and half a
+    // span's maps on average
+    y.group = y.wide ? WIDE_GROUP : 16;
+    y.span = y.wide ? 1 : 16;
     const int64_t groups = ceil_div(y.n_chunks, y.group);
     y.n_tiles = y.n_cols * y.n_chunks;
     int64_t at = 256 + up256(4 * y.n_ut);   // ticket, error; the join's counters
@@ -728,7 +771,7 @@ RecArgs args_of(const Layout &y, const float *params, const float *state, const 
     a.n_ut = static_cast<int>(y.n_ut); a.n_cols = static_cast<int>(y.n_cols); a.n_chunks = static_cast<int>(y.n_chunks);
     a.group = static_cast<int>(y.group);
     a.span = static_cast<int>(y.span);
-    a.n_tiles = y.n_tiles;
+    a.n_tiles = static_cast<uint32_t>(y.n_tiles);
     a.ticket = reinterpret_cast<uint32_t *>(ws);
     a.error = a.ticket + 1;
     a.slots = reinterpret_cast<unsigned long long *>(ws + y.slots);
@@ -753,40 +796,51 @@ unsigned ctas_for(int64_t tiles, int per_sm) {
     return static_cast<unsigned>(tiles < most ? tiles : most);
 }
 
-// 3-D map over (B, T, width) with a box of one tile's block
-template <typename TS> bool map_tile(CUtensorMap *m, const void *base, int dtype, int64_t width, int64_t T, int64_t B) {
-    return make_map_steps(m, base, dtype, width, T, B, UNITS, steps_of<TS>());
-}
-
-template <typename TS, bool PACK>
+template <typename TS, bool WIDE, bool PACK>
 cudaError_t launch_forward(const Layout &y, const RecArgs &a, int dtype, const void *P, void *H, int64_t B, cudaStream_t s) {
+    using Form = Shape<TS, WIDE>;
     static std::atomic<unsigned long long> configured{0};
-    constexpr size_t smem = 2ull * 3 * plane_of<TS>() * sizeof(TS);
+    constexpr size_t smem = static_cast<size_t>(Form::FORWARD_TILES) * 3 * Form::PLANE * sizeof(TS);
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_forward<TS, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        return cudaFuncSetAttribute(k_forward<TS, WIDE, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     });
     if (e != cudaSuccess) return e;
     CUtensorMap tmP, tmH;
-    if (!map_tile<TS>(&tmP, P, dtype, 3 * a.d, a.T, B) || !map_tile<TS>(&tmH, H, dtype, a.d, a.T, B)) return cudaErrorUnknown;
-    return launch_dependent(k_forward<TS, PACK>, ctas_for(y.n_tiles, FORWARD_CTAS), THREADS, smem, s, tmP, tmH, a);
+    if (!make_map_steps(&tmP, P, dtype, 3 * a.d, a.T, B, UNITS, Form::L) ||
+        !make_map_steps(&tmH, H, dtype, a.d, a.T, B, UNITS, Form::SEG))
+        return cudaErrorUnknown;
+    return launch_dependent(k_forward<TS, WIDE, PACK>, ctas_for(y.n_tiles, Form::FORWARD_CTAS), THREADS, smem, s, tmP, tmH, a);
 }
 
-template <typename TS, bool PACK>
+template <typename TS, bool WIDE, bool PACK>
 cudaError_t launch_backward(const Layout &y, const RecArgs &a, int dtype, const void *P, const void *H, const void *gH,
                             void *gP, int64_t B, cudaStream_t s) {
+    using Form = Shape<TS, WIDE>;
     static std::atomic<unsigned long long> configured{0};
-    constexpr size_t smem = 5ull * plane_of<TS>() * sizeof(TS);
+    constexpr size_t smem = 5ull * Form::PLANE * sizeof(TS);
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_backward<TS, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        return cudaFuncSetAttribute(k_backward<TS, WIDE, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     });
     if (e != cudaSuccess) return e;
     CUtensorMap tmP, tmH, tmG, tmGP;
-    if (!map_tile<TS>(&tmP, P, dtype, 3 * a.d, a.T, B) || !map_tile<TS>(&tmH, H, dtype, a.d, a.T, B) ||
-        !map_tile<TS>(&tmG, gH, dtype, a.d, a.T, B) ||
-        !make_map_gate_steps(&tmGP, gP, dtype, a.d, a.T, B, UNITS, steps_of<TS>()))
+    if (!make_map_steps(&tmP, P, dtype, 3 * a.d, a.T, B, UNITS, Form::L) ||
+        !make_map_steps(&tmH, H, dtype, a.d, a.T, B, UNITS, Form::L) ||
+        !make_map_steps(&tmG, gH, dtype, a.d, a.T, B, UNITS, Form::L) ||
+        !make_map_gate_steps(&tmGP, gP, dtype, a.d, a.T, B, UNITS, Form::SEG))
         return cudaErrorUnknown;
-    return launch_dependent(k_backward<TS, PACK>, ctas_for(y.n_tiles, BACKWARD_CTAS), THREADS, smem, s, tmP, tmH, tmG, tmGP, a);
+    return launch_dependent(k_backward<TS, WIDE, PACK>, ctas_for(y.n_tiles, Form::BACKWARD_CTAS), THREADS, smem, s, tmP, tmH, tmG,
+                            tmGP, a);
 }
+
+// launch<TS, WIDE, PACK>(args...) for the call
+#define BY_FORM(launch, y, dtype, pack, ...)                                                                        \
+    ((dtype) == NRNN_BF16                                                                                           \
+         ? ((y).wide ? ((pack) ? launch<__nv_bfloat16, true, true>(y, __VA_ARGS__)                                  \
+                               : launch<__nv_bfloat16, true, false>(y, __VA_ARGS__))                                \
+                     : ((pack) ? launch<__nv_bfloat16, false, true>(y, __VA_ARGS__)                                 \
+                               : launch<__nv_bfloat16, false, false>(y, __VA_ARGS__)))                              \
+         : ((y).wide ? ((pack) ? launch<float, true, true>(y, __VA_ARGS__) : launch<float, true, false>(y, __VA_ARGS__)) \
+                     : ((pack) ? launch<float, false, true>(y, __VA_ARGS__) : launch<float, false, false>(y, __VA_ARGS__))))
 
 }  // namespace
 }  // namespace nrnn
@@ -824,13 +878,7 @@ int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *p
     RecArgs a = args_of(y, params, state, cu_seqlens, rows, T, d_h, ws);
     a.last = last;
     cudaError_t e = prepare(y, a, ws, state, last, nullptr, s);
-    if (e == cudaSuccess && n > 0) {
-        const bool pack = cu_seqlens != nullptr;
-        e = dtype == NRNN_BF16 ? (pack ? launch_forward<__nv_bfloat16, true>(y, a, dtype, preact, H, B, s)
-                                       : launch_forward<__nv_bfloat16, false>(y, a, dtype, preact, H, B, s))
-                               : (pack ? launch_forward<float, true>(y, a, dtype, preact, H, B, s)
-                                       : launch_forward<float, false>(y, a, dtype, preact, H, B, s));
-    }
+    if (e == cudaSuccess && n > 0) e = BY_FORM(launch_forward, y, dtype, cu_seqlens != nullptr, a, dtype, preact, H, B, s);
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
@@ -859,11 +907,7 @@ int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *
     a.g_state = g_state;
     cudaError_t e = prepare(y, a, ws, g_last, g_state, n > 0 ? nullptr : gparams, s);
     if (e == cudaSuccess && n > 0) {
-        const bool pack = cu_seqlens != nullptr;
-        e = dtype == NRNN_BF16 ? (pack ? launch_backward<__nv_bfloat16, true>(y, a, dtype, preact, H, gH, gP, B, s)
-                                       : launch_backward<__nv_bfloat16, false>(y, a, dtype, preact, H, gH, gP, B, s))
-                               : (pack ? launch_backward<float, true>(y, a, dtype, preact, H, gH, gP, B, s)
-                                       : launch_backward<float, false>(y, a, dtype, preact, H, gH, gP, B, s));
+        e = BY_FORM(launch_backward, y, dtype, cu_seqlens != nullptr, a, dtype, preact, H, gH, gP, B, s);
         if (e == cudaSuccess) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(static_cast<unsigned>(y.n_ut), JOIN_SLICES);

@@ -119,7 +119,8 @@ def reference_backward(P, params, H, gH, cu=None, state=None, g_last=None):
             g0.cuda(), e0.cuda())
 
 
-SHAPES = [(1, 1, 8), (2, 2, 40), (3, 63, 32), (1, 64, 72), (2, 65, 264), (1, 300, 136), (5, 129, 64), (1, 2500, 64), (40, 70, 8)]
+SHAPES = [(1, 1, 8), (2, 2, 40), (3, 63, 32), (1, 64, 72), (2, 65, 264), (1, 300, 136), (5, 129, 64), (1, 2500, 64), (40, 70, 8),
+          (70, 300, 8), (3, 700, 1536), (66, 64, 72)]
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -152,8 +153,19 @@ PACKS = [[0, 1], [0, 0, 5, 5, 6, 70, 70], [0, 64, 128, 192], [0, 63, 64, 129, 12
 @pytest.mark.parametrize("given", [False, True])
 @pytest.mark.parametrize("pack", range(len(PACKS)))
 def test_packs(pack, given, t):
+    packs_of_width(pack, 40, given, t)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("pack", [1, 3, 5, 6])
+def test_wide_packs(pack, t):
+    """More than 64 tiles of units: the form with copies a tile ahead."""
+    packs_of_width(pack, 4176, True, t)
+
+
+def packs_of_width(pack, d, given, t):
     cu = torch.tensor(PACKS[pack], dtype=torch.int32)
-    N, S, d = PACKS[pack][-1], len(PACKS[pack]) - 1, 40
+    N, S = PACKS[pack][-1], len(PACKS[pack]) - 1
     g, P, params = inputs(1, N, d, t, seed=pack)
     state = randn(g, S, d) if given else None
     H, last = nr.linear_recurrence(P, params, cu_seqlens=cu, state=state)
