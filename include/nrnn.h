@@ -708,10 +708,11 @@ int nrnn_linear_recurrence_step(const void *preact, int dtype, const float *para
 
 /*
  * Bytes of what nrnn_gated_mlp_forward keeps for the gradient, and workspace bytes of
- * the forward (backward = 0) or backward; 0 for invalid sizes.
+ * the forward that keeps nothing (what = 0), the backward (1) and the forward that keeps
+ * (2); 0 for invalid sizes.
  */
 size_t nrnn_gated_mlp_kept_bytes(int64_t rows, int64_t f, int dtype);
-size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dtype, int backward);
+size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dtype, int what);
 
 /*
  * Gated feed-forward block: a = x Wg^T, b = x Wu^T, y = (silu(a) b) W_out^T.
@@ -723,7 +724,7 @@ size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dt
  *   y           device, (rows, d) of dtype
  *   kept        device, 256-byte aligned, nrnn_gated_mlp_kept_bytes: what the
  *               gradient takes (its layout is the library's); NULL: not wanted
- *   workspace   device, 256-byte aligned, nrnn_gated_mlp_workspace_bytes(..., 0).  Its
+ *   workspace   device, 256-byte aligned, nrnn_gated_mlp_workspace_bytes.  Its
  *               first 32-bit word is 0 once the work is done, or not if a device wait
  *               gave up (nrnn_set_wait_limit_ns): then outputs are NaN where they
  *               depended on it.  So too in the backward

@@ -27,7 +27,11 @@ def _rows(t, rows: int, d: int, like: torch.Tensor, what: str):
 
 def _recurrence_params(params, d: int, device) -> torch.Tensor:
     """(3, d) fp32 device tensor from a dict (rate, b_a, b_i) or a tensor."""
-    if isinstance(params, dict):
+    if isinstance(params, torch.Tensor):   # as a decode step has them: nothing to do
+        if params.dtype == torch.float32 and params.device == device and params.shape == (3, d) \
+                and params.is_contiguous():
+            return params
+    elif isinstance(params, dict):
         params = torch.stack([torch.as_tensor(params[k]).to(device, torch.float32).reshape(-1)
                               for k in RECURRENCE_ORDER])
     params = torch.as_tensor(params)
@@ -119,14 +123,16 @@ def linear_recurrence_step(params, state: torch.Tensor | None, preact: torch.Ten
     preact = _device_tensor(preact, "preact")
     if preact.dim() != 2 or preact.shape[1] % 3:
         raise ValueError("preact must have shape (slots, 3 d_h)")
-    slots, d = preact.shape[0], preact.shape[1] // 3
+    slots, d = preact.shape
+    d //= 3
     code = _storage(preact)
     prm = _recurrence_params(params, d, preact.device)
     state = _rows(state, slots, d, preact, "state")
-    h = _result(out, (slots, d), preact, "out")
+    h = preact.new_empty((slots, d)) if out is None else _result(out, (slots, d), preact, "out")
     if state_out is None:
-        state_out = torch.empty((slots, d), dtype=torch.float32, device=preact.device)
-    elif state_out.dtype != torch.float32 or tuple(state_out.shape) != (slots, d) \
+        state_out = torch.empty((slots, d), dtype=torch.float32, device=preact.device) if state is None \
+            else torch.empty_like(state)
+    elif state_out.dtype != torch.float32 or state_out.shape != h.shape \
             or state_out.device != preact.device or not state_out.is_contiguous():
         raise ValueError(f"state_out must be a contiguous float32 {(slots, d)} tensor on {preact.device}")
     _run("linear_recurrence_step", load().nrnn_linear_recurrence_step, preact, preact.data_ptr(), code,
@@ -158,7 +164,7 @@ def gated_mlp(x: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, keep: bo
     x, W_in, W_out, code, rows, d, f = _mlp_args(x, W_in, W_out)
     lib = load()
     y = _result(out, x.shape, x, "out")
-    nbytes = lib.nrnn_gated_mlp_workspace_bytes(rows, d, f, code, 0)
+    nbytes = lib.nrnn_gated_mlp_workspace_bytes(rows, d, f, code, 2 if keep else 0)
     kept = None
     if keep:
         kept = torch.empty(lib.nrnn_gated_mlp_kept_bytes(rows, f, code), dtype=torch.uint8, device=x.device)

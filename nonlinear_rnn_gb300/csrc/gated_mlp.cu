@@ -706,9 +706,158 @@ __global__ void __launch_bounds__(256)
         copy_row<T>(src + r * d, out + r * pitch, rows * pitch, d, pitch, threadIdx.x & 31, wide);
 }
 
+// ---------------------------------------------------------------- few rows
+// A decode step's rows (nothing kept): the weights are read once, on the fp32 cores, and
+// m stays fp32.  A warp of k_few_up takes UP_UNITS units at a time, the rows of Wg and
+// Wu of each against every row of x from shared memory; a CTA of k_few_down takes
+// DOWN_ROWS rows of W_out, its warps a share of the inner dimension each, and has its
+// first weights under way before it waits for m.  Bound by HBM and, at this size, by
+// latency: 8 rows over 1024 x 4096 bf16 (25 MB, 3.7 us) FEW_MEASURED
+constexpr int FEW_MOST = 16, FEW_THREADS = 256, UP_UNITS = 2, FEW_AHEAD = 4;
+constexpr size_t FEW_X_BYTES = 96 * 1024;   // of the rows of x in shared memory
+template <int N> constexpr int DOWN_ROWS = N > 8 ? 4 : 8;
+
+// Sums over the lanes of V values each: halves are exchanged and added, until lane l has
+// value l V / 32 (and, of 64, the next one), 32 / V lanes the same one.
+template <int V> __device__ __forceinline__ void sums_to_lanes(float (&z)[V], int lane) {
+#pragma unroll
+    for (int o = 16, have = V; o > 0; o >>= 1) {
+        if (have > 1) {
+            have /= 2;
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                if (i >= have) break;
+                const float give = upper ? z[i] : z[i + have], keep = upper ? z[i + have] : z[i];
+                z[i] = keep + __shfl_xor_sync(FULL_MASK, give, o);
+            }
+        } else {
+            z[0] += __shfl_xor_sync(FULL_MASK, z[0], o);
+        }
+    }
+}
+
+template <typename T, int N, int VEC>
+__global__ void __launch_bounds__(FEW_THREADS)
+    k_few_up(const T *__restrict__ x, const T *__restrict__ W, float *__restrict__ m, uint32_t *error, int n, int d, int f) {
+    extern __shared__ __align__(32) float few_x[];   // [N][pitch], zeros past n and d
+    constexpr int CHUNK = 32 * VEC, ROWS = 2 * UP_UNITS, AHEAD = N > 8 ? 2 : FEW_AHEAD;
+    const int pitch = (d + CHUNK - 1) / CHUNK * CHUNK, lane = threadIdx.x & 31;
+    wait_for_prerequisites();
+    dependents_may_launch();   // (after the wait: the next kernel reads weights before its own)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *error = 0;
+    for (int i = threadIdx.x; i < N * pitch; i += FEW_THREADS) {
+        const int r = i / pitch, c = i - r * pitch;
+        few_x[i] = r < n && c < d ? to_f32(x[static_cast<int64_t>(r) * d + c]) : 0.f;
+    }
+    __syncthreads();
+    const int warps = gridDim.x * (FEW_THREADS / 32);
+    for (int j0 = (blockIdx.x * (FEW_THREADS / 32) + (threadIdx.x >> 5)) * UP_UNITS; j0 < f; j0 += warps * UP_UNITS) {
+        float acc[N * ROWS] = {};   // [row of x][unit][Wg, Wu]
+        const T *at[ROWS];
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+            const int unit = min(j0 + q / 2, f - 1);
+            at[q] = W + (static_cast<int64_t>(q % 2 ? f : 0) + unit) * d;
+        }
+        for (int c0 = lane * VEC; c0 < pitch; c0 += CHUNK * AHEAD) {
+            Pack<T, VEC> w[AHEAD][ROWS];
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+                for (int q = 0; q < ROWS; ++q)
+                    if (c0 + e * CHUNK < d) w[e][q] = *reinterpret_cast<const Pack<T, VEC> *>(at[q] + c0 + e * CHUNK);
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e)
+                if (c0 + e * CHUNK < d)
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        float xv[VEC];
+                        load_f32<float, VEC>(few_x + r * pitch + c0 + e * CHUNK, xv);
+#pragma unroll
+                        for (int q = 0; q < ROWS; ++q)
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i)
+                                acc[r * ROWS + q] = fmaf(to_f32(w[e][q].v[i]), xv[i], acc[r * ROWS + q]);
+                    }
+        }
+        sums_to_lanes(acc, lane);
+        constexpr int V = N * ROWS;
+        float a = acc[0], b;
+        if constexpr (V == 64) b = acc[1];
+        else b = __shfl_xor_sync(FULL_MASK, a, 32 / V);
+        const int v = V == 64 ? 2 * lane : lane * V / 32;   // even: this lane has a value of Wg
+        const int r = v / ROWS, unit = j0 + v % ROWS / 2;
+        if (v % 2 == 0 && (V >= 32 || lane % (32 / V) == 0) && r < n && unit < f)
+            m[static_cast<int64_t>(r) * f + unit] = a * sigmoid_of(a) * b;
+    }
+}
+
+template <typename T, int N, int VEC>
+__global__ void __launch_bounds__(FEW_THREADS)
+    k_few_down(const float *__restrict__ m, const T *__restrict__ W, T *__restrict__ y, int n, int d, int f) {
+    constexpr int CHUNK = 32 * VEC, WARPS = FEW_THREADS / 32, ROWS = DOWN_ROWS<N>, V = N * ROWS;
+    __shared__ float share[WARPS][V];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j0 = blockIdx.x * ROWS;
+    const T *at[ROWS];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) at[q] = W + static_cast<int64_t>(min(j0 + q, d - 1)) * f;
+    Pack<T, VEC> w[ROWS];
+    int c = warp * CHUNK + lane * VEC;
+    auto fetch = [&]() {
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q)
+            if (c < f) w[q] = *reinterpret_cast<const Pack<T, VEC> *>(at[q] + c);
+    };
+    fetch();   // the kernel before writes no weights, and those before it are done
+    wait_for_prerequisites();
+    dependents_may_launch();
+    float acc[V] = {};   // [row][column of y]
+    while (c < f) {
+        Pack<T, VEC> now[ROWS];
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) now[q] = w[q];
+        const int at_m = c;
+        c += WARPS * CHUNK;
+        fetch();
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            if (r < n) {
+                float mv[VEC];
+                load_f32<float, VEC>(m + static_cast<int64_t>(r) * f + at_m, mv);
+#pragma unroll
+                for (int q = 0; q < ROWS; ++q)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) acc[r * ROWS + q] = fmaf(to_f32(now[q].v[i]), mv[i], acc[r * ROWS + q]);
+            }
+    }
+    sums_to_lanes(acc, lane);
+    if constexpr (V == 64) {
+        share[warp][2 * lane] = acc[0];
+        share[warp][2 * lane + 1] = acc[1];
+    } else if (lane % (32 / V) == 0) {
+        share[warp][lane * V / 32] = acc[0];
+    }
+    __syncthreads();
+    if (threadIdx.x < V) {
+        float sum = share[0][threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < WARPS; ++k) sum += share[k][threadIdx.x];
+        const int r = threadIdx.x / ROWS, j = j0 + threadIdx.x % ROWS;
+        if (r < n && j < d) y[static_cast<int64_t>(r) * d + j] = from_f32<T>(sum);
+    }
+}
+
 // ---------------------------------------------------------------- host side
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// rows that the few-rows form is built for, and whether a call takes it: x has to fit in
+// shared memory
+int few_size(int64_t n) { return n <= 1 ? 1 : n <= 4 ? 4 : n <= 8 ? 8 : FEW_MOST; }
+bool few_rows(int64_t n, int64_t d) {
+    return n <= FEW_MOST && few_size(n) * (d + 255) * 4 <= static_cast<int64_t>(FEW_X_BYTES);
+}
 
 struct Call {
     const void *x, *W_in, *W_out;
@@ -749,6 +898,10 @@ int tile_columns(int64_t N) { return static_cast<int>(ceil_div(ceil_div(N, ceil_
 Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in_lies, bool w_out_lies, bool g_lies,
               bool keep, bool backward) {
     Plan p{};
+    if (!keep && !backward && few_rows(n, d)) {   // m alone
+        p.total = up256(256 + sizeof(float) * n * f);
+        return p;
+    }
     p.planes = dtype == NRNN_F32 ? 3 : 1;
     p.pd = ceil_div(d, 8) * 8;
     p.pf = ceil_div(f, 8) * 8;
@@ -935,6 +1088,45 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     return gemm<GWO, T>(c, ta, tb, to, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
+template <typename T, int N, int VEC_UP, int VEC_DOWN>
+cudaError_t launch_few(const Call &c, T *y) {
+    static std::atomic<unsigned long long> configured{0};
+    cudaError_t e = once_per_device(configured, [](int) {
+        return cudaFuncSetAttribute(k_few_up<T, N, VEC_UP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(FEW_X_BYTES));
+    });
+    if (e != cudaSuccess) return e;
+    float *m = reinterpret_cast<float *>(c.ws + 256);
+    const int n = static_cast<int>(c.n), d = static_cast<int>(c.d), f = static_cast<int>(c.f);
+    const size_t smem = sizeof(float) * N * (ceil_div(d, 32 * VEC_UP) * 32 * VEC_UP);
+    const int64_t want = ceil_div(f, UP_UNITS * (FEW_THREADS / 32));
+    e = launch_dependent(k_few_up<T, N, VEC_UP>, static_cast<unsigned>(want < 304 ? want : 304), FEW_THREADS, smem, c.stream,
+                         static_cast<const T *>(c.x), static_cast<const T *>(c.W_in), m,
+                         reinterpret_cast<uint32_t *>(c.ws), n, d, f);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(k_few_down<T, N, VEC_DOWN>, static_cast<unsigned>(ceil_div(d, DOWN_ROWS<N>)), FEW_THREADS, 0, c.stream,
+                            static_cast<const float *>(m), static_cast<const T *>(c.W_out), y, n, d, f);
+}
+
+template <typename T, int N> cudaError_t launch_few(const Call &c, T *y) {
+    constexpr int WIDE = 16 / sizeof(T);
+    const bool up = c.d % WIDE == 0 && reinterpret_cast<uintptr_t>(c.W_in) % 16 == 0;
+    const bool down = c.f % WIDE == 0 && reinterpret_cast<uintptr_t>(c.W_out) % 16 == 0;
+    return up ? (down ? launch_few<T, N, WIDE, WIDE>(c, y) : launch_few<T, N, WIDE, 1>(c, y))
+              : (down ? launch_few<T, N, 1, WIDE>(c, y) : launch_few<T, N, 1, 1>(c, y));
+}
+
+template <typename T> int few_forward(const Call &c, T *y) {
+    cudaError_t e;
+    switch (few_size(c.n)) {
+        case 1: e = launch_few<T, 1>(c, y); break;
+        case 4: e = launch_few<T, 4>(c, y); break;
+        case 8: e = launch_few<T, 8>(c, y); break;
+        default: e = launch_few<T, FEW_MOST>(c, y);
+    }
+    return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+}
+
 bool sizes_fit(int64_t n, int64_t d, int64_t f) { return n <= (1 << 30) && d <= (1 << 20) && f <= (1 << 20); }
 
 int check(const Call &c) {
@@ -964,9 +1156,9 @@ size_t nrnn_gated_mlp_kept_bytes(int64_t rows, int64_t f, int dtype) {
     return kept_layout(rows, f, dtype).total;
 }
 
-size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dtype, int backward) {
-    if (d <= 0 || !sizes_fit(0, d, 1) || nrnn_gated_mlp_kept_bytes(rows, f, dtype) == 0) return 0;
-    return plan_for(rows, d, f, dtype, false, false, false, false, false, backward != 0).total;
+size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dtype, int what) {
+    if (d <= 0 || what < 0 || what > 2 || !sizes_fit(0, d, 1) || nrnn_gated_mlp_kept_bytes(rows, f, dtype) == 0) return 0;
+    return plan_for(rows, d, f, dtype, false, false, false, false, what == 2, what == 1).total;
 }
 
 int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, int dtype, int64_t rows, int64_t d,
@@ -981,6 +1173,8 @@ int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, i
     const Plan p = plan_for(rows, d, f, dtype, used_in_place(x, d, dtype), used_in_place(W_in, d, dtype),
                             used_in_place(W_out, f, dtype), false, kept != nullptr, false);
     if (!usable(workspace, ws_bytes, p.total)) return NRNN_ERR_WORKSPACE;
+    if (kept == nullptr && few_rows(rows, d))
+        return dtype == NRNN_BF16 ? few_forward(c, static_cast<__nv_bfloat16 *>(y)) : few_forward(c, static_cast<float *>(y));
     unsigned char *k = kept != nullptr ? static_cast<unsigned char *>(kept) : c.ws + p.kept;
     return dtype == NRNN_BF16 ? forward(c, p, static_cast<__nv_bfloat16 *>(y), k, kept != nullptr)
                               : forward(c, p, static_cast<float *>(y), k, kept != nullptr);

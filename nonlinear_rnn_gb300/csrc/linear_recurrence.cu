@@ -152,9 +152,6 @@ __device__ __forceinline__ void forward_gates(float2 pa, float2 pi, float2 v, co
     u = mul2(mul2(make_float2(sqrt_approx(-q.x), sqrt_approx(-q.y)), i), v);
 }
 
-__device__ __forceinline__ float2 decay_of(float2 pa, const UnitWeights &w) {
-    return ex2_2(mul2(w.fall2, rcp_2(add2(falling(pa, w.nb_a), splat2(1.f)))));
-}
 
 // ------------------------------------------------------ maps h -> A h + B of two units
 struct Map2 { float2 A, B; };
@@ -434,8 +431,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
         if (WIDE && lane == 0) bulk_wait_read<0>();   // this warp's result has left the tile before
         float2 h = carry_into<WIDE, PACK>(a, s, it, p.col, p.q, warp, lane, m, first, ok, [&]() {
             if (tid == 0) {
-                if (!WIDE) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
-                else if (next < a.n_tiles) start(next, buf ^ 1);
+                if (WIDE && next < a.n_tiles) start(next, buf ^ 1);
             }
         });
         auto write = [&](auto special) {
@@ -459,6 +455,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
             bulk_commit();
         }
         if (!WIDE) {   // (else s.tile was written before this tile's barrier, and the shared maps alternate)
+            if (tid == 0) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
             if (lane == 0) bulk_wait_read<0>();
             __syncthreads();
             if (tid == 0 && next < a.n_tiles) start(next, 0);
@@ -531,28 +528,27 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
         if (warp > 0) before0 = load2(h_mine - UNITS);
         // nu_{t+1} -> nu_t = a_t (gH_t + nu_{t+1}), the last step first; a sequence's last
         // step starts from the gradient of its last state
-        float2 da[SEG];
+        float2 dr[SEG], de[SEG];   // r, (1 - r) / r
         Map2 m{splat2(1.f), splat2(0.f)};
         auto compose = [&](auto special) {
 #pragma unroll
             for (int i = SEG - 1; i >= 0; --i) {
-                da[i] = decay_of(load2(mine + i * UNITS), w);
+                de[i] = falling(load2(mine + i * UNITS), w.nb_a);
+                dr[i] = rcp_2(add2(de[i], splat2(1.f)));
+                const float2 decay = ex2_2(mul2(w.fall2, dr[i]));
                 if (decltype(special)::value && (tails >> i & 1u)) {
                     m.B = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
                     m.A = splat2(-0.f);
                 }
-                m.B = mul2(da[i], add2(load2(g_mine + i * UNITS), m.B));
-                m.A = mul2(da[i], m.A);
+                m.B = mul2(decay, add2(load2(g_mine + i * UNITS), m.B));
+                m.A = mul2(decay, m.A);
             }
         };
         if (tails != 0) compose(std::true_type{});
         else compose(std::false_type{});
         uint32_t next = 0;
         float2 nu = carry_into<WIDE, PACK>(a, s, it, p.col, p.q, NW - 1 - warp, lane, m, splat2(0.f), ok, [&]() {
-            if (tid == 0) {
-                next = atomicAdd(a.ticket, 1u);
-                s.tile[(it + 1) & 1] = next;
-            }
+            if (WIDE && tid == 0) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
         });
         float2 g_wr = splat2(0.f), g_ba = splat2(0.f), g_bi = splat2(0.f);
         auto write = [&](auto special) {
@@ -560,28 +556,24 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
             for (int i = SEG - 1; i >= 0; --i) {
                 constexpr bool SPECIAL = decltype(special)::value;
                 if (SPECIAL && (tails >> i & 1u)) nu = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
-                const float2 one = splat2(1.f);
-                const float2 ea = falling(load2(mine + i * UNITS), w.nb_a), ei = falling(load2(mine + PLANE + i * UNITS), w.nb_i);
+                const float2 ei = falling(load2(mine + PLANE + i * UNITS), w.nb_i), gi = rcp_2(add2(ei, splat2(1.f)));
                 const float2 v = load2(mine + 2 * PLANE + i * UNITS);
-                const float2 xa = add2(ea, one), xi = add2(ei, one);
-                const float2 inv = rcp_2(mul2(xa, xi));
-                const float2 r = mul2(inv, xi), gi = mul2(inv, xa);
-                const float2 z = mul2(w.fall2, r);                       // log2 of the decay
-                const float2 q = square_less_one<TERMS>(da[i], z);
+                const float2 r = dr[i], z = mul2(w.fall2, r), decay = ex2_2(z);
+                const float2 q = square_less_one<TERMS>(decay, z);
                 const float2 rs = make_float2(q.x < 0.f ? rsqrt_approx(-q.x) : 0.f, q.y < 0.f ? rsqrt_approx(-q.y) : 0.f);
-                const float2 msq = mul2(q, rs), over = mul2(da[i], rs);   // -s, a / s
+                const float2 msq = mul2(q, rs), over = mul2(decay, rs);   // -s, a / s
                 float2 before = i > 0 ? load2(h_mine + (i - 1) * UNITS) : before0;
                 if (SPECIAL && (heads >> i & 1u)) before = two_of(a.state + row_of(i), uok && a.state != nullptr);
                 const float2 G = add2(load2(g_mine + i * UNITS), nu);
-                nu = mul2(da[i], G);
+                nu = mul2(decay, G);
                 if (SPECIAL && (heads >> i & 1u) && a.g_state != nullptr) {
                     const int64_t at = row_of(i);
                     if (uok) *reinterpret_cast<float2 *>(a.g_state + at) = nu;
                 }
                 const float2 ngi = mul2(gi, splat2(-1.f)), miv = mul2(ngi, v);
-                // w r with w = nu (before - over i v); then gP_a = -rate w r (1 - r), 1 - r = ea r
+                // w r with w = nu (before - over i v); then gP_a = -rate w r (1 - r), 1 - r = e r
                 const float2 wr = mul2(mul2(nu, r), fma2(over, miv, before));
-                const float2 ga = mul2(wr, mul2(mul2(z, splat2(0.6931471806f)), ea));   // -rate r = z ln 2
+                const float2 ga = mul2(wr, mul2(mul2(z, splat2(0.6931471806f)), de[i]));   // -rate r = z ln 2
                 const float2 mGs = mul2(G, msq);
                 const float2 gv = mul2(mGs, ngi), gp = mul2(mul2(mGs, miv), mul2(ei, gi));
                 g_wr = add2(g_wr, wr);
@@ -594,6 +586,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
         };
         if ((heads | tails) != 0) write(std::true_type{});
         else write(std::false_type{});
+        if (!WIDE && tid == 0) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
         sums[0][warp][lane] = mul2(g_wr, splat2(-1.f));
         sums[1][warp][lane] = g_ba;
         sums[2][warp][lane] = g_bi;

@@ -81,6 +81,7 @@ def test_gated_mlp_refusals(dtype):
     assert size(100, 16, 24, dtype, 0) > 0 and size(100, 16, 24, dtype, 1) > 0
     assert kept(100, 0, dtype) == kept(-1, 24, dtype) == kept(1, 24, 5) == 0
     assert size(100, 0, 24, dtype, 0) == size(100, 16, 24, 7, 1) == size((1 << 30) + 1, 16, 24, dtype, 0) == 0
+    assert size(100, 16, 24, dtype, 3) == size(100, 16, 24, dtype, -1) == 0 < size(4, 16, 24, dtype, 0) < size(4, 16, 24, dtype, 2)
 
     def forward(x=FAKE, Wi=FAKE, Wo=FAKE, dtype=dtype, n=100, d=16, f=24, y=FAKE, kept=WS, ws=WS, wsb=BIG):
         return lib.nrnn_gated_mlp_forward(x, Wi, Wo, dtype, n, d, f, y, kept, ws, wsb, None)
