@@ -23,8 +23,9 @@
 //   GWI  [ga gb]^T x           rows of gW_in, Wg's tiles, then Wu's
 //   GWO  g^T m
 //
-// UP and DH have many tiles; the others may have few and long inner dimensions.  For
-// them whole waves of tiles go one to a pair and the rest is cut by inner slices, an
+// UP and DH have many tiles; the others may have few and long inner dimensions.  Where
+// these are less than WAVES_UNCUT waves, whole waves of tiles go one to a pair and the
+// rest is cut by inner slices, an
 // equal run of the (tile, slice) sequence to every team of pairs; parts of a cut tile go
 // to the workspace in fp32 and k_join_parts adds them in order.
 //
@@ -52,6 +53,7 @@ namespace {
 
 constexpr int PAIRS = 76;   // of 152 SMs
 constexpr int MOST_SIDE = 8;
+constexpr int WAVES_UNCUT = 4;   // a last wave of this many loses less than joining its parts costs
 
 enum Form { UP, DOWN, DH, GX, GWI, GWO };
 
@@ -97,6 +99,11 @@ struct Unit { int tm, tn, k0, k1, slot; };   // slot: -1 = a whole tile
 
 template <int FORM> constexpr bool CUTS = FORM != UP && FORM != DH;
 
+// UP, DH: row tiles that the pairs work on at a time.  Their outputs (a, b and m; ga and
+// gb) pass through L2 and push out what lies there: with all row tiles against one column
+// tile after another, x came from HBM once a column tile.  BAND_MEASURED
+constexpr int BAND = 8;
+
 template <int FORM> struct Walk {
     int u, pairs, side_at;
     int64_t pos, end;
@@ -118,9 +125,11 @@ template <int FORM> struct Walk {
         t.k0 = 0; t.k1 = a.kb; t.slot = -1;
         if (!CUTS<FORM>) {
             if (u >= a.units) return false;
-            // rows fastest: the pairs working at one time share a tile of the weights
-            t.tm = u % a.tiles_m;
-            t.tn = u / a.tiles_m;
+            // bands of row tiles, each against all column tiles, rows fastest
+            const int band = u / (BAND * a.tiles_n), in_band = u - band * (BAND * a.tiles_n);
+            const int rows = min(BAND, a.tiles_m - band * BAND);
+            t.tn = in_band / rows;
+            t.tm = band * BAND + in_band - t.tn * rows;
             u += pairs;
             return true;
         }
@@ -341,6 +350,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         auto place = [&](int i, int q) {
             return reinterpret_cast<uint4 *>(stage_out + i * BOX_BYTES + lane * 128 + 16 * (q ^ (lane & 7)));
         };
+        // block i of this warp to row y, column x of an array of rows of `pitch` elements, by
+        // this warp's stores
+        auto store_rows = [&](int i, __nv_bfloat16 *to, int pitch, int x, int y) {
+#pragma unroll
+            for (int k = 0; k < BOX_ROWS / 4; ++k) {
+                const int r = 4 * k + (lane >> 3), q = lane & 7;
+                if (y + r < a.M && x + 8 * q < pitch)
+                    *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(y + r) * pitch + x + 8 * q) =
+                        *reinterpret_cast<const uint4 *>(stage_out + i * BOX_BYTES + r * 128 + 16 * (q ^ (r & 7)));
+            }
+        };
         auto blocks_free = [&]() {   // the stores before have read the blocks
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
@@ -509,11 +529,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
+                if (a.keep) {
+                    __nv_bfloat16 *kept = reinterpret_cast<__nv_bfloat16 *>(a.ab);
+                    store_rows(0, kept, a.pitch, x, y0);
+                    store_rows(1, kept + static_cast<int64_t>(a.M) * a.pitch, a.pitch, x, y0);
+                }
                 if (lane == 0 && y0 < a.M) {
-                    if (a.keep) {
-                        tma_store_3d(&tmAB, stage_out, x, y0, 0);
-                        tma_store_3d(&tmAB, stage_out + BOX_BYTES, x, y0, 1);
-                    }
                     tma_store_3d(&tmOut, stage_out + (BLOCKS - 1) * BOX_BYTES, x, y0, 0);
                     bulk_commit();
                 }
@@ -956,7 +977,7 @@ cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, 
         a.side = a.tiles_n <= MOST_SIDE && a.tiles_n <= pairs ? a.tiles_n : 1;
         a.teams = pairs / a.side;
         a.units = static_cast<int>(tiles / a.side);
-        a.whole = a.units / a.teams * a.teams;
+        a.whole = a.units >= WAVES_UNCUT * a.teams ? a.units : a.units / a.teams * a.teams;
     }
     e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, tmAB, a);
     const int64_t cut = static_cast<int64_t>(a.units - a.whole) * a.side;
