@@ -1,7 +1,8 @@
 // Gated feed-forward block and its gradient.
 //
 //   a = x Wg^T, b = x Wu^T, m = silu(a) b, y = m Wo^T        W_in = [Wg; Wu]
-//   gm = g Wo, ga = gm b silu'(a), gb = gm silu(a)
+//   p = dm/da = b silu'(a), q = dm/db = silu(a)
+//   gm = g Wo, ga = gm p, gb = gm q
 //   gx = [ga gb] W_in, gW_in = [ga gb]^T x, gW_out = g^T m
 //
 // 6 n d f operations forward and 12 n d f backward: bound by the tensor cores, except
@@ -16,9 +17,9 @@
 //                    rows of Wg, the other the same rows of Wu.  The accumulator then
 //                    holds a and b of the same 128 units beside one another, and the
 //                    epilogue forms m without either having been stored.  With the
-//                    gradient to come a and b are kept, in the storage type.
+//                    gradient to come p and q are kept, in the storage type.
 //   DOWN m W_out^T
-//   DH   g W_out     gm, from which the epilogue forms ga and gb by the kept a and b
+//   DH   g W_out     gm, from which the epilogue forms ga and gb by the kept p and q
 //   GX   [ga gb] W_in          the inner dimension runs over ga, then gb
 //   GWI  [ga gb]^T x           rows of gW_in, Wg's tiles, then Wu's
 //   GWO  g^T m
@@ -30,7 +31,7 @@
 // to the workspace in fp32 and k_join_parts adds them in order.
 //
 // For bf16, m (formed from unrounded a and b) is rounded before the second product, and
-// a, b, ga and gb where they are stored: an operand of the tensor cores is bf16, and a
+// p, q, ga and gb where they are stored: an operand of the tensor cores is bf16, and a
 // second plane of each would double every product.  y and gW_out are 1.41 times as far
 // off as rounding the exact result once, gx and gW_in 1.8 times.
 //
@@ -89,8 +90,8 @@ struct GemmArgs {
     float *parts;             // [pairs][2][BM][bn] sums of cut tiles
     void *out;                // the result in the storage type, rows of N
     bool blocks_out;          // bf16: tmOut is over the result, whose blocks leave by TMA
-    bool keep;                // UP: a and b are stored
-    float *ab;                // fp32: a and b, [2][M][pitch]
+    bool keep;                // UP: p and q are stored
+    void *pq;                 // p and q, [2][M][pitch] in the storage type
     int pitch;
 };
 
@@ -99,7 +100,7 @@ struct Unit { int tm, tn, k0, k1, slot; };   // slot: -1 = a whole tile
 
 template <int FORM> constexpr bool CUTS = FORM != UP && FORM != DH;
 
-// UP, DH: row tiles that the pairs work on at a time.  Their outputs (a, b and m; ga and
+// UP, DH: row tiles that the pairs work on at a time.  Their outputs (p, q and m; ga and
 // gb) pass through L2 and push out what lies there: with all row tiles against one column
 // tile after another, x came from HBM once a column tile.  BAND_MEASURED
 constexpr int BAND = 8;
@@ -170,12 +171,13 @@ template <typename T> __device__ __forceinline__ void store_cols(T *p, const flo
 
 __device__ __forceinline__ float sigmoid_of(float x) { return rcp_approx(1.f + ex2_approx(-LOG2E * x)); }
 
-// ga and gb in place of a and b
-__device__ __forceinline__ void gate_back(float gm, float &a, float &b) {
-    const float s = sigmoid_of(a), gs = gm * s;
-    const float ga = gs * b * fmaf(a, 1.f - s, 1.f);
-    b = gs * a;
-    a = ga;
+// m = silu(a) b; in place of a and b what the gradient takes: dm/da = b silu'(a) and
+// dm/db = silu(a), silu'(a) = s + silu(a) (1 - s)
+__device__ __forceinline__ float gate(float &a, float &b) {
+    const float s = sigmoid_of(a), q = a * s, m = q * b;
+    a = b * fmaf(q, 1.f - s, s);
+    b = q;
+    return m;
 }
 
 template <int FORM> __device__ constexpr bool mn_a() { return FORM == GWI || FORM == GWO; }
@@ -192,7 +194,7 @@ template <int FORM> __device__ __forceinline__ uint32_t stage_bytes(const GemmAr
 template <int FORM, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     k_mlp_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmAB, const GemmArgs a) {
+               const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPQ, const GemmArgs a) {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr bool MN_A = mn_a<FORM>(), MN_B = mn_b<FORM>();
     constexpr int STAGES = stages_of<FORM, T>(), BLOCKS = blocks_of<FORM, T>();
@@ -201,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], accf_bar[2], acce_bar[2],
-        drain_bar, ab_bar[EPI_WARPS];
+        drain_bar, pq_bar[EPI_WARPS];
     __shared__ uint32_t s_tmem;
     __shared__ volatile uint32_t s_abort;     // a role of either CTA gave up
     __shared__ volatile int s_issued[2];      // rank 0's: stages that each producer went through
@@ -217,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             mbar_init(&accf_bar[b], 1);
             mbar_init(&acce_bar[b], 2 * EPI_WARPS);   // rank 0's: both epilogues
         }
-        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(&ab_bar[w], 1);
+        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(&pq_bar[w], 1);
         mbar_init(&drain_bar, 1);
         s_abort = 0;
         fence_mbar_init();
@@ -335,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         unsigned char *stage_out = smem + STAGES * STAGE_BYTES + (warp - 4) * BLOCKS * BOX_BYTES;
         const float nan = __int_as_float(0x7fffffff);
         int phase = 0;
-        uint32_t ab_phase = 0;
+        uint32_t pq_phase = 0;
         bool ok = true;   // false once a wait gave up: NaN from there on
         auto release = [&](int buf) {   // this warp has read the accumulator
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -465,20 +467,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     const int x = t.tn * half_n + odd * PIECE, left = a.N - x;
                     if (mine && left > 0) {
                         if (a.keep && m < a.M) {
+                            float *p = static_cast<float *>(a.pq) + static_cast<int64_t>(m) * a.pitch + x, *q = p + static_cast<int64_t>(a.M) * a.pitch;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                store_cols<float>(a.ab + (static_cast<int64_t>(i) * a.M + m) * a.pitch + x, acc[i],
-                                                  min(a.pitch - x, PIECE), true);
+                            for (int c = 0; c < PIECE; c += 4)
+                                if (c < a.pitch - x) {   // (the pitch is a multiple of 8: whole fours)
+                                    float vp[4], vq[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        vp[e] = acc[0][c + e];
+                                        vq[e] = acc[1][c + e];
+                                        gate(vp[e], vq[e]);
+                                    }
+                                    store_f32<float, 4>(p + c, vp);
+                                    store_f32<float, 4>(q + c, vq);
+                                }
                         }
 #pragma unroll
-                        for (int e = 0; e < PIECE; ++e) acc[0][e] = acc[0][e] * sigmoid_of(acc[0][e]) * acc[1][e];
+                        for (int e = 0; e < PIECE; ++e) acc[0][e] = gate(acc[0][e], acc[1][e]);
                         store_planes(acc[0], x, y0, 0, 1);
                     }
                 } else if constexpr (FORM == DH) {
                     const int x = t.tn * a.bn + odd * PIECE, left = a.N - x;
                     if (odd * PIECE < a.bn && left > 0) {
                         float gb[PIECE];
-                        const float *pa = a.ab + static_cast<int64_t>(m) * a.pitch + x, *pb = pa + static_cast<int64_t>(a.M) * a.pitch;
+                        const float *pa = static_cast<const float *>(a.pq) + static_cast<int64_t>(m) * a.pitch + x, *pb = pa + static_cast<int64_t>(a.M) * a.pitch;
 #pragma unroll
                         for (int q = 0; q < PIECE; q += 4) {
                             float va[4] = {}, vb[4] = {};
@@ -488,9 +500,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                             }
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                gate_back(acc[0][q + e], va[e], vb[e]);
-                                acc[0][q + e] = va[e];
-                                gb[q + e] = vb[e];
+                                gb[q + e] = acc[0][q + e] * vb[e];
+                                acc[0][q + e] *= va[e];
                             }
                         }
                         store_planes(acc[0], x, y0, 0, 2);
@@ -518,19 +529,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     if (h + 32 == PIECE) release(buf);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
+                        float vm[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) vm[e] = gate(va[8 * q + e], vb[8 * q + e]);
+                        *place(BLOCKS - 1, h / 8 + q) = to_bf16(vm);
                         if (a.keep) {
                             *place(0, h / 8 + q) = to_bf16(va + 8 * q);
                             *place(1, h / 8 + q) = to_bf16(vb + 8 * q);
                         }
-#pragma unroll
-                        for (int e = 8 * q; e < 8 * q + 8; ++e) va[e] = va[e] * sigmoid_of(va[e]) * vb[e];
-                        *place(BLOCKS - 1, h / 8 + q) = to_bf16(va + 8 * q);
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (a.keep) {
-                    __nv_bfloat16 *kept = reinterpret_cast<__nv_bfloat16 *>(a.ab);
+                    __nv_bfloat16 *kept = static_cast<__nv_bfloat16 *>(a.pq);
                     store_rows(0, kept, a.pitch, x, y0);
                     store_rows(1, kept + static_cast<int64_t>(a.M) * a.pitch, a.pitch, x, y0);
                 }
@@ -544,20 +556,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 for (int c = odd * PIECE; c < a.bn; c += 2 * PIECE) {
                     const int x = t.tn * a.bn + c;
                     const bool inside = x < a.N && y0 < a.M;
-                    // a and b of the piece, while the products are under way
+                    // p and q of the piece, while the products are under way
                     if (inside) {
                         blocks_free();
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(&ab_bar[warp - 4], 2 * BOX_BYTES);
-                            tma_load_3d(stage_out, &tmAB, &ab_bar[warp - 4], x, y0, 0);
-                            tma_load_3d(stage_out + BOX_BYTES, &tmAB, &ab_bar[warp - 4], x, y0, 1);
+                            mbar_arrive_expect_tx(&pq_bar[warp - 4], 2 * BOX_BYTES);
+                            tma_load_3d(stage_out, &tmPQ, &pq_bar[warp - 4], x, y0, 0);
+                            tma_load_3d(stage_out + BOX_BYTES, &tmPQ, &pq_bar[warp - 4], x, y0, 1);
                         }
                     }
                     if (c < 2 * PIECE) accumulator(buf, (phase >> 1) & 1);
                     if (inside) {
                         // (no other role waits for these copies: they are seen through whatever happens)
-                        ok &= mbar_wait_bounded(&ab_bar[warp - 4], ab_phase, SETTLE_NS, a.error);
-                        ab_phase ^= 1;
+                        ok &= mbar_wait_bounded(&pq_bar[warp - 4], pq_phase, SETTLE_NS, a.error);
+                        pq_phase ^= 1;
 #pragma unroll
                         for (int h = 0; h < PIECE; h += 32) {
                             float g[32];
@@ -570,9 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                                 float va[8], vb[8];
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
-                                    va[e] = to_f32(pa.v[e]);
-                                    vb[e] = to_f32(pb.v[e]);
-                                    gate_back(g[8 * q + e], va[e], vb[e]);
+                                    va[e] = to_f32(pa.v[e]) * g[8 * q + e];
+                                    vb[e] = to_f32(pb.v[e]) * g[8 * q + e];
                                 }
                                 *place(0, h / 8 + q) = to_bf16(va);
                                 *place(1, h / 8 + q) = to_bf16(vb);
@@ -888,7 +899,7 @@ struct Call {
     cudaStream_t stream;
 };
 
-// What the gradient takes: a and b [2][n][pf] in the storage type, m [planes][n][pf] bf16.
+// What the gradient takes: p and q [2][n][pf] in the storage type, m [planes][n][pf] bf16.
 // (Not rounded up, so that its size tells one number of rows from another.)
 struct Kept { size_t m, total; int64_t pf; };
 Kept kept_layout(int64_t n, int64_t f, int dtype) {
@@ -958,7 +969,7 @@ cudaError_t operand(const Call &c, const void *src, size_t copy, int64_t rows, i
 
 template <int FORM, typename T>
 cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut,
-                 const CUtensorMap &tmAB, GemmArgs a) {
+                 const CUtensorMap &tmPQ, GemmArgs a) {
     static std::atomic<unsigned long long> configured{0};
     constexpr size_t smem = gemm_smem<FORM, T>();
     cudaError_t e = once_per_device(configured, [](int) {
@@ -979,7 +990,7 @@ cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, 
         a.units = static_cast<int>(tiles / a.side);
         a.whole = a.units >= WAVES_UNCUT * a.teams ? a.units : a.units / a.teams * a.teams;
     }
-    e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, tmAB, a);
+    e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, tmPQ, a);
     const int64_t cut = static_cast<int64_t>(a.units - a.whole) * a.side;
     if (e == cudaSuccess && cut > 0) {
         const bool few = cut * 8 <= pairs;   // eight parts each and more
@@ -1024,19 +1035,19 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
         operand<T>(c, c.W_in, p.w_in, 2 * c.f, c.d, p.pd, &w_in) != cudaSuccess ||
         operand<T>(c, c.W_out, p.w_out, c.d, c.f, p.pf, &w_out) != cudaSuccess)
         return NRNN_ERR_CUDA;
-    CUtensorMap ta, tb, to, tab;
+    CUtensorMap ta, tb, to, tpq;
     // UP: equal tiles of the units, in whole 64-unit blocks
     const int units = static_cast<int>(ceil_div(ceil_div(c.f, ceil_div(c.f, BN / 2)), 64) * 64);
     if (!map(&ta, x, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, BK, units) ||
-        !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS) || (p.planes == 1 && !map(&tab, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
+        !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS) || (p.planes == 1 && !map(&tpq, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
-    if (p.planes != 1) tab = to;
+    if (p.planes != 1) tpq = to;
     GemmArgs a = args_of(c, c.n, c.f, c.d, 2 * units);
     a.tiles_n = static_cast<int>(ceil_div(c.f, units));
     a.keep = keep;
-    a.ab = reinterpret_cast<float *>(kept);
+    a.pq = kept;
     a.pitch = static_cast<int>(p.pf);
-    if (gemm<UP, T>(c, ta, tb, to, tab, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    if (gemm<UP, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
     const int bn = tile_columns(c.d);
     a = args_of(c, c.n, c.d, c.f, bn);
     a.parts = reinterpret_cast<float *>(c.ws + p.parts);
@@ -1060,20 +1071,20 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
         operand<T>(c, c.W_out, p.w_out, c.d, c.f, p.pf, &w_out) != cudaSuccess ||
         operand<T>(c, g_, p.g, c.n, c.d, p.pd, &g) != cudaSuccess)
         return NRNN_ERR_CUDA;
-    CUtensorMap ta, tb, to, tab;
+    CUtensorMap ta, tb, to, tpq;
     float *parts = reinterpret_cast<float *>(c.ws + p.parts);
-    // ga and gb.  fp32: one piece of an epilogue warp holds ga and gb, so tiles of 128
+    // fp32: one piece of an epilogue warp holds ga and gb, so tiles of 128
     int bn = tile_columns(c.f);
     if (p.planes != 1 && bn > 2 * PIECE) bn = 2 * PIECE;
     GemmArgs a = args_of(c, c.n, c.f, c.d, bn);
-    a.ab = const_cast<float *>(reinterpret_cast<const float *>(kept));
+    a.pq = const_cast<unsigned char *>(kept);
     a.pitch = static_cast<int>(p.pf);
     if (!map(&ta, g, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, 64, BK) ||
         !map(&to, gab, c.f, p.pf, c.n, 2 * p.planes, PIECE, BOX_ROWS) ||
-        (p.planes == 1 && !map(&tab, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
+        (p.planes == 1 && !map(&tpq, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
-    if (p.planes != 1) tab = to;
-    if (gemm<DH, T>(c, ta, tb, to, tab, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    if (p.planes != 1) tpq = to;
+    if (gemm<DH, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gx
     bn = tile_columns(c.d);
     a = args_of(c, c.n, c.d, c.f, bn);
