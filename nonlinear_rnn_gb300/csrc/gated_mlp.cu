@@ -45,6 +45,8 @@
 // first) and the abort flag of both CTAs of the pair, which ends the other roles' waits
 // too; the epilogues write NaN from there on, and neither CTA leaves before what both
 // have in flight is done (settle).
+#include <type_traits>
+
 #include "../../include/nrnn.h"
 #include "nrnn_internal.h"
 #include "pair.cuh"
@@ -151,23 +153,6 @@ template <int FORM> struct Walk {
         return true;
     }
 };
-
-template <typename T> __device__ __forceinline__ void store_cols(T *p, const float (&v)[PIECE], int n, bool wide) {
-    constexpr int VEC = 16 / sizeof(T);
-    if (wide) {
-#pragma unroll
-        for (int c = 0; c < PIECE; c += VEC) {
-            float o[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) o[e] = v[c + e];
-            if (c < n) store_f32<T, VEC>(p + c, o);
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < PIECE; ++c)
-            if (c < n) p[c] = from_f32<T>(v[c]);
-    }
-}
 
 __device__ __forceinline__ float sigmoid_of(float x) { return rcp_approx(1.f + ex2_approx(-LOG2E * x)); }
 
@@ -377,6 +362,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             }
             return pk;
         };
+        // 32 columns of this warp's 32 rows to `to`, rows of `pitch` elements: by way of the
+        // block, so that a store takes whole lines (each lane its own row: 4.3 us a CTA for
+        // a tile's fp32 parts).  n columns are stored, of `rows` rows; wide: fours at a time
+        auto store_32 = [&](const float *v, auto *to, int64_t pitch, int rows, int n, bool wide) {
+            using O = std::remove_pointer_t<decltype(to)>;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) *place(0, q) = *reinterpret_cast<const uint4 *>(v + 4 * q);
+            __syncwarp();
+            if (wide) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = 4 * k + (lane >> 3), q = lane & 7;
+                    if (r < rows && 4 * q < n) {
+                        float o[4];
+                        load_f32<float, 4>(reinterpret_cast<const float *>(stage_out + r * 128 + 16 * (q ^ (r & 7))), o);
+                        store_f32<O, 4>(to + r * pitch + 4 * q, o);
+                    }
+                }
+            } else {
+#pragma unroll 8
+                for (int r = 0; r < 32; ++r)
+                    if (r < rows && lane < n)
+                        to[r * pitch + lane] = from_f32<O>(
+                            *reinterpret_cast<const float *>(stage_out + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3)));
+            }
+            __syncwarp();
+        };
         // the three planes of a piece, v is used up, to column x, row y, planes z, z + dz, z + 2 dz
         auto store_planes = [&](float (&v)[PIECE], int x, int y, int z, int dz) {
 #pragma unroll
@@ -420,8 +432,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 const int left = min(a.N - t.tn * a.bn, a.bn) - c, n = min(left, PIECE);
                 if (left <= 0) return;
                 if (t.slot >= 0) {
-                    float *to = a.parts + ((static_cast<int64_t>(pair) * 2 + t.slot) * BM + in_tile + lane) * a.bn + c;
-                    store_cols<float>(to, v, PIECE, true);
+                    float *to = a.parts + ((static_cast<int64_t>(pair) * 2 + t.slot) * BM + in_tile) * a.bn + c;
+                    blocks_free();
+                    store_32(v, to, a.bn, 32, 32, true);
+                    store_32(v + 32, to + 32, a.bn, 32, 32, true);
                 } else if (!SPLIT && a.blocks_out) {
                     blocks_free();
 #pragma unroll
@@ -432,10 +446,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                         tma_store_3d(&tmOut, stage_out, t.tn * a.bn + c, y0, second ? 1 : 0);
                         bulk_commit();
                     }
-                } else if (m < a.M) {
-                    const int64_t row = (second ? a.M : 0) + static_cast<int64_t>(m);
-                    const bool wide = a.N % (16 / static_cast<int>(sizeof(T))) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
-                    store_cols<T>(static_cast<T *>(a.out) + row * a.N + t.tn * a.bn + c, v, n, wide);
+                } else if (y0 < a.M) {
+                    T *to = static_cast<T *>(a.out) + ((second ? a.M : 0) + static_cast<int64_t>(y0)) * a.N + t.tn * a.bn + c;
+                    const bool wide = SPLIT && a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+                    blocks_free();
+                    store_32(v, to, a.N, a.M - y0, n, wide);
+                    if (n > 32) store_32(v + 32, to + 32, a.N, a.M - y0, n - 32, wide);
                 }
             };
             if constexpr (SPLIT) {
@@ -466,21 +482,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 if constexpr (FORM == UP) {
                     const int x = t.tn * half_n + odd * PIECE, left = a.N - x;
                     if (mine && left > 0) {
-                        if (a.keep && m < a.M) {
-                            float *p = static_cast<float *>(a.pq) + static_cast<int64_t>(m) * a.pitch + x, *q = p + static_cast<int64_t>(a.M) * a.pitch;
+                        if (a.keep && y0 < a.M) {
+                            float *p = static_cast<float *>(a.pq) + static_cast<int64_t>(y0) * a.pitch + x,
+                                  *q = p + static_cast<int64_t>(a.M) * a.pitch;
+                            blocks_free();
 #pragma unroll
-                            for (int c = 0; c < PIECE; c += 4)
-                                if (c < a.pitch - x) {   // (the pitch is a multiple of 8: whole fours)
-                                    float vp[4], vq[4];
+                            for (int h = 0; h < 2 * PIECE; h += 32) {   // p, then q
+                                float v[32];
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        vp[e] = acc[0][c + e];
-                                        vq[e] = acc[1][c + e];
-                                        gate(vp[e], vq[e]);
-                                    }
-                                    store_f32<float, 4>(p + c, vp);
-                                    store_f32<float, 4>(q + c, vq);
+                                for (int e = 0; e < 32; ++e) {
+                                    float vp = acc[0][h % PIECE + e], vq = acc[1][h % PIECE + e];
+                                    gate(vp, vq);
+                                    v[e] = h < PIECE ? vp : vq;
                                 }
+                                store_32(v, (h < PIECE ? p : q) + h % PIECE, a.pitch, a.M - y0, a.pitch - x - h % PIECE, true);
+                            }
                         }
 #pragma unroll
                         for (int e = 0; e < PIECE; ++e) acc[0][e] = gate(acc[0][e], acc[1][e]);
@@ -647,24 +663,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
 }
 
 // Adds the parts of the tiles that a launch of `pairs` pairs cut, in the order of their
-// slices.  blockIdx.x: a cut tile.  A warp takes a row, 8 columns a lane; with
-// SPLIT_PARTS (few tiles in many parts) the CTA's warps take a share of one row's parts
-// each, and the shares are added in order.
-constexpr int JOIN_WARPS = 8;
+// slices.  blockIdx.x: a cut tile; blockIdx.y: JOIN_ROWS of its rows; a thread takes four
+// columns of a row, its loads eight parts ahead.  (A warp a row and its parts shared by a
+// CTA's warps where they were many: 11 us for 6 tiles in 12 parts, JOIN_MEASURED.)
+constexpr int JOIN_THREADS = 256, JOIN_ROWS = 4;
 
-template <int FORM, typename T, bool SPLIT_PARTS>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a) {
-    __shared__ float share[SPLIT_PARTS ? JOIN_WARPS : 1][BN];
-    dependents_may_launch();
-    wait_for_prerequisites();
-    const int cut = blockIdx.x / a.side, tile = a.whole + cut;
-    if (tile >= a.units) return;
-    const int side_at = blockIdx.x % a.side, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = SPLIT_PARTS ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
+template <int FORM, typename T>
+__global__ void __launch_bounds__(JOIN_THREADS) k_join_parts(const GemmArgs a) {
+    const int cut = blockIdx.x / a.side, tile = a.whole + cut, side_at = blockIdx.x % a.side;
+    const int row = blockIdx.y * JOIN_ROWS + threadIdx.x / (BN / 4), c = threadIdx.x % (BN / 4) * 4;
     const int tm = a.side > 1 ? tile : tile / a.tiles_n, tn = a.side > 1 ? side_at : tile % a.tiles_n;
     const bool second = FORM == GWI && tm >= a.m_half;
     const int m = (second ? tm - a.m_half : tm) * BM + row;
-    if (m >= a.M) return;
     // the runs that hold slices of this tile: b0 .. b1
     const int64_t all = static_cast<int64_t>(a.units - a.whole) * a.kb;
     const int64_t first = static_cast<int64_t>(cut) * a.kb, stop = first + a.kb;
@@ -676,66 +686,69 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_join_parts(const GemmArgs a
         return b;
     };
     const int b0 = run_of(first), b1 = run_of(stop - 1);
-    if (b0 == b1) return;   // one run has it whole
+    const int n = min(min(a.bn, a.N - tn * a.bn) - c, 4);
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (b0 == b1 || m >= a.M || n <= 0) return;   // (one run has it whole)
     const bool dense = all >= a.teams;   // no run is empty
-    const int c = lane * 8;
-    float v[8] = {};
-    if (c < a.bn) {
-        const int64_t step = static_cast<int64_t>(2) * BM * a.bn * a.side;   // to the next team's
-        const float *p = a.parts + b0 * step + (static_cast<int64_t>(side_at) * 2 * BM + row) * a.bn + c;
-        const int q0 = SPLIT_PARTS ? warp : 0, dq = SPLIT_PARTS ? JOIN_WARPS : 1;
-#pragma unroll 4
-        for (int q = q0; q <= b1 - b0; q += dq) {
-            if (!dense) {
+    const int64_t step = static_cast<int64_t>(2) * BM * a.bn * a.side;   // to the next team's
+    const float *p = a.parts + b0 * step + (static_cast<int64_t>(side_at) * 2 * BM + row) * a.bn + c;
+    float v[4] = {};
+    for (int q0 = 0; q0 <= b1 - b0; q0 += 8) {
+        float x[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            bool some = q0 + i <= b1 - b0;
+            if (some && !dense) {
                 int64_t f, to;
-                Walk<FORM>::run(a, b0 + q, f, to);
-                if (f == to) continue;
+                Walk<FORM>::run(a, b0 + q0 + i, f, to);
+                some = f < to;
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
             // the first run's part begins with the tile: slot 1
-            float x[8];
-            load_f32<float, 8>(p + q * step + (q == 0 ? static_cast<int64_t>(BM) * a.bn : 0), x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += x[e];
+            if (some) load_f32<float, 4>(p + (q0 + i) * step + (q0 + i == 0 ? static_cast<int64_t>(BM) * a.bn : 0), x[i]);
         }
-    }
-    if (SPLIT_PARTS) {
-        if (c < a.bn)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) share[warp][c + e] = v[e];
-        __syncthreads();
-        if (warp > 0 || c >= a.bn) return;
-        for (int q = 1; q < JOIN_WARPS; ++q)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += share[q][c + e];
+            for (int e = 0; e < 4; ++e) v[e] += x[i][e];
     }
-    const int n = min(min(a.bn, a.N - tn * a.bn) - c, 8);
-    if (n <= 0) return;
     T *to = static_cast<T *>(a.out) + ((second ? a.M : 0) + static_cast<int64_t>(m)) * a.N + tn * a.bn + c;
-    if (a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 16 / sizeof(T)) {
-            float o[16 / sizeof(T)];
-#pragma unroll
-            for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) o[i] = v[e + i];
-            store_f32<T, 16 / sizeof(T)>(to + e, o);
-        }
+    if (a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(T)) == 0) {
+        store_f32<T, 4>(to, v);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 4; ++e)
             if (e < n) to[e] = from_f32<T>(v[e]);
     }
 }
 
-// rows of src as (planes, rows, pitch) bf16, zeros beyond column d
+// The operands that are not used where they lie as (planes, rows, pitch) bf16, zeros
+// beyond column d, in one launch; it also clears the call's error word.
+struct Copies {
+    const void *src[4];
+    __nv_bfloat16 *to[4];
+    int64_t rows[4];          // 0: none
+    int d[4], pitch[4];
+    uint32_t *error;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256)
-    k_planes(const T *src, __nv_bfloat16 *out, int64_t rows, int d, int pitch) {
+__global__ void __launch_bounds__(256) k_planes(const Copies c) {
     dependents_may_launch();
     wait_for_prerequisites();
-    const bool wide = wide_rows<T>(src, d);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *c.error = 0;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps)
-        copy_row<T>(src + r * d, out + r * pitch, rows * pitch, d, pitch, threadIdx.x & 31, wide);
+    int64_t r = blockIdx.x * 8 + (threadIdx.x >> 5);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool wide = wide_rows<T>(c.src[i], c.d[i]);
+        for (; r < c.rows[i]; r += warps)
+            copy_row<T>(static_cast<const T *>(c.src[i]) + r * c.d[i], c.to[i] + r * c.pitch[i], c.rows[i] * c.pitch[i], c.d[i],
+                        c.pitch[i], threadIdx.x & 31, wide);
+        r -= c.rows[i];
+    }
 }
 
 // ---------------------------------------------------------------- few rows
@@ -924,8 +937,16 @@ bool used_in_place(const void *p, int64_t row, int dtype) {
     return dtype == NRNN_BF16 && row % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// columns of a tile of a plain product: equal tiles of whole 64-column blocks
-int tile_columns(int64_t N) { return static_cast<int>(ceil_div(ceil_div(N, ceil_div(N, BN)), 64) * 64); }
+// columns of a tile: equal tiles of whole 64-column blocks, `most` at most
+int tile_columns(int64_t N, int most = BN) { return static_cast<int>(ceil_div(ceil_div(N, ceil_div(N, most)), 64) * 64); }
+
+// The same, narrower where there are few tiles: down to one a pair for tiles that are not
+// cut (share 1), or half of one for those that are (2): then each is cut into fewer parts.
+// COLUMNS_MEASURED
+int tile_columns_for(int64_t tiles_m, int64_t N, int share, int most = BN) {
+    while (most > 64 && tiles_m * ceil_div(N, most) * share <= PAIRS) most /= 2;
+    return tile_columns(N, most);
+}
 
 Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in_lies, bool w_out_lies, bool g_lies,
               bool keep, bool backward) {
@@ -955,16 +976,31 @@ Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in
     return p;
 }
 
-// an operand as bf16 planes: where it lies, or its copy
+// the operands as bf16 planes: where they lie, or their copies; clears the error word
 template <typename T>
-cudaError_t operand(const Call &c, const void *src, size_t copy, int64_t rows, int64_t d, int64_t pitch, const void **out) {
-    *out = src;
-    if (copy == NO_COPY) return cudaSuccess;
-    __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(c.ws + copy);
-    *out = to;
+cudaError_t operands(const Call &c, const Plan &p, const void *g_in, const void **x, const void **w_in, const void **w_out,
+                     const void **g) {
+    Copies k{};
+    k.error = reinterpret_cast<uint32_t *>(c.ws);
+    int64_t rows = 0;
+    int n = 0;
+    auto take = [&](const void *src, size_t copy, int64_t r, int64_t d, int64_t pitch) -> const void * {
+        if (copy == NO_COPY) return src;
+        k.src[n] = src;
+        k.to[n] = reinterpret_cast<__nv_bfloat16 *>(c.ws + copy);
+        k.rows[n] = r;
+        k.d[n] = static_cast<int>(d);
+        k.pitch[n] = static_cast<int>(pitch);
+        rows += r;
+        return k.to[n++];
+    };
+    *x = take(c.x, p.x, c.n, c.d, p.pd);
+    *w_in = take(c.W_in, p.w_in, 2 * c.f, c.d, p.pd);
+    *w_out = take(c.W_out, p.w_out, c.d, c.f, p.pf);
+    if (g != nullptr) *g = take(g_in, p.g, c.n, c.d, p.pd);
+    if (rows == 0) return cudaMemsetAsync(k.error, 0, sizeof(uint32_t), c.stream);
     const int64_t b = ceil_div(rows, 8);
-    return launch_dependent(k_planes<T>, static_cast<unsigned>(b < 4864 ? b : 4864), 256, 0, c.stream,
-                            static_cast<const T *>(src), to, rows, static_cast<int>(d), static_cast<int>(pitch));
+    return launch_dependent(k_planes<T>, static_cast<unsigned>(b < 4864 ? b : 4864), 256, 0, c.stream, k);
 }
 
 template <int FORM, typename T>
@@ -993,17 +1029,16 @@ cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, 
     e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, tmPQ, a);
     const int64_t cut = static_cast<int64_t>(a.units - a.whole) * a.side;
     if (e == cudaSuccess && cut > 0) {
-        const bool few = cut * 8 <= pairs;   // eight parts each and more
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(cut), few ? BM : BM / JOIN_WARPS);
-        cfg.blockDim = dim3(JOIN_WARPS * 32);
+        cfg.gridDim = dim3(static_cast<unsigned>(cut), BM / JOIN_ROWS);
+        cfg.blockDim = dim3(JOIN_THREADS);
         cfg.stream = c.stream;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, few ? k_join_parts<FORM, T, true> : k_join_parts<FORM, T, false>, a);
+        e = cudaLaunchKernelEx(&cfg, k_join_parts<FORM, T>, a);
     }
     return e;
 }
@@ -1030,14 +1065,9 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
     const Kept kl = kept_layout(c.n, c.f, c.dtype);
     unsigned char *m = kept + kl.m;
     const void *x, *w_in, *w_out;
-    if (cudaMemsetAsync(c.ws, 0, sizeof(uint32_t), c.stream) != cudaSuccess ||
-        operand<T>(c, c.x, p.x, c.n, c.d, p.pd, &x) != cudaSuccess ||
-        operand<T>(c, c.W_in, p.w_in, 2 * c.f, c.d, p.pd, &w_in) != cudaSuccess ||
-        operand<T>(c, c.W_out, p.w_out, c.d, c.f, p.pf, &w_out) != cudaSuccess)
-        return NRNN_ERR_CUDA;
+    if (operands<T>(c, p, nullptr, &x, &w_in, &w_out, nullptr) != cudaSuccess) return NRNN_ERR_CUDA;
     CUtensorMap ta, tb, to, tpq;
-    // UP: equal tiles of the units, in whole 64-unit blocks
-    const int units = static_cast<int>(ceil_div(ceil_div(c.f, ceil_div(c.f, BN / 2)), 64) * 64);
+    const int units = tile_columns_for(ceil_div(c.n, BM), c.f, 1, BN / 2);   // UP: a tile's units
     if (!map(&ta, x, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, BK, units) ||
         !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS) || (p.planes == 1 && !map(&tpq, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
@@ -1048,7 +1078,7 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
     a.pq = kept;
     a.pitch = static_cast<int>(p.pf);
     if (gemm<UP, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
-    const int bn = tile_columns(c.d);
+    const int bn = tile_columns_for(ceil_div(c.n, BM), c.d, 2);
     a = args_of(c, c.n, c.d, c.f, bn);
     a.parts = reinterpret_cast<float *>(c.ws + p.parts);
     a.out = y;
@@ -1065,17 +1095,11 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     const unsigned char *m = kept + kl.m;
     unsigned char *gab = c.ws + p.gab;
     const void *x, *w_in, *w_out, *g;
-    if (cudaMemsetAsync(c.ws, 0, sizeof(uint32_t), c.stream) != cudaSuccess ||
-        operand<T>(c, c.x, p.x, c.n, c.d, p.pd, &x) != cudaSuccess ||
-        operand<T>(c, c.W_in, p.w_in, 2 * c.f, c.d, p.pd, &w_in) != cudaSuccess ||
-        operand<T>(c, c.W_out, p.w_out, c.d, c.f, p.pf, &w_out) != cudaSuccess ||
-        operand<T>(c, g_, p.g, c.n, c.d, p.pd, &g) != cudaSuccess)
-        return NRNN_ERR_CUDA;
+    if (operands<T>(c, p, g_, &x, &w_in, &w_out, &g) != cudaSuccess) return NRNN_ERR_CUDA;
     CUtensorMap ta, tb, to, tpq;
     float *parts = reinterpret_cast<float *>(c.ws + p.parts);
     // fp32: one piece of an epilogue warp holds ga and gb, so tiles of 128
-    int bn = tile_columns(c.f);
-    if (p.planes != 1 && bn > 2 * PIECE) bn = 2 * PIECE;
+    int bn = tile_columns_for(ceil_div(c.n, BM), c.f, 1, p.planes != 1 ? 2 * PIECE : BN);
     GemmArgs a = args_of(c, c.n, c.f, c.d, bn);
     a.pq = const_cast<unsigned char *>(kept);
     a.pitch = static_cast<int>(p.pf);
@@ -1086,7 +1110,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     if (p.planes != 1) tpq = to;
     if (gemm<DH, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gx
-    bn = tile_columns(c.d);
+    bn = tile_columns_for(ceil_div(c.n, BM), c.d, 2);
     a = args_of(c, c.n, c.d, c.f, bn);
     a.kb_half = a.kb;
     a.kb *= 2;
@@ -1098,6 +1122,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
         return NRNN_ERR_CUDA;
     if (gemm<GX, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_in
+    bn = tile_columns_for(2 * ceil_div(c.f, BM), c.d, 2);
     a = args_of(c, c.f, c.d, c.n, bn);
     a.m_half = a.tiles_m;
     a.tiles_m *= 2;
@@ -1109,7 +1134,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
         return NRNN_ERR_CUDA;
     if (gemm<GWI, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_out
-    bn = tile_columns(c.f);
+    bn = tile_columns_for(ceil_div(c.d, BM), c.f, 2);
     a = args_of(c, c.d, c.f, c.n, bn);
     a.parts = parts;
     a.out = gW_out;
