@@ -142,14 +142,15 @@ def linear_recurrence_step(params, state: torch.Tensor | None, preact: torch.Ten
 
 def _mlp_args(x, W_in, W_out):
     x, W_in, W_out = _device_tensor(x, "x"), _device_tensor(W_in, "W_in"), _device_tensor(W_out, "W_out")
-    if x.dim() < 1 or W_out.dim() != 2 or W_out.shape[0] != x.shape[-1] \
-            or tuple(W_in.shape) != (2 * W_out.shape[1], x.shape[-1]):
+    if x.dim() < 1 or W_out.dim() != 2:
+        raise ValueError("x must have shape (..., d), W_in (2 f, d) and W_out (d, f)")
+    d, f = W_out.shape
+    if x.shape[-1] != d or W_in.shape != (2 * f, d):
         raise ValueError("x must have shape (..., d), W_in (2 f, d) and W_out (d, f)")
     if x.dtype != W_in.dtype or x.dtype != W_out.dtype:
         raise TypeError("x, W_in and W_out must share a dtype")
     _with(x, W_in, "W_in")
     _with(x, W_out, "W_out")
-    d, f = W_out.shape
     if d == 0 or f == 0:
         raise ValueError("d and f must be positive")
     return x, W_in, W_out, _storage(x), x.numel() // d, d, f
@@ -163,7 +164,7 @@ def gated_mlp(x: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, keep: bo
     gated_mlp_backward takes."""
     x, W_in, W_out, code, rows, d, f = _mlp_args(x, W_in, W_out)
     lib = load()
-    y = _result(out, x.shape, x, "out")
+    y = torch.empty_like(x) if out is None else _result(out, x.shape, x, "out")
     nbytes = lib.nrnn_gated_mlp_workspace_bytes(rows, d, f, code, 2 if keep else 0)
     kept = None
     if keep:
@@ -212,7 +213,7 @@ def dropout(x: torch.Tensor, p: float, seed, offset: int = 0, residual: torch.Te
         if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != x.device:
             raise ValueError(f"a seed tensor must be int64, of one element and on {x.device}")
         at, seed = seed.data_ptr(), 0
-    y = _result(out, x.shape, x, "out")
+    y = torch.empty_like(x) if out is None else _result(out, x.shape, x, "out")
     _run("dropout", load().nrnn_dropout, x, x.data_ptr(), code, x.numel(), float(p), int(seed) & (1 << 64) - 1,
          at, int(offset) & (1 << 64) - 1, _at(residual), y.data_ptr())
     return y

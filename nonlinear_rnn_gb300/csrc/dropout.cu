@@ -37,62 +37,74 @@ struct DropArgs {
     int64_t n;
     uint64_t seed, offset;
     const uint64_t *seed_at;   // device; null: seed
-    uint64_t limit;            // keep a word >= limit; 2^32: none
+    uint32_t limit;            // keep a word >= limit
     float scale;
 };
 
 constexpr int DROP_THREADS = 256;
 
-// VEC elements a thread: 16 bytes where all tensors are aligned to them, else one
-template <typename T, int VEC>
+__device__ __forceinline__ float dropped(uint32_t word, const DropArgs &a, float x, float r) {
+    return word >= a.limit ? fmaf(x, a.scale, r) : r;
+}
+
+// A thread takes groups of 16 bytes where all tensors are aligned to them (WIDE), else of
+// four elements, whose words one Philox block gives.
+template <typename T, bool WIDE, bool RESIDUAL>
 __global__ void __launch_bounds__(DROP_THREADS) k_dropout(const DropArgs a) {
+    constexpr int GROUP = WIDE ? 16 / sizeof(T) : 4;
     dependents_may_launch();
     wait_for_prerequisites();
     const uint64_t seed = a.seed_at != nullptr ? *a.seed_at : a.seed;
     const uint2 key = make_uint2(static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32));
     const T *x = static_cast<const T *>(a.x), *residual = static_cast<const T *>(a.residual);
     T *out = static_cast<T *>(a.out);
-    constexpr int GROUP = VEC < 4 ? 4 : VEC;
-    const int64_t groups = (a.n + GROUP - 1) / GROUP;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * DROP_THREADS;
-    for (int64_t g = static_cast<int64_t>(blockIdx.x) * DROP_THREADS + threadIdx.x; g < groups; g += step) {
-        const int64_t e0 = g * GROUP;
-        uint32_t word[GROUP];
+    const int64_t whole = WIDE ? a.n / GROUP : 0;   // groups that are loaded and stored at once
+    const int64_t threads = static_cast<int64_t>(gridDim.x) * DROP_THREADS;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * DROP_THREADS + threadIdx.x;
+    for (int64_t g = first; g < whole; g += threads) {
+        Pack<T, GROUP> r{};
+        const Pack<T, GROUP> v = *reinterpret_cast<const Pack<T, GROUP> *>(x + g * GROUP);   // under way while the words are made
+        if (RESIDUAL) r = *reinterpret_cast<const Pack<T, GROUP> *>(residual + g * GROUP);
+        float o[GROUP];
 #pragma unroll
-        for (int q = 0; q < GROUP / 4; ++q) {
-            const uint4 w = philox(static_cast<uint64_t>(e0 / 4 + q), a.offset, key);
-            word[4 * q] = w.x;
-            word[4 * q + 1] = w.y;
-            word[4 * q + 2] = w.z;
-            word[4 * q + 3] = w.w;
+        for (int q = 0; q < GROUP; q += 4) {
+            const uint4 w4 = philox(static_cast<uint64_t>(g * (GROUP / 4) + q / 4), a.offset, key);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[q + e] = dropped(w[e], a, to_f32(v.v[q + e]), to_f32(r.v[q + e]));
         }
-        if (VEC > 1 && e0 + GROUP <= a.n) {
-            float v[GROUP], r[GROUP] = {};
-            load_f32<T, GROUP>(x + e0, v);
-            if (residual != nullptr) load_f32<T, GROUP>(residual + e0, r);
+        store_f32<T, GROUP>(out + g * GROUP, o);
+    }
+    // the rest, four elements at a time (a whole group is a multiple of four)
+    const int64_t quads = (a.n + 3) / 4;
+    for (int64_t b = whole * (GROUP / 4) + first; b < quads; b += threads) {
+        const uint4 w4 = philox(static_cast<uint64_t>(b), a.offset, key);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        float v[4], r[4];
 #pragma unroll
-            for (int e = 0; e < GROUP; ++e) v[e] = word[e] >= a.limit ? fmaf(v[e], a.scale, r[e]) : r[e];
-            store_f32<T, GROUP>(out + e0, v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < GROUP; ++e)
-                if (e0 + e < a.n) {
-                    const float r = residual != nullptr ? to_f32(residual[e0 + e]) : 0.f;
-                    out[e0 + e] = from_f32<T>(word[e] >= a.limit ? fmaf(to_f32(x[e0 + e]), a.scale, r) : r);
-                }
+        for (int e = 0; e < 4; ++e) {
+            const bool in = b * 4 + e < a.n;
+            v[e] = in ? to_f32(x[b * 4 + e]) : 0.f;
+            r[e] = in && RESIDUAL ? to_f32(residual[b * 4 + e]) : 0.f;
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (b * 4 + e < a.n) out[b * 4 + e] = from_f32<T>(dropped(w[e], a, v[e], r[e]));
     }
 }
 
 template <typename T>
 cudaError_t dropout(const DropArgs &a, cudaStream_t s) {
-    constexpr int VEC = 16 / sizeof(T);
     const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
                         reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
-    const int64_t groups = (a.n + (wide ? VEC : 4) - 1) / (wide ? VEC : 4), want = (groups + DROP_THREADS - 1) / DROP_THREADS;
+    const int64_t per_block = DROP_THREADS * (wide ? 16 / static_cast<int64_t>(sizeof(T)) : 4);
+    const int64_t want = (a.n + per_block - 1) / per_block;
     const unsigned blocks = static_cast<unsigned>(want < 152 * 64 ? want : 152 * 64);
-    return wide ? launch_dependent(k_dropout<T, VEC>, blocks, DROP_THREADS, 0, s, a)
-                : launch_dependent(k_dropout<T, 1>, blocks, DROP_THREADS, 0, s, a);
+    if (a.residual != nullptr)
+        return wide ? launch_dependent(k_dropout<T, true, true>, blocks, DROP_THREADS, 0, s, a)
+                    : launch_dependent(k_dropout<T, false, true>, blocks, DROP_THREADS, 0, s, a);
+    return wide ? launch_dependent(k_dropout<T, true, false>, blocks, DROP_THREADS, 0, s, a)
+                : launch_dependent(k_dropout<T, false, false>, blocks, DROP_THREADS, 0, s, a);
 }
 
 }  // namespace
@@ -117,9 +129,17 @@ extern "C" int nrnn_dropout(const void *x, int dtype, int64_t n, double p, uint6
     DropArgs a{};
     a.x = x; a.residual = residual; a.out = out; a.n = n;
     a.seed = seed; a.seed_at = seed_device; a.offset = offset;
-    a.limit = static_cast<uint64_t>(std::nearbyint(p * 4294967296.0));
-    a.scale = p < 1.0 ? static_cast<float>(1.0 / (1.0 - p)) : 0.f;
-    const cudaError_t e = dtype == NRNN_BF16 ? dropout<__nv_bfloat16>(a, static_cast<cudaStream_t>(stream))
-                                             : dropout<float>(a, static_cast<cudaStream_t>(stream));
+    const double limit = std::nearbyint(p * 4294967296.0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (limit >= 4294967296.0) {   // nothing is kept
+        if (residual == nullptr) e = cudaMemsetAsync(out, 0, bytes, s);
+        else if (out != residual) e = cudaMemcpyAsync(out, residual, bytes, cudaMemcpyDeviceToDevice, s);
+        return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    }
+    a.limit = static_cast<uint32_t>(limit);
+    a.scale = static_cast<float>(1.0 / (1.0 - p));
+    e = dtype == NRNN_BF16 ? dropout<__nv_bfloat16>(a, s)
+                                             : dropout<float>(a, s);
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }

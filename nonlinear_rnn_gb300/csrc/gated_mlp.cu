@@ -752,15 +752,154 @@ __global__ void __launch_bounds__(256) k_planes(const Copies c) {
 }
 
 // ---------------------------------------------------------------- few rows
-// A decode step's rows (nothing kept): the weights are read once, on the fp32 cores, and
-// m stays fp32.  A warp of k_few_up takes UP_UNITS units at a time, the rows of Wg and
-// Wu of each against every row of x from shared memory; a CTA of k_few_down takes
-// DOWN_ROWS rows of W_out, its warps a share of the inner dimension each, and has its
-// first weights under way before it waits for m.  Bound by HBM and, at this size, by
-// latency: 8 rows over 1024 x 4096 bf16 (25 MB, 3.7 us) FEW_MEASURED
-constexpr int FEW_MOST = 16, FEW_THREADS = 256, UP_UNITS = 2, FEW_AHEAD = 4;
+// The rows of a decode step (nothing kept): the weights are read once, and the time is
+// their bytes' and latency.  m stays fp32, or two bf16 planes of it (2^-16).
+//
+// bf16 of aligned rows, up to SHORT_MOST rows of x: the weights' rows are the 16 rows of
+// mma.sync products (the 128 rows of tcgen05 would leave most SMs without a tile: 27 us
+// for 8 rows over 1024 x 4096).  A lane takes 16 bytes, 8 inner elements, of a row at a
+// time, of the weights and of x alike: inner elements may be summed in any order, so
+// these are the fragments of two products as they lie.  k_short_up: the 16 rows are 8
+// units' rows of Wg and of Wu, so a lane ends with a and b of the same unit and row of x;
+// a CTA's warps share the inner dimension.  k_short_down has its first weights under way
+// before it waits for m.  SHORT_MEASURED
+constexpr int SHORT_MOST = 16, SHORT_AHEAD = 4, UP_WARPS = 8, DOWN_WARPS = 16;
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 32 inner elements of 16 rows (lo: this lane's of rows 0..7, hi: 8..15) and 8 columns
+__device__ __forceinline__ void mma_32(float (&c)[4], const uint4 &lo, const uint4 &hi, const uint4 &b) {
+    mma_16x8x16(c, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+    mma_16x8x16(c, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+}
+
+// TILES: groups of 8 rows of x
+template <int TILES>
+__global__ void __launch_bounds__(UP_WARPS * 32)
+    k_short_up(const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__restrict__ W, __nv_bfloat16 *__restrict__ m,
+               uint32_t *error, int n, int d, int f) {
+    __shared__ float share[UP_WARPS][TILES][16][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, k0 = lane % 4 * 8, j0 = blockIdx.x * 8;
+    wait_for_prerequisites();
+    dependents_may_launch();   // (after the wait: the next kernel reads weights before its own)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *error = 0;
+    const __nv_bfloat16 *gate_row = W + static_cast<int64_t>(min(j0 + row, f - 1)) * d + k0,
+                        *up_row = gate_row + static_cast<int64_t>(f) * d;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float c[TILES][4] = {};
+    for (int k = warp * 32; k < d; k += UP_WARPS * 32 * SHORT_AHEAD) {
+        uint4 lo[SHORT_AHEAD], hi[SHORT_AHEAD], b[SHORT_AHEAD][TILES];
+#pragma unroll
+        for (int i = 0; i < SHORT_AHEAD; ++i) {
+            const int at = k + i * UP_WARPS * 32;
+            const bool in = at + k0 < d;   // (d is a multiple of 8)
+            lo[i] = in ? *reinterpret_cast<const uint4 *>(gate_row + at) : zero;
+            hi[i] = in ? *reinterpret_cast<const uint4 *>(up_row + at) : zero;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+                b[i][t] = in && t * 8 + row < n
+                              ? *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(t * 8 + row) * d + k0 + at) : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < SHORT_AHEAD; ++i)
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) mma_32(c[t], lo[i], hi[i], b[i][t]);
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+        *reinterpret_cast<float2 *>(&share[warp][t][row][lane % 4 * 2]) = make_float2(c[t][0], c[t][1]);
+        *reinterpret_cast<float2 *>(&share[warp][t][row + 8][lane % 4 * 2]) = make_float2(c[t][2], c[t][3]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < TILES * 64; i += UP_WARPS * 32) {
+        const int unit = i % 8, col = i / 8 % 8, t = i / 64, r = t * 8 + col;   // r: row of x
+        float va = 0.f, vb = 0.f;
+#pragma unroll
+        for (int w = 0; w < UP_WARPS; ++w) {
+            va += share[w][t][unit][col];
+            vb += share[w][t][unit + 8][col];
+        }
+        if (r < n && j0 + unit < f) {
+            const float v = gate(va, vb);
+            const __nv_bfloat16 h = __float2bfloat16_rn(v);
+            const int64_t to = static_cast<int64_t>(r) * f + j0 + unit;
+            m[to] = h;
+            m[to + static_cast<int64_t>(n) * f] = __float2bfloat16_rn(v - __bfloat162float(h));
+        }
+    }
+}
+
+template <int TILES>
+__global__ void __launch_bounds__(DOWN_WARPS * 32)
+    k_short_down(const __nv_bfloat16 *__restrict__ m, const __nv_bfloat16 *__restrict__ W, __nv_bfloat16 *__restrict__ y,
+                 int n, int d, int f) {
+    __shared__ float share[DOWN_WARPS][TILES][16][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, k0 = lane % 4 * 8, j0 = blockIdx.x * 16;
+    const __nv_bfloat16 *low = W + static_cast<int64_t>(min(j0 + row, d - 1)) * f + k0,
+                        *high = W + static_cast<int64_t>(min(j0 + row + 8, d - 1)) * f + k0;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 lo[SHORT_AHEAD], hi[SHORT_AHEAD];
+    int k = warp * 32;
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < SHORT_AHEAD; ++i) {
+            const int at = k + i * DOWN_WARPS * 32;
+            const bool in = at + k0 < f;
+            lo[i] = in ? *reinterpret_cast<const uint4 *>(low + at) : zero;
+            hi[i] = in ? *reinterpret_cast<const uint4 *>(high + at) : zero;
+        }
+    };
+    fetch();   // the kernel before writes no weights, and those before it are done
+    wait_for_prerequisites();
+    dependents_may_launch();
+    float c[TILES][4] = {};
+    const int64_t plane = static_cast<int64_t>(n) * f;
+    while (k < f) {
+#pragma unroll
+        for (int i = 0; i < SHORT_AHEAD; ++i) {
+            const int at = k + i * DOWN_WARPS * 32;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                const bool in = at + k0 < f && t * 8 + row < n;
+                const __nv_bfloat16 *from = m + static_cast<int64_t>(t * 8 + row) * f + k0 + at;
+                const uint4 b = in ? *reinterpret_cast<const uint4 *>(from) : zero;
+                const uint4 b_low = in ? *reinterpret_cast<const uint4 *>(from + plane) : zero;
+                mma_32(c[t], lo[i], hi[i], b_low);
+                mma_32(c[t], lo[i], hi[i], b);
+            }
+        }
+        k += DOWN_WARPS * 32 * SHORT_AHEAD;
+        if (k < f) fetch();
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+        *reinterpret_cast<float2 *>(&share[warp][t][row][lane % 4 * 2]) = make_float2(c[t][0], c[t][1]);
+        *reinterpret_cast<float2 *>(&share[warp][t][row + 8][lane % 4 * 2]) = make_float2(c[t][2], c[t][3]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < TILES * 128; i += DOWN_WARPS * 32) {
+        const int j = i % 16, col = i / 16 % 8, t = i / 128, r = t * 8 + col;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < DOWN_WARPS; ++w) v += share[w][t][j][col];
+        if (r < n && j0 + j < d) y[static_cast<int64_t>(r) * d + j0 + j] = __float2bfloat16_rn(v);
+    }
+}
+
+// Other types and rows: on the fp32 cores, in groups of FEW_GROUP rows that read the
+// weights again, from L2; one group of bf16, FEW_MOST rows of fp32, whose weights'
+// planes would be more to write and read.  A warp of k_few_up takes
+// UP_UNITS units at a time, the rows of Wg and Wu of each against every row of x from
+// shared memory; a CTA of k_few_down takes DOWN_ROWS rows of W_out, its warps a share of
+// the inner dimension each.  FEW_MEASURED
+constexpr int FEW_GROUP = 8, FEW_MOST = 64, FEW_THREADS = 256, UP_UNITS = 2, FEW_AHEAD = 2;
 constexpr size_t FEW_X_BYTES = 96 * 1024;   // of the rows of x in shared memory
-template <int N> constexpr int DOWN_ROWS = N > 8 ? 4 : 8;
+constexpr int DOWN_ROWS = 4;
 
 // Sums over the lanes of V values each: halves are exchanged and added, until lane l has
 // value l V / 32 (and, of 64, the next one), 32 / V lanes the same one.
@@ -782,23 +921,40 @@ template <int V> __device__ __forceinline__ void sums_to_lanes(float (&z)[V], in
     }
 }
 
+// sum += <w, x>, even and odd products in its two halves
+template <typename T, int VEC> __device__ __forceinline__ void dot(const Pack<T, VEC> &w, const float (&x)[VEC], float2 &sum) {
+    if constexpr (VEC == 1) {
+        sum.x = fmaf(to_f32(w.v[0]), x[0], sum.x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2)
+            sum = fma2(make_float2(to_f32(w.v[i]), to_f32(w.v[i + 1])), make_float2(x[i], x[i + 1]), sum);
+    }
+}
+
 template <typename T, int N, int VEC>
-__global__ void __launch_bounds__(FEW_THREADS)
+__global__ void __launch_bounds__(FEW_THREADS, 2)
     k_few_up(const T *__restrict__ x, const T *__restrict__ W, float *__restrict__ m, uint32_t *error, int n, int d, int f) {
     extern __shared__ __align__(32) float few_x[];   // [N][pitch], zeros past n and d
-    constexpr int CHUNK = 32 * VEC, ROWS = 2 * UP_UNITS, AHEAD = N > 8 ? 2 : FEW_AHEAD;
+    constexpr int CHUNK = 32 * VEC, ROWS = 2 * UP_UNITS, AHEAD = FEW_AHEAD;
     const int pitch = (d + CHUNK - 1) / CHUNK * CHUNK, lane = threadIdx.x & 31;
     wait_for_prerequisites();
     dependents_may_launch();   // (after the wait: the next kernel reads weights before its own)
-    if (blockIdx.x == 0 && threadIdx.x == 0) *error = 0;
-    for (int i = threadIdx.x; i < N * pitch; i += FEW_THREADS) {
-        const int r = i / pitch, c = i - r * pitch;
-        few_x[i] = r < n && c < d ? to_f32(x[static_cast<int64_t>(r) * d + c]) : 0.f;
-    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *error = 0;
+    x += static_cast<int64_t>(blockIdx.y) * N * d;
+    m += static_cast<int64_t>(blockIdx.y) * N * f;
+    n = min(n - static_cast<int>(blockIdx.y) * N, N);
+    for (int r = threadIdx.x >> 5; r < N; r += FEW_THREADS / 32)
+#pragma unroll 4
+        for (int c = lane * VEC; c < pitch; c += CHUNK) {   // (d is a multiple of VEC)
+            float v[VEC] = {};
+            if (r < n && c < d) load_f32<T, VEC>(x + static_cast<int64_t>(r) * d + c, v);
+            store_f32<float, VEC>(few_x + r * pitch + c, v);
+        }
     __syncthreads();
     const int warps = gridDim.x * (FEW_THREADS / 32);
     for (int j0 = (blockIdx.x * (FEW_THREADS / 32) + (threadIdx.x >> 5)) * UP_UNITS; j0 < f; j0 += warps * UP_UNITS) {
-        float acc[N * ROWS] = {};   // [row of x][unit][Wg, Wu]
+        float2 sum[N * ROWS] = {};   // [row of x][unit][Wg, Wu]
         const T *at[ROWS];
 #pragma unroll
         for (int q = 0; q < ROWS; ++q) {
@@ -820,14 +976,14 @@ __global__ void __launch_bounds__(FEW_THREADS)
                         float xv[VEC];
                         load_f32<float, VEC>(few_x + r * pitch + c0 + e * CHUNK, xv);
 #pragma unroll
-                        for (int q = 0; q < ROWS; ++q)
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i)
-                                acc[r * ROWS + q] = fmaf(to_f32(w[e][q].v[i]), xv[i], acc[r * ROWS + q]);
+                        for (int q = 0; q < ROWS; ++q) dot<T, VEC>(w[e][q], xv, sum[r * ROWS + q]);
                     }
         }
-        sums_to_lanes(acc, lane);
         constexpr int V = N * ROWS;
+        float acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = sum[i].x + sum[i].y;
+        sums_to_lanes(acc, lane);
         float a = acc[0], b;
         if constexpr (V == 64) b = acc[1];
         else b = __shfl_xor_sync(FULL_MASK, a, 32 / V);
@@ -839,9 +995,9 @@ __global__ void __launch_bounds__(FEW_THREADS)
 }
 
 template <typename T, int N, int VEC>
-__global__ void __launch_bounds__(FEW_THREADS)
+__global__ void __launch_bounds__(FEW_THREADS, 2)
     k_few_down(const float *__restrict__ m, const T *__restrict__ W, T *__restrict__ y, int n, int d, int f) {
-    constexpr int CHUNK = 32 * VEC, WARPS = FEW_THREADS / 32, ROWS = DOWN_ROWS<N>, V = N * ROWS;
+    constexpr int CHUNK = 32 * VEC, WARPS = FEW_THREADS / 32, ROWS = DOWN_ROWS, V = N * ROWS;
     __shared__ float share[WARPS][V];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j0 = blockIdx.x * ROWS;
     const T *at[ROWS];
@@ -857,7 +1013,10 @@ __global__ void __launch_bounds__(FEW_THREADS)
     fetch();   // the kernel before writes no weights, and those before it are done
     wait_for_prerequisites();
     dependents_may_launch();
-    float acc[V] = {};   // [row][column of y]
+    m += static_cast<int64_t>(blockIdx.y) * N * f;
+    y += static_cast<int64_t>(blockIdx.y) * N * d;
+    n = min(n - static_cast<int>(blockIdx.y) * N, N);
+    float2 sum[V] = {};   // [row][column of y]
     while (c < f) {
         Pack<T, VEC> now[ROWS];
 #pragma unroll
@@ -871,11 +1030,12 @@ __global__ void __launch_bounds__(FEW_THREADS)
                 float mv[VEC];
                 load_f32<float, VEC>(m + static_cast<int64_t>(r) * f + at_m, mv);
 #pragma unroll
-                for (int q = 0; q < ROWS; ++q)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) acc[r * ROWS + q] = fmaf(to_f32(now[q].v[i]), mv[i], acc[r * ROWS + q]);
+                for (int q = 0; q < ROWS; ++q) dot<T, VEC>(now[q], mv, sum[r * ROWS + q]);
             }
     }
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = sum[i].x + sum[i].y;
     sums_to_lanes(acc, lane);
     if constexpr (V == 64) {
         share[warp][2 * lane] = acc[0];
@@ -885,11 +1045,11 @@ __global__ void __launch_bounds__(FEW_THREADS)
     }
     __syncthreads();
     if (threadIdx.x < V) {
-        float sum = share[0][threadIdx.x];
+        float all = share[0][threadIdx.x];
 #pragma unroll
-        for (int k = 1; k < WARPS; ++k) sum += share[k][threadIdx.x];
+        for (int k = 1; k < WARPS; ++k) all += share[k][threadIdx.x];
         const int r = threadIdx.x / ROWS, j = j0 + threadIdx.x % ROWS;
-        if (r < n && j < d) y[static_cast<int64_t>(r) * d + j] = from_f32<T>(sum);
+        if (r < n && j < d) y[static_cast<int64_t>(r) * d + j] = from_f32<T>(all);
     }
 }
 
@@ -897,11 +1057,13 @@ __global__ void __launch_bounds__(FEW_THREADS)
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// rows that the few-rows form is built for, and whether a call takes it: x has to fit in
-// shared memory
-int few_size(int64_t n) { return n <= 1 ? 1 : n <= 4 ? 4 : n <= 8 ? 8 : FEW_MOST; }
-bool few_rows(int64_t n, int64_t d) {
-    return n <= FEW_MOST && few_size(n) * (d + 255) * 4 <= static_cast<int64_t>(FEW_X_BYTES);
+// The forms for few rows.  FEW: x has to fit in shared memory.
+int few_size(int64_t n) { return n <= 1 ? 1 : n <= 4 ? 4 : FEW_GROUP; }   // rows it is built for
+bool few_rows(int64_t n, int64_t d, int dtype) {
+    return n <= (dtype == NRNN_F32 ? FEW_MOST : FEW_GROUP) && few_size(n) * (d + 255) * 4 <= static_cast<int64_t>(FEW_X_BYTES);
+}
+bool short_rows(int64_t n, int64_t d, int64_t f, int dtype, bool aligned) {
+    return dtype == NRNN_BF16 && n <= SHORT_MOST && d % 8 == 0 && f % 8 == 0 && aligned;
 }
 
 struct Call {
@@ -951,10 +1113,6 @@ int tile_columns_for(int64_t tiles_m, int64_t N, int share, int most = BN) {
 Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in_lies, bool w_out_lies, bool g_lies,
               bool keep, bool backward) {
     Plan p{};
-    if (!keep && !backward && few_rows(n, d)) {   // m alone
-        p.total = up256(256 + sizeof(float) * n * f);
-        return p;
-    }
     p.planes = dtype == NRNN_F32 ? 3 : 1;
     p.pd = ceil_div(d, 8) * 8;
     p.pf = ceil_div(f, 8) * 8;
@@ -1157,17 +1315,29 @@ cudaError_t launch_few(const Call &c, T *y) {
     const int n = static_cast<int>(c.n), d = static_cast<int>(c.d), f = static_cast<int>(c.f);
     const size_t smem = sizeof(float) * N * (ceil_div(d, 32 * VEC_UP) * 32 * VEC_UP);
     const int64_t want = ceil_div(f, UP_UNITS * (FEW_THREADS / 32));
-    e = launch_dependent(k_few_up<T, N, VEC_UP>, static_cast<unsigned>(want < 304 ? want : 304), FEW_THREADS, smem, c.stream,
-                         static_cast<const T *>(c.x), static_cast<const T *>(c.W_in), m,
-                         reinterpret_cast<uint32_t *>(c.ws), n, d, f);
+    const unsigned groups = static_cast<unsigned>(ceil_div(n, N));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(want < 304 ? want : 304), groups);
+    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_few_up<T, N, VEC_UP>, static_cast<const T *>(c.x), static_cast<const T *>(c.W_in), m,
+                           reinterpret_cast<uint32_t *>(c.ws), n, d, f);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k_few_down<T, N, VEC_DOWN>, static_cast<unsigned>(ceil_div(d, DOWN_ROWS<N>)), FEW_THREADS, 0, c.stream,
-                            static_cast<const float *>(m), static_cast<const T *>(c.W_out), y, n, d, f);
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(d, DOWN_ROWS)), groups);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k_few_down<T, N, VEC_DOWN>, static_cast<const float *>(m), static_cast<const T *>(c.W_out), y,
+                              n, d, f);
 }
 
 template <typename T, int N> cudaError_t launch_few(const Call &c, T *y) {
     constexpr int WIDE = 16 / sizeof(T);
-    const bool up = c.d % WIDE == 0 && reinterpret_cast<uintptr_t>(c.W_in) % 16 == 0;
+    const bool up = c.d % WIDE == 0 && (reinterpret_cast<uintptr_t>(c.W_in) | reinterpret_cast<uintptr_t>(c.x)) % 16 == 0;
     const bool down = c.f % WIDE == 0 && reinterpret_cast<uintptr_t>(c.W_out) % 16 == 0;
     return up ? (down ? launch_few<T, N, WIDE, WIDE>(c, y) : launch_few<T, N, WIDE, 1>(c, y))
               : (down ? launch_few<T, N, 1, WIDE>(c, y) : launch_few<T, N, 1, 1>(c, y));
@@ -1178,11 +1348,30 @@ template <typename T> int few_forward(const Call &c, T *y) {
     switch (few_size(c.n)) {
         case 1: e = launch_few<T, 1>(c, y); break;
         case 4: e = launch_few<T, 4>(c, y); break;
-        case 8: e = launch_few<T, 8>(c, y); break;
-        default: e = launch_few<T, FEW_MOST>(c, y);
+        default: e = launch_few<T, FEW_GROUP>(c, y);
     }
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
+
+template <int TILES> cudaError_t launch_short(const Call &c, void *y) {
+    __nv_bfloat16 *m = reinterpret_cast<__nv_bfloat16 *>(c.ws + 256);
+    const int n = static_cast<int>(c.n), d = static_cast<int>(c.d), f = static_cast<int>(c.f);
+    const cudaError_t e = launch_dependent(k_short_up<TILES>, static_cast<unsigned>(ceil_div(f, 8)), UP_WARPS * 32, 0, c.stream,
+                                           static_cast<const __nv_bfloat16 *>(c.x), static_cast<const __nv_bfloat16 *>(c.W_in), m,
+                                           reinterpret_cast<uint32_t *>(c.ws), n, d, f);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(k_short_down<TILES>, static_cast<unsigned>(ceil_div(d, 16)), DOWN_WARPS * 32, 0, c.stream,
+                            static_cast<const __nv_bfloat16 *>(m), static_cast<const __nv_bfloat16 *>(c.W_out),
+                            static_cast<__nv_bfloat16 *>(y), n, d, f);
+}
+
+int short_forward(const Call &c, void *y) {
+    const cudaError_t e = c.n <= 8 ? launch_short<1>(c, y) : launch_short<2>(c, y);
+    return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+}
+
+// nothing kept: the workspace of the forms for few rows, the error word and m
+size_t few_bytes(int64_t n, int64_t f) { return up256(256 + sizeof(float) * n * f); }
 
 bool sizes_fit(int64_t n, int64_t d, int64_t f) { return n <= (1 << 30) && d <= (1 << 20) && f <= (1 << 20); }
 
@@ -1215,6 +1404,8 @@ size_t nrnn_gated_mlp_kept_bytes(int64_t rows, int64_t f, int dtype) {
 
 size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dtype, int what) {
     if (d <= 0 || what < 0 || what > 2 || !sizes_fit(0, d, 1) || nrnn_gated_mlp_kept_bytes(rows, f, dtype) == 0) return 0;
+    // nothing kept: enough for whichever form the call takes (an unaligned tensor's may be another)
+    if (what == 0 && few_rows(rows, d, dtype)) return few_bytes(rows, f);
     return plan_for(rows, d, f, dtype, false, false, false, false, what == 2, what == 1).total;
 }
 
@@ -1227,11 +1418,19 @@ int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, i
     const uintptr_t elem = dtype == NRNN_BF16 ? 2 : 4;
     if (y == nullptr || reinterpret_cast<uintptr_t>(y) % elem != 0 || reinterpret_cast<uintptr_t>(kept) % 256 != 0)
         return NRNN_ERR_INVALID_ARG;
+    if (kept == nullptr) {
+        const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(W_in) |
+                               reinterpret_cast<uintptr_t>(W_out)) & 15) == 0;
+        const bool in_short = short_rows(rows, d, f, dtype, aligned);
+        if (in_short || few_rows(rows, d, dtype)) {
+            if (!usable(workspace, ws_bytes, few_bytes(rows, f))) return NRNN_ERR_WORKSPACE;
+            return in_short ? short_forward(c, y)
+                 : dtype == NRNN_BF16 ? few_forward(c, static_cast<__nv_bfloat16 *>(y)) : few_forward(c, static_cast<float *>(y));
+        }
+    }
     const Plan p = plan_for(rows, d, f, dtype, used_in_place(x, d, dtype), used_in_place(W_in, d, dtype),
                             used_in_place(W_out, f, dtype), false, kept != nullptr, false);
     if (!usable(workspace, ws_bytes, p.total)) return NRNN_ERR_WORKSPACE;
-    if (kept == nullptr && few_rows(rows, d))
-        return dtype == NRNN_BF16 ? few_forward(c, static_cast<__nv_bfloat16 *>(y)) : few_forward(c, static_cast<float *>(y));
     unsigned char *k = kept != nullptr ? static_cast<unsigned char *>(kept) : c.ws + p.kept;
     return dtype == NRNN_BF16 ? forward(c, p, static_cast<__nv_bfloat16 *>(y), k, kept != nullptr)
                               : forward(c, p, static_cast<float *>(y), k, kept != nullptr);
