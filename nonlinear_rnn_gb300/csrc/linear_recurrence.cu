@@ -118,21 +118,34 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
     return y;
 }
 
-// a^2 - 1 with a = 2^z, z <= 0: for z near zero, where the difference would lose bits, by
-// the series of 2^2z - 1, y = -2 z ln 2.  TERMS 5: below y = 1/4, to y^6 / 720 (5e-8 of
-// it); 3: below 1/16, to y^4 / 24 (1.3e-7), and 2^-19 by the difference at that border.
-template <int TERMS> __device__ __forceinline__ float2 square_less_one(float2 a, float2 z) {
-    constexpr float C1 = 1.3862943611f, C2 = 0.9609060278f, C3 = 0.4440274099f, C4 = 0.1538881736f, C5 = 0.0426668398f,
-                    C6 = 0.0098579527f;   // (2 ln 2)^k / k!
-    float2 p = TERMS == 5 ? fma2(z, splat2(C6), splat2(C5)) : splat2(C4);
-    if (TERMS == 5) p = fma2(z, p, splat2(C4));
-    p = fma2(z, p, splat2(C3));
-    p = fma2(z, p, splat2(C2));
-    p = fma2(z, p, splat2(C1));
-    p = mul2(z, p);
-    const float2 q = fma2(a, a, splat2(-1.f));
-    constexpr float LIMIT = (TERMS == 5 ? -0.25f : -0.0625f) / 1.3862943611f;
-    return make_float2(z.x > LIMIT ? p.x : q.x, z.y > LIMIT ? p.y : q.y);
+// The decay a = 2^z, z <= 0, near one: a - 1 by its series, which leaves a rounding of its
+// own (ex2.approx is 2^-22 off, to one side over a range, and a unit of long memory adds
+// that up), and a^2 - 1 = (a - 1)(a + 1) without a difference.  TERMS 5: from z = -0.18 on
+// to 1e-8; 3: from -0.045 on to 4e-8, and a^2 - 1 2^-19 by the difference at that border.
+template <int TERMS> struct NearOne {
+    static constexpr float LIMIT = TERMS == 5 ? -0.18f : -0.045f;
+    __device__ static float2 less_one(float2 z) {
+        constexpr float C1 = 0.6931471806f, C2 = 0.2402265070f, C3 = 0.0555041087f, C4 = 0.0096181291f, C5 = 0.0013333558f,
+                        C6 = 0.0001540353f;   // (ln 2)^k / k!
+        float2 p = TERMS == 5 ? fma2(z, splat2(C6), splat2(C5)) : splat2(C4);
+        if (TERMS == 5) p = fma2(z, p, splat2(C4));
+        p = fma2(z, p, splat2(C3));
+        p = fma2(z, p, splat2(C2));
+        p = fma2(z, p, splat2(C1));
+        return mul2(z, p);
+    }
+};
+template <int TERMS> __device__ __forceinline__ float2 decay_of(float2 z) {
+    const float2 one_more = add2(NearOne<TERMS>::less_one(z), splat2(1.f)), far = ex2_2(z);
+    return make_float2(z.x > NearOne<TERMS>::LIMIT ? one_more.x : far.x, z.y > NearOne<TERMS>::LIMIT ? one_more.y : far.y);
+}
+// the decay, and a^2 - 1
+template <int TERMS> __device__ __forceinline__ float2 decay_of(float2 z, float2 &square_less_one) {
+    const float2 e = NearOne<TERMS>::less_one(z), one_more = add2(e, splat2(1.f)), q = mul2(e, add2(e, splat2(2.f)));
+    const float2 far = ex2_2(z), far_q = fma2(far, far, splat2(-1.f));
+    const bool x = z.x > NearOne<TERMS>::LIMIT, y = z.y > NearOne<TERMS>::LIMIT;
+    square_less_one = make_float2(x ? q.x : far_q.x, y ? q.y : far_q.y);
+    return make_float2(x ? one_more.x : far.x, y ? one_more.y : far.y);
 }
 
 // e^-x in exponent-2 units, clamped: 1 / (1 + e) = sig, e / (1 + e) = 1 - sig
@@ -147,8 +160,8 @@ __device__ __forceinline__ void forward_gates(float2 pa, float2 pi, float2 v, co
     const float2 inv = rcp_2(mul2(da, di));
     const float2 r = mul2(inv, di), i = mul2(inv, da);
     const float2 z = mul2(w.fall2, r);
-    a = ex2_2(z);
-    const float2 q = square_less_one<TERMS>(a, z);
+    float2 q;
+    a = decay_of<TERMS>(z, q);
     u = mul2(mul2(make_float2(sqrt_approx(-q.x), sqrt_approx(-q.y)), i), v);
 }
 
@@ -535,7 +548,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
             for (int i = SEG - 1; i >= 0; --i) {
                 de[i] = falling(load2(mine + i * UNITS), w.nb_a);
                 dr[i] = rcp_2(add2(de[i], splat2(1.f)));
-                const float2 decay = ex2_2(mul2(w.fall2, dr[i]));
+                const float2 decay = decay_of<TERMS>(mul2(w.fall2, dr[i]));
                 if (decltype(special)::value && (tails >> i & 1u)) {
                     m.B = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
                     m.A = splat2(-0.f);
@@ -558,8 +571,9 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
                 if (SPECIAL && (tails >> i & 1u)) nu = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
                 const float2 ei = falling(load2(mine + PLANE + i * UNITS), w.nb_i), gi = rcp_2(add2(ei, splat2(1.f)));
                 const float2 v = load2(mine + 2 * PLANE + i * UNITS);
-                const float2 r = dr[i], z = mul2(w.fall2, r), decay = ex2_2(z);
-                const float2 q = square_less_one<TERMS>(decay, z);
+                const float2 r = dr[i], z = mul2(w.fall2, r);
+                float2 q;                                                 // a^2 - 1
+                const float2 decay = decay_of<TERMS>(z, q);
                 const float2 rs = make_float2(q.x < 0.f ? rsqrt_approx(-q.x) : 0.f, q.y < 0.f ? rsqrt_approx(-q.y) : 0.f);
                 const float2 msq = mul2(q, rs), over = mul2(decay, rs);   // -s, a / s
                 float2 before = i > 0 ? load2(h_mine + (i - 1) * UNITS) : before0;
