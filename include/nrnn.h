@@ -657,7 +657,9 @@ size_t nrnn_linear_recurrence_workspace_bytes(int64_t B, int64_t T, int64_t d_h,
  *   preact      device, (B, T, 3 d_h) of dtype, blocks [a | i | v]: what
  *               nrnn_input_projection gives for W_x of these blocks
  *   params      device, fp32 (3, d_h): rows rate (>= 0; else NaN), b_a, b_i
- *   cu_seqlens  as for nrnn_newton_forward; every segment starts from its own state
+ *   cu_seqlens  device, offsets of a pack (B = 1), as for nrnn_newton_forward; they have
+ *               to keep its rules (nrnn_validate_cu_seqlens).  Every segment starts from
+ *               its own state
  *   state       device, fp32 (B, d_h), or (num_segments, d_h) for a pack: the states
  *               before the first step; NULL: zeros
  *   H           device, (B, T, d_h) of dtype

@@ -33,6 +33,12 @@
 // of a step that begins a pack's segment is marked by the sign of its A (a decay is
 // never negative), and what a marked map is applied to is not looked at, NaN or not.
 //
+// A pack of enough segments is cut into chunks of each segment instead of chunks of the
+// time axis (the plan of pack_plan.cuh, built beside the clearing of the slots): then
+// every segment is a column of its own, and many chains are short instead of few long.
+// A segment's short last chunk loads steps of the next one, which it leaves out, and
+// stores its own by rows.  PLAN_MEASURED
+//
 // A wait that gives up (the limit of nrnn_set_wait_limit_ns) sets the workspace's second
 // word, which ends the other waits too, and gives NaN in what depended on it.
 #include <type_traits>
@@ -40,6 +46,7 @@
 #include "../../include/nrnn.h"
 #include "nrnn_device.cuh"
 #include "nrnn_internal.h"
+#include "pack_plan.cuh"
 #include "rows.cuh"
 #include "tcgen05.cuh"
 
@@ -53,6 +60,10 @@ constexpr uint64_t SETTLE_NS = 2000000000ull;   // for copies in flight after a 
 // tickets and copies run a tile ahead, and every warp reads the few maps before by
 // itself.  Else chunks of a column wait for many others: tickets are taken late, and the
 // warps share the maps before.
+// MODE: how sequences lie.  ROWS: the rows of a batch; PACK: a pack cut by time; PLAN: a
+// pack cut by segments (a WIDE form).
+enum Mode { ROWS, PACK, PLAN };
+
 template <typename TS, bool WIDE> struct Shape {
     static constexpr int SEG = sizeof(TS) == 2 ? 16 : 8;      // steps a warp
     static constexpr int L = NW * SEG, PLANE = L * UNITS;     // steps and elements of a tile's block
@@ -62,6 +73,7 @@ template <typename TS, bool WIDE> struct Shape {
 
 struct RecArgs {
     const void *H;                    // backward: (B, T, d)
+    void *H_out, *gP;                 // PLAN: short chunks are stored by rows
     const float *params, *state;      // (3, d); (rows, d) or null
     const int32_t *cu;                // pack: (rows + 1) offsets
     int rows;                         // sequences: B or segments
@@ -73,7 +85,9 @@ struct RecArgs {
     const float *g_last;              // backward: (rows, d) or null
     float *g_state;                   // backward: (rows, d) or null
     float *part;                      // backward: [n_cols][n_chunks][3][UNITS] sums of a tile
-    unsigned long long *slots;        // [n_cols][n_chunks][UNITS] maps of chunks
+    const int4 *plan;                 // PLAN: the chunks; n_chunks is their most, n_cols the unit tiles
+    unsigned long long *slots;        // [n_cols][n_chunks][UNITS] maps of chunks (WIDE: of a group's last
+                                      // chunk the state after it)
     unsigned long long *maps;         // [n_cols][groups][UNITS] maps of groups
     unsigned long long *ends;         // [n_cols][spans][UNITS] states after a span
     uint32_t *ticket;
@@ -235,13 +249,58 @@ struct Shared {
 
 constexpr int WIDE_GROUP = 4;   // chunks of a group where columns are many (spans of one group)
 
-// The carry into this warp's steps.  it: the CTA's count of tiles; q: the chunk in the
-// scan's order (backward: from the end of time); m: the map of this warp's steps; place:
-// the warp in the scan's order; first: the state that the first span starts from; ok:
-// the tile's copies came.  Called by all threads; between() runs after the (first) barrier.
+// Where a tile lies: row, first unit, chunk q of nq in the scan's order, its steps t0 .. (of a
+// sequence that ends before t_end), and its place among all chunks (slots, sums)
+struct Place { int b, u0, q, nq, t0, t_end; int64_t at; };
+template <int L, bool REVERSE, int MODE> __device__ __forceinline__ Place place_of(const RecArgs &a, uint32_t tile) {
+    Place p;
+    if constexpr (MODE == PLAN) {
+        const int item = static_cast<int>(tile / static_cast<uint32_t>(a.n_ut)), ut = static_cast<int>(tile) - item * a.n_ut;
+        const int4 e = a.plan[1 + item];   // first step, the segment's end, chunk j of it, place among all chunks
+        const int after = (e.y - e.x + L - 1) / L;   // chunks from this one on
+        p.b = 0;
+        p.u0 = ut * UNITS;
+        p.nq = e.z + after;
+        p.q = REVERSE ? after - 1 : e.z;
+        p.t0 = e.x;
+        p.t_end = e.y;
+        p.at = static_cast<int64_t>(ut) * a.n_chunks + (e.w - e.z) + p.q;
+        return p;
+    }
+    p.q = static_cast<int>(tile / static_cast<uint32_t>(a.n_cols));
+    const int col = static_cast<int>(tile) - p.q * a.n_cols;
+    p.b = col / a.n_ut;
+    p.u0 = (col - p.b * a.n_ut) * UNITS;
+    p.nq = a.n_chunks;
+    p.t0 = (REVERSE ? a.n_chunks - 1 - p.q : p.q) * L;
+    p.t_end = a.T;
+    p.at = static_cast<int64_t>(col) * a.n_chunks + p.q;
+    return p;
+}
+// tiles there are
+template <int MODE> __device__ __forceinline__ uint32_t tiles_of(const RecArgs &a) {
+    return MODE == PLAN ? static_cast<uint32_t>(a.plan[0].x) * a.n_ut : a.n_tiles;
+}
+// the segment of a step
+__device__ __forceinline__ int segment_of(const RecArgs &a, int t) {
+    int lo = 0, hi = a.rows;   // the last seg with cu[seg] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.cu + mid) <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// The carry into this warp's steps.  it: the CTA's count of tiles; p: its tile (q: the
+// chunk in the scan's order, backward from the end of time); m: the map of this warp's
+// steps; place: the warp in the scan's order; first: the state that the first span starts
+// from; ok: the tile's copies came.  Called by all threads; between() runs after the last
+// barrier.
 template <bool WIDE, bool CUTS, typename Fn>
-__device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int it, int col, int q, int place, int lane,
+__device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int it, const Place &p, int place, int lane,
                                              const Map2 &m, float2 first, bool ok, Fn &&between) {
+    const int q = p.q;
     const float2 nan = splat2(__int_as_float(0x7fffffff));
     float2 (&aggA)[NW][32] = s.aggA[it & 1], (&aggB)[NW][32] = s.aggB[it & 1];
     aggA[place][lane] = m.A;
@@ -253,31 +312,32 @@ __device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int it
         for (int w = 1; w < NW; ++w) all = then<CUTS>(all, warps_map(w));
         return all;
     };
-    unsigned long long *const slot = a.slots + (static_cast<int64_t>(col) * a.n_chunks + q) * UNITS + 2 * lane;
+    unsigned long long *const slot = a.slots + p.at * UNITS + 2 * lane;
     float2 h = first;
     if constexpr (WIDE) {
-        const int g = q / WIDE_GROUP, before = q % WIDE_GROUP, groups = (a.n_chunks + WIDE_GROUP - 1) / WIDE_GROUP;
-        const bool closes = before + 1 == WIDE_GROUP && q + 1 < a.n_chunks;
-        unsigned long long *const end = a.ends + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
+        const int g = q / WIDE_GROUP, before = q % WIDE_GROUP;
+        const bool closes = before + 1 == WIDE_GROUP && q + 1 < p.nq;
+        const unsigned long long *const end = slot - (before + 1) * UNITS;   // the state after the group before
         ulonglong2 v[WIDE_GROUP - 1], e = make_ulonglong2(SLOT_EMPTY, SLOT_EMPTY);
-        if (g > 0) e = peek2(end - UNITS);
+        if (g > 0) e = peek2(end);
 #pragma unroll
         for (int k = 1; k < WIDE_GROUP; ++k)   // chunk q - k
             if (k <= before) v[k - 1] = peek2(slot - k * UNITS);
         __syncthreads();
         between();
         if (place == 0 && !closes) publish2(slot, whole_tile());
-        if (g > 0) h = await2(end - UNITS, e, a).B;
+        if (g > 0) h = await2(end, e, a).B;
 #pragma unroll
         for (int k = WIDE_GROUP - 1; k > 0; --k)
             if (k <= before) h = apply<CUTS>(await2(slot - k * UNITS, v[k - 1], a), h);
         if (!ok) h = nan;
-        if (place == 0 && closes) publish2(end, Map2{splat2(0.f), apply<CUTS>(whole_tile(), h)});
+        if (place == 0 && closes) publish2(slot, Map2{splat2(0.f), apply<CUTS>(whole_tile(), h)});
     } else {
         const int g = q / a.group, before = q - g * a.group, sp = g / a.span, gi = g - sp * a.span;
         const int groups = (a.n_chunks + a.group - 1) / a.group, spans = (groups + a.span - 1) / a.span;
-        unsigned long long *const map = a.maps + (static_cast<int64_t>(col) * groups + g) * UNITS + 2 * lane;
-        unsigned long long *const end = a.ends + (static_cast<int64_t>(col) * spans + sp) * UNITS + 2 * lane;
+        const int64_t col = p.at / a.n_chunks;
+        unsigned long long *const map = a.maps + (col * groups + g) * UNITS + 2 * lane;
+        unsigned long long *const end = a.ends + (col * spans + sp) * UNITS + 2 * lane;
         const bool closes = before + 1 == a.group, closes_span = closes && gi + 1 == a.span;
         __syncthreads();
         Map2 all{};
@@ -338,13 +398,7 @@ __device__ __forceinline__ int segments_at(const RecArgs &a, int t0, int lane, u
     int seg = 0;
     bool head = false, tail = false;
     if (lane < SEG && t < a.T) {
-        int lo = 0, hi = a.rows;   // the last seg with cu[seg] <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldg(a.cu + mid) <= t) lo = mid;
-            else hi = mid;
-        }
-        seg = lo;
+        seg = segment_of(a, t);
         head = __ldg(a.cu + seg) == t;
         tail = __ldg(a.cu + seg + 1) == t + 1;
     }
@@ -360,19 +414,8 @@ __device__ __forceinline__ bool tile_is_there(uint64_t *bar, uint32_t parity, co
     return false;
 }
 
-struct Place { int col, b, u0, q, t0; };
-template <int L, bool REVERSE> __device__ __forceinline__ Place place_of(const RecArgs &a, uint32_t tile) {
-    Place p;
-    p.q = static_cast<int>(tile / static_cast<uint32_t>(a.n_cols));
-    p.col = static_cast<int>(tile) - p.q * a.n_cols;
-    p.b = p.col / a.n_ut;
-    p.u0 = (p.col - p.b * a.n_ut) * UNITS;
-    p.t0 = (REVERSE ? a.n_chunks - 1 - p.q : p.q) * L;
-    return p;
-}
-
 // ---------------------------------------------------------------- forward
-template <typename TS, bool WIDE, bool PACK>
+template <typename TS, bool WIDE, int MODE>
 __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
     k_forward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const RecArgs a) {
     using Form = Shape<TS, WIDE>;
@@ -382,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     TS *const tiles = reinterpret_cast<TS *>(dsmem);
     auto start = [&](uint32_t tile, int buf) {   // the copies of a tile
-        const Place p = place_of<Form::L, false>(a, tile);
+        const Place p = place_of<Form::L, false, MODE>(a, tile);
         mbar_arrive_expect_tx(&s.bar[buf], 3u * PLANE * sizeof(TS));
 #pragma unroll
         for (int g = 0; g < 3; ++g)
@@ -390,30 +433,32 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
     };
     dependents_may_launch();
     wait_for_prerequisites();
+    const uint32_t n_tiles = tiles_of<MODE>(a);
     if (tid == 0) {
         mbar_init(&s.bar[0], 1);
         mbar_init(&s.bar[1], 1);
         fence_mbar_init();
         s.tile[0] = atomicAdd(a.ticket, 1u);
-        if (s.tile[0] < a.n_tiles) start(s.tile[0], 0);
+        if (s.tile[0] < n_tiles) start(s.tile[0], 0);
     }
     __syncthreads();
     for (int it = 0;; ++it) {
         const int buf = WIDE ? it & 1 : 0;
         const uint32_t tile = s.tile[it & 1];
-        if (tile >= a.n_tiles) break;
-        const Place p = place_of<Form::L, false>(a, tile);
+        if (tile >= n_tiles) break;
+        const Place p = place_of<Form::L, false, MODE>(a, tile);
         const int u = p.u0 + 2 * lane, r0 = warp * SEG;
         const bool uok = u < a.d;
         const UnitWeights w = weights_of(a.params, a.d, u, uok);
         TS *const mine = tiles + buf * 3 * PLANE + r0 * UNITS + 2 * lane;
         uint32_t heads = 0, tails = 0;
         int seg = p.b;
-        if (PACK) seg = segments_at<SEG>(a, p.t0 + r0, lane, heads, tails);
-        else if (a.T - 1 - p.t0 - r0 >= 0 && a.T - 1 - p.t0 - r0 < SEG) tails = 1u << (a.T - 1 - p.t0 - r0);
+        if (MODE == PACK) seg = segments_at<SEG>(a, p.t0 + r0, lane, heads, tails);
+        else if (p.t_end - 1 - p.t0 - r0 >= 0 && p.t_end - 1 - p.t0 - r0 < SEG) tails = 1u << (p.t_end - 1 - p.t0 - r0);
+        const bool starts = p.q < a.group * a.span && a.state != nullptr;   // in the first span
+        if (MODE == PLAN && (starts || tails != 0)) seg = segment_of(a, p.t0);
         float2 first = splat2(0.f);   // what the first span starts from
-        if (!PACK && p.q < a.group * a.span && a.state != nullptr)
-            first = two_of(a.state + static_cast<int64_t>(p.b) * a.d + u, uok);
+        if (MODE != PACK && starts) first = two_of(a.state + static_cast<int64_t>(seg) * a.d + u, uok);
         // state before a segment's first step
         auto state_at = [&](int r) {
             const int sg = __shfl_sync(FULL_MASK, seg, r);
@@ -438,23 +483,23 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
                 }
             }
         };
-        if (PACK && heads != 0) compose(std::true_type{});
+        if (MODE == PACK && heads != 0) compose(std::true_type{});
         else compose(std::false_type{});
         if (WIDE && tid == 0) s.tile[(it + 1) & 1] = next;
         if (WIDE && lane == 0) bulk_wait_read<0>();   // this warp's result has left the tile before
-        float2 h = carry_into<WIDE, PACK>(a, s, it, p.col, p.q, warp, lane, m, first, ok, [&]() {
+        float2 h = carry_into<WIDE, MODE == PACK>(a, s, it, p, warp, lane, m, first, ok, [&]() {
             if (tid == 0) {
-                if (WIDE && next < a.n_tiles) start(next, buf ^ 1);
+                if (WIDE && next < n_tiles) start(next, buf ^ 1);
             }
         });
         auto write = [&](auto special) {
 #pragma unroll
             for (int i = 0; i < SEG; ++i) {
-                if (decltype(special)::value && PACK && (heads >> i & 1u)) h = state_at(i);
+                if (decltype(special)::value && MODE == PACK && (heads >> i & 1u)) h = state_at(i);
                 h = fma2(da[i], h, du[i]);
                 store2(mine + i * UNITS, h);
                 if (decltype(special)::value && (tails >> i & 1u) && a.last != nullptr) {
-                    const int sg = PACK ? __shfl_sync(FULL_MASK, seg, i) : p.b;
+                    const int sg = MODE == PACK ? __shfl_sync(FULL_MASK, seg, i) : seg;
                     if (uok) *reinterpret_cast<float2 *>(a.last + static_cast<int64_t>(sg) * a.d + u) = h;
                 }
             }
@@ -463,7 +508,10 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
         else write(std::false_type{});
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && p.t0 + r0 < a.T) {
+        if (MODE == PLAN && p.t_end - p.t0 < Form::L) {   // the steps after the segment are the next one's
+            for (int i = 0; i < SEG && p.t0 + r0 + i < p.t_end; ++i)
+                if (uok) store2(static_cast<TS *>(a.H_out) + static_cast<int64_t>(p.t0 + r0 + i) * a.d + u, load2(mine + i * UNITS));
+        } else if (lane == 0 && p.t0 + r0 < a.T) {
             tma_store_3d(&tmH, mine, p.u0, p.t0 + r0, p.b);
             bulk_commit();
         }
@@ -471,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
             if (tid == 0) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
             if (lane == 0) bulk_wait_read<0>();
             __syncthreads();
-            if (tid == 0 && next < a.n_tiles) start(next, 0);
+            if (tid == 0 && next < n_tiles) start(next, 0);
         }
     }
     if (lane == 0) bulk_wait_read<0>();   // the tiles outlive the stores' reads
@@ -487,7 +535,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap *map, const void *
         : "memory");
 }
 
-template <typename TS, bool WIDE, bool PACK>
+template <typename TS, bool WIDE, int MODE>
 __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
     k_backward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH,
                const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmGP, const RecArgs a) {
@@ -499,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     TS *const Ps = reinterpret_cast<TS *>(dsmem), *const Hs = Ps + 3 * PLANE, *const Gs = Hs + PLANE;
     auto start = [&](uint32_t tile) {
-        const Place p = place_of<Form::L, true>(a, tile);
+        const Place p = place_of<Form::L, true, MODE>(a, tile);
         mbar_arrive_expect_tx(&s.bar[0], 5u * PLANE * sizeof(TS));
 #pragma unroll
         for (int g = 0; g < 3; ++g) tma_load_3d(Ps + g * PLANE, &tmP, &s.bar[0], g * a.d + p.u0, p.t0, p.b);
@@ -508,17 +556,18 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
     };
     dependents_may_launch();
     wait_for_prerequisites();
+    const uint32_t n_tiles = tiles_of<MODE>(a);
     if (tid == 0) {
         mbar_init(&s.bar[0], 1);
         fence_mbar_init();
         s.tile[0] = atomicAdd(a.ticket, 1u);
-        if (s.tile[0] < a.n_tiles) start(s.tile[0]);
+        if (s.tile[0] < n_tiles) start(s.tile[0]);
     }
     __syncthreads();
     for (int it = 0;; ++it) {
         const uint32_t tile = s.tile[it & 1];
-        if (tile >= a.n_tiles) break;
-        const Place p = place_of<Form::L, true>(a, tile);
+        if (tile >= n_tiles) break;
+        const Place p = place_of<Form::L, true, MODE>(a, tile);
         const int u = p.u0 + 2 * lane, r0 = warp * SEG;
         const bool uok = u < a.d;
         const UnitWeights w = weights_of(a.params, a.d, u, uok);
@@ -526,14 +575,16 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
         const TS *const h_mine = Hs + r0 * UNITS + 2 * lane, *const g_mine = Gs + r0 * UNITS + 2 * lane;
         uint32_t heads = 0, tails = 0;
         int seg = p.b;
-        if (PACK) {
+        const int valid = MODE == PLAN ? p.t_end - p.t0 - r0 : SEG;   // steps of this warp before the segment's end
+        if (MODE == PACK) {
             seg = segments_at<SEG>(a, p.t0 + r0, lane, heads, tails);
         } else {
-            const int end = a.T - 1 - p.t0 - r0;
+            const int end = p.t_end - 1 - p.t0 - r0;
             if (end >= 0 && end < SEG) tails = 1u << end;
-            if (p.t0 + r0 == 0) heads = 1u;
+            if (MODE == PLAN ? p.q + 1 == p.nq && warp == 0 : p.t0 + r0 == 0) heads = 1u;
+            if (MODE == PLAN && (heads | tails) != 0) seg = segment_of(a, p.t0);
         }
-        auto row_of = [&](int r) { return static_cast<int64_t>(PACK ? __shfl_sync(FULL_MASK, seg, r) : p.b) * a.d + u; };
+        auto row_of = [&](int r) { return static_cast<int64_t>(MODE == PACK ? __shfl_sync(FULL_MASK, seg, r) : seg) * a.d + u; };
         float2 before0 = splat2(0.f);   // H at the step before this warp's first
         if (warp == 0 && p.t0 > 0 && uok)
             before0 = load2(static_cast<const TS *>(a.H) + (static_cast<int64_t>(p.b) * a.T + p.t0 - 1) * a.d + u);
@@ -546,6 +597,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
         auto compose = [&](auto special) {
 #pragma unroll
             for (int i = SEG - 1; i >= 0; --i) {
+                if (MODE == PLAN && decltype(special)::value && i >= valid) continue;   // the next segment's
                 de[i] = falling(load2(mine + i * UNITS), w.nb_a);
                 dr[i] = rcp_2(add2(de[i], splat2(1.f)));
                 const float2 decay = decay_of<TERMS>(mul2(w.fall2, dr[i]));
@@ -557,10 +609,10 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
                 m.A = mul2(decay, m.A);
             }
         };
-        if (tails != 0) compose(std::true_type{});
+        if (tails != 0 || valid < SEG) compose(std::true_type{});
         else compose(std::false_type{});
         uint32_t next = 0;
-        float2 nu = carry_into<WIDE, PACK>(a, s, it, p.col, p.q, NW - 1 - warp, lane, m, splat2(0.f), ok, [&]() {
+        float2 nu = carry_into<WIDE, MODE == PACK>(a, s, it, p, NW - 1 - warp, lane, m, splat2(0.f), ok, [&]() {
             if (WIDE && tid == 0) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
         });
         float2 g_wr = splat2(0.f), g_ba = splat2(0.f), g_bi = splat2(0.f);
@@ -568,6 +620,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
 #pragma unroll
             for (int i = SEG - 1; i >= 0; --i) {
                 constexpr bool SPECIAL = decltype(special)::value;
+                if (MODE == PLAN && SPECIAL && i >= valid) continue;
                 if (SPECIAL && (tails >> i & 1u)) nu = two_of(a.g_last + row_of(i), uok && a.g_last != nullptr);
                 const float2 ei = falling(load2(mine + PLANE + i * UNITS), w.nb_i), gi = rcp_2(add2(ei, splat2(1.f)));
                 const float2 v = load2(mine + 2 * PLANE + i * UNITS);
@@ -598,7 +651,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
                 store2(mine + 2 * PLANE + i * UNITS, gv);
             }
         };
-        if ((heads | tails) != 0) write(std::true_type{});
+        if ((heads | tails) != 0 || valid < SEG) write(std::true_type{});
         else write(std::false_type{});
         if (!WIDE && tid == 0) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
         sums[0][warp][lane] = mul2(g_wr, splat2(-1.f));
@@ -606,19 +659,26 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
         sums[2][warp][lane] = g_bi;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && p.t0 + r0 < a.T) {
+        if (MODE == PLAN && p.t_end - p.t0 < Form::L) {
+            for (int i = 0; i < SEG && i < valid; ++i)
+#pragma unroll
+                for (int g = 0; g < 3; ++g)
+                    if (uok)
+                        store2(static_cast<TS *>(a.gP) + (static_cast<int64_t>(p.t0 + r0 + i) * 3 + g) * a.d + u,
+                               load2(mine + g * PLANE + i * UNITS));
+        } else if (lane == 0 && p.t0 + r0 < a.T) {
 #pragma unroll
             for (int g = 0; g < 3; ++g) store_block(&tmGP, Ps + g * PLANE + r0 * UNITS, p.u0, g, p.t0 + r0, p.b);
             bulk_commit();
             bulk_wait_read<0>();
         }
         __syncthreads();
-        if (tid == 0 && next < a.n_tiles) start(next);
+        if (tid == 0 && next < n_tiles) start(next);
         if (warp < 3) {
             float2 t = sums[warp][0][lane];
 #pragma unroll
             for (int k = 1; k < NW; ++k) t = add2(t, sums[warp][k][lane]);
-            float *to = a.part + ((static_cast<int64_t>(p.col) * a.n_chunks + p.q) * 3 + warp) * UNITS + 2 * lane;
+            float *to = a.part + (p.at * 3 + warp) * UNITS + 2 * lane;
             *reinterpret_cast<float2 *>(to) = t;
         }
         // (the next tile's first barrier lies between these reads and its sums)
@@ -631,12 +691,13 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
 constexpr int JOIN_SLICES = 32, JOIN_THREADS = 3 * UNITS;
 
 __global__ void __launch_bounds__(JOIN_THREADS)
-    k_join(const float *part, int rows, int n_ut, int n_chunks, int d, float *share, uint32_t *count, float *gparams) {
+    k_join(const float *part, int rows, int n_ut, int n_chunks, const int4 *plan, int d, float *share, uint32_t *count,
+           float *gparams) {
     __shared__ bool is_last;
     dependents_may_launch();
     wait_for_prerequisites();
     const int ut = blockIdx.x, slice = blockIdx.y, j = threadIdx.x;
-    const int64_t all = static_cast<int64_t>(rows) * n_chunks;
+    const int64_t all = plan != nullptr ? plan[0].x : static_cast<int64_t>(rows) * n_chunks;   // (a plan: one row)
     const int64_t k0 = all * slice / JOIN_SLICES, k1 = all * (slice + 1) / JOIN_SLICES;
     auto at = [&](int64_t k) {
         const int64_t b = k / n_chunks, q = k - b * n_chunks;
@@ -664,12 +725,27 @@ __global__ void __launch_bounds__(JOIN_THREADS)
 }
 
 // Clears a call's counters and slots.  Sequences without a step hand their state (or its
-// gradient) on; with no steps at all the parameters' gradients are zeros.
-__global__ void __launch_bounds__(256)
-    k_prepare(uint4 *clear, int64_t n16, const int32_t *cu, int rows, int T, int d, const float *in, float *out, float *zeros) {
+// gradient) on; with no steps at all the parameters' gradients are zeros.  With a plan the
+// first CTA builds it and clears nothing.
+constexpr int PREPARE_THREADS = 256;
+
+template <int L>
+__global__ void __launch_bounds__(PREPARE_THREADS)
+    k_prepare(uint4 *clear, int64_t n16, const int32_t *cu, int rows, int T, int d, const float *in, float *out, float *zeros,
+              int4 *plan, bool reverse) {
+    extern __shared__ int plan_space[];
     dependents_may_launch();
     wait_for_prerequisites();
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * 256;
+    int first = 0;
+    if (plan != nullptr) {
+        if (blockIdx.x == 0) {
+            build_pack_plan<PREPARE_THREADS, L>(cu, rows, (T + L - 1) / L, reverse, plan, plan_space);
+            return;
+        }
+        first = 1;
+    }
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x - first) * PREPARE_THREADS + threadIdx.x,
+                  step = static_cast<int64_t>(gridDim.x - first) * PREPARE_THREADS;
     for (int64_t i = i0; i < n16; i += step) clear[i] = make_uint4(0u, 0u, 0u, 0u);
     if (out != nullptr && (cu != nullptr || T == 0))
         for (int64_t i = i0; i < static_cast<int64_t>(rows) * d; i += step) {
@@ -708,20 +784,25 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 struct Layout {
     bool wide;
     int64_t n_ut, n_cols, n_chunks, group, span, n_tiles;
-    int64_t slots, maps, ends, cleared, part, share, total;
+    int64_t slots, maps, ends, cleared, plan, part, share, total;   // plan 0: none
 };
 
-// Columns from which a call takes the WIDE form.
-constexpr int64_t WIDE_COLUMNS = 64;
+// Columns from which a call takes the WIDE form.  (16 x 16384 bf16 of 64, 128 columns: 188
+// and 128 us forward, 138 and 133 the other; fp32 of 64: 199 and 107.)
+constexpr int64_t WIDE_COLUMNS = 128;
 
-Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, bool backward) {
+// num_segments > 0: a pack.  Its segments are columns where they are enough of them for
+// the WIDE form, long enough (a segment adds a short chunk), and the plan is small.
+Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, int64_t num_segments, bool backward) {
     Layout y{};
+    const int64_t wide_steps = dtype == NRNN_BF16 ? Shape<__nv_bfloat16, true>::L : Shape<float, true>::L;
+    const int64_t steps = dtype == NRNN_BF16 ? Shape<__nv_bfloat16, false>::L : Shape<float, false>::L;
     y.n_ut = ceil_div(d, UNITS);
+    const bool plan = B == 1 && num_segments >= 2 && num_segments <= PACK_PLAN_MAX_S && ceil_div(T, wide_steps) <= PACK_PLAN_MAX_CHUNKS &&
+                      8 * num_segments <= ceil_div(T, wide_steps) && num_segments * y.n_ut >= WIDE_COLUMNS;
     y.n_cols = B * y.n_ut;
-    y.wide = y.n_cols >= WIDE_COLUMNS;
-    const int64_t steps = dtype == NRNN_BF16 ? (y.wide ? Shape<__nv_bfloat16, true>::L : Shape<__nv_bfloat16, false>::L)
-                                             : (y.wide ? Shape<float, true>::L : Shape<float, false>::L);
-    y.n_chunks = ceil_div(T, steps);
+    y.wide = plan || y.n_cols >= WIDE_COLUMNS;
+    y.n_chunks = ceil_div(T, y.wide ? wide_steps : steps) + (plan ? num_segments : 0);
     // a chain has a hop a span (else, 2 to 3 us), and a chunk reads half a group's and half a
     // span's maps on average
     y.group = y.wide ? WIDE_GROUP : 16;
@@ -729,13 +810,19 @@ Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, bool backward) {
     const int64_t groups = ceil_div(y.n_chunks, y.group);
     y.n_tiles = y.n_cols * y.n_chunks;
     int64_t at = 256 + up256(4 * y.n_ut);   // ticket, error; the join's counters
-    y.slots = at;
-    at += 8 * UNITS * y.n_tiles;
-    y.maps = at;
-    at += y.span > 1 ? 8 * UNITS * y.n_cols * groups : 0;
-    y.ends = at;
-    at += 8 * UNITS * y.n_cols * ceil_div(groups, y.span);
+    auto take = [&](int64_t per_column) {
+        const int64_t o = at;
+        at += 8 * UNITS * y.n_cols * per_column;
+        return o;
+    };
+    y.slots = take(y.n_chunks);
+    y.maps = take(y.wide ? 0 : groups);
+    y.ends = take(y.wide ? 0 : ceil_div(groups, y.span));
     y.cleared = at;
+    if (plan) {
+        y.plan = at;
+        at += up256(16 * (1 + y.n_chunks));
+    }
     y.part = at;
     if (backward) {
         at += up256(4 * 3 * UNITS * y.n_tiles);
@@ -784,18 +871,39 @@ RecArgs args_of(const Layout &y, const float *params, const float *state, const 
     a.slots = reinterpret_cast<unsigned long long *>(ws + y.slots);
     a.maps = reinterpret_cast<unsigned long long *>(ws + y.maps);
     a.ends = reinterpret_cast<unsigned long long *>(ws + y.ends);
+    a.plan = y.plan != 0 ? reinterpret_cast<const int4 *>(ws + y.plan) : nullptr;
     a.part = reinterpret_cast<float *>(ws + y.part);
     a.wait_ns = wait_limit_ns();
     return a;
 }
 
+template <int L>
 cudaError_t prepare(const Layout &y, const RecArgs &a, unsigned char *ws, const float *in, float *out, float *zeros,
-                    cudaStream_t s) {
+                    bool reverse, cudaStream_t s) {
     const int64_t n16 = y.n_tiles > 0 ? y.cleared / 16 : 0;
     const int64_t most = n16 > static_cast<int64_t>(a.rows) * a.d ? n16 : static_cast<int64_t>(a.rows) * a.d;
-    const int64_t b = ceil_div(most, 256);
-    return launch_dependent(k_prepare, static_cast<unsigned>(b < 1 ? 1 : b < 1216 ? b : 1216), 256, 0, s,
-                            reinterpret_cast<uint4 *>(ws), n16, a.cu, a.rows, a.T, a.d, in, out, zeros);
+    int64_t b = ceil_div(most, PREPARE_THREADS);
+    b = b < 1 ? 1 : b < 1216 ? b : 1216;
+    size_t smem = 0;
+    int4 *plan = nullptr;
+    if (y.plan != 0) {
+        static std::atomic<unsigned long long> configured{0};
+        cudaError_t e = once_per_device(configured, [](int) {
+            return cudaFuncSetAttribute(k_prepare<L>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(pack_plan_smem(PACK_PLAN_MAX_S, PACK_PLAN_MAX_CHUNKS)));
+        });
+        if (e != cudaSuccess) return e;
+        plan = reinterpret_cast<int4 *>(ws + y.plan);
+        smem = pack_plan_smem(a.rows, static_cast<int>(ceil_div(a.T, L)));
+        b += 1;   // the first one plans
+    }
+    return launch_dependent(k_prepare<L>, static_cast<unsigned>(b), PREPARE_THREADS, smem, s, reinterpret_cast<uint4 *>(ws), n16,
+                            a.cu, a.rows, a.T, a.d, in, out, zeros, plan, reverse);
+}
+cudaError_t prepare(int dtype, const Layout &y, const RecArgs &a, unsigned char *ws, const float *in, float *out, float *zeros,
+                    bool reverse, cudaStream_t s) {
+    return dtype == NRNN_BF16 ? prepare<Shape<__nv_bfloat16, true>::L>(y, a, ws, in, out, zeros, reverse, s)
+                              : prepare<Shape<float, true>::L>(y, a, ws, in, out, zeros, reverse, s);
 }
 
 unsigned ctas_for(int64_t tiles, int per_sm) {
@@ -803,30 +911,30 @@ unsigned ctas_for(int64_t tiles, int per_sm) {
     return static_cast<unsigned>(tiles < most ? tiles : most);
 }
 
-template <typename TS, bool WIDE, bool PACK>
+template <typename TS, bool WIDE, int MODE>
 cudaError_t launch_forward(const Layout &y, const RecArgs &a, int dtype, const void *P, void *H, int64_t B, cudaStream_t s) {
     using Form = Shape<TS, WIDE>;
     static std::atomic<unsigned long long> configured{0};
     constexpr size_t smem = static_cast<size_t>(Form::FORWARD_TILES) * 3 * Form::PLANE * sizeof(TS);
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_forward<TS, WIDE, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        return cudaFuncSetAttribute(k_forward<TS, WIDE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     });
     if (e != cudaSuccess) return e;
     CUtensorMap tmP, tmH;
     if (!make_map_steps(&tmP, P, dtype, 3 * a.d, a.T, B, UNITS, Form::L) ||
         !make_map_steps(&tmH, H, dtype, a.d, a.T, B, UNITS, Form::SEG))
         return cudaErrorUnknown;
-    return launch_dependent(k_forward<TS, WIDE, PACK>, ctas_for(y.n_tiles, Form::FORWARD_CTAS), THREADS, smem, s, tmP, tmH, a);
+    return launch_dependent(k_forward<TS, WIDE, MODE>, ctas_for(y.n_tiles, Form::FORWARD_CTAS), THREADS, smem, s, tmP, tmH, a);
 }
 
-template <typename TS, bool WIDE, bool PACK>
+template <typename TS, bool WIDE, int MODE>
 cudaError_t launch_backward(const Layout &y, const RecArgs &a, int dtype, const void *P, const void *H, const void *gH,
                             void *gP, int64_t B, cudaStream_t s) {
     using Form = Shape<TS, WIDE>;
     static std::atomic<unsigned long long> configured{0};
     constexpr size_t smem = 5ull * Form::PLANE * sizeof(TS);
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_backward<TS, WIDE, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        return cudaFuncSetAttribute(k_backward<TS, WIDE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     });
     if (e != cudaSuccess) return e;
     CUtensorMap tmP, tmH, tmG, tmGP;
@@ -835,19 +943,18 @@ cudaError_t launch_backward(const Layout &y, const RecArgs &a, int dtype, const 
         !make_map_steps(&tmG, gH, dtype, a.d, a.T, B, UNITS, Form::L) ||
         !make_map_gate_steps(&tmGP, gP, dtype, a.d, a.T, B, UNITS, Form::SEG))
         return cudaErrorUnknown;
-    return launch_dependent(k_backward<TS, WIDE, PACK>, ctas_for(y.n_tiles, Form::BACKWARD_CTAS), THREADS, smem, s, tmP, tmH, tmG,
+    return launch_dependent(k_backward<TS, WIDE, MODE>, ctas_for(y.n_tiles, Form::BACKWARD_CTAS), THREADS, smem, s, tmP, tmH, tmG,
                             tmGP, a);
 }
 
-// launch<TS, WIDE, PACK>(args...) for the call
-#define BY_FORM(launch, y, dtype, pack, ...)                                                                        \
-    ((dtype) == NRNN_BF16                                                                                           \
-         ? ((y).wide ? ((pack) ? launch<__nv_bfloat16, true, true>(y, __VA_ARGS__)                                  \
-                               : launch<__nv_bfloat16, true, false>(y, __VA_ARGS__))                                \
-                     : ((pack) ? launch<__nv_bfloat16, false, true>(y, __VA_ARGS__)                                 \
-                               : launch<__nv_bfloat16, false, false>(y, __VA_ARGS__)))                              \
-         : ((y).wide ? ((pack) ? launch<float, true, true>(y, __VA_ARGS__) : launch<float, true, false>(y, __VA_ARGS__)) \
-                     : ((pack) ? launch<float, false, true>(y, __VA_ARGS__) : launch<float, false, false>(y, __VA_ARGS__))))
+// launch<TS, WIDE, MODE>(args...) for the call
+#define BY_MODE(launch, TS, y, pack, ...)                                                                         \
+    ((y).plan != 0 ? launch<TS, true, PLAN>(y, __VA_ARGS__)                                                       \
+     : (y).wide    ? ((pack) ? launch<TS, true, PACK>(y, __VA_ARGS__) : launch<TS, true, ROWS>(y, __VA_ARGS__))   \
+                   : ((pack) ? launch<TS, false, PACK>(y, __VA_ARGS__) : launch<TS, false, ROWS>(y, __VA_ARGS__)))
+#define BY_FORM(launch, y, dtype, pack, ...)                                        \
+    ((dtype) == NRNN_BF16 ? BY_MODE(launch, __nv_bfloat16, y, pack, __VA_ARGS__)    \
+                          : BY_MODE(launch, float, y, pack, __VA_ARGS__))
 
 }  // namespace
 }  // namespace nrnn
@@ -861,7 +968,7 @@ size_t nrnn_linear_recurrence_workspace_bytes(int64_t B, int64_t T, int64_t d_h,
     if (num_segments < 0 || (dtype != NRNN_F32 && dtype != NRNN_BF16) || B < 0 || T < 0 || d_h <= 0 || B > INT32_MAX ||
         T > INT32_MAX || d_h > (1 << 24) || (B > 0 && T > 0 && ceil_div(T, 32) > INT32_MAX / (B * ceil_div(d_h, UNITS))))
         return 0;
-    return static_cast<size_t>(layout_of(B, T, d_h, dtype, backward != 0).total);
+    return static_cast<size_t>(layout_of(B, T, d_h, dtype, num_segments, backward != 0).total);
 }
 
 int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *params, int64_t B,
@@ -877,14 +984,15 @@ int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *p
         overlap(state, rows * d_h * 4, last, rows * d_h * 4) || overlap(preact, 3 * n * es, last, rows * d_h * 4) ||
         overlap(H, n * es, last, rows * d_h * 4))
         return NRNN_ERR_INVALID_ARG;
-    const Layout y = layout_of(B, T, d_h, dtype, false);
+    const Layout y = layout_of(B, T, d_h, dtype, cu_seqlens != nullptr ? num_segments : 0, false);
     if (!usable(workspace, ws_bytes, y.total)) return NRNN_ERR_WORKSPACE;
     if (rows == 0) return NRNN_OK;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     RecArgs a = args_of(y, params, state, cu_seqlens, rows, T, d_h, ws);
     a.last = last;
-    cudaError_t e = prepare(y, a, ws, state, last, nullptr, s);
+    a.H_out = H;
+    cudaError_t e = prepare(dtype, y, a, ws, state, last, nullptr, false, s);
     if (e == cudaSuccess && n > 0) e = BY_FORM(launch_forward, y, dtype, cu_seqlens != nullptr, a, dtype, preact, H, B, s);
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
@@ -904,15 +1012,16 @@ int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *
         overlap(gH, n * es, gP, 3 * n * es) || overlap(state, sb, g_state, sb) || overlap(g_last, sb, g_state, sb) ||
         overlap(gP, 3 * n * es, g_state, sb))
         return NRNN_ERR_INVALID_ARG;
-    const Layout y = layout_of(B, T, d_h, dtype, true);
+    const Layout y = layout_of(B, T, d_h, dtype, cu_seqlens != nullptr ? num_segments : 0, true);
     if (!usable(workspace, ws_bytes, y.total)) return NRNN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     RecArgs a = args_of(y, params, state, cu_seqlens, rows, T, d_h, ws);
     a.H = H;
+    a.gP = gP;
     a.g_last = g_last;
     a.g_state = g_state;
-    cudaError_t e = prepare(y, a, ws, g_last, g_state, n > 0 ? nullptr : gparams, s);
+    cudaError_t e = prepare(dtype, y, a, ws, g_last, g_state, n > 0 ? nullptr : gparams, true, s);
     if (e == cudaSuccess && n > 0) {
         e = BY_FORM(launch_backward, y, dtype, cu_seqlens != nullptr, a, dtype, preact, H, gH, gP, B, s);
         if (e == cudaSuccess) {
@@ -926,7 +1035,7 @@ int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             e = cudaLaunchKernelEx(&cfg, k_join, static_cast<const float *>(a.part), static_cast<int>(B), a.n_ut, a.n_chunks,
-                                   a.d, reinterpret_cast<float *>(ws + y.share), reinterpret_cast<uint32_t *>(ws + 256), gparams);
+                                   a.plan, a.d, reinterpret_cast<float *>(ws + y.share), reinterpret_cast<uint32_t *>(ws + 256), gparams);
         }
     }
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;

@@ -60,7 +60,8 @@ __device__ int cta_exclusive_scan(const int *in, int *out, int n, int *s_warp) {
 // after j -- and within one level by the segment's number of chunks, most
 // first; the order among segments of equal chunk counts does not matter
 // (every chunk's predecessor in its chain sits one level earlier).
-template <int NT>
+// L: steps of a chunk
+template <int NT, int L = NEWTON_L>
 __device__ void build_pack_plan(const int32_t *__restrict__ cu, int S, int n_chunks, bool reverse,
                                 int4 *__restrict__ plan, int *sm) {
     __shared__ int s_warp[32];
@@ -76,7 +77,7 @@ __device__ void build_pack_plan(const int32_t *__restrict__ cu, int S, int n_chu
     __syncthreads();
     for (int s = tid; s < S; s += NT) {
         const int len = max(0, __ldg(cu + s + 1) - __ldg(cu + s));
-        const int c = min(n_chunks, (len + NEWTON_L - 1) / NEWTON_L);
+        const int c = min(n_chunks, (len + L - 1) / L);
         nc[s] = c;
         atomicAdd(&cnt[c], 1);
     }
@@ -93,7 +94,7 @@ __device__ void build_pack_plan(const int32_t *__restrict__ cu, int S, int n_chu
     for (int s = tid; s < S; s += NT) {
         const int c = nc[s], r0 = __ldg(cu + s), r1 = __ldg(cu + s + 1), b = base[s], rk = rank[s];
         for (int j = 0; j < c; ++j)
-            plan[1 + first[reverse ? c - 1 - j : j] + rk] = make_int4(r0 + j * NEWTON_L, r1, j, b + j);
+            plan[1 + first[reverse ? c - 1 - j : j] + rk] = make_int4(r0 + j * L, r1, j, b + j);
     }
     if (tid == 0) plan[0] = make_int4(total, 0, 0, 0);
 }

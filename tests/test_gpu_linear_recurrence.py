@@ -120,7 +120,7 @@ def reference_backward(P, params, H, gH, cu=None, state=None, g_last=None):
 
 
 SHAPES = [(1, 1, 8), (2, 2, 40), (3, 63, 32), (1, 64, 72), (2, 65, 264), (1, 300, 136), (5, 129, 64), (1, 2500, 64), (40, 70, 8),
-          (70, 300, 8), (3, 700, 1536), (66, 64, 72)]
+          (70, 300, 8), (130, 300, 8), (6, 700, 1408), (66, 64, 72)]
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -159,22 +159,57 @@ def test_packs(pack, given, t):
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("pack", [1, 3, 5, 6])
 def test_wide_packs(pack, t):
-    """More than 64 tiles of units: the form with copies a tile ahead."""
-    packs_of_width(pack, 4176, True, t)
+    """More than 128 tiles of units: the form with copies a tile ahead."""
+    packs_of_width(pack, 8216, True, t)
+
+
+LONG_PACKS = [[0, 300, 1100, 1100, 1101, 2400, 2433, 4100], [0, 64, 2048, 2048, 2112, 4096], [0, 0, 1, 1500, 3000, 3000]]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("pack", range(len(LONG_PACKS)))
+def test_packs_cut_by_segments(pack, given, t):
+    """Segments enough and long enough to be columns of their own: 64-unit tiles times
+    segments from 128 on, and eight chunks a segment on average."""
+    packs_of_width(LONG_PACKS[pack], 1800, given, t)
+
+
+def test_short_chunks_leave_the_next_segment_alone():
+    """What a segment's short last chunk loads beyond its end, NaN and infinities, reaches
+    nothing, and nothing is written there by it."""
+    cu, d = [0, 700, 1419, 2200, 4000], 2056
+    N = cu[-1]
+    g, P, params = inputs(1, N, d, torch.bfloat16, seed=21)
+    gH = randn(g, 1, N, d, t=torch.bfloat16)
+    H, last = nr.linear_recurrence(P, params, cu_seqlens=cu)
+    r = nr.linear_recurrence_backward(P, params, H, gH, cu_seqlens=cu)
+    Q, gQ, HQ = P.clone(), gH.clone(), H.clone()
+    for x, bad in ((Q, float("nan")), (gQ, float("inf")), (HQ, float("nan"))):
+        x[0, 1419:2200] = bad
+    H2, last2 = nr.linear_recurrence(Q, params, cu_seqlens=cu)
+    r2 = nr.linear_recurrence_backward(Q, params, HQ, gQ, cu_seqlens=cu)
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[1419:2200] = False
+    assert torch.equal(H2[0, keep], H[0, keep]) and torch.equal(r2.gP[0, keep], r.gP[0, keep])
+    assert torch.equal(last2[[0, 1, 3]], last[[0, 1, 3]])
+    again = nr.linear_recurrence_backward(P, params, H, gH, cu_seqlens=cu)
+    assert all(torch.equal(x, y) for x, y in zip(r[:2], again[:2]))
 
 
 def packs_of_width(pack, d, given, t):
-    cu = torch.tensor(PACKS[pack], dtype=torch.int32)
-    N, S = PACKS[pack][-1], len(PACKS[pack]) - 1
-    g, P, params = inputs(1, N, d, t, seed=pack)
+    bounds = PACKS[pack] if isinstance(pack, int) else pack
+    cu = torch.tensor(bounds, dtype=torch.int32)
+    N, S = bounds[-1], len(bounds) - 1
+    g, P, params = inputs(1, N, d, t, seed=len(bounds))
     state = randn(g, S, d) if given else None
     H, last = nr.linear_recurrence(P, params, cu_seqlens=cu, state=state)
-    ref, ref_last, E, e_last = reference(P, params, PACKS[pack], state)
+    ref, ref_last, E, e_last = reference(P, params, bounds, state)
     check(H, ref, E + rounding(t) * ref.abs(), "H")
     check(last, ref_last, e_last, "last")
     gH, g_last = randn(g, 1, N, d, t=t), randn(g, S, d) if given else None
     r = nr.linear_recurrence_backward(P, params, H, gH, cu_seqlens=nr.DeviceCuSeqlens(cu, N, "cuda:0"), state=state, g_state=g_last)
-    gP, dP, sums, offs, g0, e0 = reference_backward(P, params, H, gH, PACKS[pack], state, g_last)
+    gP, dP, sums, offs, g0, e0 = reference_backward(P, params, H, gH, bounds, state, g_last)
     check(r.gP, gP, dP + rounding(t) * gP.abs(), "gP")
     check(r.gparams, sums, offs, "gparams")
     if given:
