@@ -251,13 +251,14 @@ constexpr int WIDE_GROUP = 4;   // chunks of a group where columns are many (spa
 
 // Where a tile lies: row, first unit, chunk q of nq in the scan's order, its steps t0 .. (of a
 // sequence that ends before t_end), and its place among all chunks (slots, sums)
-struct Place { int b, u0, q, nq, t0, t_end; int64_t at; };
+struct Place { int col, b, u0, q, nq, t0, t_end; int64_t at; };
 template <int L, bool REVERSE, int MODE> __device__ __forceinline__ Place place_of(const RecArgs &a, uint32_t tile) {
     Place p;
     if constexpr (MODE == PLAN) {
         const int item = static_cast<int>(tile / static_cast<uint32_t>(a.n_ut)), ut = static_cast<int>(tile) - item * a.n_ut;
         const int4 e = a.plan[1 + item];   // first step, the segment's end, chunk j of it, place among all chunks
         const int after = (e.y - e.x + L - 1) / L;   // chunks from this one on
+        p.col = ut;
         p.b = 0;
         p.u0 = ut * UNITS;
         p.nq = e.z + after;
@@ -268,13 +269,13 @@ template <int L, bool REVERSE, int MODE> __device__ __forceinline__ Place place_
         return p;
     }
     p.q = static_cast<int>(tile / static_cast<uint32_t>(a.n_cols));
-    const int col = static_cast<int>(tile) - p.q * a.n_cols;
-    p.b = col / a.n_ut;
-    p.u0 = (col - p.b * a.n_ut) * UNITS;
+    p.col = static_cast<int>(tile) - p.q * a.n_cols;
+    p.b = p.col / a.n_ut;
+    p.u0 = (p.col - p.b * a.n_ut) * UNITS;
     p.nq = a.n_chunks;
     p.t0 = (REVERSE ? a.n_chunks - 1 - p.q : p.q) * L;
     p.t_end = a.T;
-    p.at = static_cast<int64_t>(col) * a.n_chunks + p.q;
+    p.at = static_cast<int64_t>(p.col) * a.n_chunks + p.q;
     return p;
 }
 // tiles there are
@@ -335,9 +336,8 @@ __device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int it
     } else {
         const int g = q / a.group, before = q - g * a.group, sp = g / a.span, gi = g - sp * a.span;
         const int groups = (a.n_chunks + a.group - 1) / a.group, spans = (groups + a.span - 1) / a.span;
-        const int64_t col = p.at / a.n_chunks;
-        unsigned long long *const map = a.maps + (col * groups + g) * UNITS + 2 * lane;
-        unsigned long long *const end = a.ends + (col * spans + sp) * UNITS + 2 * lane;
+        unsigned long long *const map = a.maps + (static_cast<int64_t>(p.col) * groups + g) * UNITS + 2 * lane;
+        unsigned long long *const end = a.ends + (static_cast<int64_t>(p.col) * spans + sp) * UNITS + 2 * lane;
         const bool closes = before + 1 == a.group, closes_span = closes && gi + 1 == a.span;
         __syncthreads();
         Map2 all{};
@@ -697,19 +697,25 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     dependents_may_launch();
     wait_for_prerequisites();
     const int ut = blockIdx.x, slice = blockIdx.y, j = threadIdx.x;
-    const int64_t all = plan != nullptr ? plan[0].x : static_cast<int64_t>(rows) * n_chunks;   // (a plan: one row)
-    const int64_t k0 = all * slice / JOIN_SLICES, k1 = all * (slice + 1) / JOIN_SLICES;
-    auto at = [&](int64_t k) {
-        const int64_t b = k / n_chunks, q = k - b * n_chunks;
-        return part[((b * n_ut + ut) * n_chunks + q) * JOIN_THREADS + j];
+    // (tiles are counted in 32 bits; a plan: one row)
+    const uint32_t all = plan != nullptr ? static_cast<uint32_t>(plan[0].x) : static_cast<uint32_t>(rows) * n_chunks;
+    const uint32_t k0 = static_cast<uint64_t>(all) * slice / JOIN_SLICES, k1 = static_cast<uint64_t>(all) * (slice + 1) / JOIN_SLICES;
+    auto at = [&](uint32_t k) {
+        const uint32_t b = k / static_cast<uint32_t>(n_chunks), q = k - b * n_chunks;
+        return part[((static_cast<int64_t>(b) * n_ut + ut) * n_chunks + q) * JOIN_THREADS + j];
     };
-    float t[4] = {};
-    int64_t k = k0;
-    for (; k + 4 <= k1; k += 4)
+    float t[8] = {};
+    uint32_t k = k0;
+    for (; k + 8 <= k1; k += 8)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] += at(k + e);
-    for (; k < k1; ++k) t[0] += at(k);
-    share[(static_cast<int64_t>(ut) * JOIN_SLICES + slice) * JOIN_THREADS + j] = (t[0] + t[1]) + (t[2] + t[3]);
+        for (int e = 0; e < 8; ++e) t[e] += at(k + e);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (k + e < k1) t[e] += at(k + e);
+#pragma unroll
+    for (int e = 4; e > 0; e /= 2)
+        for (int i = 0; i < e; ++i) t[i] += t[i + e];
+    share[(static_cast<int64_t>(ut) * JOIN_SLICES + slice) * JOIN_THREADS + j] = t[0];
     __threadfence();
     __syncthreads();
     if (j == 0) is_last = atomicAdd(count + ut, 1u) == JOIN_SLICES - 1;
