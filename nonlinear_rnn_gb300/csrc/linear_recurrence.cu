@@ -247,7 +247,11 @@ struct Shared {
     uint32_t tile[2];
 };
 
-constexpr int WIDE_GROUP = 4;   // chunks of a group where columns are many (spans of one group)
+// Chunks of a group where columns are many (spans of one group).  A chain has a hop a
+// group, about 1.3 us, which a chunk's longer work hides backward.  (16 x 16384 x 1024 bf16
+// forward in groups of 2, 4, 8: 386, 391, 402 us, but 8 x 32768: 562, 505 for 2, 4; backward
+// 717, 771, 975, and 847, 832.)
+template <bool REVERSE> constexpr int WIDE_GROUP = REVERSE ? 2 : 4;
 
 // Where a tile lies: row, first unit, chunk q of nq in the scan's order, its steps t0 .. (of a
 // sequence that ends before t_end), and its place among all chunks (slots, sums)
@@ -298,9 +302,10 @@ __device__ __forceinline__ int segment_of(const RecArgs &a, int t) {
 // steps; place: the warp in the scan's order; first: the state that the first span starts
 // from; ok: the tile's copies came.  Called by all threads; between() runs after the last
 // barrier.
-template <bool WIDE, bool CUTS, typename Fn>
+template <bool WIDE, bool REVERSE, bool CUTS, typename Fn>
 __device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int it, const Place &p, int place, int lane,
                                              const Map2 &m, float2 first, bool ok, Fn &&between) {
+    constexpr int GROUP = WIDE_GROUP<REVERSE>;
     const int q = p.q;
     const float2 nan = splat2(__int_as_float(0x7fffffff));
     float2 (&aggA)[NW][32] = s.aggA[it & 1], (&aggB)[NW][32] = s.aggB[it & 1];
@@ -316,20 +321,20 @@ __device__ __forceinline__ float2 carry_into(const RecArgs &a, Shared &s, int it
     unsigned long long *const slot = a.slots + p.at * UNITS + 2 * lane;
     float2 h = first;
     if constexpr (WIDE) {
-        const int g = q / WIDE_GROUP, before = q % WIDE_GROUP;
-        const bool closes = before + 1 == WIDE_GROUP && q + 1 < p.nq;
+        const int g = q / GROUP, before = q % GROUP;
+        const bool closes = before + 1 == GROUP && q + 1 < p.nq;
         const unsigned long long *const end = slot - (before + 1) * UNITS;   // the state after the group before
-        ulonglong2 v[WIDE_GROUP - 1], e = make_ulonglong2(SLOT_EMPTY, SLOT_EMPTY);
+        ulonglong2 v[GROUP - 1], e = make_ulonglong2(SLOT_EMPTY, SLOT_EMPTY);
         if (g > 0) e = peek2(end);
 #pragma unroll
-        for (int k = 1; k < WIDE_GROUP; ++k)   // chunk q - k
+        for (int k = 1; k < GROUP; ++k)   // chunk q - k
             if (k <= before) v[k - 1] = peek2(slot - k * UNITS);
         __syncthreads();
         between();
         if (place == 0 && !closes) publish2(slot, whole_tile());
         if (g > 0) h = await2(end, e, a).B;
 #pragma unroll
-        for (int k = WIDE_GROUP - 1; k > 0; --k)
+        for (int k = GROUP - 1; k > 0; --k)
             if (k <= before) h = apply<CUTS>(await2(slot - k * UNITS, v[k - 1], a), h);
         if (!ok) h = nan;
         if (place == 0 && closes) publish2(slot, Map2{splat2(0.f), apply<CUTS>(whole_tile(), h)});
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
         else compose(std::false_type{});
         if (WIDE && tid == 0) s.tile[(it + 1) & 1] = next;
         if (WIDE && lane == 0) bulk_wait_read<0>();   // this warp's result has left the tile before
-        float2 h = carry_into<WIDE, MODE == PACK>(a, s, it, p, warp, lane, m, first, ok, [&]() {
+        float2 h = carry_into<WIDE, false, MODE == PACK>(a, s, it, p, warp, lane, m, first, ok, [&]() {
             if (tid == 0) {
                 if (WIDE && next < n_tiles) start(next, buf ^ 1);
             }
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
         if (tails != 0 || valid < SEG) compose(std::true_type{});
         else compose(std::false_type{});
         uint32_t next = 0;
-        float2 nu = carry_into<WIDE, MODE == PACK>(a, s, it, p, NW - 1 - warp, lane, m, splat2(0.f), ok, [&]() {
+        float2 nu = carry_into<WIDE, true, MODE == PACK>(a, s, it, p, NW - 1 - warp, lane, m, splat2(0.f), ok, [&]() {
             if (WIDE && tid == 0) s.tile[(it + 1) & 1] = next = atomicAdd(a.ticket, 1u);
         });
         float2 g_wr = splat2(0.f), g_ba = splat2(0.f), g_bi = splat2(0.f);
@@ -793,9 +798,11 @@ struct Layout {
     int64_t slots, maps, ends, cleared, plan, part, share, total;   // plan 0: none
 };
 
-// Columns from which a call takes the WIDE form.  (16 x 16384 bf16 of 64, 128 columns: 188
-// and 128 us forward, 138 and 133 the other; fp32 of 64: 199 and 107.)
-constexpr int64_t WIDE_COLUMNS = 128;
+// Columns from which a call takes the WIDE form.  bf16 of 64 and 128 columns (16384 and 8192
+// steps) forward 188 and 128 us, 138 and 133 the other, backward 267 and 220, 240 and 243;
+// fp32 of 64, 128, 256 columns forward 2.7, 4.1, 6.2 TB/s, the other 5.0, backward of 128
+// 6.1, of 64 the other 4.9.
+constexpr int64_t wide_columns(int dtype, bool backward) { return dtype == NRNN_F32 && !backward ? 256 : 128; }
 
 // num_segments > 0: a pack.  Its segments are columns where they are enough of them for
 // the WIDE form, long enough (a segment adds a short chunk), and the plan is small.
@@ -805,13 +812,13 @@ Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, int64_t num_segment
     const int64_t steps = dtype == NRNN_BF16 ? Shape<__nv_bfloat16, false>::L : Shape<float, false>::L;
     y.n_ut = ceil_div(d, UNITS);
     const bool plan = B == 1 && num_segments >= 2 && num_segments <= PACK_PLAN_MAX_S && ceil_div(T, wide_steps) <= PACK_PLAN_MAX_CHUNKS &&
-                      8 * num_segments <= ceil_div(T, wide_steps) && num_segments * y.n_ut >= WIDE_COLUMNS;
+                      8 * num_segments <= ceil_div(T, wide_steps) && num_segments * y.n_ut >= wide_columns(dtype, backward);
     y.n_cols = B * y.n_ut;
-    y.wide = plan || y.n_cols >= WIDE_COLUMNS;
+    y.wide = plan || y.n_cols >= wide_columns(dtype, backward);
     y.n_chunks = ceil_div(T, y.wide ? wide_steps : steps) + (plan ? num_segments : 0);
-    // a chain has a hop a span (else, 2 to 3 us), and a chunk reads half a group's and half a
-    // span's maps on average
-    y.group = y.wide ? WIDE_GROUP : 16;
+    // where the warps share the maps before, a hop takes 2 to 3 us, and a chunk reads half a
+    // group's and half a span's maps on average
+    y.group = !y.wide ? 16 : backward ? WIDE_GROUP<true> : WIDE_GROUP<false>;
     y.span = y.wide ? 1 : 16;
     const int64_t groups = ceil_div(y.n_chunks, y.group);
     y.n_tiles = y.n_cols * y.n_chunks;
