@@ -128,7 +128,7 @@ def linear_recurrence_step(params, state: torch.Tensor | None, preact: torch.Ten
     code = _storage(preact)
     prm = _recurrence_params(params, d, preact.device)
     state = _rows(state, slots, d, preact, "state")
-    h = preact.new_empty((slots, d)) if out is None else _result(out, (slots, d), preact, "out")
+    h = _result(out, (slots, d), preact, "out")
     if state_out is None:
         state_out = torch.empty((slots, d), dtype=torch.float32, device=preact.device) if state is None \
             else torch.empty_like(state)

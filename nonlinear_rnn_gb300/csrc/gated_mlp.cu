@@ -89,6 +89,7 @@ struct GemmArgs {
     int bn;                   // columns of a tile: a multiple of 64, at most BN (UP: of both halves)
     int whole, units;         // DOWN, GX, GWI, GWO: row tiles of a team that are not cut, and all
     int side, teams;          // pairs of a team (its column tiles beside one another), teams
+    int share, longer;        // slices of cut tiles of a team: share, and one more of the first `longer`
     float *parts;             // [pairs][2][BM][bn] sums of cut tiles
     void *out;                // the result in the storage type, rows of N
     bool blocks_out;          // bf16: tmOut is over the result, whose blocks leave by TMA
@@ -108,8 +109,7 @@ template <int FORM> constexpr bool CUTS = FORM != UP && FORM != DH;
 constexpr int BAND = 8;
 
 template <int FORM> struct Walk {
-    int u, pairs, side_at;
-    int64_t pos, end;
+    int u, pairs, side_at, pos, end;
 
     __device__ Walk(const GemmArgs &a, int pair, int pairs_) : u(pair), pairs(pairs_), side_at(0), pos(0), end(0) {
         if (!CUTS<FORM>) return;
@@ -118,11 +118,15 @@ template <int FORM> struct Walk {
         if (u < a.teams) run(a, u, pos, end);
         else u = a.units;   // a pair left over
     }
-    // the run of team b
-    __device__ static void run(const GemmArgs &a, int b, int64_t &from, int64_t &to) {
-        const int64_t all = static_cast<int64_t>(a.units - a.whole) * a.kb;
-        from = all * b / a.teams;
-        to = all * (b + 1) / a.teams;
+    // the run of team b among the slices of the tiles that are cut
+    __device__ static void run(const GemmArgs &a, int b, int &from, int &to) {
+        from = b * a.share + min(b, a.longer);
+        to = from + a.share + (b < a.longer ? 1 : 0);
+    }
+    // the team whose run holds a slice
+    __device__ static int team_of(const GemmArgs &a, int slice) {
+        const int head = a.longer * (a.share + 1);
+        return slice < head ? slice / (a.share + 1) : a.longer + (slice - head) / a.share;
     }
     __device__ __forceinline__ bool next(const GemmArgs &a, Unit &t) {
         t.k0 = 0; t.k1 = a.kb; t.slot = -1;
@@ -141,9 +145,9 @@ template <int FORM> struct Walk {
             u += a.teams;
         } else {
             if (pos >= end) return false;
-            tile = a.whole + static_cast<int>(pos / a.kb);
-            t.k0 = static_cast<int>(pos % a.kb);
-            if (end - pos < a.kb - t.k0) t.k1 = t.k0 + static_cast<int>(end - pos);
+            tile = a.whole + pos / a.kb;
+            t.k0 = pos % a.kb;
+            if (end - pos < a.kb - t.k0) t.k1 = t.k0 + (end - pos);
             pos += t.k1 - t.k0;
             if (t.k0 > 0) t.slot = 0;
             else if (t.k1 < a.kb) t.slot = 1;
@@ -664,8 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
 
 // Adds the parts of the tiles that a launch of `pairs` pairs cut, in the order of their
 // slices.  blockIdx.x: a cut tile; blockIdx.y: JOIN_ROWS of its rows; a thread takes four
-// columns of a row, its loads eight parts ahead.  (A warp a row and its parts shared by a
-// CTA's warps where they were many: 11 us for 6 tiles in 12 parts, JOIN_MEASURED.)
+// columns of a row, its loads eight parts ahead.
 constexpr int JOIN_THREADS = 256, JOIN_ROWS = 4;
 
 template <int FORM, typename T>
@@ -675,22 +678,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_parts(const GemmArgs a) {
     const int tm = a.side > 1 ? tile : tile / a.tiles_n, tn = a.side > 1 ? side_at : tile % a.tiles_n;
     const bool second = FORM == GWI && tm >= a.m_half;
     const int m = (second ? tm - a.m_half : tm) * BM + row;
-    // the runs that hold slices of this tile: b0 .. b1
-    const int64_t all = static_cast<int64_t>(a.units - a.whole) * a.kb;
-    const int64_t first = static_cast<int64_t>(cut) * a.kb, stop = first + a.kb;
-    auto run_of = [&](int64_t slice) {   // the run that holds a slice
-        int b = static_cast<int>(slice * a.teams / all);
-        int64_t from, to;
-        for (Walk<FORM>::run(a, b, from, to); slice < from; Walk<FORM>::run(a, --b, from, to)) {}
-        for (; slice >= to; Walk<FORM>::run(a, ++b, from, to)) {}
-        return b;
-    };
-    const int b0 = run_of(first), b1 = run_of(stop - 1);
+    // the teams whose runs hold slices of this tile: b0 .. b1 (those without a slice are last)
+    const int b0 = Walk<FORM>::team_of(a, cut * a.kb), b1 = Walk<FORM>::team_of(a, cut * a.kb + a.kb - 1);
     const int n = min(min(a.bn, a.N - tn * a.bn) - c, 4);
     dependents_may_launch();
     wait_for_prerequisites();
     if (b0 == b1 || m >= a.M || n <= 0) return;   // (one run has it whole)
-    const bool dense = all >= a.teams;   // no run is empty
     const int64_t step = static_cast<int64_t>(2) * BM * a.bn * a.side;   // to the next team's
     const float *p = a.parts + b0 * step + (static_cast<int64_t>(side_at) * 2 * BM + row) * a.bn + c;
     float v[4] = {};
@@ -698,16 +691,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_parts(const GemmArgs a) {
         float x[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            bool some = q0 + i <= b1 - b0;
-            if (some && !dense) {
-                int64_t f, to;
-                Walk<FORM>::run(a, b0 + q0 + i, f, to);
-                some = f < to;
-            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
             // the first run's part begins with the tile: slot 1
-            if (some) load_f32<float, 4>(p + (q0 + i) * step + (q0 + i == 0 ? static_cast<int64_t>(BM) * a.bn : 0), x[i]);
+            if (q0 + i <= b1 - b0) load_f32<float, 4>(p + (q0 + i) * step + (q0 + i == 0 ? static_cast<int64_t>(BM) * a.bn : 0), x[i]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -1183,6 +1170,9 @@ cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, 
         a.teams = pairs / a.side;
         a.units = static_cast<int>(tiles / a.side);
         a.whole = a.units >= WAVES_UNCUT * a.teams ? a.units : a.units / a.teams * a.teams;
+        const int slices = (a.units - a.whole) * a.kb;   // (fits: `most` does)
+        a.share = slices / a.teams;
+        a.longer = slices % a.teams;
     }
     e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, tmPQ, a);
     const int64_t cut = static_cast<int64_t>(a.units - a.whole) * a.side;
