@@ -26,9 +26,9 @@
 //
 // UP and DH have many tiles; the others may have few and long inner dimensions.  Where
 // these are less than WAVES_UNCUT waves, whole waves of tiles go one to a pair and the
-// rest is cut by inner slices, an
-// equal run of the (tile, slice) sequence to every team of pairs; parts of a cut tile go
-// to the workspace in fp32 and k_join_parts adds them in order.
+// rest is cut by inner slices, an equal run of the (tile, slice) sequence to every team of
+// pairs; parts of a cut tile go to the workspace in fp32 and k_join_parts adds them in
+// order.
 //
 // For bf16, m (formed from unrounded a and b) is rounded before the second product, and
 // p, q, ga and gb where they are stored: an operand of the tensor cores is bf16, and a
@@ -40,6 +40,11 @@
 // accumulator takes at most 256 elements of the inner dimension before the epilogue adds
 // it to fp32 registers, as the tensor cores add less exactly than fp32 rounding does.
 // (An infinity leaves no number: in fp32 operands it counts as NaN.)
+//
+// Measured: a training step of 32768 rows of 1024 x 4096 bf16 1.78 ms (1.39 PFLOP/s; the
+// kernels apart, cool: UP 417 us, DOWN 161, DH 231, GX 303, GWI 318, GWO 168).  The forward
+// that keeps nothing runs at 1.7 PFLOP/s, the rate of cuBLAS kept up, that is, at the power
+// limit; keeping p and q costs 75 us for 0.54 GB.  1501 x 250 x 683 fp32, training: 127 us.
 //
 // Every wait is bounded.  One that gives up sets the call's error word (the workspace's
 // first) and the abort flag of both CTAs of the pair, which ends the other roles' waits
@@ -104,8 +109,9 @@ struct Unit { int tm, tn, k0, k1, slot; };   // slot: -1 = a whole tile
 template <int FORM> constexpr bool CUTS = FORM != UP && FORM != DH;
 
 // UP, DH: row tiles that the pairs work on at a time.  Their outputs (p, q and m; ga and
-// gb) pass through L2 and push out what lies there: with all row tiles against one column
-// tile after another, x came from HBM once a column tile.  BAND_MEASURED
+// gb) pass through L2 and push out what lies there, so a band's rows of x are taken while
+// they are there (all row tiles against one column tile after another: DH of 32768 x 1024
+// x 4096 bf16 280 us, in bands of 8 231; of 4 and 16 the step takes 1% longer).
 constexpr int BAND = 8;
 
 template <int FORM> struct Walk {
@@ -749,7 +755,8 @@ __global__ void __launch_bounds__(256) k_planes(const Copies c) {
 // these are the fragments of two products as they lie.  k_short_up: the 16 rows are 8
 // units' rows of Wg and of Wu, so a lane ends with a and b of the same unit and row of x;
 // a CTA's warps share the inner dimension.  k_short_down has its first weights under way
-// before it waits for m.  SHORT_MEASURED
+// before it waits for m.  8 rows over 1024 x 4096 bf16 (25 MB, 3.7 us of HBM) take 9.3 us
+// in a graph, 16 rows 14.
 constexpr int SHORT_MOST = 16, SHORT_AHEAD = 4, UP_WARPS = 8, DOWN_WARPS = 16;
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -880,10 +887,11 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32)
 
 // Other types and rows: on the fp32 cores, in groups of FEW_GROUP rows that read the
 // weights again, from L2; one group of bf16, FEW_MOST rows of fp32, whose weights'
-// planes would be more to write and read.  A warp of k_few_up takes
+// planes would be more to write and read (1024 x 4096: 8 rows 12 us, 32 37, 64 69, by the
+// planes 111).  A warp of k_few_up takes
 // UP_UNITS units at a time, the rows of Wg and Wu of each against every row of x from
 // shared memory; a CTA of k_few_down takes DOWN_ROWS rows of W_out, its warps a share of
-// the inner dimension each.  FEW_MEASURED
+// the inner dimension each.
 constexpr int FEW_GROUP = 8, FEW_MOST = 64, FEW_THREADS = 256, UP_UNITS = 2, FEW_AHEAD = 2;
 constexpr size_t FEW_X_BYTES = 96 * 1024;   // of the rows of x in shared memory
 constexpr int DOWN_ROWS = 4;
@@ -1089,12 +1097,30 @@ bool used_in_place(const void *p, int64_t row, int dtype) {
 // columns of a tile: equal tiles of whole 64-column blocks, `most` at most
 int tile_columns(int64_t N, int most = BN) { return static_cast<int>(ceil_div(ceil_div(N, ceil_div(N, most)), 64) * 64); }
 
-// The same, narrower where there are few tiles: down to one a pair for tiles that are not
-// cut (share 1), or half of one for those that are (2): then each is cut into fewer parts.
-// COLUMNS_MEASURED
-int tile_columns_for(int64_t tiles_m, int64_t N, int share, int most = BN) {
-    while (most > 64 && tiles_m * ceil_div(N, most) * share <= PAIRS) most /= 2;
-    return tile_columns(N, most);
+// The same, narrower where tiles are few.  UP and DH: the width that leaves the busiest pair
+// the least to do; a tile costs its columns and, for the rows that it reads again, about
+// 64 more (UP of 64 rows over 1024 x 4096: 64 tiles of half the width in one wave, 28.7 ->
+// 24.6 us forward; of 300 rows they would be two waves, 29.3 -> 36.9).  Tiles that are
+// cut: until one is cut in no more than CUT_MOST parts (backward of 1501 x 250 x 683, fp32
+// and bf16, uncared for 92 and 54 us, 12 parts 76 and 37, 6 parts 88 and 39; in two, 2000 x
+// 512 x 2048 fp32 would go from 192 to 334).
+constexpr int CUT_MOST = 12;
+int tile_columns_for(int64_t tiles_m, int64_t N, bool cut, int most = BN) {
+    int best = most;
+    int64_t least = INT64_MAX;
+    for (int bn = most; bn >= 64; bn /= 2) {
+        const int64_t tiles = tiles_m * ceil_div(N, bn);
+        const int64_t load = ceil_div(tiles, PAIRS) * (bn + 64);
+        if (!cut && load < least) {
+            least = load;
+            best = bn;
+        }
+        if (cut) {
+            best = bn;
+            if (tiles * CUT_MOST > PAIRS) break;
+        }
+    }
+    return tile_columns(N, best);
 }
 
 Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in_lies, bool w_out_lies, bool g_lies,
@@ -1215,7 +1241,7 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
     const void *x, *w_in, *w_out;
     if (operands<T>(c, p, nullptr, &x, &w_in, &w_out, nullptr) != cudaSuccess) return NRNN_ERR_CUDA;
     CUtensorMap ta, tb, to, tpq;
-    const int units = tile_columns_for(ceil_div(c.n, BM), c.f, 1, BN / 2);   // UP: a tile's units
+    const int units = tile_columns_for(ceil_div(c.n, BM), c.f, false, BN / 2);   // UP: a tile's units
     if (!map(&ta, x, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, BK, units) ||
         !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS) || (p.planes == 1 && !map(&tpq, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
@@ -1226,7 +1252,7 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
     a.pq = kept;
     a.pitch = static_cast<int>(p.pf);
     if (gemm<UP, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
-    const int bn = tile_columns_for(ceil_div(c.n, BM), c.d, 2);
+    const int bn = tile_columns_for(ceil_div(c.n, BM), c.d, true);
     a = args_of(c, c.n, c.d, c.f, bn);
     a.parts = reinterpret_cast<float *>(c.ws + p.parts);
     a.out = y;
@@ -1247,7 +1273,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     CUtensorMap ta, tb, to, tpq;
     float *parts = reinterpret_cast<float *>(c.ws + p.parts);
     // fp32: one piece of an epilogue warp holds ga and gb, so tiles of 128
-    int bn = tile_columns_for(ceil_div(c.n, BM), c.f, 1, p.planes != 1 ? 2 * PIECE : BN);
+    int bn = tile_columns_for(ceil_div(c.n, BM), c.f, false, p.planes != 1 ? 2 * PIECE : BN);
     GemmArgs a = args_of(c, c.n, c.f, c.d, bn);
     a.pq = const_cast<unsigned char *>(kept);
     a.pitch = static_cast<int>(p.pf);
@@ -1258,7 +1284,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     if (p.planes != 1) tpq = to;
     if (gemm<DH, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gx
-    bn = tile_columns_for(ceil_div(c.n, BM), c.d, 2);
+    bn = tile_columns_for(ceil_div(c.n, BM), c.d, true);
     a = args_of(c, c.n, c.d, c.f, bn);
     a.kb_half = a.kb;
     a.kb *= 2;
@@ -1270,7 +1296,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
         return NRNN_ERR_CUDA;
     if (gemm<GX, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_in
-    bn = tile_columns_for(2 * ceil_div(c.f, BM), c.d, 2);
+    bn = tile_columns_for(2 * ceil_div(c.f, BM), c.d, true);
     a = args_of(c, c.f, c.d, c.n, bn);
     a.m_half = a.tiles_m;
     a.tiles_m *= 2;
@@ -1282,7 +1308,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
         return NRNN_ERR_CUDA;
     if (gemm<GWI, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_out
-    bn = tile_columns_for(ceil_div(c.d, BM), c.f, 2);
+    bn = tile_columns_for(ceil_div(c.d, BM), c.f, true);
     a = args_of(c, c.d, c.f, c.n, bn);
     a.parts = parts;
     a.out = gW_out;
