@@ -670,7 +670,8 @@ size_t nrnn_linear_recurrence_workspace_bytes(int64_t B, int64_t T, int64_t d_h,
  *               word is 0 once the work is done, or not if a device wait gave up
  *               (nrnn_set_wait_limit_ns): then outputs are NaN where they depended
  *               on it.  So too in the backward
- * The outputs must not overlap one another or the inputs.  States are fp32 throughout; no result depends on the order in which threads run.
+ * The outputs must not overlap one another or the inputs (NRNN_ERR_INVALID_ARG).  States are
+ * fp32 throughout; no result depends on the order in which threads run.
  * A sigmoid is bounded below by 2^-63.
  */
 int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *params, int64_t B,
@@ -730,7 +731,8 @@ size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dt
  *               first 32-bit word is 0 once the work is done, or not if a device wait
  *               gave up (nrnn_set_wait_limit_ns): then outputs are NaN where they
  *               depended on it.  So too in the backward
- * The buffers of the tensors need only their element's alignment.
+ * The buffers of the tensors need only their element's alignment.  In both directions the
+ * outputs must not overlap one another or the inputs (NRNN_ERR_INVALID_ARG).
  */
 int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, int dtype,
                            int64_t rows, int64_t d, int64_t f, void *y, void *kept,

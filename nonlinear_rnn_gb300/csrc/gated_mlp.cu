@@ -1432,7 +1432,10 @@ int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, i
     if (st != NRNN_OK) return st;
     if (rows == 0) return NRNN_OK;
     const uintptr_t elem = dtype == NRNN_BF16 ? 2 : 4;
-    if (y == nullptr || reinterpret_cast<uintptr_t>(y) % elem != 0 || reinterpret_cast<uintptr_t>(kept) % 256 != 0)
+    const int64_t xb = rows * d * elem, wb = f * d * elem;
+    if (y == nullptr || reinterpret_cast<uintptr_t>(y) % elem != 0 || reinterpret_cast<uintptr_t>(kept) % 256 != 0 ||
+        !outputs_apart({{y, xb}, {kept, static_cast<int64_t>(nrnn_gated_mlp_kept_bytes(rows, f, dtype))}},
+                       {{x, xb}, {W_in, 2 * wb}, {W_out, wb}}))
         return NRNN_ERR_INVALID_ARG;
     if (kept == nullptr) {
         const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(W_in) |
@@ -1459,10 +1462,14 @@ int nrnn_gated_mlp_backward(const void *x, const void *W_in, const void *W_out, 
     const int st = check(c);
     if (st != NRNN_OK) return st;
     const uintptr_t elem = dtype == NRNN_BF16 ? 2 : 4;
+    const int64_t xb = rows * d * elem, wb = f * d * elem;
     if (gW_in == nullptr || gW_out == nullptr ||
         (rows > 0 && (g == nullptr || gx == nullptr || kept == nullptr || reinterpret_cast<uintptr_t>(kept) % 256 != 0)) ||
         (reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(gx) | reinterpret_cast<uintptr_t>(gW_in) |
-         reinterpret_cast<uintptr_t>(gW_out)) % elem != 0)
+         reinterpret_cast<uintptr_t>(gW_out)) % elem != 0 ||
+        !outputs_apart({{gx, xb}, {gW_in, 2 * wb}, {gW_out, wb}},
+                       {{x, xb}, {W_in, 2 * wb}, {W_out, wb}, {g, xb},
+                        {kept, static_cast<int64_t>(nrnn_gated_mlp_kept_bytes(rows, f, dtype))}}))
         return NRNN_ERR_INVALID_ARG;
     if (rows == 0)
         return cudaMemsetAsync(gW_in, 0, elem * 2 * f * d, c.stream) == cudaSuccess &&

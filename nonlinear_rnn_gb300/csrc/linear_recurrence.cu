@@ -866,12 +866,6 @@ int check(const void *P, int dtype, const float *params, int64_t B, int64_t T, i
     return NRNN_OK;
 }
 
-bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
-    if (a == nullptr || b == nullptr || a_bytes == 0 || b_bytes == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + b_bytes && y < x + a_bytes;
-}
-
 bool usable(const void *ws, size_t have, int64_t need) {
     return ws != nullptr && reinterpret_cast<uintptr_t>(ws) % 256 == 0 && have >= static_cast<size_t>(need);
 }
@@ -997,11 +991,10 @@ int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *p
     const int st = check(preact, dtype, params, B, T, d_h, cu_seqlens, num_segments);
     if (st != NRNN_OK) return st;
     const int64_t es = dtype == NRNN_BF16 ? 2 : 4, n = B * T * d_h;
-    const int64_t rows = cu_seqlens != nullptr ? num_segments : B;
+    const int64_t rows = cu_seqlens != nullptr ? num_segments : B, sb = rows * d_h * 4;
     if ((n > 0 && (H == nullptr || !aligned16(H))) || !aligned16(state) || !aligned16(last) ||
-        overlap(preact, 3 * n * es, H, n * es) || overlap(state, rows * d_h * 4, H, n * es) ||
-        overlap(state, rows * d_h * 4, last, rows * d_h * 4) || overlap(preact, 3 * n * es, last, rows * d_h * 4) ||
-        overlap(H, n * es, last, rows * d_h * 4))
+        !outputs_apart({{H, n * es}, {last, sb}},
+                       {{preact, 3 * n * es}, {params, 12 * d_h}, {state, sb}, {cu_seqlens, 4 * (rows + 1)}}))
         return NRNN_ERR_INVALID_ARG;
     const Layout y = layout_of(B, T, d_h, dtype, cu_seqlens != nullptr ? num_segments : 0, false);
     if (!usable(workspace, ws_bytes, y.total)) return NRNN_ERR_WORKSPACE;
@@ -1027,9 +1020,9 @@ int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *
     const int64_t rows = cu_seqlens != nullptr ? num_segments : B, sb = rows * d_h * 4;
     if (gparams == nullptr || !aligned16(gparams) || !aligned16(state) || !aligned16(g_last) || !aligned16(g_state) ||
         (n > 0 && (H == nullptr || gH == nullptr || gP == nullptr || !aligned16(H) || !aligned16(gH) || !aligned16(gP))) ||
-        overlap(preact, 3 * n * es, gP, 3 * n * es) || overlap(H, n * es, gP, 3 * n * es) ||
-        overlap(gH, n * es, gP, 3 * n * es) || overlap(state, sb, g_state, sb) || overlap(g_last, sb, g_state, sb) ||
-        overlap(gP, 3 * n * es, g_state, sb))
+        !outputs_apart({{gP, 3 * n * es}, {gparams, 12 * d_h}, {g_state, sb}},
+                       {{preact, 3 * n * es}, {params, 12 * d_h}, {state, sb}, {cu_seqlens, 4 * (rows + 1)},
+                        {H, n * es}, {gH, n * es}, {g_last, sb}}))
         return NRNN_ERR_INVALID_ARG;
     const Layout y = layout_of(B, T, d_h, dtype, cu_seqlens != nullptr ? num_segments : 0, true);
     if (!usable(workspace, ws_bytes, y.total)) return NRNN_ERR_WORKSPACE;
@@ -1068,9 +1061,8 @@ int nrnn_linear_recurrence_step(const void *preact, int dtype, const float *para
     const int64_t es = dtype == NRNN_BF16 ? 2 : 4, n = slots * d_h;
     if (n == 0) return NRNN_OK;
     if (h == nullptr || state_out == nullptr || !aligned16(h) || !aligned16(state_out) || !aligned16(state) ||
-        overlap(preact, 3 * n * es, h, n * es) || overlap(preact, 3 * n * es, state_out, 4 * n) ||
-        overlap(h, n * es, state_out, 4 * n) || overlap(h, n * es, state, 4 * n) ||
-        (state != state_out && overlap(state, 4 * n, state_out, 4 * n)))
+        !outputs_apart({{h, n * es}, {state_out, 4 * n}}, {{preact, 3 * n * es}, {params, 12 * d_h}}) ||
+        !outputs_apart({{h, n * es}, {state != state_out ? state_out : nullptr, 4 * n}}, {{state, 4 * n}}))
         return NRNN_ERR_INVALID_ARG;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t pairs = n / 2, blocks = ceil_div(pairs, 256);

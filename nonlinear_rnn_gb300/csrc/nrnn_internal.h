@@ -7,8 +7,28 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 
 namespace nrnn {
+
+// A buffer of a call; none where the pointer is null or the length zero
+struct Buffer { const void *at; int64_t bytes; };
+
+// no output shares memory with an input or with another output
+inline bool outputs_apart(std::initializer_list<Buffer> outs, std::initializer_list<Buffer> ins) {
+    auto meet = [](const Buffer &a, const Buffer &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+        return a.at != nullptr && b.at != nullptr && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (const Buffer *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Buffer &in : ins)
+            if (meet(*o, in)) return false;
+        for (const Buffer *other = o + 1; other != outs.end(); ++other)
+            if (meet(*o, *other)) return false;
+    }
+    return true;
+}
+
 
 // Runs configure(device) for the current device unless it already succeeded
 // there (kernel attributes are per device).  Ordinals >= 64 configure on every

@@ -29,7 +29,7 @@ def test_linear_recurrence_refusals():
         return lib.nrnn_linear_recurrence_forward(P, dtype, prm, B, T, d, cu, S, state, H, last, ws, wsb, None)
 
     def backward(P=P, dtype=0, prm=FAKE, B=1, T=8, d=16, cu=None, S=0, state=state, H=H, gH=gH, g_last=state, gP=gP,
-                 gprm=FAKE, g_state=last, ws=WS, wsb=BIG):
+                 gprm=at(8 << 24), g_state=last, ws=WS, wsb=BIG):
         return lib.nrnn_linear_recurrence_backward(P, dtype, prm, B, T, d, cu, S, state, H, gH, g_last, gP, gprm, g_state,
                                                    ws, wsb, None)
     for call in (forward, backward):
@@ -83,10 +83,11 @@ def test_gated_mlp_refusals(dtype):
     assert size(100, 0, 24, dtype, 0) == size(100, 16, 24, 7, 1) == size((1 << 30) + 1, 16, 24, dtype, 0) == 0
     assert size(100, 16, 24, dtype, 3) == size(100, 16, 24, dtype, -1) == 0 < size(4, 16, 24, dtype, 0) < size(4, 16, 24, dtype, 2)
 
-    def forward(x=FAKE, Wi=FAKE, Wo=FAKE, dtype=dtype, n=100, d=16, f=24, y=FAKE, kept=WS, ws=WS, wsb=BIG):
+    def forward(x=FAKE, Wi=FAKE, Wo=FAKE, dtype=dtype, n=100, d=16, f=24, y=at(1 << 24), kept=WS, ws=WS, wsb=BIG):
         return lib.nrnn_gated_mlp_forward(x, Wi, Wo, dtype, n, d, f, y, kept, ws, wsb, None)
 
-    def backward(x=FAKE, Wi=FAKE, Wo=FAKE, dtype=dtype, n=100, d=16, f=24, kept=WS, g=FAKE, gx=FAKE, gWi=FAKE, gWo=FAKE,
+    def backward(x=FAKE, Wi=FAKE, Wo=FAKE, dtype=dtype, n=100, d=16, f=24, kept=WS, g=FAKE, gx=at(1 << 24),
+                 gWi=at(2 << 24), gWo=at(3 << 24),
                  ws=WS, wsb=BIG):
         return lib.nrnn_gated_mlp_backward(x, Wi, Wo, kept, g, dtype, n, d, f, gx, gWi, gWo, ws, wsb, None)
     for call in (forward, backward):
@@ -142,3 +143,53 @@ def test_bindings_want_device_tensors():
                  lambda: nr.gated_mlp_backward(x, torch.zeros(6, 8), torch.zeros(8, 3), x, x)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_recurrence_outputs_apart():
+    """Every output against every input and every other output, at equal and at
+    partly covered addresses: 3 x 8 steps of 16 units in fp32."""
+    lib = nr.load()
+    names = ("P", "prm", "state", "H", "gH", "g_last", "gP", "gprm", "g_state", "last")
+    far = {k: (i + 1) << 24 for i, k in enumerate(names)}
+
+    def forward(**k):
+        a = {n: at(v) for n, v in {**far, **k}.items()}
+        return lib.nrnn_linear_recurrence_forward(a["P"], 0, a["prm"], 3, 8, 16, None, 0, a["state"], a["H"], a["last"], WS,
+                                                  16, None)
+
+    def backward(**k):
+        a = {n: at(v) for n, v in {**far, **k}.items()}
+        return lib.nrnn_linear_recurrence_backward(a["P"], 0, a["prm"], 3, 8, 16, None, 0, a["state"], a["H"], a["gH"],
+                                                   a["g_last"], a["gP"], a["gprm"], a["g_state"], WS, 16, None)
+    assert forward() == backward() == -7                         # only the workspace is too small
+    for call, outs, ins in ((forward, ("H", "last"), ("P", "prm", "state")),
+                            (backward, ("gP", "gprm", "g_state"), ("P", "prm", "state", "H", "gH", "g_last"))):
+        for o in outs:
+            for other in (*ins, *(p for p in outs if p != o)):
+                assert call(**{o: far[other]}) == -1, (o, other)
+                assert call(**{o: far[other] + 64}) == -1, (o, other)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("n", [4, 100])
+def test_gated_mlp_outputs_apart(dtype, n):
+    """The same of the feed-forward block, at a decode step's rows and more."""
+    lib = nr.load()
+    names = ("x", "Wi", "Wo", "kept", "g", "y", "gx", "gWi", "gWo")
+    far = {k: (i + 1) << 24 for i, k in enumerate(names)}
+
+    def forward(**k):
+        a = {m: at(v) for m, v in {**far, **k}.items()}
+        return lib.nrnn_gated_mlp_forward(a["x"], a["Wi"], a["Wo"], dtype, n, 64, 128, a["y"], a["kept"], WS, 16, None)
+
+    def backward(**k):
+        a = {m: at(v) for m, v in {**far, **k}.items()}
+        return lib.nrnn_gated_mlp_backward(a["x"], a["Wi"], a["Wo"], a["kept"], a["g"], dtype, n, 64, 128, a["gx"], a["gWi"],
+                                           a["gWo"], WS, 16, None)
+    assert forward() == backward() == -7
+    for call, outs, ins in ((forward, ("y", "kept"), ("x", "Wi", "Wo")),
+                            (backward, ("gx", "gWi", "gWo"), ("x", "Wi", "Wo", "kept", "g"))):
+        for o in outs:
+            for other in (*ins, *(p for p in outs if p != o)):
+                assert call(**{o: far[other]}) == -1, (o, other)
+                assert call(**{o: far[other] + 256}) == -1, (o, other)
