@@ -42,7 +42,7 @@
 // (An infinity leaves no number: in fp32 operands it counts as NaN.)
 //
 // Measured: a training step of 32768 rows of 1024 x 4096 bf16 1.78 ms (1.39 PFLOP/s; the
-// kernels apart, cool: UP 417 us, DOWN 161, DH 231, GX 303, GWI 318, GWO 168).  The forward
+// kernels apart, under a profiler: UP 417 us, DOWN 166, DH 231, GX 303, GWI 321, GWO 169).  The forward
 // that keeps nothing runs at 1.7 PFLOP/s, the rate of cuBLAS kept up, that is, at the power
 // limit; keeping p and q costs 75 us for 0.54 GB.  1501 x 250 x 683 fp32, training: 127 us.
 //
@@ -1102,7 +1102,7 @@ int tile_columns(int64_t N, int most = BN) { return static_cast<int>(ceil_div(ce
 // 64 more (UP of 64 rows over 1024 x 4096: 64 tiles of half the width in one wave, 28.7 ->
 // 24.6 us forward; of 300 rows they would be two waves, 29.3 -> 36.9).  Tiles that are
 // cut: until one is cut in no more than CUT_MOST parts (backward of 1501 x 250 x 683, fp32
-// and bf16, uncared for 92 and 54 us, 12 parts 76 and 37, 6 parts 88 and 39; in two, 2000 x
+// and bf16, at their widest 92 and 54 us, 12 parts 76 and 37, 6 parts 88 and 39; in two, 2000 x
 // 512 x 2048 fp32 would go from 192 to 334).
 constexpr int CUT_MOST = 12;
 int tile_columns_for(int64_t tiles_m, int64_t N, bool cut, int most = BN) {

@@ -225,7 +225,7 @@ __device__ __forceinline__ bool there(const ulonglong2 &v) { return v.x != SLOT_
 __device__ __forceinline__ Map2 map_of(const ulonglong2 &v) {
     return Map2{make_float2(pair_A(v.x), pair_A(v.y)), make_float2(pair_b(v.x), pair_b(v.y))};
 }
-// waits for a slot; false (and NaN) if it gave up or another wait of the call did
+// waits for a slot; a map of NaN if it gave up or another wait of the call did
 __device__ __forceinline__ Map2 await2(const unsigned long long *slot, ulonglong2 v, const RecArgs &a) {
     if (!there(v)) {
         const uint64_t t0 = globaltimer_ns();
