@@ -253,3 +253,20 @@ def test_streams_and_capture(n, t):
     y3, kept3 = nr.gated_mlp(x, W_in, W_out, keep=True)
     r3 = nr.gated_mlp_backward(x, W_in, W_out, kept3, g)
     assert torch.equal(yg, y3) and all(torch.equal(p, q) for p, q in zip(rg, r3))
+
+
+def test_offsets_beyond_32_bits():
+    """The last rows of more than 2^32 kept values; with g zero before them the gradients
+    of the weights are theirs too."""
+    n, d, f, k = (1 << 20) + 77, 8, 4104, 300
+    assert n * f > 1 << 32
+    x, W_in, W_out, g = inputs(n, d, f, torch.bfloat16, 5)
+    g[:-k] = 0
+    y, kept = nr.gated_mlp(x, W_in, W_out, keep=True)
+    gx, gWi, gWo = nr.gated_mlp_backward(x, W_in, W_out, kept, g)
+    ry, ey, rx, ex, ri, ei, ro, eo = reference(x[-k:], W_in, W_out, g[-k:])
+    check(y[-k:], ry, ey, "y")
+    check(gx[-k:], rx, ex, "gx")
+    check(gWi, ri, ei, "gW_in")
+    check(gWo, ro, eo, "gW_out")
+    assert not bool(gx[:-k].any())

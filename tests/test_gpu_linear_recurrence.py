@@ -423,3 +423,32 @@ def test_refusals():
     for call in (lambda: nr.linear_recurrence(P.double(), params), lambda: nr.linear_recurrence(P[..., :36], params[:, :12])):
         with pytest.raises(TypeError):
             call()
+
+
+def test_offsets_beyond_32_bits():
+    """The last steps of more than 2^32 preactivations against a call over them alone.
+
+    Decays are at most exp(-0.5 sig(-2.7)) < 0.97, so that 0.97^2000 < 2^-80 of what came
+    before is left.  Two scans of the same steps in other groups differ by at most their
+    errors: (4 + 2 fall) 2^-21 of magnitudes below 32, 33 times over (1 / (1 - 0.97)),
+    with fall <= 1: 33 * 32 * 6 * 2^-21 < 2^-8 each, and a result's rounding."""
+    T, d, n = 1400003, 1024, 4000
+    g = gen(7)
+    P = torch.empty(1, T, 3 * d, dtype=torch.bfloat16, device="cuda").uniform_(-2.5, 2.5, generator=g)
+    assert P.numel() > 1 << 32
+    params = torch.stack([torch.rand(d, generator=g, device="cuda") / 2 + 0.5, randn(g, d, std=0.05).clamp(-0.2, 0.2),
+                          torch.zeros(d, device="cuda")])
+
+    def same(got, want):
+        got, want = got.to(F64), want.to(F64)
+        return bool(((got - want).abs() <= 2.0 ** -8 * (got.abs() + want.abs()) + 2.0 ** -7).all()) and \
+            bool(want.abs().max() < 32) and bool(want.abs().max() > 0.5)
+    H, last = nr.linear_recurrence(P, params)
+    tail = P[:, -n:].contiguous()
+    H_tail, last_tail = nr.linear_recurrence(tail, params)
+    assert same(H[:, -n // 2:], H_tail[:, -n // 2:]) and same(last, last_tail)
+    gH = torch.empty(1, T, d, dtype=torch.bfloat16, device="cuda").uniform_(-1, 1, generator=g)
+    gP = nr.linear_recurrence_backward(P, params, H, gH).gP
+    gP_tail = nr.linear_recurrence_backward(tail, params, H[:, -n:].contiguous(), gH[:, -n:].contiguous(),
+                                            state=H[:, -n - 1].float().contiguous()).gP
+    assert same(gP[:, -n // 2:], gP_tail[:, -n // 2:])
