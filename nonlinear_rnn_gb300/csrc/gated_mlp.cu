@@ -674,11 +674,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
 
 // Adds the parts of the tiles that a launch of `pairs` pairs cut, in the order of their
 // slices.  blockIdx.x: a cut tile; blockIdx.y: JOIN_ROWS of its rows; a thread takes four
-// columns of a row, its loads eight parts ahead.
-constexpr int JOIN_THREADS = 256, JOIN_ROWS = 4;
+// columns of JOIN_EACH rows, its loads JOIN_AHEAD parts ahead.  (Backward of 300 and of 8192
+// rows over 1024 x 4096 bf16: 1 row, 8 ahead 72 and 306 us; 2 and 4 67 and 295; 4 and 4 67 and 298.)
+constexpr int JOIN_THREADS = 256, JOIN_EACH = 2, JOIN_AHEAD = 4, JOIN_ROWS = JOIN_THREADS / (BN / 4) * JOIN_EACH;
 
 template <int FORM, typename T>
 __global__ void __launch_bounds__(JOIN_THREADS) k_join_parts(const GemmArgs a) {
+    constexpr int APART = JOIN_THREADS / (BN / 4);   // rows between a thread's
     const int cut = blockIdx.x / a.side, tile = a.whole + cut, side_at = blockIdx.x % a.side;
     const int row = blockIdx.y * JOIN_ROWS + threadIdx.x / (BN / 4), c = threadIdx.x % (BN / 4) * 4;
     const int tm = a.side > 1 ? tile : tile / a.tiles_n, tn = a.side > 1 ? side_at : tile % a.tiles_n;
@@ -692,28 +694,39 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_join_parts(const GemmArgs a) {
     if (b0 == b1 || m >= a.M || n <= 0) return;   // (one run has it whole)
     const int64_t step = static_cast<int64_t>(2) * BM * a.bn * a.side;   // to the next team's
     const float *p = a.parts + b0 * step + (static_cast<int64_t>(side_at) * 2 * BM + row) * a.bn + c;
-    float v[4] = {};
-    for (int q0 = 0; q0 <= b1 - b0; q0 += 8) {
-        float x[8][4];
+    const int apart = APART * a.bn;
+    float v[JOIN_EACH][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+    for (int j = 0; j < JOIN_EACH; ++j)   // the first run's part begins with the tile: slot 1
+        load_f32<float, 4>(p + static_cast<int64_t>(BM) * a.bn + j * apart, v[j]);
+    p += step;
+    for (int left = b1 - b0; left > 0; left -= JOIN_AHEAD) {
+        float x[JOIN_AHEAD][JOIN_EACH][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
-            // the first run's part begins with the tile: slot 1
-            if (q0 + i <= b1 - b0) load_f32<float, 4>(p + (q0 + i) * step + (q0 + i == 0 ? static_cast<int64_t>(BM) * a.bn : 0), x[i]);
-        }
+        for (int i = 0; i < JOIN_AHEAD; ++i, p += step)
+            if (i < left)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+                for (int j = 0; j < JOIN_EACH; ++j) load_f32<float, 4>(p + j * apart, x[i][j]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += x[i][e];
+        for (int i = 0; i < JOIN_AHEAD; ++i)
+            if (i < left)
+#pragma unroll
+                for (int j = 0; j < JOIN_EACH; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[j][e] += x[i][j][e];
     }
     T *to = static_cast<T *>(a.out) + ((second ? a.M : 0) + static_cast<int64_t>(m)) * a.N + tn * a.bn + c;
-    if (a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(T)) == 0) {
-        store_f32<T, 4>(to, v);
-    } else {
+    const bool wide = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(T)) == 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < n) to[e] = from_f32<T>(v[e]);
+    for (int j = 0; j < JOIN_EACH; ++j, to += static_cast<int64_t>(APART) * a.N) {
+        if (m + j * APART >= a.M) break;
+        if (wide) {
+            store_f32<T, 4>(to, v[j]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n) to[e] = from_f32<T>(v[j][e]);
+        }
     }
 }
 
