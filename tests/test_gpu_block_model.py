@@ -119,3 +119,25 @@ def test_training_runs():
     from language_model import train
     losses = train(8, vocab=100, d=64, blocks=2, B=4, T=48, cell="linear", mlp=2, p=0.1)
     assert len(losses) == 8 and all(v == v and abs(v) < 100 for v in losses)
+
+
+def test_readme_usage():
+    """The README's example of the block's operators at a small size."""
+    d, f = 64, 256
+    x = torch.randn(2, 100, d, device="cuda", dtype=torch.bfloat16)
+    W_x = torch.randn(3 * d, d, device="cuda", dtype=torch.bfloat16) / 8
+    rate = torch.rand(d, device="cuda") * 0.5 + 0.01
+    rec = torch.stack([rate, torch.zeros_like(rate), torch.zeros_like(rate)])
+    P = nr.input_projection(x, W_x)
+    H, last = nr.linear_recurrence(P, rec)
+    g = nr.linear_recurrence_backward(P, rec, H, torch.ones_like(H))
+    h, last2 = nr.linear_recurrence_step(rec, last, P[:, -1])
+    W_in = torch.randn(2 * f, d, device="cuda", dtype=torch.bfloat16) / 8
+    W_out = torch.randn(d, f, device="cuda", dtype=torch.bfloat16) / 16
+    y, kept = nr.gated_mlp(x, W_in, W_out, keep=True)
+    z = nr.dropout(y, 0.1, seed=1, offset=0, residual=x)
+    gy = nr.dropout(torch.ones_like(z), 0.1, seed=1, offset=0)
+    grads = nr.gated_mlp_backward(x, W_in, W_out, kept, gy)
+    assert g.gP.shape == P.shape and h.shape == (2, d) and z.shape == x.shape
+    assert torch.equal(gy == 0, (z == x) & (gy == 0))       # what is dropped leaves the residual
+    assert all(bool(t.isfinite().all()) for t in (H, last, last2, z, *g[:2], *grads))
