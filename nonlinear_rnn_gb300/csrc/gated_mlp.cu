@@ -17,7 +17,7 @@
 //                    rows of Wg, the other the same rows of Wu.  The accumulator then
 //                    holds a and b of the same 128 units beside one another, and the
 //                    epilogue forms m without either having been stored.  With the
-//                    gradient to come p and q are kept, in the storage type.
+//                    gradient to come p and q are kept: fp32, or for bf16 24 bits of them.
 //   DOWN m W_out^T
 //   DH   g W_out     gm, from which the epilogue forms ga and gb by the kept p and q
 //   GX   [ga gb] W_in          the inner dimension runs over ga, then gb
@@ -31,9 +31,11 @@
 // order.
 //
 // For bf16, m (formed from unrounded a and b) is rounded before the second product, and
-// p, q, ga and gb where they are stored: an operand of the tensor cores is bf16, and a
-// second plane of each would double every product.  y and gW_out are 1.41 times as far
-// off as rounding the exact result once, gx and gW_in 1.8 times.
+// ga and gb (formed from unrounded gm) before theirs: an operand of the tensor cores is
+// bf16, and a second plane of each would double these products.  So every result is 1.41
+// times as far off as rounding the exact one once: two roundings.  p and q are no operands
+// and keep 16 bits of significand, 2^-15 at most off, as one of 2^-9 more would make gx and
+// gW_in 1.73 times as far off.
 //
 // fp32 operands are split into three bf16 planes, v = hi + mid + lo up to 2^-24, and a
 // product is the six plane products above 2^-24 relative, smallest first.  An
@@ -44,7 +46,7 @@
 // Measured: a training step of 32768 rows of 1024 x 4096 bf16 1.78 ms (1.39 PFLOP/s; the
 // kernels apart, under a profiler: UP 417 us, DOWN 166, DH 231, GX 303, GWI 321, GWO 169).  The forward
 // that keeps nothing runs at 1.7 PFLOP/s, the rate of cuBLAS kept up, that is, at the power
-// limit; keeping p and q costs 75 us for 0.54 GB.  1501 x 250 x 683 fp32, training: 127 us.
+// limit; keeping p and q costs 50 to 60 us for 0.81 GB.  1501 x 250 x 683 fp32, training: 127 us.
 //
 // Every wait is bounded.  One that gives up sets the call's error word (the workspace's
 // first) and the abort flag of both CTAs of the pair, which ends the other roles' waits
@@ -78,8 +80,8 @@ __device__ constexpr int PLANE_A[SEGMENTS] = {2, 1, 0, 1, 0, 0};
 __device__ constexpr int PLANE_B[SEGMENTS] = {0, 1, 2, 0, 1, 0};
 
 // staged blocks of an epilogue warp, and the stages that they leave room for
-template <int FORM, typename T> constexpr int blocks_of() { return sizeof(T) == 4 ? 1 : FORM == UP ? 3 : FORM == DH ? 2 : 1; }
-template <int FORM, typename T> constexpr int stages_of() { return blocks_of<FORM, T>() == 3 ? 4 : blocks_of<FORM, T>() == 2 ? 5 : 6; }
+template <int FORM, typename T> constexpr int blocks_of() { return sizeof(T) == 2 && FORM == DH ? 2 : 1; }
+template <int FORM, typename T> constexpr int stages_of() { return blocks_of<FORM, T>() == 2 ? 5 : 6; }
 template <int FORM, typename T> constexpr size_t gemm_smem() {
     return stages_of<FORM, T>() * STAGE_BYTES + EPI_WARPS * blocks_of<FORM, T>() * BOX_BYTES + 1024;
 }
@@ -99,8 +101,9 @@ struct GemmArgs {
     void *out;                // the result in the storage type, rows of N
     bool blocks_out;          // bf16: tmOut is over the result, whose blocks leave by TMA
     bool keep;                // UP: p and q are stored
-    void *pq;                 // p and q, [2][M][pitch] in the storage type
+    void *pq;                 // p and q: fp32 [2][M][pitch]; bf16 blocks of KEPT_ROWS x KEPT_COLS
     int pitch;
+    int kept_cols;            // bf16: blocks beside one another
 };
 
 // A unit is what a pair takes at a time: a tile, or a tile's slices k0 .. k1
@@ -175,6 +178,42 @@ __device__ __forceinline__ float gate(float &a, float &b) {
     return m;
 }
 
+// bf16: p and q as kept, without the low 8 of their 32 bits.  A block is 32 rows of 16
+// columns, a lane's row in six pieces of 16 bytes, a piece of all lanes side by side: the
+// upper halves of p and of q, two pieces each, then the third bytes of p and of q.  So the
+// epilogue that forms them and the one that takes them both move whole lines, from and to
+// the registers, past what L2 has better use for.  (Rows beyond M and columns beyond N of the
+// last blocks hold zeros.)  Against bf16 rows through shared memory, both directions of 8192
+// and of 32768 rows over 1024 x 4096: 452 and 1704 us before, 446 and 1694 now, with half as
+// many bytes more.
+constexpr int KEPT_ROWS = 32, KEPT_COLS = 16, KEPT_PIECES = 6, KEPT_BYTES = KEPT_PIECES * KEPT_ROWS * 16;
+
+// a lane's piece 0 of the block at row y, column x; piece j is KEPT_ROWS j further on
+__device__ __forceinline__ uint4 *kept_at(const GemmArgs &a, int y, int x, int lane) {
+    return static_cast<uint4 *>(a.pq) +
+           (static_cast<int64_t>(y / KEPT_ROWS) * a.kept_cols + x / KEPT_COLS) * (KEPT_BYTES / 16) + lane;
+}
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+// upper halves of 8 values; third bytes of 16
+__device__ __forceinline__ uint4 upper_halves(const float *v) {
+    return make_uint4(__byte_perm(bits(v[0]), bits(v[1]), 0x7632), __byte_perm(bits(v[2]), bits(v[3]), 0x7632),
+                      __byte_perm(bits(v[4]), bits(v[5]), 0x7632), __byte_perm(bits(v[6]), bits(v[7]), 0x7632));
+}
+__device__ __forceinline__ uint32_t third_bytes_of_4(const float *v) {
+    return __byte_perm(__byte_perm(bits(v[0]), bits(v[1]), 0x0051), __byte_perm(bits(v[2]), bits(v[3]), 0x0051), 0x5410);
+}
+__device__ __forceinline__ uint4 third_bytes(const float *v) {
+    return make_uint4(third_bytes_of_4(v), third_bytes_of_4(v + 4), third_bytes_of_4(v + 8), third_bytes_of_4(v + 12));
+}
+// Two values of a word of upper halves and the bytes k, k + 1 of a word of third bytes.  The
+// third byte stands in for the fourth too: zeros, infinities and NaN stay what they are, and
+// the dropped bits are replaced by as many on average.
+__device__ __forceinline__ float2 kept_pair(uint32_t upper, uint32_t third, int k) {
+    return make_float2(__uint_as_float(__byte_perm(upper, third, 0x1000 | (4 + k) * 0x11)),
+                       __uint_as_float(__byte_perm(upper, third, 0x3200 | (5 + k) * 0x11)));
+}
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
 template <int FORM> __device__ constexpr bool mn_a() { return FORM == GWI || FORM == GWO; }
 template <int FORM> __device__ constexpr bool mn_b() { return FORM != UP && FORM != DOWN; }
 
@@ -189,7 +228,7 @@ template <int FORM> __device__ __forceinline__ uint32_t stage_bytes(const GemmAr
 template <int FORM, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     k_mlp_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPQ, const GemmArgs a) {
+               const __grid_constant__ CUtensorMap tmOut, const GemmArgs a) {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr bool MN_A = mn_a<FORM>(), MN_B = mn_b<FORM>();
     constexpr int STAGES = stages_of<FORM, T>(), BLOCKS = blocks_of<FORM, T>();
@@ -197,8 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     extern __shared__ unsigned char dsmem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], accf_bar[2], acce_bar[2],
-        drain_bar, pq_bar[EPI_WARPS];
+    __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], accf_bar[2], acce_bar[2], drain_bar;
     __shared__ uint32_t s_tmem;
     __shared__ volatile uint32_t s_abort;     // a role of either CTA gave up
     __shared__ volatile int s_issued[2];      // rank 0's: stages that each producer went through
@@ -214,7 +252,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             mbar_init(&accf_bar[b], 1);
             mbar_init(&acce_bar[b], 2 * EPI_WARPS);   // rank 0's: both epilogues
         }
-        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(&pq_bar[w], 1);
         mbar_init(&drain_bar, 1);
         s_abort = 0;
         fence_mbar_init();
@@ -332,7 +369,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         unsigned char *stage_out = smem + STAGES * STAGE_BYTES + (warp - 4) * BLOCKS * BOX_BYTES;
         const float nan = __int_as_float(0x7fffffff);
         int phase = 0;
-        uint32_t pq_phase = 0;
         bool ok = true;   // false once a wait gave up: NaN from there on
         auto release = [&](int buf) {   // this warp has read the accumulator
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -346,17 +382,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         // block i of this warp: 16-byte piece q of this thread's row, 128-byte swizzle
         auto place = [&](int i, int q) {
             return reinterpret_cast<uint4 *>(stage_out + i * BOX_BYTES + lane * 128 + 16 * (q ^ (lane & 7)));
-        };
-        // block i of this warp to row y, column x of an array of rows of `pitch` elements, by
-        // this warp's stores
-        auto store_rows = [&](int i, __nv_bfloat16 *to, int pitch, int x, int y) {
-#pragma unroll
-            for (int k = 0; k < BOX_ROWS / 4; ++k) {
-                const int r = 4 * k + (lane >> 3), q = lane & 7;
-                if (y + r < a.M && x + 8 * q < pitch)
-                    *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(y + r) * pitch + x + 8 * q) =
-                        *reinterpret_cast<const uint4 *>(stage_out + i * BOX_BYTES + r * 128 + 16 * (q ^ (r & 7)));
-            }
         };
         auto blocks_free = [&]() {   // the stores before have read the blocks
             if (lane == 0) bulk_wait_read<0>();
@@ -558,61 +583,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                         float vm[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) vm[e] = gate(va[8 * q + e], vb[8 * q + e]);
-                        *place(BLOCKS - 1, h / 8 + q) = to_bf16(vm);
-                        if (a.keep) {
-                            *place(0, h / 8 + q) = to_bf16(va + 8 * q);
-                            *place(1, h / 8 + q) = to_bf16(vb + 8 * q);
-                        }
+                        *place(0, h / 8 + q) = to_bf16(vm);
+                    }
+                    if (a.keep && y0 < a.M) {
+#pragma unroll
+                        for (int u = 0; u < 32; u += KEPT_COLS)
+                            if (x + h + u < a.N) {
+                                uint4 *to = kept_at(a, y0, x + h + u, lane);
+                                __stcs(&to[0], upper_halves(va + u));
+                                __stcs(&to[KEPT_ROWS], upper_halves(va + u + 8));
+                                __stcs(&to[2 * KEPT_ROWS], upper_halves(vb + u));
+                                __stcs(&to[3 * KEPT_ROWS], upper_halves(vb + u + 8));
+                                __stcs(&to[4 * KEPT_ROWS], third_bytes(va + u));
+                                __stcs(&to[5 * KEPT_ROWS], third_bytes(vb + u));
+                            }
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (a.keep) {
-                    __nv_bfloat16 *kept = static_cast<__nv_bfloat16 *>(a.pq);
-                    store_rows(0, kept, a.pitch, x, y0);
-                    store_rows(1, kept + static_cast<int64_t>(a.M) * a.pitch, a.pitch, x, y0);
-                }
                 if (lane == 0 && y0 < a.M) {
-                    tma_store_3d(&tmOut, stage_out + (BLOCKS - 1) * BOX_BYTES, x, y0, 0);
+                    tma_store_3d(&tmOut, stage_out, x, y0, 0);
                     bulk_commit();
                 }
             } else if (FORM == DH) {
                 const int buf = phase & 1;
+                // p and q of two blocks, 32 columns ahead of the products
+                uint4 kept[2][KEPT_PIECES] = {};
+                auto fetch = [&](int u, int x) {
+                    if (x >= a.N || y0 >= a.M) return;
+                    const uint4 *from = kept_at(a, y0, x, lane);
+#pragma unroll
+                    for (int j = 0; j < KEPT_PIECES; ++j) kept[u][j] = __ldcs(from + j * KEPT_ROWS);
+                };
+                if (odd * PIECE < a.bn)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) fetch(u, t.tn * a.bn + odd * PIECE + u * KEPT_COLS);
 #pragma unroll 1
                 for (int c = odd * PIECE; c < a.bn; c += 2 * PIECE) {
                     const int x = t.tn * a.bn + c;
                     const bool inside = x < a.N && y0 < a.M;
-                    // p and q of the piece, while the products are under way
-                    if (inside) {
-                        blocks_free();
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(&pq_bar[warp - 4], 2 * BOX_BYTES);
-                            tma_load_3d(stage_out, &tmPQ, &pq_bar[warp - 4], x, y0, 0);
-                            tma_load_3d(stage_out + BOX_BYTES, &tmPQ, &pq_bar[warp - 4], x, y0, 1);
-                        }
-                    }
                     if (c < 2 * PIECE) accumulator(buf, (phase >> 1) & 1);
                     if (inside) {
-                        // (no other role waits for these copies: they are seen through whatever happens)
-                        ok &= mbar_wait_bounded(&pq_bar[warp - 4], pq_phase, SETTLE_NS, a.error);
-                        pq_phase ^= 1;
+                        blocks_free();
 #pragma unroll
                         for (int h = 0; h < PIECE; h += 32) {
                             float g[32];
                             read32(buf, c + h, g);
                             if (h + 32 == PIECE && c + 2 * PIECE >= a.bn) release(buf);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const Pack<__nv_bfloat16, 8> pa = *reinterpret_cast<const Pack<__nv_bfloat16, 8> *>(place(0, h / 8 + q));
-                                const Pack<__nv_bfloat16, 8> pb = *reinterpret_cast<const Pack<__nv_bfloat16, 8> *>(place(1, h / 8 + q));
-                                float va[8], vb[8];
+                            for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    va[e] = to_f32(pa.v[e]) * g[8 * q + e];
-                                    vb[e] = to_f32(pb.v[e]) * g[8 * q + e];
+                                for (int q = 0; q < 2; ++q) {   // 8 columns
+                                    const float *gq = g + u * KEPT_COLS + 8 * q;
+                                    float va[8], vb[8];
+#pragma unroll
+                                    for (int e = 0; e < 8; e += 2) {
+                                        const float2 p2 = kept_pair(word_of(kept[u][q], e / 2), word_of(kept[u][4], 2 * q + e / 4), e % 4);
+                                        const float2 q2 = kept_pair(word_of(kept[u][2 + q], e / 2), word_of(kept[u][5], 2 * q + e / 4), e % 4);
+                                        va[e] = p2.x * gq[e];
+                                        va[e + 1] = p2.y * gq[e + 1];
+                                        vb[e] = q2.x * gq[e];
+                                        vb[e + 1] = q2.y * gq[e + 1];
+                                    }
+                                    *place(0, h / 8 + 2 * u + q) = to_bf16(va);
+                                    *place(1, h / 8 + 2 * u + q) = to_bf16(vb);
                                 }
-                                *place(0, h / 8 + q) = to_bf16(va);
-                                *place(1, h / 8 + q) = to_bf16(vb);
+                                if (h + 32 < PIECE) fetch(u, x + 32 + u * KEPT_COLS);
+                                else if (c + 2 * PIECE < a.bn) fetch(u, x + 2 * PIECE + u * KEPT_COLS);
                             }
                         }
                         fence_proxy_async_smem();
@@ -1082,14 +1119,15 @@ struct Call {
     cudaStream_t stream;
 };
 
-// What the gradient takes: p and q [2][n][pf] in the storage type, m [planes][n][pf] bf16.
+// What the gradient takes: p and q, fp32 [2][n][pf] or the blocks of 24 bits, and m
+// [planes][n][pf] bf16.
 // (Not rounded up, so that its size tells one number of rows from another.)
 struct Kept { size_t m, total; int64_t pf; };
 Kept kept_layout(int64_t n, int64_t f, int dtype) {
     Kept k{};
     k.pf = ceil_div(f, 8) * 8;
-    const size_t es = dtype == NRNN_BF16 ? 2 : 4, planes = dtype == NRNN_BF16 ? 1 : 3;
-    k.m = up256(2 * es * n * k.pf);
+    const size_t planes = dtype == NRNN_BF16 ? 1 : 3;
+    k.m = dtype == NRNN_BF16 ? ceil_div(n, KEPT_ROWS) * ceil_div(f, KEPT_COLS) * KEPT_BYTES : up256(2 * sizeof(float) * n * k.pf);
     k.total = k.m + 2 * planes * n * k.pf + 16;
     return k;
 }
@@ -1188,8 +1226,7 @@ cudaError_t operands(const Call &c, const Plan &p, const void *g_in, const void 
 }
 
 template <int FORM, typename T>
-cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut,
-                 const CUtensorMap &tmPQ, GemmArgs a) {
+cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut, GemmArgs a) {
     static std::atomic<unsigned long long> configured{0};
     constexpr size_t smem = gemm_smem<FORM, T>();
     cudaError_t e = once_per_device(configured, [](int) {
@@ -1213,7 +1250,7 @@ cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, 
         a.share = slices / a.teams;
         a.longer = slices % a.teams;
     }
-    e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, tmPQ, a);
+    e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, a);
     const int64_t cut = static_cast<int64_t>(a.units - a.whole) * a.side;
     if (e == cudaSuccess && cut > 0) {
         cudaLaunchConfig_t cfg = {};
@@ -1245,6 +1282,7 @@ GemmArgs args_of(const Call &c, int64_t M, int64_t N, int64_t K, int bn) {
     a.tiles_m = static_cast<int>(ceil_div(M, BM));
     a.tiles_n = static_cast<int>(ceil_div(N, bn));
     a.kb = static_cast<int>(ceil_div(K, BK));
+    a.kept_cols = static_cast<int>(ceil_div(c.f, KEPT_COLS));
     return a;
 }
 
@@ -1253,18 +1291,17 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
     unsigned char *m = kept + kl.m;
     const void *x, *w_in, *w_out;
     if (operands<T>(c, p, nullptr, &x, &w_in, &w_out, nullptr) != cudaSuccess) return NRNN_ERR_CUDA;
-    CUtensorMap ta, tb, to, tpq;
+    CUtensorMap ta, tb, to;
     const int units = tile_columns_for(ceil_div(c.n, BM), c.f, false, BN / 2);   // UP: a tile's units
     if (!map(&ta, x, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, BK, units) ||
-        !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS) || (p.planes == 1 && !map(&tpq, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
+        !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS))
         return NRNN_ERR_CUDA;
-    if (p.planes != 1) tpq = to;
     GemmArgs a = args_of(c, c.n, c.f, c.d, 2 * units);
     a.tiles_n = static_cast<int>(ceil_div(c.f, units));
     a.keep = keep;
     a.pq = kept;
     a.pitch = static_cast<int>(p.pf);
-    if (gemm<UP, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    if (gemm<UP, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     const int bn = tile_columns_for(ceil_div(c.n, BM), c.d, true);
     a = args_of(c, c.n, c.d, c.f, bn);
     a.parts = reinterpret_cast<float *>(c.ws + p.parts);
@@ -1273,7 +1310,7 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
     if (!map(&ta, m, c.f, p.pf, c.n, p.planes, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, BK, bn / 2) ||
         (a.blocks_out && !map(&to, y, c.d, c.d, c.n, 1, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
-    return gemm<DOWN, T>(c, ta, tb, to, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    return gemm<DOWN, T>(c, ta, tb, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 template <typename T>
@@ -1283,7 +1320,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     unsigned char *gab = c.ws + p.gab;
     const void *x, *w_in, *w_out, *g;
     if (operands<T>(c, p, g_, &x, &w_in, &w_out, &g) != cudaSuccess) return NRNN_ERR_CUDA;
-    CUtensorMap ta, tb, to, tpq;
+    CUtensorMap ta, tb, to;
     float *parts = reinterpret_cast<float *>(c.ws + p.parts);
     // fp32: one piece of an epilogue warp holds ga and gb, so tiles of 128
     int bn = tile_columns_for(ceil_div(c.n, BM), c.f, false, p.planes != 1 ? 2 * PIECE : BN);
@@ -1291,11 +1328,9 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     a.pq = const_cast<unsigned char *>(kept);
     a.pitch = static_cast<int>(p.pf);
     if (!map(&ta, g, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, 64, BK) ||
-        !map(&to, gab, c.f, p.pf, c.n, 2 * p.planes, PIECE, BOX_ROWS) ||
-        (p.planes == 1 && !map(&tpq, kept, c.f, p.pf, c.n, 2, PIECE, BOX_ROWS)))
+        !map(&to, gab, c.f, p.pf, c.n, 2 * p.planes, PIECE, BOX_ROWS))
         return NRNN_ERR_CUDA;
-    if (p.planes != 1) tpq = to;
-    if (gemm<DH, T>(c, ta, tb, to, tpq, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    if (gemm<DH, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gx
     bn = tile_columns_for(ceil_div(c.n, BM), c.d, true);
     a = args_of(c, c.n, c.d, c.f, bn);
@@ -1307,7 +1342,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, 64, BK) ||
         (a.blocks_out && !map(&to, gx, c.d, c.d, c.n, 1, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
-    if (gemm<GX, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    if (gemm<GX, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_in
     bn = tile_columns_for(2 * ceil_div(c.f, BM), c.d, true);
     a = args_of(c, c.f, c.d, c.n, bn);
@@ -1319,7 +1354,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.planes, 64, BK) || !map(&tb, x, c.d, p.pd, c.n, p.planes, 64, BK) ||
         (a.blocks_out && !map(&to, gW_in, c.d, c.d, c.f, 2, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
-    if (gemm<GWI, T>(c, ta, tb, to, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    if (gemm<GWI, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_out
     bn = tile_columns_for(ceil_div(c.d, BM), c.f, true);
     a = args_of(c, c.d, c.f, c.n, bn);
@@ -1329,7 +1364,7 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     if (!map(&ta, g, c.d, p.pd, c.n, p.planes, 64, BK) || !map(&tb, m, c.f, p.pf, c.n, p.planes, 64, BK) ||
         (a.blocks_out && !map(&to, gW_out, c.f, c.f, c.d, 1, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
-    return gemm<GWO, T>(c, ta, tb, to, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
+    return gemm<GWO, T>(c, ta, tb, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
 }
 
 template <typename T, int N, int VEC_UP, int VEC_DOWN>
