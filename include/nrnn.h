@@ -689,7 +689,8 @@ int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *p
  *   g_state     device, fp32 of state's shape: dL/dstate; NULL: not wanted
  *   workspace   device, 256-byte aligned, of at least
  *               nrnn_linear_recurrence_workspace_bytes(..., 1)
- * Where s is zero (a rate of zero) its infinite derivative is left out.
+ * Where s is zero (1 - a^2 below 2^-126: a rate of zero, or one next to it) its infinite
+ * derivative is left out.
  */
 int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *params, int64_t B,
                                     int64_t T, int64_t d_h, const int32_t *cu_seqlens,

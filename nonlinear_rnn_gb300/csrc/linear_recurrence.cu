@@ -13,8 +13,8 @@
 //
 // r and i are bounded below by 2^-63 (the exponential is clamped, so that two sigmoids
 // share a reciprocal and 1 - r is exact to rounding on both sides); where s is zero all
-// the same (a rate of zero) the term with a^2 / s is left out, which is its limit as r
-// vanishes.
+// the same (1 - a^2 below 2^-126, which the square root takes for zero) the term with a^2 / s
+// is left out, which is its limit as r vanishes.
 //
 // One pass over the data in each direction, bound by HBM: 4 values a unit and step
 // forward, 8 backward.  A tile is 64 units (two a lane, on packed f32x2 arithmetic) and
@@ -132,10 +132,11 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float rsqrt_approx(float x) {
+// 1 / sqrt(x); 0 below 2^-126, where sqrt_approx is 0 (and where rsqrt would be infinite)
+__device__ __forceinline__ float rsqrt_or_zero(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    return x >= 1.17549435e-38f ? y : 0.f;
 }
 
 // The decay a = 2^z, z <= 0, near one: a - 1 by its series, which leaves a rounding of its
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
                 const float2 r = dr[i], z = mul2(w.fall2, r);
                 float2 q;                                                 // a^2 - 1
                 const float2 decay = decay_of<TERMS>(z, q);
-                const float2 rs = make_float2(q.x < 0.f ? rsqrt_approx(-q.x) : 0.f, q.y < 0.f ? rsqrt_approx(-q.y) : 0.f);
+                const float2 rs = make_float2(rsqrt_or_zero(-q.x), rsqrt_or_zero(-q.y));
                 const float2 msq = mul2(q, rs), over = mul2(decay, rs);   // -s, a / s
                 float2 before = i > 0 ? load2(h_mine + (i - 1) * UNITS) : before0;
                 if (SPECIAL && (heads >> i & 1u)) before = two_of(a.state + row_of(i), uok && a.state != nullptr);
