@@ -731,7 +731,8 @@ size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dt
  *   workspace   device, 256-byte aligned, nrnn_gated_mlp_workspace_bytes.  Its
  *               first 32-bit word is 0 once the work is done, or not if a device wait
  *               gave up (nrnn_set_wait_limit_ns): then outputs are NaN where they
- *               depended on it.  So too in the backward
+ *               depended on it.  So too in the backward.  A call of no rows needs no
+ *               workspace and leaves it alone
  * The buffers of the tensors need only their element's alignment.  In both directions the
  * outputs must not overlap one another or the inputs (NRNN_ERR_INVALID_ARG).
  */

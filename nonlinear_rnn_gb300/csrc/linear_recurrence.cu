@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     if (u < d) gparams[static_cast<int64_t>(j / UNITS) * d + u] = sum;
 }
 
-// Clears a call's counters and slots.  Sequences without a step hand their state (or its
+// Clears a call's counters, error word and slots.  Sequences without a step hand their state (or its
 // gradient) on; with no steps at all the parameters' gradients are zeros.  With a plan the
 // first CTA builds it and clears nothing.
 constexpr int PREPARE_THREADS = 256;
@@ -894,7 +894,7 @@ RecArgs args_of(const Layout &y, const float *params, const float *state, const 
 template <int L>
 cudaError_t prepare(const Layout &y, const RecArgs &a, unsigned char *ws, const float *in, float *out, float *zeros,
                     bool reverse, cudaStream_t s) {
-    const int64_t n16 = y.n_tiles > 0 ? y.cleared / 16 : 0;
+    const int64_t n16 = (y.n_tiles > 0 ? y.cleared : 256) / 16;   // (without steps: the error word's)
     const int64_t most = n16 > static_cast<int64_t>(a.rows) * a.d ? n16 : static_cast<int64_t>(a.rows) * a.d;
     int64_t b = ceil_div(most, PREPARE_THREADS);
     b = b < 1 ? 1 : b < 1216 ? b : 1216;
@@ -999,7 +999,6 @@ int nrnn_linear_recurrence_forward(const void *preact, int dtype, const float *p
         return NRNN_ERR_INVALID_ARG;
     const Layout y = layout_of(B, T, d_h, dtype, cu_seqlens != nullptr ? num_segments : 0, false);
     if (!usable(workspace, ws_bytes, y.total)) return NRNN_ERR_WORKSPACE;
-    if (rows == 0) return NRNN_OK;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     RecArgs a = args_of(y, params, state, cu_seqlens, rows, T, d_h, ws);
