@@ -139,10 +139,14 @@ __device__ __forceinline__ float rsqrt_or_zero(float x) {
     return x >= 1.17549435e-38f ? y : 0.f;
 }
 
-// The decay a = 2^z, z <= 0, near one: a - 1 by its series, which leaves a rounding of its
-// own (ex2.approx is 2^-22 off, to one side over a range, and a unit of long memory adds
-// that up), and a^2 - 1 = (a - 1)(a + 1) without a difference.  TERMS 5: from z = -0.18 on
-// to 1e-8; 3: from -0.045 on to 4e-8, and a^2 - 1 2^-19 by the difference at that border.
+// The decay a = 2^z, z <= 0, near one: a - 1 by its series (ex2.approx is 2^-22 off, to one
+// side over a range, and a unit of long memory adds that up; one more than the series is a
+// rounding of 2^-25 off), and a^2 - 1 = (a - 1)(a + 1) without a difference.  Beyond the
+// border a^2 - 1 is a difference, and ex2's error in it grows by 2 a^2 / (1 - a^2).
+// TERMS 5: to z = -0.18, where that leaves s 2^-20 off at most; 3: to -0.045, 2^-18 (measured
+// beside the borders: 3.3e-7 and 1.3e-6, on the series' side 1.6e-7).  The forward takes 5
+// whatever the storage, as its last states are fp32 and go on in steps (16 x 16384 x 1024 bf16
+// 392 us with 3, 396 with 5); the backward of bf16 takes 3 (711 us, 731).
 template <int TERMS> struct NearOne {
     static constexpr float LIMIT = TERMS == 5 ? -0.18f : -0.045f;
     __device__ static float2 less_one(float2 z) {
@@ -431,7 +435,7 @@ template <typename TS, bool WIDE, int MODE>
 __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
     k_forward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const RecArgs a) {
     using Form = Shape<TS, WIDE>;
-    constexpr int SEG = Form::SEG, PLANE = Form::PLANE, TERMS = sizeof(TS) == 2 ? 3 : 5;
+    constexpr int SEG = Form::SEG, PLANE = Form::PLANE, TERMS = 5;
     extern __shared__ __align__(128) unsigned char dsmem[];   // FORWARD_TILES tiles
     __shared__ Shared s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -40,3 +40,34 @@ def test_rates_next_to_zero(B, T, t):
         assert bool(x.isfinite().all()), name
     assert bool((r.gP.abs() <= (T + 1) * 1e-17).all())
     assert torch.equal(r.g_state, torch.full_like(state, T + 1))
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+def test_states_of_constant_decays(t):
+    """A decay that stays the same adds its error up 1 / (1 - a) times, and the states are fp32
+    whatever the storage: decays of 2^z around the places where their series ends, after many
+    steps and after one.
+
+    Relative to h = u / (1 - a): 2^-25 of a's last addition and as much of its series, or 2^-22
+    of the exponential; 2^-24 a step of the scan's own rounding; u is 2^-22 (exponential) times
+    2 a^2 / (1 - a^2) / 2 off where 1 - a^2 is a difference, which begins at z = -0.18, and 2^-21
+    for the square root and the gates besides."""
+    d, T = 2048, 900
+    z = torch.linspace(-0.4, -0.02, d, device="cuda", dtype=torch.float64)
+    params = torch.zeros(3, d, device="cuda")
+    params[0] = -z * 0.6931471805599453
+    params[1:] = 60.0                                            # both gates open: r = i = 1
+    P = torch.zeros(1, T, 3 * d, dtype=t, device="cuda")
+    P[..., 2 * d:] = 1.0
+    a = torch.exp(-params[0].double())
+    u, steps = torch.sqrt(-torch.expm1(-2 * params[0].double())), torch.arange(1, T + 1, device="cuda").double()[:, None]
+    h = u * -torch.expm1(-params[0].double() * steps) / -torch.expm1(-params[0].double())
+    series = z > -0.18
+    da = torch.where(series, 2.0 ** -24, 2.0 ** -22)
+    du = 2.0 ** -21 + torch.where(series, 0.0, 2.0 ** -22 * a * a / (1 - a * a))
+    tol = du + (da + 2.0 ** -24) / (1 - a)
+    H, last = nr.linear_recurrence(P, params)
+    for got, want, bound in ((last[0], h[-1], tol), (nr.linear_recurrence(P[:, :1], params)[1][0], h[0], du)):
+        off = (got.double() - want).abs() / want
+        assert bool((off <= bound).all()), (float((off / bound).max()), float(z[(off / bound).argmax()]), float(off.max()))
+    assert torch.equal(H[0, -1], last[0].to(t))
