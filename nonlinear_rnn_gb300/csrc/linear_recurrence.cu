@@ -38,6 +38,8 @@
 // every segment is a column of its own, and many chains are short instead of few long.
 // A segment's short last chunk loads steps of the next one, which it leaves out, and
 // stores its own by rows.  (262144 x 512 fp32 in 64 segments, backward: 952 -> 807 us.)
+// Where one segment is so long that its chain would be what takes the time, which only the
+// device knows, the same kernel goes by the time axis (by_segments).
 //
 // Measured, with HBM's measured copy rate of 6775 GB/s: 16 x 16384 x 1024 bf16 390 us forward
 // (0.81), 716 backward (0.89); 4 x 131072 x 64 fp32 143 us (0.55: four columns; without the
@@ -91,7 +93,8 @@ struct RecArgs {
     const float *g_last;              // backward: (rows, d) or null
     float *g_state;                   // backward: (rows, d) or null
     float *part;                      // backward: [n_cols][n_chunks][3][UNITS] sums of a tile
-    const int4 *plan;                 // PLAN: the chunks; n_chunks is their most, n_cols the unit tiles
+    const int4 *plan;                 // PLAN: the chunks after plan[0] = {how many, whether the call goes by
+                                      // them}; n_chunks is their most, n_cols the unit tiles
     unsigned long long *slots;        // [n_cols][n_chunks][UNITS] maps of chunks (WIDE: of a group's last
                                       // chunk the state after it)
     unsigned long long *maps;         // [n_cols][groups][UNITS] maps of groups
@@ -293,6 +296,8 @@ template <int L, bool REVERSE, int MODE> __device__ __forceinline__ Place place_
     p.at = static_cast<int64_t>(p.col) * a.n_chunks + p.q;
     return p;
 }
+// whether a call with a plan goes by its segments (k_prepare decides)
+__device__ __forceinline__ bool by_segments(const int4 *plan) { return plan[0].y != 0; }
 // tiles there are
 template <int MODE> __device__ __forceinline__ uint32_t tiles_of(const RecArgs &a) {
     return MODE == PLAN ? static_cast<uint32_t>(a.plan[0].x) * a.n_ut : a.n_tiles;
@@ -431,24 +436,19 @@ __device__ __forceinline__ bool tile_is_there(uint64_t *bar, uint32_t parity, co
 }
 
 // ---------------------------------------------------------------- forward
+// tiles: FORWARD_TILES of them in shared memory
 template <typename TS, bool WIDE, int MODE>
-__global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
-    k_forward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const RecArgs a) {
+__device__ __forceinline__ void forward_tiles(const CUtensorMap *tmP, const CUtensorMap *tmH, const RecArgs &a, Shared &s, TS *tiles) {
     using Form = Shape<TS, WIDE>;
     constexpr int SEG = Form::SEG, PLANE = Form::PLANE, TERMS = 5;
-    extern __shared__ __align__(128) unsigned char dsmem[];   // FORWARD_TILES tiles
-    __shared__ Shared s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    TS *const tiles = reinterpret_cast<TS *>(dsmem);
     auto start = [&](uint32_t tile, int buf) {   // the copies of a tile
         const Place p = place_of<Form::L, false, MODE>(a, tile);
         mbar_arrive_expect_tx(&s.bar[buf], 3u * PLANE * sizeof(TS));
 #pragma unroll
         for (int g = 0; g < 3; ++g)
-            tma_load_3d(tiles + (buf * 3 + g) * PLANE, &tmP, &s.bar[buf], g * a.d + p.u0, p.t0, p.b);
+            tma_load_3d(tiles + (buf * 3 + g) * PLANE, tmP, &s.bar[buf], g * a.d + p.u0, p.t0, p.b);
     };
-    dependents_may_launch();
-    wait_for_prerequisites();
     const uint32_t n_tiles = tiles_of<MODE>(a);
     if (tid == 0) {
         mbar_init(&s.bar[0], 1);
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
             for (int i = 0; i < SEG && p.t0 + r0 + i < p.t_end; ++i)
                 if (uok) store2(static_cast<TS *>(a.H_out) + static_cast<int64_t>(p.t0 + r0 + i) * a.d + u, load2(mine + i * UNITS));
         } else if (lane == 0 && p.t0 + r0 < a.T) {
-            tma_store_3d(&tmH, mine, p.u0, p.t0 + r0, p.b);
+            tma_store_3d(tmH, mine, p.u0, p.t0 + r0, p.b);
             bulk_commit();
         }
         if (!WIDE) {   // (else s.tile was written before this tile's barrier, and the shared maps alternate)
@@ -541,6 +541,28 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
     if (lane == 0) bulk_wait_read<0>();   // the tiles outlive the stores' reads
 }
 
+template <typename TS, bool WIDE, int MODE>
+__global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::FORWARD_CTAS))
+    k_forward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const RecArgs a) {
+    extern __shared__ __align__(128) unsigned char dsmem[];
+    __shared__ Shared s;
+    dependents_may_launch();
+    wait_for_prerequisites();
+    forward_tiles<TS, WIDE, MODE>(&tmP, &tmH, a, s, reinterpret_cast<TS *>(dsmem));
+}
+
+// a pack by its segments (a), or by the time axis (cut)
+template <typename TS>
+__global__ void __launch_bounds__(THREADS, (Shape<TS, true>::FORWARD_CTAS))
+    k_forward_pack(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const RecArgs a, const RecArgs cut) {
+    extern __shared__ __align__(128) unsigned char dsmem[];
+    __shared__ Shared s;
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (by_segments(a.plan)) forward_tiles<TS, true, PLAN>(&tmP, &tmH, a, s, reinterpret_cast<TS *>(dsmem));
+    else forward_tiles<TS, false, PACK>(&tmP, &tmH, cut, s, reinterpret_cast<TS *>(dsmem));
+}
+
 // ---------------------------------------------------------------- backward
 // shared -> global store of a block of dL/dP through the 4-D map (d, block, T, B)
 __device__ __forceinline__ void store_block(const CUtensorMap *map, const void *src, int x, int y, int z, int w) {
@@ -551,27 +573,28 @@ __device__ __forceinline__ void store_block(const CUtensorMap *map, const void *
         : "memory");
 }
 
+// The tensor maps of a backward call, as the kernels take them
+#define NRNN_BACKWARD_MAPS                                                                                    \
+    const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmG, \
+        const __grid_constant__ CUtensorMap tmGP
+using Sums = float2[3][NW][32];
+
+// Ps: one tile in shared memory: P, H, gH
 template <typename TS, bool WIDE, int MODE>
-__global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
-    k_backward(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmH,
-               const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmGP, const RecArgs a) {
+__device__ __forceinline__ void backward_tiles(const CUtensorMap *tmP, const CUtensorMap *tmH, const CUtensorMap *tmG,
+                                               const CUtensorMap *tmGP, const RecArgs &a, Shared &s, Sums &sums, TS *const Ps) {
     using Form = Shape<TS, WIDE>;
     constexpr int SEG = Form::SEG, PLANE = Form::PLANE, TERMS = sizeof(TS) == 2 ? 3 : 5;
-    extern __shared__ __align__(128) unsigned char dsmem[];   // one tile: P, H, gH
-    __shared__ Shared s;
-    __shared__ float2 sums[3][NW][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    TS *const Ps = reinterpret_cast<TS *>(dsmem), *const Hs = Ps + 3 * PLANE, *const Gs = Hs + PLANE;
+    TS *const Hs = Ps + 3 * PLANE, *const Gs = Hs + PLANE;
     auto start = [&](uint32_t tile) {
         const Place p = place_of<Form::L, true, MODE>(a, tile);
         mbar_arrive_expect_tx(&s.bar[0], 5u * PLANE * sizeof(TS));
 #pragma unroll
-        for (int g = 0; g < 3; ++g) tma_load_3d(Ps + g * PLANE, &tmP, &s.bar[0], g * a.d + p.u0, p.t0, p.b);
-        tma_load_3d(Hs, &tmH, &s.bar[0], p.u0, p.t0, p.b);
-        tma_load_3d(Gs, &tmG, &s.bar[0], p.u0, p.t0, p.b);
+        for (int g = 0; g < 3; ++g) tma_load_3d(Ps + g * PLANE, tmP, &s.bar[0], g * a.d + p.u0, p.t0, p.b);
+        tma_load_3d(Hs, tmH, &s.bar[0], p.u0, p.t0, p.b);
+        tma_load_3d(Gs, tmG, &s.bar[0], p.u0, p.t0, p.b);
     };
-    dependents_may_launch();
-    wait_for_prerequisites();
     const uint32_t n_tiles = tiles_of<MODE>(a);
     if (tid == 0) {
         mbar_init(&s.bar[0], 1);
@@ -684,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
                                load2(mine + g * PLANE + i * UNITS));
         } else if (lane == 0 && p.t0 + r0 < a.T) {
 #pragma unroll
-            for (int g = 0; g < 3; ++g) store_block(&tmGP, Ps + g * PLANE + r0 * UNITS, p.u0, g, p.t0 + r0, p.b);
+            for (int g = 0; g < 3; ++g) store_block(tmGP, Ps + g * PLANE + r0 * UNITS, p.u0, g, p.t0 + r0, p.b);
             bulk_commit();
             bulk_wait_read<0>();
         }
@@ -701,18 +724,44 @@ __global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS))
     }
 }
 
+template <typename TS, bool WIDE, int MODE>
+__global__ void __launch_bounds__(THREADS, (Shape<TS, WIDE>::BACKWARD_CTAS)) k_backward(NRNN_BACKWARD_MAPS, const RecArgs a) {
+    extern __shared__ __align__(128) unsigned char dsmem[];
+    __shared__ Shared s;
+    __shared__ Sums sums;
+    dependents_may_launch();
+    wait_for_prerequisites();
+    backward_tiles<TS, WIDE, MODE>(&tmP, &tmH, &tmG, &tmGP, a, s, sums, reinterpret_cast<TS *>(dsmem));
+}
+
+template <typename TS>
+__global__ void __launch_bounds__(THREADS, (Shape<TS, true>::BACKWARD_CTAS))
+    k_backward_pack(NRNN_BACKWARD_MAPS, const RecArgs a, const RecArgs cut) {
+    extern __shared__ __align__(128) unsigned char dsmem[];
+    __shared__ Shared s;
+    __shared__ Sums sums;
+    dependents_may_launch();
+    wait_for_prerequisites();
+    if (by_segments(a.plan)) backward_tiles<TS, true, PLAN>(&tmP, &tmH, &tmG, &tmGP, a, s, sums, reinterpret_cast<TS *>(dsmem));
+    else backward_tiles<TS, false, PACK>(&tmP, &tmH, &tmG, &tmGP, cut, s, sums, reinterpret_cast<TS *>(dsmem));
+}
+
 // Sums of the parameters' gradients over rows and chunks, in order: a CTA takes a unit
 // tile and one of JOIN_SLICES shares of (row, chunk); the CTA that ends last, by a
 // counter, adds the shares.
 constexpr int JOIN_SLICES = 32, JOIN_THREADS = 3 * UNITS;
 
 __global__ void __launch_bounds__(JOIN_THREADS)
-    k_join(const float *part, int rows, int n_ut, int n_chunks, const int4 *plan, int d, float *share, uint32_t *count,
-           float *gparams) {
+    k_join(const float *part, int rows, int n_ut, int n_chunks, const int4 *plan, int cut_chunks, int d, float *share,
+           uint32_t *count, float *gparams) {
     __shared__ bool is_last;
     dependents_may_launch();
     wait_for_prerequisites();
     const int ut = blockIdx.x, slice = blockIdx.y, j = threadIdx.x;
+    if (plan != nullptr && !by_segments(plan)) {
+        plan = nullptr;
+        n_chunks = cut_chunks;
+    }
     // (tiles are counted in 32 bits; a plan: one row)
     const uint32_t all = plan != nullptr ? static_cast<uint32_t>(plan[0].x) : static_cast<uint32_t>(rows) * n_chunks;
     const uint32_t k0 = static_cast<uint64_t>(all) * slice / JOIN_SLICES, k1 = static_cast<uint64_t>(all) * (slice + 1) / JOIN_SLICES;
@@ -746,9 +795,16 @@ __global__ void __launch_bounds__(JOIN_THREADS)
     if (u < d) gparams[static_cast<int64_t>(j / UNITS) * d + u] = sum;
 }
 
+// A pack goes by its segments where the longest of them has at most 1 / LONGEST of all tiles:
+// its chain takes a chunk in 0.45 to 0.7 us however few others are left, about as long as the
+// machine takes for that many tiles.  262144 x 512 in 64 segments of which one has 16384,
+// 32768 or 250000 steps, by segments and by the time axis: forward fp32 475, 665, 3795 and 575
+// us, bf16 262, 354, 1818 and 352; backward 854, 1126, 4890 and 838, 568, 727, 3112 and 585.
+template <bool REVERSE> constexpr int64_t LONGEST = REVERSE ? 140 : 100;
+
 // Clears a call's counters, error word and slots.  Sequences without a step hand their state (or its
 // gradient) on; with no steps at all the parameters' gradients are zeros.  With a plan the
-// first CTA builds it and clears nothing.
+// first CTA builds it, if the call is to go by it, and clears nothing.
 constexpr int PREPARE_THREADS = 256;
 
 template <int L>
@@ -761,7 +817,22 @@ __global__ void __launch_bounds__(PREPARE_THREADS)
     int first = 0;
     if (plan != nullptr) {
         if (blockIdx.x == 0) {
-            build_pack_plan<PREPARE_THREADS, L>(cu, rows, (T + L - 1) / L, reverse, plan, plan_space);
+            __shared__ int longest, all;
+            if (threadIdx.x == 0) longest = all = 0;
+            __syncthreads();
+            int most = 0, sum = 0;
+            for (int i = threadIdx.x; i < rows; i += PREPARE_THREADS) {
+                const int c = (max(0, __ldg(cu + i + 1) - __ldg(cu + i)) + L - 1) / L;
+                most = max(most, c);
+                sum += c;
+            }
+            atomicMax(&longest, most);
+            atomicAdd(&all, sum);
+            __syncthreads();
+            const int64_t tiles = static_cast<int64_t>(all) * ((d + UNITS - 1) / UNITS);
+            const bool segments = longest * (reverse ? LONGEST<true> : LONGEST<false>) <= tiles;
+            if (segments) build_pack_plan<PREPARE_THREADS, L>(cu, rows, (T + L - 1) / L, reverse, plan, plan_space);
+            if (threadIdx.x == 0) plan[0] = make_int4(all, segments, 0, 0);
             return;
         }
         first = 1;
@@ -806,8 +877,12 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 struct Layout {
     bool wide;
     int64_t n_ut, n_cols, n_chunks, group, span, n_tiles;
+    int64_t cut_chunks;   // with a plan: chunks of the time axis
     int64_t slots, maps, ends, cleared, plan, part, share, total;   // plan 0: none
 };
+// the look-back where the warps share the maps before: a hop takes 2 to 3 us, and a chunk
+// reads half a group's and half a span's maps on average
+constexpr int64_t GROUP = 16, SPAN = 16;
 
 // Columns from which a call takes the WIDE form.  bf16 of 64 and 128 columns (16384 and 8192
 // steps) forward 188 and 128 us, 138 and 133 the other, backward 267 and 220, 240 and 243;
@@ -816,7 +891,8 @@ struct Layout {
 constexpr int64_t wide_columns(int dtype, bool backward) { return dtype == NRNN_F32 && !backward ? 256 : 128; }
 
 // num_segments > 0: a pack.  Its segments are columns where they are enough of them for
-// the WIDE form, long enough (a segment adds a short chunk), and the plan is small.
+// the WIDE form, long enough (a segment adds a short chunk), and the plan is small; there is
+// room for both ways, which share the slots and sums.
 Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, int64_t num_segments, bool backward) {
     Layout y{};
     const int64_t wide_steps = dtype == NRNN_BF16 ? Shape<__nv_bfloat16, true>::L : Shape<float, true>::L;
@@ -827,11 +903,10 @@ Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, int64_t num_segment
     y.n_cols = B * y.n_ut;
     y.wide = plan || y.n_cols >= wide_columns(dtype, backward);
     y.n_chunks = ceil_div(T, y.wide ? wide_steps : steps) + (plan ? num_segments : 0);
-    // where the warps share the maps before, a hop takes 2 to 3 us, and a chunk reads half a
-    // group's and half a span's maps on average
-    y.group = !y.wide ? 16 : backward ? WIDE_GROUP<true> : WIDE_GROUP<false>;
-    y.span = y.wide ? 1 : 16;
-    const int64_t groups = ceil_div(y.n_chunks, y.group);
+    y.cut_chunks = plan ? ceil_div(T, steps) : 0;
+    y.group = !y.wide ? GROUP : backward ? WIDE_GROUP<true> : WIDE_GROUP<false>;
+    y.span = y.wide ? 1 : SPAN;
+    const int64_t groups = ceil_div(plan ? y.cut_chunks : y.n_chunks, GROUP);
     y.n_tiles = y.n_cols * y.n_chunks;
     int64_t at = 256 + up256(4 * y.n_ut);   // ticket, error; the join's counters
     auto take = [&](int64_t per_column) {
@@ -840,8 +915,8 @@ Layout layout_of(int64_t B, int64_t T, int64_t d, int dtype, int64_t num_segment
         return o;
     };
     y.slots = take(y.n_chunks);
-    y.maps = take(y.wide ? 0 : groups);
-    y.ends = take(y.wide ? 0 : ceil_div(groups, y.span));
+    y.maps = take(y.wide && !plan ? 0 : groups);
+    y.ends = take(y.wide && !plan ? 0 : ceil_div(groups, SPAN));
     y.cleared = at;
     if (plan) {
         y.plan = at;
@@ -895,6 +970,16 @@ RecArgs args_of(const Layout &y, const float *params, const float *state, const 
     return a;
 }
 
+// the arguments of a call with a plan that goes by the time axis
+RecArgs cut_args(const Layout &y, RecArgs a) {
+    a.n_chunks = static_cast<int>(y.cut_chunks);
+    a.group = static_cast<int>(GROUP);
+    a.span = static_cast<int>(SPAN);
+    a.n_tiles = static_cast<uint32_t>(y.n_cols * y.cut_chunks);
+    a.plan = nullptr;
+    return a;
+}
+
 template <int L>
 cudaError_t prepare(const Layout &y, const RecArgs &a, unsigned char *ws, const float *in, float *out, float *zeros,
                     bool reverse, cudaStream_t s) {
@@ -935,14 +1020,19 @@ cudaError_t launch_forward(const Layout &y, const RecArgs &a, int dtype, const v
     static std::atomic<unsigned long long> configured{0};
     constexpr size_t smem = static_cast<size_t>(Form::FORWARD_TILES) * 3 * Form::PLANE * sizeof(TS);
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_forward<TS, WIDE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if constexpr (MODE == PLAN)
+            return cudaFuncSetAttribute(k_forward_pack<TS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        else
+            return cudaFuncSetAttribute(k_forward<TS, WIDE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     });
     if (e != cudaSuccess) return e;
     CUtensorMap tmP, tmH;
     if (!make_map_steps(&tmP, P, dtype, 3 * a.d, a.T, B, UNITS, Form::L) ||
         !make_map_steps(&tmH, H, dtype, a.d, a.T, B, UNITS, Form::SEG))
         return cudaErrorUnknown;
-    return launch_dependent(k_forward<TS, WIDE, MODE>, ctas_for(y.n_tiles, Form::FORWARD_CTAS), THREADS, smem, s, tmP, tmH, a);
+    const unsigned ctas = ctas_for(y.n_tiles, Form::FORWARD_CTAS);
+    if constexpr (MODE == PLAN) return launch_dependent(k_forward_pack<TS>, ctas, THREADS, smem, s, tmP, tmH, a, cut_args(y, a));
+    else return launch_dependent(k_forward<TS, WIDE, MODE>, ctas, THREADS, smem, s, tmP, tmH, a);
 }
 
 template <typename TS, bool WIDE, int MODE>
@@ -952,7 +1042,10 @@ cudaError_t launch_backward(const Layout &y, const RecArgs &a, int dtype, const 
     static std::atomic<unsigned long long> configured{0};
     constexpr size_t smem = 5ull * Form::PLANE * sizeof(TS);
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_backward<TS, WIDE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if constexpr (MODE == PLAN)
+            return cudaFuncSetAttribute(k_backward_pack<TS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        else
+            return cudaFuncSetAttribute(k_backward<TS, WIDE, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     });
     if (e != cudaSuccess) return e;
     CUtensorMap tmP, tmH, tmG, tmGP;
@@ -961,8 +1054,11 @@ cudaError_t launch_backward(const Layout &y, const RecArgs &a, int dtype, const 
         !make_map_steps(&tmG, gH, dtype, a.d, a.T, B, UNITS, Form::L) ||
         !make_map_gate_steps(&tmGP, gP, dtype, a.d, a.T, B, UNITS, Form::SEG))
         return cudaErrorUnknown;
-    return launch_dependent(k_backward<TS, WIDE, MODE>, ctas_for(y.n_tiles, Form::BACKWARD_CTAS), THREADS, smem, s, tmP, tmH, tmG,
-                            tmGP, a);
+    const unsigned ctas = ctas_for(y.n_tiles, Form::BACKWARD_CTAS);
+    if constexpr (MODE == PLAN)
+        return launch_dependent(k_backward_pack<TS>, ctas, THREADS, smem, s, tmP, tmH, tmG, tmGP, a, cut_args(y, a));
+    else
+        return launch_dependent(k_backward<TS, WIDE, MODE>, ctas, THREADS, smem, s, tmP, tmH, tmG, tmGP, a);
 }
 
 // launch<TS, WIDE, MODE>(args...) for the call
@@ -1051,7 +1147,7 @@ int nrnn_linear_recurrence_backward(const void *preact, int dtype, const float *
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             e = cudaLaunchKernelEx(&cfg, k_join, static_cast<const float *>(a.part), static_cast<int>(B), a.n_ut, a.n_chunks,
-                                   a.plan, a.d, reinterpret_cast<float *>(ws + y.share), reinterpret_cast<uint32_t *>(ws + 256), gparams);
+                                   a.plan, static_cast<int>(y.cut_chunks), a.d, reinterpret_cast<float *>(ws + y.share), reinterpret_cast<uint32_t *>(ws + 256), gparams);
         }
     }
     return e == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
