@@ -1137,7 +1137,7 @@ Kept kept_layout(int64_t n, int64_t f, int dtype) {
 struct Plan {
     int planes;
     int64_t pd, pf;
-    size_t x, w_in, w_out, g, kept, gab, parts, total;
+    size_t x, w_in, w_out, g, m, gab, parts, total;
 };
 constexpr size_t NO_COPY = ~static_cast<size_t>(0);
 
@@ -1189,7 +1189,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in
     p.x = x_lies ? NO_COPY : take(2 * p.planes * n * p.pd);
     p.w_in = w_in_lies ? NO_COPY : take(2 * p.planes * 2 * f * p.pd);
     p.w_out = w_out_lies ? NO_COPY : take(2 * p.planes * d * p.pf);
-    p.kept = keep || backward ? NO_COPY : take(kept_layout(n, f, dtype).total);
+    p.m = keep || backward ? NO_COPY : take(2 * p.planes * n * p.pf);   // (else among what is kept)
     p.g = !backward || g_lies ? NO_COPY : take(2 * p.planes * n * p.pd);
     p.gab = backward ? take(2 * p.planes * 2 * n * p.pf) : NO_COPY;
     const int64_t widest = tile_columns(d) > tile_columns(f) ? tile_columns(d) : tile_columns(f);
@@ -1286,9 +1286,8 @@ GemmArgs args_of(const Call &c, int64_t M, int64_t N, int64_t K, int bn) {
     return a;
 }
 
-template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned char *kept, bool keep) {
-    const Kept kl = kept_layout(c.n, c.f, c.dtype);
-    unsigned char *m = kept + kl.m;
+template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned char *kept) {
+    unsigned char *m = kept != nullptr ? kept + kept_layout(c.n, c.f, c.dtype).m : c.ws + p.m;
     const void *x, *w_in, *w_out;
     if (operands<T>(c, p, nullptr, &x, &w_in, &w_out, nullptr) != cudaSuccess) return NRNN_ERR_CUDA;
     CUtensorMap ta, tb, to;
@@ -1298,7 +1297,7 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
         return NRNN_ERR_CUDA;
     GemmArgs a = args_of(c, c.n, c.f, c.d, 2 * units);
     a.tiles_n = static_cast<int>(ceil_div(c.f, units));
-    a.keep = keep;
+    a.keep = kept != nullptr;
     a.pq = kept;
     a.pitch = static_cast<int>(p.pf);
     if (gemm<UP, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
@@ -1498,9 +1497,8 @@ int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, i
     const Plan p = plan_for(rows, d, f, dtype, used_in_place(x, d, dtype), used_in_place(W_in, d, dtype),
                             used_in_place(W_out, f, dtype), false, kept != nullptr, false);
     if (!usable(workspace, ws_bytes, p.total)) return NRNN_ERR_WORKSPACE;
-    unsigned char *k = kept != nullptr ? static_cast<unsigned char *>(kept) : c.ws + p.kept;
-    return dtype == NRNN_BF16 ? forward(c, p, static_cast<__nv_bfloat16 *>(y), k, kept != nullptr)
-                              : forward(c, p, static_cast<float *>(y), k, kept != nullptr);
+    unsigned char *k = static_cast<unsigned char *>(kept);
+    return dtype == NRNN_BF16 ? forward(c, p, static_cast<__nv_bfloat16 *>(y), k) : forward(c, p, static_cast<float *>(y), k);
 }
 
 int nrnn_gated_mlp_backward(const void *x, const void *W_in, const void *W_out, const void *kept, const void *g,
