@@ -938,7 +938,8 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32)
 // Other types and rows: on the fp32 cores, in groups of FEW_GROUP rows that read the
 // weights again, from L2; one group of bf16, FEW_MOST rows of fp32, whose weights'
 // planes would be more to write and read (1024 x 4096: 8 rows 12 us, 32 37, 64 69, by the
-// planes 111).  A warp of k_few_up takes
+// planes 111).  A group's rows of x have to fit in FEW_X_BYTES: with 5 rows and more d is at
+// most 2817, with 2 to 4 at most 5889; wider ones go by the planes.  A warp of k_few_up takes
 // UP_UNITS units at a time, the rows of Wg and Wu of each against every row of x from
 // shared memory; a CTA of k_few_down takes DOWN_ROWS rows of W_out, its warps a share of
 // the inner dimension each.
@@ -1402,8 +1403,11 @@ template <typename T, int N> cudaError_t launch_few(const Call &c, T *y) {
     constexpr int WIDE = 16 / sizeof(T);
     const bool up = c.d % WIDE == 0 && (reinterpret_cast<uintptr_t>(c.W_in) | reinterpret_cast<uintptr_t>(c.x)) % 16 == 0;
     const bool down = c.f % WIDE == 0 && reinterpret_cast<uintptr_t>(c.W_out) % 16 == 0;
-    return up ? (down ? launch_few<T, N, WIDE, WIDE>(c, y) : launch_few<T, N, WIDE, 1>(c, y))
-              : (down ? launch_few<T, N, 1, WIDE>(c, y) : launch_few<T, N, 1, 1>(c, y));
+    if constexpr (sizeof(T) == 4)   // (bf16 that is aligned throughout takes the mma.sync form)
+        if (up && down) return launch_few<T, N, WIDE, WIDE>(c, y);
+    return up     ? launch_few<T, N, WIDE, 1>(c, y)
+           : down ? launch_few<T, N, 1, WIDE>(c, y)
+                  : launch_few<T, N, 1, 1>(c, y);
 }
 
 template <typename T> int few_forward(const Call &c, T *y) {
