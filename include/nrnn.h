@@ -738,10 +738,10 @@ size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dt
  *
  * Roundings.  Sums are fp32.  bf16 rounds m = silu(a) b once before its products with W_out
  * and g, and the gradient's dL/da and dL/db once before theirs: each result is about 1.41
- * times as far off as rounding the exact one once.  A call of at most 16 rows that keeps
- * nothing, with 16-byte aligned rows, does not round m, so y of a row may differ by that
- * rounding between a decode step and a longer call, or one that keeps.  fp32 results are a
- * few 2^-24 of the summed magnitudes off, in either form of few rows and more.
+ * times as far off as rounding the exact one once.  A call of at most 16 rows does not
+ * round m, dL/da and dL/db (they are held to 2^-16), so y of a row may differ by that
+ * rounding between a decode step and a longer call.  fp32 results are a few 2^-24 of the
+ * summed magnitudes off.
  */
 int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, int dtype,
                            int64_t rows, int64_t d, int64_t f, void *y, void *kept,

@@ -164,9 +164,8 @@ def gated_mlp(x: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, keep: bo
     gated_mlp_backward takes.
 
     bfloat16 rounds silu(a) b once between the products, and y: 1.41 times as far off
-    as rounding the exact y.  At most 16 rows that keep nothing leave the first
-    rounding out, so y of a decode step's row may differ by it from the same row of a
-    longer call."""
+    as rounding the exact y.  Calls of at most 16 rows leave the first rounding out, so
+    y of a decode step's row may differ by it from the same row of a longer call."""
     x, W_in, W_out, code, rows, d, f = _mlp_args(x, W_in, W_out)
     lib = load()
     y = torch.empty_like(x) if out is None else _result(out, x.shape, x, "out")
@@ -184,8 +183,8 @@ def gated_mlp_backward(x: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor,
                        g: torch.Tensor, workspace: torch.Tensor | None = None):
     """(dL/dx, dL/dW_in, dL/dW_out) of gated_mlp() in x's dtype, from what it kept
     for the same x and weights and g = dL/dy.  bfloat16 rounds dL/da, dL/db and silu(a) b
-    once before their products, and the results: 1.41 times as far off as rounding the
-    exact gradients."""
+    once before their products (not of at most 16 rows), and the results: 1.41 times as
+    far off as rounding the exact gradients."""
     x, W_in, W_out, code, rows, d, f = _mlp_args(x, W_in, W_out)
     g = _like(g, x, "g")
     lib = load()

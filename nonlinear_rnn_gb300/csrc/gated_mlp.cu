@@ -35,7 +35,8 @@
 // bf16, and a second plane of each would double these products.  So every result is 1.41
 // times as far off as rounding the exact one once: two roundings.  p and q are no operands
 // and keep 16 bits of significand, 2^-15 at most off, as one of 2^-9 more would make gx and
-// gW_in 1.73 times as far off.
+// gW_in 1.73 times as far off.  Up to TWO_PLANES_MOST rows m, ga and gb are two planes all the
+// same.
 //
 // fp32 operands are split into three bf16 planes, v = hi + mid + lo up to 2^-24, and a
 // product is the six plane products above 2^-24 relative, smallest first.  An
@@ -100,6 +101,7 @@ struct GemmArgs {
     float *parts;             // [pairs][2][BM][bn] sums of cut tiles
     void *out;                // the result in the storage type, rows of N
     bool blocks_out;          // bf16: tmOut is over the result, whose blocks leave by TMA
+    int inner;                // bf16: planes that UP and DH store and the other products take: 1 or 2
     bool keep;                // UP: p and q are stored
     void *pq;                 // p and q: fp32 [2][M][pitch]; bf16 blocks of KEPT_ROWS x KEPT_COLS
     int pitch;
@@ -277,6 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     Walk<FORM> w(a, pair, gridDim.x >> 1);
     Unit t;
     constexpr int PASSES = SPLIT ? SEGMENTS : 1;
+    const int again = !SPLIT && CUTS<FORM> ? a.inner : 1;   // products of a slice, one a plane
     const int half_n = a.bn / 2;
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
@@ -306,11 +309,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             // operands of two halves: plane p of half h is 2 p + h
             constexpr bool TWO_A = FORM == GX || FORM == GWI, TWO_B = FORM == UP || FORM == GX;
             const bool two = is_a ? TWO_A : TWO_B;
+            // bf16: whether this lane's operand is one of so many planes, the smaller first
+            const bool in_planes = is_a == (FORM != GWO);
             for (int c0 = t.k0; go && c0 < t.k1;) {
                 const int c1 = SPLIT && c0 + SPLIT_CHUNK < t.k1 ? c0 + SPLIT_CHUNK : t.k1;
                 for (int p = 0; go && p < PASSES; ++p) {
-                    const int plane = SPLIT ? (is_a ? PLANE_A[p] : PLANE_B[p]) : 0;
-                    for (int k = c0; k < c1; ++k, ++it) {
+                    int plane = SPLIT ? (is_a ? PLANE_A[p] : PLANE_B[p]) : 0;
+                    for (int i = 0; i < (c1 - c0) * again; ++i, ++it) {
+                        int k = c0 + i;
+                        if (!SPLIT && again == 2) {
+                            k = c0 + (i >> 1);
+                            plane = in_planes ? 1 - (i & 1) : 0;
+                        }
                         const int s = it % STAGES;
                         if (it >= STAGES)
                             go = __all_sync(FULL_MASK, wait_or_abort(a, &empty_bar[s], ((it / STAGES) - 1) & 1, &s_abort));
@@ -341,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 if (phase >= 2) go = wait_or_abort(a, &acce_bar[buf], ((phase >> 1) - 1) & 1, &s_abort);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + buf * BN;
-                const int its = (c1 - c0) * PASSES;
+                const int its = (c1 - c0) * PASSES * again;
                 for (int i = 0; go && i < its; ++i, ++it) {
                     const int s = it % STAGES;
                     go = wait_or_abort(a, &full_bar[s], (it / STAGES) & 1, &s_abort);
@@ -396,6 +406,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 o[e] = *reinterpret_cast<const uint32_t *>(&h);
             }
             return pk;
+        };
+        auto less_first_plane = [](float *v) {   // 8 values less what to_bf16 makes of them (an infinity: zero)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = __bfloat162float(__float2bfloat16_rn(v[e]));
+                v[e] = isinf(h) ? 0.f : v[e] - h;
+            }
         };
         // 32 columns of this warp's 32 rows to `to`, rows of `pitch` elements: by way of the
         // block, so that a store takes whole lines (each lane its own row: 4.3 us a CTA for
@@ -571,39 +588,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     release(buf);
                     continue;
                 }
-                blocks_free();
+                // (a second plane of m: the same once more)
+#pragma unroll 1
+                for (int plane = 0; plane < a.inner; ++plane) {
+                    blocks_free();
 #pragma unroll
-                for (int h = 0; h < PIECE; h += 32) {
-                    float va[32], vb[32];
-                    read32(buf, odd * PIECE + h, va);
-                    read32(buf, half_n + odd * PIECE + h, vb);
-                    if (h + 32 == PIECE) release(buf);
+                    for (int h = 0; h < PIECE; h += 32) {
+                        float va[32], vb[32];
+                        read32(buf, odd * PIECE + h, va);
+                        read32(buf, half_n + odd * PIECE + h, vb);
+                        if (h + 32 == PIECE && plane + 1 == a.inner) release(buf);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float vm[8];
+                        for (int q = 0; q < 4; ++q) {
+                            float vm[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) vm[e] = gate(va[8 * q + e], vb[8 * q + e]);
-                        *place(0, h / 8 + q) = to_bf16(vm);
+                            for (int e = 0; e < 8; ++e) vm[e] = gate(va[8 * q + e], vb[8 * q + e]);
+                            if (plane > 0) less_first_plane(vm);
+                            *place(0, h / 8 + q) = to_bf16(vm);
+                        }
+                        if (a.keep && plane == 0 && y0 < a.M) {
+#pragma unroll
+                            for (int u = 0; u < 32; u += KEPT_COLS)
+                                if (x + h + u < a.N) {
+                                    uint4 *to = kept_at(a, y0, x + h + u, lane);
+                                    __stcs(&to[0], upper_halves(va + u));
+                                    __stcs(&to[KEPT_ROWS], upper_halves(va + u + 8));
+                                    __stcs(&to[2 * KEPT_ROWS], upper_halves(vb + u));
+                                    __stcs(&to[3 * KEPT_ROWS], upper_halves(vb + u + 8));
+                                    __stcs(&to[4 * KEPT_ROWS], third_bytes(va + u));
+                                    __stcs(&to[5 * KEPT_ROWS], third_bytes(vb + u));
+                                }
+                        }
                     }
-                    if (a.keep && y0 < a.M) {
-#pragma unroll
-                        for (int u = 0; u < 32; u += KEPT_COLS)
-                            if (x + h + u < a.N) {
-                                uint4 *to = kept_at(a, y0, x + h + u, lane);
-                                __stcs(&to[0], upper_halves(va + u));
-                                __stcs(&to[KEPT_ROWS], upper_halves(va + u + 8));
-                                __stcs(&to[2 * KEPT_ROWS], upper_halves(vb + u));
-                                __stcs(&to[3 * KEPT_ROWS], upper_halves(vb + u + 8));
-                                __stcs(&to[4 * KEPT_ROWS], third_bytes(va + u));
-                                __stcs(&to[5 * KEPT_ROWS], third_bytes(vb + u));
-                            }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && y0 < a.M) {
+                        tma_store_3d(&tmOut, stage_out, x, y0, plane);
+                        bulk_commit();
                     }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && y0 < a.M) {
-                    tma_store_3d(&tmOut, stage_out, x, y0, 0);
-                    bulk_commit();
                 }
             } else if (FORM == DH) {
                 const int buf = phase & 1;
@@ -623,13 +645,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     const int x = t.tn * a.bn + c;
                     const bool inside = x < a.N && y0 < a.M;
                     if (c < 2 * PIECE) accumulator(buf, (phase >> 1) & 1);
-                    if (inside) {
+#pragma unroll 1
+                    for (int plane = 0; inside && plane < a.inner; ++plane) {
+                        const bool last = plane + 1 == a.inner;
                         blocks_free();
 #pragma unroll
                         for (int h = 0; h < PIECE; h += 32) {
                             float g[32];
                             read32(buf, c + h, g);
-                            if (h + 32 == PIECE && c + 2 * PIECE >= a.bn) release(buf);
+                            if (h + 32 == PIECE && c + 2 * PIECE >= a.bn && last) release(buf);
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -645,23 +669,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                                         vb[e] = q2.x * gq[e];
                                         vb[e + 1] = q2.y * gq[e + 1];
                                     }
+                                    if (plane > 0) {
+                                        less_first_plane(va);
+                                        less_first_plane(vb);
+                                    }
                                     *place(0, h / 8 + 2 * u + q) = to_bf16(va);
                                     *place(1, h / 8 + 2 * u + q) = to_bf16(vb);
                                 }
                                 if (h + 32 < PIECE) fetch(u, x + 32 + u * KEPT_COLS);
+                                else if (!last) fetch(u, x + u * KEPT_COLS);
                                 else if (c + 2 * PIECE < a.bn) fetch(u, x + 2 * PIECE + u * KEPT_COLS);
                             }
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_3d(&tmOut, stage_out, x, y0, 0);
-                            tma_store_3d(&tmOut, stage_out + BOX_BYTES, x, y0, 1);
+                            tma_store_3d(&tmOut, stage_out, x, y0, 2 * plane);
+                            tma_store_3d(&tmOut, stage_out + BOX_BYTES, x, y0, 2 * plane + 1);
                             bulk_commit();
                         }
-                    } else if (c + 2 * PIECE >= a.bn) {
-                        release(buf);
                     }
+                    if (!inside && c + 2 * PIECE >= a.bn) release(buf);
                 }
                 if (odd * PIECE >= a.bn) {
                     accumulator(buf, (phase >> 1) & 1);
@@ -1120,6 +1148,15 @@ struct Call {
     cudaStream_t stream;
 };
 
+// Rows up to which bf16 holds m, dL/da and dL/db as two planes, as the form of mma.sync does.
+// Roundings of few rows cannot be counted on to average: one of m and one of y leave y up to
+// 1.9 times as far off as rounding it once (1 row), 1.52 of 12 rows, under 1.49 from 16 on; two
+// planes 1.0.  (8 rows over 1024 x 4096 in a graph: keeping 26.7 -> 28.7 us, backward 41.7 ->
+// 49.2; up to 64 rows as much.)
+constexpr int TWO_PLANES_MOST = SHORT_MOST;
+
+int inner_planes(int64_t n, int dtype) { return dtype == NRNN_F32 ? 3 : n <= TWO_PLANES_MOST ? 2 : 1; }
+
 // What the gradient takes: p and q, fp32 [2][n][pf] or the blocks of 24 bits, and m
 // [planes][n][pf] bf16.
 // (Not rounded up, so that its size tells one number of rows from another.)
@@ -1127,16 +1164,16 @@ struct Kept { size_t m, total; int64_t pf; };
 Kept kept_layout(int64_t n, int64_t f, int dtype) {
     Kept k{};
     k.pf = ceil_div(f, 8) * 8;
-    const size_t planes = dtype == NRNN_BF16 ? 1 : 3;
+    const size_t planes = inner_planes(n, dtype);
     k.m = dtype == NRNN_BF16 ? ceil_div(n, KEPT_ROWS) * ceil_div(f, KEPT_COLS) * KEPT_BYTES : up256(2 * sizeof(float) * n * k.pf);
-    k.total = k.m + 2 * planes * n * k.pf + 16;
+    k.total = k.m + 2 * planes * n * k.pf + (planes == 2 ? 24 : 16);
     return k;
 }
 
 // The workspace.  An operand of bf16 whose rows are 16-byte aligned is used where it
 // lies, every other one is copied to bf16 planes of aligned rows.
 struct Plan {
-    int planes;
+    int planes, inner;   // of x, g and the weights; of m, dL/da and dL/db
     int64_t pd, pf;
     size_t x, w_in, w_out, g, m, gab, parts, total;
 };
@@ -1179,6 +1216,7 @@ Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in
               bool keep, bool backward) {
     Plan p{};
     p.planes = dtype == NRNN_F32 ? 3 : 1;
+    p.inner = inner_planes(n, dtype);
     p.pd = ceil_div(d, 8) * 8;
     p.pf = ceil_div(f, 8) * 8;
     size_t at = 256;   // the error word
@@ -1190,9 +1228,9 @@ Plan plan_for(int64_t n, int64_t d, int64_t f, int dtype, bool x_lies, bool w_in
     p.x = x_lies ? NO_COPY : take(2 * p.planes * n * p.pd);
     p.w_in = w_in_lies ? NO_COPY : take(2 * p.planes * 2 * f * p.pd);
     p.w_out = w_out_lies ? NO_COPY : take(2 * p.planes * d * p.pf);
-    p.m = keep || backward ? NO_COPY : take(2 * p.planes * n * p.pf);   // (else among what is kept)
+    p.m = keep || backward ? NO_COPY : take(2 * p.inner * n * p.pf);   // (else among what is kept)
     p.g = !backward || g_lies ? NO_COPY : take(2 * p.planes * n * p.pd);
-    p.gab = backward ? take(2 * p.planes * 2 * n * p.pf) : NO_COPY;
+    p.gab = backward ? take(2 * p.inner * 2 * n * p.pf) : NO_COPY;
     const int64_t widest = tile_columns(d) > tile_columns(f) ? tile_columns(d) : tile_columns(f);
     p.parts = take(sizeof(float) * 2 * PAIRS * BM * widest);
     p.total = at;
@@ -1273,7 +1311,7 @@ bool map(CUtensorMap *m, const void *base, int64_t inner, int64_t pitch, int64_t
     return make_map_pitched(m, base, inner, pitch, rows, planes, box_inner, box_rows);
 }
 
-GemmArgs args_of(const Call &c, int64_t M, int64_t N, int64_t K, int bn) {
+GemmArgs args_of(const Call &c, const Plan &p, int64_t M, int64_t N, int64_t K, int bn) {
     GemmArgs a{};
     a.error = reinterpret_cast<uint32_t *>(c.ws);
     a.wait_ns = wait_limit_ns();
@@ -1284,6 +1322,7 @@ GemmArgs args_of(const Call &c, int64_t M, int64_t N, int64_t K, int bn) {
     a.tiles_n = static_cast<int>(ceil_div(N, bn));
     a.kb = static_cast<int>(ceil_div(K, BK));
     a.kept_cols = static_cast<int>(ceil_div(c.f, KEPT_COLS));
+    a.inner = p.inner;
     return a;
 }
 
@@ -1294,20 +1333,20 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
     CUtensorMap ta, tb, to;
     const int units = tile_columns_for(ceil_div(c.n, BM), c.f, false, BN / 2);   // UP: a tile's units
     if (!map(&ta, x, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, BK, units) ||
-        !map(&to, m, c.f, p.pf, c.n, p.planes, PIECE, BOX_ROWS))
+        !map(&to, m, c.f, p.pf, c.n, p.inner, PIECE, BOX_ROWS))
         return NRNN_ERR_CUDA;
-    GemmArgs a = args_of(c, c.n, c.f, c.d, 2 * units);
+    GemmArgs a = args_of(c, p, c.n, c.f, c.d, 2 * units);
     a.tiles_n = static_cast<int>(ceil_div(c.f, units));
     a.keep = kept != nullptr;
     a.pq = kept;
     a.pitch = static_cast<int>(p.pf);
     if (gemm<UP, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     const int bn = tile_columns_for(ceil_div(c.n, BM), c.d, true);
-    a = args_of(c, c.n, c.d, c.f, bn);
+    a = args_of(c, p, c.n, c.d, c.f, bn);
     a.parts = reinterpret_cast<float *>(c.ws + p.parts);
     a.out = y;
     a.blocks_out = used_in_place(y, c.d, c.dtype);
-    if (!map(&ta, m, c.f, p.pf, c.n, p.planes, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, BK, bn / 2) ||
+    if (!map(&ta, m, c.f, p.pf, c.n, p.inner, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, BK, bn / 2) ||
         (a.blocks_out && !map(&to, y, c.d, c.d, c.n, 1, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
     return gemm<DOWN, T>(c, ta, tb, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
@@ -1324,44 +1363,44 @@ int backward(const Call &c, const Plan &p, const unsigned char *kept, const void
     float *parts = reinterpret_cast<float *>(c.ws + p.parts);
     // fp32: one piece of an epilogue warp holds ga and gb, so tiles of 128
     int bn = tile_columns_for(ceil_div(c.n, BM), c.f, false, p.planes != 1 ? 2 * PIECE : BN);
-    GemmArgs a = args_of(c, c.n, c.f, c.d, bn);
+    GemmArgs a = args_of(c, p, c.n, c.f, c.d, bn);
     a.pq = const_cast<unsigned char *>(kept);
     a.pitch = static_cast<int>(p.pf);
     if (!map(&ta, g, c.d, p.pd, c.n, p.planes, BK, HALF_M) || !map(&tb, w_out, c.f, p.pf, c.d, p.planes, 64, BK) ||
-        !map(&to, gab, c.f, p.pf, c.n, 2 * p.planes, PIECE, BOX_ROWS))
+        !map(&to, gab, c.f, p.pf, c.n, 2 * p.inner, PIECE, BOX_ROWS))
         return NRNN_ERR_CUDA;
     if (gemm<DH, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gx
     bn = tile_columns_for(ceil_div(c.n, BM), c.d, true);
-    a = args_of(c, c.n, c.d, c.f, bn);
+    a = args_of(c, p, c.n, c.d, c.f, bn);
     a.kb_half = a.kb;
     a.kb *= 2;
     a.parts = parts;
     a.out = gx;
     a.blocks_out = used_in_place(gx, c.d, c.dtype);
-    if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.planes, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, 64, BK) ||
+    if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.inner, BK, HALF_M) || !map(&tb, w_in, c.d, p.pd, c.f, 2 * p.planes, 64, BK) ||
         (a.blocks_out && !map(&to, gx, c.d, c.d, c.n, 1, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
     if (gemm<GX, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_in
     bn = tile_columns_for(2 * ceil_div(c.f, BM), c.d, true);
-    a = args_of(c, c.f, c.d, c.n, bn);
+    a = args_of(c, p, c.f, c.d, c.n, bn);
     a.m_half = a.tiles_m;
     a.tiles_m *= 2;
     a.parts = parts;
     a.out = gW_in;
     a.blocks_out = used_in_place(gW_in, c.d, c.dtype);
-    if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.planes, 64, BK) || !map(&tb, x, c.d, p.pd, c.n, p.planes, 64, BK) ||
+    if (!map(&ta, gab, c.f, p.pf, c.n, 2 * p.inner, 64, BK) || !map(&tb, x, c.d, p.pd, c.n, p.planes, 64, BK) ||
         (a.blocks_out && !map(&to, gW_in, c.d, c.d, c.f, 2, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
     if (gemm<GWI, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
     // gW_out
     bn = tile_columns_for(ceil_div(c.d, BM), c.f, true);
-    a = args_of(c, c.d, c.f, c.n, bn);
+    a = args_of(c, p, c.d, c.f, c.n, bn);
     a.parts = parts;
     a.out = gW_out;
     a.blocks_out = used_in_place(gW_out, c.f, c.dtype);
-    if (!map(&ta, g, c.d, p.pd, c.n, p.planes, 64, BK) || !map(&tb, m, c.f, p.pf, c.n, p.planes, 64, BK) ||
+    if (!map(&ta, g, c.d, p.pd, c.n, p.planes, 64, BK) || !map(&tb, m, c.f, p.pf, c.n, p.inner, 64, BK) ||
         (a.blocks_out && !map(&to, gW_out, c.f, c.f, c.d, 1, PIECE, BOX_ROWS)))
         return NRNN_ERR_CUDA;
     return gemm<GWO, T>(c, ta, tb, to, a) == cudaSuccess ? NRNN_OK : NRNN_ERR_CUDA;
