@@ -41,8 +41,8 @@
 // Where one segment is so long that its chain would be what takes the time, which only the
 // device knows, the same kernel goes by the time axis (by_segments).
 //
-// Measured, with HBM's measured copy rate of 6775 GB/s: 16 x 16384 x 1024 bf16 390 us forward
-// (0.81), 716 backward (0.89); 4 x 131072 x 64 fp32 143 us (0.55: four columns; without the
+// Measured, with HBM's measured copy rate of 6775 GB/s: 16 x 16384 x 1024 bf16 395 us forward
+// (0.80), 720 backward (0.88); 4 x 131072 x 64 fp32 143 us (0.55: four columns; without the
 // look-back 0.96); the pack 744 us backward (0.85).  Timing-only copies of the forward
 // without the look-back take 345 us: the rest is issue slots (62% busy, 16 warps an SM; two
 // values of every step are held in registers between the scan's two halves).
