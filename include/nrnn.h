@@ -741,7 +741,7 @@ size_t nrnn_gated_mlp_workspace_bytes(int64_t rows, int64_t d, int64_t f, int dt
  * times as far off as rounding the exact one once.  A call of at most 16 rows does not
  * round m, dL/da and dL/db (they are held to 2^-16), so y of a row may differ by that
  * rounding between a decode step and a longer call.  fp32 results are a few 2^-24 of the
- * summed magnitudes off; an infinity in an fp32 operand counts as NaN.
+ * summed magnitudes off; an infinity in an fp32 operand may count as NaN.
  */
 int nrnn_gated_mlp_forward(const void *x, const void *W_in, const void *W_out, int dtype,
                            int64_t rows, int64_t d, int64_t f, void *y, void *kept,
