@@ -47,7 +47,7 @@
 // Measured: a training step of 32768 rows of 1024 x 4096 bf16 1.75 ms (1.42 PFLOP/s; the
 // kernels apart, of 8192 rows under a profiler: UP 107 us, DOWN 49, DH 70, GX 85, GWI 84, GWO 49).  The forward
 // that keeps nothing runs at 1.7 PFLOP/s, the rate of cuBLAS kept up, that is, at the power
-// limit; keeping p and q costs 50 to 60 us for 0.81 GB.  1501 x 250 x 683 fp32, training: 127 us.
+// limit; keeping p and q costs 80 us for 0.81 GB.  1501 x 250 x 683 fp32, training: 127 us.
 //
 // Every wait is bounded.  One that gives up sets the call's error word (the workspace's
 // first) and the abort flag of both CTAs of the pair, which ends the other roles' waits
@@ -102,7 +102,6 @@ struct GemmArgs {
     void *out;                // the result in the storage type, rows of N
     bool blocks_out;          // bf16: tmOut is over the result, whose blocks leave by TMA
     int inner;                // bf16: planes that UP and DH store and the other products take: 1 or 2
-    bool keep;                // UP: p and q are stored
     void *pq;                 // p and q: fp32 [2][M][pitch]; bf16 blocks of KEPT_ROWS x KEPT_COLS
     int pitch;
     int kept_cols;            // bf16: blocks beside one another
@@ -226,8 +225,9 @@ template <int FORM> __device__ __forceinline__ uint32_t stage_bytes(const GemmAr
     return A_BYTES + b_rows * BK * 2;
 }
 
-// T: storage type of the inputs (float: split products)
-template <int FORM, typename T>
+// T: storage type of the inputs (float: split products).  KEEP: UP stores p and q (apart, as
+// what keeps them would cost a forward that does not 3%)
+template <int FORM, typename T, bool KEEP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     k_mlp_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmOut, const GemmArgs a) {
@@ -534,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 if constexpr (FORM == UP) {
                     const int x = t.tn * half_n + odd * PIECE, left = a.N - x;
                     if (mine && left > 0) {
-                        if (a.keep && y0 < a.M) {
+                        if (KEEP && y0 < a.M) {
                             float *p = static_cast<float *>(a.pq) + static_cast<int64_t>(y0) * a.pitch + x,
                                   *q = p + static_cast<int64_t>(a.M) * a.pitch;
                             blocks_free();
@@ -606,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                             if (plane > 0) less_first_plane(vm);
                             *place(0, h / 8 + q) = to_bf16(vm);
                         }
-                        if (a.keep && plane == 0 && y0 < a.M) {
+                        if (KEEP && plane == 0 && y0 < a.M) {
 #pragma unroll
                             for (int u = 0; u < 32; u += KEPT_COLS)
                                 if (x + h + u < a.N) {
@@ -1264,12 +1264,12 @@ cudaError_t operands(const Call &c, const Plan &p, const void *g_in, const void 
     return launch_dependent(k_planes<T>, static_cast<unsigned>(b < 4864 ? b : 4864), 256, 0, c.stream, k);
 }
 
-template <int FORM, typename T>
+template <int FORM, typename T, bool KEEP = false>
 cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmOut, GemmArgs a) {
     static std::atomic<unsigned long long> configured{0};
     constexpr size_t smem = gemm_smem<FORM, T>();
     cudaError_t e = once_per_device(configured, [](int) {
-        return cudaFuncSetAttribute(k_mlp_gemm<FORM, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        return cudaFuncSetAttribute(k_mlp_gemm<FORM, T, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     });
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
@@ -1289,7 +1289,7 @@ cudaError_t gemm(const Call &c, const CUtensorMap &tmA, const CUtensorMap &tmB, 
         a.share = slices / a.teams;
         a.longer = slices % a.teams;
     }
-    e = launch_dependent(k_mlp_gemm<FORM, T>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, a);
+    e = launch_dependent(k_mlp_gemm<FORM, T, KEEP>, 2 * pairs, GEMM_THREADS, smem, c.stream, tmA, tmB, tmOut, a);
     const int64_t cut = static_cast<int64_t>(a.units - a.whole) * a.side;
     if (e == cudaSuccess && cut > 0) {
         cudaLaunchConfig_t cfg = {};
@@ -1337,10 +1337,9 @@ template <typename T> int forward(const Call &c, const Plan &p, T *y, unsigned c
         return NRNN_ERR_CUDA;
     GemmArgs a = args_of(c, p, c.n, c.f, c.d, 2 * units);
     a.tiles_n = static_cast<int>(ceil_div(c.f, units));
-    a.keep = kept != nullptr;
     a.pq = kept;
     a.pitch = static_cast<int>(p.pf);
-    if (gemm<UP, T>(c, ta, tb, to, a) != cudaSuccess) return NRNN_ERR_CUDA;
+    if ((kept != nullptr ? gemm<UP, T, true>(c, ta, tb, to, a) : gemm<UP, T>(c, ta, tb, to, a)) != cudaSuccess) return NRNN_ERR_CUDA;
     const int bn = tile_columns_for(ceil_div(c.n, BM), c.d, true);
     a = args_of(c, p, c.n, c.d, c.f, bn);
     a.parts = reinterpret_cast<float *>(c.ws + p.parts);
