@@ -44,7 +44,7 @@
 // it to fp32 registers, as the tensor cores add less exactly than fp32 rounding does.
 // (An infinity leaves no number: in fp32 operands it counts as NaN.)
 //
-// Measured: a training step of 32768 rows of 1024 x 4096 bf16 1.75 ms (1.42 PFLOP/s; the
+// Measured: a training step of 32768 rows of 1024 x 4096 bf16 1.75 to 1.83 ms (1.35 to 1.42 PFLOP/s; the
 // kernels apart, of 8192 rows under a profiler: UP 107 us, DOWN 49, DH 70, GX 85, GWI 84, GWO 49).  The forward
 // that keeps nothing runs at 1.7 PFLOP/s, the rate of cuBLAS kept up, that is, at the power
 // limit; keeping p and q costs 80 us for 0.81 GB.  1501 x 250 x 683 fp32, training: 127 us.
